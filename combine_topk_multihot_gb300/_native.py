@@ -36,6 +36,11 @@ MOE_DEVERR_TIMEOUT = 4
 MOE_DEVERR_BOUNDS = 8
 MOE_BUILD_BOUNDS_CHECKS = 1
 MOE_STATIC_SCRATCH_INTS = 262144
+MOE_DTYPE_BF16 = 0
+MOE_DTYPE_F32 = 1
+MOE_GATE_NONE = 0
+MOE_GATE_TOKEN = 1
+MOE_GATE_ELEMENT = 2
 
 
 class MoeLayout(ctypes.Structure):
@@ -49,7 +54,17 @@ class MoeLayout(ctypes.Structure):
     ]
 
 
+class MoeNorm(ctypes.Structure):
+    """struct moe_norm."""
+    _fields_ = [
+        ("T", c_int64), ("H", c_int32), ("x_dtype", c_int32), ("weight_dtype", c_int32), ("gate_dtype", c_int32),
+        ("gate_kind", c_int32), ("gate_sigmoid", c_int32), ("residual_scale", ctypes.c_float),
+        ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float),
+    ]
+
+
 _P = c_void_p
+_NP = ctypes.POINTER(MoeNorm)
 _LP = ctypes.POINTER(MoeLayout)
 
 # name -> (restype, argtypes); every entry point of include/moe.h
@@ -81,6 +96,11 @@ SIGNATURES = {
     "moe_grouped_experts_backward": (c_int32, [_P, _P, _P, _P, _LP, c_int32, c_int32, _P, _P, _P, _P, _P, _P, _P]),
     "moe_grouped_experts_backward_scaled": (c_int32, [_P, _P, _P, _P, _LP, c_int32, c_int32, _P, _P, _P, _P, _P,
                                                       _P, _P]),
+    "moe_norm_in": (c_int32, [_NP, _P, _P, _P, _P, _P]),
+    "moe_norm_backward_workspace_bytes": (c_int32, [c_int64, c_int32, ctypes.POINTER(c_size_t)]),
+    "moe_norm_in_backward": (c_int32, [_NP] + [_P] * 9),
+    "moe_norm_out": (c_int32, [_NP] + [_P] * 10),
+    "moe_norm_out_backward": (c_int32, [_NP] + [_P] * 16),
     "moe_selftest_wait_timeout": (c_int32, [_P, c_int64, _P, _P]),
     "moe_route_to_multihot_backward": (c_int32, [_P, _P, _P, c_int32, c_int32, c_int32, _P, _P]),
 }

@@ -1,0 +1,174 @@
+"""What stands around the MoE layer in a block: Python binding, argument checks only.
+
+* moe_norm_in / moe_norm_out and their backwards: the RMS norms before and
+  after a block, fused with its gate and residual scale.
+
+As in ``moe.py`` the functions carry the names of the C entry points, all
+arithmetic runs in the CUDA library, and PyTorch only allocates the buffers and
+supplies the current stream.  Tensors are packed and on the GPU; anything
+else is refused before a kernel is launched.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+from . import _native as N
+from .moe import _check
+
+_DTYPES = {torch.bfloat16: N.MOE_DTYPE_BF16, torch.float32: N.MOE_DTYPE_F32}
+_GATES = {0: N.MOE_GATE_NONE, 1: N.MOE_GATE_TOKEN, 2: N.MOE_GATE_ELEMENT}
+
+
+def _raw_stream(stream):
+    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+
+
+def _need(t: torch.Tensor, name: str, dtype, shape, device):
+    """The address of a tensor that has to be as given (None for one without elements)."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device} (got {t.device})")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr() or None
+
+
+def _on_gpu(t: torch.Tensor, name: str) -> torch.device:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a GPU (got {t.device}): there is no CPU kernel")
+    return t.device
+
+
+def _either(t: torch.Tensor, name: str) -> int:
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be bfloat16 or float32 (got {t.dtype})")
+    return code
+
+
+def _rows(t: torch.Tensor, name: str):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [T, H] (got {tuple(t.shape)})")
+    return t.shape
+
+
+def _norm(T, H, x, weight, gate, gate_sigmoid, residual_scale, eps, weight_offset, next_weight=None):
+    if next_weight is not None and next_weight.dtype is not weight.dtype:
+        raise TypeError("weight and next_weight must have the same type")
+    if gate is not None and gate.shape != (T,) and gate.shape != (T, H):
+        raise ValueError(f"gate must have shape {(T,)} or {(T, H)} (got {tuple(gate.shape)})")
+    return N.MoeNorm(T, H, _either(x, "x"), _either(weight, "weight"),
+                     N.MOE_DTYPE_F32 if gate is None else _either(gate, "gate"),
+                     N.MOE_GATE_NONE if gate is None else _GATES[gate.dim()],
+                     int(gate_sigmoid), residual_scale, eps, weight_offset)
+
+
+def _workspace(T, H, device):
+    nbytes = ctypes.c_size_t(0)
+    _check(N.lib.moe_norm_backward_workspace_bytes(T, H, ctypes.byref(nbytes)), "moe_norm_backward_workspace_bytes")
+    return torch.empty(nbytes.value, dtype=torch.uint8, device=device)
+
+
+def moe_norm_in(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, weight_offset: float = 0.0,
+                save_rstd: bool = False, out: Optional[torch.Tensor] = None, stream=None):
+    """The norm before a block: returns (norm [T, H] bf16, rstd fp32 [T] or
+    None).  ``save_rstd`` keeps what moe_norm_in_backward needs."""
+    T, H = _rows(x, "x")
+    dev = _on_gpu(x, "x")
+    n = _norm(T, H, x, weight, None, False, 1.0, eps, weight_offset)
+    if out is None:
+        out = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
+    rstd = torch.empty(T, dtype=torch.float32, device=dev) if save_rstd else None
+    _check(N.lib.moe_norm_in(n, _need(x, "x", x.dtype, (T, H), dev), _need(weight, "weight", weight.dtype, (H,), dev),
+                             _need(out, "out", torch.bfloat16, (T, H), dev), rstd.data_ptr() or None if save_rstd else None,
+                             _raw_stream(stream)), "moe_norm_in")
+    return out, rstd
+
+
+def moe_norm_in_backward(grad_norm: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                         grad_res: Optional[torch.Tensor] = None, weight_offset: float = 0.0, stream=None):
+    """Returns (grad_x [T, H] in x's type, grad_weight fp32 [H]).  ``grad_res``
+    is the gradient that reaches x past the block; it is added to grad_x."""
+    T, H = _rows(x, "x")
+    dev = _on_gpu(x, "x")
+    n = _norm(T, H, x, weight, None, False, 1.0, 0.0, weight_offset)
+    grad_x = torch.empty(T, H, dtype=x.dtype, device=dev)
+    grad_w = torch.empty(H, dtype=torch.float32, device=dev)
+    ws = _workspace(T, H, dev)
+    _check(N.lib.moe_norm_in_backward(
+        n, _need(grad_norm, "grad_norm", torch.bfloat16, (T, H), dev), _need(x, "x", x.dtype, (T, H), dev),
+        _need(weight, "weight", weight.dtype, (H,), dev), _need(rstd, "rstd", torch.float32, (T,), dev),
+        None if grad_res is None else _need(grad_res, "grad_res", x.dtype, (T, H), dev),
+        grad_x.data_ptr() or None, grad_w.data_ptr(), ws.data_ptr() or None, _raw_stream(stream)),
+        "moe_norm_in_backward")
+    return grad_x, grad_w
+
+
+def moe_norm_out(x: torch.Tensor, y: torch.Tensor, weight: torch.Tensor, gate: Optional[torch.Tensor] = None,
+                 residual_scale: float = 1.0, gate_sigmoid: bool = True, next_weight: Optional[torch.Tensor] = None,
+                 eps: float = 1e-6, weight_offset: float = 0.0, save_rstd: bool = False, stream=None):
+    """The norm after a block, its gate ([T] or [T, H]) and the residual:
+    returns (out [T, H] in x's type, rstd or None, next [T, H] bf16 or None,
+    next_rstd or None), next being the next block's norm of out."""
+    T, H = _rows(x, "x")
+    dev = _on_gpu(x, "x")
+    n = _norm(T, H, x, weight, gate, gate_sigmoid, residual_scale, eps, weight_offset, next_weight)
+    out = torch.empty(T, H, dtype=x.dtype, device=dev)
+    rstd = torch.empty(T, dtype=torch.float32, device=dev) if save_rstd else None
+    has_next = next_weight is not None
+    nxt = torch.empty(T, H, dtype=torch.bfloat16, device=dev) if has_next else None
+    next_rstd = torch.empty(T, dtype=torch.float32, device=dev) if save_rstd and has_next else None
+    _check(N.lib.moe_norm_out(
+        n, _need(x, "x", x.dtype, (T, H), dev), _need(y, "y", torch.bfloat16, (T, H), dev),
+        _need(weight, "weight", weight.dtype, (H,), dev),
+        None if gate is None else _need(gate, "gate", gate.dtype, gate.shape, dev), out.data_ptr() or None,
+        rstd.data_ptr() or None if save_rstd else None,
+        _need(next_weight, "next_weight", weight.dtype, (H,), dev) if has_next else None,
+        nxt.data_ptr() or None if has_next else None,
+        next_rstd.data_ptr() or None if next_rstd is not None else None, _raw_stream(stream)), "moe_norm_out")
+    return out, rstd, nxt, next_rstd
+
+
+def moe_norm_out_backward(grad_out: Optional[torch.Tensor], y: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                          gate: Optional[torch.Tensor] = None, residual_scale: float = 1.0, gate_sigmoid: bool = True,
+                          grad_next: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                          next_weight: Optional[torch.Tensor] = None, next_rstd: Optional[torch.Tensor] = None,
+                          weight_offset: float = 0.0, stream=None):
+    """Returns (grad_x, grad_y, grad_gate or None, grad_weight fp32 [H],
+    grad_next_weight fp32 [H] or None).  With a next norm give grad_next, out,
+    next_weight and next_rstd; grad_out may then be None."""
+    T, H = _rows(y, "y")
+    dev = _on_gpu(y, "y")
+    has_next = next_weight is not None
+    if any((t is not None) != has_next for t in (grad_next, out, next_rstd)):
+        raise ValueError("give grad_next, out, next_weight and next_rstd, or none of them")
+    if grad_out is None and not has_next:
+        raise ValueError("grad_out may be None only with a next norm")
+    stream_like = grad_out if grad_out is not None else out
+    n = _norm(T, H, stream_like, weight, gate, gate_sigmoid, residual_scale, 0.0, weight_offset, next_weight)
+    xt = stream_like.dtype
+    grad_x = torch.empty(T, H, dtype=xt, device=dev)
+    grad_y = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
+    grad_gate = torch.empty_like(gate, memory_format=torch.contiguous_format) if gate is not None else None
+    grad_w = torch.empty(H, dtype=torch.float32, device=dev)
+    grad_w2 = torch.empty(H, dtype=torch.float32, device=dev) if has_next else None
+    ws = _workspace(T, H, dev)
+    _check(N.lib.moe_norm_out_backward(
+        n, None if grad_out is None else _need(grad_out, "grad_out", xt, (T, H), dev),
+        _need(grad_next, "grad_next", torch.bfloat16, (T, H), dev) if has_next else None,
+        _need(out, "out", xt, (T, H), dev) if has_next else None, _need(y, "y", torch.bfloat16, (T, H), dev),
+        _need(weight, "weight", weight.dtype, (H,), dev),
+        None if gate is None else _need(gate, "gate", gate.dtype, gate.shape, dev),
+        _need(rstd, "rstd", torch.float32, (T,), dev),
+        _need(next_weight, "next_weight", weight.dtype, (H,), dev) if has_next else None,
+        _need(next_rstd, "next_rstd", torch.float32, (T,), dev) if has_next else None,
+        grad_x.data_ptr() or None, grad_y.data_ptr() or None, None if gate is None else grad_gate.data_ptr() or None,
+        grad_w.data_ptr(), grad_w2.data_ptr() if has_next else None, ws.data_ptr() or None, _raw_stream(stream)),
+        "moe_norm_out_backward")
+    return grad_x, grad_y, grad_gate, grad_w, grad_w2

@@ -7,6 +7,7 @@
 #include <cstring>
 #include <atomic>
 #include <chrono>
+#include <cmath>
 #include <mutex>
 
 #include "common.cuh"
@@ -645,6 +646,188 @@ moe_status moe_grouped_experts_backward(const moe_bf16* grad_y, const moe_bf16* 
                                         void* workspace, moe_stream_t stream) {
   return experts_backward_impl("moe_grouped_experts_backward", grad_y, x_disp, h, gu_save, L, H, I, W1, W2,
                                grad_x_disp, dW1, dW2, workspace, stream, false);
+}
+
+}  // extern "C"
+
+namespace {
+
+bool is_dtype(int32_t d) { return d == MOE_DTYPE_BF16 || d == MOE_DTYPE_F32; }
+
+moe_status check_norm(const char* who, const moe_norm* n) {
+  MOE_REQUIRE(n != nullptr, MOE_ERR_INVALID_ARG, "%s: NULL moe_norm", who);
+  MOE_REQUIRE(n->T >= 0, MOE_ERR_INVALID_ARG, "%s: T must be >= 0 (got %lld)", who,
+              static_cast<long long>(n->T));
+  MOE_REQUIRE(n->H >= 1 && n->H <= 16384, MOE_ERR_UNSUPPORTED_SHAPE, "%s: H must be in [1, 16384] (got %d)", who,
+              n->H);
+  MOE_REQUIRE(is_dtype(n->x_dtype) && is_dtype(n->weight_dtype) && is_dtype(n->gate_dtype), MOE_ERR_INVALID_ARG,
+              "%s: unknown element type", who);
+  MOE_REQUIRE(n->gate_kind >= MOE_GATE_NONE && n->gate_kind <= MOE_GATE_ELEMENT, MOE_ERR_INVALID_ARG,
+              "%s: unknown gate kind %d", who, n->gate_kind);
+  MOE_REQUIRE(std::isfinite(n->eps) && n->eps >= 0.f && std::isfinite(n->residual_scale) &&
+                  std::isfinite(n->weight_offset),
+              MOE_ERR_INVALID_ARG, "%s: eps must be finite and >= 0, the scale and the offset finite", who);
+  return MOE_OK;
+}
+
+template <typename... P>
+bool all_aligned16(P... p) {
+  return (aligned16(p) && ...);
+}
+
+NormArgs norm_args(const moe_norm* n) {
+  NormArgs a{};
+  a.T = n->T;
+  a.H = n->H;
+  a.x_f32 = n->x_dtype == MOE_DTYPE_F32;
+  a.w_f32 = n->weight_dtype == MOE_DTYPE_F32;
+  a.gate_f32 = n->gate_dtype == MOE_DTYPE_F32;
+  a.gate_kind = n->gate_kind;
+  a.sigmoid = n->gate_sigmoid != 0;
+  a.residual_scale = n->residual_scale;
+  a.eps = n->eps;
+  a.offset = n->weight_offset;
+  return a;
+}
+
+NormBackwardArgs norm_backward_args(const moe_norm* n) {
+  NormBackwardArgs a{};
+  a.T = n->T;
+  a.H = n->H;
+  a.x_f32 = n->x_dtype == MOE_DTYPE_F32;
+  a.w_f32 = n->weight_dtype == MOE_DTYPE_F32;
+  a.gate_f32 = n->gate_dtype == MOE_DTYPE_F32;
+  a.gate_kind = n->gate_kind;
+  a.sigmoid = n->gate_sigmoid != 0;
+  a.residual_scale = n->residual_scale;
+  a.offset = n->weight_offset;
+  return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_norm_in(const moe_norm* n, const void* x, const void* weight, moe_bf16* norm, float* rstd,
+                       moe_stream_t stream) {
+  moe_status st = check_norm("moe_norm_in", n);
+  if (st != MOE_OK) return st;
+  MOE_REQUIRE(n->T == 0 || (x && weight && norm), MOE_ERR_INVALID_ARG, "moe_norm_in: NULL pointer");
+  MOE_REQUIRE(all_aligned16(x, weight, norm, rstd), MOE_ERR_INVALID_ARG,
+              "moe_norm_in: pointers must be 16-byte aligned");
+  if ((st = check_device()) != MOE_OK) return st;
+  NormArgs a = norm_args(n);
+  a.gate_kind = MOE_GATE_NONE;
+  a.x = x;
+  a.w2 = weight;
+  a.next = norm;
+  a.rstd2 = rstd;
+  cudaError_t err = launch_norm_forward(a, stream);
+  return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_norm_in launch");
+}
+
+moe_status moe_norm_backward_workspace_bytes(int64_t T, int32_t H, size_t* bytes) {
+  MOE_REQUIRE(bytes != nullptr, MOE_ERR_INVALID_ARG, "bytes is NULL");
+  MOE_REQUIRE(T >= 0 && H >= 1 && H <= 16384, MOE_ERR_INVALID_ARG, "bad T / H");
+  *bytes = norm_backward_workspace(T, H);
+  return MOE_OK;
+}
+
+moe_status moe_norm_in_backward(const moe_norm* n, const moe_bf16* grad_norm, const void* x, const void* weight,
+                                const float* rstd, const void* grad_res, void* grad_x, float* grad_weight,
+                                void* workspace, moe_stream_t stream) {
+  moe_status st = check_norm("moe_norm_in_backward", n);
+  if (st != MOE_OK) return st;
+  MOE_REQUIRE(grad_weight && (n->T == 0 || (grad_norm && x && weight && rstd && grad_x && workspace)),
+              MOE_ERR_INVALID_ARG, "moe_norm_in_backward: NULL pointer");
+  MOE_REQUIRE(all_aligned16(grad_norm, x, weight, rstd, grad_res, grad_x, grad_weight, workspace),
+              MOE_ERR_INVALID_ARG, "moe_norm_in_backward: pointers must be 16-byte aligned");
+  if ((st = check_device()) != MOE_OK) return st;
+  NormBackwardArgs a = norm_backward_args(n);
+  a.gate_kind = MOE_GATE_NONE;
+  a.has_next = 1;
+  a.dout = grad_res;
+  a.dnext = grad_norm;
+  a.out = x;
+  a.w2 = weight;
+  a.rstd2 = rstd;
+  a.dx = grad_x;
+  a.dw2 = grad_weight;
+  a.partials = static_cast<float*>(workspace);
+  cudaError_t err = launch_norm_backward(a, stream);
+  return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_norm_in_backward launch");
+}
+
+moe_status moe_norm_out(const moe_norm* n, const void* x, const moe_bf16* y, const void* weight, const void* gate,
+                        void* out, float* rstd, const void* next_weight, moe_bf16* next, float* next_rstd,
+                        moe_stream_t stream) {
+  moe_status st = check_norm("moe_norm_out", n);
+  if (st != MOE_OK) return st;
+  MOE_REQUIRE(n->T == 0 || (x && y && weight && out), MOE_ERR_INVALID_ARG, "moe_norm_out: NULL pointer");
+  MOE_REQUIRE((n->gate_kind == MOE_GATE_NONE) ? !gate : (gate || n->T == 0), MOE_ERR_INVALID_ARG,
+              "moe_norm_out: give gate exactly when gate_kind is not MOE_GATE_NONE");
+  MOE_REQUIRE((next_weight != nullptr) == (next != nullptr) || n->T == 0, MOE_ERR_INVALID_ARG,
+              "moe_norm_out: give next_weight and next, or neither");
+  MOE_REQUIRE(next_weight || !next_rstd, MOE_ERR_INVALID_ARG, "moe_norm_out: next_rstd without next_weight");
+  MOE_REQUIRE(all_aligned16(x, y, weight, gate, out, rstd, next_weight, next, next_rstd), MOE_ERR_INVALID_ARG,
+              "moe_norm_out: pointers must be 16-byte aligned");
+  if ((st = check_device()) != MOE_OK) return st;
+  NormArgs a = norm_args(n);
+  a.x = x;
+  a.y = y;
+  a.w = weight;
+  a.gate = gate;
+  a.w2 = next_weight;
+  a.out = out;
+  a.next = next;
+  a.rstd = rstd;
+  a.rstd2 = next_rstd;
+  cudaError_t err = launch_norm_forward(a, stream);
+  return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_norm_out launch");
+}
+
+moe_status moe_norm_out_backward(const moe_norm* n, const void* grad_out, const moe_bf16* grad_next,
+                                 const void* out, const moe_bf16* y, const void* weight, const void* gate,
+                                 const float* rstd, const void* next_weight, const float* next_rstd, void* grad_x,
+                                 moe_bf16* grad_y, void* grad_gate, float* grad_weight, float* grad_next_weight,
+                                 void* workspace, moe_stream_t stream) {
+  moe_status st = check_norm("moe_norm_out_backward", n);
+  if (st != MOE_OK) return st;
+  // which of the two there are, told by a pointer that is there for T = 0 too
+  const bool has_next = grad_next_weight != nullptr;
+  MOE_REQUIRE(grad_weight, MOE_ERR_INVALID_ARG, "moe_norm_out_backward: NULL grad_weight");
+  MOE_REQUIRE(n->T == 0 || (y && weight && rstd && grad_x && grad_y && workspace && (grad_out || has_next)),
+              MOE_ERR_INVALID_ARG, "moe_norm_out_backward: NULL pointer");
+  MOE_REQUIRE(has_next ? (n->T == 0 || (grad_next && out && next_weight && next_rstd))
+                       : (!grad_next && !next_weight && !next_rstd),
+              MOE_ERR_INVALID_ARG,
+              "moe_norm_out_backward: give grad_next, out, next_weight, next_rstd and grad_next_weight, or none");
+  MOE_REQUIRE((n->gate_kind == MOE_GATE_NONE) ? (!gate && !grad_gate) : (gate || n->T == 0), MOE_ERR_INVALID_ARG,
+              "moe_norm_out_backward: give gate exactly when gate_kind is not MOE_GATE_NONE");
+  MOE_REQUIRE(all_aligned16(grad_out, grad_next, out, y, weight, gate, rstd, next_weight, next_rstd, grad_x, grad_y,
+                            grad_gate, grad_weight, grad_next_weight, workspace),
+              MOE_ERR_INVALID_ARG, "moe_norm_out_backward: pointers must be 16-byte aligned");
+  if ((st = check_device()) != MOE_OK) return st;
+  NormBackwardArgs a = norm_backward_args(n);
+  a.has_y = 1;
+  a.has_next = has_next;
+  a.dout = grad_out;
+  a.dnext = grad_next;
+  a.out = out;
+  a.y = y;
+  a.w = weight;
+  a.gate = gate;
+  a.w2 = next_weight;
+  a.rstd = rstd;
+  a.rstd2 = next_rstd;
+  a.dx = grad_x;
+  a.dy = grad_y;
+  a.dgate = grad_gate;
+  a.dw = grad_weight;
+  a.dw2 = grad_next_weight;
+  a.partials = static_cast<float*>(workspace);
+  cudaError_t err = launch_norm_backward(a, stream);
+  return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_norm_out_backward launch");
 }
 
 }  // extern "C"

@@ -210,4 +210,32 @@ cudaError_t launch_experts_backward(const uint16_t* grad_y, const uint16_t* x_di
                                     uint16_t* grad_x_disp, float* dW1, float* dW2, void* workspace,
                                     cudaStream_t s, bool g_o_given = false);
 
+// The norms around a block (norm.cu).  Forward: y NULL is the norm before a
+// block (x -> next); otherwise out is the updated stream and next may be NULL.
+struct NormArgs {
+  long long T;
+  int H;
+  int x_f32, w_f32, gate_f32, gate_kind, sigmoid;
+  float residual_scale, eps, offset;
+  const void *x, *y, *w, *gate, *w2;
+  void *out, *next;
+  float *rstd, *rstd2;
+};
+cudaError_t launch_norm_forward(const NormArgs& a, cudaStream_t s);
+// Backward: without has_y only the next norm's half (dout then the gradient
+// that joins the stream, or NULL); partials: norm_backward_workspace bytes.
+struct NormBackwardArgs {
+  long long T;
+  int H;
+  int x_f32, w_f32, gate_f32, gate_kind, sigmoid;
+  int has_y, has_next;
+  float residual_scale, offset;
+  const void *dout, *dnext, *out, *y, *w, *gate, *w2;
+  const float *rstd, *rstd2;
+  void *dx, *dy, *dgate;
+  float *dw, *dw2, *partials;
+};
+cudaError_t launch_norm_backward(const NormBackwardArgs& a, cudaStream_t s);
+size_t norm_backward_workspace(long long T, int H);
+
 }  // namespace moe

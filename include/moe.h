@@ -505,6 +505,99 @@ MOE_API moe_status moe_grouped_experts_backward_scaled(const moe_bf16* g_o, cons
                                                        void* workspace, moe_stream_t stream);
 
 /*
+ * ------------------------------------------------------------------------
+ * Around the layer: the norms before and after a block, the optimiser's
+ * step, and products of e4m3 codes with a scale for each block of 128.  They
+ * are no part of the pages' path; they complete it to a block that trains and
+ * serves.
+ * ------------------------------------------------------------------------
+ */
+
+/* Element type of a tensor that may have either. */
+typedef enum moe_dtype { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F32 = 1 } moe_dtype;
+
+/* The gate of a block's output: none, one value per token [T], or one per
+ * element [T, H]. */
+typedef enum moe_gate_kind { MOE_GATE_NONE = 0, MOE_GATE_TOKEN = 1, MOE_GATE_ELEMENT = 2 } moe_gate_kind;
+
+/*
+ * Sizes, types and constants of a norm call.  T >= 0 rows of 1 <= H <= 16384
+ * values, any H (a multiple of 8 is faster); rows are packed.
+ */
+typedef struct moe_norm {
+  int64_t T;
+  int32_t H;
+  int32_t x_dtype;       /* of the residual stream x / out and its gradients (moe_dtype)  */
+  int32_t weight_dtype;  /* of weight and next_weight                                      */
+  int32_t gate_dtype;    /* of gate and its gradient                                       */
+  int32_t gate_kind;     /* moe_gate_kind                                                  */
+  int32_t gate_sigmoid;  /* non-zero: the gate is sigmoid(gate), else gate itself          */
+  float residual_scale;  /* a, the factor of the residual stream                           */
+  float eps;             /* >= 0, added to the mean of squares                             */
+  float weight_offset;   /* the norms' weights are weight_offset + weight                  */
+} moe_norm;
+
+/*
+ * The norm before a block: norm[t] = bf16(x[t] r_t (weight_offset + weight)),
+ * r_t = 1 / sqrt(mean(x[t]^2) + eps), in fp32 throughout.
+ *   x [T, H] bf16 or fp32; weight [H]; norm [T, H] bf16 (out);
+ *   rstd [T] fp32 (out, nullable): r_t, for the backward.
+ * Outputs must not overlap inputs, here and in the three calls below.  Errors:
+ * MOE_ERR_UNSUPPORTED_SHAPE for H outside [1, 16384], MOE_ERR_INVALID_ARG for
+ * a NULL or misaligned pointer, T < 0, an unknown type or gate kind, or an eps
+ * or scale that is not finite (eps also when negative).
+ */
+MOE_API moe_status moe_norm_in(const moe_norm* n, const void* x, const void* weight, moe_bf16* norm,
+                               float* rstd, moe_stream_t stream);
+
+/*
+ * Its backward: grad_x = grad_res + the gradient through the norm, and
+ * grad_weight[h] = sum_t grad_norm[t, h] x[t, h] r_t (the order of the sum is
+ * fixed by the sizes, so results repeat bit for bit).
+ *   grad_norm [T, H] bf16; grad_res [T, H] in x's type (nullable: no other
+ *   gradient reaches x); rstd [T] from the forward; grad_x [T, H] in x's type
+ *   (out); grad_weight [H] fp32 (out, zeros when T is 0);
+ *   workspace: moe_norm_backward_workspace_bytes(T, H) bytes, device scratch.
+ */
+MOE_API moe_status moe_norm_backward_workspace_bytes(int64_t T, int32_t H, size_t* bytes);
+MOE_API moe_status moe_norm_in_backward(const moe_norm* n, const moe_bf16* grad_norm, const void* x,
+                                        const void* weight, const float* rstd, const void* grad_res,
+                                        void* grad_x, float* grad_weight, void* workspace,
+                                        moe_stream_t stream);
+
+/*
+ * The norm after a block, with its gate and the residual:
+ *   out[t] = residual_scale x[t] + s_t (y[t] r_t (weight_offset + weight))
+ * rounded once to x's type; s_t by gate_kind and gate_sigmoid.  With
+ * next_weight also the next block's moe_norm_in of `out` as it is held (after
+ * its rounding), in the same pass: equal to a separate call on out.
+ *   x [T, H]; y [T, H] bf16, the block's output (moe_combine's out);
+ *   gate [T] or [T, H] (NULL for MOE_GATE_NONE); out [T, H] in x's type (out);
+ *   rstd [T] fp32 (out, nullable): of y.  next_weight [H], next [T, H] bf16
+ *   (out) and next_rstd [T] fp32 (out, nullable): all NULL for no next norm.
+ */
+MOE_API moe_status moe_norm_out(const moe_norm* n, const void* x, const moe_bf16* y, const void* weight,
+                                const void* gate, void* out, float* rstd, const void* next_weight,
+                                moe_bf16* next, float* next_rstd, moe_stream_t stream);
+
+/*
+ * Its backward, in one pass over the rows.  grad_out [T, H] in x's type
+ * (nullable when grad_next is given: only the next norm used out), grad_next
+ * [T, H] bf16 with out, next_weight and next_rstd from the forward (all NULL
+ * when there was no next norm).
+ *   grad_x [T, H] in x's type, grad_y [T, H] bf16, grad_weight [H] and
+ *   grad_next_weight [H] fp32 (out); grad_gate in gate's shape and type (out,
+ *   nullable; NULL for MOE_GATE_NONE).  workspace and sums as in
+ *   moe_norm_in_backward.
+ */
+MOE_API moe_status moe_norm_out_backward(const moe_norm* n, const void* grad_out, const moe_bf16* grad_next,
+                                         const void* out, const moe_bf16* y, const void* weight,
+                                         const void* gate, const float* rstd, const void* next_weight,
+                                         const float* next_rstd, void* grad_x, moe_bf16* grad_y,
+                                         void* grad_gate, float* grad_weight, float* grad_next_weight,
+                                         void* workspace, moe_stream_t stream);
+
+/*
  * Failure-detection self-test.  Runs one CTA whose wait on an mbarrier can
  * never complete, using the bounded-wait helper of the pipelined kernels with
  * a limit of limit_ns (0 < limit_ns <= 1 s).  The wait gives up, the kernel
