@@ -41,6 +41,7 @@ MOE_DTYPE_F32 = 1
 MOE_GATE_NONE = 0
 MOE_GATE_TOKEN = 1
 MOE_GATE_ELEMENT = 2
+MOE_ADAMW_STATE_BLOCK = 256
 
 
 class MoeLayout(ctypes.Structure):
@@ -60,6 +61,24 @@ class MoeNorm(ctypes.Structure):
         ("T", c_int64), ("H", c_int32), ("x_dtype", c_int32), ("weight_dtype", c_int32), ("gate_dtype", c_int32),
         ("gate_kind", c_int32), ("gate_sigmoid", c_int32), ("residual_scale", ctypes.c_float),
         ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float),
+    ]
+
+
+class MoeAdamwTensor(ctypes.Structure):
+    """struct moe_adamw_tensor."""
+    _fields_ = [
+        ("param", c_void_p), ("grad", c_void_p), ("master", c_void_p), ("exp_avg", c_void_p),
+        ("exp_avg_sq", c_void_p), ("exp_avg_scale", c_void_p), ("exp_avg_sq_scale", c_void_p), ("n", c_int64),
+        ("param_dtype", c_int32), ("grad_dtype", c_int32), ("weight_decay", ctypes.c_double),
+    ]
+
+
+class MoeAdamw(ctypes.Structure):
+    """struct moe_adamw."""
+    _fields_ = [
+        ("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+        ("step", c_int64), ("seed", ctypes.c_uint64), ("state_bits", c_int32), ("grad_scale", c_void_p),
+        ("skip", c_void_p), ("step_dev", c_void_p),
     ]
 
 
@@ -101,6 +120,7 @@ SIGNATURES = {
     "moe_norm_in_backward": (c_int32, [_NP] + [_P] * 9),
     "moe_norm_out": (c_int32, [_NP] + [_P] * 10),
     "moe_norm_out_backward": (c_int32, [_NP] + [_P] * 16),
+    "moe_adamw_step": (c_int32, [ctypes.POINTER(MoeAdamw), _P, c_int32, _P]),
     "moe_selftest_wait_timeout": (c_int32, [_P, c_int64, _P, _P]),
     "moe_route_to_multihot_backward": (c_int32, [_P, _P, _P, c_int32, c_int32, c_int32, _P, _P]),
 }

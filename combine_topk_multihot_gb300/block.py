@@ -1,7 +1,9 @@
 """What stands around the MoE layer in a block: Python binding, argument checks only.
 
 * moe_norm_in / moe_norm_out and their backwards: the RMS norms before and
-  after a block, fused with its gate and residual scale.
+  after a block, fused with its gate and residual scale;
+* AdamWState / moe_adamw_step: the optimiser's step over many tensors at once,
+  its averages in fp32 or in 8 bits.
 
 As in ``moe.py`` the functions carry the names of the C entry points, all
 arithmetic runs in the CUDA library, and PyTorch only allocates the buffers and
@@ -11,8 +13,9 @@ else is refused before a kernel is launched.
 from __future__ import annotations
 
 import ctypes
-from typing import Optional
+from typing import List, Optional, Sequence, Union
 
+import numpy as np
 import torch
 
 from . import _native as N
@@ -172,3 +175,111 @@ def moe_norm_out_backward(grad_out: Optional[torch.Tensor], y: torch.Tensor, wei
         grad_w.data_ptr(), grad_w2.data_ptr() if has_next else None, ws.data_ptr() or None, _raw_stream(stream)),
         "moe_norm_out_backward")
     return grad_x, grad_y, grad_gate, grad_w, grad_w2
+
+
+# ------------------------------------------------------------------ AdamW
+_TABLE = np.dtype([(n, {ctypes.c_void_p: np.uint64, ctypes.c_int64: np.int64, ctypes.c_int32: np.int32,
+                        ctypes.c_double: np.float64}[c]) for n, c in N.MoeAdamwTensor._fields_])
+assert _TABLE.itemsize == ctypes.sizeof(N.MoeAdamwTensor)
+
+
+class AdamWState:
+    """The parameters of an AdamW optimiser and its state, in caller-owned
+    device buffers: for each parameter exp_avg and exp_avg_sq (fp32, or with
+    state_bits=8 uint8 codes and one fp32 scale per 256 elements) and, with
+    master=True, the fp32 value of which a bf16 parameter is the rounded copy.
+
+    ``step`` counts the steps taken; ``seed`` draws the random rounding of 8-bit
+    exp_avg_sq.  The buffers may be given (to resume, or to place them): then
+    they are used as they are, else they are made for a fresh start."""
+
+    def __init__(self, params: Sequence[torch.Tensor], state_bits: int = 32, master: Union[bool, Sequence, None] = None,
+                 seed: int = 0, step: int = 0, exp_avg=None, exp_avg_sq=None, exp_avg_scale=None,
+                 exp_avg_sq_scale=None):
+        if state_bits not in (8, 32):
+            raise ValueError(f"state_bits must be 8 or 32 (got {state_bits})")
+        if step < 0:
+            raise ValueError(f"step must be >= 0 (got {step})")
+        self.params = list(params)
+        self.state_bits, self.seed, self.step = state_bits, seed & (2 ** 64 - 1), step
+        eight = state_bits == 8
+        for i, p in enumerate(self.params):
+            _on_gpu(p, f"params[{i}]")
+            _either(p, f"params[{i}]")
+        self.device = self.params[0].device if self.params else torch.device("cuda", torch.cuda.current_device())
+        blocks = [-(-p.numel() // N.MOE_ADAMW_STATE_BLOCK) for p in self.params]
+
+        def make(given, what, dtype, shapes):
+            if given is None:
+                return [torch.zeros(s, dtype=dtype, device=self.device) for s in shapes]
+            if len(given) != len(self.params):
+                raise ValueError(f"{what} must hold one tensor per parameter")
+            return list(given)
+
+        shapes = [p.shape for p in self.params]
+        avg = torch.uint8 if eight else torch.float32
+        self.exp_avg = make(exp_avg, "exp_avg", avg, shapes)
+        self.exp_avg_sq = make(exp_avg_sq, "exp_avg_sq", avg, shapes)
+        self.exp_avg_scale = make(exp_avg_scale, "exp_avg_scale", torch.float32, blocks) if eight else None
+        self.exp_avg_sq_scale = make(exp_avg_sq_scale, "exp_avg_sq_scale", torch.float32, blocks) if eight else None
+        if isinstance(master, (list, tuple)):
+            self.master: Optional[List] = make(master, "master", torch.float32, shapes)
+        else:
+            self.master = [p.detach().float() if p.dtype is torch.bfloat16 else None for p in self.params] \
+                if master else None
+        self._table = np.zeros(len(self.params), dtype=_TABLE)
+        for i, (p, row) in enumerate(zip(self.params, self._table)):
+            row["n"], row["param_dtype"] = p.numel(), _either(p, f"params[{i}]")
+            for name, dtype, shape in (("exp_avg", avg, p.shape), ("exp_avg_sq", avg, p.shape),
+                                       ("exp_avg_scale", torch.float32, (blocks[i],)),
+                                       ("exp_avg_sq_scale", torch.float32, (blocks[i],)),
+                                       ("master", torch.float32, p.shape)):
+                held = getattr(self, name)
+                if held is not None and held[i] is not None:
+                    row[name] = _need(held[i], f"{name}[{i}]", dtype, shape, self.device) or 0
+
+
+def moe_adamw_step(state: AdamWState, grads: Sequence[Optional[torch.Tensor]], lr: float, beta1: float = 0.9,
+                   beta2: float = 0.999, eps: float = 1e-8, weight_decay: Union[float, Sequence[float]] = 0.0,
+                   grad_scale: Optional[torch.Tensor] = None, skip: Optional[torch.Tensor] = None,
+                   step: Optional[torch.Tensor] = None, stream=None) -> None:
+    """One step, in place, over all of ``state``'s parameters in one launch (one
+    per 96 tensors).  A gradient is bf16 or fp32 in its parameter's shape; a
+    parameter whose gradient is None is left as it is.  ``weight_decay`` is one
+    number or one per parameter.
+
+    On the device: ``grad_scale`` fp32 [1] multiplies every gradient (an
+    unscaling or a clip that the host need not know), ``skip`` int32 [1] turns
+    the step into a no-op when it is not zero, and ``step`` int64 [1] replaces
+    state.step + 1, for a captured call whose step number changes between
+    replays.  Without ``step``, state.step is counted up here -- also when
+    ``skip`` stops the update, which only the device knows."""
+    params, table, dev = state.params, state._table, state.device
+    if len(grads) != len(params):
+        raise ValueError(f"{len(grads)} gradients for {len(params)} parameters")
+    if params:
+        addresses, kinds, counts, places = [], [], [], []
+        for i, (p, g) in enumerate(zip(params, grads)):
+            if p.dtype not in _DTYPES or p.numel() != state.exp_avg[i].numel() or not p.is_contiguous() or p.device != dev:
+                raise ValueError(f"params[{i}] is no longer what the state was made for")
+            places.append(p.data_ptr())
+            if g is None:
+                addresses.append(0)
+                kinds.append(0)
+                counts.append(0)
+                continue
+            kinds.append(_either(g, f"grads[{i}]"))
+            addresses.append(_need(g, f"grads[{i}]", g.dtype, p.shape, dev) or 0)
+            counts.append(p.numel())
+        table["param"], table["grad"], table["grad_dtype"], table["n"] = places, addresses, kinds, counts
+        table["param_dtype"] = [_DTYPES[p.dtype] for p in params]
+        table["weight_decay"] = weight_decay
+    scalar = [None if t is None else _need(t, name, dtype, (1,), dev)
+              for t, name, dtype in ((grad_scale, "grad_scale", torch.float32), (skip, "skip", torch.int32),
+                                     (step, "step", torch.int64))]
+    h = N.MoeAdamw(lr, beta1, beta2, eps, state.step + 1, state.seed, state.state_bits, *scalar)
+    _check(N.lib.moe_adamw_step(h, table.ctypes.data, len(params), _raw_stream(stream)), "moe_adamw_step")
+    if step is None:
+        state.step += 1
+    if params:
+        torch.autograd.graph.increment_version(params)

@@ -9,6 +9,7 @@
 #include <chrono>
 #include <cmath>
 #include <mutex>
+#include <new>
 
 #include "common.cuh"
 #include "launch.h"
@@ -828,6 +829,85 @@ moe_status moe_norm_out_backward(const moe_norm* n, const void* grad_out, const 
   a.partials = static_cast<float*>(workspace);
   cudaError_t err = launch_norm_backward(a, stream);
   return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_norm_out_backward launch");
+}
+
+}  // extern "C"
+
+namespace {
+
+bool aligned_to(const void* p, uintptr_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_adamw_step(const moe_adamw* h, const moe_adamw_tensor* tensors, int32_t count, moe_stream_t stream) {
+  MOE_REQUIRE(h && (tensors || count == 0) && count >= 0, MOE_ERR_INVALID_ARG,
+              "moe_adamw_step: NULL argument or negative count");
+  MOE_REQUIRE(h->state_bits == 8 || h->state_bits == 32, MOE_ERR_INVALID_ARG,
+              "moe_adamw_step: state_bits must be 8 or 32 (got %d)", h->state_bits);
+  MOE_REQUIRE(h->step >= 1, MOE_ERR_INVALID_ARG, "moe_adamw_step: step must be >= 1 (got %lld)",
+              static_cast<long long>(h->step));
+  MOE_REQUIRE(h->beta1 >= 0 && h->beta1 < 1 && h->beta2 >= 0 && h->beta2 < 1, MOE_ERR_INVALID_ARG,
+              "moe_adamw_step: betas must be in [0, 1)");
+  MOE_REQUIRE(std::isfinite(h->lr) && h->lr >= 0 && std::isfinite(h->eps) && h->eps >= 0, MOE_ERR_INVALID_ARG,
+              "moe_adamw_step: lr and eps must be finite and >= 0");
+  MOE_REQUIRE(aligned_to(h->grad_scale, 4) && aligned_to(h->skip, 4) && aligned_to(h->step_dev, 8),
+              MOE_ERR_INVALID_ARG, "moe_adamw_step: misaligned grad_scale, skip or step_dev");
+  const bool eight = h->state_bits == 8;
+  AdamWTensor* list = new (std::nothrow) AdamWTensor[count > 0 ? count : 1];
+  MOE_REQUIRE(list, MOE_ERR_INVALID_ARG, "moe_adamw_step: no host memory for %d tensors", count);
+  struct Free {
+    AdamWTensor* p;
+    ~Free() { delete[] p; }
+  } release{list};
+  int64_t blocks = 0;
+  for (int32_t k = 0; k < count; ++k) {
+    const moe_adamw_tensor& t = tensors[k];
+    MOE_REQUIRE(t.n >= 0, MOE_ERR_INVALID_ARG, "moe_adamw_step: tensor %d has n < 0", k);
+    MOE_REQUIRE(is_dtype(t.param_dtype) && is_dtype(t.grad_dtype), MOE_ERR_INVALID_ARG,
+                "moe_adamw_step: tensor %d has an unknown element type", k);
+    MOE_REQUIRE(std::isfinite(t.weight_decay) && t.weight_decay >= 0, MOE_ERR_INVALID_ARG,
+                "moe_adamw_step: tensor %d: weight_decay must be finite and >= 0", k);
+    MOE_REQUIRE(!t.master || t.param_dtype == MOE_DTYPE_BF16, MOE_ERR_INVALID_ARG,
+                "moe_adamw_step: tensor %d has a master beside an fp32 param", k);
+    MOE_REQUIRE(t.n == 0 || (t.param && t.grad && t.exp_avg && t.exp_avg_sq &&
+                             (!eight || (t.exp_avg_scale && t.exp_avg_sq_scale))),
+                MOE_ERR_INVALID_ARG, "moe_adamw_step: tensor %d has a NULL pointer", k);
+    const uintptr_t pb = t.param_dtype == MOE_DTYPE_F32 ? 4 : 2, gb = t.grad_dtype == MOE_DTYPE_F32 ? 4 : 2,
+                    sb = eight ? 1 : 4;
+    MOE_REQUIRE(aligned_to(t.param, pb) && aligned_to(t.grad, gb) && aligned_to(t.master, 4) &&
+                    aligned_to(t.exp_avg, sb) && aligned_to(t.exp_avg_sq, sb) && aligned_to(t.exp_avg_scale, 4) &&
+                    aligned_to(t.exp_avg_sq_scale, 4),
+                MOE_ERR_INVALID_ARG, "moe_adamw_step: tensor %d has a pointer misaligned for its type", k);
+    // 2^31 blocks a launch; n is checked first so that the sum cannot overflow
+    MOE_REQUIRE(t.n <= (int64_t(1) << 39) &&
+                    (blocks = (k % ADAMW_BATCH ? blocks : 0) + (t.n + ADAMW_STATE_BLOCK - 1) / ADAMW_STATE_BLOCK) <=
+                        0x7fffffffLL,
+                MOE_ERR_UNSUPPORTED_SHAPE, "moe_adamw_step: more than 2^31 - 1 blocks of 256 elements in a launch");
+    AdamWTensor& o = list[k];
+    o = {t.param, t.grad, t.master, t.exp_avg, t.exp_avg_sq, t.exp_avg_scale, t.exp_avg_sq_scale, t.n};
+    o.kind = (t.param_dtype == MOE_DTYPE_F32 ? 0 : t.master ? 2 : 1) + (t.grad_dtype == MOE_DTYPE_F32 ? 3 : 0);
+    o.wide = aligned_to(t.param, 4 * pb) && aligned_to(t.grad, 4 * gb) && aligned_to(t.master, 16) &&
+             aligned_to(t.exp_avg, 4 * sb) && aligned_to(t.exp_avg_sq, 4 * sb);
+    o.decay = static_cast<float>(1.0 - h->lr * t.weight_decay);
+    o.key = adamw_key(h->seed, static_cast<uint32_t>(k));
+  }
+  moe_status st = check_device();
+  if (st != MOE_OK) return st;
+  AdamWStep a{};
+  a.lr = h->lr;
+  a.beta1 = h->beta1;
+  a.beta2 = h->beta2;
+  a.eps = h->eps;
+  a.step = h->step;
+  a.step_size = static_cast<float>(h->lr / (1.0 - std::pow(h->beta1, static_cast<double>(h->step))));
+  a.root_bc2 = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(h->beta2, static_cast<double>(h->step))));
+  a.grad_scale = h->grad_scale;
+  a.skip = h->skip;
+  a.step_dev = reinterpret_cast<const long long*>(h->step_dev);
+  cudaError_t err = launch_adamw(list, count, a, eight, stream);
+  return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_adamw_step launch");
 }
 
 }  // extern "C"

@@ -238,4 +238,30 @@ struct NormBackwardArgs {
 cudaError_t launch_norm_backward(const NormBackwardArgs& a, cudaStream_t s);
 size_t norm_backward_workspace(long long T, int H);
 
+// AdamW over many tensors (adamw.cu), up to ADAMW_BATCH of them a launch.
+constexpr int ADAMW_BATCH = 96;
+constexpr int ADAMW_STATE_BLOCK = MOE_ADAMW_STATE_BLOCK;
+struct AdamWTensor {
+  void* param;
+  const void* grad;
+  float* master;
+  void *exp_avg, *exp_avg_sq;
+  float *exp_avg_scale, *exp_avg_sq_scale;
+  long long n;
+  int kind;      // 0 fp32, 1 bf16, 2 bf16 with a master; + 3 for fp32 gradients
+  int wide;      // every address allows accesses of four elements
+  float decay;   // 1 - lr * weight_decay
+  uint32_t key;  // of the tensor's random bits
+};
+struct AdamWStep {
+  double lr, beta1, beta2, eps;
+  long long step;
+  float step_size, root_bc2;  // from step; computed anew where step_dev is given
+  const float* grad_scale;
+  const int* skip;
+  const long long* step_dev;
+};
+uint32_t adamw_key(uint64_t seed, uint32_t tensor);
+cudaError_t launch_adamw(const AdamWTensor* tensors, int count, const AdamWStep& h, bool eight, cudaStream_t s);
+
 }  // namespace moe

@@ -598,6 +598,57 @@ MOE_API moe_status moe_norm_out_backward(const moe_norm* n, const void* grad_out
                                          void* workspace, moe_stream_t stream);
 
 /*
+ * AdamW (decoupled weight decay) over many tensors at once, in place:
+ *   g = grad_scale * grad;  m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay) - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * One launch for up to 96 tensors.  The struct and the array of tensors are
+ * HOST memory, read before the call returns; the pointers in them are device
+ * pointers.
+ */
+#define MOE_ADAMW_STATE_BLOCK 256
+typedef struct moe_adamw_tensor {
+  void* param;              /* [n] bf16 or fp32, updated                                    */
+  const void* grad;         /* [n] bf16 or fp32                                             */
+  float* master;            /* [n] fp32 or NULL: the parameter's value, of which a bf16
+                                 param is the rounded copy; only with a bf16 param          */
+  void* exp_avg;            /* m: [n] fp32, or uint8 e4m3 codes                             */
+  void* exp_avg_sq;         /* v: [n] fp32, or uint8 e5m2 codes                             */
+  float* exp_avg_scale;     /* 8-bit states: [ceil(n / 256)], value = code * scale          */
+  float* exp_avg_sq_scale;  /*   (zero codes with any finite scales are a fresh state)      */
+  int64_t n;                /* >= 0; 0 leaves the tensor out of the step                    */
+  int32_t param_dtype;      /* moe_dtype                                                    */
+  int32_t grad_dtype;
+  double weight_decay;
+} moe_adamw_tensor;
+
+typedef struct moe_adamw {
+  double lr, beta1, beta2, eps;
+  int64_t step;               /* >= 1: the number of this step                               */
+  uint64_t seed;              /* of the random rounding of 8-bit v, with the tensor's place
+                                   in the array, the step and the element's index           */
+  int32_t state_bits;         /* 32 or 8, of every tensor's exp_avg and exp_avg_sq           */
+  const float* grad_scale;    /* device, nullable: one factor for all gradients              */
+  const int32_t* skip;        /* device, nullable: non-zero at run time = change nothing     */
+  const int64_t* step_dev;    /* device, nullable: the step's number, read at run time in
+                                   place of `step` (a captured call that is replayed)        */
+} moe_adamw;
+
+/*
+ * Any address that suits its element type will do; addresses of whole 16
+ * bytes (8 for bf16, 4 for codes) are faster.  8-bit states: m is rounded to
+ * the nearest code, v up or down at random with the probability that keeps
+ * its mean, and a positive v never to zero.  A non-finite gradient makes its
+ * element's p, m and v non-finite, and with 8-bit states its block's: use
+ * `skip`.  Errors: MOE_ERR_INVALID_ARG for NULL or misaligned pointers, an
+ * unknown type, a master beside an fp32 param, state_bits not 8 or 32, step <
+ * 1, a beta outside [0, 1), a negative or non-finite lr, eps or weight_decay;
+ * MOE_ERR_UNSUPPORTED_SHAPE for 2^31 blocks of 256 elements or more in 96
+ * tensors.  Nothing is written when arguments are refused.
+ */
+MOE_API moe_status moe_adamw_step(const moe_adamw* h, const moe_adamw_tensor* tensors, int32_t count,
+                                  moe_stream_t stream);
+
+/*
  * Failure-detection self-test.  Runs one CTA whose wait on an mbarrier can
  * never complete, using the bounded-wait helper of the pipelined kernels with
  * a limit of limit_ns (0 < limit_ns <= 1 s).  The wait gives up, the kernel

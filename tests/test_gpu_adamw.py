@@ -1,0 +1,279 @@
+"""AdamW over many tensors against the formulas, in fp64 and op by op.
+
+Tolerances.  With u = 2^-24: m and v are sums of two products, each rounded
+once, so within 4 u of the sum of the terms' magnitudes.  The parameter is
+p (1 - lr wd) - step_size q; p's product and the difference round within 2 u of
+each term's magnitude, and q = m / (sqrt(v) k + eps) is a quotient of numbers
+that are off by a few u, with an approximate root and division of 2 ulp (4 u)
+each, so within 32 u of itself.  8-bit codes come from the same fp32 m and v
+(every operation rounded on its own, in both): m's codes have to equal a
+restatement of the rule bit for bit, and so do v's, whose random bits are a
+stated function of (seed, tensor, step, element).
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+U = 2.0 ** -24
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def moe():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    import combine_topk_multihot_gb300 as m
+    return m
+
+
+def _step64(p, g, m, v, t, lr, b1, b2, eps, wd):
+    p, g, m, v = (x.double() for x in (p, g, m, v))
+    m, v = b1 * m + (1 - b1) * g, b2 * v + (1 - b2) * g * g
+    q = (m / (1 - b1 ** t)) / ((v / (1 - b2 ** t)).sqrt() + eps)
+    return p * (1 - lr * wd) - lr * q, m, v, lr * q
+
+
+SIZES = [1, 3, 255, 256, 257, 511, 4096, 10007, 65536]
+
+
+@pytest.mark.parametrize("pt,master", [(F32, False), (BF16, False), (BF16, True)])
+@pytest.mark.parametrize("gt", [F32, BF16])
+def test_fp32_states(moe, pt, master, gt):
+    g = torch.Generator().manual_seed(11)
+    rnd = lambda n, std=1.0: torch.randn(n, generator=g) * std  # noqa: E731
+    lr, b1, b2, eps = 1e-2, 0.9, 0.99, 1e-8
+    wds = [0.1 * (i % 3) for i in range(len(SIZES))]
+    params = [rnd(n).to(pt).to(DEV) for n in SIZES]
+    opt = moe.AdamWState(params, master=master)
+    held = [t.clone() for t in (opt.master if master else params)]
+    m, v = [torch.zeros(n, device=DEV) for n in SIZES], [torch.zeros(n, device=DEV) for n in SIZES]
+    for t in range(1, 4):
+        grads = [rnd(n, 10.0 ** (t - 2)).to(gt).to(DEV) for n in SIZES]
+        moe.moe_adamw_step(opt, grads, lr, b1, b2, eps, wds)
+        assert opt.step == t
+        for i in range(len(SIZES)):
+            rp, rm, rv, upd = _step64(held[i], grads[i], m[i], v[i], t, lr, b1, b2, eps, wds[i])
+            gm = (1 - b1) * grads[i].double().abs()
+            assert ((opt.exp_avg[i].double() - rm).abs() <= 8 * U * (b1 * m[i].double().abs() + gm)).all()
+            assert ((opt.exp_avg_sq[i].double() - rv).abs() <= 8 * U * rv).all()
+            tol = 4 * U * (held[i].double().abs() + upd.abs()) + 32 * U * upd.abs()
+            if master:
+                assert ((opt.master[i].double() - rp).abs() <= tol).all()
+                assert torch.equal(params[i], opt.master[i].bfloat16())
+            else:
+                if pt == BF16:
+                    tol = tol + 2.0 ** -8 * rp.abs()
+                assert ((params[i].double() - rp).abs() <= tol).all()
+            held[i] = (opt.master[i] if master else params[i]).clone()
+            m[i], v[i] = opt.exp_avg[i].clone(), opt.exp_avg_sq[i].clone()
+
+
+def _mix(x):
+    x = x.astype(np.uint32)
+    x = x ^ (x >> np.uint32(16))
+    x = x * np.uint32(0xA3D95B4F)
+    x = x ^ (x >> np.uint32(15))
+    x = x * np.uint32(0xC2F1E6D3)
+    return x ^ (x >> np.uint32(16))
+
+
+def _random16(n, seed, tensor, step):
+    with np.errstate(over="ignore"):
+        key = np.array([seed & 0xFFFFFFFF], np.uint32)
+        for k in (seed >> 32, tensor, step & 0xFFFFFFFF, step >> 32):
+            key = _mix(key ^ np.uint32(k)) + np.uint32(0x9E3779B9)
+        h = _mix(np.arange((n + 1) // 2, dtype=np.uint32) ^ _mix(key))
+    return np.stack([h & 0xFFFF, h >> 16], 1).reshape(-1)[:n].astype(np.uint32)
+
+
+def _blocks(x):
+    f = np.zeros(-(-len(x) // 256) * 256, np.float32)
+    f[:len(x)] = x
+    return f.reshape(-1, 256)
+
+
+def _encode(m, v, seed, tensor, step):
+    """(m codes, m scales, v codes, v scales) by the rule, in numpy fp32."""
+    f = np.float32
+    bm, bv = _blocks(m), _blocks(v)
+    ms = np.maximum(np.abs(bm).max(1) / f(448), f(2.0 ** -120))
+    vs = np.maximum(bv.max(1) / f(57344), f(2.0 ** -120))
+    tm = (bm * (f(1) / ms)[:, None]).reshape(-1)[:len(m)]
+    mc = torch.from_numpy(tm).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    tv = (bv * (f(1) / vs)[:, None] * f(2.0 ** -112)).reshape(-1)[:len(v)]
+    code = (tv.view(np.uint32) + (_random16(len(v), seed, tensor, step) << 5)) >> 21
+    code = np.where(v > 0, np.clip(code, 1, 0x7B), code).astype(np.uint8)
+    return mc, ms, code, vs
+
+
+def _decode(mc, ms, vc, vs):
+    m = torch.from_numpy(mc).view(torch.float8_e4m3fn).float().numpy()
+    v = torch.from_numpy(vc).view(torch.float8_e5m2).float().numpy()
+    n = len(mc)
+    return (_blocks(m) * ms[:, None]).reshape(-1)[:n], (_blocks(v) * vs[:, None]).reshape(-1)[:n]
+
+
+@pytest.mark.parametrize("pt,master,gt", [(F32, False, F32), (BF16, False, BF16), (BF16, True, F32)])
+def test_8bit_states_bit_exact(moe, pt, master, gt):
+    g = torch.Generator().manual_seed(12)
+    lr, b1, b2, eps, seed = 1e-2, 0.9, 0.95, 1e-8, (7 << 32) + 99
+    f = np.float32
+    params = [torch.randn(n, generator=g).to(pt).to(DEV) for n in SIZES]
+    opt = moe.AdamWState(params, state_bits=8, master=master, seed=seed)
+    for t in range(1, 6):
+        grads = [(torch.randn(n, generator=g) * torch.exp(2 * torch.randn(n, generator=g))).to(gt) for n in SIZES]
+        if t == 3:
+            grads = [x * 0 for x in grads]      # the averages decay
+        if t == 4:
+            for x in grads:
+                x[::2] = 0                      # zeros among others
+        before = [[s[i].cpu().numpy().copy() for s in (opt.exp_avg, opt.exp_avg_scale, opt.exp_avg_sq, opt.exp_avg_sq_scale)]
+                  for i in range(len(SIZES))]
+        held = [x.clone() for x in (opt.master if master else params)]
+        moe.moe_adamw_step(opt, [x.to(DEV) for x in grads], lr, b1, b2, eps)
+        for i in range(len(SIZES)):
+            m, v = _decode(*before[i])
+            gi = grads[i].float().numpy()
+            m = m * f(b1) + gi * f(1 - b1)
+            v = v * f(b2) + gi * gi * f(1 - b2)
+            mc, ms, vc, vs = _encode(m, v, seed, i, t)
+            assert np.array_equal(opt.exp_avg_scale[i].cpu().numpy(), ms), (i, t)
+            assert np.array_equal(opt.exp_avg_sq_scale[i].cpu().numpy(), vs), (i, t)
+            assert np.array_equal(opt.exp_avg[i].cpu().numpy(), mc), (i, t)
+            assert np.array_equal(opt.exp_avg_sq[i].cpu().numpy(), vc), (i, t)
+            assert (vc[v > 0] > 0).all()
+            q = m.astype(np.float64) / (1 - b1 ** t) / (np.sqrt(v.astype(np.float64) / (1 - b2 ** t)) + eps)
+            ref = held[i].double().cpu().numpy() - lr * q
+            got = (opt.master[i] if master else params[i]).double().cpu().numpy()
+            tol = 4 * U * (np.abs(ref) + 2 * np.abs(lr * q)) + 32 * U * np.abs(lr * q)
+            if pt == BF16 and not master:
+                tol = tol + 2.0 ** -8 * np.abs(ref)
+            assert (np.abs(got - ref) <= tol).all(), (i, t)
+
+
+def test_8bit_second_moment_keeps_its_mean(moe):
+    """With b2 close to 1 and a constant gradient below the held value, v decays
+    as the formula does, on the average over many elements: by rounding to
+    nearest it would stay.  One element a block keeps the scale in place.
+    Each step's rounding has a standard deviation of at most half the distance
+    of two codes, a quarter of the value, so the mean over n elements and k
+    steps is within 5 * 0.125 * sqrt(k / n) of its own."""
+    n, k, b2 = 1 << 18, 40, 0.99
+    p = torch.zeros(n, device=DEV)
+    opt = moe.AdamWState([p], state_bits=8, seed=3)
+    top = torch.arange(n, device=DEV) % 256 == 0
+    opt.exp_avg_sq[0][top] = 0x7B
+    opt.exp_avg_sq[0][~top] = 0x60         # 512 in units of the scale
+    opt.exp_avg_sq_scale[0].fill_(1.0)
+    grad = torch.where(top, torch.full((n,), math.sqrt(57344.0), device=DEV), torch.zeros(n, device=DEV))
+    for _ in range(k):
+        moe.moe_adamw_step(opt, [grad], 0.0, 0.9, b2)
+    v = opt.exp_avg_sq[0].view(torch.float8_e5m2).double() * opt.exp_avg_sq_scale[0].double().repeat_interleave(256)
+    mean = float(v[~top].mean()) / 512
+    assert abs(mean / b2 ** k - 1) <= 5 * 0.125 * math.sqrt(k / n) / b2 ** k, mean
+
+
+def test_step_from_the_device_scale_and_skip(moe):
+    g = torch.Generator().manual_seed(4)
+    n = 3000
+    start, grad = torch.randn(n, generator=g).to(DEV), torch.randn(n, generator=g).to(DEV)
+    for bits in (32, 8):
+        a, b = start.clone(), start.clone()
+        oa, ob = moe.AdamWState([a], bits, seed=5, step=41), moe.AdamWState([b], bits, seed=5, step=0)
+        moe.moe_adamw_step(oa, [grad * 0.25], 1e-2)
+        scale, step = torch.tensor([0.25], device=DEV), torch.tensor([42], device=DEV)
+        skip = torch.tensor([1], dtype=torch.int32, device=DEV)
+        kw = dict(grad_scale=scale, skip=skip, step=step)
+        moe.moe_adamw_step(ob, [grad], 1e-2, **kw)
+        assert torch.equal(b, start) and not ob.exp_avg[0].any() and not ob.exp_avg_sq[0].any()
+        skip.zero_()
+        moe.moe_adamw_step(ob, [grad], 1e-2, **kw)
+        assert ob.step == 0 and oa.step == 42
+        # the bias corrections may differ by one rounding between the host's pow and the device's
+        assert torch.allclose(a, b, rtol=1e-6, atol=0)
+        assert torch.equal(oa.exp_avg[0], ob.exp_avg[0]) and torch.equal(oa.exp_avg_sq[0], ob.exp_avg_sq[0])
+
+
+def test_captured_with_a_step_on_the_device(moe):
+    g = torch.Generator().manual_seed(6)
+    p = torch.randn(5000, generator=g).to(DEV)
+    q, grad = p.clone(), torch.randn(5000, generator=g).to(DEV)
+    step = torch.ones(1, dtype=torch.int64, device=DEV)
+    oq = moe.AdamWState([q], 8, seed=1)
+    moe.moe_adamw_step(moe.AdamWState([torch.zeros_like(q)], 8), [grad], 1e-3, step=step)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.moe_adamw_step(oq, [grad], 1e-3, step=step)
+        step += 1
+    op = moe.AdamWState([p], 8, seed=1)
+    for _ in range(3):
+        graph.replay()
+        moe.moe_adamw_step(op, [grad], 1e-3)
+    torch.cuda.synchronize()
+    assert int(step) == 4 and torch.allclose(p, q, rtol=1e-6, atol=1e-9)
+    assert torch.equal(op.exp_avg_sq[0], oq.exp_avg_sq[0])
+
+
+def test_many_unaligned_and_empty_tensors(moe):
+    """More tensors than one launch takes, slices at odd addresses, tensors of
+    no elements, and parameters without a gradient."""
+    g = torch.Generator().manual_seed(8)
+    flat, fgrad = torch.randn(40000, generator=g).to(DEV), torch.randn(40000, generator=g).to(DEV)
+    cuts = [0] + sorted(torch.randperm(39999, generator=g)[:230].add(1).tolist()) + [40000]
+    params = [flat[a:b] for a, b in zip(cuts, cuts[1:])] + [flat[:0]]
+    grads = [fgrad[a:b] for a, b in zip(cuts, cuts[1:])] + [fgrad[:0]]
+    grads[7] = grads[101] = None
+    held = flat.clone()
+    opt = moe.AdamWState(params)
+    moe.moe_adamw_step(opt, grads, 1e-2, weight_decay=0.1)
+    whole = held.clone()
+    ow = moe.AdamWState([whole])
+    moe.moe_adamw_step(ow, [fgrad], 1e-2, weight_decay=0.1)
+    for k in (7, 101):
+        whole[cuts[k]:cuts[k + 1]] = held[cuts[k]:cuts[k + 1]]
+    assert torch.equal(flat, whole)
+    moe.moe_adamw_step(moe.AdamWState([]), [], 1e-2)
+
+
+def test_nonfinite_gradients_stay_in_their_block(moe):
+    p = torch.ones(1024, device=DEV)
+    grad = torch.ones(1024, device=DEV)
+    grad[300], grad[700] = float("nan"), float("inf")
+    opt = moe.AdamWState([p], 8)
+    moe.moe_adamw_step(opt, [grad], 1e-2)
+    bad = ~torch.isfinite(p)
+    assert bad.nonzero().flatten().tolist() == [300, 700]
+    moe.moe_adamw_step(opt, [torch.ones_like(grad)], 1e-2)
+    assert torch.isfinite(p[:256]).all() and torch.isfinite(p[768:]).all()
+    assert not torch.isfinite(opt.exp_avg_scale[0][1:3]).any() and torch.isfinite(opt.exp_avg_scale[0][[0, 3]]).all()
+
+
+def test_refusals(moe):
+    p = torch.zeros(64, device=DEV)
+    opt = moe.AdamWState([p])
+    with pytest.raises(ValueError, match="GPU"):
+        moe.AdamWState([p.cpu()])
+    with pytest.raises(TypeError, match="bfloat16 or float32"):
+        moe.AdamWState([p.half()])
+    with pytest.raises(ValueError, match="8 or 32"):
+        moe.AdamWState([p], state_bits=16)
+    with pytest.raises(ValueError, match="exp_avg"):
+        moe.AdamWState([p], exp_avg=[torch.zeros(63, device=DEV)])
+    with pytest.raises(ValueError, match="gradients for"):
+        moe.moe_adamw_step(opt, [], 1e-3)
+    with pytest.raises(ValueError, match="shape"):
+        moe.moe_adamw_step(opt, [p[:32]], 1e-3)
+    with pytest.raises(TypeError, match="grads"):
+        moe.moe_adamw_step(opt, [p.half()], 1e-3)
+    with pytest.raises(ValueError, match="contiguous"):
+        moe.moe_adamw_step(opt, [torch.zeros(128, device=DEV)[::2]], 1e-3)
+    with pytest.raises(TypeError, match="skip"):
+        moe.moe_adamw_step(opt, [p], 1e-3, skip=torch.zeros(1, device=DEV))
+    for kw in (dict(lr=-1.0), dict(lr=float("nan")), dict(lr=1e-3, beta1=1.0), dict(lr=1e-3, eps=-1.0),
+               dict(lr=1e-3, weight_decay=-0.1)):
+        with pytest.raises(moe.MoEError, match="INVALID_ARG"):
+            moe.moe_adamw_step(opt, [p], **kw)
+    assert opt.step == 0 and not p.any()
