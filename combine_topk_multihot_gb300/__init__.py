@@ -14,7 +14,9 @@ from .moe import (Layout, MoEError, ForwardResult, worst_case_rows, moe_router_t
                   moe_grouped_experts, moe_combine, moe_combine_backward,
                   moe_dispatch_backward, moe_route_to_multihot_backward, moe_layer_forward,
                   moe_grouped_experts_backward)
-from .block import AdamWState, moe_adamw_step, moe_norm_in, moe_norm_in_backward, moe_norm_out, moe_norm_out_backward
+from .block import (moe_norm_in, moe_norm_in_backward, moe_norm_out, moe_norm_out_backward,
+                    AdamWState, moe_adamw_step,
+                    moe_quantize_fp8_block, moe_matmul_fp8_block, moe_grouped_experts_fp8_block)
 from . import _native
 from . import ops
 from .ops import moe_layer, moe_layer_from_logits
@@ -29,5 +31,6 @@ __all__ = [
     "moe_dispatch_backward", "moe_route_to_multihot_backward", "moe_layer_forward",
     "moe_grouped_experts_backward", "moe_norm_in", "moe_norm_in_backward", "moe_norm_out", "moe_norm_out_backward",
     "AdamWState", "moe_adamw_step",
+    "moe_quantize_fp8_block", "moe_matmul_fp8_block", "moe_grouped_experts_fp8_block",
     "_native", "ops", "moe_layer", "moe_layer_from_logits",
 ]

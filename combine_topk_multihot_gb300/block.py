@@ -3,7 +3,10 @@
 * moe_norm_in / moe_norm_out and their backwards: the RMS norms before and
   after a block, fused with its gate and residual scale;
 * AdamWState / moe_adamw_step: the optimiser's step over many tensors at once,
-  its averages in fp32 or in 8 bits.
+  its averages in fp32 or in 8 bits;
+* moe_quantize_fp8_block, moe_matmul_fp8_block and
+  moe_grouped_experts_fp8_block: products of e4m3 codes with a scale for each
+  block of 128.
 
 As in ``moe.py`` the functions carry the names of the C entry points, all
 arithmetic runs in the CUDA library, and PyTorch only allocates the buffers and
@@ -19,7 +22,7 @@ import numpy as np
 import torch
 
 from . import _native as N
-from .moe import _check
+from .moe import Layout, _check
 
 _DTYPES = {torch.bfloat16: N.MOE_DTYPE_BF16, torch.float32: N.MOE_DTYPE_F32}
 _GATES = {0: N.MOE_GATE_NONE, 1: N.MOE_GATE_TOKEN, 2: N.MOE_GATE_ELEMENT}
@@ -283,3 +286,78 @@ def moe_adamw_step(state: AdamWState, grads: Sequence[Optional[torch.Tensor]], l
         state.step += 1
     if params:
         torch.autograd.graph.increment_version(params)
+
+
+# ------------------------------------------------------------------ e4m3 with a scale per block of 128
+def _blocks(n: int) -> int:
+    return -(-n // 128)
+
+
+def moe_quantize_fp8_block(src: torch.Tensor, block_rows: int = 1, out=None, stream=None):
+    """e4m3 codes of a bf16 tensor [..., rows, cols] (uint8, same shape) and fp32
+    scales [..., ceil(rows / block_rows), ceil(cols / 128)]: block_rows=1 for
+    activations, 128 for weights.  cols is a multiple of 16."""
+    dev = _on_gpu(src, "src")
+    if src.dim() < 2:
+        raise ValueError(f"src must be [..., rows, cols] (got {tuple(src.shape)})")
+    rows, cols = src.shape[-2:]
+    lead = src.shape[:-2]
+    batch = lead.numel()
+    if block_rows not in (1, 128):
+        raise ValueError(f"block_rows must be 1 or 128 (got {block_rows})")
+    shape = (*lead, -(-rows // block_rows), _blocks(cols))
+    if out is None:
+        out = (torch.empty(src.shape, dtype=torch.uint8, device=dev), torch.empty(shape, dtype=torch.float32, device=dev))
+    codes, scales = out
+    _check(N.lib.moe_quantize_fp8_block(_need(src, "src", torch.bfloat16, src.shape, dev), batch, rows, cols, block_rows,
+                                        _need(codes, "codes", torch.uint8, src.shape, dev),
+                                        _need(scales, "scales", torch.float32, shape, dev), _raw_stream(stream)),
+           "moe_quantize_fp8_block")
+    return codes, scales
+
+
+def moe_matmul_fp8_block(a_q: torch.Tensor, a_scale: torch.Tensor, b_q: torch.Tensor, b_scale: torch.Tensor,
+                         out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None):
+    """a b^T of codes [M, K] and [N, K] with their scales (block_rows 1 and 128):
+    [M, N] bf16."""
+    dev = _on_gpu(a_q, "a_q")
+    M, K = _rows(a_q, "a_q")
+    n = _rows(b_q, "b_q")[0]
+    if out is None:
+        out = torch.empty(M, n, dtype=torch.bfloat16, device=dev)
+    kb = _blocks(K)
+    _check(N.lib.moe_matmul_fp8_block(_need(a_q, "a_q", torch.uint8, (M, K), dev),
+                                      _need(a_scale, "a_scale", torch.float32, (M, kb), dev), M,
+                                      _need(b_q, "b_q", torch.uint8, (n, K), dev),
+                                      _need(b_scale, "b_scale", torch.float32, (_blocks(n), kb), dev), n, K,
+                                      _need(out, "out", torch.bfloat16, (M, n), dev),
+                                      None if status is None else _need(status, "status", torch.int32, (1,), dev),
+                                      _raw_stream(stream)), "moe_matmul_fp8_block")
+    return out
+
+
+def moe_grouped_experts_fp8_block(x_disp: torch.Tensor, layout: Layout, W1_q: torch.Tensor, W1_scale: torch.Tensor,
+                                  W2_q: torch.Tensor, W2_scale: torch.Tensor, out: Optional[torch.Tensor] = None,
+                                  stream=None):
+    """The grouped SwiGLU experts from e4m3 weights with 128 x 128 block scales:
+    y [C, H] bf16 with the routing weights applied, for moe_combine."""
+    dev = _on_gpu(x_disp, "x_disp")
+    C, H = layout.capacity, _rows(x_disp, "x_disp")[1]
+    if W1_q.dim() != 3 or W1_q.shape[1] % 2:
+        raise ValueError(f"W1_q must be [E, 2I, H] (got {tuple(W1_q.shape)})")
+    E, I = layout.E, W1_q.shape[1] // 2
+    if out is None:
+        out = torch.empty(C, H, dtype=torch.bfloat16, device=dev)
+    nbytes = ctypes.c_size_t(0)
+    _check(N.lib.moe_experts_fp8_block_workspace_bytes(C, layout.T, H, I, ctypes.byref(nbytes)),
+           "moe_experts_fp8_block_workspace_bytes")
+    ws = torch.empty(nbytes.value, dtype=torch.uint8, device=dev)
+    _check(N.lib.moe_grouped_experts_fp8_block(
+        _need(x_disp, "x_disp", torch.bfloat16, (C, H), dev), layout.ref, H, I,
+        _need(W1_q, "W1_q", torch.uint8, (E, 2 * I, H), dev),
+        _need(W1_scale, "W1_scale", torch.float32, (E, _blocks(2 * I), _blocks(H)), dev),
+        _need(W2_q, "W2_q", torch.uint8, (E, H, I), dev),
+        _need(W2_scale, "W2_scale", torch.float32, (E, _blocks(H), _blocks(I)), dev),
+        _need(out, "out", torch.bfloat16, (C, H), dev), ws.data_ptr() or None, _raw_stream(stream)),
+        "moe_grouped_experts_fp8_block")
+    return out

@@ -32,6 +32,7 @@
 #include <cuda_fp8.h>
 
 #include "common.cuh"
+#include "fp8_quant.cuh"
 #include "launch.h"
 
 namespace moe {
@@ -47,12 +48,6 @@ struct Table {
   int first[ADAMW_BATCH + 1];  // number of each tensor's first block
   int count;
 };
-
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
 
 __device__ __forceinline__ float warp_max_nan(float v) {
 #pragma unroll

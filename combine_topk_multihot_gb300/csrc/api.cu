@@ -911,3 +911,115 @@ moe_status moe_adamw_step(const moe_adamw* h, const moe_adamw_tensor* tensors, i
 }
 
 }  // extern "C"
+
+namespace {
+
+// The experts' scratch: x's codes and scales, h's, and for few rows the fp32
+// gate/up rows; each from a 256-byte boundary.
+struct BlockWorkspace {
+  size_t x_q, x_scale, h_q, h_scale, gu, total;
+};
+
+BlockWorkspace block_workspace(int64_t C, int32_t T, int32_t H, int32_t I) {
+  const size_t c = static_cast<size_t>(C);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += (bytes + 255) / 256 * 256;
+    return here;
+  };
+  BlockWorkspace w;
+  w.x_q = take(c * H);
+  w.x_scale = take(c * ((H + 127) / 128) * sizeof(float));
+  w.h_q = take(c * I);
+  w.h_scale = take(c * ((I + 127) / 128) * sizeof(float));
+  w.gu = take(T <= BLOCK_STREAM_ROWS ? c * 2 * I * sizeof(float) : 0);
+  w.total = at;
+  return w;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_quantize_fp8_block(const moe_bf16* src, int64_t batch, int64_t rows, int32_t cols, int32_t block_rows,
+                                  uint8_t* codes, float* scales, moe_stream_t stream) {
+  MOE_REQUIRE(batch >= 0 && rows >= 0, MOE_ERR_INVALID_ARG, "moe_quantize_fp8_block: batch and rows must be >= 0");
+  MOE_REQUIRE(cols > 0 && cols % 16 == 0, MOE_ERR_UNSUPPORTED_SHAPE,
+              "moe_quantize_fp8_block: cols must be a positive multiple of 16 (got %d)", cols);
+  MOE_REQUIRE(block_rows == 1 || block_rows == 128, MOE_ERR_INVALID_ARG,
+              "moe_quantize_fp8_block: block_rows must be 1 or 128 (got %d)", block_rows);
+  MOE_REQUIRE(rows < (int64_t(1) << 31) && batch < (int64_t(1) << 31) &&
+                  batch * ((rows + block_rows - 1) / block_rows) < (int64_t(1) << 31) / ((cols + 127) / 128),
+              MOE_ERR_UNSUPPORTED_SHAPE, "moe_quantize_fp8_block: 2^31 blocks or more");
+  MOE_REQUIRE(batch == 0 || rows == 0 || (src && codes && scales), MOE_ERR_INVALID_ARG,
+              "moe_quantize_fp8_block: NULL pointer");
+  MOE_REQUIRE(all_aligned16(src, codes, scales), MOE_ERR_INVALID_ARG,
+              "moe_quantize_fp8_block: pointers must be 16-byte aligned");
+  moe_status st = check_device();
+  if (st != MOE_OK) return st;
+  cudaError_t err = launch_quantize_block(src, batch, rows, cols, block_rows, codes, scales, nullptr, stream);
+  return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_quantize_fp8_block launch");
+}
+
+moe_status moe_matmul_fp8_block(const uint8_t* a_q, const float* a_scale, int32_t M, const uint8_t* b_q,
+                                const float* b_scale, int32_t N, int32_t K, moe_bf16* out, int32_t* status,
+                                moe_stream_t stream) {
+  MOE_REQUIRE(M >= 0 && N >= 1, MOE_ERR_INVALID_ARG, "moe_matmul_fp8_block: M must be >= 0 and N >= 1 (got %d, %d)", M,
+              N);
+  MOE_REQUIRE(K >= 16 && K % 16 == 0, MOE_ERR_UNSUPPORTED_SHAPE,
+              "moe_matmul_fp8_block: K must be a positive multiple of 16 (got %d)", K);
+  MOE_REQUIRE(M == 0 || (a_q && a_scale && b_q && b_scale && out), MOE_ERR_INVALID_ARG,
+              "moe_matmul_fp8_block: NULL pointer");
+  MOE_REQUIRE(all_aligned16(a_q, a_scale, b_q, b_scale, out), MOE_ERR_INVALID_ARG,
+              "moe_matmul_fp8_block: pointers must be 16-byte aligned");
+  MOE_REQUIRE((static_cast<int64_t>(M) + 127) / 128 * ((N + 63) / 64) < (int64_t(1) << 31), MOE_ERR_UNSUPPORTED_SHAPE,
+              "moe_matmul_fp8_block: too many tiles");
+  moe_status st = check_device();
+  if (st != MOE_OK) return st;
+  if (M == 0) return MOE_OK;
+  cudaError_t err = M <= BLOCK_STREAM_ROWS
+                        ? launch_block_matmul_stream(a_q, a_scale, M, b_q, b_scale, N, K, out, stream)
+                        : launch_block_matmul_tc(a_q, a_scale, M, b_q, b_scale, N, K, out, status, stream);
+  return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_matmul_fp8_block launch");
+}
+
+moe_status moe_experts_fp8_block_workspace_bytes(int64_t capacity, int32_t T, int32_t H, int32_t I, size_t* bytes) {
+  MOE_REQUIRE(bytes != nullptr, MOE_ERR_INVALID_ARG, "bytes is NULL");
+  MOE_REQUIRE(capacity >= 0 && T >= 0 && H > 0 && I > 0, MOE_ERR_INVALID_ARG, "bad capacity / T / H / I");
+  *bytes = block_workspace(capacity, T, H, I).total;
+  return MOE_OK;
+}
+
+moe_status moe_grouped_experts_fp8_block(const moe_bf16* x_disp, const moe_layout* L, int32_t H, int32_t I,
+                                         const uint8_t* W1_q, const float* W1_scale, const uint8_t* W2_q,
+                                         const float* W2_scale, moe_bf16* y_disp, void* workspace,
+                                         moe_stream_t stream) {
+  moe_status st = check_layout(L);
+  if (st != MOE_OK) return st;
+  if ((st = check_hidden(H)) != MOE_OK) return st;
+  MOE_REQUIRE(I > 0 && I % 128 == 0, MOE_ERR_UNSUPPORTED_SHAPE,
+              "the intermediate size must be a positive multiple of 128 (got %d)", I);
+  MOE_REQUIRE(L->capacity == 0 || (x_disp && W1_q && W1_scale && W2_q && W2_scale && y_disp && workspace),
+              MOE_ERR_INVALID_ARG, "moe_grouped_experts_fp8_block: NULL pointer");
+  MOE_REQUIRE(all_aligned16(x_disp, W1_q, W1_scale, W2_q, W2_scale, y_disp, workspace), MOE_ERR_INVALID_ARG,
+              "moe_grouped_experts_fp8_block: pointers must be 16-byte aligned");
+  if ((st = check_device()) != MOE_OK) return st;
+  if (L->capacity == 0 || L->T == 0) return MOE_OK;
+  const BlockWorkspace w = block_workspace(L->capacity, L->T, H, I);
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  uint8_t* x_q = base + w.x_q;
+  float* x_scale = reinterpret_cast<float*>(base + w.x_scale);
+  uint8_t* h_q = base + w.h_q;
+  float* h_scale = reinterpret_cast<float*>(base + w.h_scale);
+  cudaError_t err = launch_quantize_block(x_disp, 1, L->capacity, H, 1, x_q, x_scale, L->row_token, stream);
+  if (err == cudaSuccess)
+    err = L->T <= BLOCK_STREAM_ROWS
+              ? launch_block_experts_stream(x_q, x_scale, *L, H, I, W1_q, W1_scale, W2_q, W2_scale,
+                                            reinterpret_cast<float*>(base + w.gu), h_q, h_scale, y_disp, stream)
+              : launch_block_experts_tc(x_q, x_scale, *L, H, I, W1_q, W1_scale, W2_q, W2_scale, h_q, h_scale, y_disp,
+                                        stream);
+  return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_grouped_experts_fp8_block launch");
+}
+
+}  // extern "C"

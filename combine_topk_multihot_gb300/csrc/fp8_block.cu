@@ -1,0 +1,395 @@
+// e4m3 codes with a scale for each block of 128: quantisation, and the
+// products with few rows.
+//
+// Codes and scales: scale = max|v| / 448 over a block (1 for a block of
+// zeros), code = e4m3(v / scale) to nearest even; a block is 128 columns of
+// one row (activations) or 128 x 128 (weights).  Both kernels read their input
+// once and are bound by HBM.
+//
+// With at most 32 rows (per expert) the product is a stream over the weights:
+// every weight is used at most 32 times.  A 128-row tile of the tensor-core
+// kernel would be empty for the most part, and its tiles too few to keep all
+// SMs loading.  Here a warp takes 16 weight rows and a slice of K, loads them
+// straight into registers in 16-byte pieces (64 consecutive bytes of a row
+// per four lanes), and multiplies with mma.sync: the weights are its 16-row
+// operand, 8 tokens the other, both with the same permutation of K (a
+// lane's 16 bytes are 16 consecutive codes of one row in either operand, so
+// no shuffle or shared memory is needed).  The instruction sums 32 products
+// of codes exactly in fp32; after the four of a block, its scales are applied
+// in fp32.  The slices of K are joined in shared memory in a fixed order.
+
+#include "common.cuh"
+#include "fp8_quant.cuh"
+#include "launch.h"
+
+namespace moe {
+
+namespace {
+
+// ---------------------------------------------------------------- quantisation
+
+// A warp takes up to four 256-column pieces (two blocks each) of one row:
+// lane l holds 8 values, 16 lanes a block.  blockIdx.y picks the pieces.
+constexpr int PIECES = 4;
+__global__ void __launch_bounds__(256) quantize_row_blocks_kernel(const uint16_t* __restrict__ src, long long rows,
+                                                                  int cols, uint8_t* __restrict__ codes,
+                                                                  float* __restrict__ scales,
+                                                                  const int* __restrict__ row_token) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31;
+  const int blocks = (cols + 127) >> 7;
+  const int col0 = blockIdx.y * (PIECES * 256) + lane * 8;
+  const long long nwarps = static_cast<long long>(gridDim.x) * (blockDim.x >> 5);
+  for (long long r = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); r < rows;
+       r += nwarps) {
+    if (row_token && __ldg(row_token + r) < 0) continue;
+    uint4 q[PIECES];
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p) {
+      const int c = col0 + 256 * p;
+      q[p] = c < cols ? __ldcs(reinterpret_cast<const uint4*>(src + r * cols + c)) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p) {
+      const uint32_t w[4] = {q[p].x, q[p].y, q[p].z, q[p].w};
+      float top = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = max_nan(top, max_nan(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(FULL_MASK, top, o));
+      const float scale = block_scale(top);
+      const int c = col0 + 256 * p;
+      if (c < cols) {
+        *reinterpret_cast<uint2*>(codes + r * cols + c) =
+            make_uint2(e4m3x4(bf16_lo(w[0]), bf16_hi(w[0]), bf16_lo(w[1]), bf16_hi(w[1]), scale),
+                       e4m3x4(bf16_lo(w[2]), bf16_hi(w[2]), bf16_lo(w[3]), bf16_hi(w[3]), scale));
+        if ((lane & 15) == 0) scales[r * blocks + (c >> 7)] = scale;
+      }
+    }
+  }
+}
+
+// A CTA takes one 128 x 128 block: thread t holds 8 columns of rows t / 16 +
+// 16 i.  Rows and columns past the matrix count as zeros.
+__global__ void __launch_bounds__(256) quantize_square_blocks_kernel(const uint16_t* __restrict__ src, int rows,
+                                                                     int cols, uint8_t* __restrict__ codes,
+                                                                     float* __restrict__ scales) {
+  __shared__ float s_top[8];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int nr = (rows + 127) >> 7, nc = (cols + 127) >> 7;
+  const long long block = blockIdx.x;
+  const long long mat = block / (static_cast<long long>(nr) * nc);
+  const int rem = static_cast<int>(block - mat * nr * nc);
+  const int br = rem / nc, bc = rem - br * nc;
+  const int c = bc * 128 + (threadIdx.x & 15) * 8;
+  const int r0 = br * 128 + (threadIdx.x >> 4);
+  const long long base = mat * rows * cols;
+  uint4 q[8];
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = r0 + 16 * i;
+    q[i] = r < rows && c < cols ? __ldcs(reinterpret_cast<const uint4*>(src + base + static_cast<long long>(r) * cols + c))
+                                : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top = max_nan(top, max_nan(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(FULL_MASK, top, o));
+  if ((threadIdx.x & 31) == 0) s_top[threadIdx.x >> 5] = top;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max_nan(top, s_top[i]);
+  const float scale = block_scale(top);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = r0 + 16 * i;
+    if (r < rows && c < cols) {
+      const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+      *reinterpret_cast<uint2*>(codes + base + static_cast<long long>(r) * cols + c) =
+          make_uint2(e4m3x4(bf16_lo(w[0]), bf16_hi(w[0]), bf16_lo(w[1]), bf16_hi(w[1]), scale),
+                     e4m3x4(bf16_lo(w[2]), bf16_hi(w[2]), bf16_lo(w[3]), bf16_hi(w[3]), scale));
+    }
+  }
+  if (threadIdx.x == 0) scales[block] = scale;
+}
+
+// ---------------------------------------------------------------- few rows
+
+__device__ __forceinline__ void mma_e4m3_16x8x32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+enum StreamMode { STREAM_BF16 = 0, STREAM_WEIGHTED = 1, STREAM_F32 = 2 };
+
+struct StreamArgs {
+  const int* counts;   // [E]; NULL: one group of `rows` rows
+  const int* offsets;  // [E + 1]
+  int rows, E;
+  int N, K, k_blocks;  // weight rows per expert, codes per row
+  int n_blocks;        // scale rows per expert
+  int split;           // slices of K a CTA's warps are divided into (1, 2, 4 or 8)
+  const uint8_t* a;
+  const float* a_scale;
+  const uint8_t* w;
+  const float* w_scale;
+  const float* row_weight;
+  void* out;  // [rows, N] bf16, or fp32
+};
+
+// NT: 8-token tiles a group may have.  Items are (group with rows, 16-row
+// slabs of its weights, 8 / split of them at a time).
+template <int NT, int MODE>
+__global__ void __launch_bounds__(256) stream_kernel(const StreamArgs args) {
+  extern __shared__ int s_list[];  // the experts with rows, ascending
+  __shared__ int s_active;
+  __shared__ float s_part[8][NT][4][32];  // [warp][tile][register][lane]
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (!args.counts) {
+    if (threadIdx.x == 0) {
+      s_list[0] = 0;
+      s_active = 1;
+    }
+  } else if (warp == 0) {
+    int n = 0;
+    for (int e0 = 0; e0 < args.E; e0 += 32) {
+      const bool has = e0 + lane < args.E && args.counts[e0 + lane] > 0;
+      const unsigned m = __ballot_sync(FULL_MASK, has);
+      if (has) s_list[n + __popc(m & ((1u << lane) - 1u))] = e0 + lane;
+      n += __popc(m);
+    }
+    if (lane == 0) s_active = n;
+  }
+  __syncthreads();
+  const int split = args.split, slabs = 8 / split;
+  const int ks = warp % split, slab = warp / split;
+  const int per_group = ((args.N + 15) / 16 + slabs - 1) / slabs;
+  const int items = s_active * per_group;
+  const int per_slice = (args.k_blocks + split - 1) / split;
+  const int kb0 = ks * per_slice, kb1 = min(kb0 + per_slice, args.k_blocks);
+  const int g = lane >> 2, t = lane & 3;
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    const int which = item / per_group;
+    const int e = s_list[which];
+    const int n0 = ((item - which * per_group) * slabs + slab) * 16;
+    // an expert has at most T <= 8 NT rows: a token names it at most once
+    const int cnt = min(args.counts ? args.counts[e] : args.rows, 8 * NT);
+    const long long row0 = args.counts ? args.offsets[e] : 0;
+    float acc[NT][4];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+    if (n0 < args.N) {
+      // weight rows past N repeat the last one; their sums are not stored
+      const uint8_t* w_lo = args.w + (static_cast<long long>(e) * args.N + min(n0 + g, args.N - 1)) * args.K + 16 * t;
+      const uint8_t* w_hi = args.w + (static_cast<long long>(e) * args.N + min(n0 + g + 8, args.N - 1)) * args.K + 16 * t;
+      const float* sb = args.w_scale + (static_cast<long long>(e) * args.n_blocks + (n0 >> 7)) * args.k_blocks;
+#pragma unroll 2
+      for (int kb = kb0; kb < kb1; ++kb) {
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        uint4 wl[2], wh[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {  // 64 codes of each row
+          const int k = kb * 128 + 64 * j;
+          const bool in = k + 16 * t < args.K;
+          wl[j] = in ? __ldcs(reinterpret_cast<const uint4*>(w_lo + k)) : zero;
+          wh[j] = in ? __ldcs(reinterpret_cast<const uint4*>(w_hi + k)) : zero;
+        }
+        const float sbk = __ldg(sb + kb);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if (8 * n >= cnt) break;
+          const long long tok = row0 + 8 * n + g;
+          float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int k = kb * 128 + 64 * j + 16 * t;
+            const uint4 b = 8 * n + g < cnt && k < args.K
+                                ? __ldg(reinterpret_cast<const uint4*>(args.a + tok * args.K + k)) : zero;
+            const uint32_t a0[4] = {wl[j].x, wh[j].x, wl[j].y, wh[j].y};
+            const uint32_t a1[4] = {wl[j].z, wh[j].z, wl[j].w, wh[j].w};
+            mma_e4m3_16x8x32(d, a0, b.x, b.y);
+            mma_e4m3_16x8x32(d, a1, b.z, b.w);
+          }
+          // this lane's sums are those of tokens 2t and 2t + 1
+          const int c = 8 * n + 2 * t;
+          const float s0 = c < cnt ? __ldg(args.a_scale + (row0 + c) * args.k_blocks + kb) * sbk : 0.f;
+          const float s1 = c + 1 < cnt ? __ldg(args.a_scale + (row0 + c + 1) * args.k_blocks + kb) * sbk : 0.f;
+          acc[n][0] = fmaf(d[0], s0, acc[n][0]);
+          acc[n][1] = fmaf(d[1], s1, acc[n][1]);
+          acc[n][2] = fmaf(d[2], s0, acc[n][2]);
+          acc[n][3] = fmaf(d[3], s1, acc[n][3]);
+        }
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s_part[warp][n][i][lane] = acc[n][i];
+    __syncthreads();
+    // outputs (slab, token, weight row), weight rows fastest
+    const int outs = slabs * cnt * 16;
+    for (int i = threadIdx.x; i < outs; i += blockDim.x) {
+      const int r = i & 15, st = i >> 4;
+      const int sl = st / cnt, tok = st - sl * cnt;
+      const int n = ((item - which * per_group) * slabs + sl) * 16 + r;
+      if (n >= args.N) continue;
+      const int ln = (r & 7) * 4 + ((tok & 7) >> 1), reg = (r >> 3) * 2 + (tok & 1);
+      float v = 0.f;
+      for (int k = 0; k < split; ++k) v += s_part[sl * split + k][tok >> 3][reg][ln];
+      const long long row = row0 + tok;
+      if constexpr (MODE == STREAM_F32) {
+        static_cast<float*>(args.out)[row * args.N + n] = v;
+      } else {
+        if constexpr (MODE == STREAM_WEIGHTED) v *= args.row_weight[row];
+        static_cast<uint16_t*>(args.out)[row * args.N + n] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// h = silu(g) u of the fp32 gate/up rows, quantised without leaving fp32:
+// the piece layout of quantize_row_blocks_kernel, one piece a warp.
+__global__ void __launch_bounds__(256) swiglu_quantize_kernel(const float* __restrict__ gu, long long rows, int I,
+                                                              uint8_t* __restrict__ codes,
+                                                              float* __restrict__ scales,
+                                                              const int* __restrict__ row_token) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31;
+  const int c = blockIdx.y * 256 + lane * 8;
+  const long long nwarps = static_cast<long long>(gridDim.x) * (blockDim.x >> 5);
+  for (long long r = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); r < rows;
+       r += nwarps) {
+    if (row_token[r] < 0) continue;
+    float h[8] = {};
+    float top = 0.f;
+    if (c < I) {
+      const float4* g4 = reinterpret_cast<const float4*>(gu + r * 2 * I + c);
+      const float4* u4 = reinterpret_cast<const float4*>(gu + r * 2 * I + I + c);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const float4 g = g4[q], u = u4[q];
+        h[4 * q] = g.x / (1.0f + __expf(-g.x)) * u.x;
+        h[4 * q + 1] = g.y / (1.0f + __expf(-g.y)) * u.y;
+        h[4 * q + 2] = g.z / (1.0f + __expf(-g.z)) * u.z;
+        h[4 * q + 3] = g.w / (1.0f + __expf(-g.w)) * u.w;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = max_nan(top, fabsf(h[i]));
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(FULL_MASK, top, o));
+    if (c < I) {
+      const float scale = block_scale(top);
+      *reinterpret_cast<uint2*>(codes + r * I + c) =
+          make_uint2(e4m3x4(h[0], h[1], h[2], h[3], scale), e4m3x4(h[4], h[5], h[6], h[7], scale));
+      if ((lane & 15) == 0) scales[r * (I >> 7) + (c >> 7)] = scale;
+    }
+  }
+}
+
+template <int MODE>
+cudaError_t launch_stream(StreamArgs g, int most_rows, long long groups, cudaStream_t s) {
+  // as many slices of K as leave a warp two blocks or more
+  g.split = g.k_blocks >= 16 ? 8 : g.k_blocks >= 8 ? 4 : g.k_blocks >= 4 ? 2 : 1;
+  const int slabs = 8 / g.split;
+  const long long items = groups * (((g.N + 15) / 16 + slabs - 1) / slabs);
+  const long long most = 8LL * sm_count();
+  const unsigned grid = static_cast<unsigned>(items < most ? items : most);
+  const size_t smem = static_cast<size_t>(g.E) * sizeof(int);
+  if (most_rows <= 8) return launch_dependent(stream_kernel<1, MODE>, grid, 256, smem, s, g);
+  if (most_rows <= 16) return launch_dependent(stream_kernel<2, MODE>, grid, 256, smem, s, g);
+  return launch_dependent(stream_kernel<4, MODE>, grid, 256, smem, s, g);
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_block(const uint16_t* src, long long batch, long long rows, int cols, int block_rows,
+                                  uint8_t* codes, float* scales, const int* row_token, cudaStream_t s) {
+  if (batch == 0 || rows == 0) return cudaSuccess;
+  if (block_rows == 1) {
+    const long long all = batch * rows;
+    const int y = (cols + PIECES * 256 - 1) / (PIECES * 256);
+    const long long need = (all + 7) / 8, most = (8LL * sm_count() + y - 1) / y;
+    const dim3 grid(static_cast<unsigned>(need < most ? need : most), y);
+    return launch_dependent(quantize_row_blocks_kernel, grid, 256, 0, s, src, all, cols, codes, scales, row_token);
+  }
+  const long long blocks = batch * ((rows + 127) / 128) * ((cols + 127) / 128);
+  return launch_dependent(quantize_square_blocks_kernel, static_cast<unsigned>(blocks), 256, 0, s, src,
+                          static_cast<int>(rows), cols, codes, scales);
+}
+
+cudaError_t launch_block_matmul_stream(const uint8_t* a, const float* a_scale, int M, const uint8_t* b,
+                                       const float* b_scale, int N, int K, uint16_t* out, cudaStream_t s) {
+  StreamArgs g{};
+  g.rows = M;
+  g.E = 1;
+  g.N = N;
+  g.K = K;
+  g.k_blocks = (K + 127) / 128;
+  g.n_blocks = (N + 127) / 128;
+  g.a = a;
+  g.a_scale = a_scale;
+  g.w = b;
+  g.w_scale = b_scale;
+  g.out = out;
+  return launch_stream<STREAM_BF16>(g, M, 1, s);
+}
+
+cudaError_t launch_block_experts_stream(const uint8_t* x_q, const float* x_scale, const moe_layout& L, int H, int I,
+                                        const uint8_t* W1, const float* W1_scale, const uint8_t* W2,
+                                        const float* W2_scale, float* gu, uint8_t* h_q, float* h_scale, uint16_t* y,
+                                        cudaStream_t s) {
+  const long long pairs = static_cast<long long>(L.T) * L.K;
+  const long long active = pairs < L.E ? pairs : L.E;
+  if (active == 0) return cudaSuccess;
+  StreamArgs g{};
+  g.counts = L.tokens_per_expert;
+  g.offsets = L.offsets;
+  g.E = L.E;
+  g.N = 2 * I;
+  g.K = H;
+  g.k_blocks = H / 128;
+  g.n_blocks = 2 * I / 128;
+  g.a = x_q;
+  g.a_scale = x_scale;
+  g.w = W1;
+  g.w_scale = W1_scale;
+  g.out = gu;
+  cudaError_t err = launch_stream<STREAM_F32>(g, L.T, active, s);
+  if (err != cudaSuccess) return err;
+  const int y_grid = (I + 255) / 256;
+  const long long need = (L.capacity + 7) / 8, most = 8LL * sm_count();
+  err = launch_dependent(swiglu_quantize_kernel, dim3(static_cast<unsigned>(need < most ? need : most), y_grid), 256,
+                         0, s, static_cast<const float*>(gu), static_cast<long long>(L.capacity), I, h_q, h_scale,
+                         static_cast<const int*>(L.row_token));
+  if (err != cudaSuccess) return err;
+  g.N = H;
+  g.K = I;
+  g.k_blocks = I / 128;
+  g.n_blocks = H / 128;
+  g.a = h_q;
+  g.a_scale = h_scale;
+  g.w = W2;
+  g.w_scale = W2_scale;
+  g.row_weight = L.row_weight;
+  g.out = y;
+  return launch_stream<STREAM_WEIGHTED>(g, L.T, active, s);
+}
+
+}  // namespace moe

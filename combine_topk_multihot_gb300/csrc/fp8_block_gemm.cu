@@ -1,0 +1,449 @@
+// Products of e4m3 codes with a scale for each block of 128, on the 5th-
+// generation tensor cores.
+//
+//   C[m, n] = sum_kb sa[m, kb] sb[n / 128, kb] sum_{k in block kb} a[m, k] b[n, k]
+//
+// a [M, K] has a scale per row and 128 columns, b [N, K] one per 128 x 128
+// block (for the grouped form each expert's matrix has its own).  The tensor
+// cores sum one block of 128 products exactly as they stand (codes times
+// codes, fp32 accumulation in tensor memory); the scales differ from block to
+// block, so each block's partial sums are read back, scaled and added in fp32
+// registers.  That promotion is what the kernel is built around:
+//   * warp 0 stages operands by TMA (128-byte swizzle, one K block of 128
+//     codes per stage), warp 1 issues four tcgen05.mma of K = 32 per block
+//     into one of the accumulators in tensor memory (2 of 256 columns, or 4
+//     narrower ones), warps 4..11 read it back, free it and add it to their
+//     registers while the next blocks are multiplied;
+//   * with 256 columns a block takes the MMAs about 540 cycles and the
+//     promotion about 260 issue slots of each quarter of the SM plus as many
+//     cycles of tensor-memory reads, so it hides behind the MMAs;
+//   * a lane of a promoting warp owns a row of C: sa is one number per lane
+//     and block, sb one per warp.
+//
+// Three epilogues: bf16 of C; bf16 of w_row C (the experts' down product);
+// and SwiGLU with requantisation (the experts' gate/up product): the tile
+// pairs 128 gate with 128 up columns, h = silu(g) u stays in fp32 until it is
+// e4m3 codes with a scale per row and 128 columns.  (Through bf16 first, one
+// code in thirty would move by a step.)
+//
+// As in the bf16 experts, the tile list is built on the device from the
+// layout's counts, one persistent CTA per SM; every wait is bounded, and a
+// wait that runs out sets MOE_DEVERR_TIMEOUT, drains and returns.
+
+#include "common.cuh"
+#include "fp8_quant.cuh"
+#include "launch.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int BM = 128;
+constexpr int BKB = 128;  // codes per block and stage
+constexpr int EPI_WARPS = 8;
+// Three warpgroups: one for the producer and the issuer (two of its warps
+// idle), two for the promotion.  12 warps are launched with 168 registers a
+// thread; 128 x 56 + 256 x 224 = 384 x 168, so the promoting threads' share can
+// grow to hold 128 accumulators without spilling.
+constexpr int THREADS = 32 * (4 + EPI_WARPS);
+constexpr int LAUNCH_REGS = 168, FEW_REGS = 56, MANY_REGS = 224;
+static_assert(128 * FEW_REGS + 32 * EPI_WARPS * MANY_REGS <= THREADS * LAUNCH_REGS, "registers are only passed on");
+constexpr int MAX_STAGES = 8;
+constexpr int MAX_BUFS = 4;
+constexpr int SMEM_LIMIT = 232448;
+
+enum Mode { OUT_PLAIN = 0, OUT_WEIGHTED = 1, OUT_SWIGLU = 2 };
+
+template <int BN>
+struct Shape {
+  static constexpr int A_BYTES = BM * BKB;
+  static constexpr int B_BYTES = BN * BKB;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int STAGES = BN == 256 ? 4 : BN == 128 ? 6 : 8;
+  static constexpr int BUFS = BN == 256 ? 2 : 4;
+  static constexpr int TMEM_COLS = BN * BUFS;
+  static constexpr int COLS = BN / 2;  // accumulators of a promoting thread
+};
+
+struct Smem {
+  uint64_t full[MAX_STAGES];
+  uint64_t empty[MAX_STAGES];
+  uint64_t tfull[MAX_BUFS];
+  uint64_t tempty[MAX_BUFS];
+  uint64_t drain;
+  uint64_t pair[4];   // SwiGLU: the two warps of a lane quarter, once a tile
+  uint32_t tmem_base;
+  int abort;
+  int total_tiles;
+  float amax[2][2][BM];  // SwiGLU: [tile parity][column half] largest |h| of a row
+};
+
+constexpr size_t smem_bytes(int stages, int stage_bytes, int E) {
+  return 1024 + static_cast<size_t>(stages) * stage_bytes + sizeof(Smem) + static_cast<size_t>(3 * E + 2) * sizeof(int);
+}
+
+struct Args {
+  const int* counts;   // [E] rows of each expert; NULL: one group of `rows` rows
+  const int* offsets;  // [E + 1]
+  int rows;
+  int E;
+  int K, k_blocks;
+  int N;               // columns of C (OUT_SWIGLU: of h, half of b's rows)
+  int n_tiles;
+  int b_rows;          // rows of b per expert
+  int b_scale_rows;    // scale rows of b per expert
+  const float* a_scale;    // [rows, k_blocks]
+  const float* b_scale;    // [E, b_scale_rows, k_blocks]
+  const float* row_weight; // OUT_WEIGHTED
+  uint16_t* out;           // bf16 [rows, N]
+  uint8_t* out_q;          // OUT_SWIGLU: codes [rows, N] and scales [rows, N / 128]
+  float* out_scale;
+  int* status;
+};
+
+struct Tile {
+  int e, mt, nt;
+};
+
+__device__ __forceinline__ Tile decode_tile(const int* tile_prefix, int E, int n_tiles, int tile) {
+  int lo = 0, hi = E;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (tile_prefix[mid] <= tile) lo = mid; else hi = mid;
+  }
+  const int local = tile - tile_prefix[lo];
+  Tile t;
+  t.e = lo;
+  t.mt = local / n_tiles;
+  t.nt = local - t.mt * n_tiles;
+  return t;
+}
+
+__device__ __forceinline__ float silu(float g) { return g / (1.0f + __expf(-g)); }
+
+template <int MODE, int BN>
+__global__ void __launch_bounds__(THREADS, 1)
+    block_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                      const Args args) {
+  using S = Shape<BN>;
+  static_assert(MODE != OUT_SWIGLU || BN == 256, "a tile of h is one scale block wide");
+  constexpr int STAGES = S::STAGES, BUFS = S::BUFS, COLS = S::COLS;
+  constexpr uint32_t IDESC = idesc_e4m3_f32(BM, BN);
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* tiles = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+  Smem& s = *reinterpret_cast<Smem*>(tiles + STAGES * S::STAGE_BYTES);
+  int* s_off = reinterpret_cast<int*>(&s + 1);  // [E+1]
+  int* s_cnt = s_off + args.E + 1;              // [E]
+  int* s_pre = s_cnt + args.E;                  // [E+1] tile prefix
+  const uint32_t tiles_u32 = smem_u32(tiles);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int E = args.E;
+  griddep_launch_dependents();
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(smem_u32(&s.full[i]), 1);
+      mbar_init(smem_u32(&s.empty[i]), 1);
+    }
+    for (int i = 0; i < BUFS; ++i) {
+      mbar_init(smem_u32(&s.tfull[i]), 1);
+      mbar_init(smem_u32(&s.tempty[i]), EPI_WARPS);
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&s.pair[i]), 2);
+    mbar_init(smem_u32(&s.drain), 1);
+    s.abort = 0;
+    mbar_fence_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+  }
+  if (warp == 1) tmem_alloc(smem_u32(&s.tmem_base), S::TMEM_COLS);
+  griddep_wait();  // the codes, the scales and the layout come from earlier kernels
+  if (args.counts) {
+    for (int e = threadIdx.x; e <= E; e += blockDim.x) s_off[e] = args.offsets[e];
+    for (int e = threadIdx.x; e < E; e += blockDim.x) s_cnt[e] = args.counts[e];
+  } else if (threadIdx.x == 0) {
+    s_off[0] = 0;
+    s_off[1] = s_cnt[0] = args.rows;
+  }
+  __syncthreads();
+  if (warp == 0) {  // exclusive scan of per-expert tile counts
+    int running = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+      const int e = e0 + lane;
+      const int n = e < E ? ((s_cnt[e] + BM - 1) / BM) * args.n_tiles : 0;
+      int incl = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(FULL_MASK, incl, o);
+        if (lane >= o) incl += v;
+      }
+      if (e < E) s_pre[e] = running + incl - n;
+      running += __shfl_sync(FULL_MASK, incl, 31);
+    }
+    if (lane == 0) {
+      s_pre[E] = running;
+      s.total_tiles = running;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+
+  const int total = s.total_tiles;
+  const uint32_t tmem_base = s.tmem_base;
+  volatile int* abort_flag = &s.abort;
+  const int k_blocks = args.k_blocks;
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FEW_REGS));
+    // ================= TMA producer =================
+    if (warp == 0 && lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      long long issued = 0;
+      bool ok = true;
+      for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+        const Tile t = decode_tile(s_pre, E, args.n_tiles, tile);
+        const int a_row = s_off[t.e] + t.mt * BM;
+        const int b_row = t.e * args.b_rows + t.nt * (MODE == OUT_SWIGLU ? BN / 2 : BN);
+        for (int kb = 0; kb < k_blocks; ++kb) {
+          if (!mbar_wait(smem_u32(&s.empty[stage]), phase ^ 1u, abort_flag)) { ok = false; break; }
+          const uint32_t full = smem_u32(&s.full[stage]);
+          const uint32_t a_dst = tiles_u32 + stage * S::STAGE_BYTES;
+          const uint32_t b_dst = a_dst + S::A_BYTES;
+          mbar_arrive_expect_tx(full, S::STAGE_BYTES);
+          tma_load_2d(a_dst, &tmA, kb * BKB, a_row, full);
+          tma_load_2d(b_dst, &tmB, kb * BKB, b_row, full);
+          if constexpr (BN == 256)  // the up rows, or the tile's second half
+            tma_load_2d(b_dst + S::B_BYTES / 2, &tmB, kb * BKB, b_row + (MODE == OUT_SWIGLU ? args.N : BN / 2), full);
+          ++issued;
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
+      }
+      if (!ok) {  // wait for the loads of the last (up to STAGES) issued stages
+        for (int i = 0; i < STAGES && i < issued; ++i) {
+          if (--stage < 0) { stage = STAGES - 1; phase ^= 1u; }
+          mbar_wait_drain(smem_u32(&s.full[stage]), phase);
+        }
+      }
+    }
+    // ================= MMA issuer =================
+    if (warp == 1 && lane == 0) {
+      int stage = 0, buf = 0;
+      uint32_t phase = 0, use = 0;
+      bool ok = true;
+      for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+        for (int kb = 0; kb < k_blocks; ++kb) {
+          if (!mbar_wait(smem_u32(&s.tempty[buf]), use ^ 1u, abort_flag) ||
+              !mbar_wait(smem_u32(&s.full[stage]), phase, abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t a_addr = tiles_u32 + stage * S::STAGE_BYTES;
+          const uint64_t a_desc = sdesc_k_sw128(a_addr);
+          const uint64_t b_desc = sdesc_k_sw128(a_addr + S::A_BYTES);
+#pragma unroll
+          for (int kk = 0; kk < BKB / 32; ++kk)  // 32 codes = 32 bytes of the swizzled row a step
+            tc_mma_e4m3(tmem_base + buf * BN, a_desc + 2 * kk, b_desc + 2 * kk, IDESC, kk != 0);
+          tc_commit(smem_u32(&s.empty[stage]));
+          tc_commit(smem_u32(&s.tfull[buf]));
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+          if (++buf == BUFS) { buf = 0; use ^= 1u; }
+        }
+      }
+      // every MMA this thread issued has finished before anyone frees memory
+      tc_commit(smem_u32(&s.drain));
+      if (!mbar_wait_drain(smem_u32(&s.drain), 0)) *abort_flag = 1;
+    }
+    __syncwarp();
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(MANY_REGS));
+    // ================= promotion and epilogue =================
+    // lane quarter q = warp % 4 of tensor memory; column half (warp - 4) / 4.
+    // OUT_SWIGLU: the half's 64 gate columns, then its 64 up columns.
+    const int q = warp & 3, half = (warp - 4) >> 2;
+    const int r_in_tile = q * 32 + lane;
+    int buf = 0;
+    uint32_t use = 0, parity = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x, parity ^= 1u) {
+      const Tile t = decode_tile(s_pre, E, args.n_tiles, tile);
+      const int group_row = t.mt * BM + r_in_tile;
+      const bool valid = group_row < s_cnt[t.e];
+      const long long row = static_cast<long long>(s_off[t.e]) + group_row;
+      // scale rows of the columns' blocks of 128: a half's columns lie in one
+      // (BN = 256: its own; else both in the same one)
+      const int sb_row = MODE == OUT_SWIGLU ? t.nt : (t.nt * BN + half * COLS) >> 7;
+      const int sb_last = args.b_scale_rows - 1;  // a half past N reads the last one and stores nothing
+      const float* sb = args.b_scale + (static_cast<long long>(t.e) * args.b_scale_rows + min(sb_row, sb_last)) * k_blocks;
+      const float* sb_up = MODE == OUT_SWIGLU ? sb + static_cast<long long>(args.N >> 7) * k_blocks : sb;
+      const float* sa = args.a_scale + (valid ? row : static_cast<long long>(s_off[t.e])) * k_blocks;
+      float acc[COLS];
+#pragma unroll
+      for (int i = 0; i < COLS; ++i) acc[i] = 0.f;
+      float sa_v = __ldg(sa), sb_v = __ldg(sb), su_v = MODE == OUT_SWIGLU ? __ldg(sb_up) : 0.f;
+      for (int kb = 0; kb < k_blocks; ++kb) {
+        const float scale = sa_v * sb_v, scale_up = sa_v * su_v;
+        if (kb + 1 < k_blocks) {
+          sa_v = __ldg(sa + kb + 1);
+          sb_v = __ldg(sb + kb + 1);
+          if (MODE == OUT_SWIGLU) su_v = __ldg(sb_up + kb + 1);
+        }
+        const bool ready = mbar_wait(smem_u32(&s.tfull[buf]), use, abort_flag);
+        if (!__all_sync(FULL_MASK, ready)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t tb = tmem_base + buf * BN + (static_cast<uint32_t>(q * 32) << 16);
+#pragma unroll
+        for (int c = 0; c < COLS; c += 32) {
+          uint32_t p[32];
+          const int col = MODE == OUT_SWIGLU ? (c < 64 ? half * 64 + c : 128 + half * 64 + c - 64) : half * COLS + c;
+          tmem_ld32(tb + col, p);
+          tmem_ld_wait();
+          if (c + 32 >= COLS) {  // all of this warp's reads have landed
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&s.tempty[buf]));
+          }
+          const float f = MODE == OUT_SWIGLU && c >= 64 ? scale_up : scale;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) acc[c + i] = fmaf(__uint_as_float(p[i]), f, acc[c + i]);
+        }
+        if (++buf == BUFS) { buf = 0; use ^= 1u; }
+      }
+      if (!ok) break;
+      if constexpr (MODE == OUT_SWIGLU) {
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < 64; ++i) {
+          acc[i] = silu(acc[i]) * acc[64 + i];
+          top = max_nan(top, fabsf(acc[i]));
+        }
+        // The two warps of a lane quarter exchange their maxima.  One meeting a
+        // tile is enough: this parity's slots are written again two tiles
+        // on, after the next tile's meeting, which follows both reads here.
+        s.amax[parity][half][r_in_tile] = top;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&s.pair[q]));
+        const bool met = mbar_wait(smem_u32(&s.pair[q]), parity, abort_flag);
+        if (!__all_sync(FULL_MASK, met)) break;
+        const float scale = block_scale(max_nan(s.amax[parity][0][r_in_tile], s.amax[parity][1][r_in_tile]));
+        if (valid) {
+          uint8_t* dst = args.out_q + row * args.N + t.nt * 128 + half * 64;
+#pragma unroll
+          for (int i = 0; i < 64; i += 16) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              w[k] = e4m3x4(acc[i + 4 * k], acc[i + 4 * k + 1], acc[i + 4 * k + 2], acc[i + 4 * k + 3], scale);
+            *reinterpret_cast<uint4*>(dst + i) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          if (half == 0) args.out_scale[row * (args.N >> 7) + t.nt] = scale;
+        }
+      } else if (valid) {
+        const float w = MODE == OUT_WEIGHTED ? args.row_weight[row] : 1.0f;
+        const int col0 = t.nt * BN + half * COLS;
+        uint16_t* dst = args.out + row * args.N + col0;
+        const bool whole = (args.N & 7) == 0;  // 16-byte aligned rows
+#pragma unroll
+        for (int i = 0; i < COLS; i += 8) {
+          uint32_t v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] = pack_bf16x2(w * acc[i + 2 * k], w * acc[i + 2 * k + 1]);
+          if (whole) {
+            if (col0 + i < args.N) *reinterpret_cast<uint4*>(dst + i) = make_uint4(v[0], v[1], v[2], v[3]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (col0 + i + k < args.N) dst[i + k] = static_cast<uint16_t>(v[k >> 1] >> (16 * (k & 1)));
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem_base, S::TMEM_COLS);
+  if (threadIdx.x == 0 && s.abort) report(args.status, MOE_DEVERR_TIMEOUT);
+}
+
+template <int MODE, int BN>
+cudaError_t launch(const void* a, uint64_t a_rows, const void* b, uint64_t b_rows, const Args& args, int grid,
+                   cudaStream_t s) {
+  CUtensorMap ma, mb;
+  if (!make_tma_2d_u8(&ma, a, a_rows, args.K, BM) || !make_tma_2d_u8(&mb, b, b_rows, args.K, BN == 256 ? 128 : BN))
+    return cudaErrorInvalidValue;
+  auto kernel = block_gemm_kernel<MODE, BN>;
+  const size_t smem = smem_bytes(Shape<BN>::STAGES, Shape<BN>::STAGE_BYTES, args.E);
+  static_assert(smem_bytes(Shape<BN>::STAGES, Shape<BN>::STAGE_BYTES, 1024) <= SMEM_LIMIT, "fits for every E");
+  const cudaError_t err =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_LIMIT);
+  if (err != cudaSuccess) return err;
+  return launch_dependent(kernel, grid, THREADS, smem, s, ma, mb, args);
+}
+
+}  // namespace
+
+cudaError_t launch_block_matmul_tc(const uint8_t* a, const float* a_scale, int M, const uint8_t* b,
+                                   const float* b_scale, int N, int K, uint16_t* out, int* status,
+                                   cudaStream_t s) {
+  Args g{};
+  g.rows = M;
+  g.E = 1;
+  g.K = K;
+  g.k_blocks = (K + BKB - 1) / BKB;
+  g.N = N;
+  g.b_rows = N;
+  g.b_scale_rows = (N + 127) / 128;
+  g.a_scale = a_scale;
+  g.b_scale = b_scale;
+  g.out = out;
+  g.status = status;
+  const long long mt = (static_cast<long long>(M) + BM - 1) / BM;
+  auto tiles = [&](int bn) { return mt * ((N + bn - 1) / bn); };
+  const int sms = sm_count();
+  // the widest tile that still gives every SM one
+  const int bn = tiles(256) >= sms ? 256 : tiles(128) >= sms ? 128 : 64;
+  g.n_tiles = (N + bn - 1) / bn;
+  const int grid = static_cast<int>(tiles(bn) < sms ? tiles(bn) : sms);
+  if (bn == 256) return launch<OUT_PLAIN, 256>(a, M, b, N, g, grid, s);
+  if (bn == 128) return launch<OUT_PLAIN, 128>(a, M, b, N, g, grid, s);
+  return launch<OUT_PLAIN, 64>(a, M, b, N, g, grid, s);
+}
+
+cudaError_t launch_block_experts_tc(const uint8_t* x_q, const float* x_scale, const moe_layout& L, int H, int I,
+                                    const uint8_t* W1, const float* W1_scale, const uint8_t* W2,
+                                    const float* W2_scale, uint8_t* h_q, float* h_scale, uint16_t* y,
+                                    cudaStream_t s) {
+  Args g{};
+  g.counts = L.tokens_per_expert;
+  g.offsets = L.offsets;
+  g.E = L.E;
+  g.status = L.status;
+  g.K = H;
+  g.k_blocks = (H + BKB - 1) / BKB;
+  g.N = I;
+  g.n_tiles = I / 128;
+  g.b_rows = 2 * I;
+  g.b_scale_rows = 2 * I / 128;
+  g.a_scale = x_scale;
+  g.b_scale = W1_scale;
+  g.out_q = h_q;
+  g.out_scale = h_scale;
+  const uint64_t C = static_cast<uint64_t>(L.capacity), E = static_cast<uint64_t>(L.E);
+  cudaError_t err = launch<OUT_SWIGLU, 256>(x_q, C, W1, E * 2 * I, g, sm_count(), s);
+  if (err != cudaSuccess) return err;
+  g.K = I;
+  g.k_blocks = I / BKB;
+  g.N = H;
+  g.n_tiles = H / 256;
+  g.b_rows = H;
+  g.b_scale_rows = H / 128;
+  g.a_scale = h_scale;
+  g.b_scale = W2_scale;
+  g.row_weight = L.row_weight;
+  g.out = y;
+  return launch<OUT_WEIGHTED, 256>(h_q, C, W2, E * H, g, sm_count(), s);
+}
+
+}  // namespace moe

@@ -48,4 +48,28 @@ __device__ __forceinline__ float row_scale(const uint4* src, int V, int lane) {
   return amax > 0.f ? amax / E4M3_MAX : 1.0f;
 }
 
+// ---------------------------------------------------------------- blocks of 128
+// The same rule for blocks of 128 values, with two additions: the scale of a
+// block that is not zero is at least 2^-126 (so that no quotient overflows for
+// want of it), and a NaN or an infinity makes the block's scale non-finite
+// (its products are then, too) instead of being passed over by the maximum.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+__device__ __forceinline__ float block_scale(float amax) {
+  return amax == 0.f ? 1.0f : max_nan(__fdiv_rn(amax, E4M3_MAX), 0x1p-126f);
+}
+
+// Four codes of v / scale (an IEEE division each), lowest byte first.
+__device__ __forceinline__ uint32_t e4m3x4(float v0, float v1, float v2, float v3, float scale) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(v0, scale), __fdiv_rn(v1, scale)),
+                                               __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(v2, scale), __fdiv_rn(v3, scale)),
+                                               __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+
 }  // namespace moe

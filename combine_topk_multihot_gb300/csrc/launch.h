@@ -238,6 +238,29 @@ struct NormBackwardArgs {
 cudaError_t launch_norm_backward(const NormBackwardArgs& a, cudaStream_t s);
 size_t norm_backward_workspace(long long T, int H);
 
+// e4m3 codes with a scale per block of 128 (fp8_block.cu): block_rows is 1 or
+// 128; matrices [batch, rows, cols], each with its own blocks.  row_token
+// (block_rows 1, batch 1): rows whose entry is negative are left alone.
+cudaError_t launch_quantize_block(const uint16_t* src, long long batch, long long rows, int cols, int block_rows,
+                                  uint8_t* codes, float* scales, const int* row_token, cudaStream_t s);
+// Products with few rows, as a stream over the weights: at most
+// BLOCK_STREAM_ROWS rows (per expert).  gu: [capacity, 2I] fp32 scratch.
+constexpr int BLOCK_STREAM_ROWS = 32;
+cudaError_t launch_block_matmul_stream(const uint8_t* a, const float* a_scale, int M, const uint8_t* b,
+                                       const float* b_scale, int N, int K, uint16_t* out, cudaStream_t s);
+cudaError_t launch_block_experts_stream(const uint8_t* x_q, const float* x_scale, const moe_layout& L, int H, int I,
+                                        const uint8_t* W1, const float* W1_scale, const uint8_t* W2,
+                                        const float* W2_scale, float* gu, uint8_t* h_q, float* h_scale, uint16_t* y,
+                                        cudaStream_t s);
+// The same products on the tensor cores in tiles of 128 rows (fp8_block_gemm.cu).
+cudaError_t launch_block_matmul_tc(const uint8_t* a, const float* a_scale, int M, const uint8_t* b,
+                                   const float* b_scale, int N, int K, uint16_t* out, int* status,
+                                   cudaStream_t s);
+cudaError_t launch_block_experts_tc(const uint8_t* x_q, const float* x_scale, const moe_layout& L, int H, int I,
+                                    const uint8_t* W1, const float* W1_scale, const uint8_t* W2,
+                                    const float* W2_scale, uint8_t* h_q, float* h_scale, uint16_t* y,
+                                    cudaStream_t s);
+
 // AdamW over many tensors (adamw.cu), up to ADAMW_BATCH of them a launch.
 constexpr int ADAMW_BATCH = 96;
 constexpr int ADAMW_STATE_BLOCK = MOE_ADAMW_STATE_BLOCK;

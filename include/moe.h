@@ -649,6 +649,59 @@ MOE_API moe_status moe_adamw_step(const moe_adamw* h, const moe_adamw_tensor* te
                                   moe_stream_t stream);
 
 /*
+ * e4m3 codes with one fp32 scale per block: of 128 columns of one row
+ * (block_rows 1, activations) or of 128 x 128 (block_rows 128, weights).
+ * scale = max|v| / 448 over the block (at least 2^-126; 1 for a block of
+ * zeros), code = e4m3(v / scale) rounded to nearest even, in IEEE fp32
+ * divisions: the codes are functions of the input alone.  A block at the
+ * matrix's edge is smaller.  A NaN or infinity makes its block's scale
+ * non-finite.
+ *   src [batch, rows, cols] bf16, each matrix with its own blocks; cols a
+ *   multiple of 16; codes [batch, rows, cols] uint8 (out);
+ *   scales [batch, ceil(rows / block_rows), ceil(cols / 128)] fp32 (out).
+ */
+MOE_API moe_status moe_quantize_fp8_block(const moe_bf16* src, int64_t batch, int64_t rows, int32_t cols,
+                                          int32_t block_rows, uint8_t* codes, float* scales,
+                                          moe_stream_t stream);
+
+/*
+ * out[m, n] = bf16(sum_kb a_scale[m, kb] b_scale[n / 128, kb] sum_{k in block kb} a[m, k] b[n, k]):
+ * products of codes, exact, summed in fp32 within a block; the blocks scaled
+ * and added in fp32.
+ *   a_q [M, K] uint8 and a_scale [M, ceil(K / 128)] (block_rows 1);
+ *   b_q [N, K] uint8 and b_scale [ceil(N / 128), ceil(K / 128)] (block_rows
+ *   128); out [M, N] bf16 (out); status [1] int32 device status word
+ *   (nullable), receives MOE_DEVERR_TIMEOUT.
+ * M >= 0, N >= 1, K >= 16 a multiple of 16.  Up to 32 rows stream the
+ * weights through registers; more run on the tensor cores in 128-row tiles.
+ */
+MOE_API moe_status moe_matmul_fp8_block(const uint8_t* a_q, const float* a_scale, int32_t M,
+                                        const uint8_t* b_q, const float* b_scale, int32_t N, int32_t K,
+                                        moe_bf16* out, int32_t* status, moe_stream_t stream);
+
+/*
+ * The grouped SwiGLU experts from weights with 128 x 128 block scales, both
+ * products in e4m3:
+ *   q(x) = e4m3 codes of x_disp, a scale per row and 128 columns;
+ *   h = silu(q(x) Wg^T) * (q(x) Wu^T) in fp32, q(h) likewise;
+ *   y_disp[r] = bf16(w_r (q(h) W2^T)).
+ *   x_disp [C, H] bf16 (moe_dispatch's output); L its layout;
+ *   W1_q [E, 2I, H] uint8, W1_scale [E, 2I/128, H/128], W2_q [E, H, I],
+ *   W2_scale [E, H/128, I/128] (moe_quantize_fp8_block, block_rows 128);
+ *   y_disp [C, H] bf16 (out): the valid rows are written.
+ *   workspace: moe_experts_fp8_block_workspace_bytes(C, T, H, I) bytes of
+ *   device scratch, 16-byte aligned.
+ * Inference only.  Shapes and errors as in moe_grouped_experts.  Nothing is
+ * read back to the host: the call can be captured.
+ */
+MOE_API moe_status moe_experts_fp8_block_workspace_bytes(int64_t capacity, int32_t T, int32_t H, int32_t I,
+                                                         size_t* bytes);
+MOE_API moe_status moe_grouped_experts_fp8_block(const moe_bf16* x_disp, const moe_layout* L, int32_t H,
+                                                 int32_t I, const uint8_t* W1_q, const float* W1_scale,
+                                                 const uint8_t* W2_q, const float* W2_scale,
+                                                 moe_bf16* y_disp, void* workspace, moe_stream_t stream);
+
+/*
  * Failure-detection self-test.  Runs one CTA whose wait on an mbarrier can
  * never complete, using the bounded-wait helper of the pipelined kernels with
  * a limit of limit_ns (0 < limit_ns <= 1 s).  The wait gives up, the kernel
