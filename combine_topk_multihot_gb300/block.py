@@ -16,6 +16,7 @@ else is refused before a kernel is launched.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import List, Optional, Sequence, Union
 
 import numpy as np
@@ -28,21 +29,26 @@ _DTYPES = {torch.bfloat16: N.MOE_DTYPE_BF16, torch.float32: N.MOE_DTYPE_F32}
 _GATES = {0: N.MOE_GATE_NONE, 1: N.MOE_GATE_TOKEN, 2: N.MOE_GATE_ELEMENT}
 
 
-def _raw_stream(stream):
-    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+# The current stream's handle without a Python stream object around it: a
+# call for one token is bound by what happens here on the host.
+_current_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _raw_stream(stream, device):
+    return _current_raw_stream(device.index) if stream is None else stream.cuda_stream
 
 
 def _need(t: torch.Tensor, name: str, dtype, shape, device):
     """The address of a tensor that has to be as given (None for one without elements)."""
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr() or None
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
     if t.device != device:
         raise ValueError(f"{name} must be on {device} (got {t.device})")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr() or None
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _on_gpu(t: torch.Tensor, name: str) -> torch.device:
@@ -75,10 +81,16 @@ def _norm(T, H, x, weight, gate, gate_sigmoid, residual_scale, eps, weight_offse
                      int(gate_sigmoid), residual_scale, eps, weight_offset)
 
 
-def _workspace(T, H, device):
+@functools.lru_cache(maxsize=1024)
+def _bytes(query: str, *sizes) -> int:
+    """A workspace's size, which depends on its arguments (and the device's SM count) alone."""
     nbytes = ctypes.c_size_t(0)
-    _check(N.lib.moe_norm_backward_workspace_bytes(T, H, ctypes.byref(nbytes)), "moe_norm_backward_workspace_bytes")
-    return torch.empty(nbytes.value, dtype=torch.uint8, device=device)
+    _check(getattr(N.lib, query)(*sizes, ctypes.byref(nbytes)), query)
+    return nbytes.value
+
+
+def _workspace(T, H, device):
+    return torch.empty(_bytes("moe_norm_backward_workspace_bytes", T, H), dtype=torch.uint8, device=device)
 
 
 def moe_norm_in(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, weight_offset: float = 0.0,
@@ -93,7 +105,7 @@ def moe_norm_in(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, weight
     rstd = torch.empty(T, dtype=torch.float32, device=dev) if save_rstd else None
     _check(N.lib.moe_norm_in(n, _need(x, "x", x.dtype, (T, H), dev), _need(weight, "weight", weight.dtype, (H,), dev),
                              _need(out, "out", torch.bfloat16, (T, H), dev), rstd.data_ptr() or None if save_rstd else None,
-                             _raw_stream(stream)), "moe_norm_in")
+                             _raw_stream(stream, dev)), "moe_norm_in")
     return out, rstd
 
 
@@ -111,7 +123,7 @@ def moe_norm_in_backward(grad_norm: torch.Tensor, x: torch.Tensor, weight: torch
         n, _need(grad_norm, "grad_norm", torch.bfloat16, (T, H), dev), _need(x, "x", x.dtype, (T, H), dev),
         _need(weight, "weight", weight.dtype, (H,), dev), _need(rstd, "rstd", torch.float32, (T,), dev),
         None if grad_res is None else _need(grad_res, "grad_res", x.dtype, (T, H), dev),
-        grad_x.data_ptr() or None, grad_w.data_ptr(), ws.data_ptr() or None, _raw_stream(stream)),
+        grad_x.data_ptr() or None, grad_w.data_ptr(), ws.data_ptr() or None, _raw_stream(stream, dev)),
         "moe_norm_in_backward")
     return grad_x, grad_w
 
@@ -137,7 +149,7 @@ def moe_norm_out(x: torch.Tensor, y: torch.Tensor, weight: torch.Tensor, gate: O
         rstd.data_ptr() or None if save_rstd else None,
         _need(next_weight, "next_weight", weight.dtype, (H,), dev) if has_next else None,
         nxt.data_ptr() or None if has_next else None,
-        next_rstd.data_ptr() or None if next_rstd is not None else None, _raw_stream(stream)), "moe_norm_out")
+        next_rstd.data_ptr() or None if next_rstd is not None else None, _raw_stream(stream, dev)), "moe_norm_out")
     return out, rstd, nxt, next_rstd
 
 
@@ -175,7 +187,7 @@ def moe_norm_out_backward(grad_out: Optional[torch.Tensor], y: torch.Tensor, wei
         _need(next_weight, "next_weight", weight.dtype, (H,), dev) if has_next else None,
         _need(next_rstd, "next_rstd", torch.float32, (T,), dev) if has_next else None,
         grad_x.data_ptr() or None, grad_y.data_ptr() or None, None if gate is None else grad_gate.data_ptr() or None,
-        grad_w.data_ptr(), grad_w2.data_ptr() if has_next else None, ws.data_ptr() or None, _raw_stream(stream)),
+        grad_w.data_ptr(), grad_w2.data_ptr() if has_next else None, ws.data_ptr() or None, _raw_stream(stream, dev)),
         "moe_norm_out_backward")
     return grad_x, grad_y, grad_gate, grad_w, grad_w2
 
@@ -231,6 +243,8 @@ class AdamWState:
             self.master = [p.detach().float() if p.dtype is torch.bfloat16 else None for p in self.params] \
                 if master else None
         self._table = np.zeros(len(self.params), dtype=_TABLE)
+        self._made_for = [(p.dtype, p.shape) for p in self.params]
+        self._settings = None      # what the table's remaining columns were filled from
         for i, (p, row) in enumerate(zip(self.params, self._table)):
             row["n"], row["param_dtype"] = p.numel(), _either(p, f"params[{i}]")
             for name, dtype, shape in (("exp_avg", avg, p.shape), ("exp_avg_sq", avg, p.shape),
@@ -261,27 +275,27 @@ def moe_adamw_step(state: AdamWState, grads: Sequence[Optional[torch.Tensor]], l
     if len(grads) != len(params):
         raise ValueError(f"{len(grads)} gradients for {len(params)} parameters")
     if params:
-        addresses, kinds, counts, places = [], [], [], []
-        for i, (p, g) in enumerate(zip(params, grads)):
-            if p.dtype not in _DTYPES or p.numel() != state.exp_avg[i].numel() or not p.is_contiguous() or p.device != dev:
+        for i, (p, (dtype, shape)) in enumerate(zip(params, state._made_for)):
+            if p.dtype is not dtype or p.shape != shape or p.device != dev or not p.is_contiguous():
                 raise ValueError(f"params[{i}] is no longer what the state was made for")
-            places.append(p.data_ptr())
-            if g is None:
-                addresses.append(0)
-                kinds.append(0)
-                counts.append(0)
-                continue
-            kinds.append(_either(g, f"grads[{i}]"))
-            addresses.append(_need(g, f"grads[{i}]", g.dtype, p.shape, dev) or 0)
-            counts.append(p.numel())
-        table["param"], table["grad"], table["grad_dtype"], table["n"] = places, addresses, kinds, counts
-        table["param_dtype"] = [_DTYPES[p.dtype] for p in params]
-        table["weight_decay"] = weight_decay
+        table["param"] = [p.data_ptr() for p in params]
+        table["grad"] = [0 if g is None else _need(g, f"grads[{i}]", g.dtype, shape, dev) or 0
+                         for i, (g, (_, shape)) in enumerate(zip(grads, state._made_for))]
+        # only the addresses change in most steps
+        if not isinstance(weight_decay, (int, float)):
+            weight_decay = [float(d) for d in weight_decay]
+        settings = ([None if g is None else g.dtype for g in grads], weight_decay)
+        if settings != state._settings:
+            state._settings = None
+            table["grad_dtype"] = [0 if g is None else _either(g, f"grads[{i}]") for i, g in enumerate(grads)]
+            table["n"] = [0 if g is None else g.numel() for g in grads]
+            table["weight_decay"] = weight_decay
+            state._settings = settings
     scalar = [None if t is None else _need(t, name, dtype, (1,), dev)
               for t, name, dtype in ((grad_scale, "grad_scale", torch.float32), (skip, "skip", torch.int32),
                                      (step, "step", torch.int64))]
     h = N.MoeAdamw(lr, beta1, beta2, eps, state.step + 1, state.seed, state.state_bits, *scalar)
-    _check(N.lib.moe_adamw_step(h, table.ctypes.data, len(params), _raw_stream(stream)), "moe_adamw_step")
+    _check(N.lib.moe_adamw_step(h, table.ctypes.data, len(params), _raw_stream(stream, dev)), "moe_adamw_step")
     if step is None:
         state.step += 1
     if params:
@@ -311,7 +325,7 @@ def moe_quantize_fp8_block(src: torch.Tensor, block_rows: int = 1, out=None, str
     codes, scales = out
     _check(N.lib.moe_quantize_fp8_block(_need(src, "src", torch.bfloat16, src.shape, dev), batch, rows, cols, block_rows,
                                         _need(codes, "codes", torch.uint8, src.shape, dev),
-                                        _need(scales, "scales", torch.float32, shape, dev), _raw_stream(stream)),
+                                        _need(scales, "scales", torch.float32, shape, dev), _raw_stream(stream, dev)),
            "moe_quantize_fp8_block")
     return codes, scales
 
@@ -332,7 +346,7 @@ def moe_matmul_fp8_block(a_q: torch.Tensor, a_scale: torch.Tensor, b_q: torch.Te
                                       _need(b_scale, "b_scale", torch.float32, (_blocks(n), kb), dev), n, K,
                                       _need(out, "out", torch.bfloat16, (M, n), dev),
                                       None if status is None else _need(status, "status", torch.int32, (1,), dev),
-                                      _raw_stream(stream)), "moe_matmul_fp8_block")
+                                      _raw_stream(stream, dev)), "moe_matmul_fp8_block")
     return out
 
 
@@ -348,16 +362,13 @@ def moe_grouped_experts_fp8_block(x_disp: torch.Tensor, layout: Layout, W1_q: to
     E, I = layout.E, W1_q.shape[1] // 2
     if out is None:
         out = torch.empty(C, H, dtype=torch.bfloat16, device=dev)
-    nbytes = ctypes.c_size_t(0)
-    _check(N.lib.moe_experts_fp8_block_workspace_bytes(C, layout.T, H, I, ctypes.byref(nbytes)),
-           "moe_experts_fp8_block_workspace_bytes")
-    ws = torch.empty(nbytes.value, dtype=torch.uint8, device=dev)
+    ws = torch.empty(_bytes("moe_experts_fp8_block_workspace_bytes", C, layout.T, H, I), dtype=torch.uint8, device=dev)
     _check(N.lib.moe_grouped_experts_fp8_block(
         _need(x_disp, "x_disp", torch.bfloat16, (C, H), dev), layout.ref, H, I,
         _need(W1_q, "W1_q", torch.uint8, (E, 2 * I, H), dev),
         _need(W1_scale, "W1_scale", torch.float32, (E, _blocks(2 * I), _blocks(H)), dev),
         _need(W2_q, "W2_q", torch.uint8, (E, H, I), dev),
         _need(W2_scale, "W2_scale", torch.float32, (E, _blocks(H), _blocks(I)), dev),
-        _need(out, "out", torch.bfloat16, (C, H), dev), ws.data_ptr() or None, _raw_stream(stream)),
+        _need(out, "out", torch.bfloat16, (C, H), dev), ws.data_ptr() or None, _raw_stream(stream, dev)),
         "moe_grouped_experts_fp8_block")
     return out

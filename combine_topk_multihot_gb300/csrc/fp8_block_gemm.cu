@@ -10,8 +10,8 @@
 // block, so each block's partial sums are read back, scaled and added in fp32
 // registers.  That promotion is what the kernel is built around:
 //   * warp 0 stages operands by TMA (128-byte swizzle, one K block of 128
-//     codes per stage), warp 1 issues four tcgen05.mma of K = 32 per block
-//     into one of the accumulators in tensor memory (2 of 256 columns, or 4
+//     codes per stage), warps 1 and 2 issue four tcgen05.mma of K = 32 per
+//     block into one of the accumulators in tensor memory (2 of 256 columns, or 4
 //     narrower ones), warps 4..11 read it back, free it and add it to their
 //     registers while the next blocks are multiplied;
 //   * with 256 columns a block takes the MMAs about 540 cycles and the
@@ -41,8 +41,7 @@ namespace {
 constexpr int BM = 128;
 constexpr int BKB = 128;  // codes per block and stage
 constexpr int EPI_WARPS = 8;
-// Three warpgroups: one for the producer and the issuer (two of its warps
-// idle), two for the promotion.  12 warps are launched with 168 registers a
+// Three warpgroups: one for the producer and the issuers, two for the promotion.  12 warps are launched with 168 registers a
 // thread; 128 x 56 + 256 x 224 = 384 x 168, so the promoting threads' share can
 // grow to hold 128 accumulators without spilling.
 constexpr int THREADS = 32 * (4 + EPI_WARPS);
@@ -59,7 +58,9 @@ struct Shape {
   static constexpr int A_BYTES = BM * BKB;
   static constexpr int B_BYTES = BN * BKB;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int STAGES = BN == 256 ? 4 : BN == 128 ? 6 : 8;
+  // What is left beside the staged output (two bytes a value, the whole tile)
+  static constexpr int STAGES = BN == 256 ? 3 : BN == 128 ? 5 : 7;
+  static constexpr int STAGING_BYTES = BM * BN * 2;
   static constexpr int BUFS = BN == 256 ? 2 : 4;
   static constexpr int TMEM_COLS = BN * BUFS;
   static constexpr int COLS = BN / 2;  // accumulators of a promoting thread
@@ -70,7 +71,7 @@ struct Smem {
   uint64_t empty[MAX_STAGES];
   uint64_t tfull[MAX_BUFS];
   uint64_t tempty[MAX_BUFS];
-  uint64_t drain;
+  uint64_t drain[2];
   uint64_t pair[4];   // SwiGLU: the two warps of a lane quarter, once a tile
   uint32_t tmem_base;
   int abort;
@@ -78,8 +79,10 @@ struct Smem {
   float amax[2][2][BM];  // SwiGLU: [tile parity][column half] largest |h| of a row
 };
 
-constexpr size_t smem_bytes(int stages, int stage_bytes, int E) {
-  return 1024 + static_cast<size_t>(stages) * stage_bytes + sizeof(Smem) + static_cast<size_t>(3 * E + 2) * sizeof(int);
+template <int BN>
+constexpr size_t smem_bytes(int E) {
+  return 1024 + static_cast<size_t>(Shape<BN>::STAGES) * Shape<BN>::STAGE_BYTES + Shape<BN>::STAGING_BYTES +
+         sizeof(Smem) + static_cast<size_t>(3 * E + 2) * sizeof(int);
 }
 
 struct Args {
@@ -96,6 +99,7 @@ struct Args {
   const float* b_scale;    // [E, b_scale_rows, k_blocks]
   const float* row_weight; // OUT_WEIGHTED
   uint16_t* out;           // bf16 [rows, N]
+  int out_staged;          // tmOut describes the output (its rows are 16-byte aligned)
   uint8_t* out_q;          // OUT_SWIGLU: codes [rows, N] and scales [rows, N / 128]
   float* out_scale;
   int* status;
@@ -119,12 +123,23 @@ __device__ __forceinline__ Tile decode_tile(const int* tile_prefix, int E, int n
   return t;
 }
 
+// Waits for this thread's tensor-memory loads; the registers pass through, so
+// that no use of them can be scheduled before the wait.
+__device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])::"memory");
+}
+
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + __expf(-g)); }
 
 template <int MODE, int BN>
 __global__ void __launch_bounds__(THREADS, 1)
     block_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                      const Args args) {
+                      const __grid_constant__ CUtensorMap tmOut, const Args args) {
   using S = Shape<BN>;
   static_assert(MODE != OUT_SWIGLU || BN == 256, "a tile of h is one scale block wide");
   constexpr int STAGES = S::STAGES, BUFS = S::BUFS, COLS = S::COLS;
@@ -132,7 +147,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* tiles = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
-  Smem& s = *reinterpret_cast<Smem*>(tiles + STAGES * S::STAGE_BYTES);
+  Smem& s = *reinterpret_cast<Smem*>(tiles + STAGES * S::STAGE_BYTES + S::STAGING_BYTES);
   int* s_off = reinterpret_cast<int*>(&s + 1);  // [E+1]
   int* s_cnt = s_off + args.E + 1;              // [E]
   int* s_pre = s_cnt + args.E;                  // [E+1] tile prefix
@@ -151,11 +166,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(smem_u32(&s.tempty[i]), EPI_WARPS);
     }
     for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&s.pair[i]), 2);
-    mbar_init(smem_u32(&s.drain), 1);
+    for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&s.drain[i]), 1);
     s.abort = 0;
     mbar_fence_init();
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
+    if (args.out_staged) tma_prefetch_desc(&tmOut);
   }
   if (warp == 1) tmem_alloc(smem_u32(&s.tmem_base), S::TMEM_COLS);
   griddep_wait();  // the codes, the scales and the layout come from earlier kernels
@@ -228,31 +244,37 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
     }
-    // ================= MMA issuer =================
-    if (warp == 1 && lane == 0) {
-      int stage = 0, buf = 0;
+    // ================= MMA issuers =================
+    // Two warps take turns, one K block each.  A block's four instructions
+    // are accepted only as the ones before them finish, so a single issuer
+    // would spend the time of its next waits and commits (about 300 cycles)
+    // with an idle tensor pipe; the accumulators of neighbouring blocks are
+    // different ones, so their order does not matter.
+    if ((warp == 1 || warp == 2) && lane == 0) {
+      const int w = warp - 1;
+      const int my_tiles = total > static_cast<int>(blockIdx.x) ? (total - 1 - blockIdx.x) / gridDim.x + 1 : 0;
+      const long long blocks = static_cast<long long>(my_tiles) * k_blocks;
+      int stage = w, buf = w;
       uint32_t phase = 0, use = 0;
-      bool ok = true;
-      for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-        for (int kb = 0; kb < k_blocks; ++kb) {
-          if (!mbar_wait(smem_u32(&s.tempty[buf]), use ^ 1u, abort_flag) ||
-              !mbar_wait(smem_u32(&s.full[stage]), phase, abort_flag)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t a_addr = tiles_u32 + stage * S::STAGE_BYTES;
-          const uint64_t a_desc = sdesc_k_sw128(a_addr);
-          const uint64_t b_desc = sdesc_k_sw128(a_addr + S::A_BYTES);
+      for (long long it = w; it < blocks; it += 2) {
+        if (!mbar_wait(smem_u32(&s.tempty[buf]), use ^ 1u, abort_flag) ||
+            !mbar_wait(smem_u32(&s.full[stage]), phase, abort_flag))
+          break;
+        tc_fence_after();
+        const uint32_t a_addr = tiles_u32 + stage * S::STAGE_BYTES;
+        const uint64_t a_desc = sdesc_k_sw128(a_addr);
+        const uint64_t b_desc = sdesc_k_sw128(a_addr + S::A_BYTES);
 #pragma unroll
-          for (int kk = 0; kk < BKB / 32; ++kk)  // 32 codes = 32 bytes of the swizzled row a step
-            tc_mma_e4m3(tmem_base + buf * BN, a_desc + 2 * kk, b_desc + 2 * kk, IDESC, kk != 0);
-          tc_commit(smem_u32(&s.empty[stage]));
-          tc_commit(smem_u32(&s.tfull[buf]));
-          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-          if (++buf == BUFS) { buf = 0; use ^= 1u; }
-        }
+        for (int kk = 0; kk < BKB / 32; ++kk)  // 32 codes = 32 bytes of the swizzled row a step
+          tc_mma_e4m3(tmem_base + buf * BN, a_desc + 2 * kk, b_desc + 2 * kk, IDESC, kk != 0);
+        tc_commit(smem_u32(&s.empty[stage]));
+        tc_commit(smem_u32(&s.tfull[buf]));
+        if ((stage += 2) >= STAGES) { stage -= STAGES; phase ^= 1u; }
+        if ((buf += 2) >= BUFS) { buf -= BUFS; use ^= 1u; }
       }
       // every MMA this thread issued has finished before anyone frees memory
-      tc_commit(smem_u32(&s.drain));
-      if (!mbar_wait_drain(smem_u32(&s.drain), 0)) *abort_flag = 1;
+      tc_commit(smem_u32(&s.drain[w]));
+      if (!mbar_wait_drain(smem_u32(&s.drain[w]), 0)) *abort_flag = 1;
     }
     __syncwarp();
   } else {
@@ -262,54 +284,111 @@ __global__ void __launch_bounds__(THREADS, 1)
     // OUT_SWIGLU: the half's 64 gate columns, then its 64 up columns.
     const int q = warp & 3, half = (warp - 4) >> 2;
     const int r_in_tile = q * 32 + lane;
+    const uint32_t staging = tiles_u32 + STAGES * S::STAGE_BYTES + (warp - 4) * (S::STAGING_BYTES / EPI_WARPS);
+    auto column = [&](int c) {  // tensor-memory column of this thread's accumulator c
+      return MODE == OUT_SWIGLU ? (c < 64 ? half * 64 + c : 128 + half * 64 + c - 64) : half * COLS + c;
+    };
+    // This thread's part of a tile: its row, and where its scales are.
+    struct Part {
+      int nt;
+      bool valid;
+      int row0;              // of the warp's 32 rows
+      const float *sa, *sb, *sb_up;
+      float w;
+    };
+    auto part_of = [&](int tile) {
+      const Tile t = decode_tile(s_pre, E, args.n_tiles, tile);
+      Part p;
+      p.nt = t.nt;
+      p.valid = t.mt * BM + r_in_tile < s_cnt[t.e];
+      p.row0 = s_off[t.e] + t.mt * BM + q * 32;
+      const long long row = p.valid ? p.row0 + lane : s_off[t.e];
+      // scale rows of the columns' blocks of 128: a half's columns lie in one
+      // (a half past N reads the last one and stores nothing)
+      const int sb_row = min(MODE == OUT_SWIGLU ? t.nt : (t.nt * BN + half * COLS) >> 7, args.b_scale_rows - 1);
+      p.sa = args.a_scale + row * k_blocks;
+      p.sb = args.b_scale + (static_cast<long long>(t.e) * args.b_scale_rows + sb_row) * k_blocks;
+      p.sb_up = MODE == OUT_SWIGLU ? p.sb + static_cast<long long>(args.N >> 7) * k_blocks : p.sb;
+      p.w = MODE == OUT_WEIGHTED ? __ldg(args.row_weight + row) : 1.0f;
+      return p;
+    };
     int buf = 0;
     uint32_t use = 0, parity = 0;
+    int tile = blockIdx.x;
+    Part part = {}, next = {};
+    float sa_v = 0.f, sb_v = 0.f, su_v = 0.f;  // the next block's scales, one block ahead (also across tiles)
+    if (tile < total) {
+      next = part_of(tile);
+      sa_v = __ldg(next.sa);
+      sb_v = __ldg(next.sb);
+      if (MODE == OUT_SWIGLU) su_v = __ldg(next.sb_up);
+    }
     bool ok = true;
-    for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x, parity ^= 1u) {
-      const Tile t = decode_tile(s_pre, E, args.n_tiles, tile);
-      const int group_row = t.mt * BM + r_in_tile;
-      const bool valid = group_row < s_cnt[t.e];
-      const long long row = static_cast<long long>(s_off[t.e]) + group_row;
-      // scale rows of the columns' blocks of 128: a half's columns lie in one
-      // (BN = 256: its own; else both in the same one)
-      const int sb_row = MODE == OUT_SWIGLU ? t.nt : (t.nt * BN + half * COLS) >> 7;
-      const int sb_last = args.b_scale_rows - 1;  // a half past N reads the last one and stores nothing
-      const float* sb = args.b_scale + (static_cast<long long>(t.e) * args.b_scale_rows + min(sb_row, sb_last)) * k_blocks;
-      const float* sb_up = MODE == OUT_SWIGLU ? sb + static_cast<long long>(args.N >> 7) * k_blocks : sb;
-      const float* sa = args.a_scale + (valid ? row : static_cast<long long>(s_off[t.e])) * k_blocks;
+    for (; tile < total && ok; tile += gridDim.x, parity ^= 1u) {
+      part = next;
       float acc[COLS];
 #pragma unroll
       for (int i = 0; i < COLS; ++i) acc[i] = 0.f;
-      float sa_v = __ldg(sa), sb_v = __ldg(sb), su_v = MODE == OUT_SWIGLU ? __ldg(sb_up) : 0.f;
       for (int kb = 0; kb < k_blocks; ++kb) {
         const float scale = sa_v * sb_v, scale_up = sa_v * su_v;
         if (kb + 1 < k_blocks) {
-          sa_v = __ldg(sa + kb + 1);
-          sb_v = __ldg(sb + kb + 1);
-          if (MODE == OUT_SWIGLU) su_v = __ldg(sb_up + kb + 1);
+          sa_v = __ldg(part.sa + kb + 1);
+          sb_v = __ldg(part.sb + kb + 1);
+          if (MODE == OUT_SWIGLU) su_v = __ldg(part.sb_up + kb + 1);
+        } else if (tile + static_cast<int>(gridDim.x) < total) {
+          next = part_of(tile + gridDim.x);
+          sa_v = __ldg(next.sa);
+          sb_v = __ldg(next.sb);
+          if (MODE == OUT_SWIGLU) su_v = __ldg(next.sb_up);
         }
         const bool ready = mbar_wait(smem_u32(&s.tfull[buf]), use, abort_flag);
         if (!__all_sync(FULL_MASK, ready)) { ok = false; break; }
         tc_fence_after();
         const uint32_t tb = tmem_base + buf * BN + (static_cast<uint32_t>(q * 32) << 16);
+        uint32_t p[2][32];
+        tmem_ld32(tb + column(0), p[0]);
 #pragma unroll
-        for (int c = 0; c < COLS; c += 32) {
-          uint32_t p[32];
-          const int col = MODE == OUT_SWIGLU ? (c < 64 ? half * 64 + c : 128 + half * 64 + c - 64) : half * COLS + c;
-          tmem_ld32(tb + col, p);
-          tmem_ld_wait();
-          if (c + 32 >= COLS) {  // all of this warp's reads have landed
+        for (int c = 0; c < COLS; c += 32) {  // the next 32 columns are read while these are added
+          uint32_t(&now)[32] = p[(c >> 5) & 1];
+          tmem_ld_wait32(now);
+          if (c + 32 < COLS) {
+            tmem_ld32(tb + column(c + 32), p[((c >> 5) & 1) ^ 1]);
+          } else {  // all of this warp's reads have landed
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&s.tempty[buf]));
           }
           const float f = MODE == OUT_SWIGLU && c >= 64 ? scale_up : scale;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) acc[c + i] = fmaf(__uint_as_float(p[i]), f, acc[c + i]);
+          for (int i = 0; i < 32; ++i) acc[c + i] = fmaf(__uint_as_float(now[i]), f, acc[c + i]);
         }
         if (++buf == BUFS) { buf = 0; use ^= 1u; }
       }
       if (!ok) break;
+      // Output: a warp whose 32 rows all exist writes them to its staging
+      // boxes (32 rows of 64 bytes, swizzled) and stores those by TMA, which
+      // goes on while the next tile is multiplied; else rows one by one.
+      // Rows past a dense matrix are clipped by the tensor map.
+      const bool staged = args.out_staged && (!args.counts || __all_sync(FULL_MASK, part.valid));
+      const long long row = static_cast<long long>(part.row0) + lane;
+      if (staged) {
+        if (lane == 0) tma_store_wait_read<0>();  // the last tile's boxes
+        __syncwarp();
+      }
+      auto put = [&](int box, const uint32_t (&v)[16], int x) {  // x: column in units of 2 bytes
+        const uint32_t dst = staging + box * 2048;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + staged_chunk(lane, i)), "r"(v[4 * i]),
+                       "r"(v[4 * i + 1]), "r"(v[4 * i + 2]), "r"(v[4 * i + 3])
+                       : "memory");
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d(&tmOut, dst, x, part.row0);
+          tma_store_commit();
+        }
+      };
       if constexpr (MODE == OUT_SWIGLU) {
         float top = 0.f;
 #pragma unroll
@@ -326,38 +405,48 @@ __global__ void __launch_bounds__(THREADS, 1)
         const bool met = mbar_wait(smem_u32(&s.pair[q]), parity, abort_flag);
         if (!__all_sync(FULL_MASK, met)) break;
         const float scale = block_scale(max_nan(s.amax[parity][0][r_in_tile], s.amax[parity][1][r_in_tile]));
-        if (valid) {
-          uint8_t* dst = args.out_q + row * args.N + t.nt * 128 + half * 64;
+        uint32_t v[16];
 #pragma unroll
-          for (int i = 0; i < 64; i += 16) {
-            uint32_t w[4];
+        for (int k = 0; k < 16; ++k)
+          v[k] = e4m3x4(acc[4 * k], acc[4 * k + 1], acc[4 * k + 2], acc[4 * k + 3], scale);
+        if (staged) {
+          put(0, v, part.nt * 64 + half * 32);
+        } else if (part.valid) {
+          uint4* dst = reinterpret_cast<uint4*>(args.out_q + row * args.N + part.nt * 128 + half * 64);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              w[k] = e4m3x4(acc[i + 4 * k], acc[i + 4 * k + 1], acc[i + 4 * k + 2], acc[i + 4 * k + 3], scale);
-            *reinterpret_cast<uint4*>(dst + i) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-          if (half == 0) args.out_scale[row * (args.N >> 7) + t.nt] = scale;
+          for (int k = 0; k < 4; ++k) dst[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
         }
-      } else if (valid) {
-        const float w = MODE == OUT_WEIGHTED ? args.row_weight[row] : 1.0f;
-        const int col0 = t.nt * BN + half * COLS;
-        uint16_t* dst = args.out + row * args.N + col0;
+        if (part.valid && half == 0) args.out_scale[row * (args.N >> 7) + part.nt] = scale;
+      } else {
+        const int col0 = part.nt * BN + half * COLS;
         const bool whole = (args.N & 7) == 0;  // 16-byte aligned rows
 #pragma unroll
-        for (int i = 0; i < COLS; i += 8) {
-          uint32_t v[4];
+        for (int c = 0; c < COLS; c += 32) {
+          if (col0 + c >= args.N) break;
+          uint32_t v[16];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) v[k] = pack_bf16x2(w * acc[i + 2 * k], w * acc[i + 2 * k + 1]);
-          if (whole) {
-            if (col0 + i < args.N) *reinterpret_cast<uint4*>(dst + i) = make_uint4(v[0], v[1], v[2], v[3]);
-          } else {
+          for (int k = 0; k < 16; ++k) v[k] = pack_bf16x2(part.w * acc[c + 2 * k], part.w * acc[c + 2 * k + 1]);
+          if (staged) {
+            put(c >> 5, v, col0 + c);
+          } else if (part.valid) {
+            uint16_t* dst = args.out + row * args.N + col0 + c;
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (col0 + i + k < args.N) dst[i + k] = static_cast<uint16_t>(v[k >> 1] >> (16 * (k & 1)));
+            for (int i = 0; i < 32; i += 8) {
+              if (whole) {
+                if (col0 + c + i < args.N)
+                  *reinterpret_cast<uint4*>(dst + i) = make_uint4(v[i / 2], v[i / 2 + 1], v[i / 2 + 2], v[i / 2 + 3]);
+              } else {
+#pragma unroll
+                for (int k = i; k < i + 8; ++k)
+                  if (col0 + c + k < args.N) dst[k] = static_cast<uint16_t>(v[k >> 1] >> (16 * (k & 1)));
+              }
+            }
           }
         }
       }
     }
+    if (lane == 0) tma_store_wait_all();
+    __syncwarp();
   }
 
   tc_fence_before();
@@ -370,16 +459,21 @@ __global__ void __launch_bounds__(THREADS, 1)
 template <int MODE, int BN>
 cudaError_t launch(const void* a, uint64_t a_rows, const void* b, uint64_t b_rows, const Args& args, int grid,
                    cudaStream_t s) {
-  CUtensorMap ma, mb;
+  CUtensorMap ma, mb, mo;
   if (!make_tma_2d_u8(&ma, a, a_rows, args.K, BM) || !make_tma_2d_u8(&mb, b, b_rows, args.K, BN == 256 ? 128 : BN))
     return cudaErrorInvalidValue;
+  // codes are stored as pairs of bytes
+  const bool staged = args.out_staged;
+  if (staged && !(MODE == OUT_SWIGLU ? make_tma_store_2d_bf16(&mo, args.out_q, a_rows, args.N / 2)
+                                     : make_tma_store_2d_bf16(&mo, args.out, a_rows, args.N)))
+    return cudaErrorInvalidValue;
+  if (!staged) mo = ma;  // not used
   auto kernel = block_gemm_kernel<MODE, BN>;
-  const size_t smem = smem_bytes(Shape<BN>::STAGES, Shape<BN>::STAGE_BYTES, args.E);
-  static_assert(smem_bytes(Shape<BN>::STAGES, Shape<BN>::STAGE_BYTES, 1024) <= SMEM_LIMIT, "fits for every E");
+  static_assert(smem_bytes<BN>(1024) <= SMEM_LIMIT, "fits for every E");
   const cudaError_t err =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_LIMIT);
   if (err != cudaSuccess) return err;
-  return launch_dependent(kernel, grid, THREADS, smem, s, ma, mb, args);
+  return launch_dependent(kernel, grid, THREADS, smem_bytes<BN>(args.E), s, ma, mb, mo, args);
 }
 
 }  // namespace
@@ -398,6 +492,7 @@ cudaError_t launch_block_matmul_tc(const uint8_t* a, const float* a_scale, int M
   g.a_scale = a_scale;
   g.b_scale = b_scale;
   g.out = out;
+  g.out_staged = N % 8 == 0;
   g.status = status;
   const long long mt = (static_cast<long long>(M) + BM - 1) / BM;
   auto tiles = [&](int bn) { return mt * ((N + bn - 1) / bn); };
@@ -429,6 +524,7 @@ cudaError_t launch_block_experts_tc(const uint8_t* x_q, const float* x_scale, co
   g.a_scale = x_scale;
   g.b_scale = W1_scale;
   g.out_q = h_q;
+  g.out_staged = 1;
   g.out_scale = h_scale;
   const uint64_t C = static_cast<uint64_t>(L.capacity), E = static_cast<uint64_t>(L.E);
   cudaError_t err = launch<OUT_SWIGLU, 256>(x_q, C, W1, E * 2 * I, g, sm_count(), s);

@@ -238,6 +238,27 @@ def test_many_unaligned_and_empty_tensors(moe):
     moe.moe_adamw_step(moe.AdamWState([]), [], 1e-2)
 
 
+def test_settings_that_change_between_steps(moe):
+    """Gradients' types, which of them there are, and the decays may be others
+    at each step; a list of decays may be changed in place."""
+    g = torch.Generator().manual_seed(9)
+    start = [torch.randn(300, generator=g).to(DEV) for _ in range(2)]
+    a, b = [t.clone() for t in start], [t.clone() for t in start]
+    oa = moe.AdamWState(a)
+    decay = [0.1, 0.0]
+    for dtypes in ((F32, BF16), (BF16, F32), (None, F32), (F32, None), (F32, F32)):
+        grads = [None if dt is None else torch.randn(300, generator=g).to(dt).to(DEV) for dt in dtypes]
+        ob = moe.AdamWState(b, step=oa.step, exp_avg=[t.clone() for t in oa.exp_avg],
+                            exp_avg_sq=[t.clone() for t in oa.exp_avg_sq])
+        moe.moe_adamw_step(oa, grads, 1e-2, weight_decay=decay)
+        moe.moe_adamw_step(ob, grads, 1e-2, weight_decay=tuple(decay))
+        for i in range(2):
+            assert torch.equal(a[i], b[i]) and torch.equal(oa.exp_avg[i], ob.exp_avg[i])
+        decay[0], decay[1] = decay[1] + 0.3, decay[0]
+    with pytest.raises(ValueError):
+        moe.moe_adamw_step(oa, grads, 1e-2, weight_decay=[0.1, 0.2, 0.3])
+
+
 def test_nonfinite_gradients_stay_in_their_block(moe):
     p = torch.ones(1024, device=DEV)
     grad = torch.ones(1024, device=DEV)
