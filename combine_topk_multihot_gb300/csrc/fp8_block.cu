@@ -50,23 +50,26 @@ __global__ void __launch_bounds__(256) quantize_row_blocks_kernel(const uint16_t
       const int c = col0 + 256 * p;
       q[p] = c < cols ? __ldcs(reinterpret_cast<const uint4*>(src + r * cols + c)) : make_uint4(0, 0, 0, 0);
     }
+    uint32_t top[PIECES];
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p)
+      top[p] = bf16x2_abs_max(bf16x2_abs_max(q[p].x, q[p].y), bf16x2_abs_max(q[p].z, q[p].w));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+      for (int p = 0; p < PIECES; ++p) top[p] = bf16x2_abs_max(top[p], __shfl_xor_sync(FULL_MASK, top[p], o));
+    float mine = 0.f;  // lane i (and i + 16, ...): the scale of piece i / 2's block i % 2
 #pragma unroll
     for (int p = 0; p < PIECES; ++p) {
+      const float scale = block_scale(max_nan(bf16_lo(top[p]), bf16_hi(top[p])));
       const uint32_t w[4] = {q[p].x, q[p].y, q[p].z, q[p].w};
-      float top = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) top = max_nan(top, max_nan(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(FULL_MASK, top, o));
-      const float scale = block_scale(top);
       const int c = col0 + 256 * p;
-      if (c < cols) {
-        *reinterpret_cast<uint2*>(codes + r * cols + c) =
-            make_uint2(e4m3x4(bf16_lo(w[0]), bf16_hi(w[0]), bf16_lo(w[1]), bf16_hi(w[1]), scale),
-                       e4m3x4(bf16_lo(w[2]), bf16_hi(w[2]), bf16_lo(w[3]), bf16_hi(w[3]), scale));
-        if ((lane & 15) == 0) scales[r * blocks + (c >> 7)] = scale;
-      }
+      if (c < cols) *reinterpret_cast<uint2*>(codes + r * cols + c) = BlockDivide(scale).codes(w);
+      const float s = __shfl_sync(FULL_MASK, scale, (lane & 1) * 16);
+      if ((lane >> 1) == p) mine = s;
     }
+    const int b = blockIdx.y * (2 * PIECES) + lane;
+    if (lane < 2 * PIECES && b < blocks) scales[r * blocks + b] = mine;
   }
 }
 
@@ -107,14 +110,13 @@ __global__ void __launch_bounds__(256) quantize_square_blocks_kernel(const uint1
 #pragma unroll
   for (int i = 0; i < 8; ++i) top = max_nan(top, s_top[i]);
   const float scale = block_scale(top);
+  const BlockDivide by(scale);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int r = r0 + 16 * i;
     if (r < rows && c < cols) {
       const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
-      *reinterpret_cast<uint2*>(codes + base + static_cast<long long>(r) * cols + c) =
-          make_uint2(e4m3x4(bf16_lo(w[0]), bf16_hi(w[0]), bf16_lo(w[1]), bf16_hi(w[1]), scale),
-                     e4m3x4(bf16_lo(w[2]), bf16_hi(w[2]), bf16_lo(w[3]), bf16_hi(w[3]), scale));
+      *reinterpret_cast<uint2*>(codes + base + static_cast<long long>(r) * cols + c) = by.codes(w);
     }
   }
   if (threadIdx.x == 0) scales[block] = scale;
@@ -153,6 +155,7 @@ template <int NT, int MODE>
 __global__ void __launch_bounds__(256) stream_kernel(const StreamArgs args) {
   extern __shared__ int s_list[];  // the experts with rows, ascending
   __shared__ int s_active;
+  __shared__ int s_found[32];      // experts with rows in each 32
   __shared__ float s_part[8][NT][4][32];  // [warp][tile][register][lane]
   griddep_launch_dependents();
   griddep_wait();
@@ -162,15 +165,30 @@ __global__ void __launch_bounds__(256) stream_kernel(const StreamArgs args) {
       s_list[0] = 0;
       s_active = 1;
     }
-  } else if (warp == 0) {
-    int n = 0;
-    for (int e0 = 0; e0 < args.E; e0 += 32) {
-      const bool has = e0 + lane < args.E && args.counts[e0 + lane] > 0;
-      const unsigned m = __ballot_sync(FULL_MASK, has);
-      if (has) s_list[n + __popc(m & ((1u << lane) - 1u))] = e0 + lane;
-      n += __popc(m);
+  } else {
+    // all counts are loaded at once (at most 1024), then placed by ballots
+    bool has[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) has[i] = threadIdx.x + 256 * i < args.E && args.counts[threadIdx.x + 256 * i] > 0;
+    unsigned m[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      m[i] = __ballot_sync(FULL_MASK, has[i]);
+      if (lane == 0) s_found[8 * i + warp] = __popc(m[i]);
     }
-    if (lane == 0) s_active = n;
+    __syncthreads();
+    int upto = s_found[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(FULL_MASK, upto, o);
+      if (lane >= o) upto += v;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int before = __shfl_sync(FULL_MASK, upto, 8 * i + warp) - __popc(m[i]);
+      if (has[i]) s_list[before + __popc(m[i] & ((1u << lane) - 1u))] = threadIdx.x + 256 * i;
+    }
+    if (threadIdx.x == 31) s_active = upto;
   }
   __syncthreads();
   const int split = args.split, slabs = 8 / split;
@@ -284,10 +302,10 @@ __global__ void __launch_bounds__(256) swiglu_quantize_kernel(const float* __res
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         const float4 g = g4[q], u = u4[q];
-        h[4 * q] = g.x / (1.0f + __expf(-g.x)) * u.x;
-        h[4 * q + 1] = g.y / (1.0f + __expf(-g.y)) * u.y;
-        h[4 * q + 2] = g.z / (1.0f + __expf(-g.z)) * u.z;
-        h[4 * q + 3] = g.w / (1.0f + __expf(-g.w)) * u.w;
+        h[4 * q] = silu_mul(g.x, u.x);
+        h[4 * q + 1] = silu_mul(g.y, u.y);
+        h[4 * q + 2] = silu_mul(g.z, u.z);
+        h[4 * q + 3] = silu_mul(g.w, u.w);
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) top = max_nan(top, fabsf(h[i]));
@@ -296,8 +314,11 @@ __global__ void __launch_bounds__(256) swiglu_quantize_kernel(const float* __res
     for (int o = 8; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(FULL_MASK, top, o));
     if (c < I) {
       const float scale = block_scale(top);
+      const float y = __frcp_rn(scale);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[i] *= y;
       *reinterpret_cast<uint2*>(codes + r * I + c) =
-          make_uint2(e4m3x4(h[0], h[1], h[2], h[3], scale), e4m3x4(h[4], h[5], h[6], h[7], scale));
+          make_uint2(e4m3x4(h[0], h[1], h[2], h[3]), e4m3x4(h[4], h[5], h[6], h[7]));
       if ((lane & 15) == 0) scales[r * (I >> 7) + (c >> 7)] = scale;
     }
   }
@@ -325,7 +346,9 @@ cudaError_t launch_quantize_block(const uint16_t* src, long long batch, long lon
   if (block_rows == 1) {
     const long long all = batch * rows;
     const int y = (cols + PIECES * 256 - 1) / (PIECES * 256);
-    const long long need = (all + 7) / 8, most = (8LL * sm_count() + y - 1) / y;
+    // a CTA per 8 rows and 1024 columns: the SMs overlap one CTA's loads with
+    // another's arithmetic (looping CTAs, 8 per SM: 4.0 against REPLACE TB/s)
+    const long long need = (all + 7) / 8, most = 1 << 20;
     const dim3 grid(static_cast<unsigned>(need < most ? need : most), y);
     return launch_dependent(quantize_row_blocks_kernel, grid, 256, 0, s, src, all, cols, codes, scales, row_token);
   }

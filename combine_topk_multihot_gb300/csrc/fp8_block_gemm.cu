@@ -134,8 +134,6 @@ __device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
                  "+r"(r[30]), "+r"(r[31])::"memory");
 }
 
-__device__ __forceinline__ float silu(float g) { return g / (1.0f + __expf(-g)); }
-
 template <int MODE, int BN>
 __global__ void __launch_bounds__(THREADS, 1)
     block_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -393,7 +391,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         float top = 0.f;
 #pragma unroll
         for (int i = 0; i < 64; ++i) {
-          acc[i] = silu(acc[i]) * acc[64 + i];
+          acc[i] = silu_mul(acc[i], acc[64 + i]);
           top = max_nan(top, fabsf(acc[i]));
         }
         // The two warps of a lane quarter exchange their maxima.  One meeting a
@@ -405,10 +403,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         const bool met = mbar_wait(smem_u32(&s.pair[q]), parity, abort_flag);
         if (!__all_sync(FULL_MASK, met)) break;
         const float scale = block_scale(max_nan(s.amax[parity][0][r_in_tile], s.amax[parity][1][r_in_tile]));
+        const float y = __frcp_rn(scale);
         uint32_t v[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k)
-          v[k] = e4m3x4(acc[4 * k], acc[4 * k + 1], acc[4 * k + 2], acc[4 * k + 3], scale);
+          v[k] = e4m3x4(y * acc[4 * k], y * acc[4 * k + 1], y * acc[4 * k + 2], y * acc[4 * k + 3]);
         if (staged) {
           put(0, v, part.nt * 64 + half * 32);
         } else if (part.valid) {

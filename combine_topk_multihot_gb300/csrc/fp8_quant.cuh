@@ -59,17 +59,71 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+// The larger magnitudes of two pairs of bf16 values (NaN if there is one).
+__device__ __forceinline__ uint32_t bf16x2_abs_max(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&a), y = *reinterpret_cast<const __nv_bfloat162*>(&b);
+  const __nv_bfloat162 m = __hmax2_nan(__habs2(x), __habs2(y));
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
+
 __device__ __forceinline__ float block_scale(float amax) {
   return amax == 0.f ? 1.0f : max_nan(__fdiv_rn(amax, E4M3_MAX), 0x1p-126f);
 }
 
-// Four codes of v / scale (an IEEE division each), lowest byte first.
-__device__ __forceinline__ uint32_t e4m3x4(float v0, float v1, float v2, float v3, float scale) {
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(v0, scale), __fdiv_rn(v1, scale)),
-                                               __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(v2, scale), __fdiv_rn(v3, scale)),
-                                               __NV_SATFINITE, __NV_E4M3);
+// Four codes, lowest byte first.
+__device__ __forceinline__ uint32_t e4m3x4(float v0, float v1, float v2, float v3) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v0, v1), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v2, v3), __NV_SATFINITE, __NV_E4M3);
   return lo | (hi << 16);
+}
+
+// Quotients by one scale, rounded as an IEEE division rounds them, in three
+// operations each.  By Markstein's theorem ("Computation of elementary
+// functions on the IBM RISC System/6000 processor", 1990): with y the
+// correctly rounded reciprocal of s and q within an ulp of v / s, the residual
+// r = v - q s is exact in a fused multiply-add and q + r y, rounded once, is
+// the correctly rounded quotient.  The residual is exact while its last bit
+// is above fp32's smallest, which holds for |v| >= 2^-103; with a scale of at
+// least 2^-90 a smaller v has a code of zero either way (with v's sign,
+// which is set last: the residual's error may turn it).  Other scales (and
+// non-finite ones) take the division.
+// Bit-exactness matters here: a quotient of two bf16 values often lies midway
+// between two codes, or an fp32 ulp from there.
+struct BlockDivide {
+  float s, y;
+  bool fast;
+  __device__ __forceinline__ explicit BlockDivide(float scale) {
+    s = scale;
+    y = __fdiv_rn(1.0f, scale);
+    fast = scale >= 0x1p-90f && scale < 0x1p100f;
+  }
+  __device__ __forceinline__ float operator()(float v) const {
+    const float q = __fmul_rn(v, y);
+    return copysignf(__fmaf_rn(__fmaf_rn(-q, s, v), y, q), v);
+  }
+  // codes of eight bf16 values
+  __device__ __forceinline__ uint2 codes(const uint32_t (&w)[4]) const {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = bf16_lo(w[i]);
+      v[2 * i + 1] = bf16_hi(w[i]);
+    }
+    if (fast) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = (*this)(v[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __fdiv_rn(v[i], s);
+    }
+    return make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
+  }
+};
+
+// silu(g) u with a reciprocal that may be off by an ulp: h has no exact
+// rounding to keep (g and u are fp32 sums), and its codes have 3 bits.
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  return __fdividef(g, 1.0f + __expf(-g)) * u;
 }
 
 }  // namespace moe

@@ -72,6 +72,25 @@ def test_quantize_bit_exact(moe, shape, block_rows):
         assert np.array_equal(scales.cpu().numpy().reshape(-1, *s.shape)[i], s)
 
 
+def test_quantize_division_rounds_as_ieee(moe):
+    """Every pair of a bf16 significand and a block maximum's significand (128 x
+    128, in all binades that matter), so that each quotient midway between two
+    codes is met: equal to codes from an IEEE division, bit for bit."""
+    top = torch.arange(128, 256, dtype=torch.float32).view(128, 1, 1)          # a row each
+    sig = torch.arange(128, 256, dtype=torch.float32).view(1, 1, 128)
+    # halves of 64 significands: the block's first value is its maximum
+    for e in range(0, 20):
+        v = (sig * 2.0 ** -e).clamp(max=1e30).expand(128, 2, 128).clone()
+        v[v > top] *= 0.5
+        v[:, 0, 0] = top[:, 0, 0]
+        v[:, 1, 1] = top[:, 0, 0]
+        for scale in (2.0 ** -20, 2.0 ** -110, 2.0 ** 60):
+            src = (v * scale).reshape(128, 256).bfloat16()
+            codes, scales = moe.moe_quantize_fp8_block(src.to(DEV))
+            c, s = _quantize_np(src.float().numpy(), 1)
+            assert np.array_equal(codes.cpu().numpy(), c) and np.array_equal(scales.cpu().numpy(), s), (e, scale)
+
+
 def test_quantize_nonfinite(moe):
     src = torch.ones(3, 384, dtype=torch.bfloat16, device=DEV)
     src[0, 5], src[1, 200] = float("nan"), float("inf")
