@@ -1,0 +1,287 @@
+// What the forward and the backward of the norms around a block share: rows
+// as vectors of eight values, sums over a row, the gate, and the copies that
+// bring a row to shared memory.
+#pragma once
+
+#include "common.cuh"
+#include "launch.h"
+
+namespace moe {
+
+namespace norm {
+
+constexpr int MAX_WARPS = 32;
+
+// Eight consecutive values of a row.  `full` (whole, 16-byte aligned vectors)
+// holds for the entire matrix when H % 8 == 0; otherwise rows start anywhere
+// and the last vector is partial, so values go one by one.
+struct F8 {
+  float v[8];
+};
+
+template <bool F32>
+struct Raw;  // a vector as it lies in memory
+template <>
+struct Raw<false> {
+  uint4 q;
+};
+template <>
+struct Raw<true> {
+  uint4 q, r;
+};
+
+template <bool F32>
+__device__ __forceinline__ Raw<F32> raw_zero() {
+  Raw<F32> o;
+  o.q = make_uint4(0, 0, 0, 0);
+  if constexpr (F32) o.r = o.q;
+  return o;
+}
+
+// Rows that do not start on 16 bytes: value by value, out of line (the fast
+// path's code would drown in it).
+template <bool F32>
+__device__ __noinline__ Raw<F32> load_ragged(const void* row, int col, int H) {
+  Raw<F32> o = raw_zero<F32>();
+  if constexpr (F32) {
+    const float* p = static_cast<const float*>(row) + col;
+    uint32_t t[8] = {};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (col + i < H) t[i] = __float_as_uint(p[i]);
+    o.q = make_uint4(t[0], t[1], t[2], t[3]);
+    o.r = make_uint4(t[4], t[5], t[6], t[7]);
+  } else {
+    const uint16_t* p = static_cast<const uint16_t*>(row) + col;
+    uint32_t t[4] = {};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (col + i < H) t[i >> 1] |= static_cast<uint32_t>(p[i]) << (16 * (i & 1));
+    o.q = make_uint4(t[0], t[1], t[2], t[3]);
+  }
+  return o;
+}
+
+// KEEP: a tensor that every row reads again (the weights) stays in L1; the
+// others pass through it once.
+template <bool F32, bool KEEP = false>
+__device__ __forceinline__ Raw<F32> load_raw(const void* row, int col, int H, bool full) {
+  if (!full) return load_ragged<F32>(row, col, H);
+  Raw<F32> o = raw_zero<F32>();
+  if (col >= H) return o;
+  auto get = [](const uint4* p) { return KEEP ? __ldg(p) : __ldcs(p); };
+  if constexpr (F32) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(row) + col);
+    o.q = get(p);
+    o.r = get(p + 1);
+  } else {
+    o.q = get(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + col));
+  }
+  return o;
+}
+
+template <bool F32>
+__device__ __forceinline__ F8 widen(const Raw<F32>& a) {
+  F8 o;
+  if constexpr (F32) {
+    const uint32_t t[8] = {a.q.x, a.q.y, a.q.z, a.q.w, a.r.x, a.r.y, a.r.z, a.r.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o.v[i] = __uint_as_float(t[i]);
+  } else {
+    const uint32_t t[4] = {a.q.x, a.q.y, a.q.z, a.q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      o.v[2 * i] = bf16_lo(t[i]);
+      o.v[2 * i + 1] = bf16_hi(t[i]);
+    }
+  }
+  return o;
+}
+
+// Rounds once to the tensor's type (nearest even).
+template <bool F32>
+__device__ __forceinline__ Raw<F32> narrow(const F8& a) {
+  Raw<F32> o;
+  if constexpr (F32) {
+    o.q = make_uint4(__float_as_uint(a.v[0]), __float_as_uint(a.v[1]), __float_as_uint(a.v[2]), __float_as_uint(a.v[3]));
+    o.r = make_uint4(__float_as_uint(a.v[4]), __float_as_uint(a.v[5]), __float_as_uint(a.v[6]), __float_as_uint(a.v[7]));
+  } else {
+    o.q = make_uint4(pack_bf16x2(a.v[0], a.v[1]), pack_bf16x2(a.v[2], a.v[3]), pack_bf16x2(a.v[4], a.v[5]),
+                     pack_bf16x2(a.v[6], a.v[7]));
+  }
+  return o;
+}
+
+template <bool F32>
+__device__ __noinline__ void store_ragged(void* row, int col, int H, const Raw<F32> a) {
+  if constexpr (F32) {
+    float* p = static_cast<float*>(row) + col;
+    const uint32_t t[8] = {a.q.x, a.q.y, a.q.z, a.q.w, a.r.x, a.r.y, a.r.z, a.r.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (col + i < H) p[i] = __uint_as_float(t[i]);
+  } else {
+    uint16_t* p = static_cast<uint16_t*>(row) + col;
+    const uint32_t t[4] = {a.q.x, a.q.y, a.q.z, a.q.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (col + i < H) p[i] = static_cast<uint16_t>(t[i >> 1] >> (16 * (i & 1)));
+  }
+}
+
+template <bool F32>
+__device__ __forceinline__ void store_raw(void* row, int col, int H, bool full, const Raw<F32>& a) {
+  if (!full) {
+    store_ragged<F32>(row, col, H, a);
+    return;
+  }
+  if (col >= H) return;
+  if constexpr (F32) {
+    uint4* p = reinterpret_cast<uint4*>(static_cast<float*>(row) + col);
+    p[0] = a.q;
+    p[1] = a.r;
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(row) + col) = a.q;
+  }
+}
+
+// Weights and element gates: bf16 or fp32 by a flag that is the same for the
+// whole launch.
+template <bool KEEP = false>
+__device__ __forceinline__ F8 load_either(const void* row, int f32, int col, int H, bool full) {
+  return f32 ? widen(load_raw<true, KEEP>(row, col, H, full)) : widen(load_raw<false, KEEP>(row, col, H, full));
+}
+
+__device__ __forceinline__ const void* row_of(const void* p, long long row, int H, int f32) {
+  return static_cast<const char*>(p) + row * H * (f32 ? 4 : 2);
+}
+__device__ __forceinline__ void* row_of(void* p, long long row, int H, int f32) {
+  return static_cast<char*>(p) + row * H * (f32 ? 4 : 2);
+}
+
+// Sums N values over a group of `threads` threads (a multiple of 32); every
+// thread gets the totals.  The two halves of `red` (this group's) alternate,
+// so one barrier a call is enough: a warp can reach its next write of a half
+// only after a barrier that follows every read of it.
+template <int N>
+__device__ __forceinline__ void group_sum(float (&v)[N], float (*red)[MAX_WARPS][4], int threads, int group,
+                                          int& phase) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(FULL_MASK, v[k], o);
+  if (threads == 32) return;
+  const int warps = threads >> 5, first = group * warps;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (lane == 0) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) red[phase][warp][k] = v[k];
+  }
+  if (threads == blockDim.x) __syncthreads();
+  else asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(threads) : "memory");
+  // the warps' sums lie in every 2^n lanes, so that all lanes end with the total
+  const int span = 2 << (31 - __clz(warps - 1)), mine = lane & (span - 1);
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = mine < warps ? red[phase][first + mine][k] : 0.f;
+  for (int o = 1; o < span; o <<= 1)
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(FULL_MASK, v[k], o);
+  phase ^= 1;
+}
+
+// The gate's factor s and ds/dg.  From e = exp(-|g|), which cannot overflow:
+// s = 1 / (1 + e) or e / (1 + e), and ds/dg = e / (1 + e)^2 on both sides,
+// without the cancellation of 1 - s where s is near 1.
+struct Gate {
+  float s, slope;
+};
+__device__ __forceinline__ Gate gate_of(float g, int sigmoid) {
+  if (!sigmoid) return {g, 1.0f};
+  // 1 + e lies in [1, 2]: the fast division is within 2 ulp there
+  const float e = __expf(-fabsf(g)), inv = __fdividef(1.0f, 1.0f + e);
+  return {g >= 0.f ? inv : e * inv, e * inv * inv};
+}
+
+__device__ __forceinline__ float load_scalar(const void* p, long long i, int f32) {
+  return f32 ? static_cast<const float*>(p)[i]
+             : __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p)[i]) << 16);
+}
+
+// The weight of the norm: offset + w.
+__device__ __forceinline__ F8 load_weight(const void* w, int f32, float offset, int col, int H, bool full) {
+  F8 o = load_either<true>(w, f32, col, H, full);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o.v[i] += offset;
+  return o;
+}
+
+// ---------------------------------------------------------------- rows through shared memory
+// A group of threads brings its next row's tensors to shared memory with bulk
+// copies while it works on the current one from registers: one slot a group
+// is enough, since a row leaves it for the registers as a whole.
+struct RowPipe {
+  uint32_t slot, bar;   // shared-memory addresses
+  uint32_t phase;
+};
+
+// One thread: the copies of `bytes` (a multiple of 16) each from src[0 .. n)
+// to the slot, one after the other; null sources are left out.
+template <int N>
+__device__ __forceinline__ void pipe_issue(const RowPipe& p, const char* const (&src)[N], const uint32_t (&bytes)[N]) {
+  uint32_t total = 0;
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+    if (src[k]) total += bytes[k];
+  mbar_arrive_expect_tx(p.bar, total);
+  uint32_t at = p.slot;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    if (src[k])
+      asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(at),
+                   "l"(src[k]), "r"(bytes[k]), "r"(p.bar)
+                   : "memory");
+    at += bytes[k];
+  }
+}
+
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+
+template <bool F32>
+__device__ __forceinline__ Raw<F32> read_slot(uint32_t row, int col, int H) {
+  Raw<F32> o = raw_zero<F32>();
+  if (col >= H) return o;
+  if constexpr (F32) {
+    o.q = ld_shared_v4(row + col * 4);
+    o.r = ld_shared_v4(row + col * 4 + 16);
+  } else {
+    o.q = ld_shared_v4(row + col * 2);
+  }
+  return o;
+}
+
+// All threads of the group (named barrier 1 + group) agree whether all of them
+// saw their row arrive.
+__device__ __forceinline__ bool group_all(bool ok, int threads, int group) {
+  if (threads == 32) return __all_sync(FULL_MASK, ok);
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.s32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, %2, %3, p;\n\t"
+      "selp.s32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<int>(ok)), "r"(1 + group), "r"(threads)
+      : "memory");
+  return r != 0;
+}
+
+inline int vectors(int H) { return (H + 7) / 8; }
+inline int threads_of(int H, int nv) { return ((vectors(H) + nv - 1) / nv + 31) / 32 * 32; }
+
+}  // namespace norm
+
+}  // namespace moe

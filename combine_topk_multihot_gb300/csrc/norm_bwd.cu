@@ -1,0 +1,352 @@
+// The backward of the norms before and after a block (norm.cu has the forward
+// and the notation).
+//
+// Backward, with d the gradient of the stream (dout plus what comes through
+// the next norm), all sums over a row of H values:
+//   d  = dout + r2 w~2 dnext - out c,   c = r2^3 S1 / H,   S1 = sum w~2 dnext out
+//   dx = a d;   dg = s'(g) d y r w~ (summed over the row for a gate per token)
+//   dy = r w~ s d - y r^3 M / H,   M = sum w~ s y d = S2 - c S3,
+//        S2 = sum w~ s y (dout + r2 w~2 dnext),   S3 = sum w~ s y out
+//   dw = sum over rows of s d y r;   dw2 = sum over rows of dnext out r2
+// Splitting M into S2 - c S3 makes the three sums independent of one another,
+// so a row costs one reduction instead of two.
+//
+// Each tensor is read or written once: bound by HBM.  A row's values stay in
+// registers between the sums and their use, while bulk copies bring the next
+// row to shared memory.  The weight gradients are summed over a group's rows in
+// shared memory (each thread its own columns, so no barrier), written as one
+// partial row per CTA, and added in a fixed order by a second kernel: results
+// do not depend on scheduling.
+
+#include "norm.cuh"
+
+namespace moe {
+
+using namespace norm;
+
+namespace {
+
+// A CTA's threads form groups of `row_threads`, each with a row of its own and
+// its own accumulators; they are added up before the CTA's partial row is
+// written, so that there are few of those.
+// PIPE: rows arrive through shared memory (H a multiple of 8).
+template <bool XF32, bool HAS_Y, bool HAS_NEXT, bool ELEM, int NV, bool PIPE>
+__global__ void __launch_bounds__(NV == 2 ? 256 : 512, NV == 2 ? 2 : 1)
+    norm_backward_kernel(const NormBackwardArgs a, int row_threads) {
+  __shared__ float red[2][MAX_WARPS][4];
+  __shared__ uint64_t s_bar[8];
+  __shared__ int s_abort;
+  extern __shared__ float4 acc[];  // [(HAS_Y + HAS_NEXT) * NV * 2][blockDim.x], then the groups' slots
+  const int H = a.H;
+  const bool full = PIPE || (H & 7) == 0;
+  const float inv_h = 1.0f / static_cast<float>(H);
+  const int group = threadIdx.x / row_threads, in_row = threadIdx.x - group * row_threads;
+  const int groups = blockDim.x / row_threads;
+  constexpr uint32_t XB = XF32 ? 4 : 2;
+  const uint32_t bytes[4] = {a.dout ? H * XB : 0u, HAS_NEXT ? H * XB : 0u, HAS_NEXT ? 2u * H : 0u, HAS_Y ? 2u * H : 0u};
+  RowPipe pipe = {};
+  if constexpr (PIPE) {
+    pipe.slot = smem_u32(acc) + ((HAS_Y ? 1 : 0) + (HAS_NEXT ? 1 : 0)) * NV * 32 * blockDim.x +
+                group * ((bytes[0] + bytes[1] + bytes[2] + bytes[3] + 127u) & ~127u);
+    pipe.bar = smem_u32(&s_bar[group]);
+    if (in_row == 0) mbar_init(pipe.bar, 1);
+    if (threadIdx.x == 0) s_abort = 0;
+    mbar_fence_init();
+    __syncthreads();
+  }
+  griddep_launch_dependents();
+  griddep_wait();
+  auto issue = [&](long long row) {
+    const char* const src[4] = {a.dout ? static_cast<const char*>(row_of(a.dout, row, H, XF32)) : nullptr,
+                                HAS_NEXT ? static_cast<const char*>(row_of(a.out, row, H, XF32)) : nullptr,
+                                HAS_NEXT ? static_cast<const char*>(row_of(a.dnext, row, H, 0)) : nullptr,
+                                HAS_Y ? static_cast<const char*>(row_of(a.y, row, H, 0)) : nullptr};
+    pipe_issue(pipe, src, bytes);
+  };
+  int phase = 0;
+  auto col = [&](int j) { return 8 * (in_row + j * row_threads); };
+  constexpr int ACC = (HAS_Y ? 1 : 0) + (HAS_NEXT ? 1 : 0);
+#pragma unroll
+  for (int k = 0; k < ACC * NV * 2; ++k) acc[k * blockDim.x + threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto accumulate = [&](int which, int j, const F8& p, const F8& q) {  // += p q
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float4* at = acc + ((which * NV + j) * 2 + h) * blockDim.x + threadIdx.x;
+      float4 v = *at;
+      v.x += p.v[4 * h] * q.v[4 * h];
+      v.y += p.v[4 * h + 1] * q.v[4 * h + 1];
+      v.z += p.v[4 * h + 2] * q.v[4 * h + 2];
+      v.w += p.v[4 * h + 3] * q.v[4 * h + 3];
+      *at = v;
+    }
+  };
+
+  const long long stride = static_cast<long long>(gridDim.x) * groups;
+  long long t = static_cast<long long>(blockIdx.x) * groups + group;
+  if (PIPE && in_row == 0 && t < a.T) issue(t);
+  for (; t < a.T; t += stride) {
+    Raw<XF32> dout[NV], out[NV];
+    Raw<false> dnext[NV], y[NV];
+    if constexpr (PIPE) {
+      const bool here = mbar_wait(pipe.bar, pipe.phase, &s_abort);
+      pipe.phase ^= 1u;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        dout[j] = a.dout ? read_slot<XF32>(pipe.slot, col(j), H) : raw_zero<XF32>();
+        if constexpr (HAS_NEXT) {
+          out[j] = read_slot<XF32>(pipe.slot + bytes[0], col(j), H);
+          dnext[j] = read_slot<false>(pipe.slot + bytes[0] + bytes[1], col(j), H);
+        }
+        if constexpr (HAS_Y) y[j] = read_slot<false>(pipe.slot + bytes[0] + bytes[1] + bytes[2], col(j), H);
+      }
+      if (!group_all(here, row_threads, group)) break;  // (also: every read of the slot is done)
+      if (in_row == 0 && t + stride < a.T) issue(t + stride);
+    }
+#pragma unroll
+    for (int j = 0; j < NV && !PIPE; ++j) {
+      dout[j] = a.dout ? load_raw<XF32>(row_of(a.dout, t, H, XF32), col(j), H, full) : raw_zero<XF32>();
+      if constexpr (HAS_NEXT) {
+        dnext[j] = load_raw<false>(row_of(a.dnext, t, H, 0), col(j), H, full);
+        out[j] = load_raw<XF32>(row_of(a.out, t, H, XF32), col(j), H, full);
+      }
+      if constexpr (HAS_Y) y[j] = load_raw<false>(row_of(a.y, t, H, 0), col(j), H, full);
+    }
+    const float r = HAS_Y ? a.rstd[t] : 0.f;
+    const float r2 = HAS_NEXT ? a.rstd2[t] : 0.f;
+    Gate gate = {1.0f, 1.0f};
+    if constexpr (HAS_Y && !ELEM)
+      if (a.gate_kind == MOE_GATE_TOKEN) gate = gate_of(load_scalar(a.gate, t, a.gate_f32), a.sigmoid);
+    auto element_gate = [&](int j) { return load_either(row_of(a.gate, t, H, a.gate_f32), a.gate_f32, col(j), H, full); };
+
+    // S1, S2, S3: a gate per token stays outside of the sums
+    constexpr int N = HAS_Y && HAS_NEXT ? 3 : 1, S1 = 0, S2 = HAS_NEXT ? 1 : 0, S3 = 2;
+    float sum[N] = {};
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      F8 d = widen(dout[j]), o;
+      if constexpr (HAS_NEXT) {
+        o = widen(out[j]);
+        const F8 dn = widen(dnext[j]), w2 = load_weight(a.w2, a.w_f32, a.offset, col(j), H, full);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float e = w2.v[i] * dn.v[i];
+          sum[S1] += e * o.v[i];
+          d.v[i] += r2 * e;
+        }
+      }
+      if constexpr (HAS_Y) {
+        const F8 f = widen(y[j]), w = load_weight(a.w, a.w_f32, a.offset, col(j), H, full);
+        F8 g;
+        if constexpr (ELEM) g = element_gate(j);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float e = w.v[i] * f.v[i];
+          if constexpr (ELEM) e *= gate_of(g.v[i], a.sigmoid).s;
+          sum[S2] += e * d.v[i];
+          if constexpr (HAS_NEXT) sum[S3] += e * o.v[i];
+        }
+      }
+    }
+    group_sum(sum, red, row_threads, group, phase);
+    const float c = HAS_NEXT ? r2 * r2 * r2 * (sum[S1] * inv_h) : 0.f;
+    float m = HAS_Y ? sum[N == 3 ? S2 : 0] : 0.f;  // sum of w y d (times s where it is per element)
+    if constexpr (N == 3) m -= c * sum[S3];
+    const float k = r * r * r * (gate.s * m * inv_h), rs = r * gate.s;
+    if constexpr (HAS_Y && !ELEM)
+      if (a.gate_kind == MOE_GATE_TOKEN && a.dgate && in_row == 0) {
+        const float dg = gate.slope * r * m;
+        if (a.gate_f32) static_cast<float*>(a.dgate)[t] = dg;
+        else static_cast<uint16_t*>(a.dgate)[t] = static_cast<uint16_t>(pack_bf16x2(dg, 0.f));
+      }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      F8 d = widen(dout[j]);
+      if constexpr (HAS_NEXT) {
+        const F8 o = widen(out[j]), w2 = load_weight(a.w2, a.w_f32, a.offset, col(j), H, full);
+        F8 dn = widen(dnext[j]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          dn.v[i] *= r2;
+          d.v[i] += w2.v[i] * dn.v[i] - o.v[i] * c;
+        }
+        accumulate(HAS_Y ? 1 : 0, j, dn, o);
+      }
+      F8 dx;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) dx.v[i] = HAS_Y ? a.residual_scale * d.v[i] : d.v[i];
+      store_raw<XF32>(row_of(a.dx, t, H, XF32), col(j), H, full, narrow<XF32>(dx));
+      if constexpr (HAS_Y) {
+        const F8 f = widen(y[j]), w = load_weight(a.w, a.w_f32, a.offset, col(j), H, full);
+        F8 dy, sd;  // sd: r s d
+        if constexpr (ELEM) {
+          F8 g = element_gate(j);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const Gate gi = gate_of(g.v[i], a.sigmoid);
+            sd.v[i] = gi.s * (r * d.v[i]);
+            g.v[i] = gi.slope * (d.v[i] * (f.v[i] * r * w.v[i]));
+          }
+          if (a.dgate) {
+            void* dst = row_of(a.dgate, t, H, a.gate_f32);
+            if (a.gate_f32) store_raw<true>(dst, col(j), H, full, narrow<true>(g));
+            else store_raw<false>(dst, col(j), H, full, narrow<false>(g));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sd.v[i] = rs * d.v[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dy.v[i] = w.v[i] * sd.v[i] - f.v[i] * k;
+        accumulate(0, j, sd, f);
+        store_raw<false>(row_of(a.dy, t, H, 0), col(j), H, full, narrow<false>(dy));
+      }
+    }
+  }
+  __syncthreads();
+
+  // this CTA's sums: one row of [ACC, H] partials, or the result when it is
+  // alone; the groups are added in order
+  if (group == 0) {
+#pragma unroll
+    for (int which = 0; which < ACC; ++which) {
+      float* dst = a.partials + (static_cast<long long>(blockIdx.x) * ACC + which) * H;
+      if (gridDim.x == 1) dst = which == 0 && HAS_Y ? a.dw : a.dw2;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float4* at = acc + ((which * NV + j) * 2 + h) * blockDim.x + threadIdx.x;
+          float4 v = at[0];
+          for (int g = 1; g < groups; ++g) {
+            const float4 u = at[g * row_threads];
+            v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+          }
+          const int c = col(j) + 4 * h;
+          if (full) {
+            if (c < H) *reinterpret_cast<float4*>(dst + c) = v;
+          } else {
+            const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (c + i < H) dst[c + i] = f[i];
+          }
+        }
+    }
+  }
+}
+
+// Adds the partial rows [rows, cols] of the weight gradients (columns
+// [0, split) go to d0, the others to d1).  A CTA takes 32 columns, its 32
+// warps every 32nd row each; the warps' sums are added in warp order.
+__global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* __restrict__ partials, int rows, int cols,
+                                                           int split, float* __restrict__ d0,
+                                                           float* __restrict__ d1) {
+  __shared__ float part[32][33];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  float v = 0.f;
+  if (c < cols)
+    for (int r = warp; r < rows; r += 32) v += partials[static_cast<long long>(r) * cols + c];
+  part[warp][lane] = v;
+  __syncthreads();
+  v = part[lane][warp];  // warp w now holds column w's 32 sums, one per lane
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(FULL_MASK, v, o);
+  const int oc = blockIdx.x * 32 + warp;
+  if (lane == 0 && oc < cols) {
+    if (oc < split) d0[oc] = v; else d1[oc - split] = v;
+  }
+}
+
+constexpr size_t SMEM_PER_CTA = 227 * 1024 - 2048, SMEM_PER_SM = 228 * 1024;  // (static shared memory aside)
+
+// Two vectors a thread keep the four tensors of a row in 128 registers with 512
+// threads on an SM; one where a row is short or rows are few (then its
+// latency counts); four for rows above 4096.
+struct BackwardShape {
+  int nv, row_threads, groups, per_sm, grid;
+  bool pipe;
+};
+BackwardShape backward_shape(long long T, int H) {
+  const int v = vectors(H);
+  BackwardShape b = {};
+  b.nv = (v <= 32 || T < 4LL * sm_count() || H % 8) && v <= 512 ? 1 : v <= 512 ? 2 : 4;
+  b.row_threads = threads_of(H, b.nv);
+  b.pipe = b.nv > 1 && H % 8 == 0;
+  b.groups = T > sm_count() && b.row_threads <= 128 ? 256 / b.row_threads : 1;
+  if (b.groups > 8) b.groups = 8;
+  const int threads = b.row_threads * b.groups;
+  b.per_sm = threads > 256 ? 1 : 512 / threads > 4 ? 4 : 512 / threads;
+  const long long need = (T + b.groups - 1) / b.groups, most = static_cast<long long>(sm_count()) * b.per_sm;
+  b.grid = static_cast<int>(need < most ? need : most);
+  return b;
+}
+
+template <bool XF32, bool HAS_Y, bool HAS_NEXT>
+size_t slot_bytes(const NormBackwardArgs& a) {
+  const size_t row = (a.dout ? (XF32 ? 4 : 2) : 0) + (HAS_NEXT ? (XF32 ? 4 : 2) + 2 : 0) + (HAS_Y ? 2 : 0);
+  return (row * a.H + 127) / 128 * 128;
+}
+
+template <bool XF32, bool HAS_Y, bool HAS_NEXT, bool ELEM, int NV, bool PIPE>
+cudaError_t backward_launch(const NormBackwardArgs& a, const BackwardShape& b, cudaStream_t s) {
+  constexpr int ACC = (HAS_Y ? 1 : 0) + (HAS_NEXT ? 1 : 0);
+  auto kernel = norm_backward_kernel<XF32, HAS_Y, HAS_NEXT, ELEM, NV, PIPE>;
+  const int threads = b.row_threads * b.groups;
+  size_t smem = static_cast<size_t>(ACC) * NV * 2 * threads * sizeof(float4);
+  if (PIPE) smem += slot_bytes<XF32, HAS_Y, HAS_NEXT>(a) * b.groups;
+  if (smem > 32 * 1024) {  // (with the static part, above 48 KiB needs leave)
+    const cudaError_t err =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (err != cudaSuccess) return err;
+  }
+  return launch_dependent(kernel, static_cast<unsigned>(b.grid), threads, smem, s, a, b.row_threads);
+}
+
+template <bool XF32, bool HAS_Y, bool HAS_NEXT, bool ELEM>
+cudaError_t backward(const NormBackwardArgs& a, cudaStream_t s) {
+  constexpr int ACC = (HAS_Y ? 1 : 0) + (HAS_NEXT ? 1 : 0);
+  BackwardShape b = backward_shape(a.T, a.H);
+  // The slots have to fit beside the accumulators, if need be with one CTA less
+  // an SM; else (wide fp32 rows) the rows are loaded directly.
+  const size_t sums = static_cast<size_t>(ACC) * b.nv * 2 * b.row_threads * b.groups * sizeof(float4);
+  const size_t all = sums + slot_bytes<XF32, HAS_Y, HAS_NEXT>(a) * b.groups;
+  if (b.pipe && all > SMEM_PER_CTA) b.pipe = false;
+  if (b.pipe && b.per_sm > 1 && all > SMEM_PER_SM / b.per_sm - 2048) {
+    b.per_sm = 1;
+    if (b.grid > sm_count()) b.grid = sm_count();
+  }
+  if (b.grid > 0) {
+    const cudaError_t err = b.nv == 1   ? backward_launch<XF32, HAS_Y, HAS_NEXT, ELEM, 1, false>(a, b, s)
+                            : b.nv == 2 ? backward_launch<XF32, HAS_Y, HAS_NEXT, ELEM, 2, true>(a, b, s)  // always fits
+                            : b.pipe    ? backward_launch<XF32, HAS_Y, HAS_NEXT, ELEM, 4, true>(a, b, s)
+                                        : backward_launch<XF32, HAS_Y, HAS_NEXT, ELEM, 4, false>(a, b, s);
+    if (err != cudaSuccess || b.grid == 1) return err;
+  }
+  const int cols = ACC * a.H;
+  return launch_dependent(norm_reduce_kernel, (cols + 31) / 32, 1024, 0, s, a.partials, b.grid, cols,
+                          HAS_Y ? a.H : 0, a.dw, a.dw2);
+}
+
+// The three forms, each with and without a gate per element.
+template <bool XF32>
+cudaError_t backward_any(const NormBackwardArgs& a, cudaStream_t s) {
+  const bool elem = a.gate_kind == MOE_GATE_ELEMENT;
+  if (!a.has_y) return backward<XF32, false, true, false>(a, s);
+  if (a.has_next) return elem ? backward<XF32, true, true, true>(a, s) : backward<XF32, true, true, false>(a, s);
+  return elem ? backward<XF32, true, false, true>(a, s) : backward<XF32, true, false, false>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_norm_backward(const NormBackwardArgs& a, cudaStream_t s) {
+  return a.x_f32 ? backward_any<true>(a, s) : backward_any<false>(a, s);
+}
+
+size_t norm_backward_workspace(long long T, int H) {
+  return static_cast<size_t>(backward_shape(T, H).grid) * 2 * H * sizeof(float);
+}
+
+}  // namespace moe

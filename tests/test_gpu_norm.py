@@ -50,7 +50,11 @@ def _rms64(v, eps):
 
 # ragged and odd widths, one value, one vector, every vectors-per-thread form
 SIZES = [(1, 1), (1, 2048), (3, 7), (5, 8), (2, 33), (130, 256), (33, 2048), (7, 2049), (700, 512), (9, 4096),
-         (400, 4096), (5, 4104), (320, 8192), (4, 8199), (3, 16384), (310, 10000)]
+         (400, 4096), (5, 4104), (320, 8192), (4, 8199), (3, 16384), (310, 10000),
+         # rows for every SM: through shared memory, in groups of 32 to 512 threads
+         (1300, 264), (1300, 1024), (2000, 2048), (1300, 4096), (640, 5000), (650, 8192), (640, 16384),
+         # and rows that do not start on 16 bytes
+         (1300, 130), (1300, 2049), (640, 8199)]
 
 
 @pytest.mark.parametrize("T,H", SIZES)
