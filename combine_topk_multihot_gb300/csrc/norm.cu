@@ -23,15 +23,21 @@ using namespace norm;
 
 namespace {
 
-// A group of `row_threads` threads takes one row at a time.  With one vector a
-// thread (few rows: what counts is the latency of one) the weights stay in
-// registers; else they come from L1 at each use.  PIPE: rows arrive through
+// Rows in flight a group: with the weights in registers two; with the weights
+// in L1 one, which leaves them the room.
+template <int NV>
+constexpr int SLOTS_OF = NV <= 2 ? 2 : 1;
+
+// A group of `row_threads` threads takes one row at a time.  With up to two
+// vectors a thread the weights stay in registers; else they come from L1 at
+// each use.  PIPE: rows arrive through
 // shared memory (H a multiple of 8).
 template <bool XF32, bool HAS_Y, bool HAS_NEXT, bool ELEM, int NV, bool PIPE>
 __global__ void __launch_bounds__(NV == 1 ? 1024 : PIPE ? 256 : 512, PIPE ? 2 : 1)
     norm_forward_kernel(const NormArgs a, int row_threads) {
   __shared__ float red[2][MAX_WARPS][4];
-  __shared__ uint64_t s_bar[8];
+  constexpr int SLOTS = SLOTS_OF<NV>;
+  __shared__ uint64_t s_bar[MAX_GROUPS][SLOTS];
   __shared__ int s_abort;
   extern __shared__ __align__(128) uint8_t s_rows[];
   const int H = a.H;
@@ -39,11 +45,12 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : PIPE ? 256 : 512, PIPE ? 2 : 
   const int group = threadIdx.x / row_threads, in_row = threadIdx.x - group * row_threads;
   const int groups = blockDim.x / row_threads;
   const uint32_t bytes[3] = {HAS_Y ? 2u * H : 0u, H * (XF32 ? 4u : 2u), ELEM && !a.gate_f32 ? 2u * H : 0u};
-  RowPipe pipe = {};
+  RowPipe<SLOTS> pipe = {};
   if constexpr (PIPE) {
-    pipe.slot = smem_u32(s_rows) + group * ((bytes[0] + bytes[1] + bytes[2] + 127u) & ~127u);
-    pipe.bar = smem_u32(&s_bar[group]);
-    if (in_row == 0) mbar_init(pipe.bar, 1);
+    pipe.slot_bytes = (bytes[0] + bytes[1] + bytes[2] + 127u) & ~127u;
+    pipe.base = smem_u32(s_rows) + group * SLOTS * pipe.slot_bytes;
+    pipe.bars = smem_u32(&s_bar[group][0]);
+    if (in_row < SLOTS) mbar_init(pipe.bars + 8 * in_row, 1);
     if (threadIdx.x == 0) s_abort = 0;
     mbar_fence_init();
     __syncthreads();
@@ -52,37 +59,42 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : PIPE ? 256 : 512, PIPE ? 2 : 
   griddep_wait();
   const long long stride = static_cast<long long>(gridDim.x) * groups;
   long long t = static_cast<long long>(blockIdx.x) * groups + group;
-  auto issue = [&](long long row) {
+  auto issue = [&](long long row, int slot) {
     const char* const src[3] = {HAS_Y ? static_cast<const char*>(row_of(a.y, row, H, 0)) : nullptr,
                                 static_cast<const char*>(row_of(a.x, row, H, XF32)),
                                 ELEM && !a.gate_f32 ? static_cast<const char*>(row_of(a.gate, row, H, 0)) : nullptr};
-    pipe_issue(pipe, src, bytes);
+    pipe_issue(pipe.base + slot * pipe.slot_bytes, pipe.bars + 8 * slot, src, bytes);
   };
-  if (PIPE && in_row == 0 && t < a.T) issue(t);
+  if (PIPE && in_row == 0)
+    for (int i = 0; i < SLOTS; ++i)
+      if (t + i * stride < a.T) issue(t + i * stride, i);
   const float inv_h = 1.0f / static_cast<float>(H);
   int phase = 0;
   auto col = [&](int j) { return 8 * (in_row + j * row_threads); };
-  F8 wk = {}, w2k = {};
-  if constexpr (NV == 1) {
-    if constexpr (HAS_Y) wk = load_weight(a.w, a.w_f32, a.offset, col(0), H, full);
-    if constexpr (HAS_NEXT) w2k = load_weight(a.w2, a.w_f32, a.offset, col(0), H, full);
+  constexpr bool KEEP = NV <= 2;
+  F8 wk[KEEP ? NV : 1] = {}, w2k[KEEP ? NV : 1] = {};
+#pragma unroll
+  for (int j = 0; KEEP && j < NV; ++j) {
+    if constexpr (HAS_Y) wk[j] = load_weight(a.w, a.w_f32, a.offset, col(j), H, full);
+    if constexpr (HAS_NEXT) w2k[j] = load_weight(a.w2, a.w_f32, a.offset, col(j), H, full);
   }
   for (; t < a.T; t += stride) {
     Raw<XF32> x[NV];
     Raw<false> y[NV];
     Raw<false> gates[ELEM && PIPE ? NV : 1];  // an fp32 gate is read from memory again: registers
     if constexpr (PIPE) {
-      const bool here = mbar_wait(pipe.bar, pipe.phase, &s_abort);
-      pipe.phase ^= 1u;
+      const bool here = mbar_wait(pipe.bar(), pipe.phase, &s_abort);
+      const uint32_t slot = pipe.slot();
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        if constexpr (HAS_Y) y[j] = read_slot<false>(pipe.slot, col(j), H);
-        x[j] = read_slot<XF32>(pipe.slot + bytes[0], col(j), H);
+        if constexpr (HAS_Y) y[j] = read_slot<false>(slot, col(j), H);
+        x[j] = read_slot<XF32>(slot + bytes[0], col(j), H);
         if constexpr (ELEM)
-          if (!a.gate_f32) gates[j] = read_slot<false>(pipe.slot + bytes[0] + bytes[1], col(j), H);
+          if (!a.gate_f32) gates[j] = read_slot<false>(slot + bytes[0] + bytes[1], col(j), H);
       }
       if (!group_all(here, row_threads, group)) break;  // (also: every read of the slot is done)
-      if (in_row == 0 && t + stride < a.T) issue(t + stride);
+      if (in_row == 0 && t + SLOTS * stride < a.T) issue(t + SLOTS * stride, pipe.at);
+      pipe.next();
     } else {
       const void* xr = row_of(a.x, t, H, XF32);
       const void* yr = HAS_Y ? row_of(a.y, t, H, 0) : nullptr;
@@ -110,7 +122,7 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : PIPE ? 256 : 512, PIPE ? 2 : 
       void* out = row_of(a.out, t, H, XF32);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const F8 f = widen(y[j]), w = NV == 1 ? wk : load_weight(a.w, a.w_f32, a.offset, col(j), H, full);
+        const F8 f = widen(y[j]), w = KEEP ? wk[KEEP ? j : 0] : load_weight(a.w, a.w_f32, a.offset, col(j), H, full);
         F8 o = widen(x[j]);
         if constexpr (ELEM) {
           const F8 g = PIPE && !a.gate_f32 ? widen(gates[PIPE ? j : 0])
@@ -140,7 +152,7 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : PIPE ? 256 : 512, PIPE ? 2 : 
       void* next = row_of(a.next, t, H, 0);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const F8 w = NV == 1 ? w2k : load_weight(a.w2, a.w_f32, a.offset, col(j), H, full);
+        const F8 w = KEEP ? w2k[KEEP ? j : 0] : load_weight(a.w2, a.w_f32, a.offset, col(j), H, full);
         F8 o = widen(x[j]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) o.v[i] = o.v[i] * r * w.v[i];
@@ -152,9 +164,11 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : PIPE ? 256 : 512, PIPE ? 2 : 
 
 // Vectors a thread.  Each row costs a thread about 100 instructions besides
 // its elements' (sums, addresses), so with rows enough to fill the SMs a
-// thread takes four vectors (T = 16384, H = 2048, with the next norm: 64 us
-// with one, 59 with eight, REPLACE with four); with fewer than four rows an SM
-// a row is spread over as many threads as it can use.
+// thread takes two vectors, with the weights in registers, or four where a row
+// is longer than 4096 (T = 16384, H = 2048, bf16 with the next norm: 64 us with
+// one vector, 53 with two, 59 with eight and the weights in L1); with fewer than four rows an SM a row is
+// spread over as many threads as it can use: what counts then is the latency
+// of one.
 struct ForwardShape {
   int nv, row_threads, groups, per_sm;
   bool pipe;
@@ -162,10 +176,11 @@ struct ForwardShape {
 ForwardShape forward_shape(long long T, int H) {
   const int v = vectors(H);
   ForwardShape f = {};
-  f.nv = (T < 4LL * sm_count() || v <= 32 || H % 8) && v <= 1024 ? 1 : 4;
+  const bool direct = T < 4LL * sm_count() || v <= 32 || H % 8;
+  f.nv = direct && v <= 1024 ? 1 : v <= 512 ? 2 : 4;
   f.row_threads = threads_of(H, f.nv);
   f.pipe = f.nv > 1 && H % 8 == 0 && f.row_threads <= 256;
-  f.groups = f.pipe ? 256 / f.row_threads : 1;
+  f.groups = !f.pipe ? 1 : 256 / f.row_threads > MAX_GROUPS ? MAX_GROUPS : 256 / f.row_threads;
   f.per_sm = f.pipe ? 2 : f.row_threads >= 512 ? 2 : 1024 / f.row_threads > 16 ? 16 : 1024 / f.row_threads;
   return f;
 }
@@ -179,7 +194,7 @@ cudaError_t forward_launch(const NormArgs& a, const ForwardShape& f, cudaStream_
   size_t smem = 0;
   if (PIPE) {
     const size_t row = (HAS_Y ? 2 : 0) + (XF32 ? 4 : 2) + (ELEM && !a.gate_f32 ? 2 : 0);
-    smem = (row * a.H + 127) / 128 * 128 * f.groups;
+    smem = (row * a.H + 127) / 128 * 128 * f.groups * SLOTS_OF<NV>;
     if (smem > 32 * 1024) {  // (with the static part, above 48 KiB needs leave)
       const cudaError_t err =
           cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
@@ -194,6 +209,7 @@ cudaError_t forward(const NormArgs& a, cudaStream_t s) {
   const ForwardShape f = forward_shape(a.T, a.H);
   if (f.nv == 1) return forward_launch<XF32, HAS_Y, HAS_NEXT, ELEM, 1, false>(a, f, s);
   if (!f.pipe) return forward_launch<XF32, HAS_Y, HAS_NEXT, ELEM, 4, false>(a, f, s);
+  if (f.nv == 2) return forward_launch<XF32, HAS_Y, HAS_NEXT, ELEM, 2, true>(a, f, s);
   return forward_launch<XF32, HAS_Y, HAS_NEXT, ELEM, 4, true>(a, f, s);
 }
 

@@ -216,29 +216,41 @@ __device__ __forceinline__ F8 load_weight(const void* w, int f32, float offset, 
 }
 
 // ---------------------------------------------------------------- rows through shared memory
-// A group of threads brings its next row's tensors to shared memory with bulk
-// copies while it works on the current one from registers: one slot a group
-// is enough, since a row leaves it for the registers as a whole.
+// A group of threads brings its next rows' tensors to shared memory with bulk
+// copies while it works on the current one from registers: a row leaves its
+// slot for the registers as a whole, so the group's SLOTS slots are all in
+// flight while it computes.
+constexpr int MAX_GROUPS = 8;
+template <int SLOTS>
 struct RowPipe {
-  uint32_t slot, bar;   // shared-memory addresses
+  uint32_t base, slot_bytes, bars;  // shared-memory addresses of the group's slots and barriers
+  int at;                           // the slot of the current row
   uint32_t phase;
+  __device__ __forceinline__ uint32_t slot() const { return base + at * slot_bytes; }
+  __device__ __forceinline__ uint32_t bar() const { return bars + 8 * at; }
+  __device__ __forceinline__ void next() {
+    if (++at == SLOTS) {
+      at = 0;
+      phase ^= 1u;
+    }
+  }
 };
 
 // One thread: the copies of `bytes` (a multiple of 16) each from src[0 .. n)
 // to the slot, one after the other; null sources are left out.
 template <int N>
-__device__ __forceinline__ void pipe_issue(const RowPipe& p, const char* const (&src)[N], const uint32_t (&bytes)[N]) {
+__device__ __forceinline__ void pipe_issue(uint32_t slot, uint32_t bar, const char* const (&src)[N], const uint32_t (&bytes)[N]) {
   uint32_t total = 0;
 #pragma unroll
   for (int k = 0; k < N; ++k)
     if (src[k]) total += bytes[k];
-  mbar_arrive_expect_tx(p.bar, total);
-  uint32_t at = p.slot;
+  mbar_arrive_expect_tx(bar, total);
+  uint32_t at = slot;
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     if (src[k])
       asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(at),
-                   "l"(src[k]), "r"(bytes[k]), "r"(p.bar)
+                   "l"(src[k]), "r"(bytes[k]), "r"(bar)
                    : "memory");
     at += bytes[k];
   }

@@ -26,42 +26,49 @@ using namespace norm;
 
 namespace {
 
+// One row in flight a group besides the current one: a second slot takes the
+// room in L1 that the weights need (183 against 240 us at T = 16384, H = 4096).
+constexpr int SLOTS = 1;
+
 // A CTA's threads form groups of `row_threads`, each with a row of its own and
 // its own accumulators; they are added up before the CTA's partial row is
 // written, so that there are few of those.
 // PIPE: rows arrive through shared memory (H a multiple of 8).
 template <bool XF32, bool HAS_Y, bool HAS_NEXT, bool ELEM, int NV, bool PIPE>
-__global__ void __launch_bounds__(NV == 2 ? 256 : 512, NV == 2 ? 2 : 1)
+__global__ void __launch_bounds__(512, 1)
     norm_backward_kernel(const NormBackwardArgs a, int row_threads) {
   __shared__ float red[2][MAX_WARPS][4];
-  __shared__ uint64_t s_bar[8];
+  __shared__ uint64_t s_bar[MAX_GROUPS][SLOTS];
   __shared__ int s_abort;
-  extern __shared__ float4 acc[];  // [(HAS_Y + HAS_NEXT) * NV * 2][blockDim.x], then the groups' slots
+  extern __shared__ __align__(128) float4 acc[];  // [(HAS_Y + HAS_NEXT) * NV * 2][blockDim.x], then the groups' slots
   const int H = a.H;
   const bool full = PIPE || (H & 7) == 0;
   const float inv_h = 1.0f / static_cast<float>(H);
   const int group = threadIdx.x / row_threads, in_row = threadIdx.x - group * row_threads;
   const int groups = blockDim.x / row_threads;
   constexpr uint32_t XB = XF32 ? 4 : 2;
-  const uint32_t bytes[4] = {a.dout ? H * XB : 0u, HAS_NEXT ? H * XB : 0u, HAS_NEXT ? 2u * H : 0u, HAS_Y ? 2u * H : 0u};
-  RowPipe pipe = {};
+  const uint32_t bytes[5] = {a.dout ? H * XB : 0u, HAS_NEXT ? H * XB : 0u, HAS_NEXT ? 2u * H : 0u, HAS_Y ? 2u * H : 0u,
+                             ELEM && !a.gate_f32 ? 2u * H : 0u};  // (an fp32 gate is read from memory)
+  RowPipe<SLOTS> pipe = {};
   if constexpr (PIPE) {
-    pipe.slot = smem_u32(acc) + ((HAS_Y ? 1 : 0) + (HAS_NEXT ? 1 : 0)) * NV * 32 * blockDim.x +
-                group * ((bytes[0] + bytes[1] + bytes[2] + bytes[3] + 127u) & ~127u);
-    pipe.bar = smem_u32(&s_bar[group]);
-    if (in_row == 0) mbar_init(pipe.bar, 1);
+    pipe.slot_bytes = (bytes[0] + bytes[1] + bytes[2] + bytes[3] + bytes[4] + 127u) & ~127u;
+    pipe.base = smem_u32(acc) + ((HAS_Y ? 1 : 0) + (HAS_NEXT ? 1 : 0)) * NV * 32 * blockDim.x +
+                group * SLOTS * pipe.slot_bytes;
+    pipe.bars = smem_u32(&s_bar[group][0]);
+    if (in_row < SLOTS) mbar_init(pipe.bars + 8 * in_row, 1);
     if (threadIdx.x == 0) s_abort = 0;
     mbar_fence_init();
     __syncthreads();
   }
   griddep_launch_dependents();
   griddep_wait();
-  auto issue = [&](long long row) {
-    const char* const src[4] = {a.dout ? static_cast<const char*>(row_of(a.dout, row, H, XF32)) : nullptr,
+  auto issue = [&](long long row, int slot) {
+    const char* const src[5] = {a.dout ? static_cast<const char*>(row_of(a.dout, row, H, XF32)) : nullptr,
                                 HAS_NEXT ? static_cast<const char*>(row_of(a.out, row, H, XF32)) : nullptr,
                                 HAS_NEXT ? static_cast<const char*>(row_of(a.dnext, row, H, 0)) : nullptr,
-                                HAS_Y ? static_cast<const char*>(row_of(a.y, row, H, 0)) : nullptr};
-    pipe_issue(pipe, src, bytes);
+                                HAS_Y ? static_cast<const char*>(row_of(a.y, row, H, 0)) : nullptr,
+                                ELEM && !a.gate_f32 ? static_cast<const char*>(row_of(a.gate, row, H, 0)) : nullptr};
+    pipe_issue(pipe.base + slot * pipe.slot_bytes, pipe.bars + 8 * slot, src, bytes);
   };
   int phase = 0;
   auto col = [&](int j) { return 8 * (in_row + j * row_threads); };
@@ -83,24 +90,29 @@ __global__ void __launch_bounds__(NV == 2 ? 256 : 512, NV == 2 ? 2 : 1)
 
   const long long stride = static_cast<long long>(gridDim.x) * groups;
   long long t = static_cast<long long>(blockIdx.x) * groups + group;
-  if (PIPE && in_row == 0 && t < a.T) issue(t);
+  if (PIPE && in_row == 0)
+    for (int i = 0; i < SLOTS; ++i)
+      if (t + i * stride < a.T) issue(t + i * stride, i);
   for (; t < a.T; t += stride) {
     Raw<XF32> dout[NV], out[NV];
-    Raw<false> dnext[NV], y[NV];
+    Raw<false> dnext[NV], y[NV], gates[ELEM && PIPE ? NV : 1];
     if constexpr (PIPE) {
-      const bool here = mbar_wait(pipe.bar, pipe.phase, &s_abort);
-      pipe.phase ^= 1u;
+      const bool here = mbar_wait(pipe.bar(), pipe.phase, &s_abort);
+      uint32_t slot = pipe.slot();
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        dout[j] = a.dout ? read_slot<XF32>(pipe.slot, col(j), H) : raw_zero<XF32>();
+        dout[j] = a.dout ? read_slot<XF32>(slot, col(j), H) : raw_zero<XF32>();
         if constexpr (HAS_NEXT) {
-          out[j] = read_slot<XF32>(pipe.slot + bytes[0], col(j), H);
-          dnext[j] = read_slot<false>(pipe.slot + bytes[0] + bytes[1], col(j), H);
+          out[j] = read_slot<XF32>(slot + bytes[0], col(j), H);
+          dnext[j] = read_slot<false>(slot + bytes[0] + bytes[1], col(j), H);
         }
-        if constexpr (HAS_Y) y[j] = read_slot<false>(pipe.slot + bytes[0] + bytes[1] + bytes[2], col(j), H);
+        if constexpr (HAS_Y) y[j] = read_slot<false>(slot + bytes[0] + bytes[1] + bytes[2], col(j), H);
+        if constexpr (ELEM)
+          if (!a.gate_f32) gates[j] = read_slot<false>(slot + bytes[0] + bytes[1] + bytes[2] + bytes[3], col(j), H);
       }
       if (!group_all(here, row_threads, group)) break;  // (also: every read of the slot is done)
-      if (in_row == 0 && t + stride < a.T) issue(t + stride);
+      if (in_row == 0 && t + SLOTS * stride < a.T) issue(t + SLOTS * stride, pipe.at);
+      pipe.next();
     }
 #pragma unroll
     for (int j = 0; j < NV && !PIPE; ++j) {
@@ -116,39 +128,49 @@ __global__ void __launch_bounds__(NV == 2 ? 256 : 512, NV == 2 ? 2 : 1)
     Gate gate = {1.0f, 1.0f};
     if constexpr (HAS_Y && !ELEM)
       if (a.gate_kind == MOE_GATE_TOKEN) gate = gate_of(load_scalar(a.gate, t, a.gate_f32), a.sigmoid);
-    auto element_gate = [&](int j) { return load_either(row_of(a.gate, t, H, a.gate_f32), a.gate_f32, col(j), H, full); };
+    auto element_gate = [&](int j) {
+      return PIPE && !a.gate_f32 ? widen(gates[ELEM && PIPE ? j : 0])
+                                 : load_either(row_of(a.gate, t, H, a.gate_f32), a.gate_f32, col(j), H, full);
+    };
 
-    // S1, S2, S3: a gate per token stays outside of the sums
+    // S1, S2, S3 (a gate per token stays outside of them), and what needs none
+    // of them: dw2, and d without its last term, which is kept in fp32 with w
     constexpr int N = HAS_Y && HAS_NEXT ? 3 : 1, S1 = 0, S2 = HAS_NEXT ? 1 : 0, S3 = 2;
     float sum[N] = {};
+    F8 d[NV], w[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      F8 d = widen(dout[j]), o;
+      d[j] = widen(dout[j]);
+      F8 o;
       if constexpr (HAS_NEXT) {
         o = widen(out[j]);
-        const F8 dn = widen(dnext[j]), w2 = load_weight(a.w2, a.w_f32, a.offset, col(j), H, full);
+        const F8 w2 = load_weight(a.w2, a.w_f32, a.offset, col(j), H, full);
+        F8 dn = widen(dnext[j]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
+          dn.v[i] *= r2;
           const float e = w2.v[i] * dn.v[i];
           sum[S1] += e * o.v[i];
-          d.v[i] += r2 * e;
+          d[j].v[i] += e;
         }
+        accumulate(HAS_Y ? 1 : 0, j, dn, o);
       }
       if constexpr (HAS_Y) {
-        const F8 f = widen(y[j]), w = load_weight(a.w, a.w_f32, a.offset, col(j), H, full);
+        const F8 f = widen(y[j]);
+        w[j] = load_weight(a.w, a.w_f32, a.offset, col(j), H, full);
         F8 g;
         if constexpr (ELEM) g = element_gate(j);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          float e = w.v[i] * f.v[i];
+          float e = w[j].v[i] * f.v[i];
           if constexpr (ELEM) e *= gate_of(g.v[i], a.sigmoid).s;
-          sum[S2] += e * d.v[i];
+          sum[S2] += e * d[j].v[i];
           if constexpr (HAS_NEXT) sum[S3] += e * o.v[i];
         }
       }
     }
     group_sum(sum, red, row_threads, group, phase);
-    const float c = HAS_NEXT ? r2 * r2 * r2 * (sum[S1] * inv_h) : 0.f;
+    const float c = HAS_NEXT ? r2 * r2 * (sum[S1] * inv_h) : 0.f;  // S1 has one factor r2 already
     float m = HAS_Y ? sum[N == 3 ? S2 : 0] : 0.f;  // sum of w y d (times s where it is per element)
     if constexpr (N == 3) m -= c * sum[S3];
     const float k = r * r * r * (gate.s * m * inv_h), rs = r * gate.s;
@@ -160,31 +182,26 @@ __global__ void __launch_bounds__(NV == 2 ? 256 : 512, NV == 2 ? 2 : 1)
       }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      F8 d = widen(dout[j]);
       if constexpr (HAS_NEXT) {
-        const F8 o = widen(out[j]), w2 = load_weight(a.w2, a.w_f32, a.offset, col(j), H, full);
-        F8 dn = widen(dnext[j]);
+        const F8 o = widen(out[j]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          dn.v[i] *= r2;
-          d.v[i] += w2.v[i] * dn.v[i] - o.v[i] * c;
-        }
-        accumulate(HAS_Y ? 1 : 0, j, dn, o);
+        for (int i = 0; i < 8; ++i) d[j].v[i] -= o.v[i] * c;
       }
       F8 dx;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) dx.v[i] = HAS_Y ? a.residual_scale * d.v[i] : d.v[i];
+      for (int i = 0; i < 8; ++i) dx.v[i] = HAS_Y ? a.residual_scale * d[j].v[i] : d[j].v[i];
       store_raw<XF32>(row_of(a.dx, t, H, XF32), col(j), H, full, narrow<XF32>(dx));
       if constexpr (HAS_Y) {
-        const F8 f = widen(y[j]), w = load_weight(a.w, a.w_f32, a.offset, col(j), H, full);
+        const F8 f = widen(y[j]);
         F8 dy, sd;  // sd: r s d
         if constexpr (ELEM) {
           F8 g = element_gate(j);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const Gate gi = gate_of(g.v[i], a.sigmoid);
-            sd.v[i] = gi.s * (r * d.v[i]);
-            g.v[i] = gi.slope * (d.v[i] * (f.v[i] * r * w.v[i]));
+            const float rd = r * d[j].v[i];
+            sd.v[i] = gi.s * rd;
+            g.v[i] = gi.slope * (rd * (f.v[i] * w[j].v[i]));
           }
           if (a.dgate) {
             void* dst = row_of(a.dgate, t, H, a.gate_f32);
@@ -193,10 +210,10 @@ __global__ void __launch_bounds__(NV == 2 ? 256 : 512, NV == 2 ? 2 : 1)
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) sd.v[i] = rs * d.v[i];
+          for (int i = 0; i < 8; ++i) sd.v[i] = rs * d[j].v[i];
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dy.v[i] = w.v[i] * sd.v[i] - f.v[i] * k;
+        for (int i = 0; i < 8; ++i) dy.v[i] = w[j].v[i] * sd.v[i] - f.v[i] * k;
         accumulate(0, j, sd, f);
         store_raw<false>(row_of(a.dy, t, H, 0), col(j), H, full, narrow<false>(dy));
       }
@@ -260,11 +277,11 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* __restri
   }
 }
 
-constexpr size_t SMEM_PER_CTA = 227 * 1024 - 2048, SMEM_PER_SM = 228 * 1024;  // (static shared memory aside)
+constexpr size_t SMEM_PER_SM = 228 * 1024;
 
-// Two vectors a thread keep the four tensors of a row in 128 registers with 512
-// threads on an SM; one where a row is short or rows are few (then its
-// latency counts); four for rows above 4096.
+// Vectors a thread: one while there are too few rows to fill the SMs (then the
+// latency of one counts) or rows are short or ragged, else two, which keep the
+// tensors of a row in 128 registers; four above 8192 values a row.
 struct BackwardShape {
   int nv, row_threads, groups, per_sm, grid;
   bool pipe;
@@ -272,11 +289,11 @@ struct BackwardShape {
 BackwardShape backward_shape(long long T, int H) {
   const int v = vectors(H);
   BackwardShape b = {};
-  b.nv = (v <= 32 || T < 4LL * sm_count() || H % 8) && v <= 512 ? 1 : v <= 512 ? 2 : 4;
+  b.nv = (v <= 32 || T < 4LL * sm_count() || H % 8) && v <= 512 ? 1 : v <= 1024 && H % 8 == 0 ? 2 : 4;
   b.row_threads = threads_of(H, b.nv);
   b.pipe = b.nv > 1 && H % 8 == 0;
   b.groups = T > sm_count() && b.row_threads <= 128 ? 256 / b.row_threads : 1;
-  if (b.groups > 8) b.groups = 8;
+  if (b.groups > MAX_GROUPS) b.groups = MAX_GROUPS;
   const int threads = b.row_threads * b.groups;
   b.per_sm = threads > 256 ? 1 : 512 / threads > 4 ? 4 : 512 / threads;
   const long long need = (T + b.groups - 1) / b.groups, most = static_cast<long long>(sm_count()) * b.per_sm;
@@ -286,7 +303,8 @@ BackwardShape backward_shape(long long T, int H) {
 
 template <bool XF32, bool HAS_Y, bool HAS_NEXT>
 size_t slot_bytes(const NormBackwardArgs& a) {
-  const size_t row = (a.dout ? (XF32 ? 4 : 2) : 0) + (HAS_NEXT ? (XF32 ? 4 : 2) + 2 : 0) + (HAS_Y ? 2 : 0);
+  const size_t row = (a.dout ? (XF32 ? 4 : 2) : 0) + (HAS_NEXT ? (XF32 ? 4 : 2) + 2 : 0) + (HAS_Y ? 2 : 0) +
+                     (a.gate_kind == MOE_GATE_ELEMENT && !a.gate_f32 ? 2 : 0);
   return (row * a.H + 127) / 128 * 128;
 }
 
@@ -296,7 +314,7 @@ cudaError_t backward_launch(const NormBackwardArgs& a, const BackwardShape& b, c
   auto kernel = norm_backward_kernel<XF32, HAS_Y, HAS_NEXT, ELEM, NV, PIPE>;
   const int threads = b.row_threads * b.groups;
   size_t smem = static_cast<size_t>(ACC) * NV * 2 * threads * sizeof(float4);
-  if (PIPE) smem += slot_bytes<XF32, HAS_Y, HAS_NEXT>(a) * b.groups;
+  if (PIPE) smem += slot_bytes<XF32, HAS_Y, HAS_NEXT>(a) * b.groups * SLOTS;
   if (smem > 32 * 1024) {  // (with the static part, above 48 KiB needs leave)
     const cudaError_t err =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
@@ -309,18 +327,15 @@ template <bool XF32, bool HAS_Y, bool HAS_NEXT, bool ELEM>
 cudaError_t backward(const NormBackwardArgs& a, cudaStream_t s) {
   constexpr int ACC = (HAS_Y ? 1 : 0) + (HAS_NEXT ? 1 : 0);
   BackwardShape b = backward_shape(a.T, a.H);
-  // The slots have to fit beside the accumulators, if need be with one CTA less
-  // an SM; else (wide fp32 rows) the rows are loaded directly.
+  // The slots have to fit beside the sums, if need be with one CTA an SM; else
+  // (wide rows) the rows are loaded directly.
   const size_t sums = static_cast<size_t>(ACC) * b.nv * 2 * b.row_threads * b.groups * sizeof(float4);
-  const size_t all = sums + slot_bytes<XF32, HAS_Y, HAS_NEXT>(a) * b.groups;
-  if (b.pipe && all > SMEM_PER_CTA) b.pipe = false;
-  if (b.pipe && b.per_sm > 1 && all > SMEM_PER_SM / b.per_sm - 2048) {
-    b.per_sm = 1;
-    if (b.grid > sm_count()) b.grid = sm_count();
-  }
+  const size_t all = sums + slot_bytes<XF32, HAS_Y, HAS_NEXT>(a) * b.groups * SLOTS;
+  if (b.pipe && all > SMEM_PER_SM - 3072) b.pipe = false;
+  if (b.pipe && all > SMEM_PER_SM / b.per_sm - 3072 && b.grid > sm_count()) b.grid = sm_count();
   if (b.grid > 0) {
     const cudaError_t err = b.nv == 1   ? backward_launch<XF32, HAS_Y, HAS_NEXT, ELEM, 1, false>(a, b, s)
-                            : b.nv == 2 ? backward_launch<XF32, HAS_Y, HAS_NEXT, ELEM, 2, true>(a, b, s)  // always fits
+                            : b.nv == 2 ? backward_launch<XF32, HAS_Y, HAS_NEXT, ELEM, 2, true>(a, b, s)  // fits: H <= 8192
                             : b.pipe    ? backward_launch<XF32, HAS_Y, HAS_NEXT, ELEM, 4, true>(a, b, s)
                                         : backward_launch<XF32, HAS_Y, HAS_NEXT, ELEM, 4, false>(a, b, s);
     if (err != cudaSuccess || b.grid == 1) return err;
