@@ -19,7 +19,7 @@ from .block import (moe_norm_in, moe_norm_in_backward, moe_norm_out, moe_norm_ou
                     moe_quantize_fp8_block, moe_matmul_fp8_block, moe_grouped_experts_fp8_block)
 from . import _native
 from . import ops
-from .ops import moe_layer, moe_layer_from_logits
+from .ops import moe_block, moe_layer, moe_layer_from_logits, moe_layer_fp8_block
 
 __all__ = [
     "Layout", "MoEError", "ForwardResult", "worst_case_rows", "moe_router_topk",
@@ -32,5 +32,5 @@ __all__ = [
     "moe_grouped_experts_backward", "moe_norm_in", "moe_norm_in_backward", "moe_norm_out", "moe_norm_out_backward",
     "AdamWState", "moe_adamw_step",
     "moe_quantize_fp8_block", "moe_matmul_fp8_block", "moe_grouped_experts_fp8_block",
-    "_native", "ops", "moe_layer", "moe_layer_from_logits",
+    "_native", "ops", "moe_block", "moe_layer", "moe_layer_from_logits", "moe_layer_fp8_block",
 ]

@@ -8,7 +8,9 @@ autograd rule, and the dispatch handle, which no operator can carry, travels
 between them as its component tensors and is put back together on the far
 side.  Here every step of the layer is such an operator: the router (with
 its gradient registered on the operator), multihot, dispatch, grouped
-experts, combine, and the four backward steps.
+experts, combine, and the four backward steps.  So are the norms before and
+after a block (norm_in and norm_out, with their gradients) and the block-scaled
+e4m3 quantiser, product and experts.
 
 Every operator takes the sync-free route: the expanded buffers are sized for
 the worst case (T*K + E*(pad_multiple - 1) rows), nothing is read back to the
@@ -20,11 +22,12 @@ arithmetic runs in its CUDA kernels.
 """
 from __future__ import annotations
 
-from typing import List, Tuple
+from typing import List, Optional, Tuple
 
 import torch
 from torch import Tensor
 
+from . import block as _b
 from . import moe as _m
 
 NS = "moe_gb300"
@@ -285,6 +288,194 @@ def moe_layer(x: Tensor, topk_idx: Tensor, topk_probs: Tensor, W1: Tensor, W2: T
         out = _ops.combine(y, lay, T, K, pad_multiple, E)
         status = lay[-1]
     return (out, status) if return_status else out
+
+
+# ------------------------------------------------------------------ the norms around a block
+@torch.library.custom_op(f"{NS}::norm_in", mutates_args=(), device_types="cuda")
+def norm_in(x: Tensor, weight: Tensor, eps: float, weight_offset: float) -> Tuple[Tensor, Tensor]:
+    """(norm bf16 [T, H], rstd fp32 [T])."""
+    return _b.moe_norm_in(x.contiguous(), weight.contiguous(), eps, weight_offset, save_rstd=True)
+
+
+@norm_in.register_fake
+def _(x, weight, eps, weight_offset):
+    return x.new_empty(x.shape, dtype=torch.bfloat16), x.new_empty(x.shape[0], dtype=torch.float32)
+
+
+@torch.library.custom_op(f"{NS}::norm_in_backward", mutates_args=(), device_types="cuda")
+def norm_in_backward(grad_norm: Tensor, x: Tensor, weight: Tensor, rstd: Tensor, weight_offset: float) -> Tuple[Tensor, Tensor]:
+    """(grad_x, grad_weight fp32 [H])."""
+    return _b.moe_norm_in_backward(grad_norm.contiguous(), x.contiguous(), weight.contiguous(), rstd,
+                                   weight_offset=weight_offset)
+
+
+@norm_in_backward.register_fake
+def _(grad_norm, x, weight, rstd, weight_offset):
+    return x.new_empty(x.shape), weight.new_empty(weight.shape, dtype=torch.float32)
+
+
+def _norm_in_setup(ctx, inputs, output):
+    x, weight, _, ctx.weight_offset = inputs
+    ctx.save_for_backward(x, weight, output[1])
+    ctx.mark_non_differentiable(output[1])
+    ctx.set_materialize_grads(False)
+
+
+def _norm_in_backward(ctx, grad_norm, _grad_rstd):
+    x, weight, rstd = ctx.saved_tensors
+    if grad_norm is None:
+        return None, None, None, None
+    gx, gw = torch.ops.moe_gb300.norm_in_backward(grad_norm, x, weight, rstd, ctx.weight_offset)
+    return gx, gw.to(weight.dtype), None, None
+
+
+torch.library.register_autograd(f"{NS}::norm_in", _norm_in_backward, setup_context=_norm_in_setup)
+
+
+@torch.library.custom_op(f"{NS}::norm_out", mutates_args=(), device_types="cuda")
+def norm_out(x: Tensor, y: Tensor, weight: Tensor, gate: Optional[Tensor], next_weight: Optional[Tensor],
+             residual_scale: float, gate_sigmoid: bool, eps: float,
+             weight_offset: float) -> Tuple[Tensor, Tensor, Tensor, Tensor]:
+    """(out, next, rstd, next_rstd); next and next_rstd have no rows without a next norm."""
+    out, rstd, nxt, next_rstd = _b.moe_norm_out(
+        x.contiguous(), y.contiguous(), weight.contiguous(), None if gate is None else gate.contiguous(),
+        residual_scale, gate_sigmoid, None if next_weight is None else next_weight.contiguous(), eps, weight_offset,
+        save_rstd=True)
+    if nxt is None:
+        nxt, next_rstd = y.new_empty(0, x.shape[1]), rstd.new_empty(0)
+    return out, nxt, rstd, next_rstd
+
+
+@norm_out.register_fake
+def _(x, y, weight, gate, next_weight, residual_scale, gate_sigmoid, eps, weight_offset):
+    T, H = x.shape
+    S = T if next_weight is not None else 0
+    f32 = dict(dtype=torch.float32, device=x.device)
+    return (x.new_empty(T, H), torch.empty(S, H, dtype=torch.bfloat16, device=x.device), torch.empty(T, **f32),
+            torch.empty(S, **f32))
+
+
+@torch.library.custom_op(f"{NS}::norm_out_backward", mutates_args=(), device_types="cuda")
+def norm_out_backward(grad_out: Optional[Tensor], grad_next: Optional[Tensor], out: Optional[Tensor], y: Tensor,
+                      weight: Tensor, gate: Optional[Tensor], rstd: Tensor, next_weight: Optional[Tensor],
+                      next_rstd: Optional[Tensor], residual_scale: float, gate_sigmoid: bool,
+                      weight_offset: float) -> Tuple[Tensor, Tensor, Tensor, Tensor, Tensor]:
+    """(grad_x, grad_y, grad_gate, grad_weight fp32, grad_next_weight fp32); no elements where there is no such input."""
+    opt = lambda t: None if t is None else t.contiguous()  # noqa: E731
+    gx, gy, gg, gw, gw2 = _b.moe_norm_out_backward(
+        opt(grad_out), y.contiguous(), weight.contiguous(), rstd, opt(gate), residual_scale, gate_sigmoid, opt(grad_next),
+        opt(out), opt(next_weight), next_rstd, weight_offset)
+    return gx, gy, rstd.new_empty(0) if gg is None else gg, gw, rstd.new_empty(0) if gw2 is None else gw2
+
+
+@norm_out_backward.register_fake
+def _(grad_out, grad_next, out, y, weight, gate, rstd, next_weight, next_rstd, residual_scale, gate_sigmoid, weight_offset):
+    like = grad_out if grad_out is not None else out
+    f32 = dict(dtype=torch.float32, device=y.device)
+    return (like.new_empty(y.shape), y.new_empty(y.shape),
+            torch.empty(0, **f32) if gate is None else gate.new_empty(gate.shape), torch.empty(weight.shape, **f32),
+            torch.empty(weight.shape if next_weight is not None else 0, **f32))
+
+
+def _norm_out_setup(ctx, inputs, output):
+    x, y, weight, gate, next_weight, ctx.residual_scale, ctx.gate_sigmoid, _, ctx.weight_offset = inputs
+    out, nxt, rstd, next_rstd = output
+    ctx.save_for_backward(y, weight, gate, next_weight, rstd, out if next_weight is not None else None, next_rstd)
+    ctx.mark_non_differentiable(*((rstd, next_rstd) if next_weight is not None else (nxt, rstd, next_rstd)))
+    ctx.set_materialize_grads(False)
+    ctx.x_dtype = x.dtype
+
+
+def _norm_out_backward(ctx, grad_out, grad_next, _grad_rstd, _grad_next_rstd):
+    y, weight, gate, next_weight, rstd, out, next_rstd = ctx.saved_tensors
+    if grad_out is None and grad_next is None:
+        return (None,) * 9
+    if next_weight is None or grad_next is None:      # only the stream was used
+        out = used = None
+        if grad_out is None:
+            return (None,) * 9
+    else:
+        used = next_weight
+    gx, gy, gg, gw, gw2 = torch.ops.moe_gb300.norm_out_backward(
+        grad_out, grad_next if used is not None else None, out, y, weight, gate, rstd, used,
+        next_rstd if used is not None else None, ctx.residual_scale, ctx.gate_sigmoid, ctx.weight_offset)
+    return (gx, gy, gw.to(weight.dtype), gg if gate is not None else None,
+            gw2.to(used.dtype) if used is not None else None, None, None, None, None)
+
+
+torch.library.register_autograd(f"{NS}::norm_out", _norm_out_backward, setup_context=_norm_out_setup)
+
+
+# ------------------------------------------------------------------ block-scaled e4m3
+@torch.library.custom_op(f"{NS}::quantize_fp8_block", mutates_args=(), device_types="cuda")
+def quantize_fp8_block(src: Tensor, block_rows: int) -> Tuple[Tensor, Tensor]:
+    """(codes uint8, scales fp32)."""
+    return _b.moe_quantize_fp8_block(src.contiguous(), block_rows)
+
+
+@quantize_fp8_block.register_fake
+def _(src, block_rows):
+    R, C = src.shape[-2:]
+    return (src.new_empty(src.shape, dtype=torch.uint8),
+            src.new_empty((*src.shape[:-2], (R + block_rows - 1) // block_rows, (C + 127) // 128), dtype=torch.float32))
+
+
+@torch.library.custom_op(f"{NS}::matmul_fp8_block", mutates_args=(), device_types="cuda")
+def matmul_fp8_block(a_q: Tensor, a_scale: Tensor, b_q: Tensor, b_scale: Tensor) -> Tensor:
+    """a b^T, [M, N] bf16."""
+    return _b.moe_matmul_fp8_block(a_q, a_scale, b_q, b_scale)
+
+
+@matmul_fp8_block.register_fake
+def _(a_q, a_scale, b_q, b_scale):
+    return a_q.new_empty(a_q.shape[0], b_q.shape[0], dtype=torch.bfloat16)
+
+
+@torch.library.custom_op(f"{NS}::grouped_experts_fp8_block", mutates_args=(), device_types="cuda")
+def grouped_experts_fp8_block(x_disp: Tensor, W1_q: Tensor, W1_scale: Tensor, W2_q: Tensor, W2_scale: Tensor,
+                              lay: List[Tensor], T: int, top_k: int, pad_multiple: int) -> Tensor:
+    """y [C, H] bf16, for combine."""
+    return _b.moe_grouped_experts_fp8_block(x_disp, _layout(T, W1_q.shape[0], top_k, pad_multiple, lay), W1_q, W1_scale,
+                                            W2_q, W2_scale)
+
+
+@grouped_experts_fp8_block.register_fake
+def _(x_disp, W1_q, W1_scale, W2_q, W2_scale, lay, T, top_k, pad_multiple):
+    return x_disp.new_empty(x_disp.shape)
+
+
+def moe_layer_fp8_block(x: Tensor, topk_idx: Tensor, topk_probs: Tensor, W1_q: Tensor, W1_scale: Tensor, W2_q: Tensor,
+                        W2_scale: Tensor, pad_multiple: int = 1) -> Tensor:
+    """The layer for inference from weights with 128 x 128 block scales
+    (quantize_fp8_block of W1 and W2, block_rows 128): multihot, dispatch,
+    experts with both products in e4m3, combine."""
+    T, K = topk_idx.shape
+    E = W1_q.shape[0]
+    rmap, probs, _, status = _ops.route_to_multihot(topk_idx, topk_probs, E)
+    x_disp, *lay = _ops.dispatch(x, rmap, probs, status, K, pad_multiple)
+    y = _ops.grouped_experts_fp8_block(x_disp, W1_q, W1_scale, W2_q, W2_scale, lay, T, K, pad_multiple)
+    return _ops.combine(y, lay, T, K, pad_multiple, E)
+
+
+def moe_block(x: Tensor, normed: Tensor, router: Tensor, top_k: int, W1: Tensor, W2: Tensor, norm_out_weight: Tensor,
+              gate: Optional[Tensor] = None, next_weight: Optional[Tensor] = None, residual_scale: float = 1.0,
+              pad_multiple: int = 1, eps: float = 1e-6, fp8: Optional[Tuple[Tensor, Tensor]] = None):
+    """A MoE block between two norms: from the residual stream x and its norm
+    (``norm_in``, or the block before's ``next``), the router's logits
+    ``normed @ router^T``, the layer, and ``norm_out``.  Returns (out, next), next
+    being None without ``next_weight``.
+
+    Differentiable in everything but the top-k choice.  With ``fp8`` = (W1_scale,
+    W2_scale), W1 and W2 are e4m3 codes with block scales and the layer runs for
+    inference."""
+    logits = (normed.float() @ router.float().t()).contiguous()
+    if fp8 is None:
+        y = moe_layer_from_logits(normed, logits, top_k, W1, W2, pad_multiple)
+    else:
+        idx, p = _ops.router_topk(logits, top_k)
+        y = moe_layer_fp8_block(normed, idx, p, W1, fp8[0], W2, fp8[1], pad_multiple)
+    out, nxt, _, _ = _ops.norm_out(x, y, norm_out_weight, gate, next_weight, residual_scale, True, eps, 0.0)
+    return out, (nxt if next_weight is not None else None)
 
 
 def moe_layer_from_logits(x: Tensor, router_logits: Tensor, top_k: int, W1: Tensor, W2: Tensor,
