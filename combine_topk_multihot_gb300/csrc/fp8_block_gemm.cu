@@ -40,20 +40,29 @@ namespace {
 
 constexpr int BM = 128;
 constexpr int BKB = 128;  // codes per block and stage
-constexpr int EPI_WARPS = 8;
-// Three warpgroups: one for the producer and the issuers, two for the promotion.  12 warps are launched with 168 registers a
-// thread; 128 x 56 + 256 x 224 = 384 x 168, so the promoting threads' share can
-// grow to hold 128 accumulators without spilling.
-constexpr int THREADS = 32 * (4 + EPI_WARPS);
-constexpr int LAUNCH_REGS = 168, FEW_REGS = 56, MANY_REGS = 224;
-static_assert(128 * FEW_REGS + 32 * EPI_WARPS * MANY_REGS <= THREADS * LAUNCH_REGS, "registers are only passed on");
 constexpr int MAX_STAGES = 8;
 constexpr int MAX_BUFS = 4;
 constexpr int SMEM_LIMIT = 232448;
 
 enum Mode { OUT_PLAIN = 0, OUT_WEIGHTED = 1, OUT_SWIGLU = 2 };
 
-template <int BN>
+// Warps 0..3 are the producer, the issuers and the scales; EPI more warps (8 or
+// 16) promote, two or four for each quarter of the tile's columns.  A promoting
+// thread holds 128 or 64 accumulators, more registers than an even share: the
+// first warpgroup passes some of its own on.
+//   8 warps:  384 x 168 = 128 x 56 + 256 x 224
+//   16 warps: 640 x  96 = 128 x 64 + 512 x 104
+// Sixteen hide the epilogue better, which short contractions need (the
+// experts, K = 2048 and 768, T = 4096: 297 against 330 us), eight have less to
+// meet about in each block (8192 x 8192 x 4096: 225 against 247 us).
+template <int EPI>
+struct Warps {
+  static constexpr int THREADS = 32 * (4 + EPI);
+  static constexpr int LAUNCH_REGS = EPI == 8 ? 168 : 96, FEW_REGS = EPI == 8 ? 56 : 64, MANY_REGS = EPI == 8 ? 224 : 104;
+  static_assert(128 * FEW_REGS + 32 * EPI * MANY_REGS <= THREADS * LAUNCH_REGS, "registers are only passed on");
+};
+
+template <int BN, int EPI>
 struct Shape {
   static constexpr int A_BYTES = BM * BKB;
   static constexpr int B_BYTES = BN * BKB;
@@ -63,7 +72,7 @@ struct Shape {
   static constexpr int STAGING_BYTES = BM * BN * 2;
   static constexpr int BUFS = BN == 256 ? 2 : 4;
   static constexpr int TMEM_COLS = BN * BUFS;
-  static constexpr int COLS = BN / 2;  // accumulators of a promoting thread
+  static constexpr int COLS = BN / (EPI / 4);  // accumulators of a promoting thread
 };
 
 struct Smem {
@@ -72,17 +81,17 @@ struct Smem {
   uint64_t tfull[MAX_BUFS];
   uint64_t tempty[MAX_BUFS];
   uint64_t drain[2];
-  uint64_t pair[4];   // SwiGLU: the two warps of a lane quarter, once a tile
+  uint64_t meet[4];   // SwiGLU: the four warps of a lane quarter, once a tile
   uint32_t tmem_base;
   int abort;
   int total_tiles;
-  float amax[2][2][BM];  // SwiGLU: [tile parity][column half] largest |h| of a row
+  float scale[MAX_BUFS][2][BM];  // of each row, for the two blocks of 128 columns (or gate and up)
 };
 
 template <int BN>
 constexpr size_t smem_bytes(int E) {
-  return 1024 + static_cast<size_t>(Shape<BN>::STAGES) * Shape<BN>::STAGE_BYTES + Shape<BN>::STAGING_BYTES +
-         sizeof(Smem) + static_cast<size_t>(3 * E + 2) * sizeof(int);
+  using S = Shape<BN, 8>;
+  return 1024 + static_cast<size_t>(S::STAGES) * S::STAGE_BYTES + S::STAGING_BYTES + sizeof(Smem) + static_cast<size_t>(3 * E + 2) * sizeof(int);
 }
 
 struct Args {
@@ -134,12 +143,30 @@ __device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
                  "+r"(r[30]), "+r"(r[31])::"memory");
 }
 
-template <int MODE, int BN>
-__global__ void __launch_bounds__(THREADS, 1)
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) {
+  static_assert(N == 16 || N == 32, "columns");
+  if constexpr (N == 32) {
+    tmem_ld32(taddr, r);
+  } else {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+#pragma unroll
+    for (int i = 16; i < 32; ++i) r[i] = 0;
+  }
+}
+
+template <int MODE, int BN, int EPI>
+__global__ void __launch_bounds__(Warps<EPI>::THREADS, 1)
     block_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ CUtensorMap tmOut, const Args args) {
-  using S = Shape<BN>;
-  static_assert(MODE != OUT_SWIGLU || BN == 256, "a tile of h is one scale block wide");
+  using S = Shape<BN, EPI>;
+  constexpr int FEW_REGS = Warps<EPI>::FEW_REGS, MANY_REGS = Warps<EPI>::MANY_REGS;
+  static_assert(MODE != OUT_SWIGLU || (BN == 256 && EPI == 16), "a tile of h is one scale block wide, 32 columns a warp");
   constexpr int STAGES = S::STAGES, BUFS = S::BUFS, COLS = S::COLS;
   constexpr uint32_t IDESC = idesc_e4m3_f32(BM, BN);
   extern __shared__ uint8_t smem_raw[];
@@ -160,10 +187,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(smem_u32(&s.empty[i]), 1);
     }
     for (int i = 0; i < BUFS; ++i) {
-      mbar_init(smem_u32(&s.tfull[i]), 1);
-      mbar_init(smem_u32(&s.tempty[i]), EPI_WARPS);
+      mbar_init(smem_u32(&s.tfull[i]), 2);  // the products and their scales
+      mbar_init(smem_u32(&s.tempty[i]), EPI);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&s.pair[i]), 2);
+    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&s.meet[i]), 4);
     for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&s.drain[i]), 1);
     s.abort = 0;
     mbar_fence_init();
@@ -274,163 +301,178 @@ __global__ void __launch_bounds__(THREADS, 1)
       tc_commit(smem_u32(&s.drain[w]));
       if (!mbar_wait_drain(smem_u32(&s.drain[w]), 0)) *abort_flag = 1;
     }
+    // ================= scales =================
+    // Warp 3 multiplies the scales of each K block out for the promotion: for
+    // every row of the tile its own times that of each 128 columns.
+    if (warp == 3) {
+      int buf = 0;
+      uint32_t use = 0;
+      bool ok = true;
+      for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+        const Tile t = decode_tile(s_pre, E, args.n_tiles, tile);
+        const float* sa = args.a_scale + static_cast<long long>(s_off[t.e] + t.mt * BM) * k_blocks;
+        const int last = s_cnt[t.e] - 1 - t.mt * BM;  // rows past the group repeat its last one
+        // columns past N read the last block's scale and are not stored
+        const int b0 = MODE == OUT_SWIGLU ? t.nt : min(t.nt * BN >> 7, args.b_scale_rows - 1);
+        const int b1 = MODE == OUT_SWIGLU ? t.nt + (args.N >> 7) : min((t.nt * BN + BN - 1) >> 7, args.b_scale_rows - 1);
+        const float* sb = args.b_scale + static_cast<long long>(t.e) * args.b_scale_rows * k_blocks;
+        float v[4], f0, f1;
+        auto fetch = [&](int kb) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = __ldg(sa + min(lane + 32 * i, last) * k_blocks + kb);
+          f0 = __ldg(sb + b0 * k_blocks + kb);
+          f1 = __ldg(sb + b1 * k_blocks + kb);
+        };
+        fetch(0);
+        for (int kb = 0; kb < k_blocks; ++kb) {
+          const bool ready = mbar_wait(smem_u32(&s.tempty[buf]), use ^ 1u, abort_flag);
+          if (!__all_sync(FULL_MASK, ready)) { ok = false; break; }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            s.scale[buf][0][lane + 32 * i] = v[i] * f0;
+            s.scale[buf][1][lane + 32 * i] = v[i] * f1;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&s.tfull[buf]));
+          if (kb + 1 < k_blocks) fetch(kb + 1);
+          if (++buf == BUFS) { buf = 0; use ^= 1u; }
+        }
+      }
+    }
     __syncwarp();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(MANY_REGS));
     // ================= promotion and epilogue =================
-    // lane quarter q = warp % 4 of tensor memory; column half (warp - 4) / 4.
-    // OUT_SWIGLU: the half's 64 gate columns, then its 64 up columns.
-    const int q = warp & 3, half = (warp - 4) >> 2;
+    // lane quarter q = warp % 4 of tensor memory; columns cq = (warp - 4) / 4 of EPI / 4 parts.
+    // OUT_SWIGLU: 32 gate columns, then their 32 up columns.
+    const int q = warp & 3, cq = (warp - 4) >> 2;
     const int r_in_tile = q * 32 + lane;
-    const uint32_t staging = tiles_u32 + STAGES * S::STAGE_BYTES + (warp - 4) * (S::STAGING_BYTES / EPI_WARPS);
+    const uint32_t staging = tiles_u32 + STAGES * S::STAGE_BYTES + (warp - 4) * (S::STAGING_BYTES / EPI);
+    constexpr int CHUNK = COLS < 32 ? COLS : 32;
+    // SwiGLU: [tile parity][column quarter][row] largest |h| of a row, in the
+    // parts of the staging that codes leave free (1 KiB of each warp's 4 used)
+    auto amax = [&](int par, int quarter) -> float& {
+      return reinterpret_cast<float*>(tiles + STAGES * S::STAGE_BYTES + 2048)[(par * 4 + quarter) * 1024 + r_in_tile];
+    };
     auto column = [&](int c) {  // tensor-memory column of this thread's accumulator c
-      return MODE == OUT_SWIGLU ? (c < 64 ? half * 64 + c : 128 + half * 64 + c - 64) : half * COLS + c;
-    };
-    // This thread's part of a tile: its row, and where its scales are.
-    struct Part {
-      int nt;
-      bool valid;
-      int row0;              // of the warp's 32 rows
-      const float *sa, *sb, *sb_up;
-      float w;
-    };
-    auto part_of = [&](int tile) {
-      const Tile t = decode_tile(s_pre, E, args.n_tiles, tile);
-      Part p;
-      p.nt = t.nt;
-      p.valid = t.mt * BM + r_in_tile < s_cnt[t.e];
-      p.row0 = s_off[t.e] + t.mt * BM + q * 32;
-      const long long row = p.valid ? p.row0 + lane : s_off[t.e];
-      // scale rows of the columns' blocks of 128: a half's columns lie in one
-      // (a half past N reads the last one and stores nothing)
-      const int sb_row = min(MODE == OUT_SWIGLU ? t.nt : (t.nt * BN + half * COLS) >> 7, args.b_scale_rows - 1);
-      p.sa = args.a_scale + row * k_blocks;
-      p.sb = args.b_scale + (static_cast<long long>(t.e) * args.b_scale_rows + sb_row) * k_blocks;
-      p.sb_up = MODE == OUT_SWIGLU ? p.sb + static_cast<long long>(args.N >> 7) * k_blocks : p.sb;
-      p.w = MODE == OUT_WEIGHTED ? __ldg(args.row_weight + row) : 1.0f;
-      return p;
+      return MODE == OUT_SWIGLU ? (c < 32 ? cq * 32 : 128 + cq * 32) : cq * COLS + c;
     };
     int buf = 0;
     uint32_t use = 0, parity = 0;
-    int tile = blockIdx.x;
-    Part part = {}, next = {};
-    float sa_v = 0.f, sb_v = 0.f, su_v = 0.f;  // the next block's scales, one block ahead (also across tiles)
-    if (tile < total) {
-      next = part_of(tile);
-      sa_v = __ldg(next.sa);
-      sb_v = __ldg(next.sb);
-      if (MODE == OUT_SWIGLU) su_v = __ldg(next.sb_up);
-    }
     bool ok = true;
-    for (; tile < total && ok; tile += gridDim.x, parity ^= 1u) {
-      part = next;
+    for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x, parity ^= 1u) {
       float acc[COLS];
 #pragma unroll
       for (int i = 0; i < COLS; ++i) acc[i] = 0.f;
       for (int kb = 0; kb < k_blocks; ++kb) {
-        const float scale = sa_v * sb_v, scale_up = sa_v * su_v;
-        if (kb + 1 < k_blocks) {
-          sa_v = __ldg(part.sa + kb + 1);
-          sb_v = __ldg(part.sb + kb + 1);
-          if (MODE == OUT_SWIGLU) su_v = __ldg(part.sb_up + kb + 1);
-        } else if (tile + static_cast<int>(gridDim.x) < total) {
-          next = part_of(tile + gridDim.x);
-          sa_v = __ldg(next.sa);
-          sb_v = __ldg(next.sb);
-          if (MODE == OUT_SWIGLU) su_v = __ldg(next.sb_up);
-        }
         const bool ready = mbar_wait(smem_u32(&s.tfull[buf]), use, abort_flag);
         if (!__all_sync(FULL_MASK, ready)) { ok = false; break; }
         tc_fence_after();
         const uint32_t tb = tmem_base + buf * BN + (static_cast<uint32_t>(q * 32) << 16);
-        uint32_t p[2][32];
-        tmem_ld32(tb + column(0), p[0]);
+        const float scale = s.scale[buf][MODE == OUT_SWIGLU || BN < 256 ? 0 : (cq * COLS) >> 7][r_in_tile];
+        const float scale_up = MODE == OUT_SWIGLU ? s.scale[buf][1][r_in_tile] : 0.f;
+        // With eight warps the next 32 columns are read while these are added;
+        // with sixteen the other warps fill that time, and registers are short.
+        constexpr int AHEAD = EPI == 8 && COLS > CHUNK ? 1 : 0;
+        uint32_t p[1 + AHEAD][32];
+        if (AHEAD) tmem_ld<CHUNK>(tb + column(0), p[0]);
 #pragma unroll
-        for (int c = 0; c < COLS; c += 32) {  // the next 32 columns are read while these are added
-          uint32_t(&now)[32] = p[(c >> 5) & 1];
+        for (int c = 0; c < COLS; c += CHUNK) {
+          uint32_t(&now)[32] = p[AHEAD ? (c / CHUNK) & 1 : 0];
+          if (!AHEAD) tmem_ld<CHUNK>(tb + column(c), now);
           tmem_ld_wait32(now);
-          if (c + 32 < COLS) {
-            tmem_ld32(tb + column(c + 32), p[((c >> 5) & 1) ^ 1]);
-          } else {  // all of this warp's reads have landed
+          if (c + CHUNK >= COLS) {  // all of this warp's reads have landed
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&s.tempty[buf]));
+          } else if (AHEAD) {
+            tmem_ld<CHUNK>(tb + column(c + CHUNK), p[AHEAD ? ((c / CHUNK) & 1) ^ 1 : 0]);
           }
-          const float f = MODE == OUT_SWIGLU && c >= 64 ? scale_up : scale;
+          const float f = MODE == OUT_SWIGLU && c >= 32 ? scale_up : scale;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) acc[c + i] = fmaf(__uint_as_float(now[i]), f, acc[c + i]);
+          for (int i = 0; i < CHUNK; ++i) acc[c + i] = fmaf(__uint_as_float(now[i]), f, acc[c + i]);
         }
         if (++buf == BUFS) { buf = 0; use ^= 1u; }
       }
       if (!ok) break;
       // Output: a warp whose 32 rows all exist writes them to its staging
-      // boxes (32 rows of 64 bytes, swizzled) and stores those by TMA, which
-      // goes on while the next tile is multiplied; else rows one by one.
-      // Rows past a dense matrix are clipped by the tensor map.
-      const bool staged = args.out_staged && (!args.counts || __all_sync(FULL_MASK, part.valid));
-      const long long row = static_cast<long long>(part.row0) + lane;
+      // boxes (32 rows, of 64 bytes swizzled or of 32 bytes) and stores those
+      // by TMA, which goes on while the next tile is multiplied; else rows one
+      // by one.  Rows past a dense matrix are clipped by the tensor map.
+      const Tile t = decode_tile(s_pre, E, args.n_tiles, tile);
+      const bool valid = t.mt * BM + r_in_tile < s_cnt[t.e];
+      const int row0 = s_off[t.e] + t.mt * BM + q * 32;
+      const bool staged = args.out_staged && (!args.counts || __all_sync(FULL_MASK, valid));
+      const long long row = static_cast<long long>(row0) + lane;
       if (staged) {
         if (lane == 0) tma_store_wait_read<0>();  // the last tile's boxes
         __syncwarp();
       }
-      auto put = [&](int box, const uint32_t (&v)[16], int x) {  // x: column in units of 2 bytes
-        const uint32_t dst = staging + box * 2048;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + staged_chunk(lane, i)), "r"(v[4 * i]),
-                       "r"(v[4 * i + 1]), "r"(v[4 * i + 2]), "r"(v[4 * i + 3])
-                       : "memory");
+      auto put = [&](uint32_t dst, int x) {  // x: column in units of 2 bytes
         fence_async_shared();
         __syncwarp();
         if (lane == 0) {
-          tma_store_2d(&tmOut, dst, x, part.row0);
+          tma_store_2d(&tmOut, dst, x, row0);
           tma_store_commit();
         }
       };
       if constexpr (MODE == OUT_SWIGLU) {
         float top = 0.f;
 #pragma unroll
-        for (int i = 0; i < 64; ++i) {
-          acc[i] = silu_mul(acc[i], acc[64 + i]);
+        for (int i = 0; i < 32; ++i) {
+          acc[i] = silu_mul(acc[i], acc[32 + i]);
           top = max_nan(top, fabsf(acc[i]));
         }
-        // The two warps of a lane quarter exchange their maxima.  One meeting a
+        // The four warps of a lane quarter exchange their maxima.  One meeting a
         // tile is enough: this parity's slots are written again two tiles
-        // on, after the next tile's meeting, which follows both reads here.
-        s.amax[parity][half][r_in_tile] = top;
+        // on, after the next tile's meeting, which follows all reads here.
+        amax(parity, cq) = top;
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&s.pair[q]));
-        const bool met = mbar_wait(smem_u32(&s.pair[q]), parity, abort_flag);
+        if (lane == 0) mbar_arrive(smem_u32(&s.meet[q]));
+        const bool met = mbar_wait(smem_u32(&s.meet[q]), parity, abort_flag);
         if (!__all_sync(FULL_MASK, met)) break;
-        const float scale = block_scale(max_nan(s.amax[parity][0][r_in_tile], s.amax[parity][1][r_in_tile]));
-        const float y = __frcp_rn(scale);
-        uint32_t v[16];
+        const float scale = block_scale(
+            max_nan(max_nan(amax(parity, 0), amax(parity, 1)), max_nan(amax(parity, 2), amax(parity, 3))));
+        const float y = __fdiv_rn(1.0f, scale);
+        uint32_t v[8];
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
+        for (int k = 0; k < 8; ++k)
           v[k] = e4m3x4(y * acc[4 * k], y * acc[4 * k + 1], y * acc[4 * k + 2], y * acc[4 * k + 3]);
         if (staged) {
-          put(0, v, part.nt * 64 + half * 32);
-        } else if (part.valid) {
-          uint4* dst = reinterpret_cast<uint4*>(args.out_q + row * args.N + part.nt * 128 + half * 64);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) dst[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+          for (int i = 0; i < 2; ++i)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(staging + lane * 32 + 16 * i), "r"(v[4 * i]),
+                         "r"(v[4 * i + 1]), "r"(v[4 * i + 2]), "r"(v[4 * i + 3])
+                         : "memory");
+          put(staging, t.nt * 64 + cq * 16);
+        } else if (valid) {
+          uint4* dst = reinterpret_cast<uint4*>(args.out_q + row * args.N + t.nt * 128 + cq * 32);
+          dst[0] = make_uint4(v[0], v[1], v[2], v[3]);
+          dst[1] = make_uint4(v[4], v[5], v[6], v[7]);
         }
-        if (part.valid && half == 0) args.out_scale[row * (args.N >> 7) + part.nt] = scale;
+        if (valid && cq == 0) args.out_scale[row * (args.N >> 7) + t.nt] = scale;
       } else {
-        const int col0 = part.nt * BN + half * COLS;
+        const float w = MODE == OUT_WEIGHTED && valid ? __ldg(args.row_weight + row) : 1.0f;
+        const int col0 = t.nt * BN + cq * COLS;
         const bool whole = (args.N & 7) == 0;  // 16-byte aligned rows
 #pragma unroll
-        for (int c = 0; c < COLS; c += 32) {
+        for (int c = 0; c < COLS; c += CHUNK) {
           if (col0 + c >= args.N) break;
-          uint32_t v[16];
+          uint32_t v[CHUNK / 2];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) v[k] = pack_bf16x2(part.w * acc[c + 2 * k], part.w * acc[c + 2 * k + 1]);
-          if (staged) {
-            put(c >> 5, v, col0 + c);
-          } else if (part.valid) {
+          for (int k = 0; k < CHUNK / 2; ++k) v[k] = pack_bf16x2(w * acc[c + 2 * k], w * acc[c + 2 * k + 1]);
+          if (CHUNK == 32 && staged) {
+            const uint32_t dst = staging + (c >> 5) * 2048;
+#pragma unroll
+            for (int i = 0; i < CHUNK / 8; ++i)
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + staged_chunk(lane, i)), "r"(v[4 * i]),
+                           "r"(v[4 * i + 1]), "r"(v[4 * i + 2]), "r"(v[4 * i + 3])
+                           : "memory");
+            put(dst, col0 + c);
+          } else if (valid) {
             uint16_t* dst = args.out + row * args.N + col0 + c;
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
+            for (int i = 0; i < CHUNK; i += 8) {
               if (whole) {
                 if (col0 + c + i < args.N)
                   *reinterpret_cast<uint4*>(dst + i) = make_uint4(v[i / 2], v[i / 2 + 1], v[i / 2 + 2], v[i / 2 + 3]);
@@ -455,7 +497,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (threadIdx.x == 0 && s.abort) report(args.status, MOE_DEVERR_TIMEOUT);
 }
 
-template <int MODE, int BN>
+template <int MODE, int BN, int EPI>
 cudaError_t launch(const void* a, uint64_t a_rows, const void* b, uint64_t b_rows, const Args& args, int grid,
                    cudaStream_t s) {
   CUtensorMap ma, mb, mo;
@@ -463,16 +505,16 @@ cudaError_t launch(const void* a, uint64_t a_rows, const void* b, uint64_t b_row
     return cudaErrorInvalidValue;
   // codes are stored as pairs of bytes
   const bool staged = args.out_staged;
-  if (staged && !(MODE == OUT_SWIGLU ? make_tma_store_2d_bf16(&mo, args.out_q, a_rows, args.N / 2)
+  if (staged && !(MODE == OUT_SWIGLU ? make_tma_store_2d_bf16_16(&mo, args.out_q, a_rows, args.N / 2)
                                      : make_tma_store_2d_bf16(&mo, args.out, a_rows, args.N)))
     return cudaErrorInvalidValue;
   if (!staged) mo = ma;  // not used
-  auto kernel = block_gemm_kernel<MODE, BN>;
+  auto kernel = block_gemm_kernel<MODE, BN, EPI>;
   static_assert(smem_bytes<BN>(1024) <= SMEM_LIMIT, "fits for every E");
   const cudaError_t err =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_LIMIT);
   if (err != cudaSuccess) return err;
-  return launch_dependent(kernel, grid, THREADS, smem_bytes<BN>(args.E), s, ma, mb, mo, args);
+  return launch_dependent(kernel, grid, Warps<EPI>::THREADS, smem_bytes<BN>(args.E), s, ma, mb, mo, args);
 }
 
 }  // namespace
@@ -496,13 +538,16 @@ cudaError_t launch_block_matmul_tc(const uint8_t* a, const float* a_scale, int M
   const long long mt = (static_cast<long long>(M) + BM - 1) / BM;
   auto tiles = [&](int bn) { return mt * ((N + bn - 1) / bn); };
   const int sms = sm_count();
-  // the widest tile that still gives every SM one
-  const int bn = tiles(256) >= sms ? 256 : tiles(128) >= sms ? 128 : 64;
+  // The tile width with the shortest rounds in all: a K block of 64, 128 or 256
+  // columns takes about 250, 310 and 450 ns.
+  auto cost = [&](int bn, int per_block) { return (tiles(bn) + sms - 1) / sms * per_block; };
+  const long long c64 = cost(64, 25), c128 = cost(128, 31), c256 = cost(256, 45);
+  const int bn = c256 <= c128 && c256 <= c64 ? 256 : c128 <= c64 ? 128 : 64;
   g.n_tiles = (N + bn - 1) / bn;
   const int grid = static_cast<int>(tiles(bn) < sms ? tiles(bn) : sms);
-  if (bn == 256) return launch<OUT_PLAIN, 256>(a, M, b, N, g, grid, s);
-  if (bn == 128) return launch<OUT_PLAIN, 128>(a, M, b, N, g, grid, s);
-  return launch<OUT_PLAIN, 64>(a, M, b, N, g, grid, s);
+  if (bn == 256) return launch<OUT_PLAIN, 256, 8>(a, M, b, N, g, grid, s);
+  if (bn == 128) return launch<OUT_PLAIN, 128, 8>(a, M, b, N, g, grid, s);
+  return launch<OUT_PLAIN, 64, 8>(a, M, b, N, g, grid, s);
 }
 
 cudaError_t launch_block_experts_tc(const uint8_t* x_q, const float* x_scale, const moe_layout& L, int H, int I,
@@ -526,7 +571,7 @@ cudaError_t launch_block_experts_tc(const uint8_t* x_q, const float* x_scale, co
   g.out_staged = 1;
   g.out_scale = h_scale;
   const uint64_t C = static_cast<uint64_t>(L.capacity), E = static_cast<uint64_t>(L.E);
-  cudaError_t err = launch<OUT_SWIGLU, 256>(x_q, C, W1, E * 2 * I, g, sm_count(), s);
+  cudaError_t err = launch<OUT_SWIGLU, 256, 16>(x_q, C, W1, E * 2 * I, g, sm_count(), s);
   if (err != cudaSuccess) return err;
   g.K = I;
   g.k_blocks = I / BKB;
@@ -538,7 +583,7 @@ cudaError_t launch_block_experts_tc(const uint8_t* x_q, const float* x_scale, co
   g.b_scale = W2_scale;
   g.row_weight = L.row_weight;
   g.out = y;
-  return launch<OUT_WEIGHTED, 256>(h_q, C, W2, E * H, g, sm_count(), s);
+  return launch<OUT_WEIGHTED, 256, 16>(h_q, C, W2, E * H, g, sm_count(), s);
 }
 
 }  // namespace moe
