@@ -362,7 +362,7 @@ def moe_grouped_experts_fp8_block(x_disp: torch.Tensor, layout: Layout, W1_q: to
     E, I = layout.E, W1_q.shape[1] // 2
     if out is None:
         out = torch.empty(C, H, dtype=torch.bfloat16, device=dev)
-    ws = torch.empty(_bytes("moe_experts_fp8_block_workspace_bytes", C, layout.T, H, I), dtype=torch.uint8, device=dev)
+    ws = torch.empty(_bytes("moe_experts_fp8_block_workspace_bytes", C, layout.T, E, H, I), dtype=torch.uint8, device=dev)
     _check(N.lib.moe_grouped_experts_fp8_block(
         _need(x_disp, "x_disp", torch.bfloat16, (C, H), dev), layout.ref, H, I,
         _need(W1_q, "W1_q", torch.uint8, (E, 2 * I, H), dev),

@@ -914,13 +914,17 @@ moe_status moe_adamw_step(const moe_adamw* h, const moe_adamw_tensor* tensors, i
 
 namespace {
 
-// The experts' scratch: x's codes and scales, h's, and for few rows the fp32
+// The experts' scratch: x's codes and scales and h's, or for few rows the fp32
 // gate/up rows; each from a 256-byte boundary.
 struct BlockWorkspace {
   size_t x_q, x_scale, h_q, h_scale, gu, total;
 };
 
-BlockWorkspace block_workspace(int64_t C, int32_t T, int32_t H, int32_t I) {
+bool experts_stream(int32_t T, int32_t E, int32_t H, int32_t I) {
+  return block_stream_fits(T, H > I ? H : I, E);
+}
+
+BlockWorkspace block_workspace(int64_t C, bool stream, int32_t H, int32_t I) {
   const size_t c = static_cast<size_t>(C);
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -928,12 +932,15 @@ BlockWorkspace block_workspace(int64_t C, int32_t T, int32_t H, int32_t I) {
     at += (bytes + 255) / 256 * 256;
     return here;
   };
-  BlockWorkspace w;
-  w.x_q = take(c * H);
-  w.x_scale = take(c * ((H + 127) / 128) * sizeof(float));
-  w.h_q = take(c * I);
-  w.h_scale = take(c * ((I + 127) / 128) * sizeof(float));
-  w.gu = take(T <= BLOCK_STREAM_ROWS ? c * 2 * I * sizeof(float) : 0);
+  BlockWorkspace w{};
+  if (stream) {
+    w.gu = take(c * 2 * I * sizeof(float));
+  } else {
+    w.x_q = take(c * H);
+    w.x_scale = take(c * ((H + 127) / 128) * sizeof(float));
+    w.h_q = take(c * I);
+    w.h_scale = take(c * ((I + 127) / 128) * sizeof(float));
+  }
   w.total = at;
   return w;
 }
@@ -984,10 +991,11 @@ moe_status moe_matmul_fp8_block(const uint8_t* a_q, const float* a_scale, int32_
   return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_matmul_fp8_block launch");
 }
 
-moe_status moe_experts_fp8_block_workspace_bytes(int64_t capacity, int32_t T, int32_t H, int32_t I, size_t* bytes) {
+moe_status moe_experts_fp8_block_workspace_bytes(int64_t capacity, int32_t T, int32_t E, int32_t H, int32_t I,
+                                                 size_t* bytes) {
   MOE_REQUIRE(bytes != nullptr, MOE_ERR_INVALID_ARG, "bytes is NULL");
-  MOE_REQUIRE(capacity >= 0 && T >= 0 && H > 0 && I > 0, MOE_ERR_INVALID_ARG, "bad capacity / T / H / I");
-  *bytes = block_workspace(capacity, T, H, I).total;
+  MOE_REQUIRE(capacity >= 0 && T >= 0 && E > 0 && H > 0 && I > 0, MOE_ERR_INVALID_ARG, "bad capacity / T / E / H / I");
+  *bytes = block_workspace(capacity, experts_stream(T, E, H, I), H, I).total;
   return MOE_OK;
 }
 
@@ -1006,19 +1014,21 @@ moe_status moe_grouped_experts_fp8_block(const moe_bf16* x_disp, const moe_layou
               "moe_grouped_experts_fp8_block: pointers must be 16-byte aligned");
   if ((st = check_device()) != MOE_OK) return st;
   if (L->capacity == 0 || L->T == 0) return MOE_OK;
-  const BlockWorkspace w = block_workspace(L->capacity, L->T, H, I);
+  const bool stream_form = experts_stream(L->T, L->E, H, I);
+  const BlockWorkspace w = block_workspace(L->capacity, stream_form, H, I);
   uint8_t* base = static_cast<uint8_t*>(workspace);
-  uint8_t* x_q = base + w.x_q;
-  float* x_scale = reinterpret_cast<float*>(base + w.x_scale);
-  uint8_t* h_q = base + w.h_q;
-  float* h_scale = reinterpret_cast<float*>(base + w.h_scale);
-  cudaError_t err = launch_quantize_block(x_disp, 1, L->capacity, H, 1, x_q, x_scale, L->row_token, stream);
-  if (err == cudaSuccess)
-    err = L->T <= BLOCK_STREAM_ROWS
-              ? launch_block_experts_stream(x_q, x_scale, *L, H, I, W1_q, W1_scale, W2_q, W2_scale,
-                                            reinterpret_cast<float*>(base + w.gu), h_q, h_scale, y_disp, stream)
-              : launch_block_experts_tc(x_q, x_scale, *L, H, I, W1_q, W1_scale, W2_q, W2_scale, h_q, h_scale, y_disp,
-                                        stream);
+  cudaError_t err;
+  if (stream_form) {
+    err = launch_block_experts_stream(x_disp, *L, H, I, W1_q, W1_scale, W2_q, W2_scale,
+                                      reinterpret_cast<float*>(base + w.gu), y_disp, stream);
+  } else {
+    uint8_t* x_q = base + w.x_q;
+    float* x_scale = reinterpret_cast<float*>(base + w.x_scale);
+    err = launch_quantize_block(x_disp, 1, L->capacity, H, 1, x_q, x_scale, L->row_token, stream);
+    if (err == cudaSuccess)
+      err = launch_block_experts_tc(x_q, x_scale, *L, H, I, W1_q, W1_scale, W2_q, W2_scale, base + w.h_q,
+                                    reinterpret_cast<float*>(base + w.h_scale), y_disp, stream);
+  }
   return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_grouped_experts_fp8_block launch");
 }
 

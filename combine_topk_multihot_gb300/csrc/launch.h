@@ -244,14 +244,15 @@ size_t norm_backward_workspace(long long T, int H);
 cudaError_t launch_quantize_block(const uint16_t* src, long long batch, long long rows, int cols, int block_rows,
                                   uint8_t* codes, float* scales, const int* row_token, cudaStream_t s);
 // Products with few rows, as a stream over the weights: at most
-// BLOCK_STREAM_ROWS rows (per expert).  gu: [capacity, 2I] fp32 scratch.
-constexpr int BLOCK_STREAM_ROWS = 32;
+// BLOCK_STREAM_ROWS rows (per expert) whose codes fit in shared memory.  gu:
+// [capacity, 2I] fp32 scratch.
+constexpr int BLOCK_STREAM_ROWS = 8;
+bool block_stream_fits(int rows, int K, int E);
 cudaError_t launch_block_matmul_stream(const uint8_t* a, const float* a_scale, int M, const uint8_t* b,
                                        const float* b_scale, int N, int K, uint16_t* out, cudaStream_t s);
-cudaError_t launch_block_experts_stream(const uint8_t* x_q, const float* x_scale, const moe_layout& L, int H, int I,
-                                        const uint8_t* W1, const float* W1_scale, const uint8_t* W2,
-                                        const float* W2_scale, float* gu, uint8_t* h_q, float* h_scale, uint16_t* y,
-                                        cudaStream_t s);
+cudaError_t launch_block_experts_stream(const uint16_t* x_disp, const moe_layout& L, int H, int I, const uint8_t* W1,
+                                        const float* W1_scale, const uint8_t* W2, const float* W2_scale, float* gu,
+                                        uint16_t* y, cudaStream_t s);
 // The same products on the tensor cores in tiles of 128 rows (fp8_block_gemm.cu).
 cudaError_t launch_block_matmul_tc(const uint8_t* a, const float* a_scale, int M, const uint8_t* b,
                                    const float* b_scale, int N, int K, uint16_t* out, int* status,

@@ -672,7 +672,7 @@ MOE_API moe_status moe_quantize_fp8_block(const moe_bf16* src, int64_t batch, in
  *   b_q [N, K] uint8 and b_scale [ceil(N / 128), ceil(K / 128)] (block_rows
  *   128); out [M, N] bf16 (out); status [1] int32 device status word
  *   (nullable), receives MOE_DEVERR_TIMEOUT.
- * M >= 0, N >= 1, K >= 16 a multiple of 16.  Up to 32 rows stream the
+ * M >= 0, N >= 1, K >= 16 a multiple of 16.  Up to 8 rows stream the
  * weights through registers; more run on the tensor cores in 128-row tiles.
  */
 MOE_API moe_status moe_matmul_fp8_block(const uint8_t* a_q, const float* a_scale, int32_t M,
@@ -689,13 +689,13 @@ MOE_API moe_status moe_matmul_fp8_block(const uint8_t* a_q, const float* a_scale
  *   W1_q [E, 2I, H] uint8, W1_scale [E, 2I/128, H/128], W2_q [E, H, I],
  *   W2_scale [E, H/128, I/128] (moe_quantize_fp8_block, block_rows 128);
  *   y_disp [C, H] bf16 (out): the valid rows are written.
- *   workspace: moe_experts_fp8_block_workspace_bytes(C, T, H, I) bytes of
+ *   workspace: moe_experts_fp8_block_workspace_bytes(C, T, E, H, I) bytes of
  *   device scratch, 16-byte aligned.
  * Inference only.  Shapes and errors as in moe_grouped_experts.  Nothing is
  * read back to the host: the call can be captured.
  */
-MOE_API moe_status moe_experts_fp8_block_workspace_bytes(int64_t capacity, int32_t T, int32_t H, int32_t I,
-                                                         size_t* bytes);
+MOE_API moe_status moe_experts_fp8_block_workspace_bytes(int64_t capacity, int32_t T, int32_t E, int32_t H,
+                                                         int32_t I, size_t* bytes);
 MOE_API moe_status moe_grouped_experts_fp8_block(const moe_bf16* x_disp, const moe_layout* L, int32_t H,
                                                  int32_t I, const uint8_t* W1_q, const float* W1_scale,
                                                  const uint8_t* W2_q, const float* W2_scale,
