@@ -243,6 +243,7 @@ class AdamWState:
             self.master = [p.detach().float() if p.dtype is torch.bfloat16 else None for p in self.params] \
                 if master else None
         self._table = np.zeros(len(self.params), dtype=_TABLE)
+        self._address = self._table.ctypes.data
         self._made_for = [(p.dtype, p.shape) for p in self.params]
         self._settings = None      # what the table's remaining columns were filled from
         for i, (p, row) in enumerate(zip(self.params, self._table)):
@@ -275,16 +276,24 @@ def moe_adamw_step(state: AdamWState, grads: Sequence[Optional[torch.Tensor]], l
     if len(grads) != len(params):
         raise ValueError(f"{len(grads)} gradients for {len(params)} parameters")
     if params:
-        for i, (p, (dtype, shape)) in enumerate(zip(params, state._made_for)):
+        places, addresses, dtypes = [], [], []
+        for p, g, (dtype, shape) in zip(params, grads, state._made_for):
             if p.dtype is not dtype or p.shape != shape or p.device != dev or not p.is_contiguous():
-                raise ValueError(f"params[{i}] is no longer what the state was made for")
-        table["param"] = [p.data_ptr() for p in params]
-        table["grad"] = [0 if g is None else _need(g, f"grads[{i}]", g.dtype, shape, dev) or 0
-                         for i, (g, (_, shape)) in enumerate(zip(grads, state._made_for))]
+                raise ValueError(f"params[{len(places)}] is no longer what the state was made for")
+            places.append(p.data_ptr())
+            if g is None:
+                addresses.append(0)
+                dtypes.append(None)
+                continue
+            if g.shape != shape or g.device != dev or not g.is_contiguous():
+                _need(g, f"grads[{len(addresses)}]", g.dtype, shape, dev)   # says which
+            addresses.append(g.data_ptr())
+            dtypes.append(g.dtype)
+        table["param"], table["grad"] = places, addresses
         # only the addresses change in most steps
         if not isinstance(weight_decay, (int, float)):
             weight_decay = [float(d) for d in weight_decay]
-        settings = ([None if g is None else g.dtype for g in grads], weight_decay)
+        settings = (dtypes, weight_decay)
         if settings != state._settings:
             state._settings = None
             table["grad_dtype"] = [0 if g is None else _either(g, f"grads[{i}]") for i, g in enumerate(grads)]
@@ -295,7 +304,7 @@ def moe_adamw_step(state: AdamWState, grads: Sequence[Optional[torch.Tensor]], l
               for t, name, dtype in ((grad_scale, "grad_scale", torch.float32), (skip, "skip", torch.int32),
                                      (step, "step", torch.int64))]
     h = N.MoeAdamw(lr, beta1, beta2, eps, state.step + 1, state.seed, state.state_bits, *scalar)
-    _check(N.lib.moe_adamw_step(h, table.ctypes.data, len(params), _raw_stream(stream, dev)), "moe_adamw_step")
+    _check(N.lib.moe_adamw_step(h, state._address, len(params), _raw_stream(stream, dev)), "moe_adamw_step")
     if step is None:
         state.step += 1
     if params:
@@ -315,10 +324,10 @@ def moe_quantize_fp8_block(src: torch.Tensor, block_rows: int = 1, out=None, str
     if src.dim() < 2:
         raise ValueError(f"src must be [..., rows, cols] (got {tuple(src.shape)})")
     rows, cols = src.shape[-2:]
-    lead = src.shape[:-2]
-    batch = lead.numel()
     if block_rows not in (1, 128):
         raise ValueError(f"block_rows must be 1 or 128 (got {block_rows})")
+    lead = src.shape[:-2]
+    batch = lead.numel() if lead else 1
     shape = (*lead, -(-rows // block_rows), _blocks(cols))
     if out is None:
         out = (torch.empty(src.shape, dtype=torch.uint8, device=dev), torch.empty(shape, dtype=torch.float32, device=dev))

@@ -164,7 +164,7 @@ struct Step {  // what is the same for all tensors
 // PARAM: 0 fp32, 1 bf16, 2 bf16 with an fp32 master.
 template <int PARAM, bool GRAD_F32, bool EIGHT, bool WIDE>
 __device__ __forceinline__ void update_block(const AdamWTensor& T, const Step& st, long long base, long long block,
-                                             int lane) {
+                                             int lane, uint32_t key) {
   const long long n = T.n;
   float p[2][4], g[2][4], m[2][4], v[2][4];
   uint32_t mq[2], vq[2];
@@ -223,7 +223,8 @@ __device__ __forceinline__ void update_block(const AdamWTensor& T, const Step& s
     const float ms = max_nan(__fdiv_rn(warp_max_nan(m_top), 448.0f), SCALE_FLOOR);
     const float vs = max_nan(__fdiv_rn(warp_max_nan(v_top), 57344.0f), SCALE_FLOOR);
     const float mi = __frcp_rn(ms), vi = __frcp_rn(vs);
-    const uint32_t key = chain(chain(T.key, st.step_lo), st.step_hi);
+    // (a block's elements share the upper half of their number)
+    const uint32_t inner = mix(static_cast<uint32_t>(static_cast<uint64_t>(base) >> 33) ^ key);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const long long i = base + 128 * h + 4 * lane;
@@ -233,8 +234,7 @@ __device__ __forceinline__ void update_block(const AdamWTensor& T, const Step& s
         const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(m[h][k] * mi, m[h][k + 1] * mi), __NV_SATFINITE, __NV_E4M3);
         qm |= two << (8 * k);
         // one hash for two neighbours, 16 random bits each
-        const uint64_t pair = static_cast<uint64_t>(i + k) >> 1;
-        const uint32_t r = mix(static_cast<uint32_t>(pair) ^ mix(static_cast<uint32_t>(pair >> 32) ^ key));
+        const uint32_t r = mix(static_cast<uint32_t>(static_cast<uint64_t>(i + k) >> 1) ^ inner);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           // with its exponent moved by 112, an fp32's bits above the 21st are
@@ -257,20 +257,22 @@ __device__ __forceinline__ void update_block(const AdamWTensor& T, const Step& s
 }
 
 template <bool EIGHT, bool WIDE>
-__device__ __forceinline__ void update_any(const AdamWTensor& T, const Step& st, long long block, int lane) {
+__device__ __forceinline__ void update_any(const AdamWTensor& T, const Step& st, long long block, int lane, uint32_t key) {
   const long long base = block * BLOCK;
   switch (T.kind) {
-    case 0: update_block<0, false, EIGHT, WIDE>(T, st, base, block, lane); break;
-    case 1: update_block<1, false, EIGHT, WIDE>(T, st, base, block, lane); break;
-    case 2: update_block<2, false, EIGHT, WIDE>(T, st, base, block, lane); break;
-    case 3: update_block<0, true, EIGHT, WIDE>(T, st, base, block, lane); break;
-    case 4: update_block<1, true, EIGHT, WIDE>(T, st, base, block, lane); break;
-    case 5: update_block<2, true, EIGHT, WIDE>(T, st, base, block, lane); break;
+    case 0: update_block<0, false, EIGHT, WIDE>(T, st, base, block, lane, key); break;
+    case 1: update_block<1, false, EIGHT, WIDE>(T, st, base, block, lane, key); break;
+    case 2: update_block<2, false, EIGHT, WIDE>(T, st, base, block, lane, key); break;
+    case 3: update_block<0, true, EIGHT, WIDE>(T, st, base, block, lane, key); break;
+    case 4: update_block<1, true, EIGHT, WIDE>(T, st, base, block, lane, key); break;
+    case 5: update_block<2, true, EIGHT, WIDE>(T, st, base, block, lane, key); break;
   }
 }
 
 template <bool EIGHT>
-__global__ void __launch_bounds__(256) adamw_kernel(const __grid_constant__ Table table, const AdamWStep h) {
+// 8-bit states are bound by instructions as much as by HBM: 64 registers, for four
+// CTAs an SM (2^28 elements with masters: 819 -> 782 us).
+__global__ void __launch_bounds__(256, EIGHT ? 4 : 1) adamw_kernel(const __grid_constant__ Table table, const AdamWStep h) {
   __shared__ Step s_step;
   griddep_launch_dependents();
   griddep_wait();
@@ -296,13 +298,18 @@ __global__ void __launch_bounds__(256) adamw_kernel(const __grid_constant__ Tabl
   const Step st = s_step;
   const int lane = threadIdx.x & 31;
   const int warps = gridDim.x * (blockDim.x >> 5);
-  int k = 0;
+  int k = 0, keyed = -1;
+  uint32_t key = 0;
   for (long long b = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); b < table.first[table.count]; b += warps) {
     while (b >= table.first[k + 1]) ++k;
     const AdamWTensor& T = table.t[k];
     const long long block = b - table.first[k];
-    if (T.wide && (block + 1) * BLOCK <= T.n) update_any<EIGHT, true>(T, st, block, lane);
-    else update_any<EIGHT, false>(T, st, block, lane);
+    if (k != keyed) {
+      key = chain(chain(T.key, st.step_lo), st.step_hi);
+      keyed = k;
+    }
+    if (T.wide && (block + 1) * BLOCK <= T.n) update_any<EIGHT, true>(T, st, block, lane, key);
+    else update_any<EIGHT, false>(T, st, block, lane, key);
   }
 }
 
@@ -325,7 +332,7 @@ cudaError_t launch_adamw(const AdamWTensor* tensors, int count, const AdamWStep&
     }
     table.first[table.count] = static_cast<int>(blocks);
     if (blocks == 0) continue;
-    const long long need = (blocks + 7) / 8, most = 6LL * sm_count();
+    const long long need = (blocks + 7) / 8, most = (eight ? 8LL : 6LL) * sm_count();
     const cudaError_t err = launch_dependent(eight ? adamw_kernel<true> : adamw_kernel<false>,
                                              static_cast<unsigned>(need < most ? need : most), 256, 0, s, table, h);
     if (err != cudaSuccess) return err;
