@@ -11,14 +11,20 @@
 // registers.  That promotion is what the kernel is built around:
 //   * warp 0 stages operands by TMA (128-byte swizzle, one K block of 128
 //     codes per stage), warps 1 and 2 issue four tcgen05.mma of K = 32 per
-//     block into one of the accumulators in tensor memory (2 of 256 columns, or 4
-//     narrower ones), warps 4..11 read it back, free it and add it to their
-//     registers while the next blocks are multiplied;
-//   * with 256 columns a block takes the MMAs about 540 cycles and the
-//     promotion about 260 issue slots of each quarter of the SM plus as many
-//     cycles of tensor-memory reads, so it hides behind the MMAs;
-//   * a lane of a promoting warp owns a row of C: sa is one number per lane
-//     and block, sb one per warp.
+//     block into one of the accumulators in tensor memory (two of 256
+//     columns, or four narrower ones), warps 4..11 read it back, free it and
+//     add it to their registers while the next blocks are multiplied;
+//   * a lane of a promoting warp owns a row of C; warp 3 multiplies each
+//     block's scales out for it, one number per row and 128 columns.
+//
+// What bounds it, at 8192 x 8192 x 4096 (216 us, 2.5 PFLOP/s): the MMAs alone
+// run at 4.4 PFLOP/s (547 cycles a block of 128 x 256 x 128); with operands
+// arriving and accumulators handed over, but not read, 183 us; the rest is the
+// accumulators' reading.  A block's products can be replaced only when all
+// eight warps have read theirs, and two blocks fill tensor memory.  Tried
+// without gain: CTA pairs with half of B each (224 us), halves of 128 columns
+// with an accumulator pair each (250), packed fused multiply-adds (240), longer
+// and shorter pieces, reading into the next block.
 //
 // Three epilogues: bf16 of C; bf16 of w_row C (the experts' down product);
 // and SwiGLU with requantisation (the experts' gate/up product): the tile
@@ -46,23 +52,18 @@ constexpr int SMEM_LIMIT = 232448;
 
 enum Mode { OUT_PLAIN = 0, OUT_WEIGHTED = 1, OUT_SWIGLU = 2 };
 
-// Warps 0..3 are the producer, the issuers and the scales; EPI more warps (8 or
-// 16) promote, two or four for each quarter of the tile's columns.  A promoting
-// thread holds 128 or 64 accumulators, more registers than an even share: the
-// first warpgroup passes some of its own on.
-//   8 warps:  384 x 168 = 128 x 56 + 256 x 224
-//   16 warps: 640 x  96 = 128 x 64 + 512 x 104
-// Sixteen hide the epilogue better, which short contractions need (the
-// experts, K = 2048 and 768, T = 4096: 297 against 330 us), eight have less to
-// meet about in each block (8192 x 8192 x 4096: 225 against 247 us).
-template <int EPI>
-struct Warps {
-  static constexpr int THREADS = 32 * (4 + EPI);
-  static constexpr int LAUNCH_REGS = EPI == 8 ? 168 : 96, FEW_REGS = EPI == 8 ? 56 : 64, MANY_REGS = EPI == 8 ? 224 : 104;
-  static_assert(128 * FEW_REGS + 32 * EPI * MANY_REGS <= THREADS * LAUNCH_REGS, "registers are only passed on");
-};
+// Warps 0..3 are the producer, the issuers and the scales; eight more promote,
+// two for each lane quarter of tensor memory, half of the tile's columns each.
+// Such a thread holds up to 128 accumulators, more registers than an even
+// share: the first warpgroup passes some of its own on.  (Sixteen promoting
+// warps of 64 accumulators took longer to meet in each block: 247 against 216 us
+// at 8192 x 8192 x 4096.)
+constexpr int EPI_WARPS = 8;
+constexpr int THREADS = 32 * (4 + EPI_WARPS);
+constexpr int LAUNCH_REGS = 168, FEW_REGS = 56, MANY_REGS = 224;
+static_assert(128 * FEW_REGS + 32 * EPI_WARPS * MANY_REGS <= THREADS * LAUNCH_REGS, "registers are only passed on");
 
-template <int BN, int EPI>
+template <int BN>
 struct Shape {
   static constexpr int A_BYTES = BM * BKB;
   static constexpr int B_BYTES = BN * BKB;
@@ -72,7 +73,7 @@ struct Shape {
   static constexpr int STAGING_BYTES = BM * BN * 2;
   static constexpr int BUFS = BN == 256 ? 2 : 4;
   static constexpr int TMEM_COLS = BN * BUFS;
-  static constexpr int COLS = BN / (EPI / 4);  // accumulators of a promoting thread
+  static constexpr int COLS = BN / 2;  // accumulators of a promoting thread
 };
 
 struct Smem {
@@ -81,7 +82,7 @@ struct Smem {
   uint64_t tfull[MAX_BUFS];
   uint64_t tempty[MAX_BUFS];
   uint64_t drain[2];
-  uint64_t meet[4];   // SwiGLU: the four warps of a lane quarter, once a tile
+  uint64_t meet[4];   // SwiGLU: the two warps of a lane quarter, once a tile
   uint32_t tmem_base;
   int abort;
   int total_tiles;
@@ -90,7 +91,7 @@ struct Smem {
 
 template <int BN>
 constexpr size_t smem_bytes(int E) {
-  using S = Shape<BN, 8>;
+  using S = Shape<BN>;
   return 1024 + static_cast<size_t>(S::STAGES) * S::STAGE_BYTES + S::STAGING_BYTES + sizeof(Smem) + static_cast<size_t>(3 * E + 2) * sizeof(int);
 }
 
@@ -143,30 +144,12 @@ __device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
                  "+r"(r[30]), "+r"(r[31])::"memory");
 }
 
-template <int N>
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) {
-  static_assert(N == 16 || N == 32, "columns");
-  if constexpr (N == 32) {
-    tmem_ld32(taddr, r);
-  } else {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-#pragma unroll
-    for (int i = 16; i < 32; ++i) r[i] = 0;
-  }
-}
-
-template <int MODE, int BN, int EPI>
-__global__ void __launch_bounds__(Warps<EPI>::THREADS, 1)
+template <int MODE, int BN>
+__global__ void __launch_bounds__(THREADS, 1)
     block_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ CUtensorMap tmOut, const Args args) {
-  using S = Shape<BN, EPI>;
-  constexpr int FEW_REGS = Warps<EPI>::FEW_REGS, MANY_REGS = Warps<EPI>::MANY_REGS;
-  static_assert(MODE != OUT_SWIGLU || (BN == 256 && EPI == 16), "a tile of h is one scale block wide, 32 columns a warp");
+  using S = Shape<BN>;
+  static_assert(MODE != OUT_SWIGLU || BN == 256, "a tile of h is one scale block wide, 64 columns a warp");
   constexpr int STAGES = S::STAGES, BUFS = S::BUFS, COLS = S::COLS;
   constexpr uint32_t IDESC = idesc_e4m3_f32(BM, BN);
   extern __shared__ uint8_t smem_raw[];
@@ -188,9 +171,9 @@ __global__ void __launch_bounds__(Warps<EPI>::THREADS, 1)
     }
     for (int i = 0; i < BUFS; ++i) {
       mbar_init(smem_u32(&s.tfull[i]), 2);  // the products and their scales
-      mbar_init(smem_u32(&s.tempty[i]), EPI);
+      mbar_init(smem_u32(&s.tempty[i]), EPI_WARPS);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&s.meet[i]), 4);
+    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&s.meet[i]), 2);
     for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&s.drain[i]), 1);
     s.abort = 0;
     mbar_fence_init();
@@ -343,19 +326,18 @@ __global__ void __launch_bounds__(Warps<EPI>::THREADS, 1)
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(MANY_REGS));
     // ================= promotion and epilogue =================
-    // lane quarter q = warp % 4 of tensor memory; columns cq = (warp - 4) / 4 of EPI / 4 parts.
-    // OUT_SWIGLU: 32 gate columns, then their 32 up columns.
-    const int q = warp & 3, cq = (warp - 4) >> 2;
+    // lane quarter q = warp % 4 of tensor memory; column half = (warp - 4) / 4.
+    // OUT_SWIGLU: 64 gate columns, then their 64 up columns.
+    const int q = warp & 3, half = (warp - 4) >> 2;
     const int r_in_tile = q * 32 + lane;
-    const uint32_t staging = tiles_u32 + STAGES * S::STAGE_BYTES + (warp - 4) * (S::STAGING_BYTES / EPI);
-    constexpr int CHUNK = COLS < 32 ? COLS : 32;
-    // SwiGLU: [tile parity][column quarter][row] largest |h| of a row, in the
-    // parts of the staging that codes leave free (1 KiB of each warp's 4 used)
-    auto amax = [&](int par, int quarter) -> float& {
-      return reinterpret_cast<float*>(tiles + STAGES * S::STAGE_BYTES + 2048)[(par * 4 + quarter) * 1024 + r_in_tile];
+    const uint32_t staging = tiles_u32 + STAGES * S::STAGE_BYTES + (warp - 4) * (S::STAGING_BYTES / EPI_WARPS);
+    // SwiGLU: [tile parity][column half][row] largest |h| of a row, in parts of
+    // the staging that codes leave free (they take 2 KiB of each warp's 8)
+    auto amax = [&](int par, int part) -> float& {
+      return reinterpret_cast<float*>(tiles + STAGES * S::STAGE_BYTES + 4096)[(par * 2 + part) * 2048 + r_in_tile];
     };
     auto column = [&](int c) {  // tensor-memory column of this thread's accumulator c
-      return MODE == OUT_SWIGLU ? (c < 32 ? cq * 32 : 128 + cq * 32) : cq * COLS + c;
+      return MODE == OUT_SWIGLU ? (c < 64 ? half * 64 + c : 128 + half * 64 + c - 64) : half * COLS + c;
     };
     int buf = 0;
     uint32_t use = 0, parity = 0;
@@ -369,28 +351,25 @@ __global__ void __launch_bounds__(Warps<EPI>::THREADS, 1)
         if (!__all_sync(FULL_MASK, ready)) { ok = false; break; }
         tc_fence_after();
         const uint32_t tb = tmem_base + buf * BN + (static_cast<uint32_t>(q * 32) << 16);
-        const float scale = s.scale[buf][MODE == OUT_SWIGLU || BN < 256 ? 0 : (cq * COLS) >> 7][r_in_tile];
+        const float scale = s.scale[buf][MODE == OUT_SWIGLU || BN < 256 ? 0 : (half * COLS) >> 7][r_in_tile];
         const float scale_up = MODE == OUT_SWIGLU ? s.scale[buf][1][r_in_tile] : 0.f;
-        // With eight warps the next 32 columns are read while these are added;
-        // with sixteen the other warps fill that time, and registers are short.
-        constexpr int AHEAD = EPI == 8 && COLS > CHUNK ? 1 : 0;
-        uint32_t p[1 + AHEAD][32];
-        if (AHEAD) tmem_ld<CHUNK>(tb + column(0), p[0]);
+        // the next 32 columns are read while these are added
+        uint32_t p[COLS > 32 ? 2 : 1][32];
+        tmem_ld32(tb + column(0), p[0]);
 #pragma unroll
-        for (int c = 0; c < COLS; c += CHUNK) {
-          uint32_t(&now)[32] = p[AHEAD ? (c / CHUNK) & 1 : 0];
-          if (!AHEAD) tmem_ld<CHUNK>(tb + column(c), now);
+        for (int c = 0; c < COLS; c += 32) {
+          uint32_t(&now)[32] = p[COLS > 32 ? (c >> 5) & 1 : 0];
           tmem_ld_wait32(now);
-          if (c + CHUNK >= COLS) {  // all of this warp's reads have landed
+          if (c + 32 < COLS) {
+            tmem_ld32(tb + column(c + 32), p[COLS > 32 ? ((c >> 5) & 1) ^ 1 : 0]);
+          } else {  // all of this warp's reads have landed
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&s.tempty[buf]));
-          } else if (AHEAD) {
-            tmem_ld<CHUNK>(tb + column(c + CHUNK), p[AHEAD ? ((c / CHUNK) & 1) ^ 1 : 0]);
           }
-          const float f = MODE == OUT_SWIGLU && c >= 32 ? scale_up : scale;
+          const float f = MODE == OUT_SWIGLU && c >= 64 ? scale_up : scale;
 #pragma unroll
-          for (int i = 0; i < CHUNK; ++i) acc[c + i] = fmaf(__uint_as_float(now[i]), f, acc[c + i]);
+          for (int i = 0; i < 32; ++i) acc[c + i] = fmaf(__uint_as_float(now[i]), f, acc[c + i]);
         }
         if (++buf == BUFS) { buf = 0; use ^= 1u; }
       }
@@ -419,52 +398,51 @@ __global__ void __launch_bounds__(Warps<EPI>::THREADS, 1)
       if constexpr (MODE == OUT_SWIGLU) {
         float top = 0.f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          acc[i] = silu_mul(acc[i], acc[32 + i]);
+        for (int i = 0; i < 64; ++i) {
+          acc[i] = silu_mul(acc[i], acc[64 + i]);
           top = max_nan(top, fabsf(acc[i]));
         }
-        // The four warps of a lane quarter exchange their maxima.  One meeting a
+        // The two warps of a lane quarter exchange their maxima.  One meeting a
         // tile is enough: this parity's slots are written again two tiles
-        // on, after the next tile's meeting, which follows all reads here.
-        amax(parity, cq) = top;
+        // on, after the next tile's meeting, which follows both reads here.
+        amax(parity, half) = top;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&s.meet[q]));
         const bool met = mbar_wait(smem_u32(&s.meet[q]), parity, abort_flag);
         if (!__all_sync(FULL_MASK, met)) break;
-        const float scale = block_scale(
-            max_nan(max_nan(amax(parity, 0), amax(parity, 1)), max_nan(amax(parity, 2), amax(parity, 3))));
+        const float scale = block_scale(max_nan(amax(parity, 0), amax(parity, 1)));
         const float y = __fdiv_rn(1.0f, scale);
-        uint32_t v[8];
+        uint32_t v[16];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+        for (int k = 0; k < 16; ++k)
           v[k] = e4m3x4(y * acc[4 * k], y * acc[4 * k + 1], y * acc[4 * k + 2], y * acc[4 * k + 3]);
         if (staged) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(staging + lane * 32 + 16 * i), "r"(v[4 * i]),
+          for (int i = 0; i < 4; ++i)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(staging + staged_chunk(lane, i)), "r"(v[4 * i]),
                          "r"(v[4 * i + 1]), "r"(v[4 * i + 2]), "r"(v[4 * i + 3])
                          : "memory");
-          put(staging, t.nt * 64 + cq * 16);
+          put(staging, t.nt * 64 + half * 32);
         } else if (valid) {
-          uint4* dst = reinterpret_cast<uint4*>(args.out_q + row * args.N + t.nt * 128 + cq * 32);
-          dst[0] = make_uint4(v[0], v[1], v[2], v[3]);
-          dst[1] = make_uint4(v[4], v[5], v[6], v[7]);
+          uint4* dst = reinterpret_cast<uint4*>(args.out_q + row * args.N + t.nt * 128 + half * 64);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) dst[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
         }
-        if (valid && cq == 0) args.out_scale[row * (args.N >> 7) + t.nt] = scale;
+        if (valid && half == 0) args.out_scale[row * (args.N >> 7) + t.nt] = scale;
       } else {
         const float w = MODE == OUT_WEIGHTED && valid ? __ldg(args.row_weight + row) : 1.0f;
-        const int col0 = t.nt * BN + cq * COLS;
+        const int col0 = t.nt * BN + half * COLS;
         const bool whole = (args.N & 7) == 0;  // 16-byte aligned rows
 #pragma unroll
-        for (int c = 0; c < COLS; c += CHUNK) {
+        for (int c = 0; c < COLS; c += 32) {
           if (col0 + c >= args.N) break;
-          uint32_t v[CHUNK / 2];
+          uint32_t v[32 / 2];
 #pragma unroll
-          for (int k = 0; k < CHUNK / 2; ++k) v[k] = pack_bf16x2(w * acc[c + 2 * k], w * acc[c + 2 * k + 1]);
-          if (CHUNK == 32 && staged) {
+          for (int k = 0; k < 32 / 2; ++k) v[k] = pack_bf16x2(w * acc[c + 2 * k], w * acc[c + 2 * k + 1]);
+          if (staged) {
             const uint32_t dst = staging + (c >> 5) * 2048;
 #pragma unroll
-            for (int i = 0; i < CHUNK / 8; ++i)
+            for (int i = 0; i < 32 / 8; ++i)
               asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + staged_chunk(lane, i)), "r"(v[4 * i]),
                            "r"(v[4 * i + 1]), "r"(v[4 * i + 2]), "r"(v[4 * i + 3])
                            : "memory");
@@ -472,7 +450,7 @@ __global__ void __launch_bounds__(Warps<EPI>::THREADS, 1)
           } else if (valid) {
             uint16_t* dst = args.out + row * args.N + col0 + c;
 #pragma unroll
-            for (int i = 0; i < CHUNK; i += 8) {
+            for (int i = 0; i < 32; i += 8) {
               if (whole) {
                 if (col0 + c + i < args.N)
                   *reinterpret_cast<uint4*>(dst + i) = make_uint4(v[i / 2], v[i / 2 + 1], v[i / 2 + 2], v[i / 2 + 3]);
@@ -497,7 +475,7 @@ __global__ void __launch_bounds__(Warps<EPI>::THREADS, 1)
   if (threadIdx.x == 0 && s.abort) report(args.status, MOE_DEVERR_TIMEOUT);
 }
 
-template <int MODE, int BN, int EPI>
+template <int MODE, int BN>
 cudaError_t launch(const void* a, uint64_t a_rows, const void* b, uint64_t b_rows, const Args& args, int grid,
                    cudaStream_t s) {
   CUtensorMap ma, mb, mo;
@@ -505,16 +483,16 @@ cudaError_t launch(const void* a, uint64_t a_rows, const void* b, uint64_t b_row
     return cudaErrorInvalidValue;
   // codes are stored as pairs of bytes
   const bool staged = args.out_staged;
-  if (staged && !(MODE == OUT_SWIGLU ? make_tma_store_2d_bf16_16(&mo, args.out_q, a_rows, args.N / 2)
+  if (staged && !(MODE == OUT_SWIGLU ? make_tma_store_2d_bf16(&mo, args.out_q, a_rows, args.N / 2)
                                      : make_tma_store_2d_bf16(&mo, args.out, a_rows, args.N)))
     return cudaErrorInvalidValue;
   if (!staged) mo = ma;  // not used
-  auto kernel = block_gemm_kernel<MODE, BN, EPI>;
+  auto kernel = block_gemm_kernel<MODE, BN>;
   static_assert(smem_bytes<BN>(1024) <= SMEM_LIMIT, "fits for every E");
   const cudaError_t err =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_LIMIT);
   if (err != cudaSuccess) return err;
-  return launch_dependent(kernel, grid, Warps<EPI>::THREADS, smem_bytes<BN>(args.E), s, ma, mb, mo, args);
+  return launch_dependent(kernel, grid, THREADS, smem_bytes<BN>(args.E), s, ma, mb, mo, args);
 }
 
 }  // namespace
@@ -545,9 +523,9 @@ cudaError_t launch_block_matmul_tc(const uint8_t* a, const float* a_scale, int M
   const int bn = c256 <= c128 && c256 <= c64 ? 256 : c128 <= c64 ? 128 : 64;
   g.n_tiles = (N + bn - 1) / bn;
   const int grid = static_cast<int>(tiles(bn) < sms ? tiles(bn) : sms);
-  if (bn == 256) return launch<OUT_PLAIN, 256, 8>(a, M, b, N, g, grid, s);
-  if (bn == 128) return launch<OUT_PLAIN, 128, 8>(a, M, b, N, g, grid, s);
-  return launch<OUT_PLAIN, 64, 8>(a, M, b, N, g, grid, s);
+  if (bn == 256) return launch<OUT_PLAIN, 256>(a, M, b, N, g, grid, s);
+  if (bn == 128) return launch<OUT_PLAIN, 128>(a, M, b, N, g, grid, s);
+  return launch<OUT_PLAIN, 64>(a, M, b, N, g, grid, s);
 }
 
 cudaError_t launch_block_experts_tc(const uint8_t* x_q, const float* x_scale, const moe_layout& L, int H, int I,
@@ -571,7 +549,7 @@ cudaError_t launch_block_experts_tc(const uint8_t* x_q, const float* x_scale, co
   g.out_staged = 1;
   g.out_scale = h_scale;
   const uint64_t C = static_cast<uint64_t>(L.capacity), E = static_cast<uint64_t>(L.E);
-  cudaError_t err = launch<OUT_SWIGLU, 256, 16>(x_q, C, W1, E * 2 * I, g, sm_count(), s);
+  cudaError_t err = launch<OUT_SWIGLU, 256>(x_q, C, W1, E * 2 * I, g, sm_count(), s);
   if (err != cudaSuccess) return err;
   g.K = I;
   g.k_blocks = I / BKB;
@@ -583,7 +561,7 @@ cudaError_t launch_block_experts_tc(const uint8_t* x_q, const float* x_scale, co
   g.b_scale = W2_scale;
   g.row_weight = L.row_weight;
   g.out = y;
-  return launch<OUT_WEIGHTED, 256, 16>(h_q, C, W2, E * H, g, sm_count(), s);
+  return launch<OUT_WEIGHTED, 256>(h_q, C, W2, E * H, g, sm_count(), s);
 }
 
 }  // namespace moe
