@@ -38,6 +38,15 @@ def _raw_stream(stream, device):
     return _current_raw_stream(device.index) if stream is None else stream.cuda_stream
 
 
+def _used_on(stream, *made: Optional[torch.Tensor]):
+    """Buffers made here for a call on a stream other than the current one:
+    their memory is not given out again before that stream is done with it."""
+    if stream is not None:
+        for t in made:
+            if t is not None and t.numel():
+                t.record_stream(stream)
+
+
 def _need(t: torch.Tensor, name: str, dtype, shape, device):
     """The address of a tensor that has to be as given (None for one without elements)."""
     if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
@@ -106,6 +115,7 @@ def moe_norm_in(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, weight
     _check(N.lib.moe_norm_in(n, _need(x, "x", x.dtype, (T, H), dev), _need(weight, "weight", weight.dtype, (H,), dev),
                              _need(out, "out", torch.bfloat16, (T, H), dev), rstd.data_ptr() or None if save_rstd else None,
                              _raw_stream(stream, dev)), "moe_norm_in")
+    _used_on(stream, out, rstd)
     return out, rstd
 
 
@@ -125,6 +135,7 @@ def moe_norm_in_backward(grad_norm: torch.Tensor, x: torch.Tensor, weight: torch
         None if grad_res is None else _need(grad_res, "grad_res", x.dtype, (T, H), dev),
         grad_x.data_ptr() or None, grad_w.data_ptr(), ws.data_ptr() or None, _raw_stream(stream, dev)),
         "moe_norm_in_backward")
+    _used_on(stream, grad_x, grad_w, ws)
     return grad_x, grad_w
 
 
@@ -150,6 +161,7 @@ def moe_norm_out(x: torch.Tensor, y: torch.Tensor, weight: torch.Tensor, gate: O
         _need(next_weight, "next_weight", weight.dtype, (H,), dev) if has_next else None,
         nxt.data_ptr() or None if has_next else None,
         next_rstd.data_ptr() or None if next_rstd is not None else None, _raw_stream(stream, dev)), "moe_norm_out")
+    _used_on(stream, out, rstd, nxt, next_rstd)
     return out, rstd, nxt, next_rstd
 
 
@@ -189,6 +201,7 @@ def moe_norm_out_backward(grad_out: Optional[torch.Tensor], y: torch.Tensor, wei
         grad_x.data_ptr() or None, grad_y.data_ptr() or None, None if gate is None else grad_gate.data_ptr() or None,
         grad_w.data_ptr(), grad_w2.data_ptr() if has_next else None, ws.data_ptr() or None, _raw_stream(stream, dev)),
         "moe_norm_out_backward")
+    _used_on(stream, grad_x, grad_y, grad_gate, grad_w, grad_w2, ws)
     return grad_x, grad_y, grad_gate, grad_w, grad_w2
 
 
@@ -336,6 +349,7 @@ def moe_quantize_fp8_block(src: torch.Tensor, block_rows: int = 1, out=None, str
                                         _need(codes, "codes", torch.uint8, src.shape, dev),
                                         _need(scales, "scales", torch.float32, shape, dev), _raw_stream(stream, dev)),
            "moe_quantize_fp8_block")
+    _used_on(stream, codes, scales)
     return codes, scales
 
 
@@ -356,6 +370,7 @@ def moe_matmul_fp8_block(a_q: torch.Tensor, a_scale: torch.Tensor, b_q: torch.Te
                                       _need(out, "out", torch.bfloat16, (M, n), dev),
                                       None if status is None else _need(status, "status", torch.int32, (1,), dev),
                                       _raw_stream(stream, dev)), "moe_matmul_fp8_block")
+    _used_on(stream, out)
     return out
 
 
@@ -380,4 +395,5 @@ def moe_grouped_experts_fp8_block(x_disp: torch.Tensor, layout: Layout, W1_q: to
         _need(W2_scale, "W2_scale", torch.float32, (E, _blocks(H), _blocks(I)), dev),
         _need(out, "out", torch.bfloat16, (C, H), dev), ws.data_ptr() or None, _raw_stream(stream, dev)),
         "moe_grouped_experts_fp8_block")
+    _used_on(stream, out, ws)
     return out

@@ -409,7 +409,7 @@ cudaError_t launch_quantize_block(const uint16_t* src, long long batch, long lon
     const long long all = batch * rows;
     const int y = (cols + PIECES * 256 - 1) / (PIECES * 256);
     // a CTA per 8 rows and 1024 columns: the SMs overlap one CTA's loads with
-    // another's arithmetic (looping CTAs, 8 per SM: 4.0 against REPLACE TB/s)
+    // another's arithmetic (32768 x 2048: 4.8 TB/s; looping CTAs, 8 an SM, 4.0)
     const long long need = (all + 7) / 8, most = 1 << 20;
     const dim3 grid(static_cast<unsigned>(need < most ? need : most), y);
     return launch_dependent(quantize_row_blocks_kernel, grid, 256, 0, s, src, all, cols, codes, scales, row_token);

@@ -211,6 +211,28 @@ def test_repeats_and_other_stream(moe):
             assert (a is None and b is None) or torch.equal(a, b)
 
 
+def test_scratch_of_another_stream_is_not_given_out(moe):
+    """A call on a busy side stream, then allocations on the current one that
+    would get its scratch: they must not disturb it."""
+    g = torch.Generator().manual_seed(7)
+    T, H = 2000, 2048
+    y, d, w = _randn(g, T, H, dtype=BF16), _randn(g, T, H, dtype=BF16), _randn(g, H)
+    rstd = torch.rand(T, generator=g).to(DEV)
+    first = moe.moe_norm_out_backward(d, y, w, rstd)
+    torch.cuda.synchronize()
+    side, a = torch.cuda.Stream(), torch.randn(4096, 4096, device=DEV)
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            for _ in range(8):
+                a = torch.tanh(a @ a)          # keeps the side stream busy for a while
+        again = moe.moe_norm_out_backward(d, y, w, rstd, stream=side)
+        for n in (1 << 20, 1 << 21, 1 << 22, 1 << 23):
+            torch.empty(n, device=DEV).fill_(float("nan"))
+        side.synchronize()
+        assert torch.equal(first[3], again[3]) and torch.equal(first[1], again[1])
+
+
 def test_captured(moe):
     """A captured call reads its inputs anew at each replay."""
     g = torch.Generator().manual_seed(3)
