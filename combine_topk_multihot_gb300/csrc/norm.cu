@@ -92,7 +92,15 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : PIPE ? 256 : 512, PIPE ? 2 : 
         if constexpr (ELEM)
           if (!a.gate_f32) gates[j] = read_slot<false>(slot + bytes[0] + bytes[1], col(j), H);
       }
-      if (!group_all(here, row_threads, group)) break;  // (also: every read of the slot is done)
+      if (!group_all(here, row_threads, group)) {  // (also: every read of the slot is done)
+        pipe_drain(pipe, t, stride, a.T);
+#pragma unroll 1
+        for (; t < a.T; t += stride) {
+          if constexpr (HAS_Y) spoil_row<XF32>(a.out, t, H, in_row, row_threads);
+          if constexpr (HAS_NEXT) spoil_row<false>(a.next, t, H, in_row, row_threads);
+        }
+        break;
+      }
       if (in_row == 0 && t + SLOTS * stride < a.T) issue(t + SLOTS * stride, pipe.at);
       pipe.next();
     } else {

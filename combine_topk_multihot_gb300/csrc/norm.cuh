@@ -291,6 +291,26 @@ __device__ __forceinline__ bool group_all(bool ok, int threads, int group) {
   return r != 0;
 }
 
+// Before a group leaves early: its copies in flight, from the current slot on
+// (a bounded wait as well), since they write to this CTA's shared memory.
+template <int SLOTS>
+__device__ __forceinline__ void pipe_drain(RowPipe<SLOTS> pipe, long long t, long long stride, long long T) {
+#pragma unroll 1
+  for (int i = 0; i < SLOTS && t + i * stride < T; ++i, pipe.next()) mbar_wait_drain(pipe.bar(), pipe.phase);
+}
+
+// A group whose wait for a row ran out leaves NaN in the rows that it does not
+// reach, so that the call cannot pass for a finished one.
+template <bool F32>
+__device__ __forceinline__ void spoil_row(void* base, long long row, int H, int in_row, int row_threads) {
+  if (!base) return;
+#pragma unroll 1
+  for (int c = in_row; c < H; c += row_threads) {
+    if constexpr (F32) static_cast<uint32_t*>(base)[row * H + c] = 0x7fc00000u;
+    else static_cast<uint16_t*>(base)[row * H + c] = 0x7fc0u;
+  }
+}
+
 inline int vectors(int H) { return (H + 7) / 8; }
 inline int threads_of(int H, int nv) { return ((vectors(H) + nv - 1) / nv + 31) / 32 * 32; }
 

@@ -110,7 +110,18 @@ __global__ void __launch_bounds__(512, 1)
         if constexpr (ELEM)
           if (!a.gate_f32) gates[j] = read_slot<false>(slot + bytes[0] + bytes[1] + bytes[2] + bytes[3], col(j), H);
       }
-      if (!group_all(here, row_threads, group)) break;  // (also: every read of the slot is done)
+      if (!group_all(here, row_threads, group)) {  // (also: every read of the slot is done)
+        pipe_drain(pipe, t, stride, a.T);
+#pragma unroll 1
+        for (; t < a.T; t += stride) {
+          spoil_row<XF32>(a.dx, t, H, in_row, row_threads);
+          if constexpr (HAS_Y) spoil_row<false>(a.dy, t, H, in_row, row_threads);
+        }
+        const float nan = __uint_as_float(0x7fc00000u);
+#pragma unroll 1
+        for (int k = 0; k < ACC * NV * 2; ++k) acc[k * blockDim.x + threadIdx.x] = make_float4(nan, nan, nan, nan);
+        break;
+      }
       if (in_row == 0 && t + SLOTS * stride < a.T) issue(t + SLOTS * stride, pipe.at);
       pipe.next();
     }

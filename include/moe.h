@@ -542,7 +542,9 @@ typedef struct moe_norm {
  * r_t = 1 / sqrt(mean(x[t]^2) + eps), in fp32 throughout.
  *   x [T, H] bf16 or fp32; weight [H]; norm [T, H] bf16 (out);
  *   rstd [T] fp32 (out, nullable): r_t, for the backward.
- * Outputs must not overlap inputs, here and in the three calls below.  Errors:
+ * Outputs must not overlap inputs, here and in the three calls below.  If a
+ * bounded wait of a kernel runs out, the rows that it does not reach (and the
+ * weights' gradients) are NaN.  Errors:
  * MOE_ERR_UNSUPPORTED_SHAPE for H outside [1, 16384], MOE_ERR_INVALID_ARG for
  * a NULL or misaligned pointer, T < 0, an unknown type or gate kind, or an eps
  * or scale that is not finite (eps also when negative).
