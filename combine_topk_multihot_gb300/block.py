@@ -17,7 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
-from typing import List, Optional, Sequence, Union
+from typing import Optional, Sequence, Union
 
 import numpy as np
 import torch
@@ -219,7 +219,8 @@ class AdamWState:
 
     ``step`` counts the steps taken; ``seed`` draws the random rounding of 8-bit
     exp_avg_sq.  The buffers may be given (to resume, or to place them): then
-    they are used as they are, else they are made for a fresh start."""
+    they are used as they are, else they are made for a fresh start.  They stay
+    the same for the state's life: load values into them with copy_."""
 
     def __init__(self, params: Sequence[torch.Tensor], state_bits: int = 32, master: Union[bool, Sequence, None] = None,
                  seed: int = 0, step: int = 0, exp_avg=None, exp_avg_sq=None, exp_avg_scale=None,
@@ -234,26 +235,28 @@ class AdamWState:
         for i, p in enumerate(self.params):
             _on_gpu(p, f"params[{i}]")
             _either(p, f"params[{i}]")
+        if len({p.data_ptr() for p in self.params if p.numel()}) < sum(p.numel() > 0 for p in self.params):
+            raise ValueError("params holds the same tensor twice")
         self.device = self.params[0].device if self.params else torch.device("cuda", torch.cuda.current_device())
         blocks = [-(-p.numel() // N.MOE_ADAMW_STATE_BLOCK) for p in self.params]
 
         def make(given, what, dtype, shapes):
             if given is None:
-                return [torch.zeros(s, dtype=dtype, device=self.device) for s in shapes]
+                return tuple(torch.zeros(s, dtype=dtype, device=self.device) for s in shapes)
             if len(given) != len(self.params):
                 raise ValueError(f"{what} must hold one tensor per parameter")
-            return list(given)
+            return tuple(given)
 
         shapes = [p.shape for p in self.params]
         avg = torch.uint8 if eight else torch.float32
-        self.exp_avg = make(exp_avg, "exp_avg", avg, shapes)
-        self.exp_avg_sq = make(exp_avg_sq, "exp_avg_sq", avg, shapes)
-        self.exp_avg_scale = make(exp_avg_scale, "exp_avg_scale", torch.float32, blocks) if eight else None
-        self.exp_avg_sq_scale = make(exp_avg_sq_scale, "exp_avg_sq_scale", torch.float32, blocks) if eight else None
+        self._exp_avg = make(exp_avg, "exp_avg", avg, shapes)
+        self._exp_avg_sq = make(exp_avg_sq, "exp_avg_sq", avg, shapes)
+        self._exp_avg_scale = make(exp_avg_scale, "exp_avg_scale", torch.float32, blocks) if eight else None
+        self._exp_avg_sq_scale = make(exp_avg_sq_scale, "exp_avg_sq_scale", torch.float32, blocks) if eight else None
         if isinstance(master, (list, tuple)):
-            self.master: Optional[List] = make(master, "master", torch.float32, shapes)
+            self._master = make(master, "master", torch.float32, shapes)
         else:
-            self.master = [p.detach().float() if p.dtype is torch.bfloat16 else None for p in self.params] \
+            self._master = tuple(p.detach().float() if p.dtype is torch.bfloat16 else None for p in self.params) \
                 if master else None
         self._table = np.zeros(len(self.params), dtype=_TABLE)
         self._address = self._table.ctypes.data
@@ -268,6 +271,13 @@ class AdamWState:
                 held = getattr(self, name)
                 if held is not None and held[i] is not None:
                     row[name] = _need(held[i], f"{name}[{i}]", dtype, shape, self.device) or 0
+
+    # (read-only: the table that the kernel gets was made from them)
+    exp_avg = property(lambda self: self._exp_avg)
+    exp_avg_sq = property(lambda self: self._exp_avg_sq)
+    exp_avg_scale = property(lambda self: self._exp_avg_scale)
+    exp_avg_sq_scale = property(lambda self: self._exp_avg_sq_scale)
+    master = property(lambda self: self._master)
 
 
 def moe_adamw_step(state: AdamWState, grads: Sequence[Optional[torch.Tensor]], lr: float, beta1: float = 0.9,

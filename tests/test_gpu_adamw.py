@@ -298,3 +298,18 @@ def test_refusals(moe):
         with pytest.raises(moe.MoEError, match="INVALID_ARG"):
             moe.moe_adamw_step(opt, [p], **kw)
     assert opt.step == 0 and not p.any()
+
+
+def test_the_states_buffers_stay(moe):
+    p = torch.zeros(300, device=DEV)
+    opt = moe.AdamWState([p], state_bits=8)
+    with pytest.raises(ValueError, match="twice"):
+        moe.AdamWState([p, torch.zeros(4, device=DEV), p])
+    for name in ("exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale"):
+        with pytest.raises(AttributeError):
+            setattr(opt, name, [])
+        with pytest.raises(TypeError):
+            getattr(opt, name)[0] = torch.zeros(300, device=DEV)
+    # no elements: nothing to update, and not the same tensor twice
+    e = torch.zeros(0, device=DEV)
+    moe.moe_adamw_step(moe.AdamWState([e, e]), [e, e], 1e-3)
