@@ -104,7 +104,7 @@ def test_quantize_nonfinite(moe):
         assert not torch.isfinite(out[:2]).any() and torch.isfinite(out[2:]).all()
 
 
-# few rows (1..32: the weight stream, 1, 2 or 4 token tiles), the three tile
+# few rows (1 to 8: the weight stream), more on the tensor cores: the three tile
 # widths, ragged edges in every dimension, one K block, K not a multiple of 128
 MATMUL = [(1, 16, 16), (1, 4096, 2048), (7, 100, 128), (8, 64, 1024), (9, 129, 400), (16, 513, 512), (17, 77, 2064),
           (32, 2048, 768), (33, 64, 128), (64, 1000, 2048), (100, 8, 144), (128, 256, 512), (129, 2048, 1040),
@@ -155,6 +155,7 @@ def _experts_ref(xd, counts, offsets, w, W1, s1, W2, s2, I):
     (200, 512, 16, 4, 256, 128, 0.1), (700, 1024, 8, 2, 640, 1, 0.0), (300, 256, 1024, 2, 128, 1, 0.0),
     (64, 256, 8, 1, 128, 4, 1.0),   # every slot dropped: no rows at all
     (40, 256, 4, 1, 128, 1, 0.0),
+    (8, 1024, 8, 4, 256, 4, 0.1), (9, 1024, 8, 4, 256, 4, 0.1),   # the two sides of the rule on rows
 ])
 def test_experts(moe, T, H, E, K, I, P, drop):
     idx, p = random_routing(T, E, K, seed=T + H, drop=drop)
