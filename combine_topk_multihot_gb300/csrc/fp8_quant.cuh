@@ -67,6 +67,11 @@ __device__ __forceinline__ uint32_t bf16x2_abs_max(uint32_t a, uint32_t b) {
 }
 
 __device__ __forceinline__ float block_scale(float amax) {
+  if (amax >= 0x1p-90f && amax < 0x1p100f) {  // Markstein's residual again, see below
+    constexpr float inv = 1.0f / E4M3_MAX;
+    const float q = __fmul_rn(amax, inv);
+    return __fmaf_rn(-__fmaf_rn(q, E4M3_MAX, -amax), inv, q);
+  }
   return amax == 0.f ? 1.0f : max_nan(__fdiv_rn(amax, E4M3_MAX), 0x1p-126f);
 }
 
@@ -84,8 +89,8 @@ __device__ __forceinline__ uint32_t e4m3x4(float v0, float v1, float v2, float v
 // r = v - q s is exact in a fused multiply-add and q + r y, rounded once, is
 // the correctly rounded quotient.  The residual is exact while its last bit
 // is above fp32's smallest, which holds for |v| >= 2^-103; with a scale of at
-// least 2^-90 a smaller v has a code of zero either way (with v's sign,
-// which is set last: the residual's error may turn it).  Other scales (and
+// least 2^-90 a smaller v has a code of zero either way.  The residual is taken as
+// q s - v, which leaves the sign of a zero quotient v's.  Other scales (and
 // non-finite ones) take the division.
 // Bit-exactness matters here: a quotient of two bf16 values often lies midway
 // between two codes, or an fp32 ulp from there.
@@ -94,12 +99,12 @@ struct BlockDivide {
   bool fast;
   __device__ __forceinline__ explicit BlockDivide(float scale) {
     s = scale;
-    y = __fdiv_rn(1.0f, scale);
+    y = __frcp_rn(scale);
     fast = scale >= 0x1p-90f && scale < 0x1p100f;
   }
   __device__ __forceinline__ float operator()(float v) const {
     const float q = __fmul_rn(v, y);
-    return copysignf(__fmaf_rn(__fmaf_rn(-q, s, v), y, q), v);
+    return __fmaf_rn(-__fmaf_rn(q, s, -v), y, q);
   }
   // codes of eight bf16 values
   __device__ __forceinline__ uint2 codes(const uint32_t (&w)[4]) const {
