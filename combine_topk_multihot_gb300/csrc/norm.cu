@@ -28,12 +28,20 @@ namespace {
 template <int NV>
 constexpr int SLOTS_OF = NV <= 2 ? 2 : 1;
 
+// CTAs an SM with rows through shared memory: as many as the registers of the
+// form allow (T = 16384, bf16: after a block with the next norm, H = 2048 48 us
+// with three, 54 with two, 56 with four; before a block 21 with four, 24 with
+// three; of rows of 8192 values 46 with three, 51 with two).
+template <bool HAS_Y, bool ELEM, int NV>
+constexpr int PIPE_CTAS = ELEM ? 2 : NV == 2 ? (HAS_Y ? 3 : 4) : HAS_Y ? 2 : 3;
+
 // A group of `row_threads` threads takes one row at a time.  With up to two
 // vectors a thread the weights stay in registers; else they come from L1 at
 // each use.  PIPE: rows arrive through
 // shared memory (H a multiple of 8).
 template <bool XF32, bool HAS_Y, bool HAS_NEXT, bool ELEM, int NV, bool PIPE>
-__global__ void __launch_bounds__(NV == 1 ? 1024 : PIPE ? 256 : 512, PIPE ? 2 : 1)
+__global__ void __launch_bounds__(NV == 1 ? 1024 : PIPE ? 256 : 512,
+                                  !PIPE ? (NV == 4 && !HAS_Y ? 2 : 1) : PIPE_CTAS<HAS_Y, ELEM, NV>)
     norm_forward_kernel(const NormArgs a, int row_threads) {
   __shared__ float red[2][MAX_WARPS][4];
   constexpr int SLOTS = SLOTS_OF<NV>;
@@ -178,7 +186,7 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : PIPE ? 256 : 512, PIPE ? 2 : 
 // spread over as many threads as it can use: what counts then is the latency
 // of one.
 struct ForwardShape {
-  int nv, row_threads, groups, per_sm;
+  int nv, row_threads, groups, per_sm;  // (per_sm: of the direct form)
   bool pipe;
 };
 ForwardShape forward_shape(long long T, int H) {
@@ -189,14 +197,14 @@ ForwardShape forward_shape(long long T, int H) {
   f.row_threads = threads_of(H, f.nv);
   f.pipe = f.nv > 1 && H % 8 == 0 && f.row_threads <= 256;
   f.groups = !f.pipe ? 1 : 256 / f.row_threads > MAX_GROUPS ? MAX_GROUPS : 256 / f.row_threads;
-  f.per_sm = f.pipe ? 2 : f.row_threads >= 512 ? 2 : 1024 / f.row_threads > 16 ? 16 : 1024 / f.row_threads;
+  f.per_sm = f.row_threads >= 512 ? 2 : 1024 / f.row_threads > 16 ? 16 : 1024 / f.row_threads;
   return f;
 }
 
 template <bool XF32, bool HAS_Y, bool HAS_NEXT, bool ELEM, int NV, bool PIPE>
 cudaError_t forward_launch(const NormArgs& a, const ForwardShape& f, cudaStream_t s) {
   auto kernel = norm_forward_kernel<XF32, HAS_Y, HAS_NEXT, ELEM, NV, PIPE>;
-  long long grid = static_cast<long long>(sm_count()) * f.per_sm;
+  long long grid = static_cast<long long>(sm_count()) * (PIPE ? PIPE_CTAS<HAS_Y, ELEM, NV> : f.per_sm);
   const long long need = (a.T + f.groups - 1) / f.groups;
   if (grid > need) grid = need;
   size_t smem = 0;
