@@ -33,9 +33,10 @@ constexpr int SLOTS = 1;
 // A CTA's threads form groups of `row_threads`, each with a row of its own and
 // its own accumulators; they are added up before the CTA's partial row is
 // written, so that there are few of those.
-// PIPE: rows arrive through shared memory (H a multiple of 8).
-template <bool XF32, bool HAS_Y, bool HAS_NEXT, bool ELEM, int NV, bool PIPE>
-__global__ void __launch_bounds__(512, 1)
+// PIPE: rows arrive through shared memory (H a multiple of 8).  THIRD: CTAs of
+// up to 256 threads, three an SM.
+template <bool XF32, bool HAS_Y, bool HAS_NEXT, bool ELEM, int NV, bool PIPE, bool THIRD = false>
+__global__ void __launch_bounds__(THIRD ? 256 : 512, THIRD ? 3 : 1)
     norm_backward_kernel(const NormBackwardArgs a, int row_threads) {
   __shared__ float red[2][MAX_WARPS][4];
   __shared__ uint64_t s_bar[MAX_GROUPS][SLOTS];
@@ -295,9 +296,9 @@ constexpr size_t SMEM_PER_SM = 228 * 1024;
 // tensors of a row in 128 registers; four above 8192 values a row.
 struct BackwardShape {
   int nv, row_threads, groups, per_sm, grid;
-  bool pipe;
+  bool pipe, third;
 };
-BackwardShape backward_shape(long long T, int H) {
+BackwardShape backward_shape(long long T, int H, bool lean) {
   const int v = vectors(H);
   BackwardShape b = {};
   b.nv = (v <= 32 || T < 4LL * sm_count() || H % 8) && v <= 512 ? 1 : v <= 1024 && H % 8 == 0 ? 2 : 4;
@@ -306,7 +307,12 @@ BackwardShape backward_shape(long long T, int H) {
   b.groups = T > sm_count() && b.row_threads <= 128 ? 256 / b.row_threads : 1;
   if (b.groups > MAX_GROUPS) b.groups = MAX_GROUPS;
   const int threads = b.row_threads * b.groups;
-  b.per_sm = threads > 256 ? 1 : 512 / threads > 4 ? 4 : 512 / threads;
+  // A lean form's row tensors (no element gate, no second norm) fit 80
+  // registers, for a third CTA, which pays from a dozen rows a group on (before a
+  // block, 16384 x 4096 bf16: 98 -> 89 us; below, its partial sums and the
+  // smaller register file cost more: 4096 x 2048 fp32 26 -> 29).
+  b.third = lean && b.nv == 2 && threads == 256 && T >= 12LL * b.groups * 3 * sm_count();
+  b.per_sm = threads > 256 ? 1 : b.third ? 3 : 512 / threads > 4 ? 4 : 512 / threads;
   const long long need = (T + b.groups - 1) / b.groups, most = static_cast<long long>(sm_count()) * b.per_sm;
   b.grid = static_cast<int>(need < most ? need : most);
   return b;
@@ -319,10 +325,10 @@ size_t slot_bytes(const NormBackwardArgs& a) {
   return (row * a.H + 127) / 128 * 128;
 }
 
-template <bool XF32, bool HAS_Y, bool HAS_NEXT, bool ELEM, int NV, bool PIPE>
+template <bool XF32, bool HAS_Y, bool HAS_NEXT, bool ELEM, int NV, bool PIPE, bool THIRD = false>
 cudaError_t backward_launch(const NormBackwardArgs& a, const BackwardShape& b, cudaStream_t s) {
   constexpr int ACC = (HAS_Y ? 1 : 0) + (HAS_NEXT ? 1 : 0);
-  auto kernel = norm_backward_kernel<XF32, HAS_Y, HAS_NEXT, ELEM, NV, PIPE>;
+  auto kernel = norm_backward_kernel<XF32, HAS_Y, HAS_NEXT, ELEM, NV, PIPE, THIRD>;
   const int threads = b.row_threads * b.groups;
   size_t smem = static_cast<size_t>(ACC) * NV * 2 * threads * sizeof(float4);
   if (PIPE) smem += slot_bytes<XF32, HAS_Y, HAS_NEXT>(a) * b.groups * SLOTS;
@@ -337,7 +343,8 @@ cudaError_t backward_launch(const NormBackwardArgs& a, const BackwardShape& b, c
 template <bool XF32, bool HAS_Y, bool HAS_NEXT, bool ELEM>
 cudaError_t backward(const NormBackwardArgs& a, cudaStream_t s) {
   constexpr int ACC = (HAS_Y ? 1 : 0) + (HAS_NEXT ? 1 : 0);
-  BackwardShape b = backward_shape(a.T, a.H);
+  constexpr bool LEAN = !ELEM && !(HAS_Y && HAS_NEXT);
+  BackwardShape b = backward_shape(a.T, a.H, LEAN);
   // The slots have to fit beside the sums, if need be with one CTA an SM; else
   // (wide rows) the rows are loaded directly.
   const size_t sums = static_cast<size_t>(ACC) * b.nv * 2 * b.row_threads * b.groups * sizeof(float4);
@@ -346,6 +353,7 @@ cudaError_t backward(const NormBackwardArgs& a, cudaStream_t s) {
   if (b.pipe && all > SMEM_PER_SM / b.per_sm - 3072 && b.grid > sm_count()) b.grid = sm_count();
   if (b.grid > 0) {
     const cudaError_t err = b.nv == 1   ? backward_launch<XF32, HAS_Y, HAS_NEXT, ELEM, 1, false>(a, b, s)
+                            : b.third   ? backward_launch<XF32, HAS_Y, HAS_NEXT, ELEM, 2, true, LEAN>(a, b, s)
                             : b.nv == 2 ? backward_launch<XF32, HAS_Y, HAS_NEXT, ELEM, 2, true>(a, b, s)  // fits: H <= 8192
                             : b.pipe    ? backward_launch<XF32, HAS_Y, HAS_NEXT, ELEM, 4, true>(a, b, s)
                                         : backward_launch<XF32, HAS_Y, HAS_NEXT, ELEM, 4, false>(a, b, s);
@@ -372,7 +380,8 @@ cudaError_t launch_norm_backward(const NormBackwardArgs& a, cudaStream_t s) {
 }
 
 size_t norm_backward_workspace(long long T, int H) {
-  return static_cast<size_t>(backward_shape(T, H).grid) * 2 * H * sizeof(float);
+  const int lean = backward_shape(T, H, true).grid, full = backward_shape(T, H, false).grid;
+  return static_cast<size_t>(lean > full ? lean : full) * 2 * H * sizeof(float);  // (whichever form is called)
 }
 
 }  // namespace moe

@@ -278,3 +278,12 @@ def test_refusals(moe):
         moe.moe_norm_in(torch.zeros(4 * 64 + 1, dtype=BF16, device=DEV)[1:].view(4, 64), w)
     with pytest.raises(moe.MoEError, match="16384"):
         moe.moe_norm_in(torch.zeros(1, 16385, dtype=BF16, device=DEV), torch.ones(16385, device=DEV))
+
+
+# rows enough for a third CTA an SM in the backward of the forms with few row tensors
+@pytest.mark.parametrize("T,H", [(5600, 2560), (11200, 2048)])
+@pytest.mark.parametrize("xt", [BF16, F32])
+def test_many_rows(moe, T, H, xt):
+    test_norm_in(moe, T, H, xt, F32)
+    for gate_kind, gt in (("none", F32), ("token", BF16)):
+        test_norm_out(moe, T, H, xt, gate_kind, False, True, gt)
