@@ -108,7 +108,8 @@ def test_quantize_nonfinite(moe):
 # widths, ragged edges in every dimension, one K block, K not a multiple of 128
 MATMUL = [(1, 16, 16), (1, 4096, 2048), (7, 100, 128), (8, 64, 1024), (9, 129, 400), (16, 513, 512), (17, 77, 2064),
           (32, 2048, 768), (33, 64, 128), (64, 1000, 2048), (100, 8, 144), (128, 256, 512), (129, 2048, 1040),
-          (300, 4100, 2048), (1000, 384, 4096), (1111, 8192, 256), (2049, 1027, 512), (5000, 4096, 384)]
+          (300, 4100, 2048), (1000, 384, 4096), (1111, 8192, 256), (2049, 1027, 512), (5000, 4096, 384),
+          (5001, 4099, 384), (777, 2050, 640)]
 
 
 @pytest.mark.parametrize("M,N,K", MATMUL)
