@@ -39,24 +39,33 @@ __device__ __forceinline__ Raw<F32> raw_zero() {
 }
 
 // Rows that do not start on 16 bytes: value by value, out of line (the fast
-// path's code would drown in it).
+// path's code would drown in it).  There the 256 values of a warp's 32 vectors
+// are dealt out one by one, so that each access is to 32 neighbours
+// (T = 16384, H = 2049, before a block: 66 us, 8 neighbours a lane 111); a sum
+// over the row does not mind.  `col` is a multiple of 8, col / 8 of a warp's
+// first lane one of 32.
+__device__ __forceinline__ int ragged_col(int col, int i) {
+  const int v = col >> 3;
+  return ((v & ~31) << 3) + 32 * i + (v & 31);
+}
+
 template <bool F32>
 __device__ __noinline__ Raw<F32> load_ragged(const void* row, int col, int H) {
   Raw<F32> o = raw_zero<F32>();
   if constexpr (F32) {
-    const float* p = static_cast<const float*>(row) + col;
+    const float* p = static_cast<const float*>(row);
     uint32_t t[8] = {};
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (col + i < H) t[i] = __float_as_uint(p[i]);
+      if (const int c = ragged_col(col, i); c < H) t[i] = __float_as_uint(p[c]);
     o.q = make_uint4(t[0], t[1], t[2], t[3]);
     o.r = make_uint4(t[4], t[5], t[6], t[7]);
   } else {
-    const uint16_t* p = static_cast<const uint16_t*>(row) + col;
+    const uint16_t* p = static_cast<const uint16_t*>(row);
     uint32_t t[4] = {};
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (col + i < H) t[i >> 1] |= static_cast<uint32_t>(p[i]) << (16 * (i & 1));
+      if (const int c = ragged_col(col, i); c < H) t[i >> 1] |= static_cast<uint32_t>(p[c]) << (16 * (i & 1));
     o.q = make_uint4(t[0], t[1], t[2], t[3]);
   }
   return o;
@@ -115,17 +124,17 @@ __device__ __forceinline__ Raw<F32> narrow(const F8& a) {
 template <bool F32>
 __device__ __noinline__ void store_ragged(void* row, int col, int H, const Raw<F32> a) {
   if constexpr (F32) {
-    float* p = static_cast<float*>(row) + col;
+    float* p = static_cast<float*>(row);
     const uint32_t t[8] = {a.q.x, a.q.y, a.q.z, a.q.w, a.r.x, a.r.y, a.r.z, a.r.w};
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (col + i < H) p[i] = __uint_as_float(t[i]);
+      if (const int c = ragged_col(col, i); c < H) p[c] = __uint_as_float(t[i]);
   } else {
-    uint16_t* p = static_cast<uint16_t*>(row) + col;
+    uint16_t* p = static_cast<uint16_t*>(row);
     const uint32_t t[4] = {a.q.x, a.q.y, a.q.z, a.q.w};
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (col + i < H) p[i] = static_cast<uint16_t>(t[i >> 1] >> (16 * (i & 1)));
+      if (const int c = ragged_col(col, i); c < H) p[c] = static_cast<uint16_t>(t[i >> 1] >> (16 * (i & 1)));
   }
 }
 

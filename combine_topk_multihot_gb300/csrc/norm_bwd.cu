@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(THIRD ? 256 : 512, THIRD ? 3 : 1)
             const float f[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              if (c + i < H) dst[c + i] = f[i];
+              if (const int at_col = ragged_col(col(j), 4 * h + i); at_col < H) dst[at_col] = f[i];
           }
         }
     }
