@@ -267,7 +267,10 @@ __device__ __forceinline__ void pipe_issue(uint32_t slot, uint32_t bar, const ch
 
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
 
@@ -285,9 +288,14 @@ __device__ __forceinline__ Raw<F32> read_slot(uint32_t row, int col, int H) {
 }
 
 // All threads of the group (named barrier 1 + group) agree whether all of them
-// saw their row arrive.
+// saw their row arrive, and have read what they read of the slot: it may be
+// filled again.  (A vote alone orders no memory.)
 __device__ __forceinline__ bool group_all(bool ok, int threads, int group) {
-  if (threads == 32) return __all_sync(FULL_MASK, ok);
+  if (threads == 32) {
+    const bool all = __all_sync(FULL_MASK, ok);
+    __syncwarp();
+    return all;
+  }
   int r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"

@@ -287,3 +287,21 @@ def test_many_rows(moe, T, H, xt):
     test_norm_in(moe, T, H, xt, F32)
     for gate_kind, gt in (("none", F32), ("token", BF16)):
         test_norm_out(moe, T, H, xt, gate_kind, False, True, gt)
+
+
+@pytest.mark.parametrize("H", [264, 384, 512])
+def test_one_warp_a_row(moe, H):
+    """Rows that one warp takes, many of them, so that each slot in shared
+    memory is filled again and again: right, and the same bits each time."""
+    T = 20000
+    test_norm_in(moe, T, H, BF16, F32)
+    g = torch.Generator().manual_seed(H)
+    x, y, w = _randn(g, T, H, dtype=BF16), _randn(g, T, H, dtype=BF16), _randn(g, H)
+    first = moe.moe_norm_out(x, y, w, next_weight=w, save_rstd=True)
+    for _ in range(5):
+        assert all(torch.equal(a, b) for a, b in zip(first, moe.moe_norm_out(x, y, w, next_weight=w, save_rstd=True)))
+    back = dict(grad_next=y, out=first[0], next_weight=w, next_rstd=first[3])
+    grads = moe.moe_norm_out_backward(x, y, w, first[1], **back)
+    for _ in range(5):
+        for a, b in zip(grads, moe.moe_norm_out_backward(x, y, w, first[1], **back)):
+            assert (a is None and b is None) or torch.equal(a, b)
