@@ -23,6 +23,7 @@ import numpy as np
 import torch
 
 from . import _native as N
+from . import moe as _m
 from .moe import Layout, _check
 
 _DTYPES = {torch.bfloat16: N.MOE_DTYPE_BF16, torch.float32: N.MOE_DTYPE_F32}
@@ -35,7 +36,15 @@ _current_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _raw_stream(stream, device):
-    return _current_raw_stream(device.index) if stream is None else stream.cuda_stream
+    """The handle of the stream to launch on.  A launch goes to the current
+    device, so tensors and stream have to be there."""
+    if device.index != _m._current_device():
+        raise _m._wrong_device("the tensors are", device.index)
+    if stream is None:
+        return _current_raw_stream(device.index)
+    if stream.device_index != device.index:
+        raise _m._wrong_device("the stream is", stream.device_index)
+    return stream.cuda_stream
 
 
 def _used_on(stream, *made: Optional[torch.Tensor]):
@@ -91,15 +100,16 @@ def _norm(T, H, x, weight, gate, gate_sigmoid, residual_scale, eps, weight_offse
 
 
 @functools.lru_cache(maxsize=1024)
-def _bytes(query: str, *sizes) -> int:
-    """A workspace's size, which depends on its arguments (and the device's SM count) alone."""
+def _bytes(query: str, device: int, *sizes) -> int:
+    """A workspace's size, which depends on its arguments and the device's SM
+    count alone (``device``: the one that the call goes to)."""
     nbytes = ctypes.c_size_t(0)
     _check(getattr(N.lib, query)(*sizes, ctypes.byref(nbytes)), query)
     return nbytes.value
 
 
 def _workspace(T, H, device):
-    return torch.empty(_bytes("moe_norm_backward_workspace_bytes", T, H), dtype=torch.uint8, device=device)
+    return torch.empty(_bytes("moe_norm_backward_workspace_bytes", device.index, T, H), dtype=torch.uint8, device=device)
 
 
 def moe_norm_in(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, weight_offset: float = 0.0,
@@ -396,7 +406,8 @@ def moe_grouped_experts_fp8_block(x_disp: torch.Tensor, layout: Layout, W1_q: to
     E, I = layout.E, W1_q.shape[1] // 2
     if out is None:
         out = torch.empty(C, H, dtype=torch.bfloat16, device=dev)
-    ws = torch.empty(_bytes("moe_experts_fp8_block_workspace_bytes", C, layout.T, E, H, I), dtype=torch.uint8, device=dev)
+    ws = torch.empty(_bytes("moe_experts_fp8_block_workspace_bytes", dev.index, C, layout.T, E, H, I), dtype=torch.uint8,
+                     device=dev)
     _check(N.lib.moe_grouped_experts_fp8_block(
         _need(x_disp, "x_disp", torch.bfloat16, (C, H), dev), layout.ref, H, I,
         _need(W1_q, "W1_q", torch.uint8, (E, 2 * I, H), dev),

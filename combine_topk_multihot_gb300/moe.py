@@ -29,9 +29,20 @@ def _check(code: int, where: str):
         raise MoEError(code, where)
 
 
+# (looked up at each call: a test stands in for a second device)
+_current_device = torch._C._cuda_getDevice
+
+
+def _wrong_device(what, device: int):
+    return ValueError(f"{what} on cuda:{device}, but the current device is cuda:{_current_device()}, where kernels are "
+                      "launched: make it the current one (torch.cuda.device)")
+
+
 def _ptr(t: Optional[torch.Tensor]):
     if t is None:
         return None
+    if t.is_cuda and t.get_device() != _current_device():
+        raise _wrong_device("the tensors are", t.get_device())
     if not t.is_contiguous():
         raise ValueError("tensors passed to the library must be contiguous")
     return ctypes.c_void_p(t.data_ptr()) if t.numel() else None
@@ -39,6 +50,8 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _stream(stream=None):
     s = stream if stream is not None else torch.cuda.current_stream()
+    if stream is not None and s.device_index != _current_device():
+        raise _wrong_device("the stream is", s.device_index)
     return ctypes.c_void_p(s.cuda_stream)
 
 
