@@ -228,7 +228,7 @@ class AdamWState:
     master=True, the fp32 value of which a bf16 parameter is the rounded copy.
 
     ``step`` counts the steps taken; ``seed`` draws the random rounding of 8-bit
-    exp_avg_sq.  The buffers may be given (to resume, or to place them): then
+    states.  The buffers may be given (to resume, or to place them): then
     they are used as they are, else they are made for a fresh start.  They stay
     the same for the state's life: load values into them with copy_."""
 

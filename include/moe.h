@@ -626,7 +626,7 @@ typedef struct moe_adamw_tensor {
 typedef struct moe_adamw {
   double lr, beta1, beta2, eps;
   int64_t step;               /* >= 1: the number of this step                               */
-  uint64_t seed;              /* of the random rounding of 8-bit v, with the tensor's place
+  uint64_t seed;              /* of the random rounding of 8-bit states, with the tensor's place
                                    in the array, the step and the element's index           */
   int32_t state_bits;         /* 32 or 8, of every tensor's exp_avg and exp_avg_sq           */
   const float* grad_scale;    /* device, nullable: one factor for all gradients              */
@@ -637,9 +637,11 @@ typedef struct moe_adamw {
 
 /*
  * Any address that suits its element type will do; addresses of whole 16
- * bytes (8 for bf16, 4 for codes) are faster.  8-bit states: m is rounded to
- * the nearest code, v up or down at random with the probability that keeps
- * its mean, and a positive v never to zero.  A non-finite gradient makes its
+ * bytes (8 for bf16, 4 for codes) are faster.  8-bit states: v is
+ * rounded up or down at random with the probability that keeps its mean, and
+ * if positive never to zero; m likewise with beta1 > 11/12, else to the
+ * nearest code (at random below 2^-6 of its scale), and to the nearest in
+ * steps 1 to 8.  A non-finite gradient makes its
  * element's p, m and v non-finite, and with 8-bit states its block's: use
  * `skip`.  Errors: MOE_ERR_INVALID_ARG for NULL or misaligned pointers, an
  * unknown type, a master beside an fp32 param, state_bits not 8 or 32, step <

@@ -313,3 +313,109 @@ def test_the_states_buffers_stay(moe):
     # no elements: nothing to update, and not the same tensor twice
     e = torch.zeros(0, device=DEV)
     moe.moe_adamw_step(moe.AdamWState([e, e]), [e, e], 1e-3)
+
+
+@pytest.mark.parametrize("b1,b2", [(0.9, 0.95), (0.9, 0.999), (0.8, 0.95), (0.95, 0.95), (0.95, 0.99), (0.99, 0.999)])
+def test_8bit_averages_follow_adamw(moe, b1, b2):
+    """Gradients that stop: over several hundred steps the mean of the held m
+    and the parameters' way are those of fp64 AdamW.  One element of each block keeps
+    its gradient and thereby the block's scale.
+
+    Tolerances for b1 > 11/12, where m is rounded at random after the 8th step.
+    A step's rounding moves m by half a code's distance at the
+    most to nearest (m / 16; all elements alike) and by a whole
+    one at random, with a standard deviation of at most m / 16 or half the lowest code,
+    independent over n elements; what step t did is worth b1^(T - t) of it at step T.  So the
+    mean is within sum_{t <= 8} b1^(T - t) M_t / 16 + 5 sqrt(sum_t (b1^(T - t)
+    (M_t / 12 + low))^2 / n), 12 for 16 because the spread of m adds to it.
+    For other b1 normal codes go to nearest.  A step then moves m by one code or
+    more, the right number of them to within a half: with a growing sum it stops up to half a distance (1 / 16) over
+    1 - b1 short or ahead of the gradient, and from halving to halving (7 steps for 6.58 at b1 = 0.9, 3 for 3.11
+    at 0.8) it gains or loses less than 5 %, over 15 halvings at most a factor of 2.
+    v's rounding has a relative variance of at most (1 - b2) / 5 a step on
+    the average over its codes and raises the mean of 1 / sqrt(v) by 3/8 of what it has become,
+    while the way after the stop is made in the first 1 / (1 - b1 / sqrt(b2)) steps or so:
+    for these settings by less than 0.2; with the first steps' 0.07 or nearest codes' 1/16
+    0.4 is allowed above, and 0.2 below."""
+    n, stop, steps = 1 << 16, 40, 440
+    p = torch.zeros(n, device=DEV)
+    opt = moe.AdamWState([p], state_bits=8, seed=21)
+    top = torch.arange(n, device=DEV) % 256 == 0
+    on, off = torch.where(top, 1.0, 0.3), torch.where(top, 1.0, 0.0)
+    M = V = P = at_stop = P_stop = near = spread = 0.0
+    low = 2.0 ** -9 / 448
+    for t in range(1, steps + 1):
+        moe.moe_adamw_step(opt, [on if t <= stop else off], 1.0, b1, b2, 1e-8)
+        g = 0.3 if t <= stop else 0.0
+        M, V = b1 * M + (1 - b1) * g, b2 * V + (1 - b2) * g * g
+        P -= (M / (1 - b1 ** t)) / (math.sqrt(V / (1 - b2 ** t)) + 1e-8)
+        near = b1 * near + (M / 16 if t <= 8 else 0.0)
+        spread = b1 * b1 * spread + (M / 12 + low) ** 2
+        if t == stop:
+            at_stop, P_stop = p.double().clone(), P
+        if t in (8, 20, stop, stop + 20, stop + 60, stop + 100, stop + 200, steps):
+            m = opt.exp_avg[0].view(torch.float8_e4m3fn).double() * opt.exp_avg_scale[0].double().repeat_interleave(256)
+            mean, noise = float(m[~top].mean()), 5 * math.sqrt(spread / n) + 1e-12
+            if b1 > 11 / 12:
+                assert abs(mean - M) <= near + noise, (t, mean, M)
+            else:
+                assert M / 2 - noise <= mean <= 2 * M + noise, (t, mean, M)
+    way, ref = float((p.double() - at_stop)[~top].mean()), P - P_stop
+    assert 0.8 <= way / ref <= 1.4, (way, ref)
+
+
+def _encode_m(m, seed, tensor, step, beta1):
+    """(m codes, m scales) by the rule of the steps after the 8th, in numpy fp32."""
+    f = np.float32
+    bm = _blocks(m)
+    ms = np.maximum(np.abs(bm).max(1) / f(448), f(2.0 ** -120))
+    t = (bm * (f(1) / ms)[:, None]).reshape(-1)[:len(m)]
+    r = _random16(len(m) + len(m) % 2, seed, tensor, step).reshape(-1, 2)[:, ::-1].reshape(-1)[:len(m)]
+    bits = (np.abs(t) * f(2.0 ** -120)).view(np.uint32)
+    up = np.minimum((bits + (r << 4)) >> 20, 0x7E) | (np.signbit(t).astype(np.uint32) << 7)
+    near = torch.from_numpy(t).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    return np.where((np.abs(t) < 2.0 ** -6) | (beta1 > 11 / 12), up, near).astype(np.uint8), ms
+
+
+@pytest.mark.parametrize("b1", [0.9, 0.95])
+def test_8bit_first_average_bit_exact(moe, b1):
+    """The codes of m after the first steps are a stated function of m, seed,
+    tensor, step and element; v's and both scales as before."""
+    g = torch.Generator().manual_seed(13)
+    b2, seed = 0.99, 5
+    f = np.float32
+    params = [torch.randn(n, generator=g).to(DEV) for n in SIZES]
+    opt = moe.AdamWState(params, state_bits=8, seed=seed, step=6)
+    for t in range(7, 12):
+        grads = [torch.randn(n, generator=g) * torch.exp(3 * torch.randn(n, generator=g)) for n in SIZES]
+        if t > 9:
+            for x in grads:
+                x[::2] = 0
+        before = [[s[i].cpu().numpy().copy() for s in (opt.exp_avg, opt.exp_avg_scale, opt.exp_avg_sq, opt.exp_avg_sq_scale)]
+                  for i in range(len(SIZES))]
+        moe.moe_adamw_step(opt, [x.to(DEV) for x in grads], 1e-2, b1, b2)
+        for i in range(len(SIZES)):
+            m, v = _decode(*before[i])
+            gi = grads[i].numpy()
+            m = m * f(b1) + gi * f(1 - b1)
+            v = v * f(b2) + gi * gi * f(1 - b2)
+            mc, ms, vc, vs = _encode(m, v, seed, i, t)
+            if t > 8:
+                mc, ms = _encode_m(m, seed, i, t, b1)
+            assert np.array_equal(opt.exp_avg_scale[i].cpu().numpy(), ms), (i, t)
+            assert np.array_equal(opt.exp_avg[i].cpu().numpy(), mc), (i, t)
+            assert np.array_equal(opt.exp_avg_sq_scale[i].cpu().numpy(), vs), (i, t)
+            assert np.array_equal(opt.exp_avg_sq[i].cpu().numpy(), vc), (i, t)
+
+
+@pytest.mark.parametrize("b1", [0.9, 0.95])
+def test_8bit_nonfinite_after_the_first_steps(moe, b1):
+    """As in the first steps: a NaN or an infinity stays in its block of 256."""
+    p, grad = torch.ones(1024, device=DEV), torch.ones(1024, device=DEV)
+    grad[300], grad[700] = float("nan"), float("-inf")
+    opt = moe.AdamWState([p], 8, step=50)
+    moe.moe_adamw_step(opt, [grad], 1e-2, b1)
+    assert (~torch.isfinite(p)).nonzero().flatten().tolist() == [300, 700]
+    codes = opt.exp_avg[0].view(torch.float8_e4m3fn).float()
+    assert codes[300].isnan() and codes[700].isnan() and torch.isfinite(codes[:256]).all()
+    assert not torch.isfinite(opt.exp_avg_scale[0][1:3]).any() and torch.isfinite(opt.exp_avg_scale[0][[0, 3]]).all()
