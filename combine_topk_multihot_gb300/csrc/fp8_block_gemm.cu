@@ -34,7 +34,9 @@
 //
 // As in the bf16 experts, the tile list is built on the device from the
 // layout's counts, one persistent CTA per SM; every wait is bounded, and a
-// wait that runs out sets MOE_DEVERR_TIMEOUT, drains and returns.
+// wait that runs out sets MOE_DEVERR_TIMEOUT, drains and leaves NaN in the
+// tiles that the CTA does not reach (NaN codes of h, which make the second
+// product's rows NaN), so that the call cannot pass for a finished one.
 
 #include "common.cuh"
 #include "fp8_quant.cuh"
@@ -113,6 +115,7 @@ struct Args {
   uint8_t* out_q;          // OUT_SWIGLU: codes [rows, N] and scales [rows, N / 128]
   float* out_scale;
   int* status;
+  int load_tiles;          // tiles a CTA loads operands for: all, but in the self-test
 };
 
 struct Tile {
@@ -227,7 +230,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       uint32_t phase = 0;
       long long issued = 0;
       bool ok = true;
-      for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+      int left = args.load_tiles;
+      for (int tile = blockIdx.x; tile < total && ok && left > 0; tile += gridDim.x, --left) {
         const Tile t = decode_tile(s_pre, E, args.n_tiles, tile);
         const int a_row = s_off[t.e] + t.mt * BM;
         const int b_row = t.e * args.b_rows + t.nt * (MODE == OUT_SWIGLU ? BN / 2 : BN);
@@ -342,7 +346,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     int buf = 0;
     uint32_t use = 0, parity = 0;
     bool ok = true;
-    for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x, parity ^= 1u) {
+    int tile = blockIdx.x;
+    for (; tile < total && ok; tile += gridDim.x, parity ^= 1u) {
       float acc[COLS];
 #pragma unroll
       for (int i = 0; i < COLS; ++i) acc[i] = 0.f;
@@ -475,6 +480,22 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
     }
+    // after a wait that ran out: this warp's part of the tiles not reached
+    for (; tile < total; tile += gridDim.x) {
+      const Tile t = decode_tile(s_pre, E, args.n_tiles, tile);
+      const int first = t.mt * BM + q * 32, rows = min(s_cnt[t.e] - first, 32);
+      const long long row0 = s_off[t.e] + first;
+      const int col0 = MODE == OUT_SWIGLU ? t.nt * 128 + half * 64 : t.nt * BN + half * COLS;
+      const int cols = min(args.N - col0, MODE == OUT_SWIGLU ? 64 : COLS);
+#pragma unroll 1
+      for (int r = 0; r < rows; ++r)
+#pragma unroll 1
+        for (int c = lane; c < cols; c += 32) {
+          const long long at = (row0 + r) * args.N + col0 + c;
+          if constexpr (MODE == OUT_SWIGLU) args.out_q[at] = 0x7f;
+          else args.out[at] = 0x7fc0;
+        }
+    }
     if (lane == 0) tma_store_wait_all();
     __syncwarp();
   }
@@ -486,9 +507,13 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (threadIdx.x == 0 && s.abort) report(args.status, MOE_DEVERR_TIMEOUT);
 }
 
+// The self-test's limit of the tiles that a CTA loads, for this host thread's launches.
+thread_local int tls_load_tiles = 0x7fffffff;
+
 template <int MODE, int BN>
-cudaError_t launch(const void* a, uint64_t a_rows, const void* b, uint64_t b_rows, const Args& args, int grid,
+cudaError_t launch(const void* a, uint64_t a_rows, const void* b, uint64_t b_rows, Args args, int grid,
                    cudaStream_t s) {
+  args.load_tiles = tls_load_tiles;
   CUtensorMap ma, mb, mo;
   if (!make_tma_2d_u8(&ma, a, a_rows, args.K, BM) || !make_tma_2d_u8(&mb, b, b_rows, args.K, BN == 256 ? 128 : BN))
     return cudaErrorInvalidValue;
@@ -507,6 +532,8 @@ cudaError_t launch(const void* a, uint64_t a_rows, const void* b, uint64_t b_row
 }
 
 }  // namespace
+
+void selftest_block_load_tiles(int tiles) { tls_load_tiles = tiles; }
 
 cudaError_t launch_block_matmul_tc(const uint8_t* a, const float* a_scale, int M, const uint8_t* b,
                                    const float* b_scale, int N, int K, uint16_t* out, int* status,

@@ -261,6 +261,9 @@ cudaError_t launch_block_experts_tc(const uint8_t* x_q, const float* x_scale, co
                                     const uint8_t* W1, const float* W1_scale, const uint8_t* W2,
                                     const float* W2_scale, uint8_t* h_q, float* h_scale, uint16_t* y,
                                     cudaStream_t s);
+// Self-test: this host thread's launches of these kernels load operands for
+// `tiles` tiles a CTA only.
+void selftest_block_load_tiles(int tiles);
 
 // AdamW over many tensors (adamw.cu), up to ADAMW_BATCH of them a launch.
 constexpr int ADAMW_BATCH = 96;

@@ -1,4 +1,4 @@
-// Self-test of the bounded device waits that every pipelined kernel here uses.
+// Self-tests of the bounded device waits that every pipelined kernel here uses.
 //
 // One CTA initialises an mbarrier that nothing will ever arrive on and waits
 // for it with the same helper the grouped GEMMs use, under a caller-chosen
@@ -48,5 +48,12 @@ extern "C" moe_status moe_selftest_wait_timeout(int32_t* status, int64_t limit_n
                                             reinterpret_cast<unsigned long long*>(waited_ns));
   const cudaError_t err = cudaGetLastError();
   if (err != cudaSuccess) return set_last_error(MOE_ERR_CUDA, cudaGetErrorString(err));
+  return MOE_OK;
+}
+
+extern "C" moe_status moe_selftest_block_product_tiles(int32_t tiles) {
+  if (tiles < -1)
+    return set_last_error(MOE_ERR_INVALID_ARG, "moe_selftest_block_product_tiles: tiles must be >= 0, or -1 for all");
+  selftest_block_load_tiles(tiles < 0 ? 0x7fffffff : tiles);
   return MOE_OK;
 }

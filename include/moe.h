@@ -675,7 +675,8 @@ MOE_API moe_status moe_quantize_fp8_block(const moe_bf16* src, int64_t batch, in
  *   a_q [M, K] uint8 and a_scale [M, ceil(K / 128)] (block_rows 1);
  *   b_q [N, K] uint8 and b_scale [ceil(N / 128), ceil(K / 128)] (block_rows
  *   128); out [M, N] bf16 (out); status [1] int32 device status word
- *   (nullable), receives MOE_DEVERR_TIMEOUT.
+ *   (nullable), receives MOE_DEVERR_TIMEOUT if a bounded wait runs out; the
+ *   elements that are not reached then are NaN.
  * M >= 0, N >= 1, K >= 16 a multiple of 16.  Up to 8 rows stream the
  * weights through registers; more run on the tensor cores in 128-row tiles.
  */
@@ -692,7 +693,8 @@ MOE_API moe_status moe_matmul_fp8_block(const uint8_t* a_q, const float* a_scale
  *   x_disp [C, H] bf16 (moe_dispatch's output); L its layout;
  *   W1_q [E, 2I, H] uint8, W1_scale [E, 2I/128, H/128], W2_q [E, H, I],
  *   W2_scale [E, H/128, I/128] (moe_quantize_fp8_block, block_rows 128);
- *   y_disp [C, H] bf16 (out): the valid rows are written.
+ *   y_disp [C, H] bf16 (out): the valid rows are written (those that depend on
+ *   a wait that ran out with NaN, and L->status gets MOE_DEVERR_TIMEOUT).
  *   workspace: moe_experts_fp8_block_workspace_bytes(C, T, E, H, I) bytes of
  *   device scratch, 16-byte aligned.
  * Inference only.  Shapes and errors as in moe_grouped_experts.  Nothing is
@@ -715,6 +717,16 @@ MOE_API moe_status moe_grouped_experts_fp8_block(const moe_bf16* x_disp, const m
  */
 MOE_API moe_status moe_selftest_wait_timeout(int32_t* status, int64_t limit_ns, uint64_t* waited_ns,
                                              moe_stream_t stream);
+
+/*
+ * Self-test of a block-scaled product whose operands stop arriving: until it
+ * is called again with -1, the tensor-core launches of the calling host thread
+ * (moe_matmul_fp8_block with more than 8 rows, moe_grouped_experts_fp8_block
+ * with more than 8 tokens) load operands for the first `tiles` tiles of each
+ * CTA only.  Their waits then run out after about 2 s, the status word gets
+ * MOE_DEVERR_TIMEOUT, and the outputs that were not reached are NaN.
+ */
+MOE_API moe_status moe_selftest_block_product_tiles(int32_t tiles);
 
 #ifdef __cplusplus
 }  /* extern "C" */
