@@ -445,37 +445,42 @@ def _(x_disp, W1_q, W1_scale, W2_q, W2_scale, lay, T, top_k, pad_multiple):
 
 
 def moe_layer_fp8_block(x: Tensor, topk_idx: Tensor, topk_probs: Tensor, W1_q: Tensor, W1_scale: Tensor, W2_q: Tensor,
-                        W2_scale: Tensor, pad_multiple: int = 1) -> Tensor:
+                        W2_scale: Tensor, pad_multiple: int = 1, return_status: bool = False):
     """The layer for inference from weights with 128 x 128 block scales
     (quantize_fp8_block of W1 and W2, block_rows 128): multihot, dispatch,
-    experts with both products in e4m3, combine."""
+    experts with both products in e4m3, combine.  Returns out, or with
+    ``return_status`` (out, status) as moe_layer does."""
     T, K = topk_idx.shape
     E = W1_q.shape[0]
     rmap, probs, _, status = _ops.route_to_multihot(topk_idx, topk_probs, E)
     x_disp, *lay = _ops.dispatch(x, rmap, probs, status, K, pad_multiple)
     y = _ops.grouped_experts_fp8_block(x_disp, W1_q, W1_scale, W2_q, W2_scale, lay, T, K, pad_multiple)
-    return _ops.combine(y, lay, T, K, pad_multiple, E)
+    out = _ops.combine(y, lay, T, K, pad_multiple, E)
+    return (out, lay[-1]) if return_status else out
 
 
 def moe_block(x: Tensor, normed: Tensor, router: Tensor, top_k: int, W1: Tensor, W2: Tensor, norm_out_weight: Tensor,
               gate: Optional[Tensor] = None, next_weight: Optional[Tensor] = None, residual_scale: float = 1.0,
-              pad_multiple: int = 1, eps: float = 1e-6, fp8: Optional[Tuple[Tensor, Tensor]] = None):
+              pad_multiple: int = 1, eps: float = 1e-6, fp8: Optional[Tuple[Tensor, Tensor]] = None,
+              return_status: bool = False):
     """A MoE block between two norms: from the residual stream x and its norm
     (``norm_in``, or the block before's ``next``), the router's logits
     ``normed @ router^T``, the layer, and ``norm_out``.  Returns (out, next), next
-    being None without ``next_weight``.
+    being None without ``next_weight``, and with ``return_status`` the layer's
+    status as a third.
 
     Differentiable in everything but the top-k choice.  With ``fp8`` = (W1_scale,
     W2_scale), W1 and W2 are e4m3 codes with block scales and the layer runs for
     inference."""
     logits = (normed.float() @ router.float().t()).contiguous()
     if fp8 is None:
-        y = moe_layer_from_logits(normed, logits, top_k, W1, W2, pad_multiple)
+        y, status = moe_layer_from_logits(normed, logits, top_k, W1, W2, pad_multiple, return_status=True)
     else:
         idx, p = _ops.router_topk(logits, top_k)
-        y = moe_layer_fp8_block(normed, idx, p, W1, fp8[0], W2, fp8[1], pad_multiple)
+        y, status = moe_layer_fp8_block(normed, idx, p, W1, fp8[0], W2, fp8[1], pad_multiple, return_status=True)
     out, nxt, _, _ = _ops.norm_out(x, y, norm_out_weight, gate, next_weight, residual_scale, True, eps, 0.0)
-    return out, (nxt if next_weight is not None else None)
+    nxt = nxt if next_weight is not None else None
+    return (out, nxt, status) if return_status else (out, nxt)
 
 
 def moe_layer_from_logits(x: Tensor, router_logits: Tensor, top_k: int, W1: Tensor, W2: Tensor,

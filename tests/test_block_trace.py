@@ -128,3 +128,16 @@ def test_fp8_block_validation():
     L = N.MoeLayout(4, 8, 2, 1, 8)
     assert N.lib.moe_grouped_experts_fp8_block(OK, ctypes.byref(L), 256, 128, OK, OK, OK, OK, OK, OK, None) == \
         N.MOE_ERR_INVALID_ARG                                            # the layout's pointers are NULL
+
+
+def test_status_is_returned_on_request():
+    t = _inputs("meta", grad=False)
+    assert len(_block(t)) == 2
+    out, nxt, status = _block(t, return_status=True)
+    assert out.shape == nxt.shape == (T, H) and status.shape == (1,) and status.dtype == torch.int32
+    u8 = lambda s: torch.zeros(s, dtype=torch.uint8, device="meta")  # noqa: E731
+    q1, q2, s1, s2 = u8(t["W1"].shape), u8(t["W2"].shape), torch.zeros(E, 2, 2, device="meta"), torch.zeros(E, 2, 1, device="meta")
+    idx, p = torch.zeros(T, K, dtype=torch.int64, device="meta"), torch.zeros(T, K, device="meta")
+    assert torch.is_tensor(ops.moe_layer_fp8_block(t["x"], idx, p, q1, s1, q2, s2))
+    out, status = ops.moe_layer_fp8_block(t["x"], idx, p, q1, s1, q2, s2, return_status=True)
+    assert out.shape == (T, H) and status.shape == (1,) and status.dtype == torch.int32

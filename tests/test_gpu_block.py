@@ -105,3 +105,27 @@ def test_example(moe, bits):
     losses, fp8, one = ex.main(["--state-bits", bits, "--steps", "12"])
     assert all(b < a for a, b in zip(losses, losses[4:])) and losses[-1] < 0.9 * losses[0]
     assert fp8 < 0.05 and one < 0.02
+
+
+def test_fp8_block_status(moe):
+    """An expert index out of range, and a wait that runs out, reach the caller
+    of the inference layer through its status."""
+    T, H, E, K, I = 16, 256, 4, 2, 128
+    g = torch.Generator().manual_seed(6)
+    x = torch.randn(T, H, generator=g).bfloat16().to(DEV)
+    q1, s1 = moe.moe_quantize_fp8_block(torch.randn(E, 2 * I, H, generator=g).bfloat16().to(DEV), 128)
+    q2, s2 = moe.moe_quantize_fp8_block(torch.randn(E, H, I, generator=g).bfloat16().to(DEV), 128)
+    idx = torch.stack([torch.randperm(E, generator=g)[:K] for _ in range(T)]).to(DEV)
+    p = torch.rand(T, K, generator=g).to(DEV)
+    call = lambda: moe.moe_layer_fp8_block(x, idx, p, q1, s1, q2, s2, return_status=True)  # noqa: E731
+    out, status = call()
+    assert int(status) == 0 and torch.equal(out, moe.moe_layer_fp8_block(x, idx, p, q1, s1, q2, s2))
+    idx[3, 1] = E
+    assert int(call()[1]) == 1
+    idx[3, 1] = -1
+    try:
+        moe._native.lib.moe_selftest_block_product_tiles(0)
+        out, status = call()
+    finally:
+        moe._native.lib.moe_selftest_block_product_tiles(-1)
+    assert int(status) == moe._native.MOE_DEVERR_TIMEOUT and out.isnan().all()
