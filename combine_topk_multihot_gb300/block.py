@@ -11,7 +11,8 @@
 As in ``moe.py`` the functions carry the names of the C entry points, all
 arithmetic runs in the CUDA library, and PyTorch only allocates the buffers and
 supplies the current stream.  Tensors are packed and on the GPU; anything
-else is refused before a kernel is launched.
+else is refused before a kernel is launched.  (Norm weights cut from a larger
+buffer at any element are copied first, where the kernel wants whole vectors.)
 """
 from __future__ import annotations
 
@@ -69,6 +70,14 @@ def _need(t: torch.Tensor, name: str, dtype, shape, device):
     raise ValueError(f"{name} must be contiguous")
 
 
+def _vectors(w: Optional[torch.Tensor], stream):
+    """A norm's weights at an address that rows of a multiple of 8 values allow: as they are, or a copy."""
+    if w is None or w.data_ptr() % 16 == 0 or w.numel() % 8 or not w.is_contiguous() or not w.is_cuda:
+        return w
+    with torch.cuda.stream(stream):
+        return w.detach().clone()
+
+
 def _on_gpu(t: torch.Tensor, name: str) -> torch.device:
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU (got {t.device}): there is no CPU kernel")
@@ -118,6 +127,7 @@ def moe_norm_in(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, weight
     None).  ``save_rstd`` keeps what moe_norm_in_backward needs."""
     T, H = _rows(x, "x")
     dev = _on_gpu(x, "x")
+    weight = _vectors(weight, stream)
     n = _norm(T, H, x, weight, None, False, 1.0, eps, weight_offset)
     if out is None:
         out = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
@@ -135,6 +145,7 @@ def moe_norm_in_backward(grad_norm: torch.Tensor, x: torch.Tensor, weight: torch
     is the gradient that reaches x past the block; it is added to grad_x."""
     T, H = _rows(x, "x")
     dev = _on_gpu(x, "x")
+    weight = _vectors(weight, stream)
     n = _norm(T, H, x, weight, None, False, 1.0, 0.0, weight_offset)
     grad_x = torch.empty(T, H, dtype=x.dtype, device=dev)
     grad_w = torch.empty(H, dtype=torch.float32, device=dev)
@@ -157,6 +168,7 @@ def moe_norm_out(x: torch.Tensor, y: torch.Tensor, weight: torch.Tensor, gate: O
     next_rstd or None), next being the next block's norm of out."""
     T, H = _rows(x, "x")
     dev = _on_gpu(x, "x")
+    weight, next_weight = _vectors(weight, stream), _vectors(next_weight, stream)
     n = _norm(T, H, x, weight, gate, gate_sigmoid, residual_scale, eps, weight_offset, next_weight)
     out = torch.empty(T, H, dtype=x.dtype, device=dev)
     rstd = torch.empty(T, dtype=torch.float32, device=dev) if save_rstd else None
@@ -191,6 +203,7 @@ def moe_norm_out_backward(grad_out: Optional[torch.Tensor], y: torch.Tensor, wei
     if grad_out is None and not has_next:
         raise ValueError("grad_out may be None only with a next norm")
     stream_like = grad_out if grad_out is not None else out
+    weight, next_weight = _vectors(weight, stream), _vectors(next_weight, stream)
     n = _norm(T, H, stream_like, weight, gate, gate_sigmoid, residual_scale, 0.0, weight_offset, next_weight)
     xt = stream_like.dtype
     grad_x = torch.empty(T, H, dtype=xt, device=dev)

@@ -671,9 +671,21 @@ moe_status check_norm(const char* who, const moe_norm* n) {
   return MOE_OK;
 }
 
+bool aligned_to(const void* p, uintptr_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
 template <typename... P>
-bool all_aligned16(P... p) {
-  return (aligned16(p) && ...);
+bool all_aligned(uintptr_t bytes, P... p) {
+  return (aligned_to(p, bytes) && ...);
+}
+
+uintptr_t bytes_of(int32_t dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
+
+// Rows of a multiple of 8 values are read in pieces of 16 bytes, others value by value.
+uintptr_t row_bytes(const moe_norm* n, int32_t dtype) { return n->H % 8 == 0 ? 16 : bytes_of(dtype); }
+
+// A gate of one value a token is read value by value.
+uintptr_t gate_bytes(const moe_norm* n) {
+  return n->gate_kind == MOE_GATE_ELEMENT ? row_bytes(n, n->gate_dtype) : bytes_of(n->gate_dtype);
 }
 
 NormArgs norm_args(const moe_norm* n) {
@@ -714,8 +726,10 @@ moe_status moe_norm_in(const moe_norm* n, const void* x, const void* weight, moe
   moe_status st = check_norm("moe_norm_in", n);
   if (st != MOE_OK) return st;
   MOE_REQUIRE(n->T == 0 || (x && weight && norm), MOE_ERR_INVALID_ARG, "moe_norm_in: NULL pointer");
-  MOE_REQUIRE(all_aligned16(x, weight, norm, rstd), MOE_ERR_INVALID_ARG,
-              "moe_norm_in: pointers must be 16-byte aligned");
+  MOE_REQUIRE(all_aligned(row_bytes(n, n->x_dtype), x) && all_aligned(row_bytes(n, n->weight_dtype), weight) &&
+                  all_aligned(row_bytes(n, MOE_DTYPE_BF16), norm) && all_aligned(4, rstd),
+              MOE_ERR_INVALID_ARG,
+              "moe_norm_in: rows and weights must be 16-byte aligned (H % 8 == 0), others by their type");
   if ((st = check_device()) != MOE_OK) return st;
   NormArgs a = norm_args(n);
   a.gate_kind = MOE_GATE_NONE;
@@ -741,8 +755,12 @@ moe_status moe_norm_in_backward(const moe_norm* n, const moe_bf16* grad_norm, co
   if (st != MOE_OK) return st;
   MOE_REQUIRE(grad_weight && (n->T == 0 || (grad_norm && x && weight && rstd && grad_x && workspace)),
               MOE_ERR_INVALID_ARG, "moe_norm_in_backward: NULL pointer");
-  MOE_REQUIRE(all_aligned16(grad_norm, x, weight, rstd, grad_res, grad_x, grad_weight, workspace),
-              MOE_ERR_INVALID_ARG, "moe_norm_in_backward: pointers must be 16-byte aligned");
+  MOE_REQUIRE(all_aligned(row_bytes(n, MOE_DTYPE_BF16), grad_norm) &&
+                  all_aligned(row_bytes(n, n->x_dtype), x, grad_res, grad_x) &&
+                  all_aligned(row_bytes(n, n->weight_dtype), weight) &&
+                  all_aligned(row_bytes(n, MOE_DTYPE_F32), grad_weight) && all_aligned(4, rstd) && aligned16(workspace),
+              MOE_ERR_INVALID_ARG,
+              "moe_norm_in_backward: rows and weights must be 16-byte aligned (H % 8 == 0), others by their type");
   if ((st = check_device()) != MOE_OK) return st;
   NormBackwardArgs a = norm_backward_args(n);
   a.gate_kind = MOE_GATE_NONE;
@@ -770,8 +788,11 @@ moe_status moe_norm_out(const moe_norm* n, const void* x, const moe_bf16* y, con
   MOE_REQUIRE((next_weight != nullptr) == (next != nullptr) || n->T == 0, MOE_ERR_INVALID_ARG,
               "moe_norm_out: give next_weight and next, or neither");
   MOE_REQUIRE(next_weight || !next_rstd, MOE_ERR_INVALID_ARG, "moe_norm_out: next_rstd without next_weight");
-  MOE_REQUIRE(all_aligned16(x, y, weight, gate, out, rstd, next_weight, next, next_rstd), MOE_ERR_INVALID_ARG,
-              "moe_norm_out: pointers must be 16-byte aligned");
+  MOE_REQUIRE(all_aligned(row_bytes(n, n->x_dtype), x, out) && all_aligned(row_bytes(n, MOE_DTYPE_BF16), y, next) &&
+                  all_aligned(row_bytes(n, n->weight_dtype), weight, next_weight) && all_aligned(gate_bytes(n), gate) &&
+                  all_aligned(4, rstd, next_rstd),
+              MOE_ERR_INVALID_ARG,
+              "moe_norm_out: rows and weights must be 16-byte aligned (H % 8 == 0), others by their type");
   if ((st = check_device()) != MOE_OK) return st;
   NormArgs a = norm_args(n);
   a.x = x;
@@ -805,9 +826,13 @@ moe_status moe_norm_out_backward(const moe_norm* n, const void* grad_out, const 
               "moe_norm_out_backward: give grad_next, out, next_weight, next_rstd and grad_next_weight, or none");
   MOE_REQUIRE((n->gate_kind == MOE_GATE_NONE) ? (!gate && !grad_gate) : (gate || n->T == 0), MOE_ERR_INVALID_ARG,
               "moe_norm_out_backward: give gate exactly when gate_kind is not MOE_GATE_NONE");
-  MOE_REQUIRE(all_aligned16(grad_out, grad_next, out, y, weight, gate, rstd, next_weight, next_rstd, grad_x, grad_y,
-                            grad_gate, grad_weight, grad_next_weight, workspace),
-              MOE_ERR_INVALID_ARG, "moe_norm_out_backward: pointers must be 16-byte aligned");
+  MOE_REQUIRE(all_aligned(row_bytes(n, n->x_dtype), grad_out, out, grad_x) &&
+                  all_aligned(row_bytes(n, MOE_DTYPE_BF16), grad_next, y, grad_y) &&
+                  all_aligned(row_bytes(n, n->weight_dtype), weight, next_weight) &&
+                  all_aligned(row_bytes(n, MOE_DTYPE_F32), grad_weight, grad_next_weight) &&
+                  all_aligned(gate_bytes(n), gate, grad_gate) && all_aligned(4, rstd, next_rstd) && aligned16(workspace),
+              MOE_ERR_INVALID_ARG,
+              "moe_norm_out_backward: rows and weights must be 16-byte aligned (H % 8 == 0), others by their type");
   if ((st = check_device()) != MOE_OK) return st;
   NormBackwardArgs a = norm_backward_args(n);
   a.has_y = 1;
@@ -832,12 +857,6 @@ moe_status moe_norm_out_backward(const moe_norm* n, const void* grad_out, const 
 }
 
 }  // extern "C"
-
-namespace {
-
-bool aligned_to(const void* p, uintptr_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
-
-}  // namespace
 
 extern "C" {
 
@@ -961,8 +980,8 @@ moe_status moe_quantize_fp8_block(const moe_bf16* src, int64_t batch, int64_t ro
               MOE_ERR_UNSUPPORTED_SHAPE, "moe_quantize_fp8_block: 2^31 blocks or more");
   MOE_REQUIRE(batch == 0 || rows == 0 || (src && codes && scales), MOE_ERR_INVALID_ARG,
               "moe_quantize_fp8_block: NULL pointer");
-  MOE_REQUIRE(all_aligned16(src, codes, scales), MOE_ERR_INVALID_ARG,
-              "moe_quantize_fp8_block: pointers must be 16-byte aligned");
+  MOE_REQUIRE(aligned16(src) && aligned16(codes) && aligned_to(scales, 4), MOE_ERR_INVALID_ARG,
+              "moe_quantize_fp8_block: src and codes must be 16-byte aligned, scales by their type");
   moe_status st = check_device();
   if (st != MOE_OK) return st;
   cudaError_t err = launch_quantize_block(src, batch, rows, cols, block_rows, codes, scales, nullptr, stream);
@@ -978,8 +997,9 @@ moe_status moe_matmul_fp8_block(const uint8_t* a_q, const float* a_scale, int32_
               "moe_matmul_fp8_block: K must be a positive multiple of 16 (got %d)", K);
   MOE_REQUIRE(M == 0 || (a_q && a_scale && b_q && b_scale && out), MOE_ERR_INVALID_ARG,
               "moe_matmul_fp8_block: NULL pointer");
-  MOE_REQUIRE(all_aligned16(a_q, a_scale, b_q, b_scale, out), MOE_ERR_INVALID_ARG,
-              "moe_matmul_fp8_block: pointers must be 16-byte aligned");
+  MOE_REQUIRE(aligned16(a_q) && aligned16(b_q) && all_aligned(4, a_scale, b_scale) && aligned_to(out, N % 8 == 0 ? 16 : 2),
+              MOE_ERR_INVALID_ARG,
+              "moe_matmul_fp8_block: codes and (N % 8 == 0) out must be 16-byte aligned, others by their type");
   MOE_REQUIRE((static_cast<int64_t>(M) + 127) / 128 * ((N + 63) / 64) < (int64_t(1) << 31), MOE_ERR_UNSUPPORTED_SHAPE,
               "moe_matmul_fp8_block: too many tiles");
   moe_status st = check_device();
@@ -1010,8 +1030,9 @@ moe_status moe_grouped_experts_fp8_block(const moe_bf16* x_disp, const moe_layou
               "the intermediate size must be a positive multiple of 128 (got %d)", I);
   MOE_REQUIRE(L->capacity == 0 || (x_disp && W1_q && W1_scale && W2_q && W2_scale && y_disp && workspace),
               MOE_ERR_INVALID_ARG, "moe_grouped_experts_fp8_block: NULL pointer");
-  MOE_REQUIRE(all_aligned16(x_disp, W1_q, W1_scale, W2_q, W2_scale, y_disp, workspace), MOE_ERR_INVALID_ARG,
-              "moe_grouped_experts_fp8_block: pointers must be 16-byte aligned");
+  MOE_REQUIRE(all_aligned(16, x_disp, W1_q, W2_q, y_disp, workspace) && all_aligned(4, W1_scale, W2_scale),
+              MOE_ERR_INVALID_ARG,
+              "moe_grouped_experts_fp8_block: rows and codes must be 16-byte aligned, scales by their type");
   if ((st = check_device()) != MOE_OK) return st;
   if (L->capacity == 0 || L->T == 0) return MOE_OK;
   const bool stream_form = experts_stream(L->T, L->E, H, I);

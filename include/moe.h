@@ -522,7 +522,11 @@ typedef enum moe_gate_kind { MOE_GATE_NONE = 0, MOE_GATE_TOKEN = 1, MOE_GATE_ELE
 
 /*
  * Sizes, types and constants of a norm call.  T >= 0 rows of 1 <= H <= 16384
- * values, any H (a multiple of 8 is faster); rows are packed.
+ * values, any H (a multiple of 8 is faster); rows are packed.  With H a
+ * multiple of 8 the tensors of T rows and the weights and their gradients are
+ * 16-byte aligned; with another H, and for what has one value a row (rstd, a
+ * gate of one value a token), any address that suits the element type will do.
+ * Workspaces are 16-byte aligned.
  */
 typedef struct moe_norm {
   int64_t T;
@@ -663,6 +667,7 @@ MOE_API moe_status moe_adamw_step(const moe_adamw* h, const moe_adamw_tensor* te
  *   src [batch, rows, cols] bf16, each matrix with its own blocks; cols a
  *   multiple of 16; codes [batch, rows, cols] uint8 (out);
  *   scales [batch, ceil(rows / block_rows), ceil(cols / 128)] fp32 (out).
+ * src and codes are 16-byte aligned; scales, here and below, need not be.
  */
 MOE_API moe_status moe_quantize_fp8_block(const moe_bf16* src, int64_t batch, int64_t rows, int32_t cols,
                                           int32_t block_rows, uint8_t* codes, float* scales,
@@ -677,7 +682,8 @@ MOE_API moe_status moe_quantize_fp8_block(const moe_bf16* src, int64_t batch, in
  *   128); out [M, N] bf16 (out); status [1] int32 device status word
  *   (nullable), receives MOE_DEVERR_TIMEOUT if a bounded wait runs out; the
  *   elements that are not reached then are NaN.
- * M >= 0, N >= 1, K >= 16 a multiple of 16.  Up to 8 rows stream the
+ * M >= 0, N >= 1, K >= 16 a multiple of 16.  Codes are 16-byte aligned, and so
+ * is out when N is a multiple of 8.  Up to 8 rows stream the
  * weights through registers; more run on the tensor cores in 128-row tiles.
  */
 MOE_API moe_status moe_matmul_fp8_block(const uint8_t* a_q, const float* a_scale, int32_t M,

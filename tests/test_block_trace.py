@@ -141,3 +141,27 @@ def test_status_is_returned_on_request():
     assert torch.is_tensor(ops.moe_layer_fp8_block(t["x"], idx, p, q1, s1, q2, s2))
     out, status = ops.moe_layer_fp8_block(t["x"], idx, p, q1, s1, q2, s2, return_status=True)
     assert out.shape == (T, H) and status.shape == (1,) and status.dtype == torch.int32
+
+
+def test_alignment_by_what_is_read():
+    """What a kernel reads value by value needs no more than its type's alignment;
+    validation alone: without a GPU what passes it ends with a device error."""
+    if torch.cuda.is_available():
+        pytest.skip("the pointers are not real: nothing may be launched")
+    refused, two = N.MOE_ERR_INVALID_ARG, P(256 + 2)
+    x8, x7 = _norm(H=64), _norm(H=63)
+    norm_in = lambda n, x, w, o, r: N.lib.moe_norm_in(n, x, w, o, r, None)  # noqa: E731
+    assert norm_in(x8, OK, OK, OK, ODD) != refused and norm_in(x8, OK, OK, OK, two) == refused
+    for at in range(3):
+        ptrs = [OK, OK, OK]
+        ptrs[at] = ODD
+        assert norm_in(x8, *ptrs, None) == refused and norm_in(x7, *ptrs, None) != refused
+    assert norm_in(x7, OK, two, OK, None) == refused            # fp32 weights
+    out = lambda n, gate: N.lib.moe_norm_out(n, OK, OK, OK, gate, OK, None, None, None, None, None)  # noqa: E731
+    assert out(_norm(gate_kind=1), ODD) != refused and out(_norm(gate_kind=1), two) == refused
+    assert out(_norm(gate_kind=1, gate_dtype=0), two) != refused
+    assert out(_norm(gate_kind=2), ODD) == refused and out(_norm(gate_kind=2, H=63), ODD) != refused
+    mm = lambda n, sa, sb, o: N.lib.moe_matmul_fp8_block(OK, sa, 4, OK, sb, n, 128, o, None, None)  # noqa: E731
+    assert mm(8, ODD, ODD, OK) != refused and mm(8, two, OK, OK) == refused
+    assert mm(8, OK, OK, two) == refused and mm(9, OK, OK, two) != refused
+    assert N.lib.moe_quantize_fp8_block(OK, 1, 4, 128, 1, OK, ODD, None) != refused
