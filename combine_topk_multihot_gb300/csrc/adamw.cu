@@ -213,7 +213,8 @@ __device__ __forceinline__ void update_block(const AdamWTensor& T, const Step& s
       const float gk = g[h][k] * st.grad_scale;
       m[h][k] = __fadd_rn(__fmul_rn(m[h][k], st.b1), __fmul_rn(gk, st.c1));
       v[h][k] = __fadd_rn(__fmul_rn(v[h][k], st.b2), __fmul_rn(__fmul_rn(gk, gk), st.c2));
-      // the divisor is below 2^65: __fdividef's range is not left
+      // sqrt(v) < 2^64, root_bc2 < 2^27 (1 - b2^t >= 2^-53) and eps < 1e30 (else
+      // refused): the divisor is below 2^101, and __fdividef's range, 2^126, is not left
       float root;
       asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(v[h][k]));
       const float q = __fdividef(m[h][k], root * st.root_bc2 + st.eps);

@@ -869,8 +869,9 @@ moe_status moe_adamw_step(const moe_adamw* h, const moe_adamw_tensor* tensors, i
               static_cast<long long>(h->step));
   MOE_REQUIRE(h->beta1 >= 0 && h->beta1 < 1 && h->beta2 >= 0 && h->beta2 < 1, MOE_ERR_INVALID_ARG,
               "moe_adamw_step: betas must be in [0, 1)");
-  MOE_REQUIRE(std::isfinite(h->lr) && h->lr >= 0 && std::isfinite(h->eps) && h->eps >= 0, MOE_ERR_INVALID_ARG,
-              "moe_adamw_step: lr and eps must be finite and >= 0");
+  // (below 1e30: what the update divides by stays in its division's range)
+  MOE_REQUIRE(std::isfinite(h->lr) && h->lr >= 0 && h->eps >= 0 && h->eps < 1e30, MOE_ERR_INVALID_ARG,
+              "moe_adamw_step: lr must be finite and >= 0, eps in [0, 1e30)");
   MOE_REQUIRE(aligned_to(h->grad_scale, 4) && aligned_to(h->skip, 4) && aligned_to(h->step_dev, 8),
               MOE_ERR_INVALID_ARG, "moe_adamw_step: misaligned grad_scale, skip or step_dev");
   const bool eight = h->state_bits == 8;

@@ -649,7 +649,8 @@ typedef struct moe_adamw {
  * element's p, m and v non-finite, and with 8-bit states its block's: use
  * `skip`.  Errors: MOE_ERR_INVALID_ARG for NULL or misaligned pointers, an
  * unknown type, a master beside an fp32 param, state_bits not 8 or 32, step <
- * 1, a beta outside [0, 1), a negative or non-finite lr, eps or weight_decay;
+ * 1, a beta outside [0, 1), a negative or non-finite lr or weight_decay, an
+ * eps outside [0, 1e30);
  * MOE_ERR_UNSUPPORTED_SHAPE for 2^31 blocks of 256 elements or more in 96
  * tensors.  Nothing is written when arguments are refused.
  */

@@ -165,3 +165,15 @@ def test_alignment_by_what_is_read():
     assert mm(8, ODD, ODD, OK) != refused and mm(8, two, OK, OK) == refused
     assert mm(8, OK, OK, two) == refused and mm(9, OK, OK, two) != refused
     assert N.lib.moe_quantize_fp8_block(OK, 1, 4, 128, 1, OK, ODD, None) != refused
+
+
+def test_adamw_divisor_stays_in_range():
+    """An eps for which the update's fast division would leave its range is refused."""
+    def call(eps):
+        h = N.MoeAdamw(1e-3, 0.9, 0.99, eps, 1, 0, 32, None, None, None)
+        return N.lib.moe_adamw_step(h, None, 0, None)
+
+    for eps in (1e30, 1e38, float("inf"), float("nan"), -1e-8):
+        assert call(eps) == N.MOE_ERR_INVALID_ARG
+        assert "eps" in N.last_error()
+    assert call(9e29) != N.MOE_ERR_INVALID_ARG      # (without a GPU: a device error)
