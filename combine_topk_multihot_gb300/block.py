@@ -339,6 +339,8 @@ def moe_adamw_step(state: AdamWState, grads: Sequence[Optional[torch.Tensor]], l
         # only the addresses change in most steps
         if not isinstance(weight_decay, (int, float)):
             weight_decay = [float(d) for d in weight_decay]
+            if len(weight_decay) != len(params):
+                raise ValueError(f"{len(weight_decay)} weight decays for {len(params)} parameters")
         settings = (dtypes, weight_decay)
         if settings != state._settings:
             state._settings = None

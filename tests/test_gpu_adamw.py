@@ -419,3 +419,15 @@ def test_8bit_nonfinite_after_the_first_steps(moe, b1):
     codes = opt.exp_avg[0].view(torch.float8_e4m3fn).float()
     assert codes[300].isnan() and codes[700].isnan() and torch.isfinite(codes[:256]).all()
     assert not torch.isfinite(opt.exp_avg_scale[0][1:3]).any() and torch.isfinite(opt.exp_avg_scale[0][[0, 3]]).all()
+
+
+def test_one_decay_in_a_list_is_not_for_all(moe):
+    """A list has one weight decay per parameter; a list of one is refused for
+    two (numpy would have spread it)."""
+    p = [torch.ones(8, device=DEV) for _ in range(2)]
+    opt = moe.AdamWState(p)
+    with pytest.raises(ValueError, match="1 weight decays for 2"):
+        moe.moe_adamw_step(opt, p, 1e-2, weight_decay=[0.1])
+    assert opt.step == 0
+    moe.moe_adamw_step(opt, [torch.zeros(8, device=DEV)] * 2, 1e-2, weight_decay=[0.0, 0.5])
+    assert (p[0] == 1).all() and (p[1] < 1).all()
