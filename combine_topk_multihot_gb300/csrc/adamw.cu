@@ -26,9 +26,10 @@
 //
 // The averages are computed with one rounding per operation (no fused
 // multiply-add): what goes into the codes is then the same in any
-// implementation that does the operations one by one.  The quotient of the
-// update may be off by a few units of 2^-23: it is multiplied by lr and added
-// to p, whose own rounding is coarser by 1 / lr.
+// implementation that does the operations one by one.  The root and the quotient of the
+// update may be off by a few units of 2^-23: they are multiplied by lr and added
+// to p, whose own rounding is coarser by 1 / lr.  (Rounded ones take 293 us for 266
+// with 8-bit averages, 389 for 375 with fp32 ones: 100 M bf16 parameters, fp32 gradients.)
 //
 // Bound by HBM: with bf16 parameters, fp32 masters and fp32 gradients 30 bytes
 // an element with fp32 averages, 18 with 8-bit ones.  A warp takes a block of

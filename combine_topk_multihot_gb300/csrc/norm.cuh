@@ -200,7 +200,12 @@ __device__ __forceinline__ void group_sum(float (&v)[N], float (*red)[MAX_WARPS]
 
 // The gate's factor s and ds/dg.  From e = exp(-|g|), which cannot overflow:
 // s = 1 / (1 + e) or e / (1 + e), and ds/dg = e / (1 + e)^2 on both sides,
-// without the cancellation of 1 - s where s is near 1.
+// without the cancellation of 1 - s where s is near 1.  The fast exponential
+// is off by up to 2 + 1.2 |g| ulp, so s by 2^-18 of itself at |g| = 16 at the
+// worst, and less where s is near 1: below half a bf16 ulp by far, and of an fp32
+// stream it is one term.  (With expf and a rounded reciprocal a gate per
+// element costs half as much time again: 16384 x 2048, bf16, backward 131 us for 86,
+// forward 70 for 49.)
 struct Gate {
   float s, slope;
 };

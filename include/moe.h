@@ -676,8 +676,8 @@ MOE_API moe_status moe_quantize_fp8_block(const moe_bf16* src, int64_t batch, in
 
 /*
  * out[m, n] = bf16(sum_kb a_scale[m, kb] b_scale[n / 128, kb] sum_{k in block kb} a[m, k] b[n, k]):
- * products of codes, exact, summed in fp32 within a block; the blocks scaled
- * and added in fp32.
+ * products of codes are exact and summed in fp32 within a block; the blocks
+ * are scaled and added in fp32.
  *   a_q [M, K] uint8 and a_scale [M, ceil(K / 128)] (block_rows 1);
  *   b_q [N, K] uint8 and b_scale [ceil(N / 128), ceil(K / 128)] (block_rows
  *   128); out [M, N] bf16 (out); status [1] int32 device status word
@@ -695,7 +695,8 @@ MOE_API moe_status moe_matmul_fp8_block(const uint8_t* a_q, const float* a_scale
  * The grouped SwiGLU experts from weights with 128 x 128 block scales, both
  * products in e4m3:
  *   q(x) = e4m3 codes of x_disp, a scale per row and 128 columns;
- *   h = silu(q(x) Wg^T) * (q(x) Wu^T) in fp32, q(h) likewise;
+ *   h = silu(q(x) Wg^T) * (q(x) Wu^T) in fp32 (fast exponential and quotient),
+ *   q(h) likewise, v / scale as a product with the scale's reciprocal;
  *   y_disp[r] = bf16(w_r (q(h) W2^T)).
  *   x_disp [C, H] bf16 (moe_dispatch's output); L its layout;
  *   W1_q [E, 2I, H] uint8, W1_scale [E, 2I/128, H/128], W2_q [E, H, I],
