@@ -129,3 +129,19 @@ def test_fp8_block_status(moe):
     finally:
         moe._native.lib.moe_selftest_block_product_tiles(-1)
     assert int(status) == moe._native.MOE_DEVERR_TIMEOUT and out.isnan().all()
+
+
+def test_opcheck_dynamic(moe):
+    """The operators under AOT dispatch with symbolic sizes, gradients among them."""
+    g = torch.Generator().manual_seed(8)
+    rnd = lambda *s: torch.randn(*s, generator=g).to(DEV)  # noqa: E731
+    ns, tests = torch.ops.moe_gb300, ("test_aot_dispatch_dynamic",)
+    x, y, w = rnd(9, 256).bfloat16().requires_grad_(), rnd(9, 256).bfloat16().requires_grad_(), rnd(256).requires_grad_()
+    torch.library.opcheck(ns.norm_in.default, (x, w, 1e-6, 0.0), test_utils=tests)
+    for gate in (None, rnd(9).requires_grad_(), rnd(9, 256).requires_grad_()):
+        for w2 in (None, rnd(256).requires_grad_()):
+            torch.library.opcheck(ns.norm_out.default, (x, y, w, gate, w2, 0.5, True, 1e-6, 0.0), test_utils=tests)
+    codes, scales = ns.quantize_fp8_block(y.detach(), 1)
+    torch.library.opcheck(ns.quantize_fp8_block.default, (y.detach(), 128), test_utils=tests)
+    bq, bs = ns.quantize_fp8_block(rnd(40, 256).bfloat16(), 128)
+    torch.library.opcheck(ns.matmul_fp8_block.default, (codes, scales, bq, bs), test_utils=tests)

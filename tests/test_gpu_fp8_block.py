@@ -234,3 +234,19 @@ def test_refusals(moe):
         moe.moe_grouped_experts_fp8_block(xd, L, w1, s1, w2, s1)
     empty = moe.moe_matmul_fp8_block(aq[:0], sa[:0], bq, sb)
     assert empty.shape == (0, 128)
+
+
+@pytest.mark.parametrize("N,K", [(100, 128), (1027, 2064), (4096, 512)])
+def test_few_rows_as_among_many(moe, N, K):
+    """A row's product is the same, to its rounding, whether it comes alone (the
+    weight stream), among 8, or in a tile of 128: each is within the bound
+    above of fp64, so two are within twice that."""
+    g = torch.Generator().manual_seed(N)
+    aq, sa = moe.moe_quantize_fp8_block(torch.randn(130, K, generator=g).bfloat16().to(DEV))
+    bq, sb = moe.moe_quantize_fp8_block(torch.randn(N, K, generator=g).bfloat16().to(DEV), 128)
+    whole = moe.moe_matmul_fp8_block(aq, sa, bq, sb)
+    mag = _values(aq, sa, 1).abs() @ _values(bq, sb, 128).abs().T
+    for m in (1, 2, 7, 8, 9, 16, 64, 128):
+        part = moe.moe_matmul_fp8_block(aq[:m], sa[:m], bq, sb)
+        tol = 2 * ((2.0 ** -13 + 2.0 ** -16) * mag[:m] + 2.0 ** -8 * (1 + 2.0 ** -8) * whole[:m].double().abs() * (1 + 2.0 ** -7))
+        assert ((part.double() - whole[:m].double()).abs() <= tol).all(), m

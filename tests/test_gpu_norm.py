@@ -305,3 +305,43 @@ def test_one_warp_a_row(moe, H):
     for _ in range(5):
         for a, b in zip(grads, moe.moe_norm_out_backward(x, y, w, first[1], **back)):
             assert (a is None and b is None) or torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T,H", [(7, 96), (5, 33), (1300, 1024), (2000, 2048), (640, 5000), (650, 8192), (640, 8199), (600, 16384)])
+@pytest.mark.parametrize("xt,wt,gt", [(BF16, BF16, F32), (F32, BF16, F32), (F32, F32, BF16)])
+@pytest.mark.parametrize("gate_kind", ["token", "element"])
+def test_norm_out_weights_and_gates(moe, T, H, xt, wt, gt, gate_kind):
+    """The other combinations: weights of either type with an offset, and sigmoid
+    gates of either type, direct and through shared memory.  The gate's fast
+    exponential is within 2 + 1.2 |g| ulp (2^-23), |g| < 15 here: 40 u more,
+    and twice that in its slope, inside the tolerance's 320 u beside the row's."""
+    g = torch.Generator().manual_seed(T + H)
+    x, y = _randn(g, T, H, dtype=xt, std=2.0), _randn(g, T, H, dtype=BF16, std=0.3)
+    w, w2 = _randn(g, H, dtype=wt, std=0.2), _randn(g, H, dtype=wt, std=0.2)
+    gate = _randn(g, *((T,) if gate_kind == "token" else (T, H)), dtype=gt, std=3.0)
+    kw = dict(gate=gate, residual_scale=0.5, weight_offset=1.0)
+    out, rstd, nxt, rstd2 = moe.moe_norm_out(x, y, w, next_weight=w2, save_rstd=True, **kw)
+    wf, wm, w2f, w2m = 1 + w.double(), 1 + w.double().abs(), 1 + w2.double(), 1 + w2.double().abs()
+    s = torch.sigmoid(gate.double()).view(T, -1)
+    hat = y.double() * _rms64(y.double(), 1e-6)
+    _close(out, 0.5 * x.double() + s * hat * wf, 0.5 * x.double().abs() + s * hat.abs() * wm, "out")
+    o = out.double()
+    oh = o * _rms64(o, 1e-6)
+    _close(nxt, oh * w2f, oh.abs() * w2m, "next")
+    dout, dnext = _randn(g, T, H, dtype=xt), _randn(g, T, H, dtype=BF16)
+    gx, gy, gg, gw, gw2 = moe.moe_norm_out_backward(dout, y, w, rstd, grad_next=dnext, out=out, next_weight=w2,
+                                                    next_rstd=rstd2, **kw)
+    dd, dw2, mdd, mw2 = _norm_vjp(out, rstd2, w2f, w2m, dnext)
+    d, md = dout.double() + dd, dout.double().abs() + mdd
+    _close(gw2, dw2, mw2, "grad_next_weight")
+    _close(gx, 0.5 * d, 0.5 * md, "grad_x")
+    r = rstd.double()[:, None]
+    hat, slope = y.double() * r, s * (1 - s)
+    if gate_kind == "element":
+        _close(gg, slope * d * hat * wf, slope * md * hat.abs() * wm, "grad_gate")
+    else:
+        _close(gg, slope[:, 0] * (d * hat * wf).sum(1), slope[:, 0] * (md * hat.abs() * wm).sum(1), "grad_gate")
+    e, me = wf * s * d, wm * s * md
+    _close(gy, r * e - y.double() * r ** 3 * (e * y.double()).mean(1, keepdim=True),
+           r * me + y.double().abs() * r ** 3 * (me * y.double().abs()).mean(1, keepdim=True), "grad_y")
+    _close(gw, (s * d * hat).sum(0), (s * md * hat.abs()).sum(0), "grad_weight")
