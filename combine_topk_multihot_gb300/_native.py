@@ -127,6 +127,7 @@ SIGNATURES = {
     "moe_grouped_experts_fp8_block": (c_int32, [_P, _LP, c_int32, c_int32] + [_P] * 7),
     "moe_selftest_wait_timeout": (c_int32, [_P, c_int64, _P, _P]),
     "moe_selftest_block_product_tiles": (c_int32, [c_int32]),
+    "moe_selftest_norm_rows": (c_int32, [c_int64]),
     "moe_route_to_multihot_backward": (c_int32, [_P, _P, _P, c_int32, c_int32, c_int32, _P, _P]),
 }
 

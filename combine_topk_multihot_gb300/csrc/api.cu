@@ -691,6 +691,7 @@ uintptr_t gate_bytes(const moe_norm* n) {
 NormArgs norm_args(const moe_norm* n) {
   NormArgs a{};
   a.T = n->T;
+  a.load_T = norm_load_rows(n->T);
   a.H = n->H;
   a.x_f32 = n->x_dtype == MOE_DTYPE_F32;
   a.w_f32 = n->weight_dtype == MOE_DTYPE_F32;
@@ -706,6 +707,7 @@ NormArgs norm_args(const moe_norm* n) {
 NormBackwardArgs norm_backward_args(const moe_norm* n) {
   NormBackwardArgs a{};
   a.T = n->T;
+  a.load_T = norm_load_rows(n->T);
   a.H = n->H;
   a.x_f32 = n->x_dtype == MOE_DTYPE_F32;
   a.w_f32 = n->weight_dtype == MOE_DTYPE_F32;

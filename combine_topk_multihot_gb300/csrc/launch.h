@@ -214,6 +214,7 @@ cudaError_t launch_experts_backward(const uint16_t* grad_y, const uint16_t* x_di
 // block (x -> next); otherwise out is the updated stream and next may be NULL.
 struct NormArgs {
   long long T;
+  long long load_T;  // rows that are brought to shared memory: all, but in the self-test
   int H;
   int x_f32, w_f32, gate_f32, gate_kind, sigmoid;
   float residual_scale, eps, offset;
@@ -226,6 +227,7 @@ cudaError_t launch_norm_forward(const NormArgs& a, cudaStream_t s);
 // that joins the stream, or NULL); partials: norm_backward_workspace bytes.
 struct NormBackwardArgs {
   long long T;
+  long long load_T;
   int H;
   int x_f32, w_f32, gate_f32, gate_kind, sigmoid;
   int has_y, has_next;
@@ -261,9 +263,12 @@ cudaError_t launch_block_experts_tc(const uint8_t* x_q, const float* x_scale, co
                                     const uint8_t* W1, const float* W1_scale, const uint8_t* W2,
                                     const float* W2_scale, uint8_t* h_q, float* h_scale, uint16_t* y,
                                     cudaStream_t s);
-// Self-test: this host thread's launches of these kernels load operands for
+// Self-tests: this host thread's norms bring the first `rows` rows to shared
+// memory only; its tensor-core launches of these products load operands for
 // `tiles` tiles a CTA only.
 void selftest_block_load_tiles(int tiles);
+void selftest_norm_load_rows(long long rows);
+long long norm_load_rows(long long T);
 
 // AdamW over many tensors (adamw.cu), up to ADAMW_BATCH of them a launch.
 constexpr int ADAMW_BATCH = 96;

@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : PIPE ? 256 : 512,
   };
   if (PIPE && in_row == 0)
     for (int i = 0; i < SLOTS; ++i)
-      if (t + i * stride < a.T) issue(t + i * stride, i);
+      if (t + i * stride < a.load_T) issue(t + i * stride, i);
   const float inv_h = 1.0f / static_cast<float>(H);
   int phase = 0;
   auto col = [&](int j) { return 8 * (in_row + j * row_threads); };
@@ -101,15 +101,19 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : PIPE ? 256 : 512,
           if (!a.gate_f32) gates[j] = read_slot<false>(slot + bytes[0] + bytes[1], col(j), H);
       }
       if (!group_all(here, row_threads, group)) {  // (also: every read of the slot is done)
-        pipe_drain(pipe, t, stride, a.T);
+        pipe_drain(pipe, t, stride, a.load_T);
 #pragma unroll 1
         for (; t < a.T; t += stride) {
+          if (in_row == 0) {
+            if (HAS_Y && a.rstd) a.rstd[t] = __uint_as_float(0x7fc00000u);
+            if (HAS_NEXT && a.rstd2) a.rstd2[t] = __uint_as_float(0x7fc00000u);
+          }
           if constexpr (HAS_Y) spoil_row<XF32>(a.out, t, H, in_row, row_threads);
           if constexpr (HAS_NEXT) spoil_row<false>(a.next, t, H, in_row, row_threads);
         }
         break;
       }
-      if (in_row == 0 && t + SLOTS * stride < a.T) issue(t + SLOTS * stride, pipe.at);
+      if (in_row == 0 && t + SLOTS * stride < a.load_T) issue(t + SLOTS * stride, pipe.at);
       pipe.next();
     } else {
       const void* xr = row_of(a.x, t, H, XF32);
@@ -238,7 +242,13 @@ cudaError_t forward_any(const NormArgs& a, cudaStream_t s) {
   return elem ? forward<XF32, true, false, true>(a, s) : forward<XF32, true, false, false>(a, s);
 }
 
+// The self-test's limit of the rows that are loaded, for this host thread's launches.
+thread_local long long tls_load_rows = -1;
+
 }  // namespace
+
+void selftest_norm_load_rows(long long rows) { tls_load_rows = rows; }
+long long norm_load_rows(long long T) { return tls_load_rows >= 0 && tls_load_rows < T ? tls_load_rows : T; }
 
 cudaError_t launch_norm_forward(const NormArgs& a, cudaStream_t s) {
   if (a.T == 0) return cudaSuccess;

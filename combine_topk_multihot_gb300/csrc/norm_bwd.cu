@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(THIRD ? 256 : 512, THIRD ? 3 : 1)
   long long t = static_cast<long long>(blockIdx.x) * groups + group;
   if (PIPE && in_row == 0)
     for (int i = 0; i < SLOTS; ++i)
-      if (t + i * stride < a.T) issue(t + i * stride, i);
+      if (t + i * stride < a.load_T) issue(t + i * stride, i);
   for (; t < a.T; t += stride) {
     Raw<XF32> dout[NV], out[NV];
     Raw<false> dnext[NV], y[NV], gates[ELEM && PIPE ? NV : 1];
@@ -112,18 +112,23 @@ __global__ void __launch_bounds__(THIRD ? 256 : 512, THIRD ? 3 : 1)
           if (!a.gate_f32) gates[j] = read_slot<false>(slot + bytes[0] + bytes[1] + bytes[2] + bytes[3], col(j), H);
       }
       if (!group_all(here, row_threads, group)) {  // (also: every read of the slot is done)
-        pipe_drain(pipe, t, stride, a.T);
+        pipe_drain(pipe, t, stride, a.load_T);
 #pragma unroll 1
         for (; t < a.T; t += stride) {
           spoil_row<XF32>(a.dx, t, H, in_row, row_threads);
-          if constexpr (HAS_Y) spoil_row<false>(a.dy, t, H, in_row, row_threads);
+          if constexpr (HAS_Y) {
+            spoil_row<false>(a.dy, t, H, in_row, row_threads);
+            const int per_row = ELEM ? H : a.gate_kind == MOE_GATE_TOKEN ? 1 : 0;
+            if (a.gate_f32) spoil_row<true>(a.dgate, t, per_row, in_row, row_threads);
+            else spoil_row<false>(a.dgate, t, per_row, in_row, row_threads);
+          }
         }
         const float nan = __uint_as_float(0x7fc00000u);
 #pragma unroll 1
         for (int k = 0; k < ACC * NV * 2; ++k) acc[k * blockDim.x + threadIdx.x] = make_float4(nan, nan, nan, nan);
         break;
       }
-      if (in_row == 0 && t + SLOTS * stride < a.T) issue(t + SLOTS * stride, pipe.at);
+      if (in_row == 0 && t + SLOTS * stride < a.load_T) issue(t + SLOTS * stride, pipe.at);
       pipe.next();
     }
 #pragma unroll
@@ -294,7 +299,7 @@ constexpr size_t SMEM_PER_SM = 228 * 1024;
 // Vectors a thread: one while there are too few rows to fill the SMs (then the
 // latency of one counts) or rows are short or ragged, else two, which keep the
 // tensors of a row in 128 registers; four above 8192 values a row, where
-// up to 456 bytes a thread spill (4096 x 16384, bf16: before a block 90 us for 60 at the copy
+// up to 472 bytes a thread spill (4096 x 16384, bf16: before a block 90 us for 60 at the copy
 // rate, after one with the next norm 230 for 119; two vectors would be 1024 threads of 64 registers).
 struct BackwardShape {
   int nv, row_threads, groups, per_sm, grid;

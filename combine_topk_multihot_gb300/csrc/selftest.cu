@@ -57,3 +57,9 @@ extern "C" moe_status moe_selftest_block_product_tiles(int32_t tiles) {
   selftest_block_load_tiles(tiles < 0 ? 0x7fffffff : tiles);
   return MOE_OK;
 }
+
+extern "C" moe_status moe_selftest_norm_rows(int64_t rows) {
+  if (rows < -1) return set_last_error(MOE_ERR_INVALID_ARG, "moe_selftest_norm_rows: rows must be >= 0, or -1 for all");
+  selftest_norm_load_rows(rows);
+  return MOE_OK;
+}

@@ -547,8 +547,8 @@ typedef struct moe_norm {
  *   x [T, H] bf16 or fp32; weight [H]; norm [T, H] bf16 (out);
  *   rstd [T] fp32 (out, nullable): r_t, for the backward.
  * Outputs must not overlap inputs, here and in the three calls below.  If a
- * bounded wait of a kernel runs out, the rows that it does not reach (and the
- * weights' gradients) are NaN.  Errors:
+ * bounded wait of a kernel runs out, the rows that it does not reach, in every
+ * output, and the weights' gradients are NaN.  Errors:
  * MOE_ERR_UNSUPPORTED_SHAPE for H outside [1, 16384], MOE_ERR_INVALID_ARG for
  * a NULL or misaligned pointer, T < 0, an unknown type or gate kind, or an eps
  * or scale that is not finite (eps also when negative).
@@ -735,6 +735,10 @@ MOE_API moe_status moe_selftest_wait_timeout(int32_t* status, int64_t limit_ns, 
  * MOE_DEVERR_TIMEOUT, and the outputs that were not reached are NaN.
  */
 MOE_API moe_status moe_selftest_block_product_tiles(int32_t tiles);
+
+/* The same for the norms: only the first `rows` rows arrive, where rows go
+ * through shared memory (H a multiple of 8 above 256, rows for every SM). */
+MOE_API moe_status moe_selftest_norm_rows(int64_t rows);
 
 #ifdef __cplusplus
 }  /* extern "C" */
