@@ -16,7 +16,9 @@ from .moe import (Layout, MoEError, ForwardResult, worst_case_rows, moe_router_t
                   moe_grouped_experts_backward)
 from .block import (moe_norm_in, moe_norm_in_backward, moe_norm_out, moe_norm_out_backward,
                     AdamWState, moe_adamw_step,
-                    moe_quantize_fp8_block, moe_matmul_fp8_block, moe_grouped_experts_fp8_block)
+                    moe_quantize_fp8_block, moe_matmul_fp8_block, moe_grouped_experts_fp8_block,
+                    moe_quantize_fp4_block, moe_dequantize_fp4_block, moe_matmul_fp4_block, moe_fp4_scale_tiles,
+                    moe_fp4_scale_rows, moe_layer_few)
 from . import _native
 from . import ops
 from .ops import moe_block, moe_layer, moe_layer_from_logits, moe_layer_fp8_block
@@ -32,5 +34,7 @@ __all__ = [
     "moe_grouped_experts_backward", "moe_norm_in", "moe_norm_in_backward", "moe_norm_out", "moe_norm_out_backward",
     "AdamWState", "moe_adamw_step",
     "moe_quantize_fp8_block", "moe_matmul_fp8_block", "moe_grouped_experts_fp8_block",
+    "moe_quantize_fp4_block", "moe_dequantize_fp4_block", "moe_matmul_fp4_block", "moe_fp4_scale_tiles", "moe_fp4_scale_rows",
+    "moe_layer_few",
     "_native", "ops", "moe_block", "moe_layer", "moe_layer_from_logits", "moe_layer_fp8_block",
 ]

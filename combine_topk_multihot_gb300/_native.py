@@ -42,6 +42,11 @@ MOE_GATE_NONE = 0
 MOE_GATE_TOKEN = 1
 MOE_GATE_ELEMENT = 2
 MOE_ADAMW_STATE_BLOCK = 256
+MOE_WEIGHTS_BF16 = 0
+MOE_WEIGHTS_FP8_BLOCK = 1
+MOE_WEIGHTS_FP4_BLOCK = 2
+MOE_FEW_TOKENS = 8
+MOE_FEW_TOP_K = 16
 
 
 class MoeLayout(ctypes.Structure):
@@ -80,6 +85,13 @@ class MoeAdamw(ctypes.Structure):
         ("step", c_int64), ("seed", ctypes.c_uint64), ("state_bits", c_int32), ("grad_scale", c_void_p),
         ("skip", c_void_p), ("step_dev", c_void_p),
     ]
+
+
+class MoeFew(ctypes.Structure):
+    """struct moe_few."""
+    _fields_ = [(n, c_int32) for n in ("T", "E", "K", "H", "I", "router_dtype", "weights")] + [
+        (n, c_void_p) for n in ("x", "router", "topk_idx", "topk_probs", "W1", "W1_scale", "W2", "W2_scale", "out", "idx_out",
+                                "probs_out", "status", "workspace")]
 
 
 _P = c_void_p
@@ -125,6 +137,11 @@ SIGNATURES = {
     "moe_matmul_fp8_block": (c_int32, [_P, _P, c_int32, _P, _P, c_int32, c_int32, _P, _P, _P]),
     "moe_experts_fp8_block_workspace_bytes": (c_int32, [c_int64, c_int32, c_int32, c_int32, c_int32, ctypes.POINTER(c_size_t)]),
     "moe_grouped_experts_fp8_block": (c_int32, [_P, _LP, c_int32, c_int32] + [_P] * 7),
+    "moe_quantize_fp4_block": (c_int32, [_P, c_int32, c_int64, c_int64, c_int32, _P, _P, _P]),
+    "moe_dequantize_fp4_block": (c_int32, [_P, _P, c_int64, c_int64, c_int32, c_int32, _P, _P]),
+    "moe_matmul_fp4_block": (c_int32, [_P, _P, c_int32, _P, _P, c_int32, c_int32, _P, _P, _P]),
+    "moe_layer_few_workspace_bytes": (c_int32, [c_int32, c_int32, c_int32, c_int32, ctypes.POINTER(c_size_t)]),
+    "moe_layer_few": (c_int32, [ctypes.POINTER(MoeFew), _P]),
     "moe_selftest_wait_timeout": (c_int32, [_P, c_int64, _P, _P]),
     "moe_selftest_block_product_tiles": (c_int32, [c_int32]),
     "moe_selftest_norm_rows": (c_int32, [c_int64]),

@@ -6,7 +6,11 @@
   its averages in fp32 or in 8 bits;
 * moe_quantize_fp8_block, moe_matmul_fp8_block and
   moe_grouped_experts_fp8_block: products of e4m3 codes with a scale for each
-  block of 128.
+  block of 128;
+* moe_quantize_fp4_block, moe_dequantize_fp4_block and moe_matmul_fp4_block:
+  e2m1 codes with a power-of-two scale for each 32 of a row, and their product;
+* moe_layer_few: a whole layer for at most 8 tokens, from weights in bf16 or in
+  either of those forms.
 
 As in ``moe.py`` the functions carry the names of the C entry points, all
 arithmetic runs in the CUDA library, and PyTorch only allocates the buffers and
@@ -433,3 +437,146 @@ def moe_grouped_experts_fp8_block(x_disp: torch.Tensor, layout: Layout, W1_q: to
         "moe_grouped_experts_fp8_block")
     _used_on(stream, out, ws)
     return out
+
+
+# ------------------------------------------------------------------ e2m1 with a scale per 32
+def _fp4_tiles(rows: int, cols: int):
+    """The last five sizes of a matrix's scales: tiles of 128 rows and 4 blocks of 32."""
+    return (rows + 127) // 128, (cols + 127) // 128, 32, 4, 4
+
+
+def _fp4_matrix(codes: torch.Tensor, name: str):
+    if codes.dim() < 2 or codes.shape[-1] % 16:
+        raise ValueError(f"{name} must be [..., rows, cols / 2] with cols a multiple of 32 (got {tuple(codes.shape)})")
+    return codes.shape[:-2], codes.shape[-2], codes.shape[-1] * 2
+
+
+def moe_quantize_fp4_block(src: torch.Tensor, out=None, stream=None):
+    """e2m1 codes of a bf16 or fp32 tensor [..., rows, cols], two a byte (uint8 [...,
+    rows, cols / 2], the lower four bits first), and a power-of-two scale for each
+    32 of a row, its exponent's 8 bits (e8m0), in tiles: uint8 [..., ceil(rows /
+    128), ceil(cols / 128), 32, 4, 4].  cols is a multiple of 32."""
+    dev = _on_gpu(src, "src")
+    dtype = _either(src, "src")
+    if src.dim() < 2 or src.shape[-1] % 32 or src.shape[-1] == 0:
+        raise ValueError(f"src must be [..., rows, cols] with cols a positive multiple of 32 (got {tuple(src.shape)})")
+    rows, cols = src.shape[-2:]
+    lead = src.shape[:-2]
+    shape = (*lead, rows, cols // 2)
+    tiles = (*lead, *_fp4_tiles(rows, cols))
+    if out is None:
+        out = torch.empty(shape, dtype=torch.uint8, device=dev), torch.empty(tiles, dtype=torch.uint8, device=dev)
+    codes, scales = out
+    _check(N.lib.moe_quantize_fp4_block(_need(src, "src", src.dtype, src.shape, dev), dtype, lead.numel() if lead else 1, rows,
+                                        cols, _need(codes, "codes", torch.uint8, shape, dev),
+                                        _need(scales, "scales", torch.uint8, tiles, dev), _raw_stream(stream, dev)),
+           "moe_quantize_fp4_block")
+    _used_on(stream, codes, scales)
+    return codes, scales
+
+
+def moe_dequantize_fp4_block(codes: torch.Tensor, scales: torch.Tensor, dtype=torch.bfloat16,
+                             out: Optional[torch.Tensor] = None, stream=None):
+    """What codes and scales of moe_quantize_fp4_block stand for: [..., rows, cols],
+    bf16 or fp32, exact in both."""
+    dev = _on_gpu(codes, "codes")
+    lead, rows, cols = _fp4_matrix(codes, "codes")
+    if out is None:
+        out = torch.empty(*lead, rows, cols, dtype=dtype, device=dev)
+    _check(N.lib.moe_dequantize_fp4_block(_need(codes, "codes", torch.uint8, codes.shape, dev),
+                                          _need(scales, "scales", torch.uint8, (*lead, *_fp4_tiles(rows, cols)), dev),
+                                          lead.numel() if lead else 1, rows, cols, _either(out, "out"),
+                                          _need(out, "out", dtype, (*lead, rows, cols), dev), _raw_stream(stream, dev)),
+           "moe_dequantize_fp4_block")
+    _used_on(stream, out)
+    return out
+
+
+def moe_matmul_fp4_block(a_q: torch.Tensor, a_scale: torch.Tensor, b_q: torch.Tensor, b_scale: torch.Tensor,
+                         out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None):
+    """a b^T of codes [M, K / 2] and [N, K / 2] with their tiles of scales: [M, N] bf16."""
+    dev = _on_gpu(a_q, "a_q")
+    M, half = _rows(a_q, "a_q")
+    n = _rows(b_q, "b_q")[0]
+    if out is None:
+        out = torch.empty(M, n, dtype=torch.bfloat16, device=dev)
+    _check(N.lib.moe_matmul_fp4_block(_need(a_q, "a_q", torch.uint8, (M, half), dev),
+                                      _need(a_scale, "a_scale", torch.uint8, _fp4_tiles(M, 2 * half), dev), M,
+                                      _need(b_q, "b_q", torch.uint8, (n, half), dev),
+                                      _need(b_scale, "b_scale", torch.uint8, _fp4_tiles(n, 2 * half), dev), n, 2 * half,
+                                      _need(out, "out", torch.bfloat16, (M, n), dev),
+                                      None if status is None else _need(status, "status", torch.int32, (1,), dev),
+                                      _raw_stream(stream, dev)), "moe_matmul_fp4_block")
+    _used_on(stream, out)
+    return out
+
+
+def moe_fp4_scale_tiles(scales: torch.Tensor) -> torch.Tensor:
+    """Scales in rows, uint8 [..., rows, cols / 32], as other files keep them, laid out in tiles."""
+    rows, blocks = scales.shape[-2:]
+    s = torch.nn.functional.pad(scales, (0, -blocks % 4, 0, -rows % 128))
+    s = s.unflatten(-1, (-1, 4)).unflatten(-3, (-1, 4, 32))          # [..., rt, 4, 32, bt, 4]
+    return s.movedim(-2, -4).transpose(-3, -2).contiguous()
+
+
+def moe_fp4_scale_rows(tiles: torch.Tensor, rows: int, cols: int) -> torch.Tensor:
+    """The way back from moe_fp4_scale_tiles: [..., rows, cols / 32]."""
+    s = tiles.transpose(-3, -2).movedim(-4, -2)
+    return s.flatten(-2).flatten(-4, -2)[..., :rows, :cols // 32].contiguous()
+
+
+# ------------------------------------------------------------------ a layer for few tokens
+def moe_layer_few(x: torch.Tensor, router: Optional[torch.Tensor], top_k: int, W1: torch.Tensor, W2: torch.Tensor,
+                  W1_scale: Optional[torch.Tensor] = None, W2_scale: Optional[torch.Tensor] = None, routing=None,
+                  return_routing: bool = False, out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                  stream=None):
+    """The router, the layer's experts and their weighted sum for at most 8 tokens
+    x [T, H] bf16, in two launches: out [T, H] bf16, for inference.
+
+    ``router`` [E, H] bf16 or fp32 picks the experts as moe_router_topk does from
+    ``x @ router^T``; with None, ``routing`` = (topk_idx int64 [T, top_k],
+    topk_probs fp32) does (-1: no expert).  W1 [E, 2I, H] and W2 [E, H, I] are
+    bf16 without scales; e4m3 codes with the fp32 scales of
+    moe_quantize_fp8_block(block_rows=128); or e2m1 codes, two a byte, with the
+    uint8 scales of moe_quantize_fp4_block.  With ``return_routing`` it returns
+    (out, topk_idx, topk_probs)."""
+    T, H = _rows(x, "x")
+    dev = _on_gpu(x, "x")
+    if W1.dim() != 3 or W1.shape[1] % 2:
+        raise ValueError(f"W1 must be [E, 2I, H] (got {tuple(W1.shape)})")
+    E, I = W1.shape[0], W1.shape[1] // 2
+    if (W1_scale is None) != (W2_scale is None):
+        raise ValueError("give W1_scale and W2_scale, or neither")
+    if W1_scale is None:
+        fmt, wt, h, i, s1, s2 = N.MOE_WEIGHTS_BF16, torch.bfloat16, H, I, None, None
+    elif W1_scale.dtype is torch.float32:
+        fmt, wt, h, i = N.MOE_WEIGHTS_FP8_BLOCK, torch.uint8, H, I
+        s1 = _need(W1_scale, "W1_scale", torch.float32, (E, _blocks(2 * I), _blocks(H)), dev)
+        s2 = _need(W2_scale, "W2_scale", torch.float32, (E, _blocks(H), _blocks(I)), dev)
+    else:
+        fmt, wt, h, i = N.MOE_WEIGHTS_FP4_BLOCK, torch.uint8, H // 2, I // 2
+        s1 = _need(W1_scale, "W1_scale", torch.uint8, (E, *_fp4_tiles(2 * I, H)), dev)
+        s2 = _need(W2_scale, "W2_scale", torch.uint8, (E, *_fp4_tiles(H, I)), dev)
+    if (router is None) == (routing is None):
+        raise ValueError("give router or routing, and not both")
+    r_dtype = r = idx = probs = None
+    if router is not None:
+        r_dtype, r = _either(router, "router"), _need(router, "router", router.dtype, (E, H), dev)
+    else:
+        idx = _need(routing[0], "topk_idx", torch.int64, (T, top_k), dev)
+        probs = _need(routing[1], "topk_probs", torch.float32, (T, top_k), dev)
+    if out is None:
+        out = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
+    idx_out = probs_out = None
+    if return_routing:
+        idx_out = torch.empty(T, top_k, dtype=torch.int64, device=dev)
+        probs_out = torch.empty(T, top_k, dtype=torch.float32, device=dev)
+    ws = torch.empty(_bytes("moe_layer_few_workspace_bytes", dev.index, T, E, top_k, I), dtype=torch.uint8, device=dev)
+    f = N.MoeFew(T, E, top_k, H, I, r_dtype or 0, fmt, _need(x, "x", torch.bfloat16, (T, H), dev), r, idx, probs,
+                 _need(W1, "W1", wt, (E, 2 * I, h), dev), s1, _need(W2, "W2", wt, (E, H, i), dev), s2,
+                 _need(out, "out", torch.bfloat16, (T, H), dev),
+                 idx_out.data_ptr() or None if return_routing else None, probs_out.data_ptr() or None if return_routing else None,
+                 None if status is None else _need(status, "status", torch.int32, (1,), dev), ws.data_ptr())
+    _check(N.lib.moe_layer_few(f, _raw_stream(stream, dev)), "moe_layer_few")
+    _used_on(stream, out, idx_out, probs_out, ws)
+    return (out, idx_out, probs_out) if return_routing else out

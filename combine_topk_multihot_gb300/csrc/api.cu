@@ -967,6 +967,19 @@ BlockWorkspace block_workspace(int64_t C, bool stream, int32_t H, int32_t I) {
   return w;
 }
 
+moe_status check_fp4(const char* who, const void* values, int32_t dtype, int64_t batch, int64_t rows, int32_t cols,
+                     const uint8_t* codes, const uint8_t* scales) {
+  MOE_REQUIRE(batch >= 0 && rows >= 0, MOE_ERR_INVALID_ARG, "%s: batch and rows must be >= 0", who);
+  MOE_REQUIRE(dtype == MOE_DTYPE_BF16 || dtype == MOE_DTYPE_F32, MOE_ERR_INVALID_ARG, "%s: unknown type %d", who, dtype);
+  MOE_REQUIRE(cols >= 32 && cols % 32 == 0, MOE_ERR_UNSUPPORTED_SHAPE, "%s: cols must be a positive multiple of 32 (got %d)", who,
+              cols);
+  MOE_REQUIRE(rows < (int64_t(1) << 31) - 128 && (batch == 0 || rows < (int64_t(1) << 47) / cols / batch), MOE_ERR_UNSUPPORTED_SHAPE,
+              "%s: too many rows", who);
+  MOE_REQUIRE(batch == 0 || rows == 0 || (values && codes && scales), MOE_ERR_INVALID_ARG, "%s: NULL pointer", who);
+  MOE_REQUIRE(all_aligned(16, values, codes, scales), MOE_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", who);
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1014,6 +1027,44 @@ moe_status moe_matmul_fp8_block(const uint8_t* a_q, const float* a_scale, int32_
   return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_matmul_fp8_block launch");
 }
 
+moe_status moe_quantize_fp4_block(const void* src, int32_t src_dtype, int64_t batch, int64_t rows, int32_t cols, uint8_t* codes,
+                                  uint8_t* scales, moe_stream_t stream) {
+  moe_status st = check_fp4("moe_quantize_fp4_block", src, src_dtype, batch, rows, cols, codes, scales);
+  if (st != MOE_OK) return st;
+  if ((st = check_device()) != MOE_OK) return st;
+  const cudaError_t err = launch_quantize_fp4(src, src_dtype == MOE_DTYPE_F32, batch, rows, cols, codes, scales, stream);
+  return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_quantize_fp4_block launch");
+}
+
+moe_status moe_dequantize_fp4_block(const uint8_t* codes, const uint8_t* scales, int64_t batch, int64_t rows, int32_t cols,
+                                    int32_t out_dtype, void* out, moe_stream_t stream) {
+  moe_status st = check_fp4("moe_dequantize_fp4_block", out, out_dtype, batch, rows, cols, codes, scales);
+  if (st != MOE_OK) return st;
+  if ((st = check_device()) != MOE_OK) return st;
+  const cudaError_t err = launch_dequantize_fp4(codes, scales, batch, rows, cols, out_dtype == MOE_DTYPE_F32, out, stream);
+  return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_dequantize_fp4_block launch");
+}
+
+moe_status moe_matmul_fp4_block(const uint8_t* a_q, const uint8_t* a_scale, int32_t M, const uint8_t* b_q, const uint8_t* b_scale,
+                                int32_t N, int32_t K, moe_bf16* out, int32_t* status, moe_stream_t stream) {
+  MOE_REQUIRE(M >= 0 && N >= 1, MOE_ERR_INVALID_ARG, "moe_matmul_fp4_block: M must be >= 0 and N >= 1 (got %d, %d)", M, N);
+  MOE_REQUIRE(K >= 32 && K % 32 == 0, MOE_ERR_UNSUPPORTED_SHAPE,
+              "moe_matmul_fp4_block: K must be a positive multiple of 32 (got %d)", K);
+  MOE_REQUIRE(M == 0 || (a_q && a_scale && b_q && b_scale && out), MOE_ERR_INVALID_ARG, "moe_matmul_fp4_block: NULL pointer");
+  MOE_REQUIRE(all_aligned(16, a_q, a_scale, b_q, b_scale) && aligned_to(out, N % 8 == 0 ? 16 : 2) && aligned_to(status, 4),
+              MOE_ERR_INVALID_ARG,
+              "moe_matmul_fp4_block: codes, scales and (N a multiple of 8) out must be 16-byte aligned, others by their type");
+  constexpr int32_t most = (int64_t(1) << 31) - 256;
+  MOE_REQUIRE(M < most && N < most && (static_cast<int64_t>(M) + 127) / 128 * ((N + 63) / 64) < most, MOE_ERR_UNSUPPORTED_SHAPE,
+              "moe_matmul_fp4_block: too many tiles");
+  moe_status st = check_device();
+  if (st != MOE_OK) return st;
+  if (M == 0) return MOE_OK;
+  const cudaError_t err = M <= FP4_STREAM_ROWS ? launch_fp4_matmul_stream(a_q, a_scale, M, b_q, b_scale, N, K, out, stream)
+                                               : launch_fp4_matmul_tc(a_q, a_scale, M, b_q, b_scale, N, K, out, status, stream);
+  return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_matmul_fp4_block launch");
+}
+
 moe_status moe_experts_fp8_block_workspace_bytes(int64_t capacity, int32_t T, int32_t E, int32_t H, int32_t I,
                                                  size_t* bytes) {
   MOE_REQUIRE(bytes != nullptr, MOE_ERR_INVALID_ARG, "bytes is NULL");
@@ -1054,6 +1105,96 @@ moe_status moe_grouped_experts_fp8_block(const moe_bf16* x_disp, const moe_layou
                                     reinterpret_cast<float*>(base + w.h_scale), y_disp, stream);
   }
   return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_grouped_experts_fp8_block launch");
+}
+
+}  // extern "C"
+
+namespace {
+
+struct FewWorkspace {
+  size_t logits, h, total;
+};
+
+FewWorkspace few_workspace(int32_t T, int32_t E, int32_t K, int32_t I) {
+  auto up = [](size_t bytes) { return (bytes + 255) / 256 * 256; };
+  FewWorkspace w{};
+  w.logits = 256;  // behind the barrier's word
+  w.h = w.logits + up(static_cast<size_t>(T) * E * sizeof(float));
+  w.total = w.h + up(static_cast<size_t>(T) * K * I * 2);
+  return w;
+}
+
+moe_status check_few(int32_t T, int32_t E, int32_t K, int32_t I) {
+  MOE_REQUIRE(T >= 0, MOE_ERR_INVALID_ARG, "T must be >= 0 (got %d)", T);
+  MOE_REQUIRE(T <= MOE_FEW_TOKENS, MOE_ERR_UNSUPPORTED_SHAPE, "moe_layer_few takes at most %d tokens (got %d)", MOE_FEW_TOKENS, T);
+  MOE_REQUIRE(E >= 1 && E <= 1024, MOE_ERR_UNSUPPORTED_SHAPE, "E must be in [1, 1024] (got %d)", E);
+  MOE_REQUIRE(K >= 1 && K <= E && K <= MOE_FEW_TOP_K, MOE_ERR_UNSUPPORTED_SHAPE,
+              "K must be in [1, min(E, %d)] (got K=%d, E=%d)", MOE_FEW_TOP_K, K, E);
+  MOE_REQUIRE(I > 0 && I % 128 == 0, MOE_ERR_UNSUPPORTED_SHAPE,
+              "the intermediate size must be a positive multiple of 128 (got %d)", I);
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_layer_few_workspace_bytes(int32_t T, int32_t E, int32_t K, int32_t I, size_t* bytes) {
+  MOE_REQUIRE(bytes != nullptr, MOE_ERR_INVALID_ARG, "bytes is NULL");
+  const moe_status st = check_few(T, E, K, I);
+  if (st != MOE_OK) return st;
+  *bytes = few_workspace(T, E, K, I).total;
+  return MOE_OK;
+}
+
+moe_status moe_layer_few(const moe_few* f, moe_stream_t stream) {
+  MOE_REQUIRE(f != nullptr, MOE_ERR_INVALID_ARG, "moe_layer_few: NULL pointer");
+  moe_status st = check_few(f->T, f->E, f->K, f->I);
+  if (st != MOE_OK) return st;
+  if ((st = check_hidden(f->H)) != MOE_OK) return st;
+  static_assert(FEW_TOKENS == MOE_FEW_TOKENS && FEW_TOP_K == MOE_FEW_TOP_K && FEW_FP8 == MOE_WEIGHTS_FP8_BLOCK &&
+                FEW_FP4 == MOE_WEIGHTS_FP4_BLOCK, "one set of constants");
+  MOE_REQUIRE(f->weights >= MOE_WEIGHTS_BF16 && f->weights <= MOE_WEIGHTS_FP4_BLOCK, MOE_ERR_INVALID_ARG,
+              "moe_layer_few: unknown weight format %d", f->weights);
+  MOE_REQUIRE(f->router_dtype == MOE_DTYPE_BF16 || f->router_dtype == MOE_DTYPE_F32, MOE_ERR_INVALID_ARG,
+              "moe_layer_few: unknown type %d", f->router_dtype);
+  MOE_REQUIRE(few_layer_fits(f->weights, f->T, f->K, f->H, f->I), MOE_ERR_UNSUPPORTED_SHAPE,
+              "moe_layer_few: the rows of %d tokens of H=%d and I=%d do not fit in shared memory", f->T, f->H, f->I);
+  const bool coded = f->weights != MOE_WEIGHTS_BF16;
+  MOE_REQUIRE(f->T == 0 || (f->x && f->W1 && f->W2 && f->out && f->workspace && (!coded || (f->W1_scale && f->W2_scale))),
+              MOE_ERR_INVALID_ARG, "moe_layer_few: NULL pointer");
+  MOE_REQUIRE(f->T == 0 || (f->router ? !f->topk_idx && !f->topk_probs : f->topk_idx && f->topk_probs), MOE_ERR_INVALID_ARG,
+              "moe_layer_few: give the router, or topk_idx and topk_probs");
+  MOE_REQUIRE((f->idx_out == nullptr) == (f->probs_out == nullptr), MOE_ERR_INVALID_ARG,
+              "moe_layer_few: give idx_out and probs_out, or neither");
+  MOE_REQUIRE(all_aligned(16, f->x, f->router, f->W1, f->W2, f->workspace) && all_aligned(8, f->topk_idx, f->idx_out) &&
+                  all_aligned(4, f->topk_probs, f->probs_out, f->W1_scale, f->W2_scale, f->status) && aligned_to(f->out, 2),
+              MOE_ERR_INVALID_ARG, "moe_layer_few: x, router, weights and workspace must be 16-byte aligned, others by their type");
+  if ((st = check_device()) != MOE_OK) return st;
+  if (f->T == 0) return MOE_OK;
+  const FewWorkspace w = few_workspace(f->T, f->E, f->K, f->I);
+  uint8_t* base = static_cast<uint8_t*>(f->workspace);
+  FewLayer g{};
+  g.x = f->x;
+  g.router = f->router;
+  g.router_f32 = f->router_dtype == MOE_DTYPE_F32;
+  g.topk_idx = f->topk_idx;
+  g.topk_probs = f->topk_probs;
+  g.format = f->weights;
+  g.W1 = f->W1;
+  g.S1 = f->W1_scale;
+  g.W2 = f->W2;
+  g.S2 = f->W2_scale;
+  g.T = f->T, g.E = f->E, g.K = f->K, g.H = f->H, g.I = f->I;
+  g.barrier = reinterpret_cast<unsigned*>(base);
+  g.logits = reinterpret_cast<float*>(base + w.logits);
+  g.h = reinterpret_cast<uint16_t*>(base + w.h);
+  g.out = f->out;
+  g.idx_out = f->idx_out;
+  g.probs_out = f->probs_out;
+  g.status = f->status;
+  const cudaError_t err = launch_few_layer(g, stream);
+  return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_layer_few launch");
 }
 
 }  // extern "C"

@@ -270,6 +270,44 @@ void selftest_block_load_tiles(int tiles);
 void selftest_norm_load_rows(long long rows);
 long long norm_load_rows(long long T);
 
+// e2m1 codes with a scale per 32 of a row (fp4_block.cu): matrices [batch, rows,
+// cols] of bf16 or fp32, each with its own tiles of scales, and the way back.
+cudaError_t launch_quantize_fp4(const void* src, bool f32, long long batch, long long rows, int cols, uint8_t* codes,
+                                uint8_t* scales, cudaStream_t s);
+cudaError_t launch_dequantize_fp4(const uint8_t* codes, const uint8_t* scales, long long batch, long long rows, int cols, bool f32,
+                                  void* out, cudaStream_t s);
+// Their dense product: with at most FP4_STREAM_ROWS rows as a stream over the weights.
+constexpr int FP4_STREAM_ROWS = 8;
+cudaError_t launch_fp4_matmul_stream(const uint8_t* a, const uint8_t* a_scale, int M, const uint8_t* b, const uint8_t* b_scale,
+                                     int N, int K, uint16_t* out, cudaStream_t s);
+// ... with more on the tensor cores (fp4_gemm.cu).
+cudaError_t launch_fp4_matmul_tc(const uint8_t* a, const uint8_t* a_scale, int M, const uint8_t* b, const uint8_t* b_scale, int N,
+                                 int K, uint16_t* out, int* status, cudaStream_t s);
+
+// A whole layer for at most FEW_TOKENS tokens (layer_few.cu).
+constexpr int FEW_TOKENS = 8;
+constexpr int FEW_TOP_K = 16;
+enum FewFormat { FEW_BF16 = 0, FEW_FP8 = 1, FEW_FP4 = 2 };  // of the experts' weights
+struct FewLayer {
+  const uint16_t* x;         // [T, H]
+  const void* router;        // [E, H]; NULL: the routing is given
+  bool router_f32;
+  const int64_t* topk_idx;   // [T, K]
+  const float* topk_probs;
+  int format;
+  const void *W1, *S1, *W2, *S2;
+  int T, E, K, H, I;
+  float* logits;             // scratch: [T, E]
+  uint16_t* h;               // scratch: [T K, I]
+  unsigned* barrier;         // scratch: one word
+  uint16_t* out;             // [T, H]
+  int64_t* idx_out;          // [T, K], nullable (both)
+  float* probs_out;
+  int* status;
+};
+bool few_layer_fits(int format, int T, int K, int H, int I);
+cudaError_t launch_few_layer(const FewLayer& f, cudaStream_t s);
+
 // AdamW over many tensors (adamw.cu), up to ADAMW_BATCH of them a launch.
 constexpr int ADAMW_BATCH = 96;
 constexpr int ADAMW_STATE_BLOCK = MOE_ADAMW_STATE_BLOCK;

@@ -716,6 +716,105 @@ MOE_API moe_status moe_grouped_experts_fp8_block(const moe_bf16* x_disp, const m
                                                  moe_bf16* y_disp, void* workspace, moe_stream_t stream);
 
 /*
+ * Microscaled 4-bit floating point (OCP MX): e2m1 codes (0, 0.5, 1, 1.5, 2, 3,
+ * 4, 6 and their negatives; bit 3 the sign), two a byte, the lower four bits
+ * first, with a power-of-two scale for each 32 of a row, kept as its exponent's
+ * 8 bits (e8m0: 2^(e - 127), 255 for NaN).  Scales lie in tiles of 128 rows and
+ * 4 blocks, as the tensor cores read them: [batch, ceil(rows / 128),
+ * ceil(cols / 128), 32, 4, 4] bytes, the scale of row r and block b at
+ * [r / 128, b / 4, r % 32, r % 128 / 32, b % 4].
+ *
+ * Quantisation: X = 2^e with the smallest e that leaves the block's largest
+ * magnitude below 7 X, but from 2^-127 to 2^125; code = e2m1(v / X) to nearest even,
+ * what is above 6 as 6.  The codes are functions of the input alone.  A NaN or
+ * an infinity makes its block's scale NaN and its codes zeros.  Scales of a
+ * tile's rows and blocks past the matrix are written as zeros.
+ *   src [batch, rows, cols] of src_dtype (moe_dtype), cols a multiple of 32;
+ *   codes [batch, rows, cols / 2] (out); scales as above (out).
+ * The way back: out [batch, rows, cols] of out_dtype (out) = code * X, exact in
+ * either type (bf16 weights of an expert that runs in bf16, say).
+ * All pointers are 16-byte aligned.  Errors: MOE_ERR_UNSUPPORTED_SHAPE for cols
+ * that is no positive multiple of 32 or rows of 2^31 - 128 or more,
+ * MOE_ERR_INVALID_ARG for a NULL or misaligned pointer, batch or rows below 0
+ * or an unknown type.
+ */
+MOE_API moe_status moe_quantize_fp4_block(const void* src, int32_t src_dtype, int64_t batch, int64_t rows, int32_t cols,
+                                          uint8_t* codes, uint8_t* scales, moe_stream_t stream);
+MOE_API moe_status moe_dequantize_fp4_block(const uint8_t* codes, const uint8_t* scales, int64_t batch, int64_t rows,
+                                            int32_t cols, int32_t out_dtype, void* out, moe_stream_t stream);
+
+/*
+ * out[m, n] = bf16(sum_b a_scale[m, b] b_scale[n, b] sum_{k in block b} a[m, k] b[n, k])
+ * of such codes: products of codes are exact and summed in fp32.
+ *   a_q [M, K / 2], b_q [N, K / 2] uint8 and their scales in tiles; out [M, N]
+ *   bf16 (out); status [1] int32 device status word (nullable), receives
+ *   MOE_DEVERR_TIMEOUT if a bounded wait runs out; the elements that are not
+ *   reached then are NaN.
+ * M >= 0, N >= 1, K a positive multiple of 32.  Codes and scales are 16-byte
+ * aligned, and so is out when N is a multiple of 8.  Scales past the last row or
+ * block of a matrix must not be 255 (the quantiser writes zeros there).  Up to 8
+ * rows stream the weights through registers; more run on the tensor cores.
+ */
+MOE_API moe_status moe_matmul_fp4_block(const uint8_t* a_q, const uint8_t* a_scale, int32_t M, const uint8_t* b_q,
+                                        const uint8_t* b_scale, int32_t N, int32_t K, moe_bf16* out, int32_t* status,
+                                        moe_stream_t stream);
+
+/*
+ * A whole layer for at most 8 tokens, in two launches (inference):
+ *   logits = x router^T in fp32; the K largest of a token, equal ones by
+ *   ascending index (NaN as -infinity), and their softmax as weights w_k;
+ *   h_k = bf16(silu(x Wg^T) * (x Wu^T)) of expert e_k;
+ *   out = bf16(sum_k w_k (h_k W2^T)), summed in fp32 by ascending expert.
+ * With router NULL the routing is given instead: topk_idx [T, K] (-1: no
+ * expert; of an expert that a token names twice the last slot counts; another
+ * value outside [0, E) is dropped and sets MOE_DEVERR_BAD_INDEX) and topk_probs.
+ * The weights' format:
+ *   MOE_WEIGHTS_BF16: W1 [E, 2I, H], W2 [E, H, I] bf16;
+ *   MOE_WEIGHTS_FP8_BLOCK: e4m3 codes with 128 x 128 scales
+ *   (moe_quantize_fp8_block, block_rows 128: W1_scale [E, 2I/128, H/128],
+ *   W2_scale [E, H/128, I/128] fp32);
+ *   MOE_WEIGHTS_FP4_BLOCK: e2m1 codes with scales in tiles
+ *   (moe_quantize_fp4_block: W1_scale [E, 2I/128, H/128, 32, 4, 4], ...).
+ * x and h are not rounded to 8 bits for the codes: they are multiplied as the sum
+ * of two e4m3 numbers, exact for a bf16 value of 2^-10 of the largest of its 128
+ * neighbours or more, and within 2^-18 of that largest below it.  A token with
+ * a NaN or an infinity has a NaN or infinity in its own row alone.
+ */
+typedef enum moe_weights { MOE_WEIGHTS_BF16 = 0, MOE_WEIGHTS_FP8_BLOCK = 1, MOE_WEIGHTS_FP4_BLOCK = 2 } moe_weights;
+#define MOE_FEW_TOKENS 8
+#define MOE_FEW_TOP_K 16
+typedef struct moe_few {
+  int32_t T, E, K, H, I;
+  int32_t router_dtype;        /* moe_dtype                                                */
+  int32_t weights;             /* moe_weights                                              */
+  const moe_bf16* x;           /* [T, H]                                                   */
+  const void* router;          /* [E, H], or NULL: topk_idx and topk_probs are given       */
+  const int64_t* topk_idx;     /* [T, K]                                                   */
+  const float* topk_probs;     /* [T, K]                                                   */
+  const void* W1;
+  const void* W1_scale;        /* NULL for bf16                                            */
+  const void* W2;
+  const void* W2_scale;
+  moe_bf16* out;               /* [T, H] (out)                                             */
+  int64_t* idx_out;            /* [T, K] (out, nullable, both or none): the routing used   */
+  float* probs_out;
+  int32_t* status;             /* [1] device status word, nullable                         */
+  void* workspace;             /* moe_layer_few_workspace_bytes(T, E, K, I) bytes, scratch */
+} moe_few;
+
+/*
+ * 0 <= T <= 8, 1 <= E <= 1024, 1 <= K <= min(E, 16), H a multiple of 256, I of
+ * 128, and the tokens' rows fit in shared memory (T max(H, I) up to about 78,000).
+ * x, router, weights and workspace are 16-byte aligned, scales 4-byte.  The
+ * struct is HOST memory, read before the call returns.  A bounded wait that runs
+ * out sets MOE_DEVERR_TIMEOUT and leaves NaN in the columns of out that were not
+ * reached.  Errors: MOE_ERR_UNSUPPORTED_SHAPE for other sizes,
+ * MOE_ERR_INVALID_ARG for NULL or misaligned pointers, T < 0, an unknown type or format.
+ */
+MOE_API moe_status moe_layer_few_workspace_bytes(int32_t T, int32_t E, int32_t K, int32_t I, size_t* bytes);
+MOE_API moe_status moe_layer_few(const moe_few* f, moe_stream_t stream);
+
+/*
  * Failure-detection self-test.  Runs one CTA whose wait on an mbarrier can
  * never complete, using the bounded-wait helper of the pipelined kernels with
  * a limit of limit_ns (0 < limit_ns <= 1 s).  The wait gives up, the kernel

@@ -1,0 +1,236 @@
+"""A whole layer for at most 8 tokens, against fp64.
+
+The routing has to equal moe_router_topk's rule on fp64 logits (the inputs leave
+gaps between them).  The output is held element by element to a bound that adds
+up what the steps may be off:
+  * an fp32 sum of products on the tensor cores keeps at least 13 bits of its
+    largest term while aligning: 2^-13 S, S the sum of the terms' magnitudes;
+  * with coded weights a value is represented within 2^-18 of its 128
+    neighbours' largest: r(v) = 2^-18 max|v|, none for bf16 weights;
+  * |silu'| <= 1.1 and |silu(g)| <= |g|: h is off by 1.1 |u| dg + |g| du, and by 2^-8
+    |h| for its rounding to bf16 (half a step, at the most) with 2^-18 |h| for
+    the exponential and the quotient;
+  * a weight w_k moves by the logits' error, at most 2^-14 relative here;
+  * the output's rounding: 2^-8 |out|.
+"""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+gpu = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module")
+def moe():
+    import combine_topk_multihot_gb300 as m
+    return m
+
+
+def make(moe, fmt, T, H, E, K, I, seed=0):
+    """(x, router, kept W1, scales, kept W2, scales, the fp64 weights they stand for)."""
+    g = torch.Generator(device=DEV).manual_seed(seed + T + H + E + K + I)
+    rnd = lambda *s, std=1.0: torch.randn(*s, generator=g, device=DEV) * std  # noqa: E731
+    x = (rnd(T, H) * torch.exp(rnd(T, 1))).bfloat16()
+    router = rnd(E, H, std=H ** -0.5).bfloat16()
+    W1, W2 = rnd(E, 2 * I, H, std=H ** -0.5).bfloat16(), rnd(E, H, I, std=I ** -0.5).bfloat16()
+    if fmt == "bf16":
+        return x, router, W1, None, W2, None, W1.double(), W2.double()
+    if fmt == "fp8":
+        (q1, s1), (q2, s2) = moe.moe_quantize_fp8_block(W1, 128), moe.moe_quantize_fp8_block(W2, 128)
+        val = lambda q, s: (q.view(torch.float8_e4m3fn).double()  # noqa: E731
+                            * s.double().repeat_interleave(128, 1).repeat_interleave(128, 2))
+    else:
+        (q1, s1), (q2, s2) = moe.moe_quantize_fp4_block(W1), moe.moe_quantize_fp4_block(W2)
+        val = lambda q, s: moe.moe_dequantize_fp4_block(q, s, torch.float32).double()  # noqa: E731
+    return x, router, q1, s1, q2, s2, val(q1, s1), val(q2, s2)
+
+
+def routing_of(x, router, K):
+    logits = x.double() @ router.double().t()
+    v, idx = logits.sort(dim=1, descending=True, stable=True)
+    return idx[:, :K], torch.softmax(v[:, :K], 1)
+
+
+def reference(x, idx, p, W1, W2, coded):
+    """(fp64 output, its bound)."""
+    T, H = x.shape
+    I = W2.shape[2]
+    rep = (lambda v: 2.0 ** -18 * v.view(-1, 128).abs().amax(1).repeat_interleave(128)) if coded else torch.zeros_like
+    out, lim = torch.zeros(T, H, dtype=torch.float64, device=x.device), torch.zeros(T, H, dtype=torch.float64, device=x.device)
+    for t in range(T):
+        v = x[t].double()
+        for e, w in {int(e): float(w) for e, w in zip(idx[t], p[t]) if e >= 0}.items():      # the last slot counts
+            gu, d = W1[e] @ v, 2.0 ** -13 * (W1[e].abs() @ v.abs()) + W1[e].abs() @ rep(v)
+            g, u = gu[:I], gu[I:]
+            h = g / (1 + torch.exp(-g)) * u
+            dh = 1.1 * (u.abs() + d[I:]) * d[:I] + g.abs() * d[I:] + (2.0 ** -8 + 2.0 ** -18) * h.abs()
+            o = W2[e] @ h
+            do = W2[e].abs() @ dh + 2.0 ** -13 * (W2[e].abs() @ h.abs()) + W2[e].abs() @ rep(h)
+            out[t] += w * o
+            lim[t] += w * (do + 2.0 ** -14 * o.abs())
+    return out, lim + 2.0 ** -8 * (out.abs() + lim)
+
+
+def check(got, ref, lim):
+    err = (got.double() - ref).abs()
+    assert (err <= lim).all(), float((err / lim).max())
+    rel = float(err.norm() / ref.norm())
+    assert rel < 2.0 ** -8, rel       # roundings of h and out, far from the sum of the bounds
+
+
+# one token to eight; one expert and 1024; more h than tokens and the other way round;
+# sizes where a CTA has no column of h or row of the output, several pieces of 16
+# rows of it, a row shorter than a piece of the ring and one that ends inside it;
+# h of all pairs in shared memory at once or not
+SHAPES = [(1, 256, 8, 2, 128), (3, 256, 1, 1, 128), (8, 512, 8, 8, 384), (1, 2048, 128, 8, 768), (8, 2048, 128, 8, 768),
+          (5, 768, 60, 6, 1024), (2, 8192, 4, 2, 128), (8, 256, 12, 3, 2048), (7, 1280, 1024, 16, 128), (4, 4096, 16, 4, 1280)]
+
+
+@gpu
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("T,H,E,K,I", SHAPES)
+def test_layer(moe, fmt, T, H, E, K, I):
+    x, router, W1, S1, W2, S2, V1, V2 = make(moe, fmt, T, H, E, K, I)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    buf = torch.full((T + 1, H), 7.0, dtype=torch.bfloat16, device=DEV)
+    out, idx, p = moe.moe_layer_few(x, router, K, W1, W2, S1, S2, return_routing=True, out=buf[:T], status=status)
+    assert (buf[T] == 7).all() and int(status) == 0
+    ridx, rp = routing_of(x, router, K)
+    assert torch.equal(idx, ridx)
+    assert ((p.double() - rp).abs() <= 2.0 ** -14 * rp).all()
+    check(out, *reference(x, ridx, rp, V1, V2, fmt != "bf16"))
+    assert torch.equal(moe.moe_layer_few(x, router, K, W1, W2, S1, S2), out)          # and every order is fixed
+    assert torch.equal(moe.moe_layer_few(x, router.float(), K, W1, W2, S1, S2), out)
+
+
+@gpu
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
+def test_given_routing(moe, fmt):
+    T, H, E, K, I = 6, 512, 16, 4, 256
+    x, router, W1, S1, W2, S2, V1, V2 = make(moe, fmt, T, H, E, K, I)
+    idx = torch.tensor([[0, 15, 3, 7], [-1, -1, -1, -1], [2, 2, 2, 5], [1, -1, 1, -1], [9, 8, 9, 8], [4, 4, 4, 4]], device=DEV)
+    p = torch.rand(T, K, device=DEV, generator=torch.Generator(device=DEV).manual_seed(3))
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = moe.moe_layer_few(x, None, K, W1, W2, S1, S2, routing=(idx, p), status=status)
+    ref, lim = reference(x, idx, p, V1, V2, fmt != "bf16")
+    check(out, ref, lim)
+    assert (out[1] == 0).all() and int(status) == 0
+    # the same as the layer in several steps, within both roundings
+    if fmt == "bf16":
+        long = moe.moe_layer(x, idx, p, W1, W2)
+        assert float((long.double() - ref).norm() / ref.norm()) < 2.0 ** -7
+    bad = idx.clone()
+    bad[0, 1], bad[3, 0] = E, -2
+    want = idx.clone()
+    want[0, 1], want[3, 0] = -1, -1
+    got = moe.moe_layer_few(x, None, K, W1, W2, S1, S2, routing=(bad, p), status=status)
+    assert int(status) == 1
+    assert torch.equal(got, moe.moe_layer_few(x, None, K, W1, W2, S1, S2, routing=(want, p)))
+    none = torch.full_like(idx, -1)
+    assert (moe.moe_layer_few(x, None, K, W1, W2, S1, S2, routing=(none, p)) == 0).all()
+
+
+@gpu
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
+def test_unusual_values(moe, fmt):
+    """A NaN or an infinity stays in its token's row; large, small and zero tokens; equal logits."""
+    T, H, E, K, I = 8, 256, 8, 2, 128
+    x, router, W1, S1, W2, S2, V1, V2 = make(moe, fmt, T, H, E, K, I)
+    x[1, 7], x[2, 100] = float("nan"), float("inf")
+    x[3] = 0
+    x[4] *= 2.0 ** 40
+    x[5] *= 2.0 ** -60
+    x[6, 1:] *= 2.0 ** -30               # one value that dwarfs its neighbours
+    out, idx, p = moe.moe_layer_few(x, router, K, W1, W2, S1, S2, return_routing=True)
+    assert not torch.isfinite(out[1]).any() and not torch.isfinite(out[2]).any()
+    assert idx[3].tolist() == [0, 1] and idx[1].tolist() == [0, 1] and (out[3] == 0).all()
+    rest = [0, 4, 5, 6, 7]
+    ridx, rp = routing_of(x[rest], router, K)
+    assert torch.equal(idx[rest], ridx)
+    ref, lim = reference(x[rest], ridx, p[rest].double(), V1, V2, fmt != "bf16")
+    err = (out[rest].double() - ref).abs()
+    # (2^-60 squared is in fp32's range; what lies below bf16's smallest normal number is off by its step)
+    assert (err <= lim + 2.0 ** -133).all()
+
+
+@gpu
+def test_streams_graphs_and_two_at_once(moe):
+    T, H, E, K, I = 2, 1024, 32, 4, 512
+    sets = [make(moe, fmt, T, H, E, K, I, seed=9) for fmt in ("bf16", "fp8", "fp4")]
+    want = [moe.moe_layer_few(s[0], s[1], K, s[2], s[4], s[3], s[5]) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [[moe.moe_layer_few(s[0], s[1], K, s[2], s[4], s[3], s[5], stream=st) for s, st in zip(sets, streams)]
+           for _ in range(20)]
+    torch.cuda.synchronize()
+    for row in got:
+        assert all(torch.equal(a, b) for a, b in zip(row, want))
+    graphs = []
+    for s in sets:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            o = s[0]
+            for _ in range(3):
+                o = moe.moe_layer_few(o, s[1], K, s[2], s[4], s[3], s[5])
+        graphs.append((g, o))
+    for s in sets:
+        s[0].copy_(-s[0])
+    want = []
+    for s in sets:
+        o = s[0]
+        for _ in range(3):
+            o = moe.moe_layer_few(o, s[1], K, s[2], s[4], s[3], s[5])
+        want.append(o)
+    for _ in range(3):
+        for (g, _), st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for (_, o), w in zip(graphs, want))
+
+
+def test_refusals_without_a_gpu(moe):
+    from combine_topk_multihot_gb300 import _native as N
+    p = 256
+
+    def call(**kw):
+        f = N.MoeFew(4, 8, 2, 256, 128, 0, 0, p, p, None, None, p, None, p, None, p, None, None, None, p)
+        for k, v in kw.items():
+            setattr(f, k, v)
+        return N.lib.moe_layer_few(f, None)
+
+    for kw in (dict(T=9), dict(E=0), dict(E=1025), dict(K=0), dict(K=9), dict(E=64, K=17), dict(H=0), dict(H=384), dict(I=0),
+               dict(I=64), dict(T=8, H=16384), dict(T=8, I=16384), dict(T=1, H=131072)):
+        assert call(**kw) == N.MOE_ERR_UNSUPPORTED_SHAPE, kw
+    for kw in (dict(T=-1), dict(weights=3), dict(weights=-1), dict(router_dtype=2), dict(x=None), dict(W1=None), dict(W2=None),
+               dict(out=None), dict(workspace=None), dict(router=None), dict(topk_idx=p), dict(router=None, topk_idx=p),
+               dict(weights=1), dict(weights=2, W1_scale=p), dict(idx_out=p), dict(probs_out=p), dict(x=p + 8), dict(W1=p + 2),
+               dict(router=p + 4), dict(workspace=p + 8), dict(out=p + 1), dict(weights=1, W1_scale=p + 2, W2_scale=p),
+               dict(status=p + 2)):
+        assert call(**kw) == N.MOE_ERR_INVALID_ARG, kw
+    assert N.lib.moe_layer_few(None, None) == N.MOE_ERR_INVALID_ARG
+    n = ctypes.c_size_t()
+    assert N.lib.moe_layer_few_workspace_bytes(9, 8, 2, 128, ctypes.byref(n)) == N.MOE_ERR_UNSUPPORTED_SHAPE
+    assert N.lib.moe_layer_few_workspace_bytes(8, 8, 2, 128, None) == N.MOE_ERR_INVALID_ARG
+    assert N.lib.moe_layer_few_workspace_bytes(8, 8, 2, 128, ctypes.byref(n)) == 0 and n.value == 256 + 256 + 8 * 2 * 128 * 2
+
+
+@gpu
+def test_refusals(moe):
+    T, H, E, K, I = 2, 256, 8, 2, 128
+    x, router, W1, S1, W2, S2, *_ = make(moe, "fp4", T, H, E, K, I)
+    ok = dict(x=x, router=router, top_k=K, W1=W1, W2=W2, W1_scale=S1, W2_scale=S2)
+    assert moe.moe_layer_few(**ok).shape == (T, H)
+    assert moe.moe_layer_few(**{**ok, "x": x[:0]}).shape == (0, H)
+    idx, p = torch.zeros(T, K, dtype=torch.int64, device=DEV), torch.zeros(T, K, device=DEV)
+    for kw, err in ((dict(x=x.float()), TypeError), (dict(x=x.cpu()), ValueError), (dict(x=x[:, ::2]), ValueError),
+                    (dict(W2_scale=None), ValueError), (dict(router=None), ValueError), (dict(routing=(idx, p)), ValueError),
+                    (dict(router=router.half()), TypeError), (dict(router=router[:4]), ValueError),
+                    (dict(router=None, routing=(idx.int(), p)), TypeError), (dict(W1=W1.view(E, -1, H)), ValueError),
+                    (dict(W1_scale=S1.float(), W2_scale=S2.float()), ValueError), (dict(W1_scale=None, W2_scale=None), TypeError),
+                    (dict(top_k=9), moe.MoEError), (dict(x=x.repeat(5, 1)), moe.MoEError)):
+        with pytest.raises(err):
+            moe.moe_layer_few(**{**ok, **kw})
