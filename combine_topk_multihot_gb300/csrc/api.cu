@@ -1158,7 +1158,7 @@ moe_status moe_layer_few(const moe_few* f, moe_stream_t stream) {
               "moe_layer_few: unknown weight format %d", f->weights);
   MOE_REQUIRE(f->router_dtype == MOE_DTYPE_BF16 || f->router_dtype == MOE_DTYPE_F32, MOE_ERR_INVALID_ARG,
               "moe_layer_few: unknown type %d", f->router_dtype);
-  MOE_REQUIRE(few_layer_fits(f->weights, f->T, f->K, f->H, f->I), MOE_ERR_UNSUPPORTED_SHAPE,
+  MOE_REQUIRE(few_layer_fits(f->T, f->K, f->H, f->I), MOE_ERR_UNSUPPORTED_SHAPE,
               "moe_layer_few: the rows of %d tokens of H=%d and I=%d do not fit in shared memory", f->T, f->H, f->I);
   const bool coded = f->weights != MOE_WEIGHTS_BF16;
   MOE_REQUIRE(f->T == 0 || (f->x && f->W1 && f->W2 && f->out && f->workspace && (!coded || (f->W1_scale && f->W2_scale))),

@@ -8,8 +8,6 @@
 // 16 (r % 32) + 4 (r / 32); [row tiles, block tiles] of them a matrix.
 #pragma once
 
-#include <cuda_fp4.h>
-
 #include "common.cuh"
 #include "fp8_quant.cuh"
 
@@ -44,27 +42,38 @@ __device__ __forceinline__ float e8m0_value(uint32_t e) {
   return __uint_as_float(e == 0u ? 0x00400000u : e == 255u ? 0x7fc00000u : e << 23);
 }
 
-// Eight codes (the first in the lowest bits) of values already divided by their scale.
-__device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
-  uint32_t c = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    c |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(make_float2(v[2 * i], v[2 * i + 1]), __NV_E2M1, cudaRoundNearest)) << (8 * i);
+// Two codes (the first in the lower four bits) of values already divided by
+// their scale: to nearest even, saturated.  (The conversions are written as
+// instructions here: the toolkit's header takes this chip for one without them.)
+__device__ __forceinline__ uint32_t e2m1x2(float first, float second) {
+  uint32_t c;
+  asm("{\n\t.reg .b8 c;\n\t.reg .b16 h;\n\tcvt.rn.satfinite.e2m1x2.f32 c, %2, %1;\n\tmov.b16 h, {c, 0};\n\tcvt.u32.u16 %0, h;\n\t}"
+      : "=r"(c) : "f"(first), "f"(second));
   return c;
 }
-
-// Eight e2m1 codes as e4m3 codes of 2^-6 times their values: the even ones
-// (codes 0, 2, 4, 6 of the word, lowest byte first) and the odd ones.  Both
-// formats have subnormals, so that moving sign, exponent and mantissa bits into
-// place is exact for every code.
-__device__ __forceinline__ uint32_t e4m3_of_even(uint32_t w) { return ((w << 4) & 0x80808080u) | ((w << 2) & 0x1c1c1c1cu); }
-__device__ __forceinline__ uint32_t e4m3_of_odd(uint32_t w) { return (w & 0x80808080u) | ((w >> 2) & 0x1c1c1c1cu); }
-
-__device__ __forceinline__ void mma_e4m3_16x8x32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                                 uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
+// Eight codes, the first in the lowest bits.
+__device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
+  return e2m1x2(v[0], v[1]) | e2m1x2(v[2], v[3]) << 8 | e2m1x2(v[4], v[5]) << 16 | e2m1x2(v[6], v[7]) << 24;
+}
+// The eight codes of a word as pairs of f16.
+__device__ __forceinline__ void f16_of_e2m1x8(uint32_t w, uint32_t (&v)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(w));
+}
+// The four scales of a word as pairs of bf16.
+__device__ __forceinline__ void bf16_of_e8m0x4(uint32_t w, uint32_t (&v)[2]) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.bf16x2.ue8m0x2 %0, a;\n\tcvt.rn.bf16x2.ue8m0x2 %1, b;\n\t}"
+      : "=r"(v[0]), "=r"(v[1]) : "r"(w));
+}
+// The four e4m3 codes of a word as pairs of f16.
+__device__ __forceinline__ void f16_of_e4m3x4(uint32_t w, uint32_t (&v)[2]) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(v[0]), "=r"(v[1]) : "r"(w));
+}
+__device__ __forceinline__ void mma_f16_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                                uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }

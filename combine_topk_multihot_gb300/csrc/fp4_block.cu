@@ -1,6 +1,8 @@
 // Microscaled 4-bit floating point: quantisation, the way back, and the dense
 // product with few rows.  The format is in fp4.cuh.
 
+#include <cuda_fp16.h>
+
 #include "fp4.cuh"
 #include "launch.h"
 
@@ -87,11 +89,12 @@ __global__ void __launch_bounds__(256) dequantize_fp4_kernel(const uint8_t* __re
     const long long mat = r / rows;
     const uint32_t c = __ldcs(reinterpret_cast<const uint32_t*>(codes) + i);
     const float f = e8m0_value(__ldg(scales + mat * tiles + scale_word(r - mat * rows, w >> 4, kts) + ((w >> 2) & 3)));
+    uint32_t halves[4];
+    f16_of_e2m1x8(c, halves);
     float v[8];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(c >> (8 * k)), __NV_E2M1);
-      const float2 t = __half22float2(__half2(h));
+      const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&halves[k]));
       v[2 * k] = t.x * f, v[2 * k + 1] = t.y * f;
     }
     if constexpr (F32) {
@@ -109,15 +112,15 @@ __global__ void __launch_bounds__(256) dequantize_fp4_kernel(const uint8_t* __re
 
 // The product with at most 8 rows is a stream over the weights: a warp takes 16
 // of their rows and a slice of K, and multiplies with mma.sync, the 8 rows as its
-// other operand.  Codes become e4m3 codes (exact) in registers; lane t of a row's
-// four takes word t of each block of 32, so that one instruction's 32 products
-// share their scales, which are applied to its sums.  The slices of K are joined in shared memory in a fixed order.
-// 2^(ea + eb - 242) (the codes' products come 2^-12 too small) as two factors:
-// their product may leave fp32's range where the value does not.
+// other operand.  Codes become f16 numbers (exact) in registers; lane t of a row's
+// four takes word t of each block of 32, so that two instructions' 32 products
+// share their scales, which are applied to the sums.  The slices of K are joined in shared memory in a fixed order.
+// 2^(ea + eb - 254) as two factors: their product may leave fp32's range where
+// the value does not.
 struct Scale2 {
   float f1, f2;
   __device__ __forceinline__ Scale2(uint32_t ea, uint32_t eb) {
-    const int s = static_cast<int>(ea + eb) - 242, h = s >> 1;
+    const int s = static_cast<int>(ea + eb) - 254, h = s >> 1;
     const bool nan = ea == 255u || eb == 255u;
     f1 = nan ? __uint_as_float(0x7fc00000u) : __uint_as_float(static_cast<uint32_t>(min(h, 127) + 127) << 23);
     f2 = __uint_as_float(static_cast<uint32_t>(min(s - h, 127) + 127) << 23);
@@ -175,8 +178,12 @@ __global__ void __launch_bounds__(256, 3) fp4_stream_kernel(const StreamArgs arg
       for (int j = 0; j < 4; ++j) {
         if (kt * 4 + j >= args.K / FP4_BLOCK) break;  // past the last block: its scales are no one's
         float d[4] = {0.f, 0.f, 0.f, 0.f};
-        mma_e4m3_16x8x32(d, e4m3_of_even(cl[j]), e4m3_of_even(ch[j]), e4m3_of_odd(cl[j]), e4m3_of_odd(ch[j]),
-                         e4m3_of_even(cr[j]), e4m3_of_odd(cr[j]));
+        uint32_t lo[4], hi[4], row[4];
+        f16_of_e2m1x8(cl[j], lo);
+        f16_of_e2m1x8(ch[j], hi);
+        f16_of_e2m1x8(cr[j], row);
+        mma_f16_16x8x16(d, lo[0], hi[0], lo[1], hi[1], row[0], row[1]);
+        mma_f16_16x8x16(d, lo[2], hi[2], lo[3], hi[3], row[2], row[3]);
         // this lane's sums are those of rows 2t and 2t + 1, weight rows g and g + 8
 #pragma unroll
         for (int i = 0; i < 4; ++i) {

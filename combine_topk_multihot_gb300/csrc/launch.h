@@ -305,7 +305,7 @@ struct FewLayer {
   float* probs_out;
   int* status;
 };
-bool few_layer_fits(int format, int T, int K, int H, int I);
+bool few_layer_fits(int T, int K, int H, int I);
 cudaError_t launch_few_layer(const FewLayer& f, cudaStream_t s);
 
 // AdamW over many tensors (adamw.cu), up to ADAMW_BATCH of them a launch.

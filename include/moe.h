@@ -775,9 +775,9 @@ MOE_API moe_status moe_matmul_fp4_block(const uint8_t* a_q, const uint8_t* a_sca
  *   W2_scale [E, H/128, I/128] fp32);
  *   MOE_WEIGHTS_FP4_BLOCK: e2m1 codes with scales in tiles
  *   (moe_quantize_fp4_block: W1_scale [E, 2I/128, H/128, 32, 4, 4], ...).
- * x and h are not rounded to 8 bits for the codes: they are multiplied as the sum
- * of two e4m3 numbers, exact for a bf16 value of 2^-10 of the largest of its 128
- * neighbours or more, and within 2^-18 of that largest below it.  A token with
+ * x and h are not rounded to 8 bits for the codes: they are multiplied as f16
+ * numbers with a power of two for each 128 of a row, exact for a bf16 value of
+ * 2^-31 of the largest of the 128 or more, and within 2^-39 of that largest below it.  A token with
  * a NaN or an infinity has a NaN or infinity in its own row alone.
  */
 typedef enum moe_weights { MOE_WEIGHTS_BF16 = 0, MOE_WEIGHTS_FP8_BLOCK = 1, MOE_WEIGHTS_FP4_BLOCK = 2 } moe_weights;
