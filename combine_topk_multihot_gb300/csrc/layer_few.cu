@@ -63,15 +63,12 @@ __host__ __device__ constexpr int token_pitch(int K) { return 2 * K + 64; }
 
 struct Smem {
   int ok;
-  int active;
   int expert[PAIRS];         // ascending
   int first[PAIRS + 1];      // pairs before each: its first row of h
   float weight[PAIRS][TOK];
   int row[PAIRS][TOK];       // of h, of each token; -1: none
-  int4 chosen4[PAIRS / 4];   // expert of each pair, by token and slot; -1: none
-  int4 token4[PAIRS / 4];    // 1 << its token
-  int4 named4[PAIRS / 4];    // where a pair is the first of its expert: the expert's tokens, else 0
-  float prob[PAIRS];
+  uint32_t seen[32];         // a bit for each expert with tokens
+  int tokens[1024];          // the tokens of each expert, a bit each
   float part[2][WARPS][4][32];
 };
 
@@ -192,7 +189,7 @@ __device__ __forceinline__ float of_key(uint32_t k) { return __uint_as_float(k ^
 // ascending index, as moe_router_topk has them, and their softmax.  A lane keeps
 // its logits (32 at the most) in registers, J of them, and the best of those.
 template <int J>
-__device__ __forceinline__ void pick_experts(const float* logits, int E, int K, int lane, int* chosen, float* prob) {
+__device__ __forceinline__ void pick_experts(const float* logits, int E, int K, int lane, int& chosen, float& prob) {
   uint32_t key[J];
 #pragma unroll
   for (int j = 0; j < J; ++j) key[j] = lane + 32 * j < E ? sort_key(__ldcg(logits + lane + 32 * j)) : 0u;
@@ -218,7 +215,7 @@ __device__ __forceinline__ void pick_experts(const float* logits, int E, int K, 
   float sum = ex;
 #pragma unroll
   for (int o = MAX_K / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL_MASK, sum, o);
-  if (lane < K) chosen[lane] = mine, prob[lane] = ex / sum;
+  if (lane < K) chosen = mine, prob = ex / sum;  // lane k's slot k
 }
 
 // ---------------------------------------------------------------- rows of tokens
@@ -276,89 +273,109 @@ __device__ __forceinline__ void stage_rows(const uint16_t* src, int rows, int K,
 // sixteenth piece of all experts' rows).
 template <int FMT>
 struct Cursor {
-  const FewArgs& args;
   const Smem& s;
-  const int warp, lane;
+  const int active, warp, lane, I;
   const int bytes1, bytes2, steps1, steps2;  // bytes and pieces of a row
   int a, j0, left;           // first product: expert (place in the list), column, columns to come
   int m0, left2;             // second product: row of the output, rows to come
-  int st;                    // piece
+  int st, steps;             // piece, pieces of a row
   bool first;
-  // of the tile: this lane's 16 bytes of the piece in rows lane / 8 of both halves, and the halves' rows
-  const uint8_t *lo, *hi;
-  int n_lo, n_hi;
-  const uint8_t* scale;      // fp8, fp4: the first word of row lane % 16
+  int n_lo, n_hi, rb;        // rows of the tile's halves, bytes of a row
+  const uint32_t part;       // where this lane's 16 bytes of rows lane / 8 go in a slot; four rows on: ^ 32
+  // this lane's 16 bytes of the piece: in row lane / 8 of the expert's rows, of the tile's halves
+  const uint8_t *base, *lo, *hi;
+  long long stride;          // bytes of an expert
+  // fp8, fp4: the first word of row lane % 16, in the expert's scales and the tile's
+  const uint8_t *scale_base, *scale;
+  long long scale_stride;
+  const FewArgs& args;
 
-  __device__ __forceinline__ Cursor(const FewArgs& args_, const Smem& s_, int warp_, int lane_, int a_, int j0_, int cols, int r0, int rows)
-      : args(args_), s(s_), warp(warp_), lane(lane_), bytes1(row_bytes<FMT>(args_.H)), bytes2(row_bytes<FMT>(args_.I)),
+  __device__ __forceinline__ Cursor(const FewArgs& args_, const Smem& s_, int active_, int warp_, int lane_, int a_, int j0_, int cols, int r0, int rows)
+      : s(s_), active(active_), warp(warp_), lane(lane_), I(args_.I), bytes1(row_bytes<FMT>(args_.H)), bytes2(row_bytes<FMT>(args_.I)),
         steps1((bytes1 + PIECE - 1) / PIECE), steps2((bytes2 + PIECE - 1) / PIECE), a(a_), j0(j0_), left(cols), m0(r0), left2(rows),
-        st(warp_ % TEAM), first(true) {
+        st(warp_ % TEAM), steps(steps1), first(true), rb(bytes1),
+        part((lane_ >> 3) * PIECE + (((lane_ & 7) ^ (((lane_ >> 3) & 1) * 4 + (lane_ >> 4))) << 4)), args(args_) {
     for (int i = 0; i < warp / TEAM; ++i) skip_tile();
     if (st >= steps1) left = 0;  // no piece for this warp
-    aim();
+    base = args.W1 + static_cast<long long>(lane >> 3) * bytes1 + (lane & 7) * 16;
+    stride = 2ll * I * bytes1;
+    if constexpr (FMT != FEW_BF16) scale_stride = scales(2 * I, args.H);
+    if (left > 0) aim1(); else second();
   }
-  __device__ __forceinline__ int tile() const { return min(8, min(left, args.I - j0)); }
+  // scales of a matrix of [rows, K], and of the 128 rows with row r in it
+  __device__ __forceinline__ long long scales(int rows, int K) const {
+    return static_cast<long long>(rows >> 7) * (K >> 7) * (FMT == FEW_FP8 ? 4 : SCALE_TILE);
+  }
+  __device__ __forceinline__ const uint8_t* row_scales(const uint8_t* of, int K, int r) const {
+    of += scales(r, K);
+    return FMT == FEW_FP8 ? of : of + (r & 31) * 16 + ((r >> 5) & 3) * 4;
+  }
+  __device__ __forceinline__ int tile() const { return min(8, min(left, I - j0)); }
   __device__ __forceinline__ void skip_tile() {
     const int n = tile();
     left -= n;
     j0 += n;
-    if (j0 == args.I) j0 = 0, ++a;
+    if (j0 == I) j0 = 0, ++a;
   }
   __device__ __forceinline__ bool more() const { return left2 > 0; }
-  // scales of row r of matrix e of [rows, K]
-  __device__ __forceinline__ const uint8_t* scales_of(const void* base, int e, int rows, int K, int r) const {
-    const int kbs = K >> 7;
-    if constexpr (FMT == FEW_FP8) return static_cast<const uint8_t*>(base) + (static_cast<long long>(e) * (rows >> 7) + (r >> 7)) * (kbs * 4);
-    return static_cast<const uint8_t*>(base) + (static_cast<long long>(e) * (rows >> 7) + (r >> 7)) * (kbs * SCALE_TILE) +
-           (r & 31) * 16 + ((r >> 5) & 3) * 4;
+  __device__ __forceinline__ void aim1() {
+    n_lo = n_hi = tile();
+    const int e = s.expert[a];
+    lo = base + e * stride + static_cast<long long>(j0) * bytes1;
+    hi = lo + static_cast<long long>(I) * bytes1;
+    if constexpr (FMT != FEW_BF16)
+      scale = row_scales(static_cast<const uint8_t*>(args.S1) + e * scale_stride, args.H,
+                         j0 + min(lane & 7, n_lo - 1) + (lane & 8 ? I : 0));
   }
-  __device__ __forceinline__ void aim() {
-    const int r = lane & 15;
-    if (first && left > 0) {
-      n_lo = n_hi = tile();
-      const int e = s.expert[a], I = args.I;
-      lo = args.W1 + (static_cast<long long>(e) * 2 * I + j0 + (lane >> 3)) * bytes1 + (lane & 7) * 16;
-      hi = lo + static_cast<long long>(I) * bytes1;
-      if constexpr (FMT != FEW_BF16) scale = scales_of(args.S1, e, 2 * I, args.H, j0 + min(r & 7, n_lo - 1) + (r < 8 ? 0 : I));
-      return;
-    }
-    if (first) {
-      first = false;
-      a = 0;
-      st = warp;
-    }
-    while (left2 > 0) {
-      while (a < s.active && st >= steps2) st -= steps2, ++a;
-      if (a < s.active) break;
-      m0 += 16;
-      left2 -= 16;
-      a = 0;
-      st = warp;
-    }
-    if (left2 <= 0) return;
-    const int n = min(16, left2), e = s.expert[a];
+  // the 16 rows of the output from m0
+  __device__ __forceinline__ void rows_at() {
+    base = args.W2 + static_cast<long long>(m0 + (lane >> 3)) * bytes2 + (lane & 7) * 16;
+    const int n = min(16, left2);
     n_lo = min(n, 8);
     n_hi = n - n_lo;
-    lo = args.W2 + (static_cast<long long>(e) * args.H + m0 + (lane >> 3)) * bytes2 + (lane & 7) * 16;
+    if constexpr (FMT != FEW_BF16) scale_base = row_scales(static_cast<const uint8_t*>(args.S2), I, m0 + min(lane & 15, n - 1));
+    a = 0;
+    st = warp;
+  }
+  __device__ __forceinline__ void second() {
+    first = false;
+    steps = steps2;
+    rb = bytes2;
+    stride = static_cast<long long>(args.H) * bytes2;
+    if constexpr (FMT != FEW_BF16) scale_stride = scales(args.H, I);
+    if (active == 0) left2 = 0;
+    if (left2 <= 0) return;
+    rows_at();
+    aim2();
+  }
+  __device__ __forceinline__ void aim2() {
+    while (st >= steps2) {
+      st -= steps2;
+      if (++a == active) {
+        m0 += 16;
+        left2 -= 16;
+        if (left2 <= 0) return;
+        rows_at();
+      }
+    }
+    const int e = s.expert[a];
+    lo = base + e * stride;
     hi = lo + 8ll * bytes2;
-    if constexpr (FMT != FEW_BF16) scale = scales_of(args.S2, e, args.H, args.I, m0 + min(r, n - 1));
+    if constexpr (FMT != FEW_BF16) scale = scale_base + e * scale_stride;
   }
   // Asks for the piece and goes on to the next.  Row r's 16-byte part c goes to
   // part c ^ (r % 2 * 4 + r / 2 % 4): a quarter warp's four parts of each of two
   // rows, and a warp's one part of each of eight rows, meet different banks.
   __device__ __forceinline__ void issue(uint32_t slot) {
     if (more()) {
-      const int rb = first ? bytes1 : bytes2, row = lane >> 3, c = lane & 7;
-      const int at = st * PIECE;
-      if (at + c * 16 < rb) {
+      const int row = lane >> 3, at = st * PIECE;
+      if (at + (lane & 7) * 16 < rb) {
+        const uint32_t dst = slot + part, dst4 = slot + ((part + 4 * PIECE) ^ 32);
         const uint8_t *p = lo + at, *q = hi + at;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = row + 4 * i;
-          const uint32_t dst = slot + r * PIECE + ((c ^ ((r & 1) * 4 + (r >> 1))) << 4);
-          if (r < n_lo) cp_async_16(dst, p + 4 * i * rb);
-          if (r < n_hi) cp_async_16(dst + 8 * PIECE, q + 4 * i * rb);
-        }
+        if (row < n_lo) cp_async_16(dst, p);
+        if (row + 4 < n_lo) cp_async_16(dst4, p + 4 * rb);
+        if (row < n_hi) cp_async_16(dst + 8 * PIECE, q);
+        if (row + 4 < n_hi) cp_async_16(dst4 + 8 * PIECE, q + 4 * rb);
       }
       if constexpr (FMT == FEW_FP8) {
         if (lane < 16) cp_async_4(slot + 16 * PIECE + lane * 4, scale + st * 4);
@@ -366,16 +383,15 @@ struct Cursor {
         const int kb = 2 * st + (lane >> 4);
         if (kb * 64 < rb) cp_async_4(slot + 16 * PIECE + lane * 4, scale + kb * SCALE_TILE);
       }
-      if (first) {
-        st += TEAM;
-        if (st >= steps1) {
+      st += first ? TEAM : WARPS;
+      if (st >= steps) {
+        if (first) {
           st = warp % TEAM;
           for (int i = 0; i < WARPS / TEAM; ++i) skip_tile();
-          aim();
+          if (left > 0) aim1(); else second();
+        } else {
+          aim2();
         }
-      } else {
-        st += WARPS;
-        if (st >= steps2) aim();
       }
     }
     cp_async_commit();
@@ -464,93 +480,84 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
   Smem& s = *reinterpret_cast<Smem*>(region + args.region);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int T = args.T, E = args.E, K = args.K, H = args.H, I = args.I;
-  griddep_launch_dependents();
-  const int pairs = T * K;
-  int* chosen = reinterpret_cast<int*>(s.chosen4);
-  int* named = reinterpret_cast<int*>(s.named4);
-  if (threadIdx.x < PAIRS) {
-    chosen[threadIdx.x] = -1;
-    named[threadIdx.x] = 0;
-    reinterpret_cast<int*>(s.token4)[threadIdx.x] = threadIdx.x < pairs ? 1 << threadIdx.x / K : 0;
-  }
-  if (threadIdx.x == 0) s.active = 0;
-  griddep_wait();
+  // (no griddep_launch_dependents(): CTAs of the next kernel that wait beside this
+  // one's cost it 1.2 us)
+  for (int e = threadIdx.x; e < E; e += THREADS) s.tokens[e] = 0;
+  for (int i = threadIdx.x; i < PAIRS * TOK; i += THREADS) s.weight[0][i] = 0.f;
+  if (threadIdx.x < 32) s.seen[threadIdx.x] = 0;
   __syncthreads();
+  griddep_wait();
 
   // the routing, a warp a token; the other warps bring the tokens
   float* s_scale = reinterpret_cast<float*>(region + T * token_pitch(H));
+  int chosen = -1;
+  float prob = 0.f;
   if (warp >= TOK) {
     stage_rows<FMT>(args.x, T, H, region, s_scale, threadIdx.x - 32 * TOK, THREADS - 32 * TOK);
   } else if (warp < T) {
     if (args.logits) {
       const float* l = args.logits + warp * E;
-      if (E <= 128) pick_experts<4>(l, E, K, lane, chosen + warp * K, s.prob + warp * K);
-      else if (E <= 512) pick_experts<16>(l, E, K, lane, chosen + warp * K, s.prob + warp * K);
-      else pick_experts<32>(l, E, K, lane, chosen + warp * K, s.prob + warp * K);
+      if (E <= 128) pick_experts<4>(l, E, K, lane, chosen, prob);
+      else if (E <= 512) pick_experts<16>(l, E, K, lane, chosen, prob);
+      else pick_experts<32>(l, E, K, lane, chosen, prob);
     } else if (lane < K) {
-      long long e = args.topk_idx[warp * K + lane];
-      if (e < -1 || e >= E) {
-        if (blockIdx.x == 0) report(args.status, MOE_DEVERR_BAD_INDEX);
-        e = -1;
-      }
-      chosen[warp * K + lane] = static_cast<int>(e);
-      s.prob[warp * K + lane] = args.topk_probs[warp * K + lane];
+      const long long e = args.topk_idx[warp * K + lane];
+      prob = args.topk_probs[warp * K + lane];
+      if (e >= 0 && e < E) chosen = static_cast<int>(e);
+      else if (e != -1 && blockIdx.x == 0) report(args.status, MOE_DEVERR_BAD_INDEX);
+    }
+    if (chosen >= 0) {
+      atomicOr(&s.seen[chosen >> 5], 1u << (chosen & 31));
+      atomicOr(&s.tokens[chosen], 1 << warp);
     }
     if (lane < K && blockIdx.x == 0 && args.idx_out) {
-      args.idx_out[warp * K + lane] = chosen[warp * K + lane];
-      args.probs_out[warp * K + lane] = s.prob[warp * K + lane];
+      args.idx_out[warp * K + lane] = chosen;
+      args.probs_out[warp * K + lane] = prob;
     }
   }
   __syncthreads();
-  // the experts with tokens, ascending: a thread a pair
-  const int pair = threadIdx.x;
-  int e = -1, last = 1;
-  if (pair < pairs) {
-    e = chosen[pair];
-    const int mine = 1 << pair / K;
-    int tokens = 0, before = 0;
-    for (int q = 0; q < (pairs + 3) / 4; ++q) {
-      const int4 c = s.chosen4[q], m = s.token4[q];
-      auto look = [&](int other, int bit, int at) {
-        if (other != e) return;
-        tokens |= bit;
-        before |= at < pair;
-        if (bit == mine && at > pair) last = 0;  // of an expert that a token names twice the last slot counts
-      };
-      look(c.x, m.x, 4 * q);
-      look(c.y, m.y, 4 * q + 1);
-      look(c.z, m.z, 4 * q + 2);
-      look(c.w, m.w, 4 * q + 3);
-    }
-    if (e >= 0 && !before) named[pair] = tokens;
+  // the experts with tokens, ascending: each warp counts those before each 32
+  const uint32_t bits = s.seen[lane];
+  int upto = __popc(bits);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(FULL_MASK, upto, o);
+    if (lane >= o) upto += v;
+  }
+  for (int w = warp; w * 32 < E; w += WARPS) {
+    const uint32_t there = __shfl_sync(FULL_MASK, bits, w);
+    const int before = __shfl_sync(FULL_MASK, upto, w) - __popc(there);
+    if ((there >> lane) & 1) s.expert[before + __popc(there & ((1u << lane) - 1u))] = w * 32 + lane;
+  }
+  if (warp < T) {  // (of an expert that a token names twice the last slot counts)
+    const int word = max(chosen, 0) >> 5;
+    const uint32_t same = __match_any_sync(FULL_MASK, chosen), there = __shfl_sync(FULL_MASK, bits, word);
+    const int before = __shfl_sync(FULL_MASK, upto, word) - __popc(there);
+    if (chosen >= 0 && lane == 31 - __clz(same)) s.weight[before + __popc(there & ((1u << (chosen & 31)) - 1u))][warp] = prob;
   }
   __syncthreads();
-  if (e >= 0) {
-    int place = 0, rows = 0;
-    for (int q = 0; q < (pairs + 3) / 4; ++q) {
-      const int4 c = s.chosen4[q], m = s.named4[q];
-      auto count = [&](int other, int tokens) {
-        const int n = other < e ? __popc(tokens) : 0;
-        place += n != 0;
-        rows += n;
-      };
-      count(c.x, m.x);
-      count(c.y, m.y);
-      count(c.z, m.z);
-      count(c.w, m.w);
+  const int active = __shfl_sync(FULL_MASK, upto, 31);
+  if (warp == 0) {  // and their rows of h
+    int row = 0;
+    for (int a0 = 0; a0 < active; a0 += 32) {
+      const int m = a0 + lane < active ? s.tokens[s.expert[a0 + lane]] : 0;
+      int n = __popc(m);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(FULL_MASK, n, o);
+        if (lane >= o) n += v;
+      }
+      if (a0 + lane < active) {
+        int r = row + n - __popc(m);
+        s.first[a0 + lane] = r;
+#pragma unroll
+        for (int t = 0; t < TOK; ++t) s.row[a0 + lane][t] = (m >> t) & 1 ? r++ : -1;
+      }
+      row += __shfl_sync(FULL_MASK, n, 31);
     }
-    if (const int m = named[pair]) {
-      s.expert[place] = e;
-      s.first[place] = rows;
-      s.first[place + 1] = rows + __popc(m);  // (the next one's, if there is one: the same)
-      for (int t = 0; t < TOK; ++t) s.row[place][t] = (m >> t) & 1 ? rows + __popc(m & ((1 << t) - 1)) : -1;
-      atomicMax(&s.active, place + 1);
-    }
-    if (last) s.weight[place][pair / K] = s.prob[pair];
+    if (lane == 0) s.first[active] = row;
   }
-  __syncthreads();
 
-  const int active = s.active;
   const uint32_t G = gridDim.x, b = blockIdx.x;
   // this CTA's columns of h, numbered through the experts, and rows of the output
   const uint32_t cols = static_cast<uint32_t>(active) * I;
@@ -559,8 +566,9 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
   const int r0 = b * static_cast<uint32_t>(H) / G, r1 = (b + 1) * static_cast<uint32_t>(H) / G;
   const int bytes1 = row_bytes<FMT>(H), bytes2 = row_bytes<FMT>(I);
   const uint32_t slots = smem_u32(smem) + warp * args.slots * SLOT;
-  Cursor<FMT> cursor(args, s, warp, lane, first_a, first_j, my_cols, r0, r1 - r0);
+  Cursor<FMT> cursor(args, s, active, warp, lane, first_a, first_j, my_cols, r0, r1 - r0);
   for (int i = 0; i < args.slots; ++i) cursor.issue(slots + i * SLOT);
+  __syncthreads();
   int slot = 0;
   auto next = [&](float (&d)[4], int st, int bytes, uint32_t token, const float* s0, const float* s1) {
     cp_async_wait(args.slots - 1);
