@@ -43,6 +43,10 @@ bool make_tma_2d_bf16(CUtensorMap* map, const void* base, uint64_t rows, uint64_
 bool make_tma_2d_u8(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                     uint32_t box_rows);
 
+// Scales of 4-bit codes in tiles of 512 bytes, [row tiles, block tiles], read as
+// two neighbouring tiles of one row.
+bool make_tma_scale_tiles(CUtensorMap* map, const void* base, uint64_t row_tiles, uint64_t block_tiles);
+
 // Tensor maps whose boxes carry 128 columns of K as two 64-column sub-tiles
 // (128-byte swizzle; sub-tile j follows sub-tile j - 1 in shared memory), so
 // one TMA operation moves a whole 128-wide K step:

@@ -55,6 +55,18 @@ bool make_tma_2d_u8(CUtensorMap* map, const void* base, uint64_t rows, uint64_t 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_tma_scale_tiles(CUtensorMap* map, const void* base, uint64_t row_tiles, uint64_t block_tiles) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn || row_tiles == 0 || block_tiles == 0) return false;
+  const cuuint64_t dims[2] = {block_tiles * 128, row_tiles};  // words
+  const cuuint64_t strides[1] = {block_tiles * 512};
+  const cuuint32_t box[2] = {256, 1};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool make_tma_w1_gate_up_k128(CUtensorMap* map, const void* W1, uint64_t E, uint64_t I, uint64_t H) {
   EncodeTiledFn fn = encode_fn();
   if (!fn || E == 0 || I == 0 || H == 0 || H % 128) return false;
