@@ -6,9 +6,9 @@
 // The tensor cores apply these scales themselves (tcgen05.mma kind::mxf4, 64
 // codes an instruction): they are read from tensor memory, where tcgen05.cp puts
 // each tile of 128 rows' scales, 512 bytes, from shared memory.
-//   * warp 0 stages codes (128-byte swizzle, 256 codes a stage) and scales by TMA,
-//     warp 1 copies a stage's scales to its own columns of tensor memory and
-//     issues its MMAs, warps 4..11 take the finished tile out: to bf16 in
+//   * warps 0 and 3 stage codes (128-byte swizzle, 256 codes a stage) and scales by
+//     TMA, warp 2 copies a stage's scales to its own columns of tensor memory while
+//     warp 1 issues the MMAs of the stage before, warps 4..11 take the finished tile out: to bf16 in
 //     registers, which frees the accumulator, then through shared memory and TMA
 //     stores;
 //   * a stage's scale columns are written again only after the MMAs that read
@@ -55,9 +55,10 @@ struct Shape {
 struct Smem {
   uint64_t full[MAX_STAGES];
   uint64_t empty[MAX_STAGES];
+  uint64_t scaled[MAX_STAGES];  // the stage's scales are in tensor memory
   uint64_t tfull[2];
   uint64_t tempty[2];
-  uint64_t drain;
+  uint64_t drain[2];
   uint32_t tmem_base;
   int abort;
 };
@@ -113,6 +114,19 @@ __device__ __forceinline__ void tc_mma_mxf4(uint32_t d_tmem, uint64_t a_desc, ui
         : "memory");
 }
 
+// One lane of a warp that runs as a whole, always the same: what such a lane
+// issues has its operands in uniform registers already (in a branch for lane 0
+// each MMA or load took 80 to 200 cycles to issue).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+// A barrier's wait by the whole warp.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  return __all_sync(FULL_MASK, mbar_wait(bar, parity, abort_flag));
+}
+
 template <bool PAIR>
 __device__ __forceinline__ void commit(uint32_t bar) {
   if constexpr (PAIR) tc_commit_pair(bar);
@@ -156,12 +170,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(smem_u32(&s.full[i]), 1);
       mbar_init(smem_u32(&s.empty[i]), 1);
+      mbar_init(smem_u32(&s.scaled[i]), 1);
     }
     for (int i = 0; i < BUFS; ++i) {
       mbar_init(smem_u32(&s.tfull[i]), 1);
       mbar_init(smem_u32(&s.tempty[i]), CTAS * EPI_WARPS);
     }
-    mbar_init(smem_u32(&s.drain), 1);
+    for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&s.drain[i]), 1);
     s.abort = 0;
     mbar_fence_init();
     tma_prefetch_desc(&tmA);
@@ -183,8 +198,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t tmem_base = s.tmem_base;
   volatile int* abort_flag = &s.abort;
 
-  if (warp == 0 && lane == 0) {
-    // ================= TMA producer =================
+  if (warp == 0 || warp == 3) {
+    // ================= TMA producers: a and its scales, b and its scales =================
     int stage = 0;
     uint32_t phase = 0;
     long long issued = 0;
@@ -193,19 +208,21 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int mt = tile / args.n_tiles, n0 = (tile - mt * args.n_tiles) * BN;
       const int row_tile = mt * CTAS + rank;  // this CTA's 128 rows of a
       for (int ks = 0; ks < args.k_steps; ++ks) {
-        if (!mbar_wait(smem_u32(&s.empty[stage]), phase ^ 1u, abort_flag)) { ok = false; break; }
+        if (!warp_wait(smem_u32(&s.empty[stage]), phase ^ 1u, abort_flag)) { ok = false; break; }
         const uint32_t full = smem_u32(&s.full[stage]), full0 = PAIR ? mapa_shared(full, 0) : full;
         const uint32_t a_dst = tiles_u32 + stage * (S::A_BYTES + S::B_BYTES);
         const uint32_t sf = sf_u32 + stage * S::SF_BYTES;
-        // (what lies past a matrix arrives as zeros)
-        if (rank == 0) mbar_arrive_expect_tx(full, CTAS * S::STAGE_BYTES);
-        load<PAIR>(a_dst, &tmA, ks * 128, row_tile * BM, full0);
-        load<PAIR>(a_dst + S::A_BYTES, &tmB, ks * 128, n0 + rank * S::B_ROWS, full0);
-        if constexpr (S::B_ROWS == 256) load<PAIR>(a_dst + S::A_BYTES + S::B_BYTES / 2, &tmB, ks * 128, n0 + 128, full0);
-        load<PAIR>(sf, &tmSA, ks * 256, row_tile, full0);
-#pragma unroll
-        for (int i = 0; i < S::B_TILES; ++i)
-          load<PAIR>(sf + (1 + i) * 2 * SCALE_TILE, &tmSB, ks * 256, (n0 >> 7) + i, full0);
+        if (elect_one()) {  // (what lies past a matrix arrives as zeros)
+          if (warp == 0) {
+            if (rank == 0) mbar_arrive_expect_tx(full, CTAS * S::STAGE_BYTES);
+            load<PAIR>(a_dst, &tmA, ks * 128, row_tile * BM, full0);
+            load<PAIR>(sf, &tmSA, ks * 256, row_tile, full0);
+          } else {
+            load<PAIR>(a_dst + S::A_BYTES, &tmB, ks * 128, n0 + rank * S::B_ROWS, full0);
+            load<PAIR>(sf + 2 * SCALE_TILE, &tmSB, ks * 256, n0 >> 7, full0);
+          }
+        }
+        __syncwarp();
         ++issued;
         if (++stage == STAGES) { stage = 0; phase ^= 1u; }
       }
@@ -216,26 +233,21 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_wait_drain(smem_u32(&s.full[stage]), phase);
       }
     }
-  } else if (warp == 1 && lane == 0 && rank != 0) {
-    // the odd CTA issues nothing; it waits until the even CTA's last MMAs, which
-    // write its tensor memory, have finished
-    if (!mbar_wait_drain(smem_u32(&s.drain), 0)) *abort_flag = 1;
-  } else if (warp == 1 && lane == 0) {
-    // ================= scales and MMAs =================
-    int stage = 0, buf = 0;
-    uint32_t phase = 0, use = 0;
-    bool ok = true;
-    for (int tile = tile0; tile < args.tiles && ok; tile += step) {
-      const int n0 = tile % args.n_tiles * BN;
-      const uint32_t skew = BN == 64 ? (n0 & 64) >> 5 : 0;  // rows 64.. of a tile of scales
-      if (!mbar_wait(smem_u32(&s.tempty[buf]), use ^ 1u, abort_flag)) break;
+  } else if (warp < 3 && rank != 0) {
+    // the odd CTA issues nothing; it waits until the even CTA's last operations,
+    // which write its tensor memory, have finished
+    if (!mbar_wait_drain(smem_u32(&s.drain[warp - 1]), 0)) *abort_flag = 1;
+  } else if (warp == 2) {
+    // ================= scales to tensor memory =================
+    int stage = 0;
+    uint32_t phase = 0;
+    const int my_tiles = tile0 < args.tiles ? (args.tiles - 1 - tile0) / step + 1 : 0;
+    for (long long i = static_cast<long long>(my_tiles) * args.k_steps; i > 0; --i) {
+      if (!warp_wait(smem_u32(&s.full[stage]), phase, abort_flag)) break;
       tc_fence_after();
-      for (int ks = 0; ks < args.k_steps; ++ks) {
-        if (!mbar_wait(smem_u32(&s.full[stage]), phase, abort_flag)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t sf = sf_u32 + stage * S::SF_BYTES;
-        const uint32_t tsa = tmem_base + BN * BUFS + stage * S::SF_COLS, tsb = tsa + 8;
-        const int left = args.K - ks * BKC;  // codes from here on
+      const uint32_t sf = sf_u32 + stage * S::SF_BYTES;
+      const uint32_t tsa = tmem_base + BN * BUFS + stage * S::SF_COLS, tsb = tsa + 8;
+      if (elect_one()) {
         // columns: A's scales of each 128 codes (4), then B's (4 for each 128 rows)
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt) {
@@ -244,25 +256,53 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int i = 0; i < S::B_TILES; ++i)
             tc_copy_scales<PAIR>(tsb + (kt * S::B_TILES + i) * 4, sf + ((1 + i) * 2 + kt) * SCALE_TILE);
         }
+        commit<PAIR>(smem_u32(&s.scaled[stage]));
+      }
+      __syncwarp();
+      if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+    }
+    if (elect_one()) commit<PAIR>(smem_u32(&s.drain[1]));
+    if (!mbar_wait_drain(smem_u32(&s.drain[1]), 0)) *abort_flag = 1;
+  } else if (warp == 1) {
+    // ================= MMAs =================
+    int stage = 0, buf = 0;
+    uint32_t phase = 0, use = 0;
+    bool ok = true;
+    for (int tile = tile0; tile < args.tiles && ok; tile += step) {
+      const int n0 = tile % args.n_tiles * BN;
+      const uint32_t skew = BN == 64 ? (n0 & 64) >> 5 : 0;  // rows 64.. of a tile of scales
+      if (!warp_wait(smem_u32(&s.tempty[buf]), use ^ 1u, abort_flag)) break;
+      for (int ks = 0; ks < args.k_steps; ++ks) {
+        // (the scales' copy waited for the stage's arrival; this wait makes it visible here)
+        if (!warp_wait(smem_u32(&s.scaled[stage]), phase, abort_flag) || !warp_wait(smem_u32(&s.full[stage]), phase, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t tsa = tmem_base + BN * BUFS + stage * S::SF_COLS, tsb = tsa + 8;
+        const int left = args.K - ks * BKC;  // codes from here on
         const uint32_t a_addr = tiles_u32 + stage * (S::A_BYTES + S::B_BYTES);
         const uint64_t a_desc = sdesc_k_sw128(a_addr);
         const uint64_t b_desc = sdesc_k_sw128(a_addr + S::A_BYTES);
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          if (kk * 64 >= left) break;
-          tc_mma_mxf4<PAIR>(tmem_base + buf * BN, a_desc + 2 * kk, b_desc + 2 * kk, kk & 1 ? IDESC2 : IDESC0,
-                            tsa + (kk >> 1) * 4, tsb + (kk >> 1) * 4 * S::B_TILES + skew, ks != 0 || kk != 0);
+          for (int kk = 0; kk < 4; ++kk) {
+            if (kk * 64 >= left) break;
+            tc_mma_mxf4<PAIR>(tmem_base + buf * BN, a_desc + 2 * kk, b_desc + 2 * kk, kk & 1 ? IDESC2 : IDESC0,
+                              tsa + (kk >> 1) * 4, tsb + (kk >> 1) * 4 * S::B_TILES + skew, ks != 0 || kk != 0);
+          }
+          commit<PAIR>(smem_u32(&s.empty[stage]));
+          if (ks + 1 == args.k_steps) commit<PAIR>(smem_u32(&s.tfull[buf]));
         }
-        commit<PAIR>(smem_u32(&s.empty[stage]));
+        __syncwarp();
         if (++stage == STAGES) { stage = 0; phase ^= 1u; }
       }
       if (!ok) break;
-      commit<PAIR>(smem_u32(&s.tfull[buf]));
       if (++buf == BUFS) { buf = 0; use ^= 1u; }
     }
-    // every operation this thread issued has finished before anyone frees memory
-    commit<PAIR>(smem_u32(&s.drain));
-    if (!mbar_wait_drain(smem_u32(&s.drain), 0)) *abort_flag = 1;
+    // every operation this warp issued has finished before anyone frees memory
+    if (elect_one()) commit<PAIR>(smem_u32(&s.drain[0]));
+    if (!mbar_wait_drain(smem_u32(&s.drain[0]), 0)) *abort_flag = 1;
   } else if (warp >= 4) {
     // ================= epilogue =================
     // lane quarter q = warp % 4 of tensor memory; column half = (warp - 4) / 4
@@ -377,9 +417,9 @@ cudaError_t launch(const uint8_t* a, const uint8_t* a_scale, const uint8_t* b, c
   args.n_tiles = (args.N + BN - 1) / BN;
   args.tiles = (args.M + CTAS * BM - 1) / (CTAS * BM) * args.n_tiles;
   CUtensorMap ma, mb, msa, msb, mo;
-  constexpr int b_box = Shape<BN, PAIR>::B_ROWS < 128 ? Shape<BN, PAIR>::B_ROWS : 128;
-  if (!make_tma_2d_u8(&ma, a, args.M, args.K / 2, BM) || !make_tma_2d_u8(&mb, b, args.N, args.K / 2, b_box) ||
-      !make_tma_scale_tiles(&msa, a_scale, (args.M + 127) / 128, kts) || !make_tma_scale_tiles(&msb, b_scale, (args.N + 127) / 128, kts))
+  if (!make_tma_2d_u8(&ma, a, args.M, args.K / 2, BM) || !make_tma_2d_u8(&mb, b, args.N, args.K / 2, Shape<BN, PAIR>::B_ROWS) ||
+      !make_tma_scale_tiles(&msa, a_scale, (args.M + 127) / 128, kts, 1) ||
+      !make_tma_scale_tiles(&msb, b_scale, (args.N + 127) / 128, kts, Shape<BN, PAIR>::B_TILES))
     return cudaErrorInvalidValue;
   if (args.out_staged && !make_tma_store_2d_bf16(&mo, args.out, args.M, args.N)) return cudaErrorInvalidValue;
   if (!args.out_staged) mo = ma;  // not used
@@ -428,10 +468,12 @@ cudaError_t launch_fp4_matmul_tc(const uint8_t* a, const uint8_t* a_scale, int M
   const bool pair = M > BM;
   const long long mt = pair ? (static_cast<long long>(M) + 2 * BM - 1) / (2 * BM) : 1;
   const int at_once = pair ? sm_count() / 2 : sm_count();
-  // the tile width with the fewest columns in all rounds of tiles
-  auto rounds = [&](int bn) { return (mt * ((N + bn - 1) / bn) + at_once - 1) / at_once * bn; };
+  // The fewest rounds of tiles, then the narrowest tile: a stage takes about as
+  // long whatever its width (8192 x 8192 x 4096 in pairs: 27 rounds of 128 columns
+  // 177 us, 14 of 256 101 us; 333 x 4096 x 2048: 1 round of 128 7.0 us, of 256 7.7).
+  auto rounds = [&](int bn) { return (mt * ((N + bn - 1) / bn) + at_once - 1) / at_once; };
   const long long r64 = rounds(64), r128 = rounds(128), r256 = rounds(256);
-  const int bn = r256 <= r128 && r256 <= r64 ? 256 : r128 <= r64 ? 128 : 64;
+  const int bn = r64 <= r256 ? 64 : r128 <= r256 ? 128 : 256;
   if (pair)
     return bn == 256   ? launch<256, true>(a, a_scale, b, b_scale, g, s)
            : bn == 128 ? launch<128, true>(a, a_scale, b, b_scale, g, s)

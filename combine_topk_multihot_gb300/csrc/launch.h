@@ -44,8 +44,8 @@ bool make_tma_2d_u8(CUtensorMap* map, const void* base, uint64_t rows, uint64_t 
                     uint32_t box_rows);
 
 // Scales of 4-bit codes in tiles of 512 bytes, [row tiles, block tiles], read as
-// two neighbouring tiles of one row.
-bool make_tma_scale_tiles(CUtensorMap* map, const void* base, uint64_t row_tiles, uint64_t block_tiles);
+// two neighbouring tiles of box_rows row tiles.
+bool make_tma_scale_tiles(CUtensorMap* map, const void* base, uint64_t row_tiles, uint64_t block_tiles, uint32_t box_rows);
 
 // Tensor maps whose boxes carry 128 columns of K as two 64-column sub-tiles
 // (128-byte swizzle; sub-tile j follows sub-tile j - 1 in shared memory), so

@@ -55,12 +55,12 @@ bool make_tma_2d_u8(CUtensorMap* map, const void* base, uint64_t rows, uint64_t 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool make_tma_scale_tiles(CUtensorMap* map, const void* base, uint64_t row_tiles, uint64_t block_tiles) {
+bool make_tma_scale_tiles(CUtensorMap* map, const void* base, uint64_t row_tiles, uint64_t block_tiles, uint32_t box_rows) {
   EncodeTiledFn fn = encode_fn();
   if (!fn || row_tiles == 0 || block_tiles == 0) return false;
   const cuuint64_t dims[2] = {block_tiles * 128, row_tiles};  // words
   const cuuint64_t strides[1] = {block_tiles * 512};
-  const cuuint32_t box[2] = {256, 1};
+  const cuuint32_t box[2] = {256, box_rows};
   const cuuint32_t estr[2] = {1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides, box,
             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
