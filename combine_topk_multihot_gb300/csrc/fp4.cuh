@@ -42,18 +42,15 @@ __device__ __forceinline__ float e8m0_value(uint32_t e) {
   return __uint_as_float(e == 0u ? 0x00400000u : e == 255u ? 0x7fc00000u : e << 23);
 }
 
-// Two codes (the first in the lower four bits) of values already divided by
-// their scale: to nearest even, saturated.  (The conversions are written as
-// instructions here: the toolkit's header takes this chip for one without them.)
-__device__ __forceinline__ uint32_t e2m1x2(float first, float second) {
-  uint32_t c;
-  asm("{\n\t.reg .b8 c;\n\t.reg .b16 h;\n\tcvt.rn.satfinite.e2m1x2.f32 c, %2, %1;\n\tmov.b16 h, {c, 0};\n\tcvt.u32.u16 %0, h;\n\t}"
-      : "=r"(c) : "f"(first), "f"(second));
-  return c;
-}
-// Eight codes, the first in the lowest bits.
+// The codes of eight values already divided by their scale, the first in the
+// lowest bits: to nearest even, saturated.  (The conversions here are written
+// as instructions: through the toolkit's header, 13.0, they took tens of others.)
 __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
-  return e2m1x2(v[0], v[1]) | e2m1x2(v[2], v[3]) << 8 | e2m1x2(v[4], v[5]) << 16 | e2m1x2(v[6], v[7]) << 24;
+  uint32_t c;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\tmov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(c) : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return c;
 }
 // The eight codes of a word as pairs of f16.
 __device__ __forceinline__ void f16_of_e2m1x8(uint32_t w, uint32_t (&v)[4]) {

@@ -12,14 +12,16 @@ namespace {
 
 // ---------------------------------------------------------------- quantisation
 
-// A warp takes up to four 256-column pieces of one row: lane l holds 8 values, 4
-// lanes a block, 16 lanes a scale word.  blockIdx.y picks the pieces.  Rows up to
-// the next multiple of 128 have scales only, zeros.  Every quotient is a
-// product with a power of two, so codes are functions of the input alone.
+// Both ways a warp takes up to four 256-column pieces of one row, lane l 8 values
+// of each: 4 lanes a block, 16 lanes a scale word.  blockIdx.y picks the pieces.
+// Rows up to the next multiple of 128 have scales only, zeros.  Every quotient is
+// a product with a power of two, so codes are functions of the input alone.
+// Bound by HBM; for bf16 instructions are close behind.
 constexpr int PIECES = 4;
 template <bool F32>
-__global__ void __launch_bounds__(256) quantize_fp4_kernel(const void* __restrict__ src, long long all, int rows, int rows_up,
-                                                           int cols, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+__global__ void __launch_bounds__(256, F32 ? 4 : 5) quantize_fp4_kernel(const void* __restrict__ src, long long all, int rows,
+                                                                       int rows_up, int cols, uint8_t* __restrict__ codes,
+                                                                       uint8_t* __restrict__ scales) {
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31;
@@ -27,83 +29,101 @@ __global__ void __launch_bounds__(256) quantize_fp4_kernel(const void* __restric
   const int col0 = blockIdx.y * (PIECES * 256) + lane * 8;
   const long long nwarps = static_cast<long long>(gridDim.x) * (blockDim.x >> 5);
   for (long long i = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); i < all; i += nwarps) {
-    const long long mat = i / rows_up;
+    const long long mat = all == rows_up ? 0 : i / rows_up;
     const int row = static_cast<int>(i - mat * rows_up);
     const bool there = row < rows;
     const long long r = mat * rows + row;
-    float v[PIECES][8];
+    uint4 q[PIECES][F32 ? 2 : 1];
 #pragma unroll
     for (int p = 0; p < PIECES; ++p) {
       const int c = col0 + 256 * p;
       const bool in = there && c < cols;
-      if constexpr (F32) {
-        const float4* at = reinterpret_cast<const float4*>(static_cast<const float*>(src) + r * cols + c);
-        const float4 a = in ? __ldcs(at) : make_float4(0.f, 0.f, 0.f, 0.f), b = in ? __ldcs(at + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
-        v[p][0] = a.x, v[p][1] = a.y, v[p][2] = a.z, v[p][3] = a.w, v[p][4] = b.x, v[p][5] = b.y, v[p][6] = b.z, v[p][7] = b.w;
-      } else {
-        const uint4 q = in ? __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(src) + r * cols + c))
-                           : make_uint4(0, 0, 0, 0);
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+      const uint4* at = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(src) + (r * cols + c) * (F32 ? 4 : 2));
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[p][2 * k] = bf16_lo(w[k]), v[p][2 * k + 1] = bf16_hi(w[k]);
-      }
+      for (int k = 0; k < (F32 ? 2 : 1); ++k) q[p][k] = in ? __ldcs(at + k) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int p = 0; p < PIECES; ++p) {
       const int c = col0 + 256 * p;
       if (c - lane * 8 >= kts * 128) break;  // (the same for the warp)
-      float top = 0.f;
+      float v[8], top;
+      if constexpr (F32) {
+        top = 0.f;
+        const uint32_t w[8] = {q[p][0].x, q[p][0].y, q[p][0].z, q[p][0].w, q[p][1].x, q[p][1].y, q[p][1].z, q[p][1].w};
 #pragma unroll
-      for (int k = 0; k < 8; ++k) top = max_nan(top, fabsf(v[p][k]));
-      top = max_nan(top, __shfl_xor_sync(FULL_MASK, top, 1));
-      top = max_nan(top, __shfl_xor_sync(FULL_MASK, top, 2));
+        for (int k = 0; k < 8; ++k) {
+          v[k] = __uint_as_float(w[k]);
+          top = max_nan(top, fabsf(v[k]));
+        }
+        top = max_nan(top, __shfl_xor_sync(FULL_MASK, top, 1));
+        top = max_nan(top, __shfl_xor_sync(FULL_MASK, top, 2));
+      } else {
+        const uint32_t w[4] = {q[p][0].x, q[p][0].y, q[p][0].z, q[p][0].w};
+        uint32_t t = bf16x2_abs_max(bf16x2_abs_max(w[0], w[1]), bf16x2_abs_max(w[2], w[3]));
+        t = bf16x2_abs_max(t, __shfl_xor_sync(FULL_MASK, t, 1));
+        t = bf16x2_abs_max(t, __shfl_xor_sync(FULL_MASK, t, 2));
+        top = max_nan(bf16_lo(t), bf16_hi(t));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[2 * k] = bf16_lo(w[k]), v[2 * k + 1] = bf16_hi(w[k]);
+      }
       const uint32_t e = e8m0_of(top);
       const float f = e8m0_inverse(e);
-      float q[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) q[k] = e == 255u ? 0.f : v[p][k] * f;
-      if (there && c < cols) *reinterpret_cast<uint32_t*>(codes + (r * cols + c) / 2) = e2m1x8(q);
-      uint32_t word = e << (8 * ((lane >> 2) & 3));
-      word |= __shfl_xor_sync(FULL_MASK, word, 4);
-      word |= __shfl_xor_sync(FULL_MASK, word, 8);
+      for (int k = 0; k < 8; ++k) v[k] *= f;
+      const uint32_t word = e == 255u ? 0u : e2m1x8(v);
+      if (there && c < cols) *reinterpret_cast<uint32_t*>(codes + (r * cols + c) / 2) = word;
+      uint32_t s = e << (8 * ((lane >> 2) & 3));
+      s |= __shfl_xor_sync(FULL_MASK, s, 4);
+      s |= __shfl_xor_sync(FULL_MASK, s, 8);
       const int kt = c >> 7;
       if ((lane & 15) == 0 && kt < kts)
-        *reinterpret_cast<uint32_t*>(scales + mat * (rows_up >> 7) * kts * SCALE_TILE + scale_word(row, kt, kts)) = word;
+        *reinterpret_cast<uint32_t*>(scales + mat * (rows_up >> 7) * kts * SCALE_TILE + scale_word(row, kt, kts)) = s;
     }
   }
 }
 
-// The way back: a thread turns 8 codes into 16 bytes of bf16, or 32 of fp32.
-// Exact in either type: a code has two significant bits.
+// The way back: exact in either type, a code has two significant bits.
 template <bool F32>
 __global__ void __launch_bounds__(256) dequantize_fp4_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                                                              long long all, int rows, int cols, void* __restrict__ out) {
   griddep_launch_dependents();
   griddep_wait();
-  const int words = cols >> 3, kts = (cols + 127) >> 7;
+  const int lane = threadIdx.x & 31;
+  const int kts = (cols + 127) >> 7;
   const long long tiles = static_cast<long long>((rows + 127) >> 7) * kts * SCALE_TILE;
-  const long long step = static_cast<long long>(gridDim.x) * blockDim.x;
-  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < all; i += step) {
-    const long long r = i / words;
-    const int w = static_cast<int>(i - r * words);
-    const long long mat = r / rows;
-    const uint32_t c = __ldcs(reinterpret_cast<const uint32_t*>(codes) + i);
-    const float f = e8m0_value(__ldg(scales + mat * tiles + scale_word(r - mat * rows, w >> 4, kts) + ((w >> 2) & 3)));
-    uint32_t halves[4];
-    f16_of_e2m1x8(c, halves);
-    float v[8];
+  const int col0 = blockIdx.y * (PIECES * 256) + lane * 8;
+  const long long nwarps = static_cast<long long>(gridDim.x) * (blockDim.x >> 5);
+  for (long long r = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); r < all; r += nwarps) {
+    const long long mat = all == rows ? 0 : r / rows;
+    const uint8_t* sc = scales + mat * tiles + scale_word(r - mat * rows, 0, kts);
+    uint32_t c[PIECES], e[PIECES];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&halves[k]));
-      v[2 * k] = t.x * f, v[2 * k + 1] = t.y * f;
+    for (int p = 0; p < PIECES; ++p) {
+      const int col = col0 + 256 * p;
+      c[p] = col < cols ? __ldcs(reinterpret_cast<const uint32_t*>(codes + (r * cols + col) / 2)) : 0u;
+      e[p] = col < cols ? __ldg(sc + static_cast<long long>(col >> 7) * SCALE_TILE + ((col >> 5) & 3)) : 0u;
     }
-    if constexpr (F32) {
-      float4* o = reinterpret_cast<float4*>(out) + 2 * i;
-      __stcs(o, make_float4(v[0], v[1], v[2], v[3]));
-      __stcs(o + 1, make_float4(v[4], v[5], v[6], v[7]));
-    } else {
-      __stcs(reinterpret_cast<uint4*>(out) + i, make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                           pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p) {
+      const int col = col0 + 256 * p;
+      if (col >= cols) break;
+      const float f = e8m0_value(e[p]);
+      uint32_t halves[4];
+      f16_of_e2m1x8(c[p], halves);
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&halves[k]));
+        v[2 * k] = t.x * f, v[2 * k + 1] = t.y * f;
+      }
+      if constexpr (F32) {
+        float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + r * cols + col);
+        __stcs(o, make_float4(v[0], v[1], v[2], v[3]));
+        __stcs(o + 1, make_float4(v[4], v[5], v[6], v[7]));
+      } else {
+        __stcs(reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + r * cols + col),
+               make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
+      }
     }
   }
 }
@@ -227,12 +247,13 @@ cudaError_t launch_quantize_fp4(const void* src, bool f32, long long batch, long
 
 cudaError_t launch_dequantize_fp4(const uint8_t* codes, const uint8_t* scales, long long batch, long long rows, int cols, bool f32,
                                   void* out, cudaStream_t s) {
-  const long long all = batch * rows * (cols / 8);
+  const long long all = batch * rows;
   if (all == 0) return cudaSuccess;
-  const long long need = (all + 255) / 256, most = 1 << 20;
-  return launch_dependent(f32 ? dequantize_fp4_kernel<true> : dequantize_fp4_kernel<false>,
-                          static_cast<unsigned>(need < most ? need : most), 256, 0, s, codes, scales, all, static_cast<int>(rows),
-                          cols, out);
+  const int y = (cols + PIECES * 256 - 1) / (PIECES * 256);
+  const long long need = (all + 7) / 8, most = 1 << 20;
+  const dim3 grid(static_cast<unsigned>(need < most ? need : most), y);
+  return launch_dependent(f32 ? dequantize_fp4_kernel<true> : dequantize_fp4_kernel<false>, grid, 256, 0, s, codes, scales, all,
+                          static_cast<int>(rows), cols, out);
 }
 
 cudaError_t launch_fp4_matmul_stream(const uint8_t* a, const uint8_t* a_scale, int M, const uint8_t* b, const uint8_t* b_scale, int N,

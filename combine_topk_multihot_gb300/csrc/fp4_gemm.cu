@@ -44,11 +44,13 @@ struct Shape {
   static constexpr int B_TILES = (BN + 127) / 128;  // of scales
   static constexpr int SF_BYTES = 2 * SCALE_TILE * (1 + B_TILES);
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SF_BYTES;
-  static constexpr int STAGES = (SMEM_LIMIT - 1024 - STAGING_BYTES - 512) / STAGE_BYTES < MAX_STAGES
-                                    ? (SMEM_LIMIT - 1024 - STAGING_BYTES - 512) / STAGE_BYTES : MAX_STAGES;
   static constexpr int BUFS = BN == 256 ? 1 : 2;
   static constexpr int SF_COLS = 8 * (1 + B_TILES);  // of a stage
   static constexpr int TMEM_COLS = 512;
+  // as many stages as shared memory and the scales' tensor memory hold
+  static constexpr int IN_SMEM = (SMEM_LIMIT - 1024 - STAGING_BYTES - 512) / STAGE_BYTES, IN_TMEM = (TMEM_COLS - BN * BUFS) / SF_COLS;
+  static constexpr int MOST = IN_SMEM < IN_TMEM ? IN_SMEM : IN_TMEM;
+  static constexpr int STAGES = MOST < MAX_STAGES ? MOST : MAX_STAGES;
   static_assert(BN * BUFS + STAGES * SF_COLS <= TMEM_COLS, "accumulators and scales fit in tensor memory");
 };
 
@@ -270,14 +272,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     bool ok = true;
     for (int tile = tile0; tile < args.tiles && ok; tile += step) {
       const int n0 = tile % args.n_tiles * BN;
-      const uint32_t skew = BN == 64 ? (n0 & 64) >> 5 : 0;  // rows 64.. of a tile of scales
+      const uint32_t skew = BN % 128 ? (n0 & 64) >> 5 : 0;  // rows from 64 of a tile of scales on
       if (!warp_wait(smem_u32(&s.tempty[buf]), use ^ 1u, abort_flag)) break;
       for (int ks = 0; ks < args.k_steps; ++ks) {
-        // (the scales' copy waited for the stage's arrival; this wait makes it visible here)
-        if (!warp_wait(smem_u32(&s.scaled[stage]), phase, abort_flag) || !warp_wait(smem_u32(&s.full[stage]), phase, abort_flag)) {
-          ok = false;
-          break;
-        }
+        // (the scales were copied after the stage's arrival: one wait for both)
+        if (!warp_wait(smem_u32(&s.scaled[stage]), phase, abort_flag)) { ok = false; break; }
         tc_fence_after();
         const uint32_t tsa = tmem_base + BN * BUFS + stage * S::SF_COLS, tsb = tsa + 8;
         const int left = args.K - ks * BKC;  // codes from here on
@@ -319,17 +318,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int row0 = (mt * CTAS + rank) * BM + q * 32, col0 = nt * BN + half * COLS;
       const int rows = min(args.M - row0, 32);
       const uint32_t tb = tmem_base + buf * BN + half * COLS + (static_cast<uint32_t>(q * 32) << 16);
-      uint32_t v[COLS / 2];
-      uint32_t p[COLS > 32 ? 2 : 1][32];
-      tmem_ld32(tb, p[0]);
+      // all columns first, so that the accumulator is free as soon as may be
+      uint32_t p[COLS / 32][32];
 #pragma unroll
-      for (int c = 0; c < COLS; c += 32) {
-        uint32_t(&now)[32] = p[COLS > 32 ? (c >> 5) & 1 : 0];
-        tmem_ld_wait32(now);
-        if (c + 32 < COLS) tmem_ld32(tb + c + 32, p[COLS > 32 ? ((c >> 5) & 1) ^ 1 : 0]);
+      for (int c = 0; c < COLS / 32; ++c) tmem_ld32(tb + 32 * c, p[c]);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) v[c / 2 + k] = pack_bf16x2(__uint_as_float(now[2 * k]), __uint_as_float(now[2 * k + 1]));
-      }
+      for (int c = 0; c < COLS / 32; ++c) tmem_ld_wait32(p[c]);
       tc_fence_before();  // all of this warp's reads have landed
       __syncwarp();
       if (lane == 0) {
@@ -339,14 +333,17 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
       for (int c = 0; c < COLS; c += 32) {
         if (col0 + c >= args.N || rows <= 0) break;
+        uint32_t v[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) v[k] = pack_bf16x2(__uint_as_float(p[c / 32][2 * k]), __uint_as_float(p[c / 32][2 * k + 1]));
         const uint32_t dst = staging + box * 2048;
         box ^= 1u;
         if (lane == 0) tma_store_wait_read<1>();  // the box before the last
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + staged_chunk(lane, i)), "r"(v[c / 2 + 4 * i]),
-                       "r"(v[c / 2 + 4 * i + 1]), "r"(v[c / 2 + 4 * i + 2]), "r"(v[c / 2 + 4 * i + 3])
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + staged_chunk(lane, i)), "r"(v[4 * i]),
+                       "r"(v[4 * i + 1]), "r"(v[4 * i + 2]), "r"(v[4 * i + 3])
                        : "memory");
         if (args.out_staged) {  // rows and columns past the matrix are clipped by the tensor map
           fence_async_shared();
@@ -468,14 +465,29 @@ cudaError_t launch_fp4_matmul_tc(const uint8_t* a, const uint8_t* a_scale, int M
   const bool pair = M > BM;
   const long long mt = pair ? (static_cast<long long>(M) + 2 * BM - 1) / (2 * BM) : 1;
   const int at_once = pair ? sm_count() / 2 : sm_count();
-  // The fewest rounds of tiles, then the narrowest tile: a stage takes about as
-  // long whatever its width (8192 x 8192 x 4096 in pairs: 27 rounds of 128 columns
-  // 177 us, 14 of 256 101 us; 333 x 4096 x 2048: 1 round of 128 7.0 us, of 256 7.7).
+  // The width with the shortest rounds of tiles in all.  In pairs a stage of 64, 128,
+  // 192 or 256 columns takes about 240, 240, 270 and 305 ns and a tile 0.3, 0.3, 0.45
+  // and 1.0 us more (8192 x 8192 x 4096: 239, 120, 93 and 82 us; 333 x 4096 x
+  // 2048: 7.8, 5.9, 6.1 and 6.5).  A single CTA's tiles are few: the fewest
+  // rounds, then the narrowest.
   auto rounds = [&](int bn) { return (mt * ((N + bn - 1) / bn) + at_once - 1) / at_once; };
-  const long long r64 = rounds(64), r128 = rounds(128), r256 = rounds(256);
-  const int bn = r64 <= r256 ? 64 : r128 <= r256 ? 128 : 256;
+  int bn = 256;
+  if (pair) {
+    auto cost = [&](int width, int stage, int tile) { return rounds(width) * (static_cast<long long>(g.k_steps) * stage + tile); };
+    long long best = cost(256, 305, 1000);
+    auto look = [&](int width, int stage, int tile) {
+      const long long c = cost(width, stage, tile);
+      if (c < best) best = c, bn = width;
+    };
+    look(192, 270, 450);
+    look(128, 240, 300);
+    look(64, 240, 300);
+  } else {
+    bn = rounds(64) <= rounds(256) ? 64 : rounds(128) <= rounds(256) ? 128 : 256;
+  }
   if (pair)
     return bn == 256   ? launch<256, true>(a, a_scale, b, b_scale, g, s)
+           : bn == 192 ? launch<192, true>(a, a_scale, b, b_scale, g, s)
            : bn == 128 ? launch<128, true>(a, a_scale, b, b_scale, g, s)
                        : launch<64, true>(a, a_scale, b, b_scale, g, s);
   return bn == 256   ? launch<256, false>(a, a_scale, b, b_scale, g, s)
