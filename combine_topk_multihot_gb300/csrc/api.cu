@@ -971,8 +971,8 @@ moe_status check_fp4(const char* who, const void* values, int32_t dtype, int64_t
                      const uint8_t* codes, const uint8_t* scales) {
   MOE_REQUIRE(batch >= 0 && rows >= 0, MOE_ERR_INVALID_ARG, "%s: batch and rows must be >= 0", who);
   MOE_REQUIRE(dtype == MOE_DTYPE_BF16 || dtype == MOE_DTYPE_F32, MOE_ERR_INVALID_ARG, "%s: unknown type %d", who, dtype);
-  MOE_REQUIRE(cols >= 32 && cols % 32 == 0, MOE_ERR_UNSUPPORTED_SHAPE, "%s: cols must be a positive multiple of 32 (got %d)", who,
-              cols);
+  MOE_REQUIRE(cols >= 32 && cols % 32 == 0 && cols < (1 << 24) - 256, MOE_ERR_UNSUPPORTED_SHAPE,
+              "%s: cols must be a positive multiple of 32 below 2^24 - 256 (got %d)", who, cols);
   MOE_REQUIRE(rows < (int64_t(1) << 31) - 128 && (batch == 0 || rows < (int64_t(1) << 47) / cols / batch), MOE_ERR_UNSUPPORTED_SHAPE,
               "%s: too many rows", who);
   MOE_REQUIRE(batch == 0 || rows == 0 || (values && codes && scales), MOE_ERR_INVALID_ARG, "%s: NULL pointer", who);

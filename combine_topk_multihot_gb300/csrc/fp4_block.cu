@@ -12,40 +12,38 @@ namespace {
 
 // ---------------------------------------------------------------- quantisation
 
-// Both ways a warp takes up to four 256-column pieces of one row, lane l 8 values
-// of each: 4 lanes a block, 16 lanes a scale word.  blockIdx.y picks the pieces.
-// Rows up to the next multiple of 128 have scales only, zeros.  Every quotient is
-// a product with a power of two, so codes are functions of the input alone.
-// Bound by HBM; for bf16 instructions are close behind.
+// A warp takes 256 columns of four rows that lie 32 apart, whose scale words are
+// neighbours in their tile; lane l holds 8 values of each, 4 lanes a block, 16
+// lanes a scale word.  Rows up to the next multiple of 128 have scales only,
+// zeros.  Every quotient is a product with a power of two, so codes are functions
+// of the input alone.  Bound by HBM.
 constexpr int PIECES = 4;
 template <bool F32>
 __global__ void __launch_bounds__(256, F32 ? 4 : 5) quantize_fp4_kernel(const void* __restrict__ src, long long all, int rows,
-                                                                       int rows_up, int cols, uint8_t* __restrict__ codes,
+                                                                       int row_tiles, int cols, uint8_t* __restrict__ codes,
                                                                        uint8_t* __restrict__ scales) {
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31;
   const int kts = (cols + 127) >> 7;
-  const int col0 = blockIdx.y * (PIECES * 256) + lane * 8;
+  const int c = blockIdx.y * 256 + lane * 8, kt = c >> 7;
   const long long nwarps = static_cast<long long>(gridDim.x) * (blockDim.x >> 5);
   for (long long i = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); i < all; i += nwarps) {
-    const long long mat = all == rows_up ? 0 : i / rows_up;
-    const int row = static_cast<int>(i - mat * rows_up);
-    const bool there = row < rows;
-    const long long r = mat * rows + row;
+    const long long tile = i >> 5;  // of all matrices' row tiles
+    const long long mat = all == 32ll * row_tiles ? 0 : tile / row_tiles;
+    const int row0 = static_cast<int>(tile - mat * row_tiles) * 128 + static_cast<int>(i & 31);
     uint4 q[PIECES][F32 ? 2 : 1];
 #pragma unroll
     for (int p = 0; p < PIECES; ++p) {
-      const int c = col0 + 256 * p;
-      const bool in = there && c < cols;
-      const uint4* at = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(src) + (r * cols + c) * (F32 ? 4 : 2));
+      const bool in = row0 + 32 * p < rows && c < cols;
+      const uint4* at = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(src) +
+                                                       ((mat * rows + row0 + 32 * p) * cols + c) * (F32 ? 4 : 2));
 #pragma unroll
       for (int k = 0; k < (F32 ? 2 : 1); ++k) q[p][k] = in ? __ldcs(at + k) : make_uint4(0, 0, 0, 0);
     }
+    uint32_t words[PIECES];
 #pragma unroll
     for (int p = 0; p < PIECES; ++p) {
-      const int c = col0 + 256 * p;
-      if (c - lane * 8 >= kts * 128) break;  // (the same for the warp)
       float v[8], top;
       if constexpr (F32) {
         top = 0.f;
@@ -70,19 +68,20 @@ __global__ void __launch_bounds__(256, F32 ? 4 : 5) quantize_fp4_kernel(const vo
       const float f = e8m0_inverse(e);
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] *= f;
-      const uint32_t word = e == 255u ? 0u : e2m1x8(v);
-      if (there && c < cols) *reinterpret_cast<uint32_t*>(codes + (r * cols + c) / 2) = word;
+      const uint32_t code = e == 255u ? 0u : e2m1x8(v);
+      if (row0 + 32 * p < rows && c < cols) *reinterpret_cast<uint32_t*>(codes + ((mat * rows + row0 + 32 * p) * cols + c) / 2) = code;
       uint32_t s = e << (8 * ((lane >> 2) & 3));
       s |= __shfl_xor_sync(FULL_MASK, s, 4);
-      s |= __shfl_xor_sync(FULL_MASK, s, 8);
-      const int kt = c >> 7;
-      if ((lane & 15) == 0 && kt < kts)
-        *reinterpret_cast<uint32_t*>(scales + mat * (rows_up >> 7) * kts * SCALE_TILE + scale_word(row, kt, kts)) = s;
+      words[p] = s | __shfl_xor_sync(FULL_MASK, s, 8);
     }
+    if ((lane & 15) == 0 && kt < kts)
+      *reinterpret_cast<uint4*>(scales + (tile * kts + kt) * SCALE_TILE + (i & 31) * 16) =
+          make_uint4(words[0], words[1], words[2], words[3]);
   }
 }
 
-// The way back: exact in either type, a code has two significant bits.
+// The way back: exact in either type, a code has two significant bits.  A warp takes
+// up to four 256-column pieces of one row; blockIdx.y picks the pieces.
 template <bool F32>
 __global__ void __launch_bounds__(256) dequantize_fp4_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                                                              long long all, int rows, int cols, void* __restrict__ out) {
@@ -235,14 +234,13 @@ __global__ void __launch_bounds__(256, 3) fp4_stream_kernel(const StreamArgs arg
 
 cudaError_t launch_quantize_fp4(const void* src, bool f32, long long batch, long long rows, int cols, uint8_t* codes, uint8_t* scales,
                                 cudaStream_t s) {
-  const int up = static_cast<int>((rows + 127) / 128 * 128);
-  const long long all = batch * up;
+  const int row_tiles = static_cast<int>((rows + 127) / 128);
+  const long long all = batch * row_tiles * 32;
   if (all == 0) return cudaSuccess;
-  const int y = (cols + PIECES * 256 - 1) / (PIECES * 256);
   const long long need = (all + 7) / 8, most = 1 << 20;
-  const dim3 grid(static_cast<unsigned>(need < most ? need : most), y);
+  const dim3 grid(static_cast<unsigned>(need < most ? need : most), (cols + 255) / 256);
   return launch_dependent(f32 ? quantize_fp4_kernel<true> : quantize_fp4_kernel<false>, grid, 256, 0, s, src, all,
-                          static_cast<int>(rows), up, cols, codes, scales);
+                          static_cast<int>(rows), row_tiles, cols, codes, scales);
 }
 
 cudaError_t launch_dequantize_fp4(const uint8_t* codes, const uint8_t* scales, long long batch, long long rows, int cols, bool f32,

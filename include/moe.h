@@ -734,7 +734,7 @@ MOE_API moe_status moe_grouped_experts_fp8_block(const moe_bf16* x_disp, const m
  * The way back: out [batch, rows, cols] of out_dtype (out) = code * X, exact in
  * either type (bf16 weights of an expert that runs in bf16, say).
  * All pointers are 16-byte aligned.  Errors: MOE_ERR_UNSUPPORTED_SHAPE for cols
- * that is no positive multiple of 32 or rows of 2^31 - 128 or more,
+ * that is no positive multiple of 32, cols of 2^24 - 256 or rows of 2^31 - 128 or more,
  * MOE_ERR_INVALID_ARG for a NULL or misaligned pointer, batch or rows below 0
  * or an unknown type.
  */

@@ -82,6 +82,7 @@ def test_refusals_without_a_gpu(moe):
         assert d(p, p, 1, 4, cols, 0, p, None) == N.MOE_ERR_UNSUPPORTED_SHAPE
         assert mm(p, p, 4, p, p, 8, cols, p, None, None) == N.MOE_ERR_UNSUPPORTED_SHAPE
     assert q(p, 0, 1, 2 ** 31, 32, p, p, None) == N.MOE_ERR_UNSUPPORTED_SHAPE
+    assert q(p, 0, 1, 4, 2 ** 24, p, p, None) == N.MOE_ERR_UNSUPPORTED_SHAPE
     assert q(p, 0, 2 ** 40, 2 ** 10, 32, p, p, None) == N.MOE_ERR_UNSUPPORTED_SHAPE
     assert q(p, 7, 1, 4, 32, p, p, None) == N.MOE_ERR_INVALID_ARG
     assert d(p, p, 1, 4, 32, -1, p, None) == N.MOE_ERR_INVALID_ARG
