@@ -465,12 +465,13 @@ def moe_quantize_fp4_block(src: torch.Tensor, out=None, stream=None):
     shape = (*lead, rows, cols // 2)
     tiles = (*lead, *_fp4_tiles(rows, cols))
     if out is None:
-        out = torch.empty(shape, dtype=torch.uint8, device=dev), torch.empty(tiles, dtype=torch.uint8, device=dev)
-    codes, scales = out
+        codes, scales = torch.empty(shape, dtype=torch.uint8, device=dev), torch.empty(tiles, dtype=torch.uint8, device=dev)
+        places = codes.data_ptr() or None, scales.data_ptr() or None
+    else:
+        codes, scales = out
+        places = _need(codes, "codes", torch.uint8, shape, dev), _need(scales, "scales", torch.uint8, tiles, dev)
     _check(N.lib.moe_quantize_fp4_block(_need(src, "src", src.dtype, src.shape, dev), dtype, lead.numel() if lead else 1, rows,
-                                        cols, _need(codes, "codes", torch.uint8, shape, dev),
-                                        _need(scales, "scales", torch.uint8, tiles, dev), _raw_stream(stream, dev)),
-           "moe_quantize_fp4_block")
+                                        cols, *places, _raw_stream(stream, dev)), "moe_quantize_fp4_block")
     _used_on(stream, codes, scales)
     return codes, scales
 
@@ -481,13 +482,17 @@ def moe_dequantize_fp4_block(codes: torch.Tensor, scales: torch.Tensor, dtype=to
     bf16 or fp32, exact in both."""
     dev = _on_gpu(codes, "codes")
     lead, rows, cols = _fp4_matrix(codes, "codes")
+    if dtype not in _DTYPES:
+        raise TypeError(f"dtype must be bfloat16 or float32 (got {dtype})")
     if out is None:
         out = torch.empty(*lead, rows, cols, dtype=dtype, device=dev)
+        place = out.data_ptr() or None
+    else:
+        place = _need(out, "out", dtype, (*lead, rows, cols), dev)
     _check(N.lib.moe_dequantize_fp4_block(_need(codes, "codes", torch.uint8, codes.shape, dev),
                                           _need(scales, "scales", torch.uint8, (*lead, *_fp4_tiles(rows, cols)), dev),
-                                          lead.numel() if lead else 1, rows, cols, _either(out, "out"),
-                                          _need(out, "out", dtype, (*lead, rows, cols), dev), _raw_stream(stream, dev)),
-           "moe_dequantize_fp4_block")
+                                          lead.numel() if lead else 1, rows, cols, _DTYPES[dtype], place,
+                                          _raw_stream(stream, dev)), "moe_dequantize_fp4_block")
     _used_on(stream, out)
     return out
 
@@ -500,12 +505,14 @@ def moe_matmul_fp4_block(a_q: torch.Tensor, a_scale: torch.Tensor, b_q: torch.Te
     n = _rows(b_q, "b_q")[0]
     if out is None:
         out = torch.empty(M, n, dtype=torch.bfloat16, device=dev)
+        place = out.data_ptr() or None
+    else:
+        place = _need(out, "out", torch.bfloat16, (M, n), dev)
     _check(N.lib.moe_matmul_fp4_block(_need(a_q, "a_q", torch.uint8, (M, half), dev),
                                       _need(a_scale, "a_scale", torch.uint8, _fp4_tiles(M, 2 * half), dev), M,
                                       _need(b_q, "b_q", torch.uint8, (n, half), dev),
                                       _need(b_scale, "b_scale", torch.uint8, _fp4_tiles(n, 2 * half), dev), n, 2 * half,
-                                      _need(out, "out", torch.bfloat16, (M, n), dev),
-                                      None if status is None else _need(status, "status", torch.int32, (1,), dev),
+                                      place, None if status is None else _need(status, "status", torch.int32, (1,), dev),
                                       _raw_stream(stream, dev)), "moe_matmul_fp4_block")
     _used_on(stream, out)
     return out
@@ -567,6 +574,9 @@ def moe_layer_few(x: torch.Tensor, router: Optional[torch.Tensor], top_k: int, W
         probs = _need(routing[1], "topk_probs", torch.float32, (T, top_k), dev)
     if out is None:
         out = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
+        place = out.data_ptr() or None
+    else:
+        place = _need(out, "out", torch.bfloat16, (T, H), dev)
     idx_out = probs_out = None
     if return_routing:
         idx_out = torch.empty(T, top_k, dtype=torch.int64, device=dev)
@@ -574,8 +584,7 @@ def moe_layer_few(x: torch.Tensor, router: Optional[torch.Tensor], top_k: int, W
     ws = torch.empty(_bytes("moe_layer_few_workspace_bytes", dev.index, T, E, top_k, I), dtype=torch.uint8, device=dev)
     f = N.MoeFew(T, E, top_k, H, I, r_dtype or 0, fmt, _need(x, "x", torch.bfloat16, (T, H), dev), r, idx, probs,
                  _need(W1, "W1", wt, (E, 2 * I, h), dev), s1, _need(W2, "W2", wt, (E, H, i), dev), s2,
-                 _need(out, "out", torch.bfloat16, (T, H), dev),
-                 idx_out.data_ptr() or None if return_routing else None, probs_out.data_ptr() or None if return_routing else None,
+                 place, idx_out.data_ptr() or None if return_routing else None, probs_out.data_ptr() or None if return_routing else None,
                  None if status is None else _need(status, "status", torch.int32, (1,), dev), ws.data_ptr())
     _check(N.lib.moe_layer_few(f, _raw_stream(stream, dev)), "moe_layer_few")
     _used_on(stream, out, idx_out, probs_out, ws)

@@ -1120,7 +1120,7 @@ FewWorkspace few_workspace(int32_t T, int32_t E, int32_t K, int32_t I) {
   FewWorkspace w{};
   w.logits = 256;  // behind the barrier's word
   w.h = w.logits + up(static_cast<size_t>(T) * E * sizeof(float));
-  w.total = w.h + up(static_cast<size_t>(T) * K * I * 2);
+  w.total = w.h + up(static_cast<size_t>(T) * K * I * sizeof(float));
   return w;
 }
 
@@ -1152,13 +1152,15 @@ moe_status moe_layer_few(const moe_few* f, moe_stream_t stream) {
   moe_status st = check_few(f->T, f->E, f->K, f->I);
   if (st != MOE_OK) return st;
   if ((st = check_hidden(f->H)) != MOE_OK) return st;
+  MOE_REQUIRE(f->H <= 1 << 20 && f->I <= 1 << 20, MOE_ERR_UNSUPPORTED_SHAPE, "moe_layer_few: H and I must be at most 2^20 (got %d, %d)",
+              f->H, f->I);
   static_assert(FEW_TOKENS == MOE_FEW_TOKENS && FEW_TOP_K == MOE_FEW_TOP_K && FEW_FP8 == MOE_WEIGHTS_FP8_BLOCK &&
                 FEW_FP4 == MOE_WEIGHTS_FP4_BLOCK, "one set of constants");
   MOE_REQUIRE(f->weights >= MOE_WEIGHTS_BF16 && f->weights <= MOE_WEIGHTS_FP4_BLOCK, MOE_ERR_INVALID_ARG,
               "moe_layer_few: unknown weight format %d", f->weights);
   MOE_REQUIRE(f->router_dtype == MOE_DTYPE_BF16 || f->router_dtype == MOE_DTYPE_F32, MOE_ERR_INVALID_ARG,
               "moe_layer_few: unknown type %d", f->router_dtype);
-  MOE_REQUIRE(few_layer_fits(f->T, f->K, f->H, f->I), MOE_ERR_UNSUPPORTED_SHAPE,
+  MOE_REQUIRE(few_layer_fits(f->weights, f->T, f->K, f->H, f->I), MOE_ERR_UNSUPPORTED_SHAPE,
               "moe_layer_few: the rows of %d tokens of H=%d and I=%d do not fit in shared memory", f->T, f->H, f->I);
   const bool coded = f->weights != MOE_WEIGHTS_BF16;
   MOE_REQUIRE(f->T == 0 || (f->x && f->W1 && f->W2 && f->out && f->workspace && (!coded || (f->W1_scale && f->W2_scale))),
@@ -1188,7 +1190,7 @@ moe_status moe_layer_few(const moe_few* f, moe_stream_t stream) {
   g.T = f->T, g.E = f->E, g.K = f->K, g.H = f->H, g.I = f->I;
   g.barrier = reinterpret_cast<unsigned*>(base);
   g.logits = reinterpret_cast<float*>(base + w.logits);
-  g.h = reinterpret_cast<uint16_t*>(base + w.h);
+  g.h = reinterpret_cast<float*>(base + w.h);
   g.out = f->out;
   g.idx_out = f->idx_out;
   g.probs_out = f->probs_out;

@@ -302,14 +302,14 @@ struct FewLayer {
   const void *W1, *S1, *W2, *S2;
   int T, E, K, H, I;
   float* logits;             // scratch: [T, E]
-  uint16_t* h;               // scratch: [T K, I]
+  float* h;                  // scratch: [T K, I]
   unsigned* barrier;         // scratch: one word
   uint16_t* out;             // [T, H]
   int64_t* idx_out;          // [T, K], nullable (both)
   float* probs_out;
   int* status;
 };
-bool few_layer_fits(int T, int K, int H, int I);
+bool few_layer_fits(int format, int T, int K, int H, int I);
 cudaError_t launch_few_layer(const FewLayer& f, cudaStream_t s);
 
 // AdamW over many tensors (adamw.cu), up to ADAMW_BATCH of them a launch.

@@ -1,7 +1,7 @@
 // A whole MoE layer for at most 8 tokens, in two launches.
 //
 //   logits = x R^T;  e_k, w_k: the K largest of a token and their softmax
-//   h_k = silu(x Wg[e_k]^T) * (x Wu[e_k]^T)         (rounded to bf16)
+//   h_k = silu(x Wg[e_k]^T) * (x Wu[e_k]^T)
 //   out = sum_k w_k (h_k W2[e_k]^T)
 //
 // With so few rows the layer is a stream over the active experts' weights, read
@@ -32,10 +32,13 @@
 // of a row.  Codes are multiplied as f16 numbers, which they are exactly, by
 // tokens (and h) in f16 with a power of two for each 128 values: exact for
 // bf16 values down to 2^-31 of their block's largest, and within 2^-39 of that below
-// it.  (mma.sync on e4m3 operands takes 28 cycles an SM quarter here, on f16 12 for
+// it.  With bf16 weights h, which is held in fp32, is multiplied as the sum of two
+// bf16 numbers: rounded to one it would add as much error as the output's rounding.  (mma.sync on e4m3 operands takes 28 cycles an SM quarter here, on f16 12 for
 // half of K, and converting a pair of codes 2.3.)
 
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "fp4.cuh"
@@ -59,7 +62,10 @@ constexpr int SMEM_LIMIT = 232448;
 template <int FMT>
 __host__ __device__ constexpr int row_bytes(int K) { return FMT == FEW_BF16 ? 2 * K : FMT == FEW_FP8 ? K : K / 2; }
 
+// bytes from row to row of tokens, and of h, in shared memory
 __host__ __device__ constexpr int token_pitch(int K) { return 2 * K + 64; }
+template <int FMT>
+__host__ __device__ constexpr int h_pitch(int K) { return (FMT == FEW_BF16 ? 4 : 2) * K + 64; }
 
 struct Smem {
   int ok;
@@ -82,7 +88,7 @@ struct FewArgs {
   int T, E, K, H, I;
   int slots, cap;            // of a warp; rows of h that shared memory holds
   int region;                // bytes of the tokens' rows and their scales
-  uint16_t* h;               // [T K, I]
+  float* h;                  // [T K, I]
   unsigned* barrier;
   uint16_t* out;
   int64_t* idx_out;
@@ -219,12 +225,35 @@ __device__ __forceinline__ void pick_experts(const float* logits, int E, int K, 
 }
 
 // ---------------------------------------------------------------- rows of tokens
+// Eight f16 numbers of a block of 128 that 16 threads hold, in units of its scale:
+// 2^(floor(log2 amax) - 14), at least 2^-126, so that values are below 2^15.
+__device__ __forceinline__ uint4 scaled_f16(const float (&v)[8], float top, float& scale) {
+  const uint32_t bits = __float_as_uint(top);
+  const uint32_t e = bits >> 23 > 15u ? (bits >> 23) - 14u : 1u;
+  const float inv = __uint_as_float((254u - e) << 23);
+  scale = bits >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : __uint_as_float(e << 23);
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const __half2 h = __floats2half2_rn(v[2 * k] * inv, v[2 * k + 1] * inv);
+    w[k] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Where the 16 bytes of values [8 v, 8 v + 8) of a row lie: in their place, or for e4m3 of
+// each 64 first the first 8 of every 16, then the others, as a lane's codes meet them.
+template <int FMT>
+__device__ __forceinline__ int place_of(int v) {
+  return FMT == FEW_FP8 ? (v & ~7) | (v & 1) << 2 | (v & 7) >> 1 : v;
+}
+
 // `rows` rows of K bf16 values (row r from src + r K) into shared memory, as the
 // products read them: as they are, or as f16 with a scale for each 128 of a
 // row.  By `threads` threads, of which this is number `tid`; each asks for four
 // pieces of 16 bytes before it uses the first.
 template <int FMT>
-__device__ __forceinline__ void stage_rows(const uint16_t* src, int rows, int K, uint8_t* dst, float* scales, int tid, int threads) {
+__device__ __forceinline__ void stage_tokens(const uint16_t* src, int rows, int K, uint8_t* dst, float* scales, int tid, int threads) {
   const int pitch = token_pitch(K), per_row = K >> 3, all = rows * per_row;
   for (int i0 = tid; i0 < all; i0 += 4 * threads) {
     uint4 q[4];
@@ -236,32 +265,65 @@ __device__ __forceinline__ void stage_rows(const uint16_t* src, int rows, int K,
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int i = i0 + j * threads;
+      if (i >= all) break;  // (all of a block's 16 threads or none: K is a multiple of 128)
       if constexpr (FMT != FEW_BF16) {
-        // 16 threads hold a block (all or none of them: K is a multiple of 128)
         const unsigned half = 0xffffu << (tid & 16);
         uint32_t top = bf16x2_abs_max(bf16x2_abs_max(q[j].x, q[j].y), bf16x2_abs_max(q[j].z, q[j].w));
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) top = bf16x2_abs_max(top, __shfl_xor_sync(half, top, o));
-        if (i >= all) break;
-        const uint32_t bits = __float_as_uint(max_nan(bf16_lo(top), bf16_hi(top)));
-        const bool bad = bits >= 0x7f800000u;
-        // 2^(floor(log2 amax) - 14), at least 2^-126: values below 2^15
-        const uint32_t e = bits >> 23 > 15u ? (bits >> 23) - 14u : 1u;
-        const float inv = __uint_as_float((254u - e) << 23);
-        uint32_t w[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
+        const uint32_t w[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
+        float v[8], scale;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[2 * k] = bf16_lo(w[k]), v[2 * k + 1] = bf16_hi(w[k]);
+        q[j] = scaled_f16(v, max_nan(bf16_lo(top), bf16_hi(top)), scale);
+        if ((tid & 15) == 0) scales[i >> 4] = scale;
+      }
+      const int r = i / per_row, v = i - r * per_row;
+      *reinterpret_cast<uint4*>(dst + r * pitch + place_of<FMT>(v) * 16) = q[j];
+    }
+  }
+}
+
+// The same for rows of h in fp32: f16 with scales, or the nearest bf16 and, 2 K
+// bytes on, what that leaves.
+template <int FMT>
+__device__ __forceinline__ void stage_h(const float* src, int rows, int K, uint8_t* dst, float* scales) {
+  const int pitch = h_pitch<FMT>(K), per_row = K >> 3, all = rows * per_row;
+  for (int i0 = threadIdx.x; i0 < all; i0 += 2 * THREADS) {
+    float4 q[2][2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int i = i0 + j * THREADS;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        q[j][k] = i < all ? __ldcg(reinterpret_cast<const float4*>(src) + 2 * i + k) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int i = i0 + j * THREADS;
+      if (i >= all) break;
+      const float v[8] = {q[j][0].x, q[j][0].y, q[j][0].z, q[j][0].w, q[j][1].x, q[j][1].y, q[j][1].z, q[j][1].w};
+      const int r = i / per_row, c = i - r * per_row;
+      uint8_t* at = dst + r * pitch + place_of<FMT>(c) * 16;
+      if constexpr (FMT == FEW_BF16) {
+        uint32_t hi[4], lo[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const __half2 h = __floats2half2_rn(bf16_lo(w[k]) * inv, bf16_hi(w[k]) * inv);
-          w[k] = *reinterpret_cast<const uint32_t*>(&h);
+          hi[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
+          lo[k] = pack_bf16x2(v[2 * k] - bf16_lo(hi[k]), v[2 * k + 1] - bf16_hi(hi[k]));
         }
-        q[j] = make_uint4(w[0], w[1], w[2], w[3]);
-        if ((tid & 15) == 0) scales[i >> 4] = bad ? __uint_as_float(0x7fc00000u) : __uint_as_float(e << 23);
+        *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(at + 2 * K) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      } else {
+        const unsigned half = 0xffffu << (threadIdx.x & 16);
+        float top = 0.f, scale;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) top = max_nan(top, fabsf(v[k]));
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(half, top, o));
+        *reinterpret_cast<uint4*>(at) = scaled_f16(v, top, scale);
+        if ((threadIdx.x & 15) == 0) scales[i >> 4] = scale;
       }
-      if (i >= all) break;
-      const int r = i / per_row, v = i - r * per_row;
-      // (e4m3: of each 64 the first 8 of every 16, then the others, as a lane's codes meet them)
-      const int at = FMT == FEW_FP8 ? (v & ~7) | (v & 1) << 2 | (v & 7) >> 1 : v;
-      *reinterpret_cast<uint4*>(dst + r * pitch + at * 16) = q[j];
     }
   }
 }
@@ -401,8 +463,9 @@ struct Cursor {
 // ---------------------------------------------------------------- products
 // d[16 rows x 8 tokens] += a slot's rows times the tokens' rows.  `token`: the row
 // of token lane / 4 (0: none, zeros), s0 and s1 the scales of tokens 2 (lane %
-// 4) and the next, `st` the piece, `bytes` those of a weight row.
-template <int FMT>
+// 4) and the next, `st` the piece, `bytes` those of a weight row.  With SUM (bf16)
+// a token's row is followed by what it was rounded from.
+template <int FMT, bool SUM>
 __device__ __forceinline__ void multiply(float (&d)[4], uint32_t slot, int st, int bytes, int lane, uint32_t token, const float* s0,
                                          const float* s1) {
   const int g = lane >> 2, t = lane & 3;
@@ -418,6 +481,11 @@ __device__ __forceinline__ void multiply(float (&d)[4], uint32_t slot, int st, i
       const uint4 b = token ? lds128(token + st * PIECE + h * 64 + 16 * t) : zero;
       mma_bf16_16x8x16(d, a.x, c.x, a.y, c.y, b.x, b.y);
       mma_bf16_16x8x16(d, a.z, c.z, a.w, c.w, b.z, b.w);
+      if constexpr (SUM) {
+        const uint4 r = token ? lds128(token + bytes + st * PIECE + h * 64 + 16 * t) : zero;
+        mma_bf16_16x8x16(d, a.x, c.x, a.y, c.y, r.x, r.y);
+        mma_bf16_16x8x16(d, a.z, c.z, a.w, c.w, r.z, r.w);
+      }
     } else if constexpr (FMT == FEW_FP8) {
       const uint32_t part = (h * 4 + t) << 4;
       const uint4 a = lds128(lo ^ part), c = lds128(hi ^ part);
@@ -493,7 +561,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
   int chosen = -1;
   float prob = 0.f;
   if (warp >= TOK) {
-    stage_rows<FMT>(args.x, T, H, region, s_scale, threadIdx.x - 32 * TOK, THREADS - 32 * TOK);
+    stage_tokens<FMT>(args.x, T, H, region, s_scale, threadIdx.x - 32 * TOK, THREADS - 32 * TOK);
   } else if (warp < T) {
     if (args.logits) {
       const float* l = args.logits + warp * E;
@@ -570,10 +638,10 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
   for (int i = 0; i < args.slots; ++i) cursor.issue(slots + i * SLOT);
   __syncthreads();
   int slot = 0;
-  auto next = [&](float (&d)[4], int st, int bytes, uint32_t token, const float* s0, const float* s1) {
+  auto next = [&](auto sum, float (&d)[4], int st, int bytes, uint32_t token, const float* s0, const float* s1) {
     cp_async_wait(args.slots - 1);
     __syncwarp();
-    multiply<FMT>(d, slots + slot * SLOT, st, bytes, lane, token, s0, s1);
+    multiply<FMT, decltype(sum)::value>(d, slots + slot * SLOT, st, bytes, lane, token, s0, s1);
     __syncwarp();
     cursor.issue(slots + slot * SLOT);
     if (++slot == args.slots) slot = 0;
@@ -597,7 +665,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
       if (++turn == WARPS / TEAM) turn = 0;
       if (!mine) continue;
       float d[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int st = warp % TEAM; st * PIECE < bytes1; st += TEAM) next(d, st, bytes1, token, s0, s1);
+      for (int st = warp % TEAM; st * PIECE < bytes1; st += TEAM) next(std::false_type{}, d, st, bytes1, token, s0, s1);
 #pragma unroll
       for (int i = 0; i < 4; ++i) s.part[par][warp][i][lane] = d[i];
       // one meeting a tile: this parity's sums are written again after the next
@@ -613,8 +681,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
             gate += s.part[par][team * TEAM + w][tok & 1][i * 4 + (tok >> 1)];
             up += s.part[par][team * TEAM + w][2 + (tok & 1)][i * 4 + (tok >> 1)];
           }
-          args.h[static_cast<long long>(row) * I + j0 + i] =
-              __bfloat16_as_ushort(__float2bfloat16_rn(gate / (1.0f + expf(-gate)) * up));
+          args.h[static_cast<long long>(row) * I + j0 + i] = gate / (1.0f + expf(-gate)) * up;
         }
       }
       par ^= 1;
@@ -646,7 +713,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
   }
 
   // ---- out
-  const int hp = token_pitch(I), steps2 = (bytes2 + PIECE - 1) / PIECE;
+  const int hp = h_pitch<FMT>(I), steps2 = (bytes2 + PIECE - 1) / PIECE;
   float* h_scale = reinterpret_cast<float*>(region + args.cap * hp);
   const bool whole = s.first[active] <= args.cap;  // all rows of h at once
   for (int m0 = r0; m0 < r1; m0 += 16) {
@@ -657,7 +724,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
       while (sb < active && s.first[sb + 1] - s.first[sa] <= args.cap) ++sb;
       if (!whole || m0 == r0) {
         __syncthreads();
-        stage_rows<FMT>(args.h + static_cast<long long>(s.first[sa]) * I, s.first[sb] - s.first[sa], I, region, h_scale, threadIdx.x, THREADS);
+        stage_h<FMT>(args.h + static_cast<long long>(s.first[sa]) * I, s.first[sb] - s.first[sa], I, region, h_scale);
         __syncthreads();
       }
       while (true) {
@@ -668,7 +735,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
         const float* s0 = h_scale + (max(row0, base) - base) * (I >> 7);
         const float* s1 = h_scale + (max(row1, base) - base) * (I >> 7);
         float d[4] = {0.f, 0.f, 0.f, 0.f};
-        next(d, st, bytes2, token, s0, s1);
+        next(std::bool_constant<FMT == FEW_BF16>{}, d, st, bytes2, token, s0, s1);
         if (row0 >= 0) {
           const float w = s.weight[a][2 * t];
           acc[0] = fmaf(w, d[0], acc[0]);
@@ -700,17 +767,18 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
 
 constexpr int FIXED = sizeof(Smem);
 
+template <int FMT>
 bool plan(FewArgs& g, size_t* smem) {
-  const int x_row = token_pitch(g.H) + 4 * (g.H / 128), h_row = token_pitch(g.I) + 4 * (g.I / 128);
+  const long long x_row = token_pitch(g.H) + 4 * (g.H / 128), h_row = h_pitch<FMT>(g.I) + 4 * (g.I / 128);
   // all rows of h where they leave three slots a warp, else as many as there are tokens
-  const int need = g.T * (x_row > h_row ? x_row : h_row), most = SMEM_LIMIT - FIXED - 128 - 3 * WARPS * SLOT;
-  int room = g.T * g.K * h_row;
+  const long long need = g.T * (x_row > h_row ? x_row : h_row), most = SMEM_LIMIT - FIXED - 128 - 3 * WARPS * SLOT;
+  long long room = g.T * g.K * h_row;
   if (room > most) room = most;
   if (room < need) room = need;
-  g.cap = room / h_row < g.T * g.K ? room / h_row : g.T * g.K;
-  g.region = (room + 127) / 128 * 128;
-  const int left = SMEM_LIMIT - FIXED - g.region;
-  g.slots = left < 0 ? 0 : left / (WARPS * SLOT);
+  if (room > SMEM_LIMIT - FIXED - 128) return false;
+  g.cap = static_cast<int>(room / h_row < g.T * g.K ? room / h_row : g.T * g.K);
+  g.region = static_cast<int>((room + 127) / 128 * 128);
+  g.slots = (SMEM_LIMIT - FIXED - g.region) / (WARPS * SLOT);
   if (g.slots > MAX_SLOTS) g.slots = MAX_SLOTS;
   if (g.slots < 2) return false;
   *smem = static_cast<size_t>(g.slots) * WARPS * SLOT + g.region + FIXED;
@@ -720,7 +788,7 @@ bool plan(FewArgs& g, size_t* smem) {
 template <int FMT>
 cudaError_t launch(FewArgs g, const void* router, bool router_f32, float* logits, cudaStream_t s) {
   size_t smem = 0;
-  if (!plan(g, &smem)) return cudaErrorInvalidValue;
+  if (!plan<FMT>(g, &smem)) return cudaErrorInvalidValue;
   auto first = router_f32 ? few_logits_kernel<true> : few_logits_kernel<false>;
   cudaError_t err = launch_dependent(first, router ? g.E : 1, LOGIT_THREADS, 0, s, g.x, router, g.T, g.E, g.H,
                                      router ? logits : static_cast<float*>(nullptr), g.barrier);
@@ -745,11 +813,11 @@ cudaError_t launch(FewArgs g, const void* router, bool router_f32, float* logits
 
 }  // namespace
 
-bool few_layer_fits(int T, int K, int H, int I) {
+bool few_layer_fits(int format, int T, int K, int H, int I) {
   FewArgs g{};
   g.T = T, g.K = K, g.H = H, g.I = I;
   size_t smem;
-  return plan(g, &smem);
+  return format == FEW_BF16 ? plan<FEW_BF16>(g, &smem) : format == FEW_FP8 ? plan<FEW_FP8>(g, &smem) : plan<FEW_FP4>(g, &smem);
 }
 
 cudaError_t launch_few_layer(const FewLayer& f, cudaStream_t s) {
