@@ -18,10 +18,10 @@ from .block import (moe_norm_in, moe_norm_in_backward, moe_norm_out, moe_norm_ou
                     AdamWState, moe_adamw_step,
                     moe_quantize_fp8_block, moe_matmul_fp8_block, moe_grouped_experts_fp8_block,
                     moe_quantize_fp4_block, moe_dequantize_fp4_block, moe_matmul_fp4_block, moe_fp4_scale_tiles,
-                    moe_fp4_scale_rows, moe_layer_few)
+                    moe_fp4_scale_rows, moe_layer_few, moe_layer_few_fits)
 from . import _native
 from . import ops
-from .ops import moe_block, moe_layer, moe_layer_from_logits, moe_layer_fp8_block
+from .ops import moe_block, moe_layer, moe_layer_from_logits, moe_layer_fp8_block, moe_layer_fp4_block
 
 __all__ = [
     "Layout", "MoEError", "ForwardResult", "worst_case_rows", "moe_router_topk",
@@ -35,6 +35,7 @@ __all__ = [
     "AdamWState", "moe_adamw_step",
     "moe_quantize_fp8_block", "moe_matmul_fp8_block", "moe_grouped_experts_fp8_block",
     "moe_quantize_fp4_block", "moe_dequantize_fp4_block", "moe_matmul_fp4_block", "moe_fp4_scale_tiles", "moe_fp4_scale_rows",
-    "moe_layer_few",
+    "moe_layer_few", "moe_layer_few_fits",
     "_native", "ops", "moe_block", "moe_layer", "moe_layer_from_logits", "moe_layer_fp8_block",
+    "moe_layer_fp4_block",
 ]

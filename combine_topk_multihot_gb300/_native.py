@@ -141,9 +141,11 @@ SIGNATURES = {
     "moe_dequantize_fp4_block": (c_int32, [_P, _P, c_int64, c_int64, c_int32, c_int32, _P, _P]),
     "moe_matmul_fp4_block": (c_int32, [_P, _P, c_int32, _P, _P, c_int32, c_int32, _P, _P, _P]),
     "moe_layer_few_workspace_bytes": (c_int32, [c_int32, c_int32, c_int32, c_int32, ctypes.POINTER(c_size_t)]),
+    "moe_layer_few_fits": (c_int32, [c_int32] * 6),
     "moe_layer_few": (c_int32, [ctypes.POINTER(MoeFew), _P]),
     "moe_selftest_wait_timeout": (c_int32, [_P, c_int64, _P, _P]),
     "moe_selftest_block_product_tiles": (c_int32, [c_int32]),
+    "moe_selftest_few_ctas": (c_int32, [c_int32]),
     "moe_selftest_norm_rows": (c_int32, [c_int64]),
     "moe_route_to_multihot_backward": (c_int32, [_P, _P, _P, c_int32, c_int32, c_int32, _P, _P]),
 }

@@ -533,6 +533,18 @@ def moe_fp4_scale_rows(tiles: torch.Tensor, rows: int, cols: int) -> torch.Tenso
 
 
 # ------------------------------------------------------------------ a layer for few tokens
+def _few_format(W1_scale: Optional[torch.Tensor]) -> int:
+    """The weights' format, which their scales' type tells."""
+    if W1_scale is None:
+        return N.MOE_WEIGHTS_BF16
+    return N.MOE_WEIGHTS_FP8_BLOCK if W1_scale.dtype is torch.float32 else N.MOE_WEIGHTS_FP4_BLOCK
+
+
+def moe_layer_few_fits(T: int, E: int, top_k: int, H: int, I: int, W1_scale: Optional[torch.Tensor] = None) -> bool:
+    """Whether moe_layer_few takes a layer of these sizes, from weights of W1_scale's format."""
+    return bool(N.lib.moe_layer_few_fits(T, E, top_k, H, I, _few_format(W1_scale)))
+
+
 def moe_layer_few(x: torch.Tensor, router: Optional[torch.Tensor], top_k: int, W1: torch.Tensor, W2: torch.Tensor,
                   W1_scale: Optional[torch.Tensor] = None, W2_scale: Optional[torch.Tensor] = None, routing=None,
                   return_routing: bool = False, out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
@@ -554,14 +566,15 @@ def moe_layer_few(x: torch.Tensor, router: Optional[torch.Tensor], top_k: int, W
     E, I = W1.shape[0], W1.shape[1] // 2
     if (W1_scale is None) != (W2_scale is None):
         raise ValueError("give W1_scale and W2_scale, or neither")
-    if W1_scale is None:
-        fmt, wt, h, i, s1, s2 = N.MOE_WEIGHTS_BF16, torch.bfloat16, H, I, None, None
-    elif W1_scale.dtype is torch.float32:
-        fmt, wt, h, i = N.MOE_WEIGHTS_FP8_BLOCK, torch.uint8, H, I
+    fmt = _few_format(W1_scale)
+    if fmt == N.MOE_WEIGHTS_BF16:
+        wt, h, i, s1, s2 = torch.bfloat16, H, I, None, None
+    elif fmt == N.MOE_WEIGHTS_FP8_BLOCK:
+        wt, h, i = torch.uint8, H, I
         s1 = _need(W1_scale, "W1_scale", torch.float32, (E, _blocks(2 * I), _blocks(H)), dev)
         s2 = _need(W2_scale, "W2_scale", torch.float32, (E, _blocks(H), _blocks(I)), dev)
     else:
-        fmt, wt, h, i = N.MOE_WEIGHTS_FP4_BLOCK, torch.uint8, H // 2, I // 2
+        wt, h, i = torch.uint8, H // 2, I // 2
         s1 = _need(W1_scale, "W1_scale", torch.uint8, (E, *_fp4_tiles(2 * I, H)), dev)
         s2 = _need(W2_scale, "W2_scale", torch.uint8, (E, *_fp4_tiles(H, I)), dev)
     if (router is None) == (routing is None):

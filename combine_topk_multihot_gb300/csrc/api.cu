@@ -1135,6 +1135,20 @@ moe_status check_few(int32_t T, int32_t E, int32_t K, int32_t I) {
   return MOE_OK;
 }
 
+moe_status check_few_all(int32_t T, int32_t E, int32_t K, int32_t H, int32_t I, int32_t weights) {
+  moe_status st = check_few(T, E, K, I);
+  if (st != MOE_OK) return st;
+  if ((st = check_hidden(H)) != MOE_OK) return st;
+  MOE_REQUIRE(H <= 1 << 20 && I <= 1 << 20, MOE_ERR_UNSUPPORTED_SHAPE, "moe_layer_few: H and I must be at most 2^20 (got %d, %d)", H, I);
+  static_assert(FEW_TOKENS == MOE_FEW_TOKENS && FEW_TOP_K == MOE_FEW_TOP_K && int(FEW_FP8) == int(MOE_WEIGHTS_FP8_BLOCK) &&
+                int(FEW_FP4) == int(MOE_WEIGHTS_FP4_BLOCK), "one set of constants");
+  MOE_REQUIRE(weights >= MOE_WEIGHTS_BF16 && weights <= MOE_WEIGHTS_FP4_BLOCK, MOE_ERR_INVALID_ARG,
+              "moe_layer_few: unknown weight format %d", weights);
+  MOE_REQUIRE(few_layer_fits(weights, T, K, H, I), MOE_ERR_UNSUPPORTED_SHAPE,
+              "moe_layer_few: the rows of %d tokens of H=%d and I=%d do not fit in shared memory", T, H, I);
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1147,21 +1161,16 @@ moe_status moe_layer_few_workspace_bytes(int32_t T, int32_t E, int32_t K, int32_
   return MOE_OK;
 }
 
+int32_t moe_layer_few_fits(int32_t T, int32_t E, int32_t K, int32_t H, int32_t I, int32_t weights) {
+  return check_few_all(T, E, K, H, I, weights) == MOE_OK;
+}
+
 moe_status moe_layer_few(const moe_few* f, moe_stream_t stream) {
   MOE_REQUIRE(f != nullptr, MOE_ERR_INVALID_ARG, "moe_layer_few: NULL pointer");
-  moe_status st = check_few(f->T, f->E, f->K, f->I);
+  moe_status st = check_few_all(f->T, f->E, f->K, f->H, f->I, f->weights);
   if (st != MOE_OK) return st;
-  if ((st = check_hidden(f->H)) != MOE_OK) return st;
-  MOE_REQUIRE(f->H <= 1 << 20 && f->I <= 1 << 20, MOE_ERR_UNSUPPORTED_SHAPE, "moe_layer_few: H and I must be at most 2^20 (got %d, %d)",
-              f->H, f->I);
-  static_assert(FEW_TOKENS == MOE_FEW_TOKENS && FEW_TOP_K == MOE_FEW_TOP_K && FEW_FP8 == MOE_WEIGHTS_FP8_BLOCK &&
-                FEW_FP4 == MOE_WEIGHTS_FP4_BLOCK, "one set of constants");
-  MOE_REQUIRE(f->weights >= MOE_WEIGHTS_BF16 && f->weights <= MOE_WEIGHTS_FP4_BLOCK, MOE_ERR_INVALID_ARG,
-              "moe_layer_few: unknown weight format %d", f->weights);
   MOE_REQUIRE(f->router_dtype == MOE_DTYPE_BF16 || f->router_dtype == MOE_DTYPE_F32, MOE_ERR_INVALID_ARG,
               "moe_layer_few: unknown type %d", f->router_dtype);
-  MOE_REQUIRE(few_layer_fits(f->weights, f->T, f->K, f->H, f->I), MOE_ERR_UNSUPPORTED_SHAPE,
-              "moe_layer_few: the rows of %d tokens of H=%d and I=%d do not fit in shared memory", f->T, f->H, f->I);
   const bool coded = f->weights != MOE_WEIGHTS_BF16;
   MOE_REQUIRE(f->T == 0 || (f->x && f->W1 && f->W2 && f->out && f->workspace && (!coded || (f->W1_scale && f->W2_scale))),
               MOE_ERR_INVALID_ARG, "moe_layer_few: NULL pointer");

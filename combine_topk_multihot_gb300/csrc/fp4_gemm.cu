@@ -77,6 +77,7 @@ struct Args {
   uint16_t* out;
   int out_staged;
   int* status;
+  int load_tiles;  // tiles a CTA loads operands for: all, but in the self-test
 };
 
 // Loads whose arrival is counted on this CTA's barrier, or on the even CTA's.
@@ -206,7 +207,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint32_t phase = 0;
     long long issued = 0;
     bool ok = true;
-    for (int tile = tile0; tile < args.tiles && ok; tile += step) {
+    int left = args.load_tiles;
+    for (int tile = tile0; tile < args.tiles && ok && left > 0; tile += step, --left) {
       const int mt = tile / args.n_tiles, n0 = (tile - mt * args.n_tiles) * BN;
       const int row_tile = mt * CTAS + rank;  // this CTA's 128 rows of a
       for (int ks = 0; ks < args.k_steps; ++ks) {
@@ -462,6 +464,7 @@ cudaError_t launch_fp4_matmul_tc(const uint8_t* a, const uint8_t* a_scale, int M
   g.out = out;
   g.out_staged = N % 8 == 0;
   g.status = status;
+  g.load_tiles = block_load_tiles();
   const bool pair = M > BM;
   const long long mt = pair ? (static_cast<long long>(M) + 2 * BM - 1) / (2 * BM) : 1;
   const int at_once = pair ? sm_count() / 2 : sm_count();

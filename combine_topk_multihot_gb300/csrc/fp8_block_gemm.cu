@@ -524,6 +524,7 @@ cudaError_t launch(const void* a, uint64_t a_rows, const void* b, uint64_t b_row
 }  // namespace
 
 void selftest_block_load_tiles(int tiles) { tls_load_tiles = tiles; }
+int block_load_tiles() { return tls_load_tiles; }
 
 cudaError_t launch_block_matmul_tc(const uint8_t* a, const float* a_scale, int M, const uint8_t* b,
                                    const float* b_scale, int N, int K, uint16_t* out, int* status,

@@ -271,6 +271,8 @@ cudaError_t launch_block_experts_tc(const uint8_t* x_q, const float* x_scale, co
 // memory only; its tensor-core launches of these products load operands for
 // `tiles` tiles a CTA only.
 void selftest_block_load_tiles(int tiles);
+int block_load_tiles();
+void selftest_few_ctas(int ctas);
 void selftest_norm_load_rows(long long rows);
 long long norm_load_rows(long long T);
 

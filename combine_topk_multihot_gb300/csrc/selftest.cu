@@ -51,6 +51,12 @@ extern "C" moe_status moe_selftest_wait_timeout(int32_t* status, int64_t limit_n
   return MOE_OK;
 }
 
+extern "C" moe_status moe_selftest_few_ctas(int32_t ctas) {
+  if (ctas < -1) return set_last_error(MOE_ERR_INVALID_ARG, "moe_selftest_few_ctas: ctas must be >= 0, or -1 for all");
+  selftest_few_ctas(ctas < 0 ? 0x7fffffff : ctas);
+  return MOE_OK;
+}
+
 extern "C" moe_status moe_selftest_block_product_tiles(int32_t tiles) {
   if (tiles < -1)
     return set_last_error(MOE_ERR_INVALID_ARG, "moe_selftest_block_product_tiles: tiles must be >= 0, or -1 for all");

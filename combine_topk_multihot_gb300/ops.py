@@ -9,8 +9,9 @@ between them as its component tensors and is put back together on the far
 side.  Here every step of the layer is such an operator: the router (with
 its gradient registered on the operator), multihot, dispatch, grouped
 experts, combine, and the four backward steps.  So are the norms before and
-after a block (norm_in and norm_out, with their gradients) and the block-scaled
-e4m3 quantiser, product and experts.
+after a block (norm_in and norm_out, with their gradients), the block-scaled
+e4m3 quantiser, product and experts, the e2m1 quantiser, its way back and its
+product, and the layer for at most 8 tokens.
 
 Every operator takes the sync-free route: the expanded buffers are sized for
 the worst case (T*K + E*(pad_multiple - 1) rows), nothing is read back to the
@@ -459,25 +460,111 @@ def moe_layer_fp8_block(x: Tensor, topk_idx: Tensor, topk_probs: Tensor, W1_q: T
     return (out, lay[-1]) if return_status else out
 
 
+# ------------------------------------------------------------------ e2m1 with a scale per 32, layers for few tokens
+@torch.library.custom_op(f"{NS}::quantize_fp4_block", mutates_args=(), device_types="cuda")
+def quantize_fp4_block(src: Tensor) -> Tuple[Tensor, Tensor]:
+    """(codes uint8, two a byte; scales uint8 in tiles)."""
+    return _b.moe_quantize_fp4_block(src.contiguous())
+
+
+@quantize_fp4_block.register_fake
+def _(src):
+    R, C = src.shape[-2:]
+    return (src.new_empty((*src.shape[:-1], C // 2), dtype=torch.uint8),
+            src.new_empty((*src.shape[:-2], (R + 127) // 128, (C + 127) // 128, 32, 4, 4), dtype=torch.uint8))
+
+
+@torch.library.custom_op(f"{NS}::dequantize_fp4_block", mutates_args=(), device_types="cuda")
+def dequantize_fp4_block(codes: Tensor, scales: Tensor) -> Tensor:
+    """What they stand for, in bf16."""
+    return _b.moe_dequantize_fp4_block(codes, scales)
+
+
+@dequantize_fp4_block.register_fake
+def _(codes, scales):
+    return codes.new_empty((*codes.shape[:-1], 2 * codes.shape[-1]), dtype=torch.bfloat16)
+
+
+@torch.library.custom_op(f"{NS}::matmul_fp4_block", mutates_args=(), device_types="cuda")
+def matmul_fp4_block(a_q: Tensor, a_scale: Tensor, b_q: Tensor, b_scale: Tensor) -> Tensor:
+    """a b^T, [M, N] bf16."""
+    return _b.moe_matmul_fp4_block(a_q, a_scale, b_q, b_scale)
+
+
+@matmul_fp4_block.register_fake
+def _(a_q, a_scale, b_q, b_scale):
+    return a_q.new_empty(a_q.shape[0], b_q.shape[0], dtype=torch.bfloat16)
+
+
+@torch.library.custom_op(f"{NS}::layer_few", mutates_args=(), device_types="cuda")
+def layer_few(x: Tensor, router: Optional[Tensor], topk_idx: Optional[Tensor], topk_probs: Optional[Tensor], top_k: int, W1: Tensor,
+              W2: Tensor, W1_scale: Optional[Tensor], W2_scale: Optional[Tensor]) -> Tuple[Tensor, Tensor]:
+    """(out [T, H], status int32 [1]) of a layer for at most 8 tokens; router, or topk_idx and topk_probs."""
+    status = torch.zeros(1, dtype=torch.int32, device=x.device)
+    out = _b.moe_layer_few(x.contiguous(), None if router is None else router.contiguous(), top_k, W1.contiguous(), W2.contiguous(),
+                           W1_scale, W2_scale,
+                           None if topk_idx is None else (topk_idx.contiguous(), topk_probs.contiguous()), status=status)
+    return out, status
+
+
+@layer_few.register_fake
+def _(x, router, topk_idx, topk_probs, top_k, W1, W2, W1_scale, W2_scale):
+    return x.new_empty(x.shape), x.new_empty(1, dtype=torch.int32)
+
+
+def _few(T: int, top_k: int, H: int, W1: Tensor, W1_scale: Optional[Tensor]) -> bool:
+    """Whether a layer of these sizes goes through layer_few."""
+    return 0 < T <= 8 and _b.moe_layer_few_fits(T, W1.shape[0], top_k, H, W1.shape[1] // 2, W1_scale)
+
+
+def _grad_wanted(*tensors: Tensor) -> bool:
+    return torch.is_grad_enabled() and any(t.requires_grad for t in tensors)
+
+
+def moe_layer_fp4_block(x: Tensor, topk_idx: Tensor, topk_probs: Tensor, W1_q: Tensor, W1_scale: Tensor, W2_q: Tensor,
+                        W2_scale: Tensor, pad_multiple: int = 1, return_status: bool = False):
+    """The layer from e2m1 codes with a scale per 32 (quantize_fp4_block of W1 and
+    W2), which get no gradients.  At most 8 tokens, where no gradient is wanted,
+    take layer_few, which reads the codes; others take moe_layer on the weights
+    turned back to bf16, which is exact.  Returns out, or with ``return_status``
+    (out, status) as moe_layer does."""
+    T, K = topk_idx.shape
+    if not _grad_wanted(x, topk_probs) and _few(T, K, x.shape[1], W1_q, W1_scale):
+        out, status = _ops.layer_few(x, None, topk_idx, topk_probs, K, W1_q, W2_q, W1_scale, W2_scale)
+        return (out, status) if return_status else out
+    return moe_layer(x, topk_idx, topk_probs, _ops.dequantize_fp4_block(W1_q, W1_scale), _ops.dequantize_fp4_block(W2_q, W2_scale),
+                     pad_multiple, return_status)
+
+
 def moe_block(x: Tensor, normed: Tensor, router: Tensor, top_k: int, W1: Tensor, W2: Tensor, norm_out_weight: Tensor,
               gate: Optional[Tensor] = None, next_weight: Optional[Tensor] = None, residual_scale: float = 1.0,
               pad_multiple: int = 1, eps: float = 1e-6, fp8: Optional[Tuple[Tensor, Tensor]] = None,
-              return_status: bool = False):
+              return_status: bool = False, fp4: Optional[Tuple[Tensor, Tensor]] = None, few: bool = False):
     """A MoE block between two norms: from the residual stream x and its norm
     (``norm_in``, or the block before's ``next``), the router's logits
     ``normed @ router^T``, the layer, and ``norm_out``.  Returns (out, next), next
     being None without ``next_weight``, and with ``return_status`` the layer's
     status as a third.
 
-    Differentiable in everything but the top-k choice.  With ``fp8`` = (W1_scale,
-    W2_scale), W1 and W2 are e4m3 codes with block scales and the layer runs for
-    inference."""
-    logits = (normed.float() @ router.float().t()).contiguous()
-    if fp8 is None:
-        y, status = moe_layer_from_logits(normed, logits, top_k, W1, W2, pad_multiple, return_status=True)
+    Differentiable in everything but the top-k choice.  With ``fp8`` =
+    (W1_scale, W2_scale), W1 and W2 are e4m3 codes with block scales and the layer
+    runs for inference; with ``fp4`` they are e2m1 codes with a scale per 32.  With ``few`` at
+    most 8 tokens, where no gradient is wanted, go through router and layer in
+    the two launches of moe_layer_few (with ``fp4`` they always do): the same
+    sums in another order, and h not rounded between the products."""
+    scales = fp8 if fp8 is not None else fp4
+    if fp8 is not None and fp4 is not None:
+        raise ValueError("give fp8 or fp4, not both")
+    if (few or fp4 is not None) and not _grad_wanted(normed, router, *(() if scales else (W1, W2))) and _few(normed.shape[0], top_k, normed.shape[1], W1, scales and scales[0]):
+        y, status = _ops.layer_few(normed, router, None, None, top_k, W1, W2, *(scales or (None, None)))
     else:
-        idx, p = _ops.router_topk(logits, top_k)
-        y, status = moe_layer_fp8_block(normed, idx, p, W1, fp8[0], W2, fp8[1], pad_multiple, return_status=True)
+        logits = (normed.float() @ router.float().t()).contiguous()
+        if scales is None:
+            y, status = moe_layer_from_logits(normed, logits, top_k, W1, W2, pad_multiple, return_status=True)
+        else:
+            idx, p = _ops.router_topk(logits, top_k)
+            layer = moe_layer_fp8_block if fp8 is not None else moe_layer_fp4_block
+            y, status = layer(normed, idx, p, W1, scales[0], W2, scales[1], pad_multiple, return_status=True)
     out, nxt, _, _ = _ops.norm_out(x, y, norm_out_weight, gate, next_weight, residual_scale, True, eps, 0.0)
     nxt = nxt if next_weight is not None else None
     return (out, nxt, status) if return_status else (out, nxt)

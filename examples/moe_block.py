@@ -1,12 +1,13 @@
-"""Trains a small stack of MoE blocks, then serves it from e4m3 weights.
+"""Trains a small stack of MoE blocks, then serves it from e4m3 and e2m1 weights.
 
     python examples/moe_block.py [--tokens 512] [--steps 20] [--state-bits 8]
 
 A block is norm -> router -> experts -> norm with a gate per token and the
 residual; a block's exit norm and the next one's entry norm are one pass.  The
 optimiser takes all parameters in one launch.  After training, the experts'
-weights become e4m3 codes with a scale per 128 x 128 block, and the same blocks
-run for inference, for the whole batch and for single tokens.
+weights become e4m3 codes with a scale per 128 x 128 block, or e2m1 codes with a
+scale per 32 of a row, and the same blocks run for inference, for the whole batch
+and for single tokens (those of the latter through router and layer in two launches).
 """
 import argparse
 import os
@@ -31,7 +32,7 @@ class Stack:
                      gate=torch.zeros(H, 1, device="cuda"), next=torch.ones(H, device="cuda"))
             self.blocks.append({k: v.requires_grad_(True) for k, v in b.items()})
         self.blocks[-1].pop("next")
-        self.fp8 = None
+        self.fp8 = self.fp4 = None
 
     def parameters(self):
         return [self.entry] + [p for b in self.blocks for p in b.values()]
@@ -41,16 +42,21 @@ class Stack:
         self.fp8 = [(moe.moe_quantize_fp8_block(b["W1"].detach(), 128), moe.moe_quantize_fp8_block(b["W2"].detach(), 128))
                     for b in self.blocks]
 
+    def to_fp4(self):
+        """The same in 4 bits."""
+        self.fp8, self.fp4 = None, [(moe.moe_quantize_fp4_block(b["W1"].detach()), moe.moe_quantize_fp4_block(b["W2"].detach()))
+                                    for b in self.blocks]
+
     def __call__(self, x):
         normed, _ = torch.ops.moe_gb300.norm_in(x, self.entry, 1e-6, 0.0)
         for i, b in enumerate(self.blocks):
-            W1, W2, scales = b["W1"], b["W2"], None
-            if self.fp8 is not None:
-                (W1, s1), (W2, s2) = self.fp8[i]
-                scales = (s1, s2)
+            W1, W2, kept = b["W1"], b["W2"], {}
+            if self.fp8 is not None or self.fp4 is not None:
+                (W1, s1), (W2, s2) = (self.fp8 or self.fp4)[i]
+                kept = {"fp8" if self.fp8 is not None else "fp4": (s1, s2)}
             gate = (normed.float() @ b["gate"]).squeeze(1)
             x, normed = moe.moe_block(x, normed, b["router"], self.K, W1, W2, b["exit"], gate=gate,
-                                      next_weight=b.get("next"), fp8=scales)
+                                      next_weight=b.get("next"), few=self.fp4 is not None, **kept)
         return x
 
 
@@ -90,9 +96,13 @@ def main(argv=None):
         stack.to_fp8()
         fp8 = stack(x)
         one = torch.cat([stack(x[i:i + 1]) for i in range(4)])
+        stack.to_fp4()
+        fp4 = stack(x)
+        one4 = torch.cat([stack(x[i:i + 1]) for i in range(4)])
     rel = lambda p, q: float((p.float() - q.float()).norm() / q.float().norm())  # noqa: E731
     print(f"loss {losses[0]:.4f} -> {losses[-1]:.4f} in {a.steps} steps with {a.state_bits}-bit states; "
-          f"e4m3 experts against bf16: {rel(fp8, bf16):.4f}; one token at a time: {rel(one, fp8[:4]):.4f}")
+          f"e4m3 experts against bf16: {rel(fp8, bf16):.4f}; one token at a time: {rel(one, fp8[:4]):.4f}; "
+          f"e2m1 experts against bf16: {rel(fp4, bf16):.4f}; one token at a time: {rel(one4, fp4[:4]):.4f}")
     return losses, rel(fp8, bf16), rel(one, fp8[:4])
 
 

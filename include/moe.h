@@ -814,6 +814,8 @@ typedef struct moe_few {
  * MOE_ERR_INVALID_ARG for NULL or misaligned pointers, T < 0, an unknown type or format.
  */
 MOE_API moe_status moe_layer_few_workspace_bytes(int32_t T, int32_t E, int32_t K, int32_t I, size_t* bytes);
+/* 1 if moe_layer_few takes these sizes, 0 if it refuses them.  Host only. */
+MOE_API int32_t moe_layer_few_fits(int32_t T, int32_t E, int32_t K, int32_t H, int32_t I, int32_t weights);
 MOE_API moe_status moe_layer_few(const moe_few* f, moe_stream_t stream);
 
 /*
@@ -830,8 +832,8 @@ MOE_API moe_status moe_selftest_wait_timeout(int32_t* status, int64_t limit_ns, 
 /*
  * Self-test of a block-scaled product whose operands stop arriving: until it
  * is called again with -1, the tensor-core launches of the calling host thread
- * (moe_matmul_fp8_block with more than 8 rows, moe_grouped_experts_fp8_block
- * with more than 8 tokens) load operands for the first `tiles` tiles of each
+ * (moe_matmul_fp8_block and moe_matmul_fp4_block with more than 8 rows,
+ * moe_grouped_experts_fp8_block with more than 8 tokens) load operands for the first `tiles` tiles of each
  * CTA only.  Their waits then run out after about 2 s, the status word gets
  * MOE_DEVERR_TIMEOUT, and the outputs that were not reached are NaN.
  */
@@ -840,6 +842,11 @@ MOE_API moe_status moe_selftest_block_product_tiles(int32_t tiles);
 /* The same for the norms: only the first `rows` rows arrive, where rows go
  * through shared memory (H a multiple of 8 above 256, rows for every SM). */
 MOE_API moe_status moe_selftest_norm_rows(int64_t rows);
+
+/* The same for moe_layer_few: until it is called again with -1, only the first
+ * `ctas` CTAs of the calling host thread's launches come to the meeting between
+ * the two products. */
+MOE_API moe_status moe_selftest_few_ctas(int32_t ctas);
 
 #ifdef __cplusplus
 }  /* extern "C" */

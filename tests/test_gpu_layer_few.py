@@ -234,3 +234,143 @@ def test_refusals(moe):
                     (dict(top_k=9), moe.MoEError), (dict(x=x.repeat(5, 1)), moe.MoEError)):
         with pytest.raises(err):
             moe.moe_layer_few(**{**ok, **kw})
+
+
+# ------------------------------------------------------------------ through the operators and the block
+def _meta(T=3, H=256, E=8, K=2, I=128):
+    mk = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt, device="meta")  # noqa: E731
+    u8 = lambda *s: mk(*s, dt=torch.uint8)  # noqa: E731
+    return dict(x=mk(T, H), normed=mk(T, H), router=mk(E, H), W1=mk(E, 2 * I, H), W2=mk(E, H, I), w=mk(H, dt=torch.float32),
+                q1=u8(E, 2 * I, H // 2), s1=u8(E, 2 * I // 128, H // 128, 32, 4, 4), q2=u8(E, H, I // 2),
+                s2=u8(E, H // 128, I // 128, 32, 4, 4))
+
+
+def _used(fn, *a):
+    from torch.fx.experimental.proxy_tensor import make_fx
+    gm = make_fx(fn)(*a)
+    return {str(n.target).split(".")[1] for n in gm.graph.nodes if str(n.target).startswith("moe_gb300.")}
+
+
+def test_block_takes_the_short_way_without_a_gpu(moe):
+    """Which operators a block goes through, by tokens, weights, `few` and wanted gradients."""
+    short, plain = {"layer_few", "norm_out"}, {"router_topk", "route_to_multihot", "dispatch", "grouped_experts", "combine", "norm_out"}
+    for T in (1, 8, 9):
+        t = _meta(T)
+        run = lambda W1, W2, **kw: moe.moe_block(t["x"], t["normed"], t["router"], 2, W1, W2, t["w"], **kw)[0]  # noqa: E731
+        bf = (t["W1"], t["W2"])
+        assert _used(lambda *a: run(*a), *bf) == plain
+        assert _used(lambda *a: run(*a, few=True), *bf) == (short if T <= 8 else plain)
+        assert _used(lambda q1, q2: run(q1, q2, fp4=(t["s1"], t["s2"])), t["q1"], t["q2"]) == (
+            short if T <= 8 else plain | {"dequantize_fp4_block"})
+        grad = t["normed"].clone().requires_grad_()
+        block = lambda n, W1, W2, **kw: moe.moe_block(t["x"], n, t["router"], 2, W1, W2, t["w"], **kw)[0]  # noqa: E731
+        assert block(grad, *bf, few=True).requires_grad
+        out = block(grad, t["q1"], t["q2"], fp4=(t["s1"], t["s2"]))
+        out.float().sum().backward()
+        assert grad.grad.shape == grad.shape
+        with torch.no_grad():
+            assert _used(lambda n: block(n, *bf, few=True), grad.detach()) == (short if T <= 8 else plain)
+    with pytest.raises(ValueError, match="not both"):
+        moe.moe_block(t["x"], t["normed"], t["router"], 2, t["q1"], t["q2"], t["w"], fp8=(1, 2), fp4=(1, 2))
+    assert moe.moe_layer_few_fits(8, 128, 8, 2048, 768) and not moe.moe_layer_few_fits(9, 128, 8, 2048, 768)
+    assert not moe.moe_layer_few_fits(8, 128, 8, 2048, 8192) and moe.moe_layer_few_fits(8, 128, 8, 2048, 7168, _meta()["s1"])
+    ns = torch.ops.moe_gb300
+    c, s = ns.quantize_fp4_block(torch.zeros(3, 200, 160, device="meta"))
+    assert c.shape == (3, 200, 80) and s.shape == (3, 2, 2, 32, 4, 4) and ns.dequantize_fp4_block(c, s).shape == (3, 200, 160)
+    with pytest.raises(NotImplementedError, match="CPU"):
+        ns.quantize_fp4_block(torch.zeros(4, 64))
+
+
+@gpu
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
+def test_block(moe, fmt):
+    """A block for a few tokens against the same block of more tokens, whose first rows they are."""
+    H, E, K, I = 512, 16, 4, 256
+    x, router, W1, S1, W2, S2, V1, V2 = make(moe, fmt, 8, H, E, K, I)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    many, (w, w2) = torch.randn(40, H, generator=g, device=DEV).bfloat16(), torch.rand(2, H, generator=g, device=DEV) + 0.5
+    gate = torch.randn(40, generator=g, device=DEV)
+    kw = {} if fmt == "bf16" else {fmt: (S1, S2)}
+    normed, _ = torch.ops.moe_gb300.norm_in(many, w, 1e-6, 0.0)
+    whole = moe.moe_block(many, normed, router, K, W1, W2, w, gate=gate, next_weight=w2, return_status=True, **kw)
+    for T in (1, 5, 8):
+        few = moe.moe_block(many[:T], normed[:T], router, K, W1, W2, w, gate=gate[:T], next_weight=w2, return_status=True, few=True, **kw)
+        assert int(few[2]) == 0
+        for a, b in zip(few[:2], whole[:2]):
+            rel = float((a.double() - b[:T].double()).norm() / b[:T].double().norm())
+            # the layer's own roundings: e4m3 activations (2^-4, two of them) in moe_layer_fp8_block, bf16 in the others
+            assert rel < (2.0 ** -4 if fmt == "fp8" else 2.0 ** -7), rel
+    if fmt == "fp4":
+        idx, p = torch.ops.moe_gb300.router_topk((normed.float() @ router.float().t()).contiguous(), K)
+        long, st = moe.moe_layer_fp4_block(normed, idx, p, W1, S1, W2, S2, return_status=True)
+        assert torch.equal(long, moe.moe_layer(normed, idx, p, moe.moe_dequantize_fp4_block(W1, S1), moe.moe_dequantize_fp4_block(W2, S2)))
+        short = moe.moe_layer_fp4_block(normed[:8], idx[:8], p[:8], W1, S1, W2, S2)
+        assert torch.equal(short, moe.moe_layer_few(normed[:8], None, K, W1, W2, S1, S2, routing=(idx[:8], p[:8])))
+        assert float((short.double() - long[:8].double()).norm() / long[:8].double().norm()) < 2.0 ** -7
+
+
+@gpu
+def test_opcheck(moe):
+    ns, tests = torch.ops.moe_gb300, ("test_schema", "test_autograd_registration", "test_faketensor", "test_aot_dispatch_dynamic")
+    x, router, W1, S1, W2, S2, *_ = make(moe, "fp4", 3, 256, 8, 2, 128)
+    idx, p = routing_of(x, router, 2)
+    torch.library.opcheck(ns.layer_few.default, (x, router, None, None, 2, W1, W2, S1, S2), test_utils=tests)
+    torch.library.opcheck(ns.layer_few.default, (x, None, idx, p.float(), 2, W1, W2, S1, S2), test_utils=tests)
+    a = torch.randn(9, 160, device=DEV)
+    q, s = ns.quantize_fp4_block(a)
+    torch.library.opcheck(ns.quantize_fp4_block.default, (a,), test_utils=tests)
+    torch.library.opcheck(ns.dequantize_fp4_block.default, (q, s), test_utils=tests)
+    torch.library.opcheck(ns.matmul_fp4_block.default, (q, s, q, s), test_utils=tests)
+
+
+@gpu
+def test_another_device_is_refused(moe, monkeypatch):
+    from combine_topk_multihot_gb300 import moe as core
+    x, router, W1, S1, W2, S2, *_ = make(moe, "fp4", 3, 256, 8, 2, 128)
+    q, s = moe.moe_quantize_fp4_block(x)
+    now = torch.cuda.current_device()
+    monkeypatch.setattr(core, "_current_device", lambda: now + 1)
+    for call in (lambda: moe.moe_quantize_fp4_block(x), lambda: moe.moe_dequantize_fp4_block(q, s),
+                 lambda: moe.moe_matmul_fp4_block(q, s, q, s), lambda: moe.moe_layer_few(x, router, 2, W1, W2, S1, S2)):
+        with pytest.raises(ValueError, match="current device"):
+            call()
+
+
+@gpu
+@pytest.mark.parametrize("ctas", [0, 7])
+def test_a_meeting_that_fails(moe, ctas):
+    """CTAs that do not come to the meeting: about 2 s, then a status and NaN; the next call is whole again."""
+    x, router, W1, S1, W2, S2, *_ = make(moe, "fp8", 3, 256, 8, 2, 128)
+    whole = moe.moe_layer_few(x, router, 2, W1, W2, S1, S2)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    lib = moe._native.lib
+    try:
+        assert lib.moe_selftest_few_ctas(ctas) == 0
+        out = moe.moe_layer_few(x, router, 2, W1, W2, S1, S2, status=status)
+    finally:
+        assert lib.moe_selftest_few_ctas(-1) == 0
+    torch.cuda.synchronize()
+    assert out.isnan().all() and int(status) == moe._native.MOE_DEVERR_TIMEOUT
+    assert torch.equal(moe.moe_layer_few(x, router, 2, W1, W2, S1, S2), whole)
+
+
+# the two kinds of CTA and all widths: no tile arrives, or the first of each CTA's
+@gpu
+@pytest.mark.parametrize("M,N,K,tiles", [(100, 520, 512, 0), (100, 513, 512, 0), (300, 513, 96, 0), (1000, 4096, 384, 0),
+                                         (2049, 4096, 256, 0), (5000, 8192, 384, 1), (4100, 8195, 384, 1)])
+def test_a_product_whose_operands_stop(moe, M, N, K, tiles):
+    g = torch.Generator(device=DEV).manual_seed(M)
+    a, b = (moe.moe_quantize_fp4_block(torch.randn(n, K, generator=g, device=DEV)) for n in (M, N))
+    whole = moe.moe_matmul_fp4_block(*a, *b)
+    lib = moe._native.lib
+    status, out = torch.zeros(1, dtype=torch.int32, device=DEV), torch.zeros(M, N, dtype=torch.bfloat16, device=DEV)
+    try:
+        assert lib.moe_selftest_block_product_tiles(tiles) == 0
+        moe.moe_matmul_fp4_block(*a, *b, out=out, status=status)
+    finally:
+        assert lib.moe_selftest_block_product_tiles(-1) == 0
+    torch.cuda.synchronize()
+    missing = out.isnan()
+    assert missing.all() if tiles == 0 else missing.any() and not missing.all()
+    assert torch.equal(out[~missing], whole[~missing]) and int(status) == moe._native.MOE_DEVERR_TIMEOUT
+    assert torch.equal(moe.moe_matmul_fp4_block(*a, *b), whole)
