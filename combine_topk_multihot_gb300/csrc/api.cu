@@ -1060,8 +1060,12 @@ moe_status moe_matmul_fp4_block(const uint8_t* a_q, const uint8_t* a_scale, int3
   moe_status st = check_device();
   if (st != MOE_OK) return st;
   if (M == 0) return MOE_OK;
-  const cudaError_t err = M <= FP4_STREAM_ROWS ? launch_fp4_matmul_stream(a_q, a_scale, M, b_q, b_scale, N, K, out, stream)
-                                               : launch_fp4_matmul_tc(a_q, a_scale, M, b_q, b_scale, N, K, out, status, stream);
+  // Few rows by few weight rows leave the tensor cores' tiles too few to keep all SMs
+  // loading (8 x N x K, stream against tiles: 1024 x 8192 8.8 us and 11.3, 256 x 512
+  // 2.7 and 2.8; 2048 x 768 3.7 and 3.4, 4096 x 2048 6.6 and 5.1, 16384 x 4096 23 and 12).
+  const bool few = M <= FP4_STREAM_ROWS && N <= 1024;
+  const cudaError_t err = few ? launch_fp4_matmul_stream(a_q, a_scale, M, b_q, b_scale, N, K, out, stream)
+                              : launch_fp4_matmul_tc(a_q, a_scale, M, b_q, b_scale, N, K, out, status, stream);
   return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_matmul_fp4_block launch");
 }
 

@@ -753,7 +753,8 @@ MOE_API moe_status moe_dequantize_fp4_block(const uint8_t* codes, const uint8_t*
  * M >= 0, N >= 1, K a positive multiple of 32.  Codes and scales are 16-byte
  * aligned, and so is out when N is a multiple of 8.  Scales past the last row or
  * block of a matrix must not be 255 (the quantiser writes zeros there).  Up to 8
- * rows stream the weights through registers; more run on the tensor cores.
+ * rows by up to 1024 stream the weights through registers; others run on the
+ * tensor cores.
  */
 MOE_API moe_status moe_matmul_fp4_block(const uint8_t* a_q, const uint8_t* a_scale, int32_t M, const uint8_t* b_q,
                                         const uint8_t* b_scale, int32_t N, int32_t K, moe_bf16* out, int32_t* status,

@@ -157,10 +157,10 @@ def _bound_check(out, a, b):
     assert (err <= lim).all(), float((err - lim).max())
 
 
-# few rows (1 to 8: the weight stream), more on the tensor cores: every tile
-# width, ragged edges in every dimension, one block of K, K not a multiple of 64,
-# 128 or 256
-MATMUL = [(1, 16, 32), (1, 4096, 2048), (7, 100, 160), (8, 4097, 2080), (2, 1, 64), (5, 33, 8192), (9, 64, 32), (9, 1, 64),
+# few rows by few (up to 8 by 1024: the weight stream), others on the tensor cores:
+# every tile width, ragged edges in every dimension, one block of K, K not a
+# multiple of 64, 128 or 256
+MATMUL = [(8, 1024, 2080), (3, 1023, 96), (8, 1025, 544), (1, 20000, 256), (4000, 192 * 43, 512), (1, 16, 32), (1, 4096, 2048), (7, 100, 160), (8, 4097, 2080), (2, 1, 64), (5, 33, 8192), (9, 64, 32), (9, 1, 64),
           (16, 513, 512), (17, 77, 2080), (64, 1000, 2048), (100, 8, 160), (128, 256, 512), (129, 2048, 1056),
           (300, 4100, 2048), (1000, 384, 4096), (1111, 8192, 256), (2049, 1027, 544), (5000, 4096, 384), (777, 2050, 96)]
 
