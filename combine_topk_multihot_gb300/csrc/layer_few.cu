@@ -30,9 +30,8 @@
 //
 // Weights are bf16, e4m3 with a scale per 128 x 128, or e2m1 with a scale per 32
 // of a row.  Codes are multiplied as f16 numbers, which they are exactly, by
-// tokens (and h) in f16 with a power of two for each 128 values: exact for
-// bf16 values down to 2^-31 of their block's largest, and within 2^-39 of that below
-// it.  With bf16 weights h, which is held in fp32, is multiplied as the sum of two
+// tokens (and h) in f16 with a power of two for each row: exact for bf16 values
+// down to 2^-31 of their row's largest, and within 2^-39 of that below it.  With bf16 weights h, which is held in fp32, is multiplied as the sum of two
 // bf16 numbers: rounded to one it would add as much error as the output's rounding.  (mma.sync on e4m3 operands takes 28 cycles an SM quarter here, on f16 12 for
 // half of K, and converting a pair of codes 2.3.)
 
@@ -56,7 +55,13 @@ constexpr int THREADS = 32 * WARPS;
 constexpr int TEAM = 4;                // warps that share a tile of the first product
 constexpr int MAX_SLOTS = 6;           // of a warp
 constexpr int PIECE = 128;             // bytes of a weight row in a slot
-constexpr int SLOT = 16 * PIECE + 128; // and a word or two of scales of each row
+// Bytes from row to row in a slot, whose rows' banks are kept apart: 16 more for
+// e2m1 (a warp reads 16 bytes of each of eight rows), else by turning the parts
+// (a quarter warp reads 64 bytes of each of two rows).
+template <int FMT>
+__host__ __device__ constexpr int slot_pitch() { return FMT == FEW_FP4 ? PIECE + 16 : PIECE; }
+template <int FMT>
+__host__ __device__ constexpr int slot_bytes() { return 16 * slot_pitch<FMT>() + 128; }  // and a word or two of scales of each row
 constexpr int SMEM_LIMIT = 232448;
 
 template <int FMT>
@@ -141,8 +146,11 @@ __global__ void __launch_bounds__(LOGIT_THREADS) few_logits_kernel(const uint16_
                                                                    unsigned* __restrict__ barrier) {
   __shared__ float s_sum[LOGIT_THREADS / 32][TOK];
   griddep_launch_dependents();
-  griddep_wait();
   const int e = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (logits)  // (only a hint, so it may come before the wait for earlier kernels)
+    for (int k = threadIdx.x * 128; k < H * (F32 ? 4 : 2); k += LOGIT_THREADS * 128)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint8_t*>(router) + static_cast<long long>(e) * H * (F32 ? 4 : 2) + k));
+  griddep_wait();
   if (e == 0 && threadIdx.x == 0) *barrier = 0u;
   if (logits == nullptr) return;
   float acc[TOK] = {};
@@ -169,12 +177,12 @@ __global__ void __launch_bounds__(LOGIT_THREADS) few_logits_kernel(const uint16_
     }
   }
 #pragma unroll
-  for (int t = 0; t < TOK; ++t)
+  for (int t = 0; t < TOK; ++t) {
+    if (t >= T) break;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(FULL_MASK, acc[t], o);
-  if (lane == 0)
-#pragma unroll
-    for (int t = 0; t < TOK; ++t) s_sum[warp][t] = acc[t];
+    if (lane == 0) s_sum[warp][t] = acc[t];
+  }
   __syncthreads();
   if (threadIdx.x < T) {
     float v = 0.f;
@@ -226,13 +234,16 @@ __device__ __forceinline__ void pick_experts(const float* logits, int E, int K, 
 }
 
 // ---------------------------------------------------------------- rows of tokens
-// Eight f16 numbers of a block of 128 that 16 threads hold, in units of its scale:
-// 2^(floor(log2 amax) - 14), at least 2^-126, so that values are below 2^15.
-__device__ __forceinline__ uint4 scaled_f16(const float (&v)[8], float top, float& scale) {
-  const uint32_t bits = __float_as_uint(top);
+// The power of two by which a row is divided to become f16: 2^(floor(log2 amax) -
+// 14), at least 2^-126, so that values are below 2^15; NaN for a row with a NaN or
+// an infinity.  `inv`: its reciprocal.
+__device__ __forceinline__ float row_scale_f16(float amax, float& inv) {
+  const uint32_t bits = __float_as_uint(amax);
   const uint32_t e = bits >> 23 > 15u ? (bits >> 23) - 14u : 1u;
-  const float inv = __uint_as_float((254u - e) << 23);
-  scale = bits >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : __uint_as_float(e << 23);
+  inv = __uint_as_float((254u - e) << 23);
+  return bits >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : __uint_as_float(e << 23);
+}
+__device__ __forceinline__ uint4 f16x8(const float (&v)[8], float inv) {
   uint32_t w[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -249,81 +260,76 @@ __device__ __forceinline__ int place_of(int v) {
   return FMT == FEW_FP8 ? (v & ~7) | (v & 1) << 2 | (v & 7) >> 1 : v;
 }
 
-// `rows` rows of K bf16 values (row r from src + r K) into shared memory, as the
-// products read them: as they are, or as f16 with a scale for each 128 of a
-// row.  By `threads` threads, of which this is number `tid`; each asks for four
-// pieces of 16 bytes before it uses the first.
-template <int FMT>
-__device__ __forceinline__ void stage_tokens(const uint16_t* src, int rows, int K, uint8_t* dst, float* scales, int tid, int threads) {
-  const int pitch = token_pitch(K), per_row = K >> 3, all = rows * per_row;
-  for (int i0 = tid; i0 < all; i0 += 4 * threads) {
-    uint4 q[4];
+// Eight values of a row of bf16, or of fp32.
+__device__ __forceinline__ void load8(const uint16_t* row, int v, float (&f)[8]) {
+  const uint4 q = __ldcg(reinterpret_cast<const uint4*>(row) + v);
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int i = i0 + j * threads;
-      q[j] = i < all ? __ldcg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int i = i0 + j * threads;
-      if (i >= all) break;  // (all of a block's 16 threads or none: K is a multiple of 128)
-      if constexpr (FMT != FEW_BF16) {
-        const unsigned half = 0xffffu << (tid & 16);
-        uint32_t top = bf16x2_abs_max(bf16x2_abs_max(q[j].x, q[j].y), bf16x2_abs_max(q[j].z, q[j].w));
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) top = bf16x2_abs_max(top, __shfl_xor_sync(half, top, o));
-        const uint32_t w[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
-        float v[8], scale;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[2 * k] = bf16_lo(w[k]), v[2 * k + 1] = bf16_hi(w[k]);
-        q[j] = scaled_f16(v, max_nan(bf16_lo(top), bf16_hi(top)), scale);
-        if ((tid & 15) == 0) scales[i >> 4] = scale;
-      }
-      const int r = i / per_row, v = i - r * per_row;
-      *reinterpret_cast<uint4*>(dst + r * pitch + place_of<FMT>(v) * 16) = q[j];
-    }
-  }
+  for (int k = 0; k < 4; ++k) f[2 * k] = bf16_lo(w[k]), f[2 * k + 1] = bf16_hi(w[k]);
+}
+__device__ __forceinline__ void load8(const float* row, int v, float (&f)[8]) {
+  const float4 a = __ldcg(reinterpret_cast<const float4*>(row) + 2 * v), b = __ldcg(reinterpret_cast<const float4*>(row) + 2 * v + 1);
+  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
 }
 
-// The same for rows of h in fp32: f16 with scales, or the nearest bf16 and, 2 K
-// bytes on, what that leaves.
-template <int FMT>
-__device__ __forceinline__ void stage_h(const float* src, int rows, int K, uint8_t* dst, float* scales) {
-  const int pitch = h_pitch<FMT>(K), per_row = K >> 3, all = rows * per_row;
-  for (int i0 = threadIdx.x; i0 < all; i0 += 2 * THREADS) {
-    float4 q[2][2];
+// `rows` rows of K values (row r from src + r K; tokens in bf16 or h in fp32) into
+// shared memory as the products read them, `warps` warps of which this is number
+// `warp`, a row each.  For codes: f16 with a scale for each row.  For bf16 weights:
+// tokens as they are; h as the nearest bf16 and, 2 K bytes on, what that leaves.
+template <int FMT, typename Value>
+__device__ __forceinline__ void stage_rows(const Value* src, int rows, int K, int pitch, uint8_t* dst, float* scales, int warp, int warps) {
+  constexpr int V = 4;  // of a lane at a time
+  const int per_row = K >> 3, lane = threadIdx.x & 31;
+  for (int r = warp; r < rows; r += warps) {
+    const Value* row = src + static_cast<long long>(r) * K;
+    uint8_t* to = dst + r * pitch;
+    float f[V][8], inv = 1.f;
+    auto load = [&](int v0) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int i = i0 + j * THREADS;
+      for (int j = 0; j < V; ++j) {
+        if (v0 + 32 * j < per_row) {
+          load8(row, v0 + 32 * j, f[j]);
+        } else {
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        q[j][k] = i < all ? __ldcg(reinterpret_cast<const float4*>(src) + 2 * i + k) : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int i = i0 + j * THREADS;
-      if (i >= all) break;
-      const float v[8] = {q[j][0].x, q[j][0].y, q[j][0].z, q[j][0].w, q[j][1].x, q[j][1].y, q[j][1].z, q[j][1].w};
-      const int r = i / per_row, c = i - r * per_row;
-      uint8_t* at = dst + r * pitch + place_of<FMT>(c) * 16;
-      if constexpr (FMT == FEW_BF16) {
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          hi[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
-          lo[k] = pack_bf16x2(v[2 * k] - bf16_lo(hi[k]), v[2 * k + 1] - bf16_hi(hi[k]));
+          for (int k = 0; k < 8; ++k) f[j][k] = 0.f;
         }
-        *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(at + 2 * K) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-      } else {
-        const unsigned half = 0xffffu << (threadIdx.x & 16);
-        float top = 0.f, scale;
+      }
+    };
+    if constexpr (FMT != FEW_BF16) {
+      float top = 0.f;
+      for (int v0 = lane; v0 < per_row; v0 += 32 * V) {
+        load(v0);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) top = max_nan(top, fabsf(v[k]));
+        for (int j = 0; j < V; ++j)
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(half, top, o));
-        *reinterpret_cast<uint4*>(at) = scaled_f16(v, top, scale);
-        if ((threadIdx.x & 15) == 0) scales[i >> 4] = scale;
+          for (int k = 0; k < 8; ++k) top = max_nan(top, fabsf(f[j][k]));
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(FULL_MASK, top, o));
+      const float scale = row_scale_f16(top, inv);
+      if (lane == 0) scales[r] = scale;
+    }
+    for (int v0 = lane; v0 < per_row; v0 += 32 * V) {
+      if (FMT == FEW_BF16 || per_row > 32 * V) load(v0);  // (else they are still here)
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int v = v0 + 32 * j;
+        if (v >= per_row) break;
+        uint8_t* at = to + place_of<FMT>(v) * 16;
+        if constexpr (FMT == FEW_BF16) {
+          uint32_t hi[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) hi[k] = pack_bf16x2(f[j][2 * k], f[j][2 * k + 1]);
+          *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          if constexpr (sizeof(Value) == 4) {
+            uint32_t lo[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) lo[k] = pack_bf16x2(f[j][2 * k] - bf16_lo(hi[k]), f[j][2 * k + 1] - bf16_hi(hi[k]));
+            *reinterpret_cast<uint4*>(at + 2 * K) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
+        } else {
+          *reinterpret_cast<uint4*>(at) = f16x8(f[j], inv);
+        }
       }
     }
   }
@@ -344,7 +350,7 @@ struct Cursor {
   int st, steps;             // piece, pieces of a row
   bool first;
   int n_lo, n_hi, rb;        // rows of the tile's halves, bytes of a row
-  const uint32_t part;       // where this lane's 16 bytes of rows lane / 8 go in a slot; four rows on: ^ 32
+  const uint32_t part;       // where this lane's 16 bytes of rows lane / 8 go in a slot
   // this lane's 16 bytes of the piece: in row lane / 8 of the expert's rows, of the tile's halves
   const uint8_t *base, *lo, *hi;
   long long stride;          // bytes of an expert
@@ -357,7 +363,8 @@ struct Cursor {
       : s(s_), active(active_), warp(warp_), lane(lane_), I(args_.I), bytes1(row_bytes<FMT>(args_.H)), bytes2(row_bytes<FMT>(args_.I)),
         steps1((bytes1 + PIECE - 1) / PIECE), steps2((bytes2 + PIECE - 1) / PIECE), a(a_), j0(j0_), left(cols), m0(r0), left2(rows),
         st(warp_ % TEAM), steps(steps1), first(true), rb(bytes1),
-        part((lane_ >> 3) * PIECE + (((lane_ & 7) ^ (((lane_ >> 3) & 1) * 4 + (lane_ >> 4))) << 4)), args(args_) {
+        part((lane_ >> 3) * slot_pitch<FMT>() + (((lane_ & 7) ^ (FMT == FEW_FP4 ? 0 : ((lane_ >> 3) & 1) * 4 + (lane_ >> 4))) << 4)),
+        args(args_) {
     for (int i = 0; i < warp / TEAM; ++i) skip_tile();
     if (st >= steps1) left = 0;  // no piece for this warp
     base = args.W1 + static_cast<long long>(lane >> 3) * bytes1 + (lane & 7) * 16;
@@ -426,25 +433,25 @@ struct Cursor {
     hi = lo + 8ll * bytes2;
     if constexpr (FMT != FEW_BF16) scale = scale_base + e * scale_stride;
   }
-  // Asks for the piece and goes on to the next.  Row r's 16-byte part c goes to
-  // part c ^ (r % 2 * 4 + r / 2 % 4): a quarter warp's four parts of each of two
-  // rows, and a warp's one part of each of eight rows, meet different banks.
+  // Asks for the piece and goes on to the next.  Unless rows are 16 bytes apart
+  // more (e2m1), row r's 16-byte part c goes to part c ^ (r % 2 * 4 + r / 2 % 4).
   __device__ __forceinline__ void issue(uint32_t slot) {
+    constexpr int PITCH = slot_pitch<FMT>();
     if (more()) {
       const int row = lane >> 3, at = st * PIECE;
       if (at + (lane & 7) * 16 < rb) {
-        const uint32_t dst = slot + part, dst4 = slot + ((part + 4 * PIECE) ^ 32);
+        const uint32_t dst = slot + part, dst4 = slot + ((part + 4 * PITCH) ^ (FMT == FEW_FP4 ? 0 : 32));
         const uint8_t *p = lo + at, *q = hi + at;
         if (row < n_lo) cp_async_16(dst, p);
         if (row + 4 < n_lo) cp_async_16(dst4, p + 4 * rb);
-        if (row < n_hi) cp_async_16(dst + 8 * PIECE, q);
-        if (row + 4 < n_hi) cp_async_16(dst4 + 8 * PIECE, q + 4 * rb);
+        if (row < n_hi) cp_async_16(dst + 8 * PITCH, q);
+        if (row + 4 < n_hi) cp_async_16(dst4 + 8 * PITCH, q + 4 * rb);
       }
       if constexpr (FMT == FEW_FP8) {
-        if (lane < 16) cp_async_4(slot + 16 * PIECE + lane * 4, scale + st * 4);
+        if (lane < 16) cp_async_4(slot + 16 * PITCH + lane * 4, scale + st * 4);
       } else if constexpr (FMT == FEW_FP4) {
         const int kb = 2 * st + (lane >> 4);
-        if (kb * 64 < rb) cp_async_4(slot + 16 * PIECE + lane * 4, scale + kb * SCALE_TILE);
+        if (kb * 64 < rb) cp_async_4(slot + 16 * PITCH + lane * 4, scale + kb * SCALE_TILE);
       }
       st += first ? TEAM : WARPS;
       if (st >= steps) {
@@ -463,35 +470,35 @@ struct Cursor {
 
 // ---------------------------------------------------------------- products
 // d[16 rows x 8 tokens] += a slot's rows times the tokens' rows.  `token`: the row
-// of token lane / 4 (0: none, zeros), s0 and s1 the scales of tokens 2 (lane %
-// 4) and the next, `st` the piece, `bytes` those of a weight row.  With SUM (bf16)
-// a token's row is followed by what it was rounded from.
+// of token lane / 4 (any row where there is none: its column is no one's), `st` the
+// piece, `bytes` those of a weight row.  With SUM (bf16) a token's row is followed by
+// what it was rounded from.
 template <int FMT, bool SUM>
-__device__ __forceinline__ void multiply(float (&d)[4], uint32_t slot, int st, int bytes, int lane, uint32_t token, const float* s0,
-                                         const float* s1) {
+__device__ __forceinline__ void multiply(float (&d)[4], uint32_t slot, int st, int bytes, int lane, uint32_t token) {
+  constexpr int PITCH = slot_pitch<FMT>();
   const int g = lane >> 2, t = lane & 3;
-  // rows are 128 bytes at multiples of 128: part c of the row is at lo ^ (c << 4)
-  const uint32_t lo = slot + g * PIECE + (((g & 1) * 4 + (g >> 1)) << 4), hi = lo + 8 * PIECE;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
+  // part c of the row: at lo ^ (c << 4) (rows are 128 bytes at multiples of 128), or at lo + 16 c
+  const uint32_t turn = FMT == FEW_FP4 ? 4 * t : (((g & 1) * 4 + (g >> 1)) ^ t) << 4;
+  const uint32_t lo = slot + g * PITCH + turn, hi = lo + 8 * PITCH;
+  const uint32_t sc = slot + 16 * PITCH + g * 4;
+  token += 16 * t;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {  // halves of 64 bytes
     if (st * PIECE + h * 64 >= bytes) break;
     if constexpr (FMT == FEW_BF16) {
-      const uint32_t part = (h * 4 + t) << 4;
-      const uint4 a = lds128(lo ^ part), c = lds128(hi ^ part);
-      const uint4 b = token ? lds128(token + st * PIECE + h * 64 + 16 * t) : zero;
+      const uint4 a = lds128(lo ^ (h * 64)), c = lds128(hi ^ (h * 64));
+      const uint4 b = lds128(token + st * PIECE + h * 64);
       mma_bf16_16x8x16(d, a.x, c.x, a.y, c.y, b.x, b.y);
       mma_bf16_16x8x16(d, a.z, c.z, a.w, c.w, b.z, b.w);
       if constexpr (SUM) {
-        const uint4 r = token ? lds128(token + bytes + st * PIECE + h * 64 + 16 * t) : zero;
+        const uint4 r = lds128(token + bytes + st * PIECE + h * 64);
         mma_bf16_16x8x16(d, a.x, c.x, a.y, c.y, r.x, r.y);
         mma_bf16_16x8x16(d, a.z, c.z, a.w, c.w, r.z, r.w);
       }
     } else if constexpr (FMT == FEW_FP8) {
-      const uint32_t part = (h * 4 + t) << 4;
-      const uint4 a = lds128(lo ^ part), c = lds128(hi ^ part);
-      const uint32_t from = token + (2 * st + h) * 128 + 16 * t;
-      const uint4 b0 = token ? lds128(from) : zero, b1 = token ? lds128(from + 64) : zero;
+      const uint4 a = lds128(lo ^ (h * 64)), c = lds128(hi ^ (h * 64));
+      const uint32_t from = token + (2 * st + h) * 128;
+      const uint4 b0 = lds128(from), b1 = lds128(from + 64);
       float p[4] = {0.f, 0.f, 0.f, 0.f}, q[4] = {0.f, 0.f, 0.f, 0.f};
       const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wc[4] = {c.x, c.y, c.z, c.w};
       const uint32_t wb[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
@@ -502,24 +509,19 @@ __device__ __forceinline__ void multiply(float (&d)[4], uint32_t slot, int st, i
         f16_of_e4m3x4(wc[i], hc);
         mma_f16_16x8x16(i & 1 ? q : p, ha[0], hc[0], ha[1], hc[1], wb[2 * i], wb[2 * i + 1]);
       }
-      const float w0 = __uint_as_float(lds32(slot + 16 * PIECE + g * 4)), w1 = __uint_as_float(lds32(slot + 16 * PIECE + g * 4 + 32));
-      const float x0 = s0[st], x1 = s1[st];
-      d[0] = fmaf(p[0] + q[0], w0 * x0, d[0]);
-      d[1] = fmaf(p[1] + q[1], w0 * x1, d[1]);
-      d[2] = fmaf(p[2] + q[2], w1 * x0, d[2]);
-      d[3] = fmaf(p[3] + q[3], w1 * x1, d[3]);
+      const float w0 = __uint_as_float(lds32(sc)), w1 = __uint_as_float(lds32(sc + 32));
+      d[0] = fmaf(p[0] + q[0], w0, d[0]);
+      d[1] = fmaf(p[1] + q[1], w0, d[1]);
+      d[2] = fmaf(p[2] + q[2], w1, d[2]);
+      d[3] = fmaf(p[3] + q[3], w1, d[3]);
     } else {
-      const int kb = 2 * st + h;
-      const uint32_t e0 = lds32(slot + 16 * PIECE + h * 64 + g * 4), e1 = lds32(slot + 16 * PIECE + h * 64 + g * 4 + 32);
       uint32_t f0[2], f1[2];
-      bf16_of_e8m0x4(e0, f0);
-      bf16_of_e8m0x4(e1, f1);
-      float q[4] = {0.f, 0.f, 0.f, 0.f};
+      bf16_of_e8m0x4(lds32(sc + h * 64), f0);
+      bf16_of_e8m0x4(lds32(sc + h * 64 + 32), f1);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t part = (h * 4 + j) << 4;
-        const uint32_t a = lds32((lo ^ part) + 4 * t), c = lds32((hi ^ part) + 4 * t);
-        const uint4 b = token ? lds128(token + kb * 256 + j * 64 + 16 * t) : zero;
+        const uint32_t a = lds32(lo + (h * 4 + j) * 16), c = lds32(hi + (h * 4 + j) * 16);
+        const uint4 b = lds128(token + st * 512 + (h * 4 + j) * 64);
         float p[4] = {0.f, 0.f, 0.f, 0.f};
         uint32_t ha[4], hc[4];
         f16_of_e2m1x8(a, ha);
@@ -527,16 +529,11 @@ __device__ __forceinline__ void multiply(float (&d)[4], uint32_t slot, int st, i
         mma_f16_16x8x16(p, ha[0], hc[0], ha[1], hc[1], b.x, b.y);
         mma_f16_16x8x16(p, ha[2], hc[2], ha[3], hc[3], b.z, b.w);
         const float w0 = j & 1 ? bf16_hi(f0[j >> 1]) : bf16_lo(f0[j >> 1]), w1 = j & 1 ? bf16_hi(f1[j >> 1]) : bf16_lo(f1[j >> 1]);
-        q[0] = fmaf(p[0], w0, q[0]);
-        q[1] = fmaf(p[1], w0, q[1]);
-        q[2] = fmaf(p[2], w1, q[2]);
-        q[3] = fmaf(p[3], w1, q[3]);
+        d[0] = fmaf(p[0], w0, d[0]);
+        d[1] = fmaf(p[1], w0, d[1]);
+        d[2] = fmaf(p[2], w1, d[2]);
+        d[3] = fmaf(p[3], w1, d[3]);
       }
-      const float x0 = s0[kb], x1 = s1[kb];
-      d[0] = fmaf(q[0], x0, d[0]);
-      d[1] = fmaf(q[1], x1, d[1]);
-      d[2] = fmaf(q[2], x0, d[2]);
-      d[3] = fmaf(q[3], x1, d[3]);
     }
   }
 }
@@ -545,6 +542,7 @@ __device__ __forceinline__ void multiply(float (&d)[4], uint32_t slot, int st, i
 template <int FMT>
 __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs args) {
   extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int SLOT = slot_bytes<FMT>();
   uint8_t* region = smem + args.slots * WARPS * SLOT;
   Smem& s = *reinterpret_cast<Smem*>(region + args.region);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -562,7 +560,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
   int chosen = -1;
   float prob = 0.f;
   if (warp >= TOK) {
-    stage_tokens<FMT>(args.x, T, H, region, s_scale, threadIdx.x - 32 * TOK, THREADS - 32 * TOK);
+    stage_rows<FMT>(args.x, T, H, token_pitch(H), region, s_scale, warp - TOK, WARPS - TOK);
   } else if (warp < T) {
     if (args.logits) {
       const float* l = args.logits + warp * E;
@@ -639,10 +637,10 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
   for (int i = 0; i < args.slots; ++i) cursor.issue(slots + i * SLOT);
   __syncthreads();
   int slot = 0;
-  auto next = [&](auto sum, float (&d)[4], int st, int bytes, uint32_t token, const float* s0, const float* s1) {
+  auto next = [&](auto sum, float (&d)[4], int st, int bytes, uint32_t token) {
     cp_async_wait(args.slots - 1);
     __syncwarp();
-    multiply<FMT, decltype(sum)::value>(d, slots + slot * SLOT, st, bytes, lane, token, s0, s1);
+    multiply<FMT, decltype(sum)::value>(d, slots + slot * SLOT, st, bytes, lane, token);
     __syncwarp();
     cursor.issue(slots + slot * SLOT);
     if (++slot == args.slots) slot = 0;
@@ -652,9 +650,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
   const int g = lane >> 2, t = lane & 3;
   const uint32_t rows_u32 = smem_u32(region);
   {
-    const uint32_t token = g < T ? rows_u32 + g * token_pitch(H) : 0u;
-    const float* s0 = s_scale + min(2 * t, T - 1) * (H >> 7);
-    const float* s1 = s_scale + min(2 * t + 1, T - 1) * (H >> 7);
+    const uint32_t token = rows_u32 + min(g, T - 1) * token_pitch(H);
     const int team = warp / TEAM, tid = threadIdx.x % (32 * TEAM);
     int par = 0, a = first_a, j = first_j, turn = 0;
     for (int left = my_cols, n; left > 0; left -= n) {
@@ -666,7 +662,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
       if (++turn == WARPS / TEAM) turn = 0;
       if (!mine) continue;
       float d[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int st = warp % TEAM; st * PIECE < bytes1; st += TEAM) next(std::false_type{}, d, st, bytes1, token, s0, s1);
+      for (int st = warp % TEAM; st * PIECE < bytes1; st += TEAM) next(std::false_type{}, d, st, bytes1, token);
 #pragma unroll
       for (int i = 0; i < 4; ++i) s.part[par][warp][i][lane] = d[i];
       // one meeting a tile: this parity's sums are written again after the next
@@ -682,6 +678,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
             gate += s.part[par][team * TEAM + w][tok & 1][i * 4 + (tok >> 1)];
             up += s.part[par][team * TEAM + w][2 + (tok & 1)][i * 4 + (tok >> 1)];
           }
+          if constexpr (FMT != FEW_BF16) gate *= s_scale[tok], up *= s_scale[tok];
           args.h[static_cast<long long>(row) * I + j0 + i] = gate / (1.0f + expf(-gate)) * up;
         }
       }
@@ -725,25 +722,25 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
       while (sb < active && s.first[sb + 1] - s.first[sa] <= args.cap) ++sb;
       if (!whole || m0 == r0) {
         __syncthreads();
-        stage_h<FMT>(args.h + static_cast<long long>(s.first[sa]) * I, s.first[sb] - s.first[sa], I, region, h_scale);
+        stage_rows<FMT>(args.h + static_cast<long long>(s.first[sa]) * I, s.first[sb] - s.first[sa], I, hp, region, h_scale, warp, WARPS);
         __syncthreads();
       }
       while (true) {
         while (a < sb && st >= steps2) st -= steps2, ++a;
         if (a >= sb) break;
         const int base = s.first[sa], mine = s.row[a][g], row0 = s.row[a][2 * t], row1 = s.row[a][2 * t + 1];
-        const uint32_t token = mine >= 0 ? rows_u32 + (mine - base) * hp : 0u;
-        const float* s0 = h_scale + (max(row0, base) - base) * (I >> 7);
-        const float* s1 = h_scale + (max(row1, base) - base) * (I >> 7);
+        const uint32_t token = rows_u32 + max(mine - base, 0) * hp;
         float d[4] = {0.f, 0.f, 0.f, 0.f};
-        next(std::bool_constant<FMT == FEW_BF16>{}, d, st, bytes2, token, s0, s1);
+        next(std::bool_constant<FMT == FEW_BF16>{}, d, st, bytes2, token);
         if (row0 >= 0) {
-          const float w = s.weight[a][2 * t];
+          float w = s.weight[a][2 * t];
+          if constexpr (FMT != FEW_BF16) w *= h_scale[row0 - base];
           acc[0] = fmaf(w, d[0], acc[0]);
           acc[2] = fmaf(w, d[2], acc[2]);
         }
         if (row1 >= 0) {
-          const float w = s.weight[a][2 * t + 1];
+          float w = s.weight[a][2 * t + 1];
+          if constexpr (FMT != FEW_BF16) w *= h_scale[row1 - base];
           acc[1] = fmaf(w, d[1], acc[1]);
           acc[3] = fmaf(w, d[3], acc[3]);
         }
@@ -773,7 +770,8 @@ thread_local int tls_ctas = 0x7fffffff;
 
 template <int FMT>
 bool plan(FewArgs& g, size_t* smem) {
-  const long long x_row = token_pitch(g.H) + 4 * (g.H / 128), h_row = h_pitch<FMT>(g.I) + 4 * (g.I / 128);
+  constexpr int SLOT = slot_bytes<FMT>();
+  const long long x_row = token_pitch(g.H) + 4, h_row = h_pitch<FMT>(g.I) + 4;
   // all rows of h where they leave three slots a warp, else as many as there are tokens
   const long long need = g.T * (x_row > h_row ? x_row : h_row), most = SMEM_LIMIT - FIXED - 128 - 3 * WARPS * SLOT;
   long long room = g.T * g.K * h_row;

@@ -777,8 +777,8 @@ MOE_API moe_status moe_matmul_fp4_block(const uint8_t* a_q, const uint8_t* a_sca
  *   MOE_WEIGHTS_FP4_BLOCK: e2m1 codes with scales in tiles
  *   (moe_quantize_fp4_block: W1_scale [E, 2I/128, H/128, 32, 4, 4], ...).
  * x and h are not rounded to 8 bits for the codes: they are multiplied as f16
- * numbers with a power of two for each 128 of a row, exact for a bf16 value of
- * 2^-31 of the largest of the 128 or more, and within 2^-39 of that largest below it.
+ * numbers with a power of two for each row, exact for a bf16 value of 2^-31 of
+ * the row's largest or more, and within 2^-39 of that largest below it.
  * By bf16 weights h is multiplied as the sum of two bf16 numbers.  A token with
  * a NaN or an infinity has a NaN or infinity in its own row alone.
  */

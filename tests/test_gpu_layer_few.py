@@ -5,8 +5,8 @@ gaps between them).  The output is held element by element to a bound that adds
 up what the steps may be off:
   * an fp32 sum of products on the tensor cores keeps at least 13 bits of its
     largest term while aligning: 2^-13 S, S the sum of the terms' magnitudes;
-  * with coded weights a value is represented within 2^-39 of its 128
-    neighbours' largest: r(v) = 2^-39 max|v|, none for bf16 weights;
+  * with coded weights a value is represented within 2^-39 of its row's largest:
+    r(v) = 2^-39 max|v|, none for bf16 weights;
   * |silu'| <= 1.1 and |silu(g)| <= |g|: h is off by 1.1 |u| dg + |g| du, and by 2^-11
     |h| for its rounding to f16 (half a step, at the most; as two bf16 numbers by
     less) with 2^-18 |h| for the exponential and the quotient;
@@ -58,7 +58,7 @@ def reference(x, idx, p, W1, W2, coded):
     """(fp64 output, its bound)."""
     T, H = x.shape
     I = W2.shape[2]
-    rep = (lambda v: 2.0 ** -39 * v.view(-1, 128).abs().amax(1).repeat_interleave(128)) if coded else torch.zeros_like
+    rep = (lambda v: 2.0 ** -39 * v.abs().amax().expand(v.shape)) if coded else torch.zeros_like
     out, lim = torch.zeros(T, H, dtype=torch.float64, device=x.device), torch.zeros(T, H, dtype=torch.float64, device=x.device)
     for t in range(T):
         v = x[t].double()
