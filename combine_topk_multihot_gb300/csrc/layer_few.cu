@@ -201,36 +201,40 @@ __device__ __forceinline__ uint32_t sort_key(float v) {
 __device__ __forceinline__ float of_key(uint32_t k) { return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu)); }
 
 // One token's K largest logits by one warp, in descending order, equal ones by
-// ascending index, as moe_router_topk has them, and their softmax.  A lane keeps
-// its logits (32 at the most) in registers, J of them, and the best of those.
+// ascending index, as moe_router_topk has them: lane k's slot k.  Lane l keeps logits
+// J l .. J l + J - 1 in registers, and the first of the best of those: of lanes with
+// the same best the first has the lowest index.
 template <int J>
-__device__ __forceinline__ void pick_experts(const float* logits, int E, int K, int lane, int& chosen, float& prob) {
+__device__ __forceinline__ void pick_experts(const float* logits, int E, int K, int lane, int& chosen, float& logit) {
   uint32_t key[J];
 #pragma unroll
-  for (int j = 0; j < J; ++j) key[j] = lane + 32 * j < E ? sort_key(__ldcg(logits + lane + 32 * j)) : 0u;
+  for (int j = 0; j < J; ++j) key[j] = lane * J + j < E ? sort_key(__ldcg(logits + lane * J + j)) : 0u;
   int mine = 0;
-  float l = -INFINITY;
+  uint32_t won = 0;
   for (int k = 0; k < K; ++k) {
     uint32_t best = key[0];
+    int at = 0;
 #pragma unroll
-    for (int j = 1; j < J; ++j) best = max(best, key[j]);
+    for (int j = 1; j < J; ++j)
+      if (key[j] > best) best = key[j], at = j;
     const uint32_t top = __reduce_max_sync(FULL_MASK, best);
-    uint32_t at = 0x7fffffffu;
-#pragma unroll
-    for (int j = J - 1; j >= 0; --j)
-      if (key[j] == top) at = lane + 32 * j;
-    const uint32_t e = __reduce_min_sync(FULL_MASK, at);
+    const int src = __ffs(__ballot_sync(FULL_MASK, best == top)) - 1;
+    const int e = src * J + __shfl_sync(FULL_MASK, at, src);
+    if (lane == k) mine = e, won = top;
 #pragma unroll
     for (int j = 0; j < J; ++j)
-      if (e == static_cast<uint32_t>(lane + 32 * j)) key[j] = 0u;
-    if (lane == k) mine = static_cast<int>(e), l = of_key(top);
+      if (lane == src && j == at) key[j] = 0u;
   }
-  const float l0 = __shfl_sync(FULL_MASK, l, 0);
-  const float ex = lane < K ? expf(l - l0) : 0.f;
+  if (lane < K) chosen = mine, logit = of_key(won);
+}
+// and their softmax
+__device__ __forceinline__ float softmax_of(float logit, int K, int lane) {
+  const float top = __shfl_sync(FULL_MASK, logit, 0);
+  const float ex = lane < K ? expf(logit - top) : 0.f;
   float sum = ex;
 #pragma unroll
   for (int o = MAX_K / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL_MASK, sum, o);
-  if (lane < K) chosen = mine, prob = ex / sum;  // lane k's slot k
+  return ex / sum;
 }
 
 // ---------------------------------------------------------------- rows of tokens
@@ -260,17 +264,30 @@ __device__ __forceinline__ int place_of(int v) {
   return FMT == FEW_FP8 ? (v & ~7) | (v & 1) << 2 | (v & 7) >> 1 : v;
 }
 
-// Eight values of a row of bf16, or of fp32.
-__device__ __forceinline__ void load8(const uint16_t* row, int v, float (&f)[8]) {
-  const uint4 q = __ldcg(reinterpret_cast<const uint4*>(row) + v);
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+// Eight values of a row, of bf16 or of fp32, as they lie in memory.
+template <typename Value>
+struct Eight {
+  uint4 q[sizeof(Value) / 2];
+  __device__ __forceinline__ void load(const Value* row, int v) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) f[2 * k] = bf16_lo(w[k]), f[2 * k + 1] = bf16_hi(w[k]);
-}
-__device__ __forceinline__ void load8(const float* row, int v, float (&f)[8]) {
-  const float4 a = __ldcg(reinterpret_cast<const float4*>(row) + 2 * v), b = __ldcg(reinterpret_cast<const float4*>(row) + 2 * v + 1);
-  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-}
+    for (int i = 0; i < static_cast<int>(sizeof(Value) / 2); ++i) q[i] = __ldcg(reinterpret_cast<const uint4*>(row) + v * (sizeof(Value) / 2) + i);
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(Value) / 2); ++i) q[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void values(float (&f)[8]) const {
+    if constexpr (sizeof(Value) == 2) {
+      const uint32_t w[4] = {q[0].x, q[0].y, q[0].z, q[0].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) f[2 * k] = bf16_lo(w[k]), f[2 * k + 1] = bf16_hi(w[k]);
+    } else {
+      const uint32_t w[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(w[k]);
+    }
+  }
+};
 
 // `rows` rows of K values (row r from src + r K; tokens in bf16 or h in fp32) into
 // shared memory as the products read them, `warps` warps of which this is number
@@ -278,31 +295,54 @@ __device__ __forceinline__ void load8(const float* row, int v, float (&f)[8]) {
 // tokens as they are; h as the nearest bf16 and, 2 K bytes on, what that leaves.
 template <int FMT, typename Value>
 __device__ __forceinline__ void stage_rows(const Value* src, int rows, int K, int pitch, uint8_t* dst, float* scales, int warp, int warps) {
-  constexpr int V = 4;  // of a lane at a time
+  constexpr int V = 16 / sizeof(Value);  // eights of a lane at a time
   const int per_row = K >> 3, lane = threadIdx.x & 31;
-  for (int r = warp; r < rows; r += warps) {
+  Eight<Value> e[V];
+  auto load = [&](int r, int v0) {
     const Value* row = src + static_cast<long long>(r) * K;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      if (v0 + 32 * j < per_row) e[j].load(row, v0 + 32 * j);
+      else e[j].zero();
+    }
+  };
+  auto store = [&](int r, int v0, float inv) {
     uint8_t* to = dst + r * pitch;
-    float f[V][8], inv = 1.f;
-    auto load = [&](int v0) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        if (v0 + 32 * j < per_row) {
-          load8(row, v0 + 32 * j, f[j]);
-        } else {
+    for (int j = 0; j < V; ++j) {
+      const int v = v0 + 32 * j;
+      if (v >= per_row) break;
+      float f[8];
+      e[j].values(f);
+      uint8_t* at = to + place_of<FMT>(v) * 16;
+      if constexpr (FMT != FEW_BF16) {
+        *reinterpret_cast<uint4*>(at) = f16x8(f, inv);
+      } else if constexpr (sizeof(Value) == 2) {
+        *reinterpret_cast<uint4*>(at) = e[j].q[0];
+      } else {
+        uint32_t hi[4], lo[4];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) f[j][k] = 0.f;
-        }
+        for (int k = 0; k < 4; ++k) hi[k] = pack_bf16x2(f[2 * k], f[2 * k + 1]);
+        *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) lo[k] = pack_bf16x2(f[2 * k] - bf16_lo(hi[k]), f[2 * k + 1] - bf16_hi(hi[k]));
+        *reinterpret_cast<uint4*>(at + 2 * K) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
-    };
+    }
+  };
+  for (int r = warp; r < rows; r += warps) {
+    float inv = 1.f;
     if constexpr (FMT != FEW_BF16) {
       float top = 0.f;
       for (int v0 = lane; v0 < per_row; v0 += 32 * V) {
-        load(v0);
+        load(r, v0);
 #pragma unroll
-        for (int j = 0; j < V; ++j)
+        for (int j = 0; j < V; ++j) {
+          float f[8];
+          e[j].values(f);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) top = max_nan(top, fabsf(f[j][k]));
+          for (int k = 0; k < 8; ++k) top = max_nan(top, fabsf(f[k]));
+        }
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(FULL_MASK, top, o));
@@ -310,27 +350,8 @@ __device__ __forceinline__ void stage_rows(const Value* src, int rows, int K, in
       if (lane == 0) scales[r] = scale;
     }
     for (int v0 = lane; v0 < per_row; v0 += 32 * V) {
-      if (FMT == FEW_BF16 || per_row > 32 * V) load(v0);  // (else they are still here)
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int v = v0 + 32 * j;
-        if (v >= per_row) break;
-        uint8_t* at = to + place_of<FMT>(v) * 16;
-        if constexpr (FMT == FEW_BF16) {
-          uint32_t hi[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) hi[k] = pack_bf16x2(f[j][2 * k], f[j][2 * k + 1]);
-          *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          if constexpr (sizeof(Value) == 4) {
-            uint32_t lo[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) lo[k] = pack_bf16x2(f[j][2 * k] - bf16_lo(hi[k]), f[j][2 * k + 1] - bf16_hi(hi[k]));
-            *reinterpret_cast<uint4*>(at + 2 * K) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          }
-        } else {
-          *reinterpret_cast<uint4*>(at) = f16x8(f[j], inv);
-        }
-      }
+      if (FMT == FEW_BF16 || per_row > 32 * V) load(r, v0);  // (else they are still here)
+      store(r, v0, inv);
     }
   }
 }
@@ -545,7 +566,8 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
   constexpr int SLOT = slot_bytes<FMT>();
   uint8_t* region = smem + args.slots * WARPS * SLOT;
   Smem& s = *reinterpret_cast<Smem*>(region + args.region);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (a number that the compiler knows to be the warp's)
+  const int warp = __shfl_sync(FULL_MASK, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int T = args.T, E = args.E, K = args.K, H = args.H, I = args.I;
   // (no griddep_launch_dependents(): CTAs of the next kernel that wait beside this
   // one's cost it 1.2 us)
@@ -558,14 +580,13 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
   // the routing, a warp a token; the other warps bring the tokens
   float* s_scale = reinterpret_cast<float*>(region + T * token_pitch(H));
   int chosen = -1;
-  float prob = 0.f;
+  float prob = 0.f;  // its logit, until there is time for the softmax
   if (warp >= TOK) {
     stage_rows<FMT>(args.x, T, H, token_pitch(H), region, s_scale, warp - TOK, WARPS - TOK);
   } else if (warp < T) {
     if (args.logits) {
       const float* l = args.logits + warp * E;
       if (E <= 128) pick_experts<4>(l, E, K, lane, chosen, prob);
-      else if (E <= 512) pick_experts<16>(l, E, K, lane, chosen, prob);
       else pick_experts<32>(l, E, K, lane, chosen, prob);
     } else if (lane < K) {
       const long long e = args.topk_idx[warp * K + lane];
@@ -576,10 +597,6 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
     if (chosen >= 0) {
       atomicOr(&s.seen[chosen >> 5], 1u << (chosen & 31));
       atomicOr(&s.tokens[chosen], 1 << warp);
-    }
-    if (lane < K && blockIdx.x == 0 && args.idx_out) {
-      args.idx_out[warp * K + lane] = chosen;
-      args.probs_out[warp * K + lane] = prob;
     }
   }
   __syncthreads();
@@ -596,15 +613,31 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
     const int before = __shfl_sync(FULL_MASK, upto, w) - __popc(there);
     if ((there >> lane) & 1) s.expert[before + __popc(there & ((1u << lane) - 1u))] = w * 32 + lane;
   }
-  if (warp < T) {  // (of an expert that a token names twice the last slot counts)
+  __syncthreads();
+  const int active = __shfl_sync(FULL_MASK, upto, 31);
+
+  const uint32_t G = gridDim.x, b = blockIdx.x;
+  // this CTA's columns of h, numbered through the experts, and rows of the output
+  const uint32_t cols = static_cast<uint32_t>(active) * I;
+  const int f0 = b * cols / G, my_cols = (b + 1) * cols / G - f0;
+  const int first_a = f0 / I, first_j = f0 - first_a * I;
+  const int r0 = b * static_cast<uint32_t>(H) / G, r1 = (b + 1) * static_cast<uint32_t>(H) / G;
+  const int bytes1 = row_bytes<FMT>(H), bytes2 = row_bytes<FMT>(I);
+  const uint32_t slots = smem_u32(smem) + warp * args.slots * SLOT;
+  Cursor<FMT> cursor(args, s, active, warp, lane, first_a, first_j, my_cols, r0, r1 - r0);
+  for (int i = 0; i < args.slots; ++i) cursor.issue(slots + i * SLOT);
+  if (warp < T) {  // the experts' weights (of an expert that a token names twice the last slot counts)
+    if (args.logits) prob = softmax_of(prob, K, lane);
+    if (lane < K && blockIdx.x == 0 && args.idx_out) {
+      args.idx_out[warp * K + lane] = chosen;
+      args.probs_out[warp * K + lane] = prob;
+    }
     const int word = max(chosen, 0) >> 5;
     const uint32_t same = __match_any_sync(FULL_MASK, chosen), there = __shfl_sync(FULL_MASK, bits, word);
     const int before = __shfl_sync(FULL_MASK, upto, word) - __popc(there);
     if (chosen >= 0 && lane == 31 - __clz(same)) s.weight[before + __popc(there & ((1u << (chosen & 31)) - 1u))][warp] = prob;
   }
-  __syncthreads();
-  const int active = __shfl_sync(FULL_MASK, upto, 31);
-  if (warp == 0) {  // and their rows of h
+  if (warp == TOK) {  // the experts' rows of h
     int row = 0;
     for (int a0 = 0; a0 < active; a0 += 32) {
       const int m = a0 + lane < active ? s.tokens[s.expert[a0 + lane]] : 0;
@@ -624,17 +657,6 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
     }
     if (lane == 0) s.first[active] = row;
   }
-
-  const uint32_t G = gridDim.x, b = blockIdx.x;
-  // this CTA's columns of h, numbered through the experts, and rows of the output
-  const uint32_t cols = static_cast<uint32_t>(active) * I;
-  const int f0 = b * cols / G, my_cols = (b + 1) * cols / G - f0;
-  const int first_a = f0 / I, first_j = f0 - first_a * I;
-  const int r0 = b * static_cast<uint32_t>(H) / G, r1 = (b + 1) * static_cast<uint32_t>(H) / G;
-  const int bytes1 = row_bytes<FMT>(H), bytes2 = row_bytes<FMT>(I);
-  const uint32_t slots = smem_u32(smem) + warp * args.slots * SLOT;
-  Cursor<FMT> cursor(args, s, active, warp, lane, first_a, first_j, my_cols, r0, r1 - r0);
-  for (int i = 0; i < args.slots; ++i) cursor.issue(slots + i * SLOT);
   __syncthreads();
   int slot = 0;
   auto next = [&](auto sum, float (&d)[4], int st, int bytes, uint32_t token) {
