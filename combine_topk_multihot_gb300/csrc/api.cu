@@ -1124,7 +1124,7 @@ FewWorkspace few_workspace(int32_t T, int32_t E, int32_t K, int32_t I) {
   FewWorkspace w{};
   w.logits = 256;  // behind the barrier's word
   w.h = w.logits + up(static_cast<size_t>(T) * E * sizeof(float));
-  w.total = w.h + up(static_cast<size_t>(T) * K * I * sizeof(float));
+  w.total = w.h + up(static_cast<size_t>(T) * K * I / 8 * 17);  // 2 bytes a number and 1 for eight
   return w;
 }
 
@@ -1203,7 +1203,7 @@ moe_status moe_layer_few(const moe_few* f, moe_stream_t stream) {
   g.T = f->T, g.E = f->E, g.K = f->K, g.H = f->H, g.I = f->I;
   g.barrier = reinterpret_cast<unsigned*>(base);
   g.logits = reinterpret_cast<float*>(base + w.logits);
-  g.h = reinterpret_cast<float*>(base + w.h);
+  g.h = reinterpret_cast<uint16_t*>(base + w.h);
   g.out = f->out;
   g.idx_out = f->idx_out;
   g.probs_out = f->probs_out;

@@ -304,7 +304,7 @@ struct FewLayer {
   const void *W1, *S1, *W2, *S2;
   int T, E, K, H, I;
   float* logits;             // scratch: [T, E]
-  float* h;                  // scratch: [T K, I]
+  uint16_t* h;               // scratch: [T K, I] and as many bytes as eights of that
   unsigned* barrier;         // scratch: one word
   uint16_t* out;             // [T, H]
   int64_t* idx_out;          // [T, K], nullable (both)

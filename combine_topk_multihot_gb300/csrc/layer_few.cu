@@ -93,7 +93,8 @@ struct FewArgs {
   int T, E, K, H, I;
   int slots, cap;            // of a warp; rows of h that shared memory holds
   int region;                // bytes of the tokens' rows and their scales
-  float* h;                  // [T K, I]
+  uint16_t* h;               // [T K, I] in f16, eight columns of a row to a power of two,
+  uint8_t* h_exp;            // [T K, I / 8], as the exponent of an fp32 number; 255: NaN
   unsigned* barrier;
   uint16_t* out;
   int64_t* idx_out;
@@ -264,82 +265,32 @@ __device__ __forceinline__ int place_of(int v) {
   return FMT == FEW_FP8 ? (v & ~7) | (v & 1) << 2 | (v & 7) >> 1 : v;
 }
 
-// Eight values of a row, of bf16 or of fp32, as they lie in memory.
-template <typename Value>
-struct Eight {
-  uint4 q[sizeof(Value) / 2];
-  __device__ __forceinline__ void load(const Value* row, int v) {
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(Value) / 2); ++i) q[i] = __ldcg(reinterpret_cast<const uint4*>(row) + v * (sizeof(Value) / 2) + i);
-  }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(Value) / 2); ++i) q[i] = make_uint4(0, 0, 0, 0);
-  }
-  __device__ __forceinline__ void values(float (&f)[8]) const {
-    if constexpr (sizeof(Value) == 2) {
-      const uint32_t w[4] = {q[0].x, q[0].y, q[0].z, q[0].w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) f[2 * k] = bf16_lo(w[k]), f[2 * k + 1] = bf16_hi(w[k]);
-    } else {
-      const uint32_t w[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
-#pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(w[k]);
-    }
-  }
-};
-
-// `rows` rows of K values (row r from src + r K; tokens in bf16 or h in fp32) into
-// shared memory as the products read them, `warps` warps of which this is number
-// `warp`, a row each.  For codes: f16 with a scale for each row.  For bf16 weights:
-// tokens as they are; h as the nearest bf16 and, 2 K bytes on, what that leaves.
-template <int FMT, typename Value>
-__device__ __forceinline__ void stage_rows(const Value* src, int rows, int K, int pitch, uint8_t* dst, float* scales, int warp, int warps) {
-  constexpr int V = 16 / sizeof(Value);  // eights of a lane at a time
+// `rows` rows of K bf16 values into shared memory as the products read them, `warps`
+// warps of which this is number `warp`, a row each.  For codes: f16 with a scale for each row.
+template <int FMT>
+__device__ __forceinline__ void stage_tokens(const uint16_t* src, int rows, int K, int pitch, uint8_t* dst, float* scales, int warp, int warps) {
+  constexpr int V = 8;  // eights of a lane at a time
   const int per_row = K >> 3, lane = threadIdx.x & 31;
-  Eight<Value> e[V];
+  uint4 q[V];
   auto load = [&](int r, int v0) {
-    const Value* row = src + static_cast<long long>(r) * K;
+    const uint4* row = reinterpret_cast<const uint4*>(src + static_cast<long long>(r) * K);
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      if (v0 + 32 * j < per_row) e[j].load(row, v0 + 32 * j);
-      else e[j].zero();
-    }
+    for (int j = 0; j < V; ++j) q[j] = v0 + 32 * j < per_row ? __ldcg(row + v0 + 32 * j) : make_uint4(0, 0, 0, 0);
   };
-  auto store = [&](int r, int v0, float inv) {
-    uint8_t* to = dst + r * pitch;
+  auto values = [&](const uint4& of, float (&f)[8]) {
+    const uint32_t w[4] = {of.x, of.y, of.z, of.w};
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int v = v0 + 32 * j;
-      if (v >= per_row) break;
-      float f[8];
-      e[j].values(f);
-      uint8_t* at = to + place_of<FMT>(v) * 16;
-      if constexpr (FMT != FEW_BF16) {
-        *reinterpret_cast<uint4*>(at) = f16x8(f, inv);
-      } else if constexpr (sizeof(Value) == 2) {
-        *reinterpret_cast<uint4*>(at) = e[j].q[0];
-      } else {
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) hi[k] = pack_bf16x2(f[2 * k], f[2 * k + 1]);
-        *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) lo[k] = pack_bf16x2(f[2 * k] - bf16_lo(hi[k]), f[2 * k + 1] - bf16_hi(hi[k]));
-        *reinterpret_cast<uint4*>(at + 2 * K) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-      }
-    }
+    for (int k = 0; k < 4; ++k) f[2 * k] = bf16_lo(w[k]), f[2 * k + 1] = bf16_hi(w[k]);
   };
   for (int r = warp; r < rows; r += warps) {
-    float inv = 1.f;
+    float f[8], inv = 1.f;
     if constexpr (FMT != FEW_BF16) {
       float top = 0.f;
       for (int v0 = lane; v0 < per_row; v0 += 32 * V) {
         load(r, v0);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          float f[8];
-          e[j].values(f);
+          values(q[j], f);
 #pragma unroll
           for (int k = 0; k < 8; ++k) top = max_nan(top, fabsf(f[k]));
         }
@@ -351,7 +302,101 @@ __device__ __forceinline__ void stage_rows(const Value* src, int rows, int K, in
     }
     for (int v0 = lane; v0 < per_row; v0 += 32 * V) {
       if (FMT == FEW_BF16 || per_row > 32 * V) load(r, v0);  // (else they are still here)
-      store(r, v0, inv);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int v = v0 + 32 * j;
+        if (v >= per_row) break;
+        uint4 to = q[j];
+        if constexpr (FMT != FEW_BF16) {
+          values(q[j], f);
+          to = f16x8(f, inv);
+        }
+        *reinterpret_cast<uint4*>(dst + r * pitch + place_of<FMT>(v) * 16) = to;
+      }
+    }
+  }
+}
+
+// 2^-d as two f16 numbers, 0 where that is below their least.
+__device__ __forceinline__ __half2 f16x2_of_exp(int d) {
+  const uint32_t h = d <= 14 ? (15 - d) << 10 : d <= 24 ? 1u << (24 - d) : 0u;
+  const uint32_t w = h | h << 16;
+  return *reinterpret_cast<const __half2*>(&w);
+}
+__device__ __forceinline__ float scale_of_exp(uint32_t e) { return __uint_as_float(e == 255u ? 0x7fc00000u : e << 23); }
+
+// `rows` rows of h, from row r0, in the same way.  For codes: f16 to the largest of
+// its powers of two.  For bf16 weights: the nearest bf16 numbers and, 2 I bytes on,
+// what those leave (11 bits are the sum of two numbers of 8).
+template <int FMT>
+__device__ __forceinline__ void stage_h(const FewArgs& args, int r0, int rows, int pitch, uint8_t* dst, float* scales, int warp) {
+  constexpr int V = 4, AT = 2;  // eights of a lane and rows of a warp at a time
+  const int per_row = args.I >> 3, lane = threadIdx.x & 31;
+  uint4 q[AT][V];
+  uint32_t e[AT][V];
+  auto load = [&](int n, int r, int v0) {
+    const uint4* row = reinterpret_cast<const uint4*>(args.h) + static_cast<long long>(r0 + r) * per_row;
+    const uint8_t* exp = args.h_exp + static_cast<long long>(r0 + r) * per_row;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const bool there = v0 + 32 * j < per_row;
+      q[n][j] = there ? __ldcg(row + v0 + 32 * j) : make_uint4(0, 0, 0, 0);
+      e[n][j] = there ? __ldcg(exp + v0 + 32 * j) : 0u;
+    }
+  };
+  auto largest = [&](int n) { return max(max(e[n][0], e[n][1]), max(e[n][2], e[n][3])); };
+  auto store = [&](int n, int r, int v0, uint32_t top) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int v = v0 + 32 * j;
+      if (v >= per_row) break;
+      uint8_t* at = dst + r * pitch + place_of<FMT>(v) * 16;
+      const uint32_t w[4] = {q[n][j].x, q[n][j].y, q[n][j].z, q[n][j].w};
+      uint32_t hi[4], lo[4];
+      if constexpr (FMT == FEW_BF16) {
+        const float scale = scale_of_exp(e[n][j]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+          f.x *= scale, f.y *= scale;
+          hi[k] = pack_bf16x2(f.x, f.y);
+          lo[k] = pack_bf16x2(f.x - bf16_lo(hi[k]), f.y - bf16_hi(hi[k]));
+        }
+        *reinterpret_cast<uint4*>(at + 2 * args.I) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      } else {
+        const __half2 scale = f16x2_of_exp(static_cast<int>(top - e[n][j]));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const __half2 f = __hmul2(*reinterpret_cast<const __half2*>(&w[k]), scale);
+          hi[k] = *reinterpret_cast<const uint32_t*>(&f);
+        }
+      }
+      *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    }
+  };
+  for (int i = warp; i < rows; i += AT * WARPS) {
+    if (per_row <= 32 * V) {
+#pragma unroll
+      for (int n = 0; n < AT; ++n)
+        if (i + n * WARPS < rows) load(n, i + n * WARPS, lane);
+    }
+#pragma unroll
+    for (int n = 0; n < AT; ++n) {
+      const int r = i + n * WARPS;
+      if (r >= rows) break;
+      uint32_t top = 0;
+      if constexpr (FMT != FEW_BF16) {
+        for (int v0 = lane; v0 < per_row; v0 += 32 * V) {
+          if (per_row > 32 * V) load(n, r, v0);
+          top = max(top, largest(n));
+        }
+        top = __reduce_max_sync(FULL_MASK, top);
+        if (lane == 0) scales[r] = scale_of_exp(top);
+      }
+      for (int v0 = lane; v0 < per_row; v0 += 32 * V) {
+        if (per_row > 32 * V) load(n, r, v0);
+        store(n, r, v0, top);
+      }
     }
   }
 }
@@ -401,22 +446,20 @@ struct Cursor {
     of += scales(r, K);
     return FMT == FEW_FP8 ? of : of + (r & 31) * 16 + ((r >> 5) & 3) * 4;
   }
-  __device__ __forceinline__ int tile() const { return min(8, min(left, I - j0)); }
   __device__ __forceinline__ void skip_tile() {
-    const int n = tile();
-    left -= n;
-    j0 += n;
+    left -= 8;
+    j0 += 8;
     if (j0 == I) j0 = 0, ++a;
   }
   __device__ __forceinline__ bool more() const { return left2 > 0; }
   __device__ __forceinline__ void aim1() {
-    n_lo = n_hi = tile();
+    n_lo = n_hi = 8;
     const int e = s.expert[a];
     lo = base + e * stride + static_cast<long long>(j0) * bytes1;
     hi = lo + static_cast<long long>(I) * bytes1;
     if constexpr (FMT != FEW_BF16)
       scale = row_scales(static_cast<const uint8_t*>(args.S1) + e * scale_stride, args.H,
-                         j0 + min(lane & 7, n_lo - 1) + (lane & 8 ? I : 0));
+                         j0 + (lane & 7) + (lane & 8 ? I : 0));
   }
   // the 16 rows of the output from m0
   __device__ __forceinline__ void rows_at() {
@@ -582,7 +625,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
   int chosen = -1;
   float prob = 0.f;  // its logit, until there is time for the softmax
   if (warp >= TOK) {
-    stage_rows<FMT>(args.x, T, H, token_pitch(H), region, s_scale, warp - TOK, WARPS - TOK);
+    stage_tokens<FMT>(args.x, T, H, token_pitch(H), region, s_scale, warp - TOK, WARPS - TOK);
   } else if (warp < T) {
     if (args.logits) {
       const float* l = args.logits + warp * E;
@@ -618,8 +661,8 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
 
   const uint32_t G = gridDim.x, b = blockIdx.x;
   // this CTA's columns of h, numbered through the experts, and rows of the output
-  const uint32_t cols = static_cast<uint32_t>(active) * I;
-  const int f0 = b * cols / G, my_cols = (b + 1) * cols / G - f0;
+  const uint32_t tiles = static_cast<uint32_t>(active) * (I >> 3);
+  const int f0 = b * tiles / G * 8, my_cols = (b + 1) * tiles / G * 8 - f0;
   const int first_a = f0 / I, first_j = f0 - first_a * I;
   const int r0 = b * static_cast<uint32_t>(H) / G, r1 = (b + 1) * static_cast<uint32_t>(H) / G;
   const int bytes1 = row_bytes<FMT>(H), bytes2 = row_bytes<FMT>(I);
@@ -675,11 +718,10 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
     const uint32_t token = rows_u32 + min(g, T - 1) * token_pitch(H);
     const int team = warp / TEAM, tid = threadIdx.x % (32 * TEAM);
     int par = 0, a = first_a, j = first_j, turn = 0;
-    for (int left = my_cols, n; left > 0; left -= n) {
+    for (int left = my_cols; left > 0; left -= 8) {
       if (j == I) j = 0, ++a;
       const int j0 = j;
-      n = min(8, min(left, I - j0));
-      j += n;
+      j += 8;
       const bool mine = turn == team;
       if (++turn == WARPS / TEAM) turn = 0;
       if (!mine) continue;
@@ -691,17 +733,23 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
       // tile's, which follows their reading here
       team_sync(team);
       if (tid < 64) {
-        const int i = tid >> 3, tok = tid & 7;
-        const int row = s.row[a][tok];
-        if (i < n && row >= 0) {
-          float gate = 0.f, up = 0.f;
+        const int tok = tid >> 3, i = tid & 7;
+        float gate = 0.f, up = 0.f;
 #pragma unroll
-          for (int w = 0; w < TEAM; ++w) {
-            gate += s.part[par][team * TEAM + w][tok & 1][i * 4 + (tok >> 1)];
-            up += s.part[par][team * TEAM + w][2 + (tok & 1)][i * 4 + (tok >> 1)];
-          }
-          if constexpr (FMT != FEW_BF16) gate *= s_scale[tok], up *= s_scale[tok];
-          args.h[static_cast<long long>(row) * I + j0 + i] = gate / (1.0f + expf(-gate)) * up;
+        for (int w = 0; w < TEAM; ++w) {
+          gate += s.part[par][team * TEAM + w][tok & 1][i * 4 + (tok >> 1)];
+          up += s.part[par][team * TEAM + w][2 + (tok & 1)][i * 4 + (tok >> 1)];
+        }
+        if constexpr (FMT != FEW_BF16) gate *= s_scale[min(tok, T - 1)], up *= s_scale[min(tok, T - 1)];
+        const float v = gate / (1.0f + expf(-gate)) * up;
+        float top = fabsf(v), inv;
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) top = max_nan(top, __shfl_xor_sync(FULL_MASK, top, o));
+        const float scale = row_scale_f16(top, inv);
+        const int row = s.row[a][tok];
+        if (row >= 0) {
+          args.h[static_cast<long long>(row) * I + j0 + i] = __half_as_ushort(__float2half_rn(v * inv));
+          if (i == 0) args.h_exp[static_cast<long long>(row) * (I >> 3) + (j0 >> 3)] = static_cast<uint8_t>(__float_as_uint(scale) >> 23);
         }
       }
       par ^= 1;
@@ -744,7 +792,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
       while (sb < active && s.first[sb + 1] - s.first[sa] <= args.cap) ++sb;
       if (!whole || m0 == r0) {
         __syncthreads();
-        stage_rows<FMT>(args.h + static_cast<long long>(s.first[sa]) * I, s.first[sb] - s.first[sa], I, hp, region, h_scale, warp, WARPS);
+        stage_h<FMT>(args, s.first[sa], s.first[sb] - s.first[sa], hp, region, h_scale, warp);
         __syncthreads();
       }
       while (true) {
@@ -858,6 +906,7 @@ cudaError_t launch_few_layer(const FewLayer& f, cudaStream_t s) {
   g.S2 = f.S2;
   g.T = f.T, g.E = f.E, g.K = f.K, g.H = f.H, g.I = f.I;
   g.h = f.h;
+  g.h_exp = reinterpret_cast<uint8_t*>(f.h + static_cast<size_t>(f.T) * f.K * f.I);
   g.barrier = f.barrier;
   g.out = f.out;
   g.idx_out = f.idx_out;
