@@ -74,14 +74,17 @@ __host__ __device__ constexpr int h_pitch(int K) { return (FMT == FEW_BF16 ? 4 :
 
 struct Smem {
   int ok;
-  int expert[PAIRS];         // ascending
-  int first[PAIRS + 1];      // pairs before each: its first row of h
-  float weight[PAIRS][TOK];
-  int row[PAIRS][TOK];       // of h, of each token; -1: none
-  uint32_t seen[32];         // a bit for each expert with tokens
-  int tokens[1024];          // the tokens of each expert, a bit each
-  float part[2][WARPS][4][32];
+  int expert[PAIRS];          // ascending
+  int first[PAIRS + 1];       // pairs before each: its first row of h
+  float weight[PAIRS];        // of each row of h
+  int8_t row[PAIRS][TOK];     // of h, of each token; -1: none
+  uint32_t seen[32];          // a bit for each expert with tokens
+  uint32_t tokens[1024 / 4];  // the tokens of each expert, a bit each, four experts a word
+  float part[WARPS][4][32];   // the second product's sums; the first's are behind the tokens
 };
+constexpr int FRONT_PARTS = 2 * WARPS * 4 * 32 * 4;
+// bytes of T tokens' rows, and their scales
+__host__ __device__ constexpr int front_bytes(int T, int H) { return T * token_pitch(H) + 64; }
 
 struct FewArgs {
   const uint16_t* x;
@@ -317,40 +320,34 @@ __device__ __forceinline__ void stage_tokens(const uint16_t* src, int rows, int 
   }
 }
 
-// 2^-d as two f16 numbers, 0 where that is below their least.
-__device__ __forceinline__ __half2 f16x2_of_exp(int d) {
-  const uint32_t h = d <= 14 ? (15 - d) << 10 : d <= 24 ? 1u << (24 - d) : 0u;
-  const uint32_t w = h | h << 16;
-  return *reinterpret_cast<const __half2*>(&w);
-}
 __device__ __forceinline__ float scale_of_exp(uint32_t e) { return __uint_as_float(e == 255u ? 0x7fc00000u : e << 23); }
 
-// `rows` rows of h, from row r0, in the same way.  For codes: f16 to the largest of
-// its powers of two.  For bf16 weights: the nearest bf16 numbers and, 2 I bytes on,
-// what those leave (11 bits are the sum of two numbers of 8).
+// `rows` rows of h, from row r0, in the same way, two of a warp on their way at a time.
+// For codes: f16 to the largest of its powers of two.  For bf16 weights: the nearest
+// bf16 numbers and, 2 I bytes on, what those leave (11 bits are the sum of two numbers of 8).
 template <int FMT>
 __device__ __forceinline__ void stage_h(const FewArgs& args, int r0, int rows, int pitch, uint8_t* dst, float* scales, int warp) {
   constexpr int V = 4, AT = 2;  // eights of a lane and rows of a warp at a time
   const int per_row = args.I >> 3, lane = threadIdx.x & 31;
+  const uint4* codes = reinterpret_cast<const uint4*>(args.h) + r0 * per_row + lane;
+  const uint8_t* exps = args.h_exp + r0 * per_row + lane;
+  dst += place_of<FMT>(lane) * 16;
   uint4 q[AT][V];
   uint32_t e[AT][V];
-  auto load = [&](int n, int r, int v0) {
-    const uint4* row = reinterpret_cast<const uint4*>(args.h) + static_cast<long long>(r0 + r) * per_row;
-    const uint8_t* exp = args.h_exp + static_cast<long long>(r0 + r) * per_row;
+  auto load = [&](int n, int r, int v0) {  // eights v0 + lane + 32 j
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const bool there = v0 + 32 * j < per_row;
-      q[n][j] = there ? __ldcg(row + v0 + 32 * j) : make_uint4(0, 0, 0, 0);
-      e[n][j] = there ? __ldcg(exp + v0 + 32 * j) : 0u;
+      const bool there = r < rows && v0 + lane + 32 * j < per_row;
+      e[n][j] = there ? __ldcg(exps + r * per_row + v0 + 32 * j) : 0u;
+      if (there) q[n][j] = __ldcg(codes + r * per_row + v0 + 32 * j);
     }
   };
   auto largest = [&](int n) { return max(max(e[n][0], e[n][1]), max(e[n][2], e[n][3])); };
   auto store = [&](int n, int r, int v0, uint32_t top) {
+    uint8_t* to = dst + r * pitch + v0 * 16;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int v = v0 + 32 * j;
-      if (v >= per_row) break;
-      uint8_t* at = dst + r * pitch + place_of<FMT>(v) * 16;
+      if (v0 + lane + 32 * j >= per_row) break;
       const uint32_t w[4] = {q[n][j].x, q[n][j].y, q[n][j].z, q[n][j].w};
       uint32_t hi[4], lo[4];
       if constexpr (FMT == FEW_BF16) {
@@ -362,41 +359,52 @@ __device__ __forceinline__ void stage_h(const FewArgs& args, int r0, int rows, i
           hi[k] = pack_bf16x2(f.x, f.y);
           lo[k] = pack_bf16x2(f.x - bf16_lo(hi[k]), f.y - bf16_hi(hi[k]));
         }
-        *reinterpret_cast<uint4*>(at + 2 * args.I) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        *reinterpret_cast<uint4*>(to + 512 * j + 2 * args.I) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       } else {
-        const __half2 scale = f16x2_of_exp(static_cast<int>(top - e[n][j]));
+        const float down = __uint_as_float((127u - min(top - e[n][j], 126u)) << 23);
+        const __half2 scale = __float2half2_rn(down);  // 0 below f16's least
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const __half2 f = __hmul2(*reinterpret_cast<const __half2*>(&w[k]), scale);
           hi[k] = *reinterpret_cast<const uint32_t*>(&f);
         }
       }
-      *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(to + 512 * j) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     }
   };
-  for (int i = warp; i < rows; i += AT * WARPS) {
-    if (per_row <= 32 * V) {
+  auto scale_row = [&](int r, uint32_t top) {
+    top = __reduce_max_sync(FULL_MASK, top);
+    if (lane == 0) scales[r] = scale_of_exp(top);
+    return top;
+  };
+  if (per_row <= 32 * V) {
 #pragma unroll
-      for (int n = 0; n < AT; ++n)
-        if (i + n * WARPS < rows) load(n, i + n * WARPS, lane);
+    for (int n = 0; n < AT; ++n) load(n, warp + n * WARPS, 0);
+    for (int i = warp; i < rows; i += AT * WARPS) {
+#pragma unroll
+      for (int n = 0; n < AT; ++n) {
+        const int r = i + n * WARPS;
+        if (r >= rows) break;
+        uint32_t top = 0;
+        if constexpr (FMT != FEW_BF16) top = scale_row(r, largest(n));
+        store(n, r, 0, top);
+        load(n, r + AT * WARPS, 0);
+      }
     }
-#pragma unroll
-    for (int n = 0; n < AT; ++n) {
-      const int r = i + n * WARPS;
-      if (r >= rows) break;
-      uint32_t top = 0;
-      if constexpr (FMT != FEW_BF16) {
-        for (int v0 = lane; v0 < per_row; v0 += 32 * V) {
-          if (per_row > 32 * V) load(n, r, v0);
-          top = max(top, largest(n));
-        }
-        top = __reduce_max_sync(FULL_MASK, top);
-        if (lane == 0) scales[r] = scale_of_exp(top);
+    return;
+  }
+  for (int r = warp; r < rows; r += WARPS) {  // a row in pieces
+    uint32_t top = 0;
+    if constexpr (FMT != FEW_BF16) {
+      for (int v0 = 0; v0 < per_row; v0 += 32 * V) {
+        load(0, r, v0);
+        top = max(top, largest(0));
       }
-      for (int v0 = lane; v0 < per_row; v0 += 32 * V) {
-        if (per_row > 32 * V) load(n, r, v0);
-        store(n, r, v0, top);
-      }
+      top = scale_row(r, top);
+    }
+    for (int v0 = 0; v0 < per_row; v0 += 32 * V) {
+      load(0, r, v0);
+      store(0, r, v0, top);
     }
   }
 }
@@ -614,8 +622,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
   const int T = args.T, E = args.E, K = args.K, H = args.H, I = args.I;
   // (no griddep_launch_dependents(): CTAs of the next kernel that wait beside this
   // one's cost it 1.2 us)
-  for (int e = threadIdx.x; e < E; e += THREADS) s.tokens[e] = 0;
-  for (int i = threadIdx.x; i < PAIRS * TOK; i += THREADS) s.weight[0][i] = 0.f;
+  if (static_cast<int>(threadIdx.x) * 4 < E) s.tokens[threadIdx.x] = 0;
   if (threadIdx.x < 32) s.seen[threadIdx.x] = 0;
   __syncthreads();
   griddep_wait();
@@ -639,7 +646,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
     }
     if (chosen >= 0) {
       atomicOr(&s.seen[chosen >> 5], 1u << (chosen & 31));
-      atomicOr(&s.tokens[chosen], 1 << warp);
+      atomicOr(&s.tokens[chosen >> 2], 1u << ((chosen & 3) * 8 + warp));
     }
   }
   __syncthreads();
@@ -669,7 +676,8 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
   const uint32_t slots = smem_u32(smem) + warp * args.slots * SLOT;
   Cursor<FMT> cursor(args, s, active, warp, lane, first_a, first_j, my_cols, r0, r1 - r0);
   for (int i = 0; i < args.slots; ++i) cursor.issue(slots + i * SLOT);
-  if (warp < T) {  // the experts' weights (of an expert that a token names twice the last slot counts)
+  int at = -1;  // this slot's expert's place (of an expert that a token names twice the last slot counts)
+  if (warp < T) {
     if (args.logits) prob = softmax_of(prob, K, lane);
     if (lane < K && blockIdx.x == 0 && args.idx_out) {
       args.idx_out[warp * K + lane] = chosen;
@@ -678,12 +686,13 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
     const int word = max(chosen, 0) >> 5;
     const uint32_t same = __match_any_sync(FULL_MASK, chosen), there = __shfl_sync(FULL_MASK, bits, word);
     const int before = __shfl_sync(FULL_MASK, upto, word) - __popc(there);
-    if (chosen >= 0 && lane == 31 - __clz(same)) s.weight[before + __popc(there & ((1u << (chosen & 31)) - 1u))][warp] = prob;
+    if (chosen >= 0 && lane == 31 - __clz(same)) at = before + __popc(there & ((1u << (chosen & 31)) - 1u));
   }
   if (warp == TOK) {  // the experts' rows of h
     int row = 0;
     for (int a0 = 0; a0 < active; a0 += 32) {
-      const int m = a0 + lane < active ? s.tokens[s.expert[a0 + lane]] : 0;
+      const int e = a0 + lane < active ? s.expert[a0 + lane] : 0;
+      const int m = a0 + lane < active ? (s.tokens[e >> 2] >> ((e & 3) * 8)) & 0xff : 0;
       int n = __popc(m);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -694,13 +703,14 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
         int r = row + n - __popc(m);
         s.first[a0 + lane] = r;
 #pragma unroll
-        for (int t = 0; t < TOK; ++t) s.row[a0 + lane][t] = (m >> t) & 1 ? r++ : -1;
+        for (int t = 0; t < TOK; ++t) s.row[a0 + lane][t] = static_cast<int8_t>((m >> t) & 1 ? r++ : -1);
       }
       row += __shfl_sync(FULL_MASK, n, 31);
     }
     if (lane == 0) s.first[active] = row;
   }
   __syncthreads();
+  if (at >= 0) s.weight[s.row[at][warp]] = prob;  // read after the meeting
   int slot = 0;
   auto next = [&](auto sum, float (&d)[4], int st, int bytes, uint32_t token) {
     cp_async_wait(args.slots - 1);
@@ -716,6 +726,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
   const uint32_t rows_u32 = smem_u32(region);
   {
     const uint32_t token = rows_u32 + min(g, T - 1) * token_pitch(H);
+    auto* parts = reinterpret_cast<float (*)[WARPS][4][32]>(region + front_bytes(T, H));
     const int team = warp / TEAM, tid = threadIdx.x % (32 * TEAM);
     int par = 0, a = first_a, j = first_j, turn = 0;
     for (int left = my_cols; left > 0; left -= 8) {
@@ -728,7 +739,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
       float d[4] = {0.f, 0.f, 0.f, 0.f};
       for (int st = warp % TEAM; st * PIECE < bytes1; st += TEAM) next(std::false_type{}, d, st, bytes1, token);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s.part[par][warp][i][lane] = d[i];
+      for (int i = 0; i < 4; ++i) parts[par][warp][i][lane] = d[i];
       // one meeting a tile: this parity's sums are written again after the next
       // tile's, which follows their reading here
       team_sync(team);
@@ -737,8 +748,8 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
         float gate = 0.f, up = 0.f;
 #pragma unroll
         for (int w = 0; w < TEAM; ++w) {
-          gate += s.part[par][team * TEAM + w][tok & 1][i * 4 + (tok >> 1)];
-          up += s.part[par][team * TEAM + w][2 + (tok & 1)][i * 4 + (tok >> 1)];
+          gate += parts[par][team * TEAM + w][tok & 1][i * 4 + (tok >> 1)];
+          up += parts[par][team * TEAM + w][2 + (tok & 1)][i * 4 + (tok >> 1)];
         }
         if constexpr (FMT != FEW_BF16) gate *= s_scale[min(tok, T - 1)], up *= s_scale[min(tok, T - 1)];
         const float v = gate / (1.0f + expf(-gate)) * up;
@@ -803,13 +814,13 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
         float d[4] = {0.f, 0.f, 0.f, 0.f};
         next(std::bool_constant<FMT == FEW_BF16>{}, d, st, bytes2, token);
         if (row0 >= 0) {
-          float w = s.weight[a][2 * t];
+          float w = s.weight[row0];
           if constexpr (FMT != FEW_BF16) w *= h_scale[row0 - base];
           acc[0] = fmaf(w, d[0], acc[0]);
           acc[2] = fmaf(w, d[2], acc[2]);
         }
         if (row1 >= 0) {
-          float w = s.weight[a][2 * t + 1];
+          float w = s.weight[row1];
           if constexpr (FMT != FEW_BF16) w *= h_scale[row1 - base];
           acc[1] = fmaf(w, d[1], acc[1]);
           acc[3] = fmaf(w, d[3], acc[3]);
@@ -817,19 +828,19 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
         st += WARPS;
       }
     }
-    const int par = ((m0 - r0) >> 4) & 1;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s.part[par][warp][i][lane] = acc[i];
+    for (int i = 0; i < 4; ++i) s.part[warp][i][lane] = acc[i];
     __syncthreads();
     if (threadIdx.x < 128) {  // rows fastest
       const int r = threadIdx.x & 15, tok = threadIdx.x >> 4;
       if (r < n && tok < T) {
         float v = 0.f;
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) v += s.part[par][w][(r >> 3) * 2 + (tok & 1)][(r & 7) * 4 + (tok >> 1)];
+        for (int w = 0; w < WARPS; ++w) v += s.part[w][(r >> 3) * 2 + (tok & 1)][(r & 7) * 4 + (tok >> 1)];
         args.out[static_cast<long long>(tok) * H + m0 + r] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
       }
     }
+    if (m0 + 16 < r1) __syncthreads();
   }
 }
 
@@ -841,9 +852,10 @@ thread_local int tls_ctas = 0x7fffffff;
 template <int FMT>
 bool plan(FewArgs& g, size_t* smem) {
   constexpr int SLOT = slot_bytes<FMT>();
-  const long long x_row = token_pitch(g.H) + 4, h_row = h_pitch<FMT>(g.I) + 4;
+  if (g.H > 1 << 20 || g.I > 1 << 20) return false;  // no row fits, and the sizes below pass 32 bits
+  const long long h_row = h_pitch<FMT>(g.I) + 4, front = front_bytes(g.T, g.H) + FRONT_PARTS;
   // all rows of h where they leave three slots a warp, else as many as there are tokens
-  const long long need = g.T * (x_row > h_row ? x_row : h_row), most = SMEM_LIMIT - FIXED - 128 - 3 * WARPS * SLOT;
+  const long long need = g.T * h_row > front ? g.T * h_row : front, most = SMEM_LIMIT - FIXED - 128 - 3 * WARPS * SLOT;
   long long room = g.T * g.K * h_row;
   if (room > most) room = most;
   if (room < need) room = need;
