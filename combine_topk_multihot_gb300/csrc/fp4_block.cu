@@ -16,7 +16,9 @@ namespace {
 // neighbours in their tile; lane l holds 8 values of each, 4 lanes a block, 16
 // lanes a scale word.  Rows up to the next multiple of 128 have scales only,
 // zeros.  Every quotient is a product with a power of two, so codes are functions
-// of the input alone.  Bound by HBM.
+// of the input alone.  403 M bf16 weights take 189 us, 5.4 TB/s (a row a warp: 217),
+// which the instructions bound as much as HBM: the issue slots are 79 % busy, the integer
+// pipe, which compares and packs, 66 %, HBM 60 % by the profiler's peak.
 constexpr int PIECES = 4;
 template <bool F32>
 __global__ void __launch_bounds__(256, F32 ? 4 : 5) quantize_fp4_kernel(const void* __restrict__ src, long long all, int rows,
@@ -81,7 +83,8 @@ __global__ void __launch_bounds__(256, F32 ? 4 : 5) quantize_fp4_kernel(const vo
 }
 
 // The way back: exact in either type, a code has two significant bits.  A warp takes
-// up to four 256-column pieces of one row; blockIdx.y picks the pieces.
+// up to four 256-column pieces of one row; blockIdx.y picks the pieces.  Bound by
+// HBM: 403 M bf16 weights take 146 us, 7.0 TB/s.
 template <bool F32>
 __global__ void __launch_bounds__(256) dequantize_fp4_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                                                              long long all, int rows, int cols, void* __restrict__ out) {
@@ -133,7 +136,10 @@ __global__ void __launch_bounds__(256) dequantize_fp4_kernel(const uint8_t* __re
 // of their rows and a slice of K, and multiplies with mma.sync, the 8 rows as its
 // other operand.  Codes become f16 numbers (exact) in registers; lane t of a row's
 // four takes word t of each block of 32, so that two instructions' 32 products
-// share their scales, which are applied to the sums.  The slices of K are joined in shared memory in a fixed order.
+// share their scales, which are applied to the sums.  The slices of K are joined in
+// shared memory in a fixed order.  It takes the calls of few tiles, where the
+// tensor cores' kernel is bound by its start and end; from 1024 columns on that one is
+// faster (8 x 16384 x 4096: 12 us for 23 here).
 // 2^(ea + eb - 254) as two factors: their product may leave fp32's range where
 // the value does not.
 struct Scale2 {

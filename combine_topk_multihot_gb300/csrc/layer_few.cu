@@ -22,18 +22,27 @@
 //     each a slice of K, all sixteen one of the second; their sums are joined in
 //     shared memory in a fixed order.  A token's column is computed for
 //     every expert and used for its own.
-// What bounds it: HBM for bf16; for the codes, and for one token, the instructions
-// and latencies around the products.  A ring of TMA boxes shared by all warps, filled
-// by one, was slower for every format (T = 8, E = 128, H = 2048, I = 768: 167 us in
-// bf16, 113 in e4m3, 144 in e2m1): what a warp does for a stage, the wait for it
-// included, is a chain of a thousand cycles, and each stage took all of them.
+// What bounds it, at H = 2048, I = 768 and 8 of E = 128 experts a token: HBM for 8
+// tokens in bf16 (89 us, 70.6 of them the bytes of 51 experts); for the codes (e4m3 57.5,
+// bytes 35.4; e2m1 46.6, bytes 18.8) the instructions that make f16 numbers of them, 250
+// for a piece; for one token (23.4, 18.7 and 15.2) the way from launch to launch: the logits
+// 2 us, the list of experts 3, both products' first bytes, the meeting 1.5 to 2, h 1.5.
+//
+// Tried and slower: a ring of TMA boxes shared by all warps and filled by one (8 tokens: 167 us
+// in bf16, 113 in e4m3, 144 in e2m1: what a warp does for a stage, the wait for it included,
+// is a chain of a thousand cycles, and each stage took all of them); clusters of two CTAs that
+// share rows of the output and split the experts (1.2 us more a launch, 49.9 us for 49.5).
 //
 // Weights are bf16, e4m3 with a scale per 128 x 128, or e2m1 with a scale per 32
-// of a row.  Codes are multiplied as f16 numbers, which they are exactly, by
-// tokens (and h) in f16 with a power of two for each row: exact for bf16 values
-// down to 2^-31 of their row's largest, and within 2^-39 of that below it.  With bf16 weights h, which is held in fp32, is multiplied as the sum of two
-// bf16 numbers: rounded to one it would add as much error as the output's rounding.  (mma.sync on e4m3 operands takes 28 cycles an SM quarter here, on f16 12 for
-// half of K, and converting a pair of codes 2.3.)
+// of a row.  Codes are multiplied as f16 numbers, which they are exactly, by tokens and h
+// in f16 with a power of two for each row: exact for values down to 2^-28 of the row's
+// largest (a bf16 token: 2^-31), and within 2^-38 of that below it.  (mma.sync on e4m3
+// operands takes 28 cycles an SM quarter here, on f16 12 for half of K, and converting a pair
+// of codes 2.3.)  h goes through memory as f16 with a power of two for eight columns:
+// its rounding, 2^-12, is an eighth of the output's, and half the bytes of fp32 have to reach
+// every SM (in fp32 8 tokens took 0.9 to 2.3 us more).  With bf16 weights it is multiplied as
+// the sum of two bf16 numbers, which is exact: rounded to one it would add as much error as
+// the output's rounding.
 
 #include <cuda_fp16.h>
 

@@ -764,7 +764,8 @@ MOE_API moe_status moe_matmul_fp4_block(const uint8_t* a_q, const uint8_t* a_sca
  * A whole layer for at most 8 tokens, in two launches (inference):
  *   logits = x router^T in fp32; the K largest of a token, equal ones by
  *   ascending index (NaN as -infinity), and their softmax as weights w_k;
- *   h_k = silu(x Wg^T) * (x Wu^T) of expert e_k, in fp32;
+ *   h_k = silu(x Wg^T) * (x Wu^T) of expert e_k, rounded to 11 bits (f16 with a
+ *   power of two for eight columns);
  *   out = bf16(sum_k w_k (h_k W2^T)), summed in fp32 by ascending expert.
  * With router NULL the routing is given instead: topk_idx [T, K] (-1: no
  * expert; of an expert that a token names twice the last slot counts; another
@@ -776,11 +777,10 @@ MOE_API moe_status moe_matmul_fp4_block(const uint8_t* a_q, const uint8_t* a_sca
  *   W2_scale [E, H/128, I/128] fp32);
  *   MOE_WEIGHTS_FP4_BLOCK: e2m1 codes with scales in tiles
  *   (moe_quantize_fp4_block: W1_scale [E, 2I/128, H/128, 32, 4, 4], ...).
- * x and h are not rounded to 8 bits for the codes: they are multiplied as f16
- * numbers with a power of two for each row, exact for a bf16 value of 2^-31 of
- * the row's largest or more, and within 2^-39 of that largest below it.
- * By bf16 weights h is multiplied as the sum of two bf16 numbers.  A token with
- * a NaN or an infinity has a NaN or infinity in its own row alone.
+ * Codes are multiplied by x and h as f16 numbers with a power of two for each
+ * row, exact for values of 2^-28 of the row's largest or more, and within 2^-38 of that
+ * largest below it.  By bf16 weights h is multiplied as the sum of two bf16
+ * numbers.  A token with a NaN or an infinity has a NaN or infinity in its own row alone.
  */
 typedef enum moe_weights { MOE_WEIGHTS_BF16 = 0, MOE_WEIGHTS_FP8_BLOCK = 1, MOE_WEIGHTS_FP4_BLOCK = 2 } moe_weights;
 #define MOE_FEW_TOKENS 8
@@ -806,8 +806,8 @@ typedef struct moe_few {
 
 /*
  * 0 <= T <= 8, 1 <= E <= 1024, 1 <= K <= min(E, 16), H a multiple of 256, I of
- * 128, and the tokens' rows fit in shared memory (T H and T I up to about 66,000; with
- * bf16 weights T I up to 33,000).
+ * 128, and the tokens' rows fit in shared memory (T H up to about 65,000 and T I up
+ * to 74,000; by e2m1 weights 61,000 and 70,000; by bf16 weights T I up to 36,000).
  * x, router, weights and workspace are 16-byte aligned, scales 4-byte.  The
  * struct is HOST memory, read before the call returns.  A bounded wait that runs
  * out sets MOE_DEVERR_TIMEOUT and leaves NaN in the columns of out that were not
@@ -833,8 +833,8 @@ MOE_API moe_status moe_selftest_wait_timeout(int32_t* status, int64_t limit_ns, 
 /*
  * Self-test of a block-scaled product whose operands stop arriving: until it
  * is called again with -1, the tensor-core launches of the calling host thread
- * (moe_matmul_fp8_block and moe_matmul_fp4_block with more than 8 rows,
- * moe_grouped_experts_fp8_block with more than 8 tokens) load operands for the first `tiles` tiles of each
+ * (moe_matmul_fp8_block with more than 8 rows, moe_matmul_fp4_block
+ * on the tensor cores, moe_grouped_experts_fp8_block with more than 8 tokens) load operands for the first `tiles` tiles of each
  * CTA only.  Their waits then run out after about 2 s, the status word gets
  * MOE_DEVERR_TIMEOUT, and the outputs that were not reached are NaN.
  */

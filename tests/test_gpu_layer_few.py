@@ -5,11 +5,15 @@ gaps between them).  The output is held element by element to a bound that adds
 up what the steps may be off:
   * an fp32 sum of products on the tensor cores keeps at least 13 bits of its
     largest term while aligning: 2^-13 S, S the sum of the terms' magnitudes;
-  * with coded weights a value is represented within 2^-39 of its row's largest:
-    r(v) = 2^-39 max|v|, none for bf16 weights;
+  * with coded weights a token's value is represented within 2^-39 of its row's
+    largest: r(x) = 2^-39 max|x|, none for bf16 weights;
   * |silu'| <= 1.1 and |silu(g)| <= |g|: h is off by 1.1 |u| dg + |g| du, and by 2^-11
-    |h| for its rounding to f16 (half a step, at the most; as two bf16 numbers by
-    less) with 2^-18 |h| for the exponential and the quotient;
+    |h| for its rounding to f16 (half a step of 11 bits, at the most) with 2^-18 |h| for
+    the exponential and the quotient;
+  * h's small values: f16 has steps of 2^-24 below 2^-14, and the largest of eight
+    columns is brought to 2^14 or more, so half a step is 2^-25 / 2^14 = 2^-39 of that
+    largest; brought to the row's power of two (coded weights) a value is rounded so once
+    more: r(h) = 2 * 2^-39 max|h| = 2^-38 max|h|;
   * a weight w_k moves by the logits' error, at most 2^-14 relative here;
   * the output's rounding: 2^-8 |out|.
 """
@@ -58,17 +62,17 @@ def reference(x, idx, p, W1, W2, coded):
     """(fp64 output, its bound)."""
     T, H = x.shape
     I = W2.shape[2]
-    rep = (lambda v: 2.0 ** -39 * v.abs().amax().expand(v.shape)) if coded else torch.zeros_like
+    rep = lambda v, r: r * v.abs().amax().expand(v.shape)  # noqa: E731
     out, lim = torch.zeros(T, H, dtype=torch.float64, device=x.device), torch.zeros(T, H, dtype=torch.float64, device=x.device)
     for t in range(T):
         v = x[t].double()
         for e, w in {int(e): float(w) for e, w in zip(idx[t], p[t]) if e >= 0}.items():      # the last slot counts
-            gu, d = W1[e] @ v, 2.0 ** -13 * (W1[e].abs() @ v.abs()) + W1[e].abs() @ rep(v)
+            gu, d = W1[e] @ v, 2.0 ** -13 * (W1[e].abs() @ v.abs()) + W1[e].abs() @ rep(v, 2.0 ** -39 if coded else 0.0)
             g, u = gu[:I], gu[I:]
             h = g / (1 + torch.exp(-g)) * u
             dh = 1.1 * (u.abs() + d[I:]) * d[:I] + g.abs() * d[I:] + (2.0 ** -11 + 2.0 ** -18) * h.abs()
             o = W2[e] @ h
-            do = W2[e].abs() @ dh + 2.0 ** -13 * (W2[e].abs() @ h.abs()) + W2[e].abs() @ rep(h)
+            do = W2[e].abs() @ dh + 2.0 ** -13 * (W2[e].abs() @ h.abs()) + W2[e].abs() @ rep(h, 2.0 ** -38)
             out[t] += w * o
             lim[t] += w * (do + 2.0 ** -14 * o.abs())
     return out, lim + 2.0 ** -8 * (out.abs() + lim)
@@ -215,7 +219,7 @@ def test_refusals_without_a_gpu(moe):
     n = ctypes.c_size_t()
     assert N.lib.moe_layer_few_workspace_bytes(9, 8, 2, 128, ctypes.byref(n)) == N.MOE_ERR_UNSUPPORTED_SHAPE
     assert N.lib.moe_layer_few_workspace_bytes(8, 8, 2, 128, None) == N.MOE_ERR_INVALID_ARG
-    assert N.lib.moe_layer_few_workspace_bytes(8, 8, 2, 128, ctypes.byref(n)) == 0 and n.value == 256 + 256 + 8 * 2 * 128 * 4
+    assert N.lib.moe_layer_few_workspace_bytes(8, 8, 2, 128, ctypes.byref(n)) == 0 and n.value == 256 + 256 + 8 * 2 * 128 // 8 * 17
 
 
 @gpu
