@@ -23,6 +23,7 @@ arithmetic runs in its CUDA kernels.
 """
 from __future__ import annotations
 
+import functools
 from typing import List, Optional, Tuple
 
 import torch
@@ -512,9 +513,23 @@ def _(x, router, topk_idx, topk_probs, top_k, W1, W2, W1_scale, W2_scale):
     return x.new_empty(x.shape), x.new_empty(1, dtype=torch.int32)
 
 
-def _few(T: int, top_k: int, H: int, W1: Tensor, W1_scale: Optional[Tensor]) -> bool:
-    """Whether a layer of these sizes goes through layer_few."""
-    return 0 < T <= 8 and _b.moe_layer_few_fits(T, W1.shape[0], top_k, H, W1.shape[1] // 2, W1_scale)
+@functools.lru_cache(maxsize=1024)
+def _few_most_of(*sizes: int) -> int:
+    return max((T for T in range(1, 9) if _b.N.lib.moe_layer_few_fits(T, *sizes)), default=0)
+
+
+@torch.compiler.assume_constant_result
+def _few_most(E: int, top_k: int, H: int, I: int, weights: int) -> int:
+    """The most tokens that layer_few takes: a constant of a compiled program."""
+    return _few_most_of(E, top_k, H, I, weights)
+
+
+def _few(x: Tensor, top_k: int, W1: Tensor, W1_scale: Optional[Tensor], router: Optional[Tensor] = None) -> bool:
+    """Whether a layer of these operands goes through layer_few."""
+    if not 0 < x.shape[0] <= 8 or (router is not None and router.dtype not in (torch.bfloat16, torch.float32)):
+        return False
+    E, H, I2 = (len(range(n)) for n in (W1.shape[0], x.shape[1], W1.shape[1]))  # numbers where sizes are symbols
+    return x.shape[0] <= _few_most(E, top_k, H, I2 // 2, _b._few_format(W1_scale))
 
 
 def _grad_wanted(*tensors: Tensor) -> bool:
@@ -529,7 +544,7 @@ def moe_layer_fp4_block(x: Tensor, topk_idx: Tensor, topk_probs: Tensor, W1_q: T
     turned back to bf16, which is exact.  Returns out, or with ``return_status``
     (out, status) as moe_layer does."""
     T, K = topk_idx.shape
-    if not _grad_wanted(x, topk_probs) and _few(T, K, x.shape[1], W1_q, W1_scale):
+    if not _grad_wanted(x, topk_probs) and _few(x, K, W1_q, W1_scale):
         out, status = _ops.layer_few(x, None, topk_idx, topk_probs, K, W1_q, W2_q, W1_scale, W2_scale)
         return (out, status) if return_status else out
     return moe_layer(x, topk_idx, topk_probs, _ops.dequantize_fp4_block(W1_q, W1_scale), _ops.dequantize_fp4_block(W2_q, W2_scale),
@@ -551,11 +566,12 @@ def moe_block(x: Tensor, normed: Tensor, router: Tensor, top_k: int, W1: Tensor,
     runs for inference; with ``fp4`` they are e2m1 codes with a scale per 32.  With ``few`` at
     most 8 tokens, where no gradient is wanted, go through router and layer in
     the two launches of moe_layer_few (with ``fp4`` they always do): the same
-    sums in another order, and h not rounded between the products."""
+    sums in another order, and h rounded to 11 bits between the products."""
     scales = fp8 if fp8 is not None else fp4
     if fp8 is not None and fp4 is not None:
         raise ValueError("give fp8 or fp4, not both")
-    if (few or fp4 is not None) and not _grad_wanted(normed, router, *(() if scales else (W1, W2))) and _few(normed.shape[0], top_k, normed.shape[1], W1, scales and scales[0]):
+    wanted = _grad_wanted(normed, router, *(() if scales else (W1, W2)))
+    if (few or fp4 is not None) and not wanted and _few(normed, top_k, W1, scales and scales[0], router):
         y, status = _ops.layer_few(normed, router, None, None, top_k, W1, W2, *(scales or (None, None)))
     else:
         logits = (normed.float() @ router.float().t()).contiguous()

@@ -285,6 +285,27 @@ def test_block_takes_the_short_way_without_a_gpu(moe):
         ns.quantize_fp4_block(torch.zeros(4, 64))
 
 
+@pytest.mark.parametrize("dynamic", [None, False, True])
+def test_block_compiles_as_one_graph_without_a_gpu(moe, dynamic):
+    t = _meta(8)
+    blocks = (lambda x, n: moe.moe_block(x, n, t["router"], 2, t["W1"], t["W2"], t["w"], few=True)[0],
+              lambda x, n: moe.moe_block(x, n, t["router"], 2, t["q1"], t["q2"], t["w"], fp4=(t["s1"], t["s2"]))[0])
+    for block in blocks:
+        torch._dynamo.reset()
+        compiled = torch.compile(block, fullgraph=True, backend="aot_eager", dynamic=dynamic)
+        with torch.no_grad():
+            for T in (1, 3, 8, 9, 40):
+                x = torch.zeros(T, t["x"].shape[1], dtype=torch.bfloat16, device="meta")
+                assert compiled(x, x).shape == x.shape
+    torch._dynamo.reset()
+
+
+def test_block_with_another_router_type_takes_the_long_way_without_a_gpu(moe):
+    t = _meta(4)
+    run = lambda r: moe.moe_block(t["x"], t["normed"], r, 2, t["W1"], t["W2"], t["w"], few=True)[0]  # noqa: E731
+    assert "layer_few" in _used(run, t["router"].float()) and "layer_few" not in _used(run, t["router"].half())
+
+
 @gpu
 @pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
 def test_block(moe, fmt):
