@@ -23,15 +23,16 @@
 //     shared memory in a fixed order.  A token's column is computed for
 //     every expert and used for its own.
 // What bounds it, at H = 2048, I = 768 and 8 of E = 128 experts a token: HBM for 8
-// tokens in bf16 (89 us, 70.6 of them the bytes of 51 experts); for the codes (e4m3 57.5,
-// bytes 35.4; e2m1 46.6, bytes 18.8) the instructions that make f16 numbers of them, 250
-// for a piece; for one token (23.4, 18.7 and 15.2) the way from launch to launch: the logits
+// tokens in bf16 (89 us, 70.6 of them the bytes of 51 experts); for the codes (e4m3 57.4,
+// bytes 35.4; e2m1 46.3, bytes 18.8) the instructions that make f16 numbers of them, 250
+// for a piece; for one token (23.3, 18.7 and 15.1) the way from launch to launch: the logits
 // 2 us, the list of experts 3, both products' first bytes, the meeting 1.5 to 2, h 1.5.
 //
 // Tried and slower: a ring of TMA boxes shared by all warps and filled by one (8 tokens: 167 us
 // in bf16, 113 in e4m3, 144 in e2m1: what a warp does for a stage, the wait for it included,
 // is a chain of a thousand cycles, and each stage took all of them); clusters of two CTAs that
-// share rows of the output and split the experts (1.2 us more a launch, 49.9 us for 49.5).
+// share rows of the output and split the experts (1.2 us more a launch, 49.9 us for 49.5);
+// scales by loads of words that are stored to their slots a piece later, for cp.async (47.9 for 46.6).
 //
 // Weights are bf16, e4m3 with a scale per 128 x 128, or e2m1 with a scale per 32
 // of a row.  Codes are multiplied as f16 numbers, which they are exactly, by tokens and h
@@ -752,8 +753,8 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
       // one meeting a tile: this parity's sums are written again after the next
       // tile's, which follows their reading here
       team_sync(team);
-      if (tid < 64) {
-        const int tok = tid >> 3, i = tid & 7;
+      if (tid >> 6 == par) {  // two of the team's warps, the others at the next tile
+        const int tok = (tid >> 3) & 7, i = tid & 7;
         float gate = 0.f, up = 0.f;
 #pragma unroll
         for (int w = 0; w < TEAM; ++w) {
