@@ -781,6 +781,8 @@ MOE_API moe_status moe_matmul_fp4_block(const uint8_t* a_q, const uint8_t* a_sca
  * row, exact for values of 2^-28 of the row's largest or more, and within 2^-38 of that
  * largest below it.  By bf16 weights h is multiplied as the sum of two bf16
  * numbers.  A token with a NaN or an infinity has a NaN or infinity in its own row alone.
+ * A row's power of two is applied after the products: weights (code times scale)
+ * have to lie below 2^96, so that sums of products with values below 2^15 are finite.
  */
 typedef enum moe_weights { MOE_WEIGHTS_BF16 = 0, MOE_WEIGHTS_FP8_BLOCK = 1, MOE_WEIGHTS_FP4_BLOCK = 2 } moe_weights;
 #define MOE_FEW_TOKENS 8
