@@ -22,6 +22,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 from typing import Optional, Sequence, Union
 
 import numpy as np
@@ -445,10 +446,17 @@ def _fp4_tiles(rows: int, cols: int):
     return (rows + 127) // 128, (cols + 127) // 128, 32, 4, 4
 
 
-def _fp4_matrix(codes: torch.Tensor, name: str):
-    if codes.dim() < 2 or codes.shape[-1] % 16:
-        raise ValueError(f"{name} must be [..., rows, cols / 2] with cols a multiple of 32 (got {tuple(codes.shape)})")
-    return codes.shape[:-2], codes.shape[-2], codes.shape[-1] * 2
+@functools.lru_cache(maxsize=1024)
+def _fp4_sizes(shape: tuple, of_codes: bool):
+    """From the shape of values or of codes: matrices, rows, columns and the shapes of
+    codes, scales and values; None for one that is neither's.  (Cached: a call from Python
+    takes longer than its kernel where there are few rows.)"""
+    if len(shape) < 2 or shape[-1] % (16 if of_codes else 32):
+        return None
+    *lead, rows, cols = shape
+    if of_codes:
+        cols *= 2
+    return math.prod(lead), rows, cols, (*lead, rows, cols // 2), (*lead, *_fp4_tiles(rows, cols)), (*lead, rows, cols)
 
 
 def moe_quantize_fp4_block(src: torch.Tensor, out=None, stream=None):
@@ -458,20 +466,20 @@ def moe_quantize_fp4_block(src: torch.Tensor, out=None, stream=None):
     128), ceil(cols / 128), 32, 4, 4].  cols is a multiple of 32."""
     dev = _on_gpu(src, "src")
     dtype = _either(src, "src")
-    if src.dim() < 2 or src.shape[-1] % 32 or src.shape[-1] == 0:
+    sizes = _fp4_sizes(src.shape, False)
+    if sizes is None or sizes[2] == 0:
         raise ValueError(f"src must be [..., rows, cols] with cols a positive multiple of 32 (got {tuple(src.shape)})")
-    rows, cols = src.shape[-2:]
-    lead = src.shape[:-2]
-    shape = (*lead, rows, cols // 2)
-    tiles = (*lead, *_fp4_tiles(rows, cols))
+    batch, rows, cols, shape, tiles, _ = sizes
     if out is None:
         codes, scales = torch.empty(shape, dtype=torch.uint8, device=dev), torch.empty(tiles, dtype=torch.uint8, device=dev)
         places = codes.data_ptr() or None, scales.data_ptr() or None
     else:
         codes, scales = out
         places = _need(codes, "codes", torch.uint8, shape, dev), _need(scales, "scales", torch.uint8, tiles, dev)
-    _check(N.lib.moe_quantize_fp4_block(_need(src, "src", src.dtype, src.shape, dev), dtype, lead.numel() if lead else 1, rows,
-                                        cols, *places, _raw_stream(stream, dev)), "moe_quantize_fp4_block")
+    if not src.is_contiguous():
+        raise ValueError("src must be contiguous")
+    _check(N.lib.moe_quantize_fp4_block(src.data_ptr() or None, dtype, batch, rows, cols, *places, _raw_stream(stream, dev)),
+           "moe_quantize_fp4_block")
     _used_on(stream, codes, scales)
     return codes, scales
 
@@ -481,18 +489,20 @@ def moe_dequantize_fp4_block(codes: torch.Tensor, scales: torch.Tensor, dtype=to
     """What codes and scales of moe_quantize_fp4_block stand for: [..., rows, cols],
     bf16 or fp32, exact in both."""
     dev = _on_gpu(codes, "codes")
-    lead, rows, cols = _fp4_matrix(codes, "codes")
+    sizes = _fp4_sizes(codes.shape, True)
+    if sizes is None:
+        raise ValueError(f"codes must be [..., rows, cols / 2] with cols a multiple of 32 (got {tuple(codes.shape)})")
+    batch, rows, cols, shape, tiles, values = sizes
     if dtype not in _DTYPES:
         raise TypeError(f"dtype must be bfloat16 or float32 (got {dtype})")
     if out is None:
-        out = torch.empty(*lead, rows, cols, dtype=dtype, device=dev)
+        out = torch.empty(values, dtype=dtype, device=dev)
         place = out.data_ptr() or None
     else:
-        place = _need(out, "out", dtype, (*lead, rows, cols), dev)
-    _check(N.lib.moe_dequantize_fp4_block(_need(codes, "codes", torch.uint8, codes.shape, dev),
-                                          _need(scales, "scales", torch.uint8, (*lead, *_fp4_tiles(rows, cols)), dev),
-                                          lead.numel() if lead else 1, rows, cols, _DTYPES[dtype], place,
-                                          _raw_stream(stream, dev)), "moe_dequantize_fp4_block")
+        place = _need(out, "out", dtype, values, dev)
+    _check(N.lib.moe_dequantize_fp4_block(_need(codes, "codes", torch.uint8, shape, dev), _need(scales, "scales", torch.uint8, tiles, dev),
+                                          batch, rows, cols, _DTYPES[dtype], place, _raw_stream(stream, dev)),
+           "moe_dequantize_fp4_block")
     _used_on(stream, out)
     return out
 
