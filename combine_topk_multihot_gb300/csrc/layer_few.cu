@@ -5,7 +5,8 @@
 //   out = sum_k w_k (h_k W2[e_k]^T)
 //
 // With so few rows the layer is a stream over the active experts' weights, read
-// once: 3 H I numbers each.  The first launch makes the logits, a CTA an expert.
+// once: 3 H I numbers each.  The first launch makes the logits, a CTA an expert and a
+// token.
 // The second is one persistent cooperative kernel, a CTA an SM, that has one
 // grid barrier, between h and the second product:
 //   * every CTA picks the experts itself (T K values), so that the weights can be
@@ -23,9 +24,9 @@
 //     shared memory in a fixed order.  A token's column is computed for
 //     every expert and used for its own.
 // What bounds it, at H = 2048, I = 768 and 8 of E = 128 experts a token: HBM for 8
-// tokens in bf16 (89 us, 70.6 of them the bytes of 51 experts); for the codes (e4m3 57.4,
-// bytes 35.4; e2m1 46.3, bytes 18.8) the instructions that make f16 numbers of them, 250
-// for a piece; for one token (23.3, 18.7 and 15.1) the way from launch to launch: the logits
+// tokens in bf16 (85 us, 70.6 of them the bytes of 51 experts); for the codes (e4m3 54,
+// bytes 35.4; e2m1 43.6, bytes 18.8) the instructions that make f16 numbers of them, 250
+// for a piece; for one token (22.1, 17.7 and 14.4) the way from launch to launch: the logits
 // 2 us, the list of experts 3, both products' first bytes, the meeting 1.5 to 2, h 1.5.
 //
 // Tried and slower: a ring of TMA boxes shared by all warps and filled by one (8 tokens: 167 us
@@ -151,23 +152,27 @@ __device__ __forceinline__ void mma_bf16_16x8x16(float (&d)[4], uint32_t a0, uin
 }
 
 // ---------------------------------------------------------------- logits
-// A CTA an expert: its row of the router against every token, in fp32.  The
-// first CTA also clears the other kernel's barrier.
-constexpr int LOGIT_THREADS = 128;
+// A CTA an expert and a token: their rows' product in fp32.  The first CTA also
+// clears the other kernel's barrier.  The latency of its loads bounds it, so that
+// all are on their way at once (H = 2048; longer rows in a few steps): an expert's 8
+// tokens in one CTA of 128 threads, which read the router's rows once, took 3 to 4 us more
+// with 128 experts; with 1024, where the rows come from L2 eight times, 2 us less.
+constexpr int LOGIT_THREADS = 256;
 template <bool F32>
 __global__ void __launch_bounds__(LOGIT_THREADS) few_logits_kernel(const uint16_t* __restrict__ x, const void* __restrict__ router,
-                                                                   int T, int E, int H, float* __restrict__ logits,
+                                                                   int E, int H, float* __restrict__ logits,
                                                                    unsigned* __restrict__ barrier) {
-  __shared__ float s_sum[LOGIT_THREADS / 32][TOK];
+  __shared__ float s_sum[LOGIT_THREADS / 32];
   griddep_launch_dependents();
-  const int e = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (logits)  // (only a hint, so it may come before the wait for earlier kernels)
+  const int e = blockIdx.x, t = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (logits && t == 0)  // (only a hint, so it may come before the wait for earlier kernels)
     for (int k = threadIdx.x * 128; k < H * (F32 ? 4 : 2); k += LOGIT_THREADS * 128)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint8_t*>(router) + static_cast<long long>(e) * H * (F32 ? 4 : 2) + k));
   griddep_wait();
-  if (e == 0 && threadIdx.x == 0) *barrier = 0u;
+  if (e == 0 && t == 0 && threadIdx.x == 0) *barrier = 0u;
   if (logits == nullptr) return;
-  float acc[TOK] = {};
+  float acc = 0.f;
+#pragma unroll 4
   for (int k = threadIdx.x * 8; k < H; k += LOGIT_THREADS * 8) {
     float r[8];
     if constexpr (F32) {
@@ -180,29 +185,20 @@ __global__ void __launch_bounds__(LOGIT_THREADS) few_logits_kernel(const uint16_
 #pragma unroll
       for (int i = 0; i < 4; ++i) r[2 * i] = bf16_lo(w[i]), r[2 * i + 1] = bf16_hi(w[i]);
     }
+    const uint4 q = __ldg(reinterpret_cast<const uint4*>(x + static_cast<long long>(t) * H + k));
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-    for (int t = 0; t < TOK; ++t) {
-      if (t < T) {
-        const uint4 q = __ldg(reinterpret_cast<const uint4*>(x + static_cast<long long>(t) * H + k));
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[t] = fmaf(bf16_hi(w[i]), r[2 * i + 1], fmaf(bf16_lo(w[i]), r[2 * i], acc[t]));
-      }
-    }
+    for (int i = 0; i < 4; ++i) acc = fmaf(bf16_hi(w[i]), r[2 * i + 1], fmaf(bf16_lo(w[i]), r[2 * i], acc));
   }
 #pragma unroll
-  for (int t = 0; t < TOK; ++t) {
-    if (t >= T) break;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(FULL_MASK, acc[t], o);
-    if (lane == 0) s_sum[warp][t] = acc[t];
-  }
+  for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(FULL_MASK, acc, o);
+  if (lane == 0) s_sum[warp] = acc;
   __syncthreads();
-  if (threadIdx.x < T) {
+  if (threadIdx.x == 0) {
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < LOGIT_THREADS / 32; ++w) v += s_sum[w][threadIdx.x];
-    logits[static_cast<long long>(threadIdx.x) * E + e] = v;
+    for (int w = 0; w < LOGIT_THREADS / 32; ++w) v += s_sum[w];
+    logits[static_cast<long long>(t) * E + e] = v;
   }
 }
 
@@ -884,7 +880,7 @@ cudaError_t launch(FewArgs g, const void* router, bool router_f32, float* logits
   size_t smem = 0;
   if (!plan<FMT>(g, &smem)) return cudaErrorInvalidValue;
   auto first = router_f32 ? few_logits_kernel<true> : few_logits_kernel<false>;
-  cudaError_t err = launch_dependent(first, router ? g.E : 1, LOGIT_THREADS, 0, s, g.x, router, g.T, g.E, g.H,
+  cudaError_t err = launch_dependent(first, router ? dim3(g.E, g.T) : dim3(1), LOGIT_THREADS, 0, s, g.x, router, g.E, g.H,
                                      router ? logits : static_cast<float*>(nullptr), g.barrier);
   if (err != cudaSuccess) return err;
   g.logits = router ? logits : nullptr;
