@@ -6,9 +6,8 @@
 //
 // With so few rows the layer is a stream over the active experts' weights, read
 // once: 3 H I numbers each.  The first launch makes the logits, a CTA an expert and a
-// token.
-// The second is one persistent cooperative kernel, a CTA an SM, that has one
-// grid barrier, between h and the second product:
+// token.  The second is one persistent cooperative kernel, a CTA an SM, that has
+// one grid barrier, between h and the second product:
 //   * every CTA picks the experts itself (T K values), so that the weights can be
 //     asked for without another launch or barrier;
 //   * the active experts' h columns are numbered through and cut into equal runs,
@@ -25,8 +24,8 @@
 //     every expert and used for its own.
 // What bounds it, at H = 2048, I = 768 and 8 of E = 128 experts a token: HBM for 8
 // tokens in bf16 (85 us, 70.6 of them the bytes of 51 experts); for the codes (e4m3 54,
-// bytes 35.4; e2m1 43.6, bytes 18.8) the instructions that make f16 numbers of them, 250
-// for a piece; for one token (22.1, 17.7 and 14.4) the way from launch to launch: the logits
+// bytes 35.4; e2m1 43.5, bytes 18.8) the instructions that make f16 numbers of them, 250
+// for a piece; for one token (22.2, 17.7 and 14.0) the way from launch to launch: the logits
 // 2 us, the list of experts 3, both products' first bytes, the meeting 1.5 to 2, h 1.5.
 //
 // Tried and slower: a ring of TMA boxes shared by all warps and filled by one (8 tokens: 167 us
@@ -682,18 +681,6 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
   const uint32_t slots = smem_u32(smem) + warp * args.slots * SLOT;
   Cursor<FMT> cursor(args, s, active, warp, lane, first_a, first_j, my_cols, r0, r1 - r0);
   for (int i = 0; i < args.slots; ++i) cursor.issue(slots + i * SLOT);
-  int at = -1;  // this slot's expert's place (of an expert that a token names twice the last slot counts)
-  if (warp < T) {
-    if (args.logits) prob = softmax_of(prob, K, lane);
-    if (lane < K && blockIdx.x == 0 && args.idx_out) {
-      args.idx_out[warp * K + lane] = chosen;
-      args.probs_out[warp * K + lane] = prob;
-    }
-    const int word = max(chosen, 0) >> 5;
-    const uint32_t same = __match_any_sync(FULL_MASK, chosen), there = __shfl_sync(FULL_MASK, bits, word);
-    const int before = __shfl_sync(FULL_MASK, upto, word) - __popc(there);
-    if (chosen >= 0 && lane == 31 - __clz(same)) at = before + __popc(there & ((1u << (chosen & 31)) - 1u));
-  }
   if (warp == TOK) {  // the experts' rows of h
     int row = 0;
     for (int a0 = 0; a0 < active; a0 += 32) {
@@ -716,7 +703,6 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
     if (lane == 0) s.first[active] = row;
   }
   __syncthreads();
-  if (at >= 0) s.weight[s.row[at][warp]] = prob;  // read after the meeting
   int slot = 0;
   auto next = [&](auto sum, float (&d)[4], int st, int bytes, uint32_t token) {
     cp_async_wait(args.slots - 1);
@@ -775,7 +761,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
   // h is whole once every CTA has been here
   __threadfence();
   __syncthreads();
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 32 * TOK) {
     int met = 1;
     if (static_cast<int>(blockIdx.x) < args.ctas) atomicAdd(args.barrier, 1u);
     const unsigned long long t0 = global_timer_ns();
@@ -787,6 +773,18 @@ __global__ void __launch_bounds__(THREADS, 1) few_layer_kernel(const FewArgs arg
     }
     __threadfence();
     s.ok = met;
+  }
+  // meanwhile, the weights of the rows of h (of an expert that a token names twice the last slot counts)
+  if (warp < T) {
+    if (args.logits) prob = softmax_of(prob, K, lane);
+    if (lane < K && blockIdx.x == 0 && args.idx_out) {
+      args.idx_out[warp * K + lane] = chosen;
+      args.probs_out[warp * K + lane] = prob;
+    }
+    const int word = max(chosen, 0) >> 5;
+    const uint32_t same = __match_any_sync(FULL_MASK, chosen), there = __shfl_sync(FULL_MASK, bits, word);
+    const int before = __shfl_sync(FULL_MASK, upto, word) - __popc(there);
+    if (chosen >= 0 && lane == 31 - __clz(same)) s.weight[s.row[before + __popc(there & ((1u << (chosen & 31)) - 1u))][warp]] = prob;
   }
   __syncthreads();
   if (!s.ok) {  // the wait ran out: this CTA's rows are no result
