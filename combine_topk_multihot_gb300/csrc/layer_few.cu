@@ -366,11 +366,14 @@ __device__ __forceinline__ void stage_h(const FewArgs& args, int r0, int rows, i
         }
         *reinterpret_cast<uint4*>(to + 512 * j + 2 * args.I) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       } else {
-        const float down = __uint_as_float((127u - min(top - e[n][j], 126u)) << 23);
-        const __half2 scale = __float2half2_rn(down);  // 0 below f16's least
+        // 2^-24 is the least f16: what is further below the row's largest goes down in two steps
+        const uint32_t down = top - e[n][j];
+        const __half2 scale = __float2half2_rn(__uint_as_float((127u - min(down, 24u)) << 23));
+        const __half2 rest = __float2half2_rn(__uint_as_float((127u - min(max(down, 24u) - 24u, 24u)) << 23));
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const __half2 f = __hmul2(*reinterpret_cast<const __half2*>(&w[k]), scale);
+          __half2 f = __hmul2(*reinterpret_cast<const __half2*>(&w[k]), scale);
+          if (down > 24u) f = __hmul2(f, rest);
           hi[k] = *reinterpret_cast<const uint32_t*>(&f);
         }
       }

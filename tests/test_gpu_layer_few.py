@@ -399,3 +399,33 @@ def test_a_product_whose_operands_stop(moe, M, N, K, tiles):
     assert missing.all() if tiles == 0 else missing.any() and not missing.all()
     assert torch.equal(out[~missing], whole[~missing]) and int(status) == moe._native.MOE_DEVERR_TIMEOUT
     assert torch.equal(moe.moe_matmul_fp4_block(*a, *b), whole)
+
+
+@gpu
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("apart", [16, 26, 27])
+def test_columns_of_h_far_below_others(moe, fmt, apart):
+    """Columns of h around 2^apart below others of their row, which W2 multiplies by zero: with codes they
+    still are exact down to 2^-28 of the row's largest, and never off by more than 2^-38 of it."""
+    T, H, E, K, I = 3, 256, 2, 1, 256
+    g = torch.Generator(device=DEV).manual_seed(apart)
+    rnd = lambda *s, std=1.0: torch.randn(*s, generator=g, device=DEV) * std  # noqa: E731
+    x, W1, W2 = rnd(T, H).bfloat16(), rnd(E, 2 * I, H, std=H ** -0.5), rnd(E, H, I, std=I ** -0.5)
+    W1[:, I:I + 128] *= 2.0 ** apart     # up rows of the first 128 columns
+    W2[:, :, :128] = 0
+    W1, W2, S1, S2 = W1.bfloat16(), W2.bfloat16(), None, None
+    V1, V2 = W1.double(), W2.double()
+    if fmt != "bf16":
+        quantize = (lambda w: moe.moe_quantize_fp8_block(w, 128)) if fmt == "fp8" else moe.moe_quantize_fp4_block
+        (W1, S1), (W2, S2) = quantize(W1), quantize(W2)
+        if fmt == "fp8":
+            V1, V2 = (q.view(torch.float8_e4m3fn).double() * s.double().repeat_interleave(128, 1).repeat_interleave(128, 2)
+                      for q, s in ((W1, S1), (W2, S2)))
+        else:
+            V1, V2 = (moe.moe_dequantize_fp4_block(q, s, torch.float32).double() for q, s in ((W1, S1), (W2, S2)))
+    idx, p = torch.tensor([[0], [1], [0]], device=DEV), torch.ones(T, K, device=DEV)
+    out = moe.moe_layer_few(x, None, K, W1, W2, S1, S2, routing=(idx, p))
+    ref, lim = reference(x, idx, p, V1, V2, fmt != "bf16")
+    err = (out.double() - ref).abs()
+    assert (err <= lim).all(), float((err / lim).max())
+    assert float(lim.norm() / ref.norm()) < 0.25       # (columns that were lost would show)
