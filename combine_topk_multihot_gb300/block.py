@@ -441,6 +441,9 @@ def moe_grouped_experts_fp8_block(x_disp: torch.Tensor, layout: Layout, W1_q: to
 
 
 # ------------------------------------------------------------------ e2m1 with a scale per 32
+_INT32 = 2 ** 31 - 1  # sizes cross to the library in 32 bits
+
+
 def _fp4_tiles(rows: int, cols: int):
     """The last five sizes of a matrix's scales: tiles of 128 rows and 4 blocks of 32."""
     return (rows + 127) // 128, (cols + 127) // 128, 32, 4, 4
@@ -449,13 +452,15 @@ def _fp4_tiles(rows: int, cols: int):
 @functools.lru_cache(maxsize=1024)
 def _fp4_sizes(shape: tuple, of_codes: bool):
     """From the shape of values or of codes: matrices, rows, columns and the shapes of
-    codes, scales and values; None for one that is neither's.  (Cached: a call from Python
+    codes, scales and values; None for one that is neither's or that no kernel takes.  (Cached: a call from Python
     takes longer than its kernel where there are few rows.)"""
     if len(shape) < 2 or shape[-1] % (16 if of_codes else 32):
         return None
     *lead, rows, cols = shape
     if of_codes:
         cols *= 2
+    if cols > _INT32:
+        return None
     return math.prod(lead), rows, cols, (*lead, rows, cols // 2), (*lead, *_fp4_tiles(rows, cols)), (*lead, rows, cols)
 
 
@@ -468,7 +473,7 @@ def moe_quantize_fp4_block(src: torch.Tensor, out=None, stream=None):
     dtype = _either(src, "src")
     sizes = _fp4_sizes(src.shape, False)
     if sizes is None or sizes[2] == 0:
-        raise ValueError(f"src must be [..., rows, cols] with cols a positive multiple of 32 (got {tuple(src.shape)})")
+        raise ValueError(f"src must be [..., rows, cols] with cols a positive multiple of 32 below 2^31 (got {tuple(src.shape)})")
     batch, rows, cols, shape, tiles, _ = sizes
     if out is None:
         codes, scales = torch.empty(shape, dtype=torch.uint8, device=dev), torch.empty(tiles, dtype=torch.uint8, device=dev)
@@ -491,7 +496,7 @@ def moe_dequantize_fp4_block(codes: torch.Tensor, scales: torch.Tensor, dtype=to
     dev = _on_gpu(codes, "codes")
     sizes = _fp4_sizes(codes.shape, True)
     if sizes is None:
-        raise ValueError(f"codes must be [..., rows, cols / 2] with cols a multiple of 32 (got {tuple(codes.shape)})")
+        raise ValueError(f"codes must be [..., rows, cols / 2] with cols a multiple of 32 below 2^31 (got {tuple(codes.shape)})")
     batch, rows, cols, shape, tiles, values = sizes
     if dtype not in _DTYPES:
         raise TypeError(f"dtype must be bfloat16 or float32 (got {dtype})")
@@ -513,6 +518,8 @@ def moe_matmul_fp4_block(a_q: torch.Tensor, a_scale: torch.Tensor, b_q: torch.Te
     dev = _on_gpu(a_q, "a_q")
     M, half = _rows(a_q, "a_q")
     n = _rows(b_q, "b_q")[0]
+    if max(M, n, 2 * half) > _INT32:
+        raise ValueError(f"sizes must be below 2^31 (got M={M}, N={n}, K={2 * half})")
     if out is None:
         out = torch.empty(M, n, dtype=torch.bfloat16, device=dev)
         place = out.data_ptr() or None

@@ -1048,8 +1048,9 @@ moe_status moe_dequantize_fp4_block(const uint8_t* codes, const uint8_t* scales,
 moe_status moe_matmul_fp4_block(const uint8_t* a_q, const uint8_t* a_scale, int32_t M, const uint8_t* b_q, const uint8_t* b_scale,
                                 int32_t N, int32_t K, moe_bf16* out, int32_t* status, moe_stream_t stream) {
   MOE_REQUIRE(M >= 0 && N >= 1, MOE_ERR_INVALID_ARG, "moe_matmul_fp4_block: M must be >= 0 and N >= 1 (got %d, %d)", M, N);
-  MOE_REQUIRE(K >= 32 && K % 32 == 0, MOE_ERR_UNSUPPORTED_SHAPE,
-              "moe_matmul_fp4_block: K must be a positive multiple of 32 (got %d)", K);
+  // (a tile's 2^21 steps of K take less than the limit of a wait, and no count of them passes 32 bits)
+  MOE_REQUIRE(K >= 32 && K % 32 == 0 && K <= 1 << 29, MOE_ERR_UNSUPPORTED_SHAPE,
+              "moe_matmul_fp4_block: K must be a positive multiple of 32 up to 2^29 (got %d)", K);
   MOE_REQUIRE(M == 0 || (a_q && a_scale && b_q && b_scale && out), MOE_ERR_INVALID_ARG, "moe_matmul_fp4_block: NULL pointer");
   MOE_REQUIRE(all_aligned(16, a_q, a_scale, b_q, b_scale) && aligned_to(out, N % 8 == 0 ? 16 : 2) && aligned_to(status, 4),
               MOE_ERR_INVALID_ARG,

@@ -750,7 +750,7 @@ MOE_API moe_status moe_dequantize_fp4_block(const uint8_t* codes, const uint8_t*
  *   bf16 (out); status [1] int32 device status word (nullable), receives
  *   MOE_DEVERR_TIMEOUT if a bounded wait runs out; the elements that are not
  *   reached then are NaN.
- * M >= 0, N >= 1, K a positive multiple of 32.  Codes and scales are 16-byte
+ * M >= 0, N >= 1, K a positive multiple of 32 up to 2^29.  Codes and scales are 16-byte
  * aligned, and so is out when N is a multiple of 8.  Scales past the last row or
  * block of a matrix must not be 255 (the quantiser writes zeros there).  Up to 8
  * rows by up to 1024 stream the weights through registers; others run on the

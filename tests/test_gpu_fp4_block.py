@@ -250,3 +250,24 @@ def test_on_another_stream_and_captured(moe):
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(g, -2 * w) for g, w in zip(held, want))
+
+
+def test_sizes_past_32_bits_are_refused_without_a_gpu(moe, monkeypatch):
+    """K of 2^31 - 32, which rounded up passes 32 bits, and sizes that would cross to the library without their upper bits."""
+    import ctypes
+    from combine_topk_multihot_gb300 import _native as N, block
+    p = ctypes.c_void_p(256)
+    for K in (2 ** 29 + 32, 2 ** 30, 2 ** 31 - 256, 2 ** 31 - 32):
+        for M in (1, 9, 300):
+            assert N.lib.moe_matmul_fp4_block(p, p, M, p, p, 8, K, p, None, None) == N.MOE_ERR_UNSUPPORTED_SHAPE
+            assert b"2^29" in N.lib.moe_last_error()
+    monkeypatch.setattr(block, "_on_gpu", lambda t, name: t.device)
+    big = lambda *s, dt=torch.uint8: torch.empty(*s, dtype=dt, device="meta")  # noqa: E731
+    with pytest.raises(ValueError, match="below 2\\^31"):
+        moe.moe_quantize_fp4_block(big(1, 2 ** 32 + 32, dt=torch.bfloat16))
+    with pytest.raises(ValueError, match="below 2\\^31"):
+        moe.moe_dequantize_fp4_block(big(1, 2 ** 31 + 16), big(1, 2 ** 25 + 1, 32, 4, 4))
+    small, scales = big(8, 16), big(1, 1, 32, 4, 4)
+    for a, b in ((big(1, 2 ** 31 + 16), small), (big(2 ** 32 + 1, 16), small), (small, big(2 ** 32 + 1, 16))):
+        with pytest.raises(ValueError, match="below 2\\^31"):
+            moe.moe_matmul_fp4_block(a, scales, b, scales)
