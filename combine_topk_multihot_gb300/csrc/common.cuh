@@ -121,6 +121,24 @@ __device__ __forceinline__ bool mbar_wait_drain(uint32_t bar, uint32_t parity) {
   return true;
 }
 
+// The same for a CTA that works on meanwhile and counts what it has done: the limit
+// starts again with every change of `done` that it finds, so that it bounds a
+// standstill and not the work.
+__device__ __forceinline__ bool mbar_wait_working(uint32_t bar, uint32_t parity, const volatile uint32_t* done,
+                                                  unsigned long long limit_ns) {
+  unsigned long long t0 = global_timer_ns();
+  uint32_t seen = *done;
+  while (!mbar_try_wait(bar, parity)) {
+    if (global_timer_ns() - t0 > limit_ns) {
+      const uint32_t now = *done;
+      if (now == seen) return false;
+      seen = now;
+      t0 = global_timer_ns();
+    }
+  }
+  return true;
+}
+
 // ---------------------------------------------------------------- cp.async
 // 16-byte global -> shared copy; bytes past src_bytes (0 or 16) are zero-filled
 // and not read.

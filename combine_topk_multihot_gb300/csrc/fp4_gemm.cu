@@ -71,6 +71,7 @@ struct Smem {
   uint64_t drain[2];
   uint32_t tmem_base;
   int abort;
+  uint32_t issued;    // of the odd CTA's stages
 };
 
 template <int BN, bool PAIR>
@@ -86,6 +87,7 @@ struct Args {
   int out_staged;
   int* status;
   int load_tiles;  // tiles a CTA loads operands for: all, but in the self-test
+  unsigned long long pair_wait_ns;
 };
 
 // Loads whose arrival is counted on this CTA's barrier, or on the even CTA's.
@@ -189,6 +191,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&s.drain[i]), 1);
     s.abort = 0;
+    s.issued = 0;
     mbar_fence_init();
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
@@ -227,6 +230,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (elect_one()) {  // (what lies past a matrix arrives as zeros)
           if (warp == 0) {
             if (rank == 0) mbar_arrive_expect_tx(full, CTAS * S::STAGE_BYTES);
+            else *const_cast<volatile uint32_t*>(&s.issued) = static_cast<uint32_t>(issued) + 1;
             load<PAIR>(a_dst, &tmA, ks * 128, row_tile * BM, full0);
             load<PAIR>(sf, &tmSA, ks * 256, row_tile, full0);
           } else {
@@ -247,8 +251,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   } else if (warp < 3 && rank != 0) {
     // the odd CTA issues nothing; it waits until the even CTA's last operations,
-    // which write its tensor memory, have finished
-    if (!mbar_wait_drain(smem_u32(&s.drain[warp - 1]), 0)) *abort_flag = 1;
+    // which write its tensor memory, have finished: as long as its own loads go on
+    if (!mbar_wait_working(smem_u32(&s.drain[warp - 1]), 0, &s.issued, args.pair_wait_ns)) *abort_flag = 1;
   } else if (warp == 2) {
     // ================= scales to tensor memory =================
     int stage = 0;
@@ -473,6 +477,7 @@ cudaError_t launch_fp4_matmul_tc(const uint8_t* a, const uint8_t* a_scale, int M
   g.out_staged = N % 8 == 0;
   g.status = status;
   g.load_tiles = block_load_tiles();
+  g.pair_wait_ns = pair_wait_ns();
   const bool pair = M > BM;
   const long long mt = pair ? (static_cast<long long>(M) + 2 * BM - 1) / (2 * BM) : 1;
   const int at_once = pair ? sm_count() / 2 : sm_count();

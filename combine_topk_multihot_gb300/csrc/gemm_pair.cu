@@ -104,6 +104,7 @@ struct PairArgs {
   int* ready;              // per row chunk: h-ready signals (NULL: the down launch waits for the whole gate/up launch)
   unsigned int* done;      // the down launch's finished CTAs; the last one clears `ready`
   int ready_target;        // signals that make a chunk ready: gate/up tiles per chunk x 16 epilogue warps
+  unsigned long long pair_wait_ns;
 };
 
 // Barriers and scalars; the per-expert tables (offsets [E+1], counts [E],
@@ -118,6 +119,7 @@ struct Smem {
   int abort;
   int total_tiles;
   int last;  // the down launch's last CTA (it clears the readiness counters)
+  uint32_t tiles_begun;  // by the odd CTA's loads
 };
 
 constexpr size_t smem_bytes(int stages, int E) {
@@ -342,6 +344,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     mbar_init(smem_u32(&s.drain), 1);
     s.abort = 0;
+    s.tiles_begun = 0;
     mbar_fence_init();
     tma_prefetch_desc(&tmW);
     tma_prefetch_desc(&tmR32);
@@ -424,6 +427,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (!wait_ready(args.ready + t.chunk, args.ready_target, abort_flag)) { ok = false; break; }
           fence_proxy_async_global();
         }
+        if (rank != 0) *const_cast<volatile uint32_t*>(&s.tiles_begun) += 1;
         // this CTA loads t.n / 2 expert rows (a multiple of 8): rows t.row0 + rank * t.n / 2 on
         ok = load_tile_n<EPI, STAGES>(&tmW, rm, t, rank, tiles_u32, s, args.k_blocks, args.w_rows_per_expert,
                                       stage, phase, issued, abort_flag, tile == tile0 ? pre : 0);
@@ -441,8 +445,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // ================= MMA issuer (the even CTA) =================
     if (lane == 0 && rank != 0) {
       // the odd CTA issues nothing; it waits until the even CTA's last MMAs,
-      // which write its tensor memory, have completed
-      if (!mbar_wait_drain(smem_u32(&s.drain), 0)) *abort_flag = 1;
+      // which write its tensor memory, have completed: as long as its own loads go on
+      if (!mbar_wait_working(smem_u32(&s.drain), 0, &s.tiles_begun, args.pair_wait_ns)) *abort_flag = 1;
     } else if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
@@ -816,6 +820,7 @@ cudaError_t launch_experts_forward_pair(const uint16_t* x_disp, const moe_layout
   g1.I = I;
   g1.write_pad = gu_save != nullptr;  // training: the backward reads the pad rows
   g1.status = L.status;
+  g1.pair_wait_ns = pair_wait_ns();
   // readiness counters when the layer's row chunks fit a slot (at most one
   // chunk per expert more than its rows / 256)
   const long long rows_bound = static_cast<long long>(L.T) * L.K +

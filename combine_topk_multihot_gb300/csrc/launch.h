@@ -273,6 +273,9 @@ cudaError_t launch_block_experts_tc(const uint8_t* x_q, const float* x_scale, co
 void selftest_block_load_tiles(int tiles);
 int block_load_tiles();
 void selftest_few_ctas(int ctas);
+// How long the odd CTA of a pair may stand still before it gives up: the limit of
+// every wait, but in the self-test.
+unsigned long long pair_wait_ns();
 void selftest_norm_load_rows(long long rows);
 long long norm_load_rows(long long T);
 

@@ -31,7 +31,11 @@ __global__ void wait_timeout_kernel(int* status, unsigned long long limit_ns,
   }
 }
 
+thread_local unsigned long long tls_pair_wait_ns = WAIT_LIMIT_NS;
+
 }  // namespace
+
+unsigned long long pair_wait_ns() { return tls_pair_wait_ns; }
 
 }  // namespace moe
 
@@ -48,6 +52,13 @@ extern "C" moe_status moe_selftest_wait_timeout(int32_t* status, int64_t limit_n
                                             reinterpret_cast<unsigned long long*>(waited_ns));
   const cudaError_t err = cudaGetLastError();
   if (err != cudaSuccess) return set_last_error(MOE_ERR_CUDA, cudaGetErrorString(err));
+  return MOE_OK;
+}
+
+extern "C" moe_status moe_selftest_pair_wait(int64_t limit_ns) {
+  if (limit_ns < -1 || limit_ns == 0 || limit_ns > static_cast<int64_t>(WAIT_LIMIT_NS))
+    return set_last_error(MOE_ERR_INVALID_ARG, "moe_selftest_pair_wait: needs 0 < limit_ns <= 2e9, or -1 for the usual limit");
+  tls_pair_wait_ns = limit_ns < 0 ? WAIT_LIMIT_NS : static_cast<unsigned long long>(limit_ns);
   return MOE_OK;
 }
 

@@ -851,6 +851,15 @@ MOE_API moe_status moe_selftest_norm_rows(int64_t rows);
  * the two products. */
 MOE_API moe_status moe_selftest_few_ctas(int32_t ctas);
 
+/*
+ * Self-test of products that take longer than the limit of a wait (2 s): until it is
+ * called again with -1, the odd CTA of a pair (moe_matmul_fp4_block above 128 rows,
+ * moe_grouped_experts and its backward with CTA pairs), in the calling host thread's
+ * launches, gives up after limit_ns (0 < limit_ns <= 2e9) in which its loads stand
+ * still.  A product that goes on, for however long, is whole.
+ */
+MOE_API moe_status moe_selftest_pair_wait(int64_t limit_ns);
+
 #ifdef __cplusplus
 }  /* extern "C" */
 #endif
