@@ -481,10 +481,10 @@ cudaError_t launch_fp4_matmul_tc(const uint8_t* a, const uint8_t* a_scale, int M
   const bool pair = M > BM;
   const long long mt = pair ? (static_cast<long long>(M) + 2 * BM - 1) / (2 * BM) : 1;
   const int at_once = pair ? sm_count() / 2 : sm_count();
-  // The width with the shortest rounds of tiles in all.  In pairs a stage of 64, 128,
-  // 192 or 256 columns takes about 240, 240, 270 and 305 ns and a tile 0.3, 0.3, 0.45
-  // and 1.0 us more (8192 x 8192 x 4096: 239, 120, 93 and 82 us; 333 x 4096 x
-  // 2048: 7.8, 5.9, 6.1 and 6.5).  A single CTA's tiles are few: the fewest
+  // The width with the shortest rounds of tiles in all.  In pairs a stage of 128, 192
+  // or 256 columns takes about 240, 270 and 305 ns and a tile 0.3, 0.45 and 1.0 us
+  // more (8192 x 8192 x 4096: 120, 93 and 82 us; 333 x 4096 x 2048: 5.9, 6.1 and 6.5;
+  // 64 columns take as long a stage as 128: 239 and 7.8 us).  A single CTA's tiles are few: the fewest
   // rounds, then the narrowest.
   auto rounds = [&](int bn) { return (mt * ((N + bn - 1) / bn) + at_once - 1) / at_once; };
   int bn = 256;
@@ -497,15 +497,13 @@ cudaError_t launch_fp4_matmul_tc(const uint8_t* a, const uint8_t* a_scale, int M
     };
     look(192, 270, 450);
     look(128, 240, 300);
-    look(64, 240, 300);
   } else {
     bn = rounds(64) <= rounds(256) ? 64 : rounds(128) <= rounds(256) ? 128 : 256;
   }
   if (pair)
     return bn == 256   ? launch<256, true>(a, a_scale, b, b_scale, g, s)
            : bn == 192 ? launch<192, true>(a, a_scale, b, b_scale, g, s)
-           : bn == 128 ? launch<128, true>(a, a_scale, b, b_scale, g, s)
-                       : launch<64, true>(a, a_scale, b, b_scale, g, s);
+                       : launch<128, true>(a, a_scale, b, b_scale, g, s);
   return bn == 256   ? launch<256, false>(a, a_scale, b, b_scale, g, s)
          : bn == 128 ? launch<128, false>(a, a_scale, b, b_scale, g, s)
                      : launch<64, false>(a, a_scale, b, b_scale, g, s);
