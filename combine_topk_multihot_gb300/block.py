@@ -545,6 +545,10 @@ def moe_fp4_scale_tiles(scales: torch.Tensor) -> torch.Tensor:
 
 def moe_fp4_scale_rows(tiles: torch.Tensor, rows: int, cols: int) -> torch.Tensor:
     """The way back from moe_fp4_scale_tiles: [..., rows, cols / 32]."""
+    if tiles.dim() < 5 or tiles.shape[-3:] != (32, 4, 4):
+        raise ValueError(f"tiles must be [..., row tiles, block tiles, 32, 4, 4] (got {tuple(tiles.shape)})")
+    if not 0 <= rows <= 128 * tiles.shape[-5] or cols % 32 or not 0 <= cols <= 128 * tiles.shape[-4]:
+        raise ValueError(f"tiles {tuple(tiles.shape)} hold no {rows} rows of {cols} columns, a multiple of 32")
     s = tiles.transpose(-3, -2).movedim(-4, -2)
     return s.flatten(-2).flatten(-4, -2)[..., :rows, :cols // 32].contiguous()
 

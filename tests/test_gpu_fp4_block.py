@@ -271,3 +271,14 @@ def test_sizes_past_32_bits_are_refused_without_a_gpu(moe, monkeypatch):
     for a, b in ((big(1, 2 ** 31 + 16), small), (big(2 ** 32 + 1, 16), small), (small, big(2 ** 32 + 1, 16))):
         with pytest.raises(ValueError, match="below 2\\^31"):
             moe.moe_matmul_fp4_block(a, scales, b, scales)
+
+
+def test_scale_rows_that_the_tiles_do_not_hold(moe):
+    t = torch.arange(2 * 512, dtype=torch.int32).to(torch.uint8).view(1, 2, 32, 4, 4)
+    assert moe.moe_fp4_scale_rows(t, 128, 256).shape == (128, 8) and moe.moe_fp4_scale_rows(t, 0, 0).shape == (0, 0)
+    for rows, cols in ((129, 256), (128, 288), (-1, 32), (5, 40), (5, -32)):
+        with pytest.raises(ValueError, match="hold no"):
+            moe.moe_fp4_scale_rows(t, rows, cols)
+    for bad in (t[0, 0], t.view(1, 2, 32, 2, 8), t.view(2, 512)):
+        with pytest.raises(ValueError, match="tiles must be"):
+            moe.moe_fp4_scale_rows(bad, 1, 32)
