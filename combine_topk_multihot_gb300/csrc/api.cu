@@ -527,8 +527,7 @@ moe_status experts_backward_impl(const char* who, const moe_bf16* grad_y, const 
   if ((st = check_hidden(H)) != MOE_OK) return st;
   MOE_REQUIRE(I > 0 && I % 128 == 0, MOE_ERR_UNSUPPORTED_SHAPE,
               "the intermediate size must be a positive multiple of 128 (got %d)", I);
-  MOE_REQUIRE(W1 && W2 && dW1 && dW2 && workspace, MOE_ERR_INVALID_ARG,
-              "%s: NULL weight, weight-gradient or workspace pointer", who);
+  MOE_REQUIRE(W1 && W2 && workspace, MOE_ERR_INVALID_ARG, "%s: NULL weight or workspace pointer", who);
   MOE_REQUIRE(L->capacity == 0 || (grad_y && x_disp && h && gu_save && grad_x_disp),
               MOE_ERR_INVALID_ARG, "%s: NULL row buffer", who);
   MOE_REQUIRE(aligned16(grad_y) && aligned16(x_disp) && aligned16(h) && aligned16(gu_save) &&

@@ -696,7 +696,7 @@ cudaError_t launch_experts_backward(const uint16_t* grad_y, const uint16_t* x_di
   }
 
   // wgrad2: dW2[e] = G_o^T h     (M = H, N = I, K = the expert's rows)
-  {
+  if (dW2) {
     CUtensorMap mA, mB, mA3, mB3, mO;
     const uint64_t rows = C > 0 ? static_cast<uint64_t>(C) : 1;
     const void* a_src = C > 0 ? static_cast<const void*>(g_o) : static_cast<const void*>(dW2);
@@ -719,7 +719,7 @@ cudaError_t launch_experts_backward(const uint16_t* grad_y, const uint16_t* x_di
     if (err != cudaSuccess) return err;
   }
   // wgrad1: dW1[e] = G_gu^T x_disp   (M = 2I, N = H)
-  {
+  if (dW1) {
     CUtensorMap mA, mB, mA3, mB3, mO;
     const uint64_t rows = C > 0 ? static_cast<uint64_t>(C) : 1;
     const void* a_src = C > 0 ? static_cast<const void*>(g_gu) : static_cast<const void*>(dW1);

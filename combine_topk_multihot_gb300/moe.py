@@ -378,9 +378,9 @@ def moe_route_to_multihot_backward(grad_probs: torch.Tensor, topk_idx: torch.Ten
 def moe_grouped_experts_backward(grad_y: torch.Tensor, x_disp: torch.Tensor, h: torch.Tensor,
                                  gu_save: torch.Tensor, layout: Layout, W1: torch.Tensor,
                                  W2: torch.Tensor, stream=None, return_operands: bool = False,
-                                 scaled: bool = False):
-    """a9: returns (grad_x_disp [C, H] bf16, dW1 [E, 2I, H] fp32, dW2 [E, H, I] fp32),
-    plus, with return_operands, views of the workspace's G_o [C, H] and
+                                 scaled: bool = False, weight_grads: bool = True):
+    """a9: returns (grad_x_disp [C, H] bf16, dW1 [E, 2I, H] fp32, dW2 [E, H, I] fp32)
+    (None for both weights' gradients without ``weight_grads``), plus, with return_operands, views of the workspace's G_o [C, H] and
     [G_g | G_u] [C, 2I] (bf16, valid rows).  With ``scaled``
     (moe_grouped_experts_backward_scaled) ``grad_y`` is G_o from
     moe_combine_backward(..., scaled=True), and the G_o returned is ``grad_y``."""
@@ -392,8 +392,8 @@ def moe_grouped_experts_backward(grad_y: torch.Tensor, x_disp: torch.Tensor, h: 
            "moe_experts_backward_workspace_bytes")
     ws = torch.empty(nbytes.value, dtype=torch.uint8, device=dev)
     grad_x_disp = torch.empty(layout.capacity, H, dtype=torch.bfloat16, device=dev)
-    dW1 = torch.empty(E, 2 * I, H, dtype=torch.float32, device=dev)
-    dW2 = torch.empty(E, H, I, dtype=torch.float32, device=dev)
+    dW1 = torch.empty(E, 2 * I, H, dtype=torch.float32, device=dev) if weight_grads else None
+    dW2 = torch.empty(E, H, I, dtype=torch.float32, device=dev) if weight_grads else None
     fn = N.lib.moe_grouped_experts_backward_scaled if scaled else N.lib.moe_grouped_experts_backward
     _check(fn(_ptr(grad_y), _ptr(x_disp), _ptr(h), _ptr(gu_save), layout.ref, H, I, _ptr(W1), _ptr(W2),
               _ptr(grad_x_disp), _ptr(dW1), _ptr(dW2), _ptr(ws), _stream(stream)),

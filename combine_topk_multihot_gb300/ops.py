@@ -208,6 +208,20 @@ def _(g_o, x_disp, h, gu_save, W1, W2, lay, T, top_k, pad_multiple):
             torch.empty(W2.shape, dtype=torch.float32, device=W2.device))
 
 
+@torch.library.custom_op(f"{NS}::experts_backward_rows", mutates_args=(), device_types="cuda")
+def experts_backward_rows(g_o: Tensor, x_disp: Tensor, h: Tensor, gu_save: Tensor, W1: Tensor, W2: Tensor, lay: List[Tensor],
+                          T: int, top_k: int, pad_multiple: int) -> Tensor:
+    """grad_x_disp alone, of weights that get no gradients."""
+    L = _layout(T, W1.shape[0], top_k, pad_multiple, lay)
+    return _m.moe_grouped_experts_backward(g_o, x_disp, h, gu_save, L, W1.contiguous(), W2.contiguous(), scaled=True,
+                                           weight_grads=False)[0]
+
+
+@experts_backward_rows.register_fake
+def _(g_o, x_disp, h, gu_save, W1, W2, lay, T, top_k, pad_multiple):
+    return x_disp.new_empty(x_disp.shape)
+
+
 @torch.library.custom_op(f"{NS}::dispatch_backward", mutates_args=(), device_types="cuda")
 def dispatch_backward(grad_x_disp: Tensor, grad_w: Tensor, lay: List[Tensor], T: int, top_k: int,
                       pad_multiple: int, num_experts: int) -> Tuple[Tensor, Tensor]:
@@ -238,22 +252,28 @@ def _(grad_probs, topk_idx, winner_slot):
 _ops = torch.ops.moe_gb300
 
 
+def _bf16(W: Tensor, scale: Optional[Tensor]) -> Tensor:
+    return W if scale is None else _ops.dequantize_fp4_block(W, scale)
+
+
 class MoELayerFunction(torch.autograd.Function):
     """out = combine(experts(dispatch(x, multihot(topk_idx, topk_probs)), W1, W2)).
 
-    The backward gives gradients for x, topk_probs, W1 and W2.  The kernels
+    The backward gives gradients for x, topk_probs, W1 and W2, and computes those
+    of the weights only where one of them wants its own.  The kernels
     accumulate the weight gradients in fp32; autograd wants them in the
-    weights' own dtype, so they are cast on the way out."""
+    weights' own dtype, so they are cast on the way out.  With scales W1 and W2 are
+    e2m1 codes, kept as such for the backward and turned into bf16 in either direction."""
 
     @staticmethod
-    def forward(ctx, x, topk_idx, topk_probs, W1, W2, pad_multiple: int):
+    def forward(ctx, x, topk_idx, topk_probs, W1, W2, pad_multiple: int, W1_scale, W2_scale):
         T, K = topk_idx.shape
         E = W1.shape[0]
         rmap, probs, win, status = _ops.route_to_multihot(topk_idx, topk_probs, E)
         x_disp, *lay = _ops.dispatch(x, rmap, probs, status, K, pad_multiple)
-        y, h, o, gu = _ops.grouped_experts(x_disp, W1, W2, lay, T, K, pad_multiple, True)
+        y, h, o, gu = _ops.grouped_experts(x_disp, _bf16(W1, W1_scale), _bf16(W2, W2_scale), lay, T, K, pad_multiple, True)
         out = _ops.combine(y, lay, T, K, pad_multiple, E)
-        ctx.save_for_backward(topk_idx, win, x_disp, h, o, gu, W1, W2, *lay)
+        ctx.save_for_backward(topk_idx, win, x_disp, h, o, gu, W1, W2, W1_scale, W2_scale, *lay)
         ctx.meta = (T, K, E, pad_multiple)
         status = lay[-1]
         ctx.mark_non_differentiable(status)
@@ -262,13 +282,20 @@ class MoELayerFunction(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, grad_out, _grad_status):
-        topk_idx, win, x_disp, h, o, gu, W1, W2, *lay = ctx.saved_tensors
+        topk_idx, win, x_disp, h, o, gu, W1, W2, W1_scale, W2_scale, *lay = ctx.saved_tensors
         T, K, E, P = ctx.meta
         g_o, grad_w = _ops.combine_backward(grad_out, o, lay, T, K, P, E)
-        gxd, dW1, dW2 = _ops.experts_backward(g_o, x_disp, h, gu, W1, W2, lay, T, K, P)
+        operands = (g_o, x_disp, h, gu, _bf16(W1, W1_scale), _bf16(W2, W2_scale), lay, T, K, P)
+        dW1 = dW2 = None
+        if ctx.needs_input_grad[3] or ctx.needs_input_grad[4]:
+            gxd, dW1, dW2 = _ops.experts_backward(*operands)
+            dW1 = dW1.to(W1.dtype) if ctx.needs_input_grad[3] else None
+            dW2 = dW2.to(W2.dtype) if ctx.needs_input_grad[4] else None
+        else:
+            gxd = _ops.experts_backward_rows(*operands)
         grad_x, grad_probs = _ops.dispatch_backward(gxd, grad_w, lay, T, K, P, E)
         grad_topk = _ops.route_to_multihot_backward(grad_probs, topk_idx, win)
-        return grad_x, None, grad_topk, dW1.to(W1.dtype), dW2.to(W2.dtype), None
+        return grad_x, None, grad_topk, dW1, dW2, None, None, None
 
 
 def moe_layer(x: Tensor, topk_idx: Tensor, topk_probs: Tensor, W1: Tensor, W2: Tensor,
@@ -280,7 +307,7 @@ def moe_layer(x: Tensor, topk_idx: Tensor, topk_probs: Tensor, W1: Tensor, W2: T
     expert index outside [-1, E) was seen and dropped), left on the device so
     that reading it is the caller's choice of synchronisation point."""
     if torch.is_grad_enabled() and any(t.requires_grad for t in (x, topk_probs, W1, W2)):
-        out, status = MoELayerFunction.apply(x, topk_idx, topk_probs, W1, W2, pad_multiple)
+        out, status = MoELayerFunction.apply(x, topk_idx, topk_probs, W1, W2, pad_multiple, None, None)
     else:
         T, K = topk_idx.shape
         E = W1.shape[0]
@@ -541,14 +568,16 @@ def moe_layer_fp4_block(x: Tensor, topk_idx: Tensor, topk_probs: Tensor, W1_q: T
     """The layer from e2m1 codes with a scale per 32 (quantize_fp4_block of W1 and
     W2), which get no gradients.  At most 8 tokens, where no gradient is wanted,
     take layer_few, which reads the codes; others take moe_layer on the weights
-    turned back to bf16, which is exact.  Returns out, or with ``return_status``
-    (out, status) as moe_layer does."""
+    turned back to bf16, which is exact, once more in the backward (the codes are what
+    is kept).  Returns out, or with ``return_status`` (out, status) as moe_layer does."""
     T, K = topk_idx.shape
-    if not _grad_wanted(x, topk_probs) and _few(x, K, W1_q, W1_scale):
+    if _grad_wanted(x, topk_probs):
+        out, status = MoELayerFunction.apply(x, topk_idx, topk_probs, W1_q, W2_q, pad_multiple, W1_scale, W2_scale)
+    elif _few(x, K, W1_q, W1_scale):
         out, status = _ops.layer_few(x, None, topk_idx, topk_probs, K, W1_q, W2_q, W1_scale, W2_scale)
-        return (out, status) if return_status else out
-    return moe_layer(x, topk_idx, topk_probs, _ops.dequantize_fp4_block(W1_q, W1_scale), _ops.dequantize_fp4_block(W2_q, W2_scale),
-                     pad_multiple, return_status)
+    else:
+        return moe_layer(x, topk_idx, topk_probs, _bf16(W1_q, W1_scale), _bf16(W2_q, W2_scale), pad_multiple, return_status)
+    return (out, status) if return_status else out
 
 
 def moe_block(x: Tensor, normed: Tensor, router: Tensor, top_k: int, W1: Tensor, W2: Tensor, norm_out_weight: Tensor,

@@ -468,8 +468,8 @@ MOE_API moe_status moe_route_to_multihot_backward(const float* grad_probs, const
  *   W1, W2: as in moe_grouped_experts.
  *   grad_x_disp [C, H] bf16 (out): written on the valid rows and the pad
  *     rows inside each expert's tiles (zeros there).
- *   dW1 [E, 2I, H], dW2 [E, H, I] fp32 (out): fully overwritten, fp32
- *     accumulation; an expert with no rows gets zeros.
+ *   dW1 [E, 2I, H], dW2 [E, H, I] fp32 (out, each nullable: not computed then):
+ *     fully overwritten, fp32 accumulation; an expert with no rows gets zeros.
  *   workspace: moe_experts_backward_workspace_bytes(capacity, H, I) bytes,
  *     caller-owned scratch.  On return it holds the backward GEMMs' bf16
  *     operands on the valid rows: G_o [C, H] from the workspace's first
