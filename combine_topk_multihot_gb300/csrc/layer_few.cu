@@ -467,7 +467,7 @@ struct Cursor {
     j0 += 8;
     if (j0 == I) j0 = 0, ++a;
   }
-  __device__ __forceinline__ bool more() const { return left2 > 0; }
+  __device__ __forceinline__ bool more() const { return left2 > 0; }  // (every CTA has rows of the output)
   __device__ __forceinline__ void aim1() {
     n_lo = n_hi = 8;
     const int e = s.expert[a];
@@ -889,7 +889,9 @@ cudaError_t launch(FewArgs g, const void* router, bool router_f32, float* logits
   auto kernel = few_layer_kernel<FMT>;
   if ((err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_LIMIT)) != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(sm_count());
+  // No more CTAs than rows of the output: the cursor asks for nothing once it has no row left, so that
+  // a CTA with columns of h alone would multiply what it never loaded.  (H is 256 at the least.)
+  cfg.gridDim = dim3(g.H < sm_count() ? g.H : sm_count());
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
