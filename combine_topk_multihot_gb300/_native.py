@@ -147,6 +147,7 @@ SIGNATURES = {
     "moe_selftest_block_product_tiles": (c_int32, [c_int32]),
     "moe_selftest_few_ctas": (c_int32, [c_int32]),
     "moe_selftest_norm_rows": (c_int32, [c_int64]),
+    "moe_selftest_few_plan": (c_int32, [c_int32] * 5 + [ctypes.POINTER(c_int32)] * 2),
     "moe_selftest_pair_wait": (c_int32, [c_int64]),
     "moe_route_to_multihot_backward": (c_int32, [_P, _P, _P, c_int32, c_int32, c_int32, _P, _P]),
 }

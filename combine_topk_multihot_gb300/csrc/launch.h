@@ -314,7 +314,8 @@ struct FewLayer {
   float* probs_out;
   int* status;
 };
-bool few_layer_fits(int format, int T, int K, int H, int I);
+// (and how many rows of h lie in shared memory at once, and pieces of weights a warp)
+bool few_layer_fits(int format, int T, int K, int H, int I, int* rows = nullptr, int* slots = nullptr);
 cudaError_t launch_few_layer(const FewLayer& f, cudaStream_t s);
 
 // AdamW over many tensors (adamw.cu), up to ADAMW_BATCH of them a launch.

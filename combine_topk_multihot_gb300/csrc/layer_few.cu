@@ -909,11 +909,14 @@ cudaError_t launch(FewArgs g, const void* router, bool router_f32, float* logits
 
 void selftest_few_ctas(int ctas) { tls_ctas = ctas; }
 
-bool few_layer_fits(int format, int T, int K, int H, int I) {
+bool few_layer_fits(int format, int T, int K, int H, int I, int* rows, int* slots) {
   FewArgs g{};
   g.T = T, g.K = K, g.H = H, g.I = I;
   size_t smem;
-  return format == FEW_BF16 ? plan<FEW_BF16>(g, &smem) : format == FEW_FP8 ? plan<FEW_FP8>(g, &smem) : plan<FEW_FP4>(g, &smem);
+  const bool fits = format == FEW_BF16 ? plan<FEW_BF16>(g, &smem) : format == FEW_FP8 ? plan<FEW_FP8>(g, &smem) : plan<FEW_FP4>(g, &smem);
+  if (rows) *rows = fits ? g.cap : 0;
+  if (slots) *slots = fits ? g.slots : 0;
+  return fits;
 }
 
 cudaError_t launch_few_layer(const FewLayer& f, cudaStream_t s) {

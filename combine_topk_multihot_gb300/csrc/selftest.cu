@@ -68,6 +68,14 @@ extern "C" moe_status moe_selftest_few_ctas(int32_t ctas) {
   return MOE_OK;
 }
 
+extern "C" moe_status moe_selftest_few_plan(int32_t T, int32_t K, int32_t H, int32_t I, int32_t weights, int32_t* rows,
+                                            int32_t* slots) {
+  if (!rows || !slots || !moe_layer_few_fits(T, MOE_FEW_TOP_K, K, H, I, weights))
+    return set_last_error(MOE_ERR_INVALID_ARG, "moe_selftest_few_plan: needs rows, slots and a layer that fits");
+  few_layer_fits(weights, T, K, H, I, rows, slots);
+  return MOE_OK;
+}
+
 extern "C" moe_status moe_selftest_block_product_tiles(int32_t tiles) {
   if (tiles < -1)
     return set_last_error(MOE_ERR_INVALID_ARG, "moe_selftest_block_product_tiles: tiles must be >= 0, or -1 for all");

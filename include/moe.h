@@ -851,6 +851,10 @@ MOE_API moe_status moe_selftest_norm_rows(int64_t rows);
  * the two products. */
 MOE_API moe_status moe_selftest_few_ctas(int32_t ctas);
 
+/* What a layer of moe_layer_few with T tokens keeps in shared memory: how many rows of h (of
+ * T K) at once, and how many pieces of weights a warp.  Host only. */
+MOE_API moe_status moe_selftest_few_plan(int32_t T, int32_t K, int32_t H, int32_t I, int32_t weights, int32_t* rows, int32_t* slots);
+
 /*
  * Self-test of products that take longer than the limit of a wait (2 s): until it is
  * called again with -1, the odd CTA of a pair (moe_matmul_fp4_block above 128 rows,

@@ -429,3 +429,31 @@ def test_columns_of_h_far_below_others(moe, fmt, apart):
     err = (out.double() - ref).abs()
     assert (err <= lim).all(), float((err / lim).max())
     assert float(lim.norm() / ref.norm()) < 0.25       # (columns that were lost would show)
+
+
+# layers of which h does not lie in shared memory at once: with several groups of 16 rows of the output a CTA
+# h is brought again for each, in parts, and two pieces a warp are the fewest
+LARGE = [(8, 4096, 32, 8, 1536), (8, 7168, 16, 8, 2048), (3, 16384, 8, 4, 2048)]
+
+
+@pytest.mark.parametrize("fmt", [0, 1, 2])
+def test_large_shapes_reach_every_way_of_bringing_h_without_a_gpu(moe, fmt):
+    from combine_topk_multihot_gb300 import _native as N
+    seen = set()
+    for T, H, E, K, I in SHAPES + LARGE:
+        rows, slots = ctypes.c_int32(), ctypes.c_int32()
+        assert N.lib.moe_selftest_few_plan(T, K, H, I, fmt, ctypes.byref(rows), ctypes.byref(slots)) == 0
+        assert T <= rows.value <= T * K and 2 <= slots.value <= 6
+        seen.add(("whole" if rows.value == T * K else "parts", "one group" if H <= 152 * 16 else "groups"))
+        seen.add(slots.value)
+    assert {("whole", "one group"), ("whole", "groups"), ("parts", "groups"), 2} <= seen, seen
+    out = ctypes.byref(ctypes.c_int32())
+    assert N.lib.moe_selftest_few_plan(8, 8, 16384, 128, fmt, out, out) == N.MOE_ERR_INVALID_ARG
+    assert N.lib.moe_selftest_few_plan(8, 8, 256, 128, fmt, None, out) == N.MOE_ERR_INVALID_ARG
+
+
+@gpu
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("T,H,E,K,I", LARGE)
+def test_large_layer(moe, fmt, T, H, E, K, I):
+    test_layer(moe, fmt, T, H, E, K, I)
