@@ -84,7 +84,7 @@ struct Smem {
   uint32_t tmem_base;
   int abort;
   int total_tiles;
-  uint32_t tiles_begun;  // by the odd CTA's loads
+  uint32_t last_begun;  // tile that the odd CTA has begun to load, and 1
 };
 
 // Epilogue staging for TMA stores: 4 KiB per epilogue warp (two boxes of
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     mbar_init(smem_u32(&s.drain), 1);
     s.abort = 0;
-    s.tiles_begun = 0;
+    s.last_begun = 0;
     mbar_fence_init();
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const int kbs = GROUP_K ? (s_cnt[t.e] + BK - 1) / BK : args.k_blocks;
         const int m0 = t.mt * RB + static_cast<int>(rank) * BM;         // this CTA's M rows
         const int n0 = t.nt * BN + static_cast<int>(rank) * (BN / 2);   // (pair) this CTA's N half
-        if (PAIR && rank != 0) *const_cast<volatile uint32_t*>(&s.tiles_begun) += 1;
+        if (PAIR && rank != 0) *const_cast<volatile uint32_t*>(&s.last_begun) = static_cast<uint32_t>(tile) + 1u;
         for (int kb = 0; kb < kbs; ++kb) {
           if (!mbar_wait(smem_u32(&s.empty[stage]), phase ^ 1u, abort_flag)) { ok = false; break; }
           const uint32_t full = smem_u32(&s.full[stage]);
@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   } else if (warp == 1 && PAIR && rank != 0) {
     // ================= the odd CTA of a pair: no MMAs; wait for the even CTA's last ones =================
     // (as long as its own loads go on)
-    if (lane == 0 && !mbar_wait_working(smem_u32(&s.drain), 0, &s.tiles_begun, args.pair_wait_ns)) *abort_flag = 1;
+    if (lane == 0 && !mbar_wait_working(smem_u32(&s.drain), 0, &s.last_begun, args.pair_wait_ns)) *abort_flag = 1;
     __syncwarp();
   } else if (warp == 1) {
     // ================= MMA warp (lane 0 issues; the warp zeroes tail K lines) =================

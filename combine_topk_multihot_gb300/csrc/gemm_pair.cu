@@ -119,7 +119,7 @@ struct Smem {
   int abort;
   int total_tiles;
   int last;  // the down launch's last CTA (it clears the readiness counters)
-  uint32_t tiles_begun;  // by the odd CTA's loads
+  uint32_t last_begun;  // tile that the odd CTA has begun to load, and 1
 };
 
 constexpr size_t smem_bytes(int stages, int E) {
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     mbar_init(smem_u32(&s.drain), 1);
     s.abort = 0;
-    s.tiles_begun = 0;
+    s.last_begun = 0;
     mbar_fence_init();
     tma_prefetch_desc(&tmW);
     tma_prefetch_desc(&tmR32);
@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (!wait_ready(args.ready + t.chunk, args.ready_target, abort_flag)) { ok = false; break; }
           fence_proxy_async_global();
         }
-        if (rank != 0) *const_cast<volatile uint32_t*>(&s.tiles_begun) += 1;
+        if (rank != 0) *const_cast<volatile uint32_t*>(&s.last_begun) = static_cast<uint32_t>(tile) + 1u;
         // this CTA loads t.n / 2 expert rows (a multiple of 8): rows t.row0 + rank * t.n / 2 on
         ok = load_tile_n<EPI, STAGES>(&tmW, rm, t, rank, tiles_u32, s, args.k_blocks, args.w_rows_per_expert,
                                       stage, phase, issued, abort_flag, tile == tile0 ? pre : 0);
@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     if (lane == 0 && rank != 0) {
       // the odd CTA issues nothing; it waits until the even CTA's last MMAs,
       // which write its tensor memory, have completed: as long as its own loads go on
-      if (!mbar_wait_working(smem_u32(&s.drain), 0, &s.tiles_begun, args.pair_wait_ns)) *abort_flag = 1;
+      if (!mbar_wait_working(smem_u32(&s.drain), 0, &s.last_begun, args.pair_wait_ns)) *abort_flag = 1;
     } else if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0;

@@ -369,12 +369,18 @@ __device__ __forceinline__ void stage_h(const FewArgs& args, int r0, int rows, i
         // 2^-24 is the least f16: what is further below the row's largest goes down in two steps
         const uint32_t down = top - e[n][j];
         const __half2 scale = __float2half2_rn(__uint_as_float((127u - min(down, 24u)) << 23));
-        const __half2 rest = __float2half2_rn(__uint_as_float((127u - min(max(down, 24u) - 24u, 24u)) << 23));
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          __half2 f = __hmul2(*reinterpret_cast<const __half2*>(&w[k]), scale);
-          if (down > 24u) f = __hmul2(f, rest);
+          const __half2 f = __hmul2(*reinterpret_cast<const __half2*>(&w[k]), scale);
           hi[k] = *reinterpret_cast<const uint32_t*>(&f);
+        }
+        if (down > 24u) {
+          const __half2 rest = __float2half2_rn(__uint_as_float((127u - min(down - 24u, 24u)) << 23));
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const __half2 f = __hmul2(*reinterpret_cast<const __half2*>(&hi[k]), rest);
+            hi[k] = *reinterpret_cast<const uint32_t*>(&f);
+          }
         }
       }
       *reinterpret_cast<uint4*>(to + 512 * j) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
