@@ -74,6 +74,20 @@ def train(stack, x, target, steps: int, lr: float, state_bits: int):
     return torch.stack(losses).tolist()
 
 
+def serve(stack, x):
+    """How far, by the norm, the outputs from e4m3 and e2m1 weights are from those from bf16, and those of the first four
+    tokens one at a time from those in the batch."""
+    with torch.no_grad():
+        out = dict(bf16=stack(x))
+        for kind, convert in (("fp8", stack.to_fp8), ("fp4", stack.to_fp4)):
+            convert()
+            out[kind] = stack(x)
+            out[kind + " one"] = torch.cat([stack(x[i:i + 1]) for i in range(4)])
+    rel = lambda p, q: float((out[p].float() - q.float()).norm() / q.float().norm())  # noqa: E731
+    return {"fp8": rel("fp8", out["bf16"]), "fp8 one": rel("fp8 one", out["fp8"][:4]),
+            "fp4": rel("fp4", out["bf16"]), "fp4 one": rel("fp4 one", out["fp4"][:4])}
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--tokens", type=int, default=512)
@@ -91,19 +105,11 @@ def main(argv=None):
     x = torch.randn(a.tokens, a.hidden, generator=g, device="cuda").bfloat16()
     target = torch.randn(a.tokens, a.hidden, generator=g, device="cuda") + x.float()
     losses = train(stack, x, target, a.steps, a.lr, a.state_bits)
-    with torch.no_grad():
-        bf16 = stack(x)
-        stack.to_fp8()
-        fp8 = stack(x)
-        one = torch.cat([stack(x[i:i + 1]) for i in range(4)])
-        stack.to_fp4()
-        fp4 = stack(x)
-        one4 = torch.cat([stack(x[i:i + 1]) for i in range(4)])
-    rel = lambda p, q: float((p.float() - q.float()).norm() / q.float().norm())  # noqa: E731
+    off = serve(stack, x)
     print(f"loss {losses[0]:.4f} -> {losses[-1]:.4f} in {a.steps} steps with {a.state_bits}-bit states; "
-          f"e4m3 experts against bf16: {rel(fp8, bf16):.4f}; one token at a time: {rel(one, fp8[:4]):.4f}; "
-          f"e2m1 experts against bf16: {rel(fp4, bf16):.4f}; one token at a time: {rel(one4, fp4[:4]):.4f}")
-    return losses, rel(fp8, bf16), rel(one, fp8[:4])
+          f"e4m3 experts against bf16: {off['fp8']:.4f}; one token at a time: {off['fp8 one']:.4f}; "
+          f"e2m1 experts against bf16: {off['fp4']:.4f}; one token at a time: {off['fp4 one']:.4f}")
+    return losses, off["fp8"], off["fp8 one"]
 
 
 if __name__ == "__main__":
