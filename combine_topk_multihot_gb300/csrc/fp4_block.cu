@@ -137,9 +137,10 @@ __global__ void __launch_bounds__(256) dequantize_fp4_kernel(const uint8_t* __re
 // other operand.  Codes become f16 numbers (exact) in registers; lane t of a row's
 // four takes word t of each block of 32, so that two instructions' 32 products
 // share their scales, which are applied to the sums.  The slices of K are joined in
-// shared memory in a fixed order.  It takes the calls of few tiles, where the
-// tensor cores' kernel is bound by its start and end; from 1024 columns on that one is
-// faster (8 x 16384 x 4096: 12 us for 23 here).
+// shared memory in a fixed order.  It takes the calls of few tiles (8 rows by 1024
+// columns at the most), where the tensor cores' kernel leaves SMs idle and is bound by its
+// start and end (8 x 1024 x 8192: 8.8 us here, 11.3 there); with more columns that one is
+// faster at the larger depths (8 x 16384 x 4096: 12 us for 23 here).
 // 2^(ea + eb - 254) as two factors: their product may leave fp32's range where
 // the value does not.
 struct Scale2 {

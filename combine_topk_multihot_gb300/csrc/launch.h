@@ -285,11 +285,11 @@ cudaError_t launch_quantize_fp4(const void* src, bool f32, long long batch, long
                                 uint8_t* scales, cudaStream_t s);
 cudaError_t launch_dequantize_fp4(const uint8_t* codes, const uint8_t* scales, long long batch, long long rows, int cols, bool f32,
                                   void* out, cudaStream_t s);
-// Their dense product: with at most FP4_STREAM_ROWS rows as a stream over the weights.
+// Their dense product: with at most FP4_STREAM_ROWS rows by 1024 as a stream over the weights.
 constexpr int FP4_STREAM_ROWS = 8;
 cudaError_t launch_fp4_matmul_stream(const uint8_t* a, const uint8_t* a_scale, int M, const uint8_t* b, const uint8_t* b_scale,
                                      int N, int K, uint16_t* out, cudaStream_t s);
-// ... with more on the tensor cores (fp4_gemm.cu).
+// ... with more of either on the tensor cores (fp4_gemm.cu).
 cudaError_t launch_fp4_matmul_tc(const uint8_t* a, const uint8_t* a_scale, int M, const uint8_t* b, const uint8_t* b_scale, int N,
                                  int K, uint16_t* out, int* status, cudaStream_t s);
 

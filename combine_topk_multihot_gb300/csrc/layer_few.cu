@@ -23,9 +23,9 @@
 //     shared memory in a fixed order.  A token's column is computed for
 //     every expert and used for its own.
 // What bounds it, at H = 2048, I = 768 and 8 of E = 128 experts a token: HBM for 8
-// tokens in bf16 (85 us, 70.6 of them the bytes of 51 experts); for the codes (e4m3 54,
-// bytes 35.4; e2m1 43.5, bytes 18.8) the instructions that make f16 numbers of them, 250
-// for a piece; for one token (22.2, 17.7 and 14.0) the way from launch to launch: the logits
+// tokens in bf16 (86 us, 70.6 of them the bytes of 51 experts); for the codes (e4m3 54.6,
+// bytes 35.4; e2m1 43.4, bytes 18.8) the instructions that make f16 numbers of them, 250
+// to 330 for a piece; for one token (22.2, 17.7 and 14.0) the way from launch to launch: the logits
 // 2 us, the list of experts 3, both products' first bytes, the meeting 1.5 to 2, h 1.5.
 //
 // Tried and slower: a ring of TMA boxes shared by all warps and filled by one (8 tokens: 167 us
@@ -40,7 +40,7 @@
 // largest (a bf16 token: 2^-31), and within 2^-38 of that below it.  (mma.sync on e4m3
 // operands takes 28 cycles an SM quarter here, on f16 12 for half of K, and converting a pair
 // of codes 2.3.)  h goes through memory as f16 with a power of two for eight columns:
-// its rounding, 2^-12, is an eighth of the output's, and half the bytes of fp32 have to reach
+// its rounding, 2^-11 at the most, is an eighth of the output's, and half the bytes of fp32 have to reach
 // every SM (in fp32 8 tokens took 0.9 to 2.3 us more).  With bf16 weights it is multiplied as
 // the sum of two bf16 numbers, which is exact: rounded to one it would add as much error as
 // the output's rounding.

@@ -766,7 +766,8 @@ MOE_API moe_status moe_matmul_fp4_block(const uint8_t* a_q, const uint8_t* a_sca
  *   ascending index (NaN as -infinity), and their softmax as weights w_k;
  *   h_k = silu(x Wg^T) * (x Wu^T) of expert e_k, rounded to 11 bits (f16 with a
  *   power of two for eight columns);
- *   out = bf16(sum_k w_k (h_k W2^T)), summed in fp32 by ascending expert.
+ *   out = bf16(sum_k w_k (h_k W2^T)), summed in fp32 in a fixed order: pieces of the active
+ *   experts' rows, 128 bytes each, go to 16 sums in turn, by ascending expert; then these.
  * With router NULL the routing is given instead: topk_idx [T, K] (-1: no
  * expert; of an expert that a token names twice the last slot counts; another
  * value outside [0, E) is dropped and sets MOE_DEVERR_BAD_INDEX) and topk_probs.
