@@ -48,26 +48,29 @@ def test_matmul_fp4(moe, M, N, K):
     assert int(status) == 0 and not whole.isnan().any() and torch.equal(out, whole)
 
 
+# (called one by one: autograd would run the backward on a thread of its own, whose limit is the usual one)
 @gpu
-def test_layer_and_its_gradients(moe):
+@pytest.mark.parametrize("backward", [False, True])
+def test_grouped_products(moe, backward):
     """The grouped products, forward and backward, each of 0.5 ms or more; the limit is 0.25 ms (a tile of the weights'
     gradients takes 0.09)."""
     T, H, E, K, I = 65536, 2048, 32, 4, 768
     g = torch.Generator(device=DEV).manual_seed(0)
     rnd = lambda *s, std=1.0: (torch.randn(*s, generator=g, device=DEV) * std).bfloat16()  # noqa: E731
-    leaves = [rnd(T, H), torch.rand(T, K, generator=g, device=DEV), rnd(E, 2 * I, H, std=H ** -0.5), rnd(E, H, I, std=I ** -0.5)]
+    x, W1, W2, p = rnd(T, H), rnd(E, 2 * I, H, std=H ** -0.5), rnd(E, H, I, std=I ** -0.5), torch.rand(T, K, generator=g, device=DEV)
     idx = torch.rand(T, E, generator=g, device=DEV).topk(K, dim=1).indices
-    grad = rnd(T, H)
-
-    def run():
-        x, p, W1, W2 = (t.detach().requires_grad_() for t in leaves)
-        out, status = moe.moe_layer(x, idx, p, W1, W2, 64, return_status=True)
-        return [out.detach(), *torch.autograd.grad(out, (x, p, W1, W2), grad)], status
-
-    whole, status = run()
+    f = moe.moe_layer_forward(x, idx, p, W1, W2, 64, host_sync=False, save_for_backward=True)
+    if backward:
+        g_o, _ = moe.moe_combine_backward(rnd(T, H), f.layout, o_save=f.o, scaled=True)
+        run = lambda: moe.moe_grouped_experts_backward(g_o, f.x_disp, f.h, f.gu, f.layout, W1, W2, scaled=True)  # noqa: E731
+    else:
+        run = lambda: moe.moe_grouped_experts(f.x_disp, f.layout, W1, W2, save_o=True, save_gu=True).values()  # noqa: E731
+    rows = f.layout.row_token >= 0                     # (others are not all written)
+    cut = lambda out: [t[rows] if t.shape[0] == f.layout.capacity else t for t in out]  # noqa: E731
+    whole = cut(run())
     torch.cuda.synchronize()
-    assert int(status) == 0 and all(t.isfinite().all() for t in whole)
+    assert int(f.layout.status) == 0 and all(t.isfinite().all() for t in whole)
     with _limit(moe, 250):
-        got, status = run()
+        got = cut(run())
         torch.cuda.synchronize()
-    assert int(status) == 0 and all(torch.equal(a, b) for a, b in zip(got, whole))
+    assert int(f.layout.status) == 0 and all(torch.equal(a, b) for a, b in zip(got, whole))
