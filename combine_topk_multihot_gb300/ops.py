@@ -266,7 +266,7 @@ class MoELayerFunction(torch.autograd.Function):
     e2m1 codes, kept as such for the backward and turned into bf16 in either direction."""
 
     @staticmethod
-    def forward(ctx, x, topk_idx, topk_probs, W1, W2, pad_multiple: int, W1_scale, W2_scale):
+    def forward(ctx, x, topk_idx, topk_probs, W1, W2, pad_multiple: int, W1_scale=None, W2_scale=None):
         T, K = topk_idx.shape
         E = W1.shape[0]
         rmap, probs, win, status = _ops.route_to_multihot(topk_idx, topk_probs, E)
