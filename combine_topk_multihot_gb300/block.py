@@ -96,9 +96,14 @@ def _either(t: torch.Tensor, name: str) -> int:
     return code
 
 
+_INT32 = 2 ** 31 - 1  # sizes cross to the library in 32 bits
+
+
 def _rows(t: torch.Tensor, name: str):
     if t.dim() != 2:
         raise ValueError(f"{name} must be [T, H] (got {tuple(t.shape)})")
+    if max(t.shape) > _INT32:
+        raise ValueError(f"{name}'s sizes must be below 2^31 (got {tuple(t.shape)})")
     return t.shape
 
 
@@ -377,6 +382,8 @@ def moe_quantize_fp8_block(src: torch.Tensor, block_rows: int = 1, out=None, str
     if src.dim() < 2:
         raise ValueError(f"src must be [..., rows, cols] (got {tuple(src.shape)})")
     rows, cols = src.shape[-2:]
+    if cols > _INT32:
+        raise ValueError(f"cols must be below 2^31 (got {cols})")
     if block_rows not in (1, 128):
         raise ValueError(f"block_rows must be 1 or 128 (got {block_rows})")
     lead = src.shape[:-2]
@@ -441,9 +448,6 @@ def moe_grouped_experts_fp8_block(x_disp: torch.Tensor, layout: Layout, W1_q: to
 
 
 # ------------------------------------------------------------------ e2m1 with a scale per 32
-_INT32 = 2 ** 31 - 1  # sizes cross to the library in 32 bits
-
-
 def _fp4_tiles(rows: int, cols: int):
     """The last five sizes of a matrix's scales: tiles of 128 rows and 4 blocks of 32."""
     return (rows + 127) // 128, (cols + 127) // 128, 32, 4, 4
@@ -518,8 +522,8 @@ def moe_matmul_fp4_block(a_q: torch.Tensor, a_scale: torch.Tensor, b_q: torch.Te
     dev = _on_gpu(a_q, "a_q")
     M, half = _rows(a_q, "a_q")
     n = _rows(b_q, "b_q")[0]
-    if max(M, n, 2 * half) > _INT32:
-        raise ValueError(f"sizes must be below 2^31 (got M={M}, N={n}, K={2 * half})")
+    if 2 * half > _INT32:
+        raise ValueError(f"K must be below 2^31 (got {2 * half})")
     if out is None:
         out = torch.empty(M, n, dtype=torch.bfloat16, device=dev)
         place = out.data_ptr() or None

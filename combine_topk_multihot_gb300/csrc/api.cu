@@ -1008,8 +1008,9 @@ moe_status moe_matmul_fp8_block(const uint8_t* a_q, const float* a_scale, int32_
                                 moe_stream_t stream) {
   MOE_REQUIRE(M >= 0 && N >= 1, MOE_ERR_INVALID_ARG, "moe_matmul_fp8_block: M must be >= 0 and N >= 1 (got %d, %d)", M,
               N);
-  MOE_REQUIRE(K >= 16 && K % 16 == 0, MOE_ERR_UNSUPPORTED_SHAPE,
-              "moe_matmul_fp8_block: K must be a positive multiple of 16 (got %d)", K);
+  constexpr int32_t most_k = (int64_t(1) << 31) - 256;  // (rounded up to whole blocks it stays within 32 bits)
+  MOE_REQUIRE(K >= 16 && K % 16 == 0 && K <= most_k, MOE_ERR_UNSUPPORTED_SHAPE,
+              "moe_matmul_fp8_block: K must be a positive multiple of 16 up to 2^31 - 256 (got %d)", K);
   MOE_REQUIRE(M == 0 || (a_q && a_scale && b_q && b_scale && out), MOE_ERR_INVALID_ARG,
               "moe_matmul_fp8_block: NULL pointer");
   MOE_REQUIRE(aligned16(a_q) && aligned16(b_q) && all_aligned(4, a_scale, b_scale) && aligned_to(out, N % 8 == 0 ? 16 : 2),

@@ -683,7 +683,7 @@ MOE_API moe_status moe_quantize_fp8_block(const moe_bf16* src, int64_t batch, in
  *   128); out [M, N] bf16 (out); status [1] int32 device status word
  *   (nullable), receives MOE_DEVERR_TIMEOUT if a bounded wait runs out; the
  *   elements that are not reached then are NaN.
- * M >= 0, N >= 1, K >= 16 a multiple of 16.  Codes are 16-byte aligned, and so
+ * M >= 0, N >= 1, K >= 16 a multiple of 16 up to 2^31 - 256.  Codes are 16-byte aligned, and so
  * is out when N is a multiple of 8.  Up to 8 rows stream the
  * weights through registers; more run on the tensor cores in 128-row tiles.
  */
